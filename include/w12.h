@@ -465,6 +465,165 @@ W12_API int gdn_commit(float* S, const uint16_t* k, const uint16_t* v, const flo
                        const int32_t* path_len, const int32_t* path_nodes, int64_t n, int64_t H, int64_t dk,
                        int64_t dv, int32_t* status, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Attention layers over a paged cache.  The recurrent layers above keep a state;
+ * a target's attention layers keep K and V of every committed token instead.  The
+ * calls below (no counterpart in the pages) are the same three steps for them: the
+ * outputs of every node of the draft trees (tree_attn), and the commit of the
+ * accepted paths, here as slots for the new tokens (kv_slots) and a copy of their
+ * rows into them (kv_write).  The cache holds committed tokens only: a drafted
+ * node's K and V stay in the pass's own rows until its path is accepted.  Node 0, the
+ * root, is the last known token: this pass is the first to compute its K and V, so
+ * a commit appends path_nodes[0 .. path_len], path_len + 1 tokens.
+ *
+ * A cache is a pool of n_blocks blocks of block_size tokens, shared by all requests
+ * and laid out alike for every layer.  Element (layer l, block b, token t, head h,
+ * column c) of k and of v is at l*layer_stride + b*block_stride + t*token_stride +
+ * h*head_stride + c (elements; the columns are adjacent), so tokens may stand
+ * outside heads or heads outside tokens, and K and V may be halves of one array.
+ * Request r's token at position p is token p % block_size of block
+ * table[r*table_stride + p / block_size].  k, v and every stride must be multiples of
+ * 8 elements (16 bytes).
+ */
+typedef struct kv_cache {
+  uint16_t* k;
+  uint16_t* v;
+  int64_t n_layers, n_blocks;
+  int64_t layer_stride, block_stride, token_stride, head_stride;
+  int32_t block_size, n_heads, head_dim;
+} kv_cache;
+
+/* Slots for the tokens that n_req requests append, with their blocks taken from a pool,
+ * entirely on the device (the lengths may be the previous call's results).  Request r
+ * holds cache_len[r] tokens and appends a_r = add[r] + extra; a_r = -1 ends the request
+ * instead: its blocks return to the pool and its length becomes 0 (its table row is left
+ * as it is).  For a commit, add is tree_verify's path_len and extra 1 (an invalid tree
+ * appends nothing); for prompts, add holds the token counts and extra is 0.
+ * The pool is a ring of n_blocks entries: pool[i % n_blocks], i in
+ * [pool_pos[0], pool_pos[1]), are the free blocks.  New blocks are taken at the front in
+ * request order and entered in the table (the entries below ceil(cache_len[r] /
+ * block_size) are read, those above written); returned blocks are added at the back.
+ * Outputs: for the t-th appended token (requests in order, a_r tokens each), slot[t] =
+ * block * block_size + token in the block, and src[t] = the row of its K and V: t
+ * itself, or, with path_nodes, req_offsets[r] + path_nodes[req_offsets[r] + j] for
+ * the request's j-th token (path_nodes has n_nodes entries; req_offsets = NULL: one
+ * request from 0).  Both hold -1 from *total up to capacity.  new_len[n_req],
+ * pool_pos_out[2] (not pool_pos itself), *total (int64).
+ * The call is all or nothing: if a request's numbers are out of range (a length
+ * or a_r negative other than -1, more blocks than table_width, a path longer than the
+ * request's nodes or beyond n_nodes) bit 0 of *status is set, if the pool has too few
+ * free blocks or is not consistent bit 1, if more than capacity tokens are appended bit
+ * 2; then the table and the pool stay as they were, *total = 0, every slot and src is -1,
+ * new_len = cache_len and pool_pos_out = pool_pos.  A path node outside its request
+ * gives its token src -1, which kv_write refuses, and sets bit 3.  *status (device
+ * int32) is zeroed by the caller.  Errors: W12_ERR_INVALID_ARG (null pointer, pool_pos_out = pool_pos,
+ * new_len = cache_len), W12_ERR_SHAPE (n_req outside 1..4096, block_size or table_width
+ * outside 1..2^24, n_blocks outside 1..2^31-1, capacity outside 1..2^31-1). */
+W12_API int kv_slots(const int32_t* cache_len, const int32_t* add, int32_t extra, int32_t n_req, int32_t* table,
+                     int64_t table_stride, int64_t table_width, int32_t* pool, int64_t n_blocks,
+                     const int64_t* pool_pos, int64_t block_size, const int32_t* path_nodes,
+                     const int32_t* req_offsets, int64_t n_nodes, int64_t capacity, int64_t* slot, int32_t* src,
+                     int32_t* new_len, int64_t* pool_pos_out, int64_t* total, int32_t* status, void* stream);
+
+/* Rows of K and V into their slots, for layers layer .. layer + n_layers - 1 of the cache
+ * in one launch: cache[layer + l] at slot[t] = row src[t] of k and v (src = NULL: row t),
+ * t < n.  Row i of layer l starts at k + l*k_layer_stride + i*k_row_stride and holds
+ * n_heads * head_dim adjacent elements; v likewise; pointers and strides are multiples of
+ * 8 elements.  A slot of -1 is skipped (kv_slots' padding).  Any other slot outside the
+ * cache or row outside 0..n_rows-1 is skipped too and sets bit 0 of *status.  Two tokens
+ * with one slot leave either's row.  head_dim: a multiple of 8 up to 1024.
+ * Errors: W12_ERR_INVALID_ARG, W12_ERR_SHAPE. */
+W12_API int kv_write(const kv_cache* cache, int64_t layer, int64_t n_layers, const uint16_t* k, int64_t k_layer_stride,
+                     int64_t k_row_stride, const uint16_t* v, int64_t v_layer_stride, int64_t v_row_stride,
+                     int64_t n_rows, const int64_t* slot, const int32_t* src, int64_t n, int32_t* status,
+                     void* stream);
+
+/* Attention of M drafted nodes of n_req requests (offsets and parents as for
+ * tree_verify_tokens; a request may have no nodes).  Node i of request r attends to the
+ * request's cache_len[r] cached tokens, to its ancestors and to itself:
+ *     out[i, h] = sum_j p_j v_j[h / G],  p = softmax_j(scale * q[i, h] . k_j[h / G]),
+ * G = n_q_heads / n_heads of the cache (query heads h*G .. h*G + G-1 share cache head h).
+ * One node per request is plain decoding; a chain (parent i - 1) is a prompt's chunk.
+ * q[i] starts at q + i*q_stride, heads adjacent, likewise k and v (strides in elements);
+ * out is [M, n_q_heads, head_dim] bf16, adjacent.  Scores, the softmax's statistics and the
+ * sums are float; the probabilities are rounded to bf16 before they meet V, and the
+ * output once.  Repeated calls give identical bits.
+ * head_dim 64, 128 or 256; at most 256 nodes a request.  A request whose numbers are out of range
+ * (offsets, more than 256 nodes, a malformed tree, a length outside 0..table_width *
+ * block_size) sets bit 0 of *status, one whose table names a block outside the cache
+ * bit 1, and its out rows are left unwritten; other requests are not affected.
+ * K and V of a token that a node does not attend to do not reach its output, whatever
+ * they hold.  ws: tree_attn_workspace_size bytes, no initial state needed (do not pass
+ * a GEMM's workspace, whose counters must stay zero).
+ * Errors: W12_ERR_INVALID_ARG (null or misaligned pointers or strides), W12_ERR_SHAPE,
+ * W12_ERR_BUFFER_TOO_SMALL. */
+W12_API size_t tree_attn_workspace_size(int64_t M, int32_t n_req, int64_t n_q_heads, int64_t n_heads,
+                                        int64_t head_dim);
+W12_API int tree_attn(const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_stride, const uint16_t* v,
+                      int64_t v_stride, int64_t M, int64_t n_q_heads, const kv_cache* cache, int64_t layer,
+                      const int32_t* table, int64_t table_stride, int64_t table_width, const int32_t* cache_len,
+                      const int32_t* parent, const int32_t* req_offsets, int32_t n_req, float scale, uint16_t* out,
+                      int32_t* status, void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Rules on logits before the argmax (no counterpart in the pages): penalties for
+ * repeated tokens, a bias per token, and a mask of the tokens a grammar allows.  Device
+ * pointers; NULL leaves a rule out.
+ *   hist      request r's tokens are hist[r*hist_stride + i], i < hist_len[r], of which the
+ *             first prompt_len[r] (NULL: 0) are its prompt.  They end before the
+ *             root of its tree.
+ *   rep, freq, pres   n_req factors each.
+ *   bias_off[n_req+1], bias_tok, bias_val[n_bias]   request r's entries
+ *             bias_off[r] .. bias_off[r+1]-1; the last entry of a token counts.
+ *   mask      row m allows token v if bit v%32 of mask[m*mask_stride + v/32] is set.
+ * For row m of request r and token v, with count = occurrences of v behind the
+ * prompt plus those among the drafted tokens from the root to the node, and seen = count >
+ * 0 or v is in the prompt (float arithmetic, each step rounded):
+ *   x = logits[m, v];  if seen: x = x > 0 ? x / rep : x * rep;
+ *   x = x - freq * count;  if count > 0: x = x - pres;  x = x + bias[v];
+ *   x = -inf if v is not allowed.
+ * Tokens outside 0..V-1 in hist, draft or bias_tok are ignored.
+ */
+typedef struct logit_rules {
+  const int32_t* hist;
+  int64_t hist_stride;
+  const int32_t* hist_len;
+  const int32_t* prompt_len;
+  const float* rep;
+  const float* freq;
+  const float* pres;
+  const int32_t* bias_off;
+  const int32_t* bias_tok;
+  const float* bias_val;
+  int64_t n_bias;
+  const uint32_t* mask;
+  int64_t mask_stride;
+} logit_rules;
+
+/* out[m*out_stride + v] = the formula above, for M rows of V logits (row m at
+ * logits + m*stride) that are the nodes of n_req requests (parent, draft, req_offsets as
+ * for tree_verify_tokens; parent and draft NULL: rows without drafted tokens).  out may be
+ * logits.  A request that is out of range (offsets, a malformed tree, more than 1024
+ * nodes) sets bit 0 of *status and its rows are left; a length or bias range out of range
+ * is clamped and sets bit 1.  Asynchronous; allocates nothing.  Errors:
+ * W12_ERR_INVALID_ARG, W12_ERR_SHAPE (M, V, n_req, strides). */
+W12_API int logits_process(const float* logits, int64_t stride, int64_t M, int64_t V, const logit_rules* rules,
+                           const int32_t* parent, const int32_t* draft, const int32_t* req_offsets, int32_t n_req,
+                           float* out, int64_t out_stride, int32_t* status, void* stream);
+
+/* The processed rows' argmax over the allowed tokens (ties to the lowest token, NaN below
+ * every number, -1 where nothing is allowed) and greedy acceptance, without writing the
+ * processed logits: tok[M], path_len, path_nodes and bonus as tree_verify gives them for
+ * logits_process's result, except that a row without an allowed token has tok -1, which
+ * no draft matches, and path_nodes is -1 behind the path.  ws:
+ * logits_verify_workspace_size bytes, no initial state needed (do not pass a GEMM's).
+ * Errors as above and W12_ERR_BUFFER_TOO_SMALL. */
+W12_API size_t logits_verify_workspace_size(int64_t M, int64_t V, int32_t n_req);
+W12_API int logits_verify(const float* logits, int64_t stride, int64_t M, int64_t V, const logit_rules* rules,
+                          const int32_t* parent, const int32_t* draft, const int32_t* req_offsets, int32_t n_req,
+                          int32_t* tok, int32_t* path_len, int32_t* path_nodes, int32_t* bonus, int32_t* status,
+                          void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

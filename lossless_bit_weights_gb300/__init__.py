@@ -15,6 +15,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+import typing
 
 import torch
 
@@ -43,6 +44,21 @@ class w12_matrix(ctypes.Structure):
 class w12_i8_head(ctypes.Structure):
     _fields_ = [("V", ctypes.c_int64), ("K", ctypes.c_int64), ("code", ctypes.c_void_p), ("scale", ctypes.c_void_p),
                 ("cbound", ctypes.c_void_p)]
+
+
+class kv_cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("n_layers", ctypes.c_int64),
+                ("n_blocks", ctypes.c_int64), ("layer_stride", ctypes.c_int64), ("block_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("block_size", ctypes.c_int32),
+                ("n_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+class logit_rules(ctypes.Structure):
+    _fields_ = [("hist", ctypes.c_void_p), ("hist_stride", ctypes.c_int64), ("hist_len", ctypes.c_void_p),
+                ("prompt_len", ctypes.c_void_p), ("rep", ctypes.c_void_p), ("freq", ctypes.c_void_p),
+                ("pres", ctypes.c_void_p), ("bias_off", ctypes.c_void_p), ("bias_tok", ctypes.c_void_p),
+                ("bias_val", ctypes.c_void_p), ("n_bias", ctypes.c_int64), ("mask", ctypes.c_void_p),
+                ("mask_stride", ctypes.c_int64)]
 
 
 # (name, restype, argtypes) of every exported symbol, in include/w12.h order.
@@ -91,6 +107,18 @@ SIGNATURES = [
     ("gdn_path_verify", ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _P, _P, _P]),
     ("gdn_wy_verify", ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _P, _P, _P]),
     ("gdn_commit", ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _P, _P]),
+    ("kv_slots", ctypes.c_int, [_P, _P, _I32, _I32, _P, _I64, _I64, _P, _I64, _P, _I64, _P, _P, _I64, _I64, _P, _P, _P,
+                                _P, _P, _P, _P]),
+    ("kv_write", ctypes.c_int, [ctypes.POINTER(kv_cache), _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _I64, _P, _P,
+                                _I64, _P, _P]),
+    ("tree_attn_workspace_size", _SZ, [_I64, _I32, _I64, _I64, _I64]),
+    ("tree_attn", ctypes.c_int, [_P, _I64, _P, _I64, _P, _I64, _I64, _I64, ctypes.POINTER(kv_cache), _I64, _P, _I64,
+                                 _I64, _P, _P, _P, _I32, ctypes.c_float, _P, _P, _P, _SZ, _P]),
+    ("logits_process", ctypes.c_int, [_P, _I64, _I64, _I64, ctypes.POINTER(logit_rules), _P, _P, _P, _I32, _P, _I64,
+                                      _P, _P]),
+    ("logits_verify_workspace_size", _SZ, [_I64, _I64, _I32]),
+    ("logits_verify", ctypes.c_int, [_P, _I64, _I64, _I64, ctypes.POINTER(logit_rules), _P, _P, _P, _I32, _P, _P, _P,
+                                     _P, _P, _P, _SZ, _P]),
 ]
 
 
@@ -127,6 +155,24 @@ def _stream(stream) -> int:
 
 def _ptr(t) -> int | None:
     return None if t is None else t.data_ptr()
+
+
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """A new tensor that belongs to the stream it is used on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _zero_status(status, device, stream) -> torch.Tensor:
+    """The caller's status word, or a new one zeroed on the call's stream."""
+    if status is not None:
+        return _i32(status)
+    if stream is None:
+        return torch.zeros(1, dtype=torch.int32, device=device)
+    with torch.cuda.stream(stream):
+        return torch.zeros(1, dtype=torch.int32, device=device)
 
 
 def _bits16(t: torch.Tensor) -> torch.Tensor:
@@ -255,11 +301,23 @@ class Workspace:
     def __init__(self, device=None):
         self.device = device or torch.device("cuda")
         self.buf = torch.zeros(256, dtype=torch.uint8, device=self.device)
+        self._scratch, self._scratch_stream = None, 0
 
     def get(self, nbytes: int) -> torch.Tensor:
         if nbytes > self.buf.numel():
             self.buf = torch.zeros(int(nbytes), dtype=torch.uint8, device=self.device)
         return self.buf
+
+    def scratch(self, nbytes: int, stream) -> torch.Tensor:
+        """A buffer for the calls on `stream` whose workspace needs no initial state, apart from
+        get()'s: what they leave in it must not stand where a GEMM expects its counters at zero."""
+        t = self._scratch
+        if t is None or nbytes > t.numel():
+            t = self._scratch = _empty(max(int(nbytes), 256), torch.uint8, self.device, stream)
+            self._scratch_stream = stream.cuda_stream
+        if stream.cuda_stream != self._scratch_stream:  # not to be reused while that stream still works on it
+            t.record_stream(stream)
+        return t
 
     def status(self, stream=None) -> int:
         """w12_workspace_status: W12_OK, W12_ERR_TIMEOUT or W12_ERR_BOUNDS for the calls made
@@ -553,3 +611,230 @@ def gdn_commit(S, k, v, alpha, beta, path_len, path_nodes, status=None, stream=N
     _check(lib().gdn_commit(_ptr(S), _ptr(k), _ptr(v), _ptr(alpha), _ptr(beta), _ptr(path_len), _ptr(path_nodes), n, H,
                             dk, dv, _ptr(status), _stream(stream)))
     return status
+
+
+# ---------------------------------------------------------------- attention layers over a paged cache
+
+def _rows16(t: torch.Tensor, name: str, dims: int) -> torch.Tensor:
+    """Rows of bf16 heads whose last two dimensions are adjacent (leading strides are free)."""
+    if t.dtype not in (torch.bfloat16, torch.int16, torch.uint16):
+        raise TypeError(f"expected bf16 bits (bfloat16/int16/uint16) in {name}, got {t.dtype}")
+    if t.dim() != dims or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor of {dims} dimensions")
+    if t.stride(-1) != 1 and t.shape[-1] != 1 or t.stride(-2) != t.shape[-1] and t.shape[-2] != 1:
+        raise ValueError(f"the heads of a row of {name} must be adjacent")
+    return t
+
+
+class KVCache:
+    """Pools of K and V blocks (include/w12.h, kv_cache): two tensors of bf16 values, indexed
+    [layer,] block, token, head, column, with the columns adjacent and any other strides (a
+    transposed view of blocks that keep heads outside tokens will do)."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor):
+        for t in (k, v):
+            if t.dtype not in (torch.bfloat16, torch.int16, torch.uint16):
+                raise TypeError(f"expected bf16 bits (bfloat16/int16/uint16), got {t.dtype}")
+            if not t.is_cuda or t.dim() not in (4, 5) or t.stride(-1) != 1:
+                raise ValueError("a cache is a CUDA tensor [layer,] block, token, head, column with adjacent columns")
+        if k.shape != v.shape or k.stride() != v.stride():
+            raise ValueError("K and V must have the same shape and strides")
+        self.k, self.v = k, v
+        self.n_layers = k.shape[0] if k.dim() == 5 else 1
+        self.n_blocks, self.block_size, self.n_heads, self.head_dim = k.shape[-4:]
+        layer_stride = k.stride(0) if k.dim() == 5 else 0
+        self._desc = kv_cache(_ptr(k), _ptr(v), self.n_layers, self.n_blocks, layer_stride, *k.stride()[-4:-1],
+                              self.block_size, self.n_heads, self.head_dim)
+        self._ref = ctypes.byref(self._desc)
+
+    def desc(self):
+        return self._ref
+
+
+class Slots(typing.NamedTuple):
+    """What kv_slots returns: slot [capacity] int64 and src [capacity] int32 (-1 behind the
+    total), new_len [n_req] int32, pool_pos [2] int64, total [1] int64, status [1] int32."""
+    slot: torch.Tensor
+    src: torch.Tensor
+    new_len: torch.Tensor
+    pool_pos: torch.Tensor
+    total: torch.Tensor
+    status: torch.Tensor
+
+
+def kv_slots(cache_len, add, table, pool, pool_pos, block_size: int, capacity: int, extra: int = 0, path_nodes=None,
+             req_offsets=None, status=None, stream=None) -> Slots:
+    """Slots for the tokens that requests append (add + extra each; -1 ends a request), with
+    blocks from the ring `pool`; table [n_req, width] and pool are updated in place (see
+    include/w12.h).  For a commit pass tree_verify's path_len as add, extra=1, its path_nodes
+    and the trees' req_offsets."""
+    if table.dim() != 2 or table.dtype != torch.int32 or not table.is_cuda or (table.stride(1) != 1 and table.shape[1] != 1):
+        raise ValueError("table must be an int32 CUDA tensor [n_req, width] with adjacent columns")
+    if pool_pos.dtype != torch.int64 or pool_pos.numel() != 2 or not pool_pos.is_cuda or not pool_pos.is_contiguous():
+        raise ValueError("pool_pos must be an int64 CUDA tensor of two values")
+    n_req, dev = table.shape[0], table.device
+    if _i32(cache_len).numel() != n_req or _i32(add).numel() != n_req:
+        raise ValueError(f"cache_len and add must have an entry for each of the table's {n_req} rows")
+    if path_nodes is not None:
+        _check_offsets(req_offsets, n_req)
+    # one allocation for the int64 results and one for the int32 ones
+    wide = _empty(capacity + 3, torch.int64, dev, stream)
+    slim = _empty(capacity + n_req, torch.int32, dev, stream)
+    out = Slots(wide[3:], slim[n_req:], slim[:n_req], wide[:2], wide[2:3], _zero_status(status, dev, stream))
+    w, i = wide.data_ptr(), slim.data_ptr()
+    _check(lib().kv_slots(_ptr(cache_len), _ptr(add), int(extra), n_req, _ptr(table), _row_stride(table),
+                          table.shape[1], _ptr(_i32(pool)), pool.numel(), _ptr(pool_pos), int(block_size),
+                          _ptr(None if path_nodes is None else _i32(path_nodes)),
+                          _ptr(None if req_offsets is None else _i32(req_offsets)), 0 if path_nodes is None else path_nodes.numel(), int(capacity), w + 24, i + 4 * n_req, i, w,
+                          w + 16, _ptr(out.status), _stream(stream)))
+    return out
+
+
+def _row_stride(t: torch.Tensor) -> int:
+    """Elements from row to row of a matrix; a single row's is its width."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _check_offsets(req_offsets, n_req: int) -> None:
+    if req_offsets is None:
+        if n_req != 1:
+            raise ValueError(f"req_offsets is needed for {n_req} requests")
+    elif _i32(req_offsets).numel() != n_req + 1:
+        raise ValueError(f"req_offsets must have {n_req + 1} entries")
+
+
+def kv_write(cache: KVCache, k, v, slot, src=None, layer: int = 0, status=None, stream=None):
+    """Rows of k and v [layers,] rows, heads, columns into their slots of the cache, from layer
+    `layer` on (src: the row of each slot's token; None: row t for slot t).  Returns status."""
+    dims = 4 if k.dim() == 4 else 3
+    k, v = _rows16(k, "k", dims), _rows16(v, "v", dims)
+    if k.shape != v.shape or tuple(k.shape[-2:]) != (cache.n_heads, cache.head_dim):
+        raise ValueError(f"k and v must be [layers,] rows, {cache.n_heads}, {cache.head_dim}")
+    if slot.dtype != torch.int64 or not slot.is_cuda or not slot.is_contiguous():
+        raise ValueError("slot must be a contiguous int64 CUDA tensor")
+    n = slot.numel()
+    if src is None and n > k.shape[-3]:
+        raise ValueError(f"{n} slots for {k.shape[-3]} rows")
+    if src is not None and _i32(src).numel() != n:
+        raise ValueError("src must have an entry for each slot")
+    status = _zero_status(status, slot.device, stream)
+    _check(lib().kv_write(cache.desc(), layer, k.shape[0] if dims == 4 else 1, _ptr(k), k.stride(0) if dims == 4 else 0,
+                          k.stride(-3), _ptr(v), v.stride(0) if dims == 4 else 0, v.stride(-3), k.shape[-3], _ptr(slot),
+                          _ptr(src), n, _ptr(status), _stream(stream)))
+    return status
+
+
+def tree_attn(q, k, v, cache: KVCache, table, cache_len, parent, req_offsets=None, layer: int = 0,
+              scale: float | None = None, out=None, ws: Workspace | None = None, status=None, stream=None):
+    """Attention of drafted nodes over their request's cached tokens, their ancestors and
+    themselves (see include/w12.h).  q [M, query heads, D], k, v [M, heads, D] bf16 bits, rows at
+    any stride; table [n_req, width], cache_len [n_req], parent [M], req_offsets [n_req + 1] int32;
+    scale: 1/sqrt(D) if not given.  Returns (out [M, query heads, D], status)."""
+    q, k, v = _rows16(q, "q", 3), _rows16(k, "k", 3), _rows16(v, "v", 3)
+    M, hq, D = q.shape
+    if k.shape != v.shape or tuple(k.shape) != (M, cache.n_heads, D) or D != cache.head_dim:
+        raise ValueError(f"k and v must be [{M}, {cache.n_heads}, {cache.head_dim}] and q's columns {cache.head_dim}")
+    if table.dim() != 2 or table.dtype != torch.int32 or not table.is_cuda or (table.stride(1) != 1 and table.shape[1] != 1):
+        raise ValueError("table must be an int32 CUDA tensor [n_req, width] with adjacent columns")
+    n_req = table.shape[0]
+    if _i32(cache_len).numel() != n_req or _i32(parent).numel() != M:
+        raise ValueError(f"cache_len must have {n_req} entries and parent {M}")
+    _check_offsets(req_offsets, n_req)
+    if out is None:
+        out = _empty((M, hq, D), q.dtype, q.device, stream)
+    elif _bits16(out).shape != q.shape:
+        raise ValueError(f"out must be {tuple(q.shape)}")
+    status = _zero_status(status, q.device, stream)
+    L = lib()
+    on = stream if stream is not None else torch.cuda.current_stream()
+    buf = (ws or Workspace(q.device)).scratch(L.tree_attn_workspace_size(M, n_req, hq, cache.n_heads, D), on)
+    _check(L.tree_attn(q.data_ptr(), q.stride(0), k.data_ptr(), k.stride(0), v.data_ptr(), v.stride(0), M, hq,
+                       cache.desc(), layer, table.data_ptr(), _row_stride(table), table.shape[1],
+                       cache_len.data_ptr(), parent.data_ptr(), _ptr(req_offsets), n_req,
+                       D ** -0.5 if scale is None else scale, out.data_ptr(), status.data_ptr(), buf.data_ptr(),
+                       buf.numel(), on.cuda_stream))
+    return out, status
+
+
+# ---------------------------------------------------------------- rules on logits
+
+class LogitRules:
+    """Rules on logits (include/w12.h, logit_rules); the tensors stay the caller's and may change
+    between calls.  hist [n_req, capacity] int32 with hist_len and prompt_len [n_req] int32;
+    repetition, frequency, presence [n_req] float32; bias: (offsets [n_req + 1], tokens, values);
+    mask [M, words] int32, bit v%32 of word v/32 set where token v is allowed."""
+
+    def __init__(self, hist=None, hist_len=None, prompt_len=None, repetition=None, frequency=None, presence=None,
+                 bias=None, mask=None):
+        if hist is not None and (hist.dim() != 2 or hist_len is None):
+            raise ValueError("hist must be [n_req, capacity], with hist_len")
+        if mask is not None and mask.dim() != 2:
+            raise ValueError("mask must be [M, words]")
+        off, tok, val = bias if bias is not None else (None, None, None)
+        if bias is not None and _i32(tok).numel() != _f32(val).numel():
+            raise ValueError("a bias needs as many values as tokens")
+        ints = [None if t is None else _i32(t) for t in (hist, hist_len, prompt_len, off, mask)]
+        floats = [None if t is None else _f32(t) for t in (repetition, frequency, presence)]
+        self.n_req = {t.shape[0] for t in ints[:3] + floats if t is not None}
+        self.n_req |= set() if off is None else {off.numel() - 1}
+        if len(self.n_req) > 1:
+            raise ValueError("the rules are for different numbers of requests")
+        self.rows, self.words = (None, 0) if mask is None else mask.shape
+        self._keep = (ints, floats, tok, val)
+        self._desc = logit_rules(_ptr(hist), 0 if hist is None else hist.shape[1], _ptr(hist_len), _ptr(prompt_len),
+                                 *[_ptr(t) for t in floats], _ptr(off), _ptr(tok), _ptr(val),
+                                 0 if tok is None else tok.numel(), _ptr(mask), self.words)
+        self._ref = ctypes.byref(self._desc)
+
+    def desc(self):
+        return self._ref
+
+
+def _rule_args(logits, rules: LogitRules, parent, draft, req_offsets):
+    if logits.dtype != torch.float32 or not logits.is_cuda or logits.dim() != 2 or (logits.stride(1) != 1 and logits.shape[1] != 1):
+        raise ValueError("logits must be a float32 CUDA tensor [M, V] with adjacent columns")
+    M, V = logits.shape
+    n_req = 1 if req_offsets is None else _i32(req_offsets).numel() - 1
+    if rules.n_req - {n_req}:
+        raise ValueError(f"the rules are for {rules.n_req.pop()} requests, the rows of {n_req}")
+    if rules.rows is not None and (rules.rows != M or rules.words * 32 < V):
+        raise ValueError(f"the mask must have {M} rows of {(V + 31) // 32} words or more")
+    for t in (parent, draft):
+        if t is not None and _i32(t).numel() != M:
+            raise ValueError(f"parent and draft must have {M} entries")
+    return M, V, n_req, _row_stride(logits)
+
+
+def logits_process(logits, rules: LogitRules, parent=None, draft=None, req_offsets=None, out=None, status=None,
+                   stream=None):
+    """The rows of logits [M, V] under the rules (see include/w12.h); out may be logits.  Rows
+    are the nodes of the requests' trees, whose drafted tokens count as repeated.  Returns
+    (out, status)."""
+    M, V, n_req, stride = _rule_args(logits, rules, parent, draft, req_offsets)
+    if out is None:
+        out = _empty((M, V), torch.float32, logits.device, stream)
+    elif out.dtype != torch.float32 or out.shape != logits.shape or not out.is_cuda or (out.stride(1) != 1 and V != 1):
+        raise ValueError(f"out must be a float32 CUDA tensor [{M}, {V}] with adjacent columns")
+    status = _zero_status(status, logits.device, stream)
+    _check(lib().logits_process(logits.data_ptr(), stride, M, V, rules.desc(), _ptr(parent), _ptr(draft),
+                                _ptr(req_offsets), n_req, out.data_ptr(), _row_stride(out), status.data_ptr(),
+                                _stream(stream)))
+    return out, status
+
+
+def logits_verify(logits, rules: LogitRules, parent, draft, req_offsets=None, ws: Workspace | None = None, status=None,
+                  stream=None):
+    """Argmax under the rules and greedy acceptance, without writing the processed logits:
+    returns (tok, path_len, path_nodes, bonus, status)."""
+    M, V, n_req, stride = _rule_args(logits, rules, parent, draft, req_offsets)
+    L = lib()
+    both = _empty(2 * M + 2 * n_req, torch.int32, logits.device, stream)
+    tok, path_nodes, path_len, bonus = both[:M], both[M:2 * M], both[2 * M:2 * M + n_req], both[2 * M + n_req:]
+    status = _zero_status(status, logits.device, stream)
+    on = stream if stream is not None else torch.cuda.current_stream()
+    buf = (ws or Workspace(logits.device)).scratch(L.logits_verify_workspace_size(M, V, n_req), on)
+    at = both.data_ptr()
+    _check(L.logits_verify(logits.data_ptr(), stride, M, V, rules.desc(), _ptr(parent), _ptr(draft), _ptr(req_offsets),
+                           n_req, at, at + 8 * M, at + 4 * M, at + 8 * M + 4 * n_req, status.data_ptr(), buf.data_ptr(),
+                           buf.numel(), on.cuda_stream))
+    return tok, path_len, path_nodes, bonus, status

@@ -1,0 +1,398 @@
+// w12_logits.cu - rules on logits before the argmax: penalties for repeated tokens, a
+// bias per token, a mask of allowed tokens; and the rows' argmax with greedy acceptance
+// behind them.
+//
+// One block takes one request and one chunk of the vocabulary.  It builds the request's
+// side of the rules for its chunk in shared memory (integer counts of the history, the
+// prompt flag, the place of the last bias entry, and a bitmap of the tokens that any rule
+// of the request can touch), then streams the chunk of each of the request's rows once.
+// A token outside the bitmap costs one bit test; one inside it takes its count from the
+// table plus the drafted tokens on the row's own path, so the table is never changed and
+// rows need no barriers between them.
+#include <cstdint>
+
+#include "w12_internal.cuh"
+
+namespace w12 {
+namespace {
+
+constexpr int kRuleThreads = 256;
+constexpr int kRuleWarps = kRuleThreads / 32;
+constexpr int kRuleMaxNodes = 1024;  // nodes of one request
+constexpr uint32_t kPromptFlag = 0x80000000u;
+constexpr int32_t kRuleBadRequest = 1, kRuleClamped = 2;
+
+struct RuleArgs {
+  const float* logits;
+  int64_t stride, M, V;
+  logit_rules r;
+  const int32_t *parent, *draft, *req_offsets;
+  int32_t n_req;
+  float* out;
+  int64_t out_stride;
+  int32_t* status;
+  unsigned long long* key;  // [M][chunks] argmax keys, or null
+  int32_t chunk, chunks, parts;
+  bool vec;                 // rows allow 16-byte accesses
+};
+
+// Nodes of request r, or false: its offsets are out of range or it has too many.
+__device__ __forceinline__ bool request_rows(const int32_t* offsets, int64_t M, int r, int64_t& off, int& n) {
+  off = offsets ? offsets[r] : 0;
+  const int64_t end = offsets ? offsets[r + 1] : M;
+  if (off < 0 || end < off || end > M || end - off > kRuleMaxNodes) return false;
+  n = (int)(end - off);
+  return true;
+}
+
+struct RowRules {
+  const uint32_t *cnt, *bits;
+  const int32_t *bias_at, *up, *parent, *draft;  // up: nearest node on the path whose token is in the chunk
+  int64_t v0;
+  bool has_rep, has_freq, has_pres;
+  float rep, freq, pres;
+  const float* bias_val;
+};
+
+// The formula for one token that some rule may touch; i = token - v0, node = the row's node.
+__device__ __noinline__ float apply_rules(const RowRules& w, float x, int i, int node) {
+  uint32_t c = w.cnt ? w.cnt[i] : 0u;
+  const int32_t tok = (int32_t)(w.v0 + i);
+  if (w.up)
+    for (int32_t p = w.up[node]; p >= 0;) {
+      if (w.draft[p] == tok) ++c;
+      p = w.parent[p] >= 0 ? w.up[w.parent[p]] : -1;
+    }
+  const uint32_t n = c & ~kPromptFlag;
+  if (c && w.has_rep) x = x > 0.0f ? __fdiv_rn(x, w.rep) : __fmul_rn(x, w.rep);
+  if (n) {
+    if (w.has_freq) x = __fsub_rn(x, __fmul_rn(w.freq, (float)n));
+    if (w.has_pres) x = __fsub_rn(x, w.pres);
+  }
+  if (w.bias_at && w.bias_at[i] > 0) x = __fadd_rn(x, w.bias_val[w.bias_at[i] - 1]);
+  return x;
+}
+
+__device__ __forceinline__ unsigned long long arg_key(float x, int64_t v) {
+  return ((unsigned long long)((uint32_t)order_key(x) ^ 0x80000000u) << 32) | (0xFFFFFFFFu - (uint32_t)v);
+}
+
+__global__ void __launch_bounds__(kRuleThreads) k_logit_rules(RuleArgs a) {
+  extern __shared__ uint32_t sm[];
+  const int r = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t v0 = (int64_t)blockIdx.x * a.chunk;
+  const int width = (int)min((int64_t)a.chunk, a.V - v0);
+  int64_t off;
+  int n;
+  if (!request_rows(a.req_offsets, a.M, r, off, n)) {
+    if (tid == 0) atomicOr(a.status, kRuleBadRequest);
+    return;
+  }
+  const bool count = a.r.rep || a.r.freq || a.r.pres;
+  const bool tree = a.parent != nullptr;
+  // shared memory: bitmap, counts, bias places (chunk entries each), then the tree
+  uint32_t* bits = sm;
+  uint32_t* cnt = bits + a.chunk / 32;
+  int32_t* bias_at = reinterpret_cast<int32_t*>(cnt + (count ? a.chunk : 0));
+  int32_t* parent = bias_at + (a.r.bias_off ? a.chunk : 0);
+  int32_t* draft = parent + (tree ? n : 0);
+  int32_t* up = draft + (tree ? n : 0);
+  unsigned long long* best = reinterpret_cast<unsigned long long*>(
+      (reinterpret_cast<uintptr_t>(up + (tree ? n : 0)) + 7) & ~(uintptr_t)7);
+
+  for (int i = tid; i < a.chunk / 32; i += kRuleThreads) bits[i] = 0;
+  if (count)
+    for (int i = tid; i < a.chunk; i += kRuleThreads) cnt[i] = 0;
+  if (a.r.bias_off)
+    for (int i = tid; i < a.chunk; i += kRuleThreads) bias_at[i] = 0;
+  if (a.key)
+    for (int i = tid; i < n; i += kRuleThreads) best[i] = 0;
+  bool ok = true;
+  if (tree)
+    for (int i = tid; i < n; i += kRuleThreads) {
+      const int32_t p = a.parent[off + i];
+      ok = ok && (i == 0 ? p == -1 : p >= 0 && p < i);
+      parent[i] = p;
+      draft[i] = a.draft[off + i];
+    }
+  if (!__syncthreads_and(ok)) {
+    if (tid == 0) atomicOr(a.status, kRuleBadRequest);
+    if (a.key)  // no token: acceptance reports the tree as invalid
+      for (int i = tid; i < n; i += kRuleThreads) a.key[(off + i) * a.chunks + blockIdx.x] = 0;
+    return;
+  }
+  if (count && a.r.hist) {
+    const int64_t given = a.r.hist_len[r];
+    const int64_t len = min(max(given, (int64_t)0), a.r.hist_stride);
+    const int64_t prompt = a.r.prompt_len ? a.r.prompt_len[r] : 0;
+    if (tid == 0 && (len != given || prompt < 0 || prompt > given)) atomicOr(a.status, kRuleClamped);
+    const int32_t* h = a.r.hist + r * a.r.hist_stride;
+    for (int64_t j = tid; j < len; j += kRuleThreads) {
+      const int64_t i = (int64_t)h[j] - v0;
+      if (i >= 0 && i < width) {
+        if (j < prompt) atomicOr(&cnt[i], kPromptFlag); else atomicAdd(&cnt[i], 1u);
+        atomicOr(&bits[i >> 5], 1u << (i & 31));
+      }
+    }
+  }
+  if (a.r.bias_off) {
+    const int64_t g0 = a.r.bias_off[r], g1 = a.r.bias_off[r + 1];
+    const int64_t b0 = min(max(g0, (int64_t)0), a.r.n_bias), b1 = min(max(g1, b0), a.r.n_bias);
+    if (tid == 0 && (b0 != g0 || b1 != g1)) atomicOr(a.status, kRuleClamped);
+    for (int64_t j = b0 + tid; j < b1; j += kRuleThreads) {
+      const int64_t i = (int64_t)a.r.bias_tok[j] - v0;
+      if (i >= 0 && i < width) {
+        atomicMax(&bias_at[i], (int32_t)j + 1);
+        atomicOr(&bits[i >> 5], 1u << (i & 31));
+      }
+    }
+  }
+  if (tree && count)
+    for (int i = tid; i < n; i += kRuleThreads) {
+      int32_t p = i;
+      while (p >= 0 && !(draft[p] >= v0 && draft[p] < v0 + width)) p = parent[p];
+      up[i] = p;
+      if (p == i) {
+        const int b = (int)(draft[i] - v0);
+        atomicOr(&bits[b >> 5], 1u << (b & 31));
+      }
+    }
+  __syncthreads();
+
+  RowRules w;
+  w.cnt = count ? cnt : nullptr;
+  w.bits = bits;
+  w.bias_at = a.r.bias_off ? bias_at : nullptr;
+  w.up = tree && count ? up : nullptr;
+  w.parent = parent;
+  w.draft = draft;
+  w.v0 = v0;
+  w.has_rep = a.r.rep != nullptr;
+  w.has_freq = a.r.freq != nullptr;
+  w.has_pres = a.r.pres != nullptr;
+  w.rep = w.has_rep ? a.r.rep[r] : 1.0f;
+  w.freq = w.has_freq ? a.r.freq[r] : 0.0f;
+  w.pres = w.has_pres ? a.r.pres[r] : 0.0f;
+  w.bias_val = a.r.bias_val;
+
+  // a warp takes one part of one row's chunk
+  const int part_len = a.chunk / a.parts;
+  for (int u = warp; u < n * a.parts; u += kRuleWarps) {
+    const int node = u / a.parts, c0 = (u - node * a.parts) * part_len, c1 = min(width, c0 + part_len);
+    const int64_t m = off + node;
+    const float* x = a.logits + m * a.stride + v0;
+    float* y = a.out ? a.out + m * a.out_stride + v0 : nullptr;
+    const uint32_t* mask = a.r.mask ? a.r.mask + m * a.r.mask_stride + v0 / 32 : nullptr;
+    unsigned long long top = 0;
+    for (int i = c0 + lane; i < c1; i += 32) {
+      float f = x[i];
+      const bool allowed = !mask || (mask[i >> 5] >> (i & 31) & 1u);
+      if (bits[i >> 5] >> (i & 31) & 1u) f = apply_rules(w, f, i, node);
+      if (y) y[i] = allowed ? f : -INFINITY;
+      if (a.key && allowed) {
+        const unsigned long long k = arg_key(f, v0 + i);
+        top = k > top ? k : top;
+      }
+    }
+    if (a.key) {
+      for (int o = 16; o; o >>= 1) {
+        const unsigned long long t = __shfl_xor_sync(0xFFFFFFFFu, top, o);
+        top = t > top ? t : top;
+      }
+      if (lane == 0 && top) atomicMax(&best[node], top);
+    }
+  }
+  if (a.key) {
+    __syncthreads();
+    for (int i = tid; i < n; i += kRuleThreads) a.key[(off + i) * a.chunks + blockIdx.x] = best[i];
+  }
+}
+
+// One block per request: the rows' tokens from their chunks' keys, then acceptance.
+__global__ void __launch_bounds__(kRuleThreads) k_rule_accept(const unsigned long long* __restrict__ key, int chunks,
+                                                              const int32_t* __restrict__ parent_g,
+                                                              const int32_t* __restrict__ draft_g,
+                                                              const int32_t* __restrict__ offsets, int64_t M,
+                                                              int32_t* __restrict__ tok_out, int32_t* path_len,
+                                                              int32_t* __restrict__ path_nodes, int32_t* bonus) {
+  __shared__ int32_t tok[kRuleMaxNodes], parent[kRuleMaxNodes], draft[kRuleMaxNodes];
+  __shared__ unsigned long long s_best;
+  const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int64_t off;
+  int n;
+  const bool in = request_rows(offsets, M, r, off, n);
+  if (!in || n == 0) {
+    if (tid == 0) path_len[r] = bonus[r] = -1;
+    return;
+  }
+  bool ok = true;
+  for (int i = tid; i < n; i += kRuleThreads) {
+    const int32_t p = parent_g[off + i];
+    ok = ok && (i == 0 ? p == -1 : p >= 0 && p < i);
+    parent[i] = p;
+    draft[i] = draft_g[off + i];
+    path_nodes[off + i] = -1;
+  }
+  if (tid == 0) s_best = 0;
+  ok = __syncthreads_and(ok) != 0;
+  for (int i = warp; i < n; i += kRuleWarps) {
+    unsigned long long top = 0;
+    const unsigned long long* k = key + (off + i) * chunks;
+    for (int c = lane; c < chunks; c += 32) top = k[c] > top ? k[c] : top;
+    for (int o = 16; o; o >>= 1) {
+      const unsigned long long t = __shfl_xor_sync(0xFFFFFFFFu, top, o);
+      top = t > top ? t : top;
+    }
+    if (lane == 0) tok[i] = tok_out[off + i] = top ? (int32_t)(0xFFFFFFFFu - (uint32_t)top) : -1;
+  }
+  if (!ok) {
+    if (tid == 0) path_len[r] = bonus[r] = -1;
+    return;
+  }
+  __syncthreads();
+  // every node walks its own path; the deepest accepted one wins, the lowest index among equals
+  for (int i = tid; i < n; i += kRuleThreads) {
+    int32_t depth = 0, p = i;
+    bool taken = true;
+    while (p > 0 && taken) {
+      const int32_t t = tok[parent[p]];
+      taken = t >= 0 && draft[p] == t;
+      p = parent[p];
+      ++depth;
+    }
+    if (taken) atomicMax(&s_best, ((unsigned long long)(depth + 1) << 32) | (0xFFFFFFFFu - (uint32_t)i));
+  }
+  __syncthreads();
+  if (tid == 0) {
+    const int32_t depth = (int32_t)(s_best >> 32) - 1, node = (int32_t)(0xFFFFFFFFu - (uint32_t)s_best);
+    path_len[r] = depth;
+    bonus[r] = tok[node];
+    int32_t p = node;
+    for (int32_t j = depth; j >= 0; --j) {
+      path_nodes[off + j] = p;
+      p = parent[p];
+    }
+  }
+}
+
+struct RulePlan {
+  int chunk, chunks, parts;
+};
+
+// Chunk of the vocabulary per block, a multiple of 256: the larger it is, the fewer blocks
+// scan a request's history and the more rows share the table; the smaller, the more blocks
+// there are.  The largest of 4096, 2048, 1024 with at least two blocks per SM.
+RulePlan rule_plan(int64_t M, int64_t V, int32_t n_req) {
+  RulePlan p{};
+  for (p.chunk = 4096; p.chunk > 1024; p.chunk /= 2)
+    if ((V + p.chunk - 1) / p.chunk * n_req >= 304) break;
+  p.chunks = (int)((V + p.chunk - 1) / p.chunk);
+  const int64_t rows = (M + n_req - 1) / n_req;
+  p.parts = rows >= 8 ? 1 : rows >= 4 ? 2 : rows >= 2 ? 4 : 8;
+  return p;
+}
+
+int check_rules(const float* logits, int64_t stride, int64_t M, int64_t V, const logit_rules* rules,
+                const int32_t* parent, const int32_t* draft, const int32_t* req_offsets, int32_t n_req,
+                const int32_t* status, const char* fn) {
+  if (!logits || !rules || !status) return fail(W12_ERR_INVALID_ARG, "%s: null pointer", fn);
+  if (M < 1 || M > 0x7FFFFFFF || V < 1 || V > 0x7FFFFFFF || stride < V || n_req < 1 || n_req > 65535)
+    return fail(W12_ERR_SHAPE, "%s: M=%lld, V=%lld (stride %lld), n_req=%d (1..65535) out of range", fn, (long long)M,
+                (long long)V, (long long)stride, n_req);
+  if (!req_offsets && n_req != 1)
+    return fail(W12_ERR_INVALID_ARG, "%s: req_offsets is null but n_req=%d", fn, n_req);
+  if (!parent != !draft) return fail(W12_ERR_INVALID_ARG, "%s: parent and draft go together", fn);
+  if (rules->hist && (!rules->hist_len || rules->hist_stride < 1))
+    return fail(W12_ERR_INVALID_ARG, "%s: a history needs its lengths and a stride", fn);
+  if ((rules->bias_off != nullptr) != (rules->bias_tok != nullptr) ||
+      (rules->bias_off != nullptr) != (rules->bias_val != nullptr) || rules->n_bias < 0 || rules->n_bias > 0x7FFFFFFE)
+    return fail(W12_ERR_INVALID_ARG, "%s: a bias needs offsets, tokens, values and a count", fn);
+  if (rules->mask && rules->mask_stride < (V + 31) / 32)
+    return fail(W12_ERR_SHAPE, "%s: mask_stride=%lld is less than a row's words", fn, (long long)rules->mask_stride);
+  return W12_OK;
+}
+
+int launch_rules(const float* logits, int64_t stride, int64_t M, int64_t V, const logit_rules* rules,
+                 const int32_t* parent, const int32_t* draft, const int32_t* req_offsets, int32_t n_req, float* out,
+                 int64_t out_stride, int32_t* status, unsigned long long* key, cudaStream_t s, const char* what) {
+  const RulePlan p = rule_plan(M, V, n_req);
+  RuleArgs a{};
+  a.logits = logits;
+  a.stride = stride;
+  a.M = M;
+  a.V = V;
+  a.r = *rules;
+  a.parent = parent;
+  a.draft = draft;
+  a.req_offsets = req_offsets;
+  a.n_req = n_req;
+  a.out = out;
+  a.out_stride = out_stride;
+  a.status = status;
+  a.key = key;
+  a.chunk = p.chunk;
+  a.chunks = p.chunks;
+  a.parts = p.parts;
+  const bool count = rules->rep || rules->freq || rules->pres;
+  const int64_t nodes = M < kRuleMaxNodes ? M : kRuleMaxNodes;
+  const size_t smem = (size_t)p.chunk / 8 + (count ? (size_t)p.chunk * 4 : 0) + (rules->bias_off ? (size_t)p.chunk * 4 : 0) +
+                      (parent ? (size_t)nodes * 12 : 0) + 8 + (key ? (size_t)nodes * 8 : 0);
+  constexpr size_t most = 4096 / 8 + 4096 * 8 + kRuleMaxNodes * 20 + 8;
+  static int configured[64] = {0};
+  int dev = 0;
+  W12_CUDA_TRY(cudaGetDevice(&dev));
+  if (dev >= 64 || !configured[dev]) {
+    W12_CUDA_TRY(cudaFuncSetAttribute(k_logit_rules, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most));
+    if (dev < 64) configured[dev] = 1;
+  }
+  k_logit_rules<<<dim3((unsigned)p.chunks, (unsigned)n_req), kRuleThreads, smem, s>>>(a);
+  W12_LAUNCH_CHECK(what);
+  return W12_OK;
+}
+
+}  // namespace
+}  // namespace w12
+
+using namespace w12;
+
+extern "C" {
+
+int logits_process(const float* logits, int64_t stride, int64_t M, int64_t V, const logit_rules* rules,
+                   const int32_t* parent, const int32_t* draft, const int32_t* req_offsets, int32_t n_req, float* out,
+                   int64_t out_stride, int32_t* status, void* stream) {
+  int st = check_rules(logits, stride, M, V, rules, parent, draft, req_offsets, n_req, status, "logits_process");
+  if (st) return st;
+  if (!out) return fail(W12_ERR_INVALID_ARG, "logits_process: null pointer");
+  if (out_stride < V) return fail(W12_ERR_SHAPE, "logits_process: out_stride=%lld is less than V", (long long)out_stride);
+  return launch_rules(logits, stride, M, V, rules, parent, draft, req_offsets, n_req, out, out_stride, status, nullptr,
+                      (cudaStream_t)stream, "logits_process kernel");
+}
+
+size_t logits_verify_workspace_size(int64_t M, int64_t V, int32_t n_req) {
+  if (M < 1 || V < 1 || n_req < 1) return 0;
+  return (size_t)M * (size_t)rule_plan(M, V, n_req).chunks * 8;
+}
+
+int logits_verify(const float* logits, int64_t stride, int64_t M, int64_t V, const logit_rules* rules,
+                  const int32_t* parent, const int32_t* draft, const int32_t* req_offsets, int32_t n_req, int32_t* tok,
+                  int32_t* path_len, int32_t* path_nodes, int32_t* bonus, int32_t* status, void* ws, size_t ws_bytes,
+                  void* stream) {
+  int st = check_rules(logits, stride, M, V, rules, parent, draft, req_offsets, n_req, status, "logits_verify");
+  if (st) return st;
+  if (!parent || !tok || !path_len || !path_nodes || !bonus || !ws)
+    return fail(W12_ERR_INVALID_ARG, "logits_verify: null pointer");
+  if ((uintptr_t)ws & 7u) return fail(W12_ERR_INVALID_ARG, "logits_verify: the workspace must be 8-byte aligned");
+  if (ws_bytes < logits_verify_workspace_size(M, V, n_req))
+    return fail(W12_ERR_BUFFER_TOO_SMALL, "logits_verify: workspace %zu < %zu", ws_bytes,
+                logits_verify_workspace_size(M, V, n_req));
+  unsigned long long* key = static_cast<unsigned long long*>(ws);
+  st = launch_rules(logits, stride, M, V, rules, parent, draft, req_offsets, n_req, nullptr, 0, status, key,
+                    (cudaStream_t)stream, "logits_verify: rules kernel");
+  if (st) return st;
+  k_rule_accept<<<(unsigned)n_req, kRuleThreads, 0, (cudaStream_t)stream>>>(
+      key, rule_plan(M, V, n_req).chunks, parent, draft, req_offsets, M, tok, path_len, path_nodes, bonus);
+  W12_LAUNCH_CHECK("logits_verify: acceptance kernel");
+  return W12_OK;
+}
+
+}  // extern "C"
