@@ -1,7 +1,29 @@
 // w12_attn.cu - attention of draft-tree nodes over a paged cache and their ancestors.
 //
-// Plain form: one block per (node, query head), an online softmax in float over tiles of
-// 128 keys, a key per thread for the scores and a column per thread for the sums.
+// For one cache head, the rows (node, query head of the group) of a request share every
+// key: R = nodes * group rows, cut into units of 128 or 256, meet T = ceil((len + n) / BK)
+// tiles of keys, the n drafted nodes standing behind the len cached tokens.  A CTA takes
+// an equal, contiguous share of all units' tiles (one CTA per SM); a unit that falls
+// into several shares leaves its parts (running reference, sum, unnormalised output) in
+// the workspace, and a second kernel adds them in order, so the bits do not depend on
+// who came first.
+//
+// Inside a CTA the score and output products run on the tensor core (tcgen05):
+//   S = Q K^T   both operands in shared memory, 128 rows x BK keys, float in tensor memory;
+//   P = exp2(S c - m) by one thread per row, bf16, written over S in tensor memory;
+//   O += P V    P from tensor memory, V as it lies in shared memory (keys x columns).
+// The reference m follows the running maximum only when it has fallen more than 2^8
+// behind, so O is rarely rescaled; any reference gives the same quotient.  Four producer
+// warps copy rows of K and V (16 bytes a thread, so any block size and any strides do)
+// into a ring of tiles that runs on across units.
+//
+// Per 128 keys of a head with D = 128, an SM's share of the memory rate is about 2800 cycles
+// (64 KB), its two products 1024, its exponentials 1024: the kernel is bound by the cache's
+// bytes up to 128 rows, whose padding costs nothing.  Up to 128 rows the two softmax
+// warpgroups take tiles in turn (each with its own S, O and statistics, added at the end);
+// above, they take 128 rows each of the same tile, so K and V are read once for 256 rows.
+// D = 256 fills tensor memory with one O: one warpgroup, two S in turn, tiles of 64 keys.
+#include <cmath>
 #include <cstdint>
 
 #include "w12_internal.cuh"
@@ -12,9 +34,15 @@ int check_cache(const kv_cache* c, const char* fn);
 
 namespace {
 
-constexpr int kAttnThreads = 128;
 constexpr int kAttnMaxNodes = 256;
-constexpr int32_t kAttnBadRequest = 1, kAttnBadBlock = 2;
+constexpr int32_t kAttnBadRequest = 1, kAttnBadBlock = 2, kAttnTimeout = 4;
+constexpr int kAttnCtas = 152;  // one per SM of a GB300; fewer SMs only run them in turn
+constexpr int kMetaRing = 4;     // units whose tree the producers may hold at once
+// P enters its product in two bf16 pieces, the upper one cut off, the lower one rounded: 2^-16
+// of P is lost instead of 2^-8.  The lower piece is taken of P (1 + 2^-20), so that it is above
+// zero wherever P is and an infinity in V stays one (no 0 * inf, no inf - inf).
+constexpr float kUp = 1.0f + 1.0f / 1048576.0f;
+constexpr float kRefSlack = 8.0f;  // log2 of the largest P before the reference moves
 
 struct AttnArgs {
   const uint16_t *q, *k, *v, *kc, *vc;
@@ -22,99 +50,912 @@ struct AttnArgs {
   int64_t block_stride, token_stride, head_stride, n_blocks;
   const int32_t *table, *cache_len, *parent, *req_offsets;
   int64_t table_stride, table_width;
-  int32_t n_req, block_size, group, n_q_heads;
-  float scale;
+  int32_t n_req, block_size, group, n_heads, n_q_heads, row_cap;
+  float scale_log2;  // scale * log2(e)
   uint16_t* out;
   int32_t* status;
+  float *part_o, *part_ml;  // [2 * CTAs][D / 4][row_cap][4], [2 * CTAs][row_cap][2]
+  int32_t* part_bad;        // [2 * CTAs]
 };
 
-__device__ __forceinline__ float bf16_f(uint16_t h) { return __uint_as_float((uint32_t)h << 16); }
+template <int D>
+struct AttnPlan {
+  static constexpr int kWG = D <= 128 ? 2 : 1;       // softmax warpgroups
+  static constexpr int kRows = 128 * kWG;            // rows of a unit
+  static constexpr int kBK = D <= 128 ? 128 : 64;    // keys of a tile
+  static constexpr int kSlots = D == 64 ? 10 : 5;    // tiles of the ring
+  static constexpr int kSlotBytes = kBK * D * 2;
+  static constexpr int kSoftmaxThreads = 128 * kWG;
+  static constexpr int kThreads = kSoftmaxThreads + 128 + 32;  // + producers + MMA warp
+  static constexpr int kQ = 0;
+  static constexpr int kQTile = 128 * D * 2;
+  static constexpr int kRing = kQ + kWG * kQTile;
+  static constexpr int kPar = kRing + kSlots * kSlotBytes;     // parents, kMetaRing x 256 bytes
+  static constexpr int kML = kPar + kMetaRing * kAttnMaxNodes; // 128 x (reference, sum)
+  static constexpr int kNf = kML + 128 * 8;                    // nodes with infinities or NaN in V, kMetaRing x 8 words
+  static constexpr int kBad = kNf + kMetaRing * 32;            // kMetaRing words
+  static constexpr int kMisc = kBad + kMetaRing * 4;           // tensor memory address, abort, schedule
+  static constexpr int kBar = (kMisc + 48 + 7) & ~7;
+  static constexpr int kBytes = kBar + 8 * (2 * kSlots + 3 * 2 + 6 + kMetaRing);
+  static_assert(kBytes <= 227 * 1024, "shared memory plan too large");
+  static_assert(kThreads * 8 <= kSlots * kSlotBytes, "the ring holds the schedule's sums");
+  // tensor memory columns
+  static constexpr int kO(int g) { return g * 128; }
+  static constexpr int kS(int b) { return 256 + b * 128; }
+};
 
-__device__ __forceinline__ uint16_t f_bf16(float f) {
-  uint16_t h;
-  asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(h) : "f"(f));
-  return h;
+// ---------------------------------------------------------------- schedule
+
+struct Req {
+  int64_t off;
+  int32_t n, len, tiles, row_units;
+  bool ok;
+};
+
+template <int D>
+__device__ __forceinline__ Req load_request(const AttnArgs& a, int r) {
+  using P = AttnPlan<D>;
+  Req q{0, 0, 0, 0, 0, true};
+  q.off = a.req_offsets ? a.req_offsets[r] : 0;
+  const int64_t end = a.req_offsets ? a.req_offsets[r + 1] : a.M, n = end - q.off;
+  const int64_t len = a.cache_len[r], most = a.table_width * a.block_size;
+  if (q.off < 0 || n < 0 || end > a.M || n > kAttnMaxNodes || len < 0 || len > most || len > 0x7FFFFFFF - 1024) {
+    q.ok = false;
+    return q;
+  }
+  q.n = (int32_t)n;
+  q.len = (int32_t)len;
+  if (n == 0) return q;
+  q.tiles = (q.len + q.n + P::kBK - 1) / P::kBK;
+  q.row_units = (q.n * a.group + P::kRows - 1) / P::kRows;
+  return q;
+}
+
+__device__ __forceinline__ int64_t share(int64_t total, int ctas, int c) { return total * c / ctas; }
+
+struct Start {
+  int64_t total, at;  // all tiles; the place of the wanted tile within its request
+  int32_t r, ctas;
+};
+
+// Total number of tiles and, for CTA c of the grid, the request in which its share begins
+// (every thread of the block calls this; scratch: 2 + threads/32 int64 of shared memory).
+template <int D>
+__device__ __forceinline__ Start find_start(const AttnArgs& a, int c, int threads, int64_t* scratch, int32_t* bad) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = threads >> 5;
+  int64_t mine = 0, sum = 0;
+  for (int r = tid; r < a.n_req; r += threads) {
+    const Req q = load_request<D>(a, r);
+    if (!q.ok && bad) *bad = 1;
+    mine = (int64_t)q.tiles * q.row_units * a.n_heads;
+    sum += mine;
+  }
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+  if (lane == 0) scratch[2 + warp] = sum;
+  __syncthreads();
+  Start s{0, 0, 0, 0};
+  for (int w = 0; w < warps; ++w) s.total += scratch[2 + w];
+  s.ctas = (int32_t)(s.total < kAttnCtas ? s.total : kAttnCtas);
+  if (s.ctas == 0 || c >= s.ctas) return s;
+  const int64_t want = share(s.total, s.ctas, c);
+  if (a.n_req == 1) {
+    s.at = want;
+    return s;
+  }
+  int64_t carry = 0;
+  for (int r0 = 0; r0 < a.n_req; r0 += threads) {  // one pass unless there are more requests than threads
+    const int r = r0 + tid;
+    int64_t w = mine;
+    if (a.n_req > threads) {
+      w = 0;
+      if (r < a.n_req) {
+        const Req q = load_request<D>(a, r);
+        w = (int64_t)q.tiles * q.row_units * a.n_heads;
+      }
+    } else if (r >= a.n_req) {
+      w = 0;
+    }
+    int64_t v = w;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t u = __shfl_up_sync(0xFFFFFFFFu, v, o);
+      if (lane >= o) v += u;
+    }
+    __syncthreads();
+    if (lane == 31) scratch[2 + warp] = v;
+    __syncthreads();
+    int64_t before = carry + v - w;
+    for (int i = 0; i < warps; ++i) {
+      if (i < warp) before += scratch[2 + i];
+      carry += scratch[2 + i];
+    }
+    if (want >= before && want < before + w) {
+      scratch[0] = r;
+      scratch[1] = want - before;
+    }
+    if (want < carry) break;
+  }
+  __syncthreads();
+  s.r = (int32_t)scratch[0];
+  s.at = scratch[1];
+  return s;
+}
+
+// The parts of a CTA's share, in order.  Every role of the CTA walks them for itself.
+struct Part {
+  Req q;
+  int32_t r, h, row0, rows;  // rows row0 .. row0 + rows - 1 of the request's nodes * group
+  int32_t ta, tb;            // tiles
+};
+
+template <int D>
+struct Walk {
+  int64_t at, left;
+  int32_t r;
+  bool fresh;
+  Req q;
+
+  __device__ __forceinline__ Walk(const Start& s, int c)
+      : at(s.at), left(c < s.ctas ? share(s.total, s.ctas, c + 1) - share(s.total, s.ctas, c) : 0), r(s.r), fresh(true) {}
+
+  __device__ __forceinline__ bool next(const AttnArgs& a, Part& p) {
+    if (left <= 0) return false;
+    if (fresh) {
+      while ((q = load_request<D>(a, r)).tiles == 0) ++r;  // left > 0: a request with tiles follows
+      fresh = false;
+    }
+    const int64_t u = at / q.tiles;
+    p.q = q;
+    p.r = r;
+    p.ta = (int32_t)(at - u * q.tiles);
+    const int64_t take = left < q.tiles - p.ta ? left : q.tiles - p.ta;
+    p.tb = p.ta + (int32_t)take;
+    p.h = (int32_t)(u % a.n_heads);
+    p.row0 = (int32_t)(u / a.n_heads) * AttnPlan<D>::kRows;
+    p.rows = min(AttnPlan<D>::kRows, q.n * a.group - p.row0);
+    at += take;
+    left -= take;
+    if (at == (int64_t)q.tiles * q.row_units * a.n_heads) {
+      ++r;
+      at = 0;
+      fresh = true;
+    }
+    return true;
+  }
+};
+
+// ---------------------------------------------------------------- PTX
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+__device__ __forceinline__ void cp_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float v[32]) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,"
+      "%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t r[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// A from tensor memory, B from shared memory.
+__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(
+          d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+// Shared-memory descriptor of V as the second operand of O = P V: rows are keys, 64 columns
+// (128 bytes, swizzled) each; 8 keys are 1024 bytes apart, the next 64 columns `slab` bytes.
+__device__ __forceinline__ uint64_t umma_desc_v(uint32_t saddr, uint32_t slab) {
+  return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(slab >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+constexpr uint32_t kTransposeB = 1u << 16;
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
+// ---------------------------------------------------------------- the kernel
+
+struct Shared {
+  uint32_t base;         // shared-memory address of the block
+  uint8_t* sm;
+  volatile int32_t* abort;
+  uint32_t full, empty, q_full, q_free, s_full, p_full, o_done, unit_end, fin, meta, reset, drain;
+};
+
+// A bounded wait; one that runs out stops every role of the CTA.
+__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int32_t* abort) {
+  const long long start = clock64();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*abort) return false;
+    if (clock64() - start > kWaitCycles) {
+      *abort = 1;
+      return false;
+    }
+  }
+  return true;
+}
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, const Shared& s) {
+  if (mbar_try_wait(bar, parity)) return true;
+  return wait_slow(bar, parity, s.abort);
+}
+// The same answer for the whole warp, whose next steps (tensor memory accesses, shuffles) take
+// all of its threads.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, const Shared& s) {
+  return __all_sync(0xFFFFFFFFu, wait(bar, parity, s));
+}
+
+// Which tile the item-th ring entry of a part holds, in the order in which the MMA warp
+// takes them.  Rows in two halves: K0 V0 K1 V1 ...; tiles in turn: K0 K1 V0 K2 V1 ... V(n-1).
+__device__ __forceinline__ int ring_tile(int item, int cnt, bool two, bool& is_v) {
+  if (two) {
+    is_v = item & 1;
+    return item >> 1;
+  }
+  if (item == 2 * cnt - 1) {
+    is_v = true;
+    return cnt - 1;
+  }
+  if (item < 2) {
+    is_v = false;
+    return item;
+  }
+  is_v = !(item & 1);
+  return is_v ? (item - 2) >> 1 : (item + 1) >> 1;
 }
 
 template <int D>
-__global__ void __launch_bounds__(kAttnThreads) k_tree_attn(AttnArgs a) {
-  constexpr int kCols = (D + kAttnThreads - 1) / kAttnThreads;
-  __shared__ float qs[D], ps[kAttnThreads], red[kAttnThreads / 32];
-  __shared__ const uint16_t* vrow[kAttnThreads];
-  __shared__ bool anc[kAttnMaxNodes];
-  const int tid = threadIdx.x;
-  const int64_t m = blockIdx.x;
-  const int hq = blockIdx.y, h = hq / a.group;
-  int r = 0;
-  int64_t off = 0, end = a.M;
-  if (a.req_offsets) {
-    while (r < a.n_req && a.req_offsets[r + 1] <= m) ++r;
-    if (r == a.n_req) return;
-    off = a.req_offsets[r];
-    end = a.req_offsets[r + 1];
-    if (off > m) return;
+__device__ bool produce(const AttnArgs& a, const Shared& s, Walk<D> walk) {
+  using P = AttnPlan<D>;
+  constexpr int CPR = D / 8;              // 16-byte chunks of a row
+  constexpr int RPW = 32 / CPR;           // rows a warp copies at once
+  constexpr int IT = P::kBK / (4 * RPW);  // rounds of a tile
+  const int pt = threadIdx.x - P::kSoftmaxThreads, pw = pt >> 5, lane = pt & 31;
+  const int chunk = lane % CPR, sub = lane / CPR;
+  uint32_t* nf_all = reinterpret_cast<uint32_t*>(s.sm + P::kNf);
+  int32_t* bad_all = reinterpret_cast<int32_t*>(s.sm + P::kBad);
+  uint32_t entry = 0;  // ring entries so far
+  Part p;
+  for (int unit = 0; walk.next(a, p); ++unit) {
+    const int ring = unit & (kMetaRing - 1);
+    uint32_t* nf = nf_all + ring * 8;
+    int32_t* bad = bad_all + ring;
+    // ---- the unit's tree, if the part reaches it
+    if (pt < 8) nf[pt] = 0;
+    if (pt == 8) *bad = 0;
+    mbar_arrive(s.reset);
+    if (!wait_warp(s.reset, unit & 1, s)) return false;
+    if ((int64_t)p.tb * P::kBK > p.q.len) {
+      uint8_t* par = s.sm + P::kPar + ring * kAttnMaxNodes;
+      for (int i = pt; i < p.q.n; i += 128) {
+        const int32_t x = a.parent[p.q.off + i];
+        const bool in = i == 0 ? x == -1 : x >= 0 && x < i;
+        par[i] = in && i ? (uint8_t)x : (uint8_t)255;  // 255: no parent
+        if (!in) atomicOr(bad, kAttnBadRequest);
+      }
+    }
+    mbar_arrive(s.meta + 8 * ring);
+    // ---- query rows, zero past the unit's
+    if (unit > 0 && !wait_warp(s.q_free, (unit - 1) & 1, s)) return false;
+    const int q_rows = p.rows > 128 ? 256 : 128;
+    for (int row0 = 0; row0 < q_rows; row0 += 4 * RPW) {
+      const int row = row0 + pw * RPW + sub, g = p.row0 + row, node = g / a.group;
+      const bool in = row < p.rows;
+      const uint16_t* src = in ? a.q + (p.q.off + node) * a.q_stride + (int64_t)(p.h * a.group + g - node * a.group) * D + chunk * 8
+                               : a.q;
+      cp16(s.base + P::kQ + (row >> 7) * P::kQTile + (chunk >> 3) * 16384 + (row & 127) * 128 +
+               (((chunk & 7) ^ (row & 7)) << 4),
+           src, in);
+    }
+    cp_arrive(s.q_full);
+    // ---- K and V tiles
+    const int cnt = p.tb - p.ta;
+    const bool two = P::kWG == 2 && p.rows > 128;
+    const int32_t* table = a.table + p.r * a.table_stride;
+    // lane L looks up the row that the warp copies in round L / RPW as its (L % RPW)-th
+    auto lookup = [&](int item) -> const uint16_t* {
+      bool is_v;
+      const int tile = p.ta + ring_tile(item, cnt, two, is_v);
+      const int row = (lane / RPW) * 4 * RPW + pw * RPW + lane % RPW;
+      const int32_t j = tile * P::kBK + row;
+      if (lane >= IT * RPW) return nullptr;
+      if (j < p.q.len) {
+        const int32_t b = j / a.block_size, id = table[b];
+        if ((uint32_t)id >= (uint64_t)a.n_blocks) {
+          atomicOr(bad, kAttnBadBlock);
+          return nullptr;
+        }
+        return (is_v ? a.vc : a.kc) + (int64_t)id * a.block_stride + (int64_t)(j - b * a.block_size) * a.token_stride +
+               (int64_t)p.h * a.head_stride;
+      }
+      if (j - p.q.len < p.q.n)
+        return is_v ? a.v + (p.q.off + j - p.q.len) * a.v_stride + (int64_t)p.h * D
+                    : a.k + (p.q.off + j - p.q.len) * a.k_stride + (int64_t)p.h * D;
+      return nullptr;
+    };
+    const uint16_t* mine = lookup(0);
+    for (int item = 0; item < 2 * cnt; ++item, ++entry) {
+      bool is_v;
+      const int tile = p.ta + ring_tile(item, cnt, two, is_v);
+      const uint16_t* ahead = item + 1 < 2 * cnt ? lookup(item + 1) : nullptr;
+      const uint32_t slot = entry % P::kSlots, round = entry / P::kSlots;
+      if (round > 0 && !wait_warp(s.empty + 8 * slot, (round - 1) & 1, s)) return false;
+      const uint32_t dst = s.base + P::kRing + slot * P::kSlotBytes;
+#pragma unroll
+      for (int it = 0; it < IT; ++it) {
+        const uint16_t* src =
+            reinterpret_cast<const uint16_t*>(__shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(mine), it * RPW + sub));
+        const int row = it * 4 * RPW + pw * RPW + sub;
+        cp16(dst + (chunk >> 3) * (P::kBK * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4),
+             src ? src + chunk * 8 : a.kc, src != nullptr);
+      }
+      if ((int64_t)(tile + 1) * P::kBK > p.q.len && is_v) {
+        // A tile with drafted nodes: an infinity or a NaN in a node's V would reach every row
+        // (0 * inf), also those that do not attend to it.  It is taken out here, the node
+        // marked, and the rows that do attend to it get it back at the end.
+        cp_wait_all();
+        for (int it = 0; it < IT; ++it) {
+          const int row = it * 4 * RPW + pw * RPW + sub;
+          const int32_t node = tile * P::kBK + row - p.q.len;
+          if (node < 0 || node >= p.q.n) continue;
+          const uint32_t at = dst + (chunk >> 3) * (P::kBK * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
+          const uint4 x = lds128(at);
+          uint32_t w[4] = {x.x, x.y, x.z, x.w};
+          bool found = false;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if ((w[i] & 0x7F80u) == 0x7F80u) w[i] &= 0xFFFF0000u, found = true;
+            if ((w[i] & 0x7F800000u) == 0x7F800000u) w[i] &= 0xFFFFu, found = true;
+          }
+          if (found) {
+            sts128(at, w[0], w[1], w[2], w[3]);
+            atomicOr(&nf[node >> 5], 1u << (node & 31));
+          }
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(s.full + 8 * slot);
+      } else {
+        cp_arrive(s.full + 8 * slot);
+      }
+      mine = ahead;
+    }
   }
-  const int64_t n64 = end - off, len = a.cache_len[r];
-  bool ok = off >= 0 && end <= a.M && n64 <= kAttnMaxNodes && len >= 0 && len <= a.table_width * a.block_size;
-  const int n = ok ? (int)n64 : 0;
-  for (int i = tid; i < n; i += kAttnThreads) {
-    const int32_t p = a.parent[off + i];
-    ok = ok && (i == 0 ? p == -1 : p >= 0 && p < i);
-    anc[i] = false;
+  cp_wait_all();
+  return true;
+}
+
+template <int D>
+__device__ bool issue_mma(const AttnArgs& a, const Shared& s, Walk<D> walk, uint32_t tmem) {
+  using P = AttnPlan<D>;
+  constexpr uint32_t kIdS = umma_idesc_n(P::kBK), kIdO = umma_idesc_n(D) | kTransposeB;
+  uint32_t entry = 0, p_seen[2] = {0, 0}, o_count[2] = {0, 0};
+  Part p;
+  auto take = [&](uint32_t& addr, uint32_t& slot) {  // the next ring entry, filled
+    slot = entry % P::kSlots;
+    addr = s.base + P::kRing + slot * P::kSlotBytes;
+    if (!wait(s.full + 8 * slot, (entry / P::kSlots) & 1, s)) return false;
+    fence_proxy_async_smem();  // the copies of other threads, before the tensor core reads them
+    ++entry;
+    return true;
+  };
+  auto scores = [&](int q_tile, uint32_t k_addr, int b) {
+    const uint32_t q_addr = s.base + P::kQ + q_tile * P::kQTile;
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks)
+      umma_bf16(tmem + P::kS(b), umma_desc(q_addr + (ks >> 2) * 16384 + (ks & 3) * 32),
+                umma_desc(k_addr + (ks >> 2) * (P::kBK * 128) + (ks & 3) * 32), kIdS, ks > 0);
+    umma_commit(s.s_full + 8 * b);
+  };
+  auto output = [&](int o, int b, uint32_t v_addr, bool acc) {  // o_done goes by the buffer of P
+#pragma unroll
+    for (int ks = 0; ks < P::kBK / 16; ++ks) {  // 32 keys: 16 columns of upper halves, 16 of lower ones
+      const uint32_t p_addr = tmem + P::kS(b) + (ks >> 1) * 32 + (ks & 1) * 8;
+      const uint64_t v_desc = umma_desc_v(v_addr + ks * 2048, P::kBK * 128);
+      umma_bf16_ts(tmem + P::kO(o), p_addr, v_desc, kIdO, acc || ks > 0);
+      umma_bf16_ts(tmem + P::kO(o), p_addr + 16, v_desc, kIdO, 1);
+    }
+    umma_commit(s.o_done + 8 * b);
+    ++o_count[b];
+  };
+  // New scores overwrite the P of an earlier product.  Products with different results are not
+  // ordered among themselves, so that product has to have ended.
+  auto drained = [&](int b) { return o_count[b] == 0 || wait(s.o_done + 8 * b, (o_count[b] - 1) & 1, s); };
+  auto softmaxed = [&](int b) {
+    if (!wait(s.p_full + 8 * b, p_seen[b] & 1, s)) return false;
+    ++p_seen[b];
+    tc_fence_after();
+    return true;
+  };
+  for (int unit = 0; walk.next(a, p); ++unit) {
+    const int cnt = p.tb - p.ta;
+    const bool two = P::kWG == 2 && p.rows > 128;
+    uint32_t k_addr, v_addr, k_slot, v_slot;
+    if (!wait(s.q_full, unit & 1, s)) return false;
+    if (!take(k_addr, k_slot)) return false;
+    if (!drained(0) || !drained(1)) return false;
+    tc_fence_after();
+    scores(0, k_addr, 0);
+    if (two) scores(1, k_addr, 1);
+    umma_commit(s.empty + 8 * k_slot);
+    if (!two && cnt > 1) {
+      if (!take(k_addr, k_slot)) return false;
+      scores(0, k_addr, 1);
+      umma_commit(s.empty + 8 * k_slot);
+    }
+    if (cnt <= (two ? 1 : 2)) umma_commit(s.q_free);
+    if (unit > 0 && !wait(s.unit_end, (unit - 1) & 1, s)) return false;  // the last unit's outputs have been read
+    for (int i = 0; i < cnt; ++i) {
+      if (!take(v_addr, v_slot)) return false;
+      if (two) {
+        if (!softmaxed(0)) return false;
+        output(0, 0, v_addr, i > 0);
+        if (i + 1 < cnt) {
+          if (!take(k_addr, k_slot) || !drained(0)) return false;
+          scores(0, k_addr, 0);
+        }
+        if (!softmaxed(1)) return false;
+        output(P::kWG - 1, 1, v_addr, i > 0);
+        umma_commit(s.empty + 8 * v_slot);
+        if (i + 1 < cnt) {
+          if (!drained(1)) return false;
+          scores(1, k_addr, 1);
+          umma_commit(s.empty + 8 * k_slot);
+          if (i + 2 == cnt) umma_commit(s.q_free);
+        }
+      } else {
+        const int b = i & 1, o = P::kWG == 2 ? b : 0;
+        if (!softmaxed(b)) return false;
+        output(o, b, v_addr, P::kWG == 2 ? i >= 2 : i >= 1);
+        umma_commit(s.empty + 8 * v_slot);
+        if (i + 2 < cnt) {
+          if (!take(k_addr, k_slot) || !drained(b)) return false;
+          scores(0, k_addr, b);
+          umma_commit(s.empty + 8 * k_slot);
+          if (i + 3 == cnt) umma_commit(s.q_free);
+        }
+      }
+    }
   }
-  if (!__syncthreads_and(ok)) {
-    if (tid == 0) atomicOr(a.status, kAttnBadRequest);
+  return true;
+}
+
+template <int D>
+__device__ bool softmax(const AttnArgs& a, const Shared& s, Walk<D> walk, uint32_t tmem, int c) {
+  using P = AttnPlan<D>;
+  constexpr int NW = P::kBK / 32;
+  const int g = threadIdx.x >> 7, lane_row = threadIdx.x & 127;  // warpgroup, tensor memory lane
+  const uint32_t lane_base = tmem + ((uint32_t)((threadIdx.x >> 5) & 3) << 21);
+  float2* ml = reinterpret_cast<float2*>(s.sm + P::kML);
+  uint32_t s_seen[2] = {0, 0}, o_seen[2] = {0, 0}, fin_seen = 0;
+  // Every product is waited for once and in order: a wait that skipped one could take its
+  // end for the next one's.
+  auto product_done = [&](int b) {
+    if (!wait_warp(s.o_done + 8 * b, o_seen[b] & 1, s)) return false;
+    ++o_seen[b];
+    tc_fence_after();
+    return true;
+  };
+  Part p;
+  for (int unit = 0; walk.next(a, p); ++unit) {
+    const int ring = unit & (kMetaRing - 1), cnt = p.tb - p.ta;
+    const bool two = P::kWG == 2 && p.rows > 128;
+    const int row = (two ? g * 128 : 0) + lane_row;
+    const bool live = row < p.rows;
+    const int node = live ? (p.row0 + row) / a.group : -1;
+    const uint8_t* par = s.sm + P::kPar + ring * kAttnMaxNodes;
+    if (!wait_warp(s.meta + 8 * ring, (unit / kMetaRing) & 1, s)) return false;
+    float ref = -INFINITY, sum = 0.0f;  // log2 reference of the row, sum of its probabilities
+    int done = 0;                       // tiles of this warpgroup
+    const int first = P::kWG == 2 && !two ? g : 0, step = P::kWG == 2 && !two ? 2 : 1;
+    for (int i = first; i < cnt; i += step, ++done) {
+      const int b = P::kWG == 2 ? g : i & 1;
+      const int32_t j0 = (p.ta + i) * P::kBK, lim = p.q.len - j0;  // cached tokens from the tile's first key on
+      const bool masked = lim < P::kBK;
+      uint32_t may[NW];
+      if (masked) {
+#pragma unroll
+        for (int w = 0; w < NW; ++w)
+          may[w] = lim >= 32 * (w + 1) ? 0xFFFFFFFFu : lim <= 32 * w ? 0u : (1u << (lim - 32 * w)) - 1u;
+        for (int x = node; x >= 0;) {
+          const int at = x + lim;
+          if (at < 0) break;
+          if (at < P::kBK) {
+#pragma unroll
+            for (int w = 0; w < NW; ++w)
+              if ((at >> 5) == w) may[w] |= 1u << (at & 31);
+          }
+          const int up = par[x];
+          if (up == 255) break;
+          x = up;
+        }
+      }
+      if (!wait_warp(s.s_full + 8 * b, s_seen[b] & 1, s)) return false;
+      ++s_seen[b];
+      tc_fence_after();
+      const uint32_t st = lane_base + P::kS(b);
+      float top = -INFINITY, v[32];
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        tmem_ld32(st + w * 32, v);
+        if (masked) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = (may[w] >> e) & 1u ? v[e] : -INFINITY;
+        }
+#pragma unroll
+        for (int e = 0; e < 32; ++e) top = fmaxf(top, v[e]);
+      }
+      const float want = top * a.scale_log2;
+      const bool move = want - ref > kRefSlack;
+      const int b_last = P::kWG == 2 ? g : b ^ 1;
+      bool waited = done == 0;
+      if (__any_sync(0xFFFFFFFFu, move)) {
+        const float next = move ? want : ref;
+        if (done > 0) {
+          const float fix = move ? ex2(ref - next) : 1.0f;
+          sum *= fix;
+          if (!product_done(b_last)) return false;
+          waited = true;
+#pragma unroll 1
+          for (int d = 0; d < D; d += 32) {
+            tmem_ld32(lane_base + P::kO(P::kWG == 2 ? g : 0) + d, v);
+            uint32_t u[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(v[e] * fix);
+            tmem_st16(lane_base + P::kO(P::kWG == 2 ? g : 0) + d, u);
+            tmem_st16(lane_base + P::kO(P::kWG == 2 ? g : 0) + d + 16, u + 16);
+          }
+        }
+        ref = next;
+      }
+      const float m = ref == -INFINITY ? 0.0f : ref;
+      float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        tmem_ld32(st + w * 32, v);
+        uint32_t u[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          v[e] = ex2(fmaf(v[e], a.scale_log2, -m));
+          if (masked) v[e] = (may[w] >> e) & 1u ? v[e] : 0.0f;
+          part[e & 3] += v[e];
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const uint32_t p0 = __float_as_uint(v[2 * e]), p1 = __float_as_uint(v[2 * e + 1]);
+          u[e] = __byte_perm(p0, p1, 0x7632);
+          u[16 + e] = pack2(fmaf(v[2 * e], kUp, -__uint_as_float(p0 & 0xFFFF0000u)),
+                            fmaf(v[2 * e + 1], kUp, -__uint_as_float(p1 & 0xFFFF0000u)));
+        }
+        tmem_st16(st + w * 32, u);
+        tmem_st16(st + w * 32 + 16, u + 16);
+      }
+      sum += (part[0] + part[1]) + (part[2] + part[3]);
+      tmem_st_wait();
+      if (!waited && !product_done(b_last)) return false;
+      tc_fence_before();
+      mbar_arrive(s.p_full + 8 * b);
+    }
+    // ---- the part's result
+    if (done > 0 && !product_done(P::kWG == 2 ? g : (cnt - 1) & 1)) return false;
+    const bool merge = P::kWG == 2 && !two && cnt > 1;
+    if (merge && g == 1) ml[lane_row] = make_float2(ref, sum);
+    if (P::kWG == 2 && !two && g == 1) {
+      if (merge) {
+        tc_fence_before();
+        mbar_arrive(s.fin);
+      }
+      mbar_arrive(s.unit_end);
+      if (!wait_warp(s.unit_end, unit & 1, s)) return false;  // it may have had no tile: not to run ahead
+      continue;
+    }
+    float w0 = 1.0f, w1 = 0.0f;
+    if (merge) {
+      if (!wait_warp(s.fin, fin_seen & 1, s)) return false;
+      ++fin_seen;
+      tc_fence_after();
+      const float2 other = ml[lane_row];
+      const float both = fmaxf(ref, other.x), m = both == -INFINITY ? 0.0f : both;
+      w0 = ex2(ref - m);
+      w1 = ex2(other.x - m);
+      sum = w0 * sum + w1 * other.y;
+      ref = both;
+    }
+    const bool whole = p.ta == 0 && p.tb == p.q.tiles;
+    const int32_t bad = reinterpret_cast<volatile int32_t*>(s.sm + P::kBad)[ring];
+    const uint32_t* nf = reinterpret_cast<const uint32_t*>(s.sm + P::kNf) + ring * 8;
+    uint32_t any_nf = 0;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) any_nf |= nf[w];
+    const int part_slot = 2 * c + (p.ta > 0 ? 0 : 1);
+    float* po = a.part_o + (int64_t)part_slot * D * a.row_cap;
+    const int qrow = p.row0 + row, head = p.h * a.group + (live ? qrow - node * a.group : 0);
+    uint16_t* out = a.out + ((p.q.off + (live ? node : 0)) * a.n_q_heads + head) * (int64_t)D;
+    if (whole && bad && lane_row == 0) atomicOr(a.status, bad);
+    if (!whole && lane_row == 0 && row == 0) a.part_bad[part_slot] = bad;
+    if (!whole && live) *reinterpret_cast<float2*>(a.part_ml + 2 * ((int64_t)part_slot * a.row_cap + row)) = make_float2(ref, sum);
+    const float inv = 1.0f / sum;
+#pragma unroll 1
+    for (int d = 0; d < D; d += 16) {
+      float v[16];
+      tmem_ld16(lane_base + P::kO(two ? g : 0) + d, v);
+      if (merge) {
+        float x[16];
+        tmem_ld16(lane_base + P::kO(1) + d, x);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] = w0 * v[e] + w1 * x[e];
+      }
+      if (any_nf && live) {
+        for (int x = node;;) {
+          if (nf[x >> 5] >> (x & 31) & 1u) {
+            const uint16_t* vr = a.v + (p.q.off + x) * a.v_stride + (int64_t)p.h * D + d;
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if ((vr[e] & 0x7F80u) == 0x7F80u) v[e] += __uint_as_float((uint32_t)vr[e] << 16);
+          }
+          const int up = par[x];
+          if (up == 255) break;
+          x = up;
+        }
+      }
+      if (!live) continue;
+      if (whole) {
+        if (!bad) {
+#pragma unroll
+          for (int e = 0; e < 16; e += 8) {
+            uint4 x;
+            x.x = pack2(v[e] * inv, v[e + 1] * inv);
+            x.y = pack2(v[e + 2] * inv, v[e + 3] * inv);
+            x.z = pack2(v[e + 4] * inv, v[e + 5] * inv);
+            x.w = pack2(v[e + 6] * inv, v[e + 7] * inv);
+            *reinterpret_cast<uint4*>(out + d + e) = x;
+          }
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16; e += 4)
+          *reinterpret_cast<float4*>(po + ((int64_t)(d + e) / 4 * a.row_cap + row) * 4) =
+              make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+      }
+    }
+    tc_fence_before();
+    mbar_arrive(s.unit_end);
+    if (g == 1 && !wait_warp(s.unit_end, unit & 1, s)) return false;
+  }
+  return true;
+}
+
+template <int D>
+__global__ void __launch_bounds__(AttnPlan<D>::kThreads, 1) k_tree_attn(AttnArgs a) {
+  using P = AttnPlan<D>;
+  extern __shared__ __align__(1024) uint8_t attn_sm[];
+  const int tid = threadIdx.x, warp = tid >> 5, c = blockIdx.x;
+  // the kernel that adds the parts may be set up meanwhile; it waits for this one's end
+  if (tid == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  Shared s;
+  s.sm = attn_sm;
+  s.base = smem_u32(attn_sm);
+  int32_t* misc = reinterpret_cast<int32_t*>(attn_sm + P::kMisc);
+  s.abort = misc + 1;
+  uint32_t bar = s.base + P::kBar;
+  auto bars = [&](int n) {
+    const uint32_t b = bar;
+    bar += 8 * n;
+    return b;
+  };
+  s.full = bars(P::kSlots);
+  s.empty = bars(P::kSlots);
+  s.s_full = bars(2);
+  s.p_full = bars(2);
+  s.o_done = bars(2);
+  s.unit_end = bars(1);
+  s.q_full = bars(1);
+  s.q_free = bars(1);
+  s.fin = bars(1);
+  s.meta = bars(kMetaRing);
+  s.reset = bars(1);
+  s.drain = bars(1);
+  if (tid == 0) {
+    for (int i = 0; i < P::kSlots; ++i) {
+      mbar_init(s.full + 8 * i, 128);
+      mbar_init(s.empty + 8 * i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(s.s_full + 8 * i, 1);
+      mbar_init(s.p_full + 8 * i, 128);
+      mbar_init(s.o_done + 8 * i, 1);
+    }
+    mbar_init(s.q_full, 128);
+    mbar_init(s.q_free, 1);
+    mbar_init(s.fin, 128);
+    mbar_init(s.unit_end, P::kSoftmaxThreads);
+    for (int i = 0; i < kMetaRing; ++i) mbar_init(s.meta + 8 * i, 128);
+    mbar_init(s.reset, 128);
+    mbar_init(s.drain, 1);
+    mbar_init_fence();
+    misc[1] = 0;  // abort
+    misc[2] = 0;  // a request out of range
+  }
+  __syncthreads();
+  const Start start = find_start<D>(a, c, P::kThreads, reinterpret_cast<int64_t*>(attn_sm + P::kRing), misc + 2);
+  __syncthreads();  // the sums' scratch is the ring's from here on
+  if (c == 0 && tid == 0 && misc[2]) atomicOr(a.status, kAttnBadRequest);
+  if (c >= start.ctas) return;
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(s.base + P::kMisc) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = (uint32_t)misc[0];
+  const Walk<D> walk(start, c);
+  bool ok = true;
+  if (warp < P::kSoftmaxThreads / 32) {
+    ok = softmax<D>(a, s, walk, tmem, c);
+  } else if (warp < P::kSoftmaxThreads / 32 + 4) {
+    ok = produce<D>(a, s, walk);
+    if (!ok) cp_wait_all();
+  } else if ((tid & 31) == 0) {
+    ok = issue_mma<D>(a, s, walk, tmem);
+    if (!ok) {  // nothing may be in flight when tensor memory goes back
+      umma_commit(s.drain);
+      mbar_wait_bounded(s.drain, 0);
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  }
+  if (tid == 0 && misc[1]) atomicOr(a.status, kAttnTimeout);
+}
+
+// Adds the parts of the units that several CTAs worked on.  Block (c, y): the unit in which
+// CTA c + 1's share begins, if that is the first share to begin inside it; the y-th part
+// of its rows.
+constexpr int kJoinThreads = 256;
+
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) k_tree_attn_join(AttnArgs a) {
+  __shared__ int64_t scratch[2 + kJoinThreads / 32];
+  const int tid = threadIdx.x, c = blockIdx.x + 1;
+  const Start s = find_start<D>(a, c, kJoinThreads, scratch, nullptr);
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are the previous kernel's
+  if (c >= s.ctas) return;
+  Part p;
+  Walk<D> walk(s, c);
+  walk.next(a, p);
+  if (p.ta == 0) return;
+  const int64_t begin = share(s.total, s.ctas, c) - p.ta, end = begin + p.q.tiles;
+  if (share(s.total, s.ctas, c - 1) > begin) return;
+  int last = c;  // the parts are CTA c - 1's second slot and the first slots of c .. last
+  while (last + 1 < s.ctas && share(s.total, s.ctas, last + 1) < end) ++last;
+  int32_t bad = 0;
+  for (int i = tid; i < p.q.n; i += kJoinThreads) {
+    const int32_t x = a.parent[p.q.off + i];
+    if (!(i == 0 ? x == -1 : x >= 0 && x < i)) bad |= kAttnBadRequest;
+  }
+  for (int i = c - 1 + tid; i <= last; i += kJoinThreads) bad |= a.part_bad[2 * i + (i < c ? 1 : 0)];
+  bad = (__syncthreads_or(bad & kAttnBadRequest) ? kAttnBadRequest : 0) | (__syncthreads_or(bad & kAttnBadBlock) ? kAttnBadBlock : 0);
+  if (bad) {
+    if (tid == 0) atomicOr(a.status, bad);
     return;
   }
-  const int32_t* table = a.table + r * a.table_stride;
-  for (int64_t b = tid; b * a.block_size < len; b += kAttnThreads) ok = ok && table[b] >= 0 && table[b] < a.n_blocks;
-  if (!__syncthreads_and(ok)) {
-    if (tid == 0) atomicOr(a.status, kAttnBadBlock);
-    return;
+  for (int e = blockIdx.y * kJoinThreads + tid; e < p.rows * (D / 4); e += gridDim.y * kJoinThreads) {
+    const int c4 = e / p.rows, row = e - c4 * p.rows;
+    auto slot = [&](int i) { return (int64_t)(2 * i + (i < c ? 1 : 0)); };
+    auto stat = [&](int i) { return *reinterpret_cast<const float2*>(a.part_ml + 2 * (slot(i) * a.row_cap + row)); };
+    float top = -INFINITY;
+    for (int i = c - 1; i <= last; ++i) top = fmaxf(top, stat(i).x);
+    const float m = top == -INFINITY ? 0.0f : top;
+    float sum = 0.0f;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int i = c - 1; i <= last; ++i) {
+      const float2 t = stat(i);
+      const float4 x = *reinterpret_cast<const float4*>(a.part_o + slot(i) * D * a.row_cap + ((int64_t)c4 * a.row_cap + row) * 4);
+      const float w = ex2(t.x - m);
+      sum += w * t.y;
+      o.x += w * x.x;
+      o.y += w * x.y;
+      o.z += w * x.z;
+      o.w += w * x.w;
+    }
+    const float inv = 1.0f / sum;
+    const int g = p.row0 + row, node = g / a.group;
+    uint16_t* out = a.out + ((p.q.off + node) * a.n_q_heads + p.h * a.group + (g - node * a.group)) * (int64_t)D + c4 * 4;
+    *reinterpret_cast<uint2*>(out) = make_uint2(pack2(o.x * inv, o.y * inv), pack2(o.z * inv, o.w * inv));
   }
-  if (tid == 0)
-    for (int32_t p = (int32_t)(m - off); p >= 0; p = a.parent[off + p]) anc[p] = true;
-  for (int d = tid; d < D; d += kAttnThreads) qs[d] = bf16_f(a.q[m * a.q_stride + hq * D + d]) * a.scale;
-  float acc[kCols] = {}, mx = -INFINITY, sum = 0.0f;
-  for (int64_t j0 = 0; j0 < len + n; j0 += kAttnThreads) {
-    __syncthreads();
-    const int64_t j = j0 + tid;
-    const uint16_t *kr = nullptr, *vr = nullptr;
-    if (j < len) {
-      const int64_t b = j / a.block_size, at = table[b] * a.block_stride + (j - b * a.block_size) * a.token_stride + h * a.head_stride;
-      kr = a.kc + at;
-      vr = a.vc + at;
-    } else if (j < len + n && anc[j - len]) {
-      kr = a.k + (off + j - len) * a.k_stride + h * D;
-      vr = a.v + (off + j - len) * a.v_stride + h * D;
-    }
-    float s = -INFINITY;
-    if (kr) {
-      s = 0.0f;
-      for (int d = 0; d < D; ++d) s = fmaf(qs[d], bf16_f(kr[d]), s);
-    }
-    float t = s;
-    for (int o = 16; o; o >>= 1) t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, o));
-    if ((tid & 31) == 0) red[tid >> 5] = t;
-    __syncthreads();
-    for (int w = 0; w < kAttnThreads / 32; ++w) t = fmaxf(t, red[w]);
-    const float top = fmaxf(mx, t), ref = top == -INFINITY ? 0.0f : top, fix = mx == -INFINITY ? 0.0f : expf(mx - ref);
-    mx = top;
-    ps[tid] = kr ? expf(s - ref) : 0.0f;
-    vrow[tid] = vr;
-    __syncthreads();
-    sum *= fix;
-    for (int c = 0; c < kCols; ++c) acc[c] *= fix;
-    for (int i = 0; i < kAttnThreads; ++i) {
-      if (!vrow[i]) continue;
-      sum += ps[i];
-      for (int c = 0; c < kCols; ++c)
-        if (tid + c * kAttnThreads < D) acc[c] = fmaf(ps[i], bf16_f(vrow[i][tid + c * kAttnThreads]), acc[c]);
-    }
+}
+
+int64_t row_cap(int64_t M, int64_t group, int64_t D) {
+  const int64_t rows = M * group, most = D == 256 ? 128 : 256;
+  return rows >= most ? most : (rows + 31) / 32 * 32;
+}
+
+template <int D>
+int launch_attn(const AttnArgs& a, cudaStream_t s) {
+  using P = AttnPlan<D>;
+  static int configured[64] = {0};
+  int dev = 0;
+  W12_CUDA_TRY(cudaGetDevice(&dev));
+  if (dev >= 64 || !configured[dev]) {
+    W12_CUDA_TRY(cudaFuncSetAttribute(k_tree_attn<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kBytes));
+    if (dev < 64) configured[dev] = 1;
   }
-  for (int c = 0; c < kCols; ++c)
-    if (tid + c * kAttnThreads < D)
-      a.out[(m * a.n_q_heads + hq) * D + tid + c * kAttnThreads] = f_bf16(acc[c] / sum);
+  k_tree_attn<D><<<kAttnCtas, P::kThreads, P::kBytes, s>>>(a);
+  W12_LAUNCH_CHECK("tree_attn kernel");
+  const int64_t items = (int64_t)a.row_cap * (D / 4);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kAttnCtas - 1, (unsigned)(items <= 2 * kJoinThreads ? 1 : items <= 8 * kJoinThreads ? 4 : 8));
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  W12_CUDA_TRY(cudaLaunchKernelEx(&cfg, k_tree_attn_join<D>, a));
+  W12_LAUNCH_CHECK("tree_attn: joining kernel");
+  return W12_OK;
+}
+
+struct AttnWs {
+  size_t o, ml, bad, total;
+};
+
+AttnWs attn_ws(int64_t M, int64_t group, int64_t D) {
+  auto up = [](size_t b) { return (b + 255) & ~(size_t)255; };
+  const size_t slots = 2 * (size_t)kAttnCtas, rows = (size_t)row_cap(M, group, D);
+  AttnWs w{};
+  w.o = 0;
+  w.ml = up(slots * rows * (size_t)D * 4);
+  w.bad = w.ml + up(slots * rows * 8);
+  w.total = w.bad + up(slots * 4);
+  return w;
 }
 
 }  // namespace
@@ -125,7 +966,10 @@ using namespace w12;
 extern "C" {
 
 size_t tree_attn_workspace_size(int64_t M, int32_t n_req, int64_t n_q_heads, int64_t n_heads, int64_t head_dim) {
-  return M >= 1 && n_req >= 1 && n_q_heads >= 1 && n_heads >= 1 && head_dim >= 1 ? 256 : 0;
+  if (M < 1 || n_req < 1 || n_heads < 1 || n_q_heads < n_heads || n_q_heads % n_heads || M > 0x7FFFFFFF ||
+      (head_dim != 64 && head_dim != 128 && head_dim != 256))
+    return 0;
+  return attn_ws(M, n_q_heads / n_heads, head_dim).total;
 }
 
 int tree_attn(const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_stride, const uint16_t* v,
@@ -153,9 +997,8 @@ int tree_attn(const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_
       ((q_stride | k_stride | v_stride) & 7) || q_stride < 0 || k_stride < 0 || v_stride < 0)
     return fail(W12_ERR_INVALID_ARG,
                 "tree_attn: q, k, v, out and ws must be 16-byte aligned, strides non-negative multiples of 8");
-  if (ws_bytes < tree_attn_workspace_size(M, n_req, n_q_heads, H, D))
-    return fail(W12_ERR_BUFFER_TOO_SMALL, "tree_attn: workspace %zu < %zu", ws_bytes,
-                tree_attn_workspace_size(M, n_req, n_q_heads, H, D));
+  const AttnWs w = attn_ws(M, n_q_heads / H, D);
+  if (ws_bytes < w.total) return fail(W12_ERR_BUFFER_TOO_SMALL, "tree_attn: workspace %zu < %zu", ws_bytes, w.total);
   AttnArgs a{};
   a.q = q;
   a.k = k;
@@ -179,16 +1022,18 @@ int tree_attn(const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_
   a.n_req = n_req;
   a.block_size = cache->block_size;
   a.group = (int32_t)(n_q_heads / H);
+  a.n_heads = (int32_t)H;
   a.n_q_heads = (int32_t)n_q_heads;
-  a.scale = scale;
+  a.row_cap = (int32_t)row_cap(M, a.group, D);
+  a.scale_log2 = scale * 1.4426950408889634f;
   a.out = out;
   a.status = status;
-  const dim3 grid((unsigned)M, (unsigned)n_q_heads);
-  if (D == 64) k_tree_attn<64><<<grid, kAttnThreads, 0, (cudaStream_t)stream>>>(a);
-  else if (D == 128) k_tree_attn<128><<<grid, kAttnThreads, 0, (cudaStream_t)stream>>>(a);
-  else k_tree_attn<256><<<grid, kAttnThreads, 0, (cudaStream_t)stream>>>(a);
-  W12_LAUNCH_CHECK("tree_attn kernel");
-  return W12_OK;
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  a.part_o = reinterpret_cast<float*>(base + w.o);
+  a.part_ml = reinterpret_cast<float*>(base + w.ml);
+  a.part_bad = reinterpret_cast<int32_t*>(base + w.bad);
+  cudaStream_t s = (cudaStream_t)stream;
+  return D == 64 ? launch_attn<64>(a, s) : D == 128 ? launch_attn<128>(a, s) : launch_attn<256>(a, s);
 }
 
 }  // extern "C"

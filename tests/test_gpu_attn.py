@@ -219,6 +219,20 @@ def test_long_contexts(w12, d, hkv, group, nodes):
     assert torch.equal(out, again)                       # the same bits on every call
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("lens,counts", [([200] * 400, [1] * 400), ([1000, 40, 5000] * 40, [3, 60, 2] * 40),
+                                         ([130] * 90, [40, 1, 70] * 30)])
+def test_several_units_per_block(w12, d, lens, counts):
+    """More work than blocks: each takes several heads and requests in turn, and parts of some."""
+    p = Problem(len(lens), lens, counts, 2, 4, d, 16)
+    args = p.args(w12)
+    out, st = w12.tree_attn(*args)
+    p.check(out)
+    assert int(st) == 0
+    again, _ = w12.tree_attn(*args)
+    assert torch.equal(out, again)
+
+
 def test_peaked_and_flat_scores(w12):
     """Scores from -100 to 100 (one key takes all) and all alike; a running maximum that keeps rising."""
     for q_scale in (0.0, 0.01, 8.0, 24.0):
