@@ -18,11 +18,13 @@
 // into a ring of tiles that runs on across units.
 //
 // Per 128 keys of a head with D = 128, an SM's share of the memory rate is about 2800 cycles
-// (64 KB), its two products 1024, its exponentials 1024: the kernel is bound by the cache's
-// bytes up to 128 rows, whose padding costs nothing.  Up to 128 rows the two softmax
-// warpgroups take tiles in turn (each with its own S, O and statistics, added at the end);
-// above, they take 128 rows each of the same tile, so K and V are read once for 256 rows.
-// D = 256 fills tensor memory with one O: one warpgroup, two S in turn, tiles of 64 keys.
+// (64 KB), its two products 1536, its exponentials 1024: the kernel is bound by the cache's
+// bytes up to 128 rows, whose padding costs nothing.  Both softmax warpgroups work on
+// the same tile, half of its keys each (they share the row's lanes of tensor memory and
+// exchange the halves' maxima), so that scores computed ahead wait for no product.
+// Above 128 rows (D <= 128) a tile of keys meets two tiles of rows in turn, with an O each,
+// so K and V are read once for 256 rows.  D = 256 has room for one O: 128 rows, tiles of
+// 64 keys.
 #include <cmath>
 #include <cstdint>
 
@@ -37,7 +39,7 @@ namespace {
 constexpr int kAttnMaxNodes = 256;
 constexpr int32_t kAttnBadRequest = 1, kAttnBadBlock = 2, kAttnTimeout = 4;
 constexpr int kAttnCtas = 152;  // one per SM of a GB300; fewer SMs only run them in turn
-constexpr int kMetaRing = 4;     // units whose tree the producers may hold at once
+constexpr int kMetaRing = 2;     // units whose tree shared memory holds
 // P enters its product in two bf16 pieces, the upper one cut off, the lower one rounded: 2^-16
 // of P is lost instead of 2^-8.  The lower piece is taken of P (1 + 2^-20), so that it is above
 // zero wherever P is and an infinity in V stays one (no 0 * inf, no inf - inf).
@@ -60,28 +62,30 @@ struct AttnArgs {
 
 template <int D>
 struct AttnPlan {
-  static constexpr int kWG = D <= 128 ? 2 : 1;       // softmax warpgroups
-  static constexpr int kRows = 128 * kWG;            // rows of a unit
+  static constexpr int kRowTiles = D <= 128 ? 2 : 1;
+  static constexpr int kRows = 128 * kRowTiles;      // rows of a unit
   static constexpr int kBK = D <= 128 ? 128 : 64;    // keys of a tile
   static constexpr int kSlots = D == 64 ? 10 : 5;    // tiles of the ring
+  static constexpr int kSB = D <= 128 ? 3 : 4;       // score buffers in tensor memory
   static constexpr int kSlotBytes = kBK * D * 2;
-  static constexpr int kSoftmaxThreads = 128 * kWG;
+  static constexpr int kSoftmaxThreads = 256;
   static constexpr int kThreads = kSoftmaxThreads + 128 + 32;  // + producers + MMA warp
   static constexpr int kQ = 0;
   static constexpr int kQTile = 128 * D * 2;
-  static constexpr int kRing = kQ + kWG * kQTile;
-  static constexpr int kPar = kRing + kSlots * kSlotBytes;     // parents, kMetaRing x 256 bytes
-  static constexpr int kML = kPar + kMetaRing * kAttnMaxNodes; // 128 x (reference, sum)
-  static constexpr int kNf = kML + 128 * 8;                    // nodes with infinities or NaN in V, kMetaRing x 8 words
+  static constexpr int kRing = kQ + kRowTiles * kQTile;
+  static constexpr int kX = kRing + kSlots * kSlotBytes;       // what the halves exchange: 2 x 2 x 128 floats
+  static constexpr int kPar = kX + 2 * 2 * 128 * 4;            // parents, kMetaRing x 256 bytes
+  static constexpr int kNf = kPar + kMetaRing * kAttnMaxNodes; // nodes with infinities or NaN in V, kMetaRing x 8 words
   static constexpr int kBad = kNf + kMetaRing * 32;            // kMetaRing words
   static constexpr int kMisc = kBad + kMetaRing * 4;           // tensor memory address, abort, schedule
-  static constexpr int kBar = (kMisc + 48 + 7) & ~7;
-  static constexpr int kBytes = kBar + 8 * (2 * kSlots + 3 * 2 + 6 + kMetaRing);
+  static constexpr int kBar = (kMisc + 16 + 7) & ~7;
+  static constexpr int kBytes = kBar + 8 * (2 * kSlots + 3 * kSB + 5 + kMetaRing + 4);
   static_assert(kBytes <= 227 * 1024, "shared memory plan too large");
   static_assert(kThreads * 8 <= kSlots * kSlotBytes, "the ring holds the schedule's sums");
-  // tensor memory columns
-  static constexpr int kO(int g) { return g * 128; }
-  static constexpr int kS(int b) { return 256 + b * 128; }
+  // Tensor memory columns: O of the first tile of rows, then D <= 128: three score buffers, of
+  // which the first gives way to the second O where a unit has two tiles of rows; D = 256:
+  // four of 64 columns.
+  static constexpr int kO1 = 128, kS0 = D <= 128 ? 128 : 256, kSCols = kBK;
 };
 
 // ---------------------------------------------------------------- schedule
@@ -236,8 +240,9 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float v[32]) {
-  uint32_t r[32];
+// 32 lanes x 32 columns, on their way; tmem_wait32 makes them readable (and waits for every
+// load before it).
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t r[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,"
       "%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
@@ -246,6 +251,8 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float v[32]) {
         "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait32(uint32_t r[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
                  "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
@@ -253,8 +260,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float v[32]) {
                  "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
                :
                : "memory");
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t r[16]) {
@@ -301,7 +306,7 @@ struct Shared {
   uint32_t base;         // shared-memory address of the block
   uint8_t* sm;
   volatile int32_t* abort;
-  uint32_t full, empty, q_full, q_free, s_full, p_full, o_done, unit_end, fin, meta, reset, drain;
+  uint32_t full, empty, q_full, q_free, s_full, p_full, o_done, unit_end, meta, reset, drain, pair;
 };
 
 // A bounded wait; one that runs out stops every role of the CTA.
@@ -351,14 +356,17 @@ __device__ bool produce(const AttnArgs& a, const Shared& s, Walk<D> walk) {
   constexpr int CPR = D / 8;              // 16-byte chunks of a row
   constexpr int RPW = 32 / CPR;           // rows a warp copies at once
   constexpr int IT = P::kBK / (4 * RPW);  // rounds of a tile
-  const int pt = threadIdx.x - P::kSoftmaxThreads, pw = pt >> 5, lane = pt & 31;
+  const int pt = (int)threadIdx.x - P::kSoftmaxThreads, pw = pt >> 5, lane = pt & 31;
   const int chunk = lane % CPR, sub = lane / CPR;
   uint32_t* nf_all = reinterpret_cast<uint32_t*>(s.sm + P::kNf);
   int32_t* bad_all = reinterpret_cast<int32_t*>(s.sm + P::kBad);
   uint32_t entry = 0;  // ring entries so far
   Part p;
   for (int unit = 0; walk.next(a, p); ++unit) {
-    const int ring = unit & (kMetaRing - 1);
+    const int ring = unit & 1;
+    // The last unit's scores are there and the one before it is at its end: the query rows of
+    // the one and the tree of the other may go.
+    if (unit > 0 && !wait_warp(s.q_free, (unit - 1) & 1, s)) return false;
     uint32_t* nf = nf_all + ring * 8;
     int32_t* bad = bad_all + ring;
     // ---- the unit's tree, if the part reaches it
@@ -377,7 +385,6 @@ __device__ bool produce(const AttnArgs& a, const Shared& s, Walk<D> walk) {
     }
     mbar_arrive(s.meta + 8 * ring);
     // ---- query rows, zero past the unit's
-    if (unit > 0 && !wait_warp(s.q_free, (unit - 1) & 1, s)) return false;
     const int q_rows = p.rows > 128 ? 256 : 128;
     for (int row0 = 0; row0 < q_rows; row0 += 4 * RPW) {
       const int row = row0 + pw * RPW + sub, g = p.row0 + row, node = g / a.group;
@@ -391,22 +398,26 @@ __device__ bool produce(const AttnArgs& a, const Shared& s, Walk<D> walk) {
     cp_arrive(s.q_full);
     // ---- K and V tiles
     const int cnt = p.tb - p.ta;
-    const bool two = P::kWG == 2 && p.rows > 128;
+    const bool two = P::kRowTiles == 2 && p.rows > 128;
     const int32_t* table = a.table + p.r * a.table_stride;
-    // lane L looks up the row that the warp copies in round L / RPW as its (L % RPW)-th
-    auto lookup = [&](int item) -> const uint16_t* {
+    // Lane L finds the row that the warp copies in round L / RPW as its (L % RPW)-th: first the
+    // block (a load, on its way while the entry before is copied), then the address.
+    const int my_row = (lane / RPW) * 4 * RPW + pw * RPW + lane % RPW;
+    auto find_block = [&](int item) -> int32_t {
       bool is_v;
-      const int tile = p.ta + ring_tile(item, cnt, two, is_v);
-      const int row = (lane / RPW) * 4 * RPW + pw * RPW + lane % RPW;
-      const int32_t j = tile * P::kBK + row;
+      const int32_t j = (p.ta + ring_tile(item, cnt, two, is_v)) * P::kBK + my_row;
+      return lane < IT * RPW && j < p.q.len ? table[j / a.block_size] : 0;
+    };
+    auto find_row = [&](int item, int32_t id) -> const uint16_t* {
+      bool is_v;
+      const int32_t j = (p.ta + ring_tile(item, cnt, two, is_v)) * P::kBK + my_row;
       if (lane >= IT * RPW) return nullptr;
       if (j < p.q.len) {
-        const int32_t b = j / a.block_size, id = table[b];
         if ((uint32_t)id >= (uint64_t)a.n_blocks) {
           atomicOr(bad, kAttnBadBlock);
           return nullptr;
         }
-        return (is_v ? a.vc : a.kc) + (int64_t)id * a.block_stride + (int64_t)(j - b * a.block_size) * a.token_stride +
+        return (is_v ? a.vc : a.kc) + (int64_t)id * a.block_stride + (int64_t)(j % a.block_size) * a.token_stride +
                (int64_t)p.h * a.head_stride;
       }
       if (j - p.q.len < p.q.n)
@@ -414,11 +425,12 @@ __device__ bool produce(const AttnArgs& a, const Shared& s, Walk<D> walk) {
                     : a.k + (p.q.off + j - p.q.len) * a.k_stride + (int64_t)p.h * D;
       return nullptr;
     };
-    const uint16_t* mine = lookup(0);
+    const uint16_t* mine = find_row(0, find_block(0));
     for (int item = 0; item < 2 * cnt; ++item, ++entry) {
       bool is_v;
       const int tile = p.ta + ring_tile(item, cnt, two, is_v);
-      const uint16_t* ahead = item + 1 < 2 * cnt ? lookup(item + 1) : nullptr;
+      const int next = min(item + 1, 2 * cnt - 1);
+      const int32_t next_id = find_block(next);
       const uint32_t slot = entry % P::kSlots, round = entry / P::kSlots;
       if (round > 0 && !wait_warp(s.empty + 8 * slot, (round - 1) & 1, s)) return false;
       const uint32_t dst = s.base + P::kRing + slot * P::kSlotBytes;
@@ -458,7 +470,7 @@ __device__ bool produce(const AttnArgs& a, const Shared& s, Walk<D> walk) {
       } else {
         cp_arrive(s.full + 8 * slot);
       }
-      mine = ahead;
+      mine = find_row(next, next_id);
     }
   }
   cp_wait_all();
@@ -469,7 +481,9 @@ template <int D>
 __device__ bool issue_mma(const AttnArgs& a, const Shared& s, Walk<D> walk, uint32_t tmem) {
   using P = AttnPlan<D>;
   constexpr uint32_t kIdS = umma_idesc_n(P::kBK), kIdO = umma_idesc_n(D) | kTransposeB;
-  uint32_t entry = 0, p_seen[2] = {0, 0}, o_count[2] = {0, 0};
+  uint32_t entry = 0, slot_k = 0, slot_v = 0;
+  uint32_t p_par = 0, o_par = 0, o_any = 0;  // per score buffer: parities of what comes next; any product so far
+  bool had_two = false;
   Part p;
   auto take = [&](uint32_t& addr, uint32_t& slot) {  // the next ring entry, filled
     slot = entry % P::kSlots;
@@ -479,82 +493,75 @@ __device__ bool issue_mma(const AttnArgs& a, const Shared& s, Walk<D> walk, uint
     ++entry;
     return true;
   };
-  auto scores = [&](int q_tile, uint32_t k_addr, int b) {
-    const uint32_t q_addr = s.base + P::kQ + q_tile * P::kQTile;
+  // Scores overwrite the P of an earlier product.  Products with different results are not
+  // ordered among themselves, so that product has to have ended.
+  auto drained = [&](int b) {
+    return !(o_any >> b & 1u) || wait(s.o_done + 8 * b, (o_par >> b & 1u) ^ 1u, s);
+  };
+  auto scores = [&](int row_tile, uint32_t k_addr, int b) {
+    if (!drained(b)) return false;
+    tc_fence_after();
+    const uint32_t q_addr = s.base + P::kQ + row_tile * P::kQTile, d = tmem + P::kS0 + b * P::kSCols;
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks)
-      umma_bf16(tmem + P::kS(b), umma_desc(q_addr + (ks >> 2) * 16384 + (ks & 3) * 32),
+      umma_bf16(d, umma_desc(q_addr + (ks >> 2) * 16384 + (ks & 3) * 32),
                 umma_desc(k_addr + (ks >> 2) * (P::kBK * 128) + (ks & 3) * 32), kIdS, ks > 0);
     umma_commit(s.s_full + 8 * b);
+    return true;
   };
-  auto output = [&](int o, int b, uint32_t v_addr, bool acc) {  // o_done goes by the buffer of P
+  auto output = [&](int row_tile, int b, uint32_t v_addr, bool acc) {  // o_done goes by the buffer of P
+    if (!wait(s.p_full + 8 * b, p_par >> b & 1u, s)) return false;
+    p_par ^= 1u << b;
+    tc_fence_after();
+    const uint32_t d = tmem + row_tile * P::kO1, a0 = tmem + P::kS0 + b * P::kSCols;
 #pragma unroll
-    for (int ks = 0; ks < P::kBK / 16; ++ks) {  // 32 keys: 16 columns of upper halves, 16 of lower ones
-      const uint32_t p_addr = tmem + P::kS(b) + (ks >> 1) * 32 + (ks & 1) * 8;
+    for (int ks = 0; ks < P::kBK / 16; ++ks) {  // 32 keys: 16 columns of upper pieces, 16 of lower ones
+      const uint32_t p_addr = a0 + (ks >> 1) * 32 + (ks & 1) * 8;
       const uint64_t v_desc = umma_desc_v(v_addr + ks * 2048, P::kBK * 128);
-      umma_bf16_ts(tmem + P::kO(o), p_addr, v_desc, kIdO, acc || ks > 0);
-      umma_bf16_ts(tmem + P::kO(o), p_addr + 16, v_desc, kIdO, 1);
+      umma_bf16_ts(d, p_addr, v_desc, kIdO, acc || ks > 0);
+      umma_bf16_ts(d, p_addr + 16, v_desc, kIdO, 1);
     }
     umma_commit(s.o_done + 8 * b);
-    ++o_count[b];
-  };
-  // New scores overwrite the P of an earlier product.  Products with different results are not
-  // ordered among themselves, so that product has to have ended.
-  auto drained = [&](int b) { return o_count[b] == 0 || wait(s.o_done + 8 * b, (o_count[b] - 1) & 1, s); };
-  auto softmaxed = [&](int b) {
-    if (!wait(s.p_full + 8 * b, p_seen[b] & 1, s)) return false;
-    ++p_seen[b];
-    tc_fence_after();
+    o_par ^= 1u << b;
+    o_any |= 1u << b;
     return true;
   };
   for (int unit = 0; walk.next(a, p); ++unit) {
     const int cnt = p.tb - p.ta;
-    const bool two = P::kWG == 2 && p.rows > 128;
-    uint32_t k_addr, v_addr, k_slot, v_slot;
+    const bool two = P::kRowTiles == 2 && p.rows > 128;
+    uint32_t k_addr, v_addr;
     if (!wait(s.q_full, unit & 1, s)) return false;
-    if (!take(k_addr, k_slot)) return false;
-    if (!drained(0) || !drained(1)) return false;
-    tc_fence_after();
-    scores(0, k_addr, 0);
-    if (two) scores(1, k_addr, 1);
-    umma_commit(s.empty + 8 * k_slot);
-    if (!two && cnt > 1) {
-      if (!take(k_addr, k_slot)) return false;
-      scores(0, k_addr, 1);
-      umma_commit(s.empty + 8 * k_slot);
+    // The second O and score buffer 0 share their columns.
+    bool ended = unit == 0;
+    if (two ? !drained(0) : had_two && !(ended = wait(s.unit_end, (unit - 1) & 1, s))) return false;
+    had_two = two;
+    for (int i = 0; i < (two ? 1 : min(cnt, 2)); ++i) {
+      if (!take(k_addr, slot_k)) return false;
+      if (!scores(0, k_addr, two ? 1 : i)) return false;
+      if (two && !scores(1, k_addr, 2)) return false;
+      umma_commit(s.empty + 8 * slot_k);
     }
-    if (cnt <= (two ? 1 : 2)) umma_commit(s.q_free);
-    if (unit > 0 && !wait(s.unit_end, (unit - 1) & 1, s)) return false;  // the last unit's outputs have been read
-    for (int i = 0; i < cnt; ++i) {
-      if (!take(v_addr, v_slot)) return false;
+    if (!ended && !wait(s.unit_end, (unit - 1) & 1, s)) return false;  // the last unit's outputs have been read
+    if (cnt <= (two ? 1 : 2)) umma_commit(s.q_free);  // (not before that: its tree goes with it)
+    tc_fence_after();
+    for (int i = 0, b = 0; i < cnt; ++i) {
+      if (!take(v_addr, slot_v)) return false;
+      const bool more = i + (two ? 1 : 2) < cnt, last = i + (two ? 2 : 3) == cnt;
       if (two) {
-        if (!softmaxed(0)) return false;
-        output(0, 0, v_addr, i > 0);
-        if (i + 1 < cnt) {
-          if (!take(k_addr, k_slot) || !drained(0)) return false;
-          scores(0, k_addr, 0);
-        }
-        if (!softmaxed(1)) return false;
-        output(P::kWG - 1, 1, v_addr, i > 0);
-        umma_commit(s.empty + 8 * v_slot);
-        if (i + 1 < cnt) {
-          if (!drained(1)) return false;
-          scores(1, k_addr, 1);
-          umma_commit(s.empty + 8 * k_slot);
-          if (i + 2 == cnt) umma_commit(s.q_free);
-        }
+        if (!output(0, 1, v_addr, i > 0)) return false;
+        if (more && (!take(k_addr, slot_k) || !scores(0, k_addr, 1))) return false;
+        if (!output(1, 2, v_addr, i > 0)) return false;
+        umma_commit(s.empty + 8 * slot_v);
+        if (more && !scores(1, k_addr, 2)) return false;
       } else {
-        const int b = i & 1, o = P::kWG == 2 ? b : 0;
-        if (!softmaxed(b)) return false;
-        output(o, b, v_addr, P::kWG == 2 ? i >= 2 : i >= 1);
-        umma_commit(s.empty + 8 * v_slot);
-        if (i + 2 < cnt) {
-          if (!take(k_addr, k_slot) || !drained(b)) return false;
-          scores(0, k_addr, b);
-          umma_commit(s.empty + 8 * k_slot);
-          if (i + 3 == cnt) umma_commit(s.q_free);
-        }
+        if (!output(0, b, v_addr, i > 0)) return false;
+        umma_commit(s.empty + 8 * slot_v);
+        const int ahead = b + 2 < P::kSB ? b + 2 : b + 2 - P::kSB;
+        if (more && (!take(k_addr, slot_k) || !scores(0, k_addr, ahead))) return false;
+        b = b + 1 < P::kSB ? b + 1 : 0;
       }
+      if (more) umma_commit(s.empty + 8 * slot_k);
+      if (more && last) umma_commit(s.q_free);
     }
   }
   return true;
@@ -563,144 +570,145 @@ __device__ bool issue_mma(const AttnArgs& a, const Shared& s, Walk<D> walk, uint
 template <int D>
 __device__ bool softmax(const AttnArgs& a, const Shared& s, Walk<D> walk, uint32_t tmem, int c) {
   using P = AttnPlan<D>;
+  constexpr int NC = P::kBK / 2, CH = NC / 32;  // keys of a thread in a tile, in chunks of 32
   constexpr int NW = P::kBK / 32;
-  const int g = threadIdx.x >> 7, lane_row = threadIdx.x & 127;  // warpgroup, tensor memory lane
-  const uint32_t lane_base = tmem + ((uint32_t)((threadIdx.x >> 5) & 3) << 21);
-  float2* ml = reinterpret_cast<float2*>(s.sm + P::kML);
-  uint32_t s_seen[2] = {0, 0}, o_seen[2] = {0, 0}, fin_seen = 0;
+  // warpgroup (the half of a tile's keys), tensor memory lane, and the quarter of the lanes
+  const int g = threadIdx.x >> 7, lane_row = threadIdx.x & 127, quarter = lane_row >> 5;
+  const uint32_t lane_base = tmem + ((uint32_t)quarter << 21);
+  volatile float* xs = reinterpret_cast<volatile float*>(s.sm + P::kX);
+  uint32_t x_count = 0, s_par = 0, o_par = 0;
+  // The value that the thread of the other half has for the same row.
+  auto exchange = [&](float mine, float& other) {
+    volatile float* x = xs + (x_count & 1) * 256 + lane_row;
+    x[g * 128] = mine;
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(s.pair + 8 * quarter);
+    if (!wait_warp(s.pair + 8 * quarter, x_count & 1, s)) return false;
+    other = x[(g ^ 1) * 128];
+    ++x_count;
+    return true;
+  };
   // Every product is waited for once and in order: a wait that skipped one could take its
   // end for the next one's.
   auto product_done = [&](int b) {
-    if (!wait_warp(s.o_done + 8 * b, o_seen[b] & 1, s)) return false;
-    ++o_seen[b];
+    if (!wait_warp(s.o_done + 8 * b, o_par >> b & 1u, s)) return false;
+    o_par ^= 1u << b;
     tc_fence_after();
     return true;
   };
   Part p;
   for (int unit = 0; walk.next(a, p); ++unit) {
-    const int ring = unit & (kMetaRing - 1), cnt = p.tb - p.ta;
-    const bool two = P::kWG == 2 && p.rows > 128;
-    const int row = (two ? g * 128 : 0) + lane_row;
-    const bool live = row < p.rows;
-    const int node = live ? (p.row0 + row) / a.group : -1;
+    const int ring = unit & 1, cnt = p.tb - p.ta;
+    const bool two = P::kRowTiles == 2 && p.rows > 128;
     const uint8_t* par = s.sm + P::kPar + ring * kAttnMaxNodes;
-    if (!wait_warp(s.meta + 8 * ring, (unit / kMetaRing) & 1, s)) return false;
-    float ref = -INFINITY, sum = 0.0f;  // log2 reference of the row, sum of its probabilities
-    int done = 0;                       // tiles of this warpgroup
-    const int first = P::kWG == 2 && !two ? g : 0, step = P::kWG == 2 && !two ? 2 : 1;
-    for (int i = first; i < cnt; i += step, ++done) {
-      const int b = P::kWG == 2 ? g : i & 1;
-      const int32_t j0 = (p.ta + i) * P::kBK, lim = p.q.len - j0;  // cached tokens from the tile's first key on
+    if (!wait_warp(s.meta + 8 * ring, (unit >> 1) & 1, s)) return false;
+    // log2 reference of the row and sum of the half's probabilities, for the tile of rows in
+    // turn and the other one
+    float ref = -INFINITY, sum = 0.0f, ref2 = -INFINITY, sum2 = 0.0f;
+    int b = two ? 1 : 0, b_last = 0;
+    for (int step = 0; step < (two ? 2 * cnt : cnt); ++step) {
+      const int i = two ? step >> 1 : step, row = (two ? (step & 1) * 128 : 0) + lane_row;
+      if (two) b_last = b;
+      const bool warp_live = (row & ~31) < p.rows;  // a warp of padding only keeps step
+      const int32_t lim = p.q.len - (p.ta + i) * P::kBK;  // cached tokens from the tile's first key on
       const bool masked = lim < P::kBK;
-      uint32_t may[NW];
-      if (masked) {
+      uint32_t may[CH];
+      if (masked && warp_live) {
 #pragma unroll
-        for (int w = 0; w < NW; ++w)
-          may[w] = lim >= 32 * (w + 1) ? 0xFFFFFFFFu : lim <= 32 * w ? 0u : (1u << (lim - 32 * w)) - 1u;
-        for (int x = node; x >= 0;) {
-          const int at = x + lim;
+        for (int w = 0; w < CH; ++w) {
+          const int l = lim - g * NC - 32 * w;
+          may[w] = l >= 32 ? 0xFFFFFFFFu : l <= 0 ? 0u : (1u << l) - 1u;
+        }
+        for (int x = row < p.rows ? (p.row0 + row) / a.group : -1; x >= 0;) {
+          const int at = x + lim - g * NC;
           if (at < 0) break;
-          if (at < P::kBK) {
 #pragma unroll
-            for (int w = 0; w < NW; ++w)
-              if ((at >> 5) == w) may[w] |= 1u << (at & 31);
-          }
+          for (int w = 0; w < CH; ++w)
+            if ((at >> 5) == w) may[w] |= 1u << (at & 31);
           const int up = par[x];
           if (up == 255) break;
           x = up;
         }
       }
-      if (!wait_warp(s.s_full + 8 * b, s_seen[b] & 1, s)) return false;
-      ++s_seen[b];
-      tc_fence_after();
-      const uint32_t st = lane_base + P::kS(b);
-      float top = -INFINITY, v[32];
+      if (!wait_warp(s.s_full + 8 * b, s_par >> b & 1u, s)) return false;
+      s_par ^= 1u << b;
+      bool waited = i == 0;
+      if (warp_live) {
+        tc_fence_after();
+        const uint32_t st = lane_base + P::kS0 + b * P::kSCols + g * NC;
+        uint32_t v[NC];
 #pragma unroll
-      for (int w = 0; w < NW; ++w) {
-        tmem_ld32(st + w * 32, v);
+        for (int w = 0; w < CH; ++w) tmem_ld32(st + w * 32, v + w * 32);
+        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int w = 0; w < CH; ++w) tmem_wait32(v + w * 32);
         if (masked) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = (may[w] >> e) & 1u ? v[e] : -INFINITY;
+          for (int e = 0; e < NC; ++e) v[e] = (may[e >> 5] >> (e & 31)) & 1u ? v[e] : 0xFF800000u;
         }
 #pragma unroll
-        for (int e = 0; e < 32; ++e) top = fmaxf(top, v[e]);
-      }
-      const float want = top * a.scale_log2;
-      const bool move = want - ref > kRefSlack;
-      const int b_last = P::kWG == 2 ? g : b ^ 1;
-      bool waited = done == 0;
-      if (__any_sync(0xFFFFFFFFu, move)) {
-        const float next = move ? want : ref;
-        if (done > 0) {
-          const float fix = move ? ex2(ref - next) : 1.0f;
-          sum *= fix;
-          if (!product_done(b_last)) return false;
-          waited = true;
+        for (int e = 0; e < NC; ++e) top[e & 3] = fmaxf(top[e & 3], __uint_as_float(v[e]));
+        top[0] = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+        if (!exchange(top[0], top[1])) return false;
+        const float want = fmaxf(top[0], top[1]) * a.scale_log2;
+        const bool move = want - ref > kRefSlack;
+        if (__any_sync(0xFFFFFFFFu, move)) {
+          const float next = move ? want : ref;
+          if (i > 0) {
+            const float fix = move ? ex2(ref - next) : 1.0f;
+            sum *= fix;
+            if (!product_done(b_last)) return false;
+            waited = true;
+            const uint32_t o = lane_base + (two ? (step & 1) * P::kO1 : 0) + g * (D / 2);
 #pragma unroll 1
-          for (int d = 0; d < D; d += 32) {
-            tmem_ld32(lane_base + P::kO(P::kWG == 2 ? g : 0) + d, v);
-            uint32_t u[32];
+            for (int d = 0; d < D / 2; d += 16) {
+              float x[16];
+              tmem_ld16(o + d, x);
+              uint32_t u[16];
 #pragma unroll
-            for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(v[e] * fix);
-            tmem_st16(lane_base + P::kO(P::kWG == 2 ? g : 0) + d, u);
-            tmem_st16(lane_base + P::kO(P::kWG == 2 ? g : 0) + d + 16, u + 16);
+              for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(x[e] * fix);
+              tmem_st16(o + d, u);
+            }
           }
+          ref = next;
         }
-        ref = next;
+        const float m = ref == -INFINITY ? 0.0f : ref;
+        float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int w = 0; w < CH; ++w) {
+          uint32_t u[32];  // upper pieces, lower pieces
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float x0 = ex2(fmaf(__uint_as_float(v[w * 32 + 2 * e]), a.scale_log2, -m));
+            const float x1 = ex2(fmaf(__uint_as_float(v[w * 32 + 2 * e + 1]), a.scale_log2, -m));
+            part[2 * (e & 1)] += x0;
+            part[2 * (e & 1) + 1] += x1;
+            const uint32_t p0 = __float_as_uint(x0), p1 = __float_as_uint(x1);
+            u[e] = __byte_perm(p0, p1, 0x7632);
+            u[16 + e] = pack2(fmaf(x0, kUp, -__uint_as_float(p0 & 0xFFFF0000u)), fmaf(x1, kUp, -__uint_as_float(p1 & 0xFFFF0000u)));
+          }
+          tmem_st16(st + w * 32, u);
+          tmem_st16(st + w * 32 + 16, u + 16);
+        }
+        sum += (part[0] + part[1]) + (part[2] + part[3]);
+        tmem_st_wait();
       }
-      const float m = ref == -INFINITY ? 0.0f : ref;
-      float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int w = 0; w < NW; ++w) {
-        tmem_ld32(st + w * 32, v);
-        uint32_t u[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          v[e] = ex2(fmaf(v[e], a.scale_log2, -m));
-          if (masked) v[e] = (may[w] >> e) & 1u ? v[e] : 0.0f;
-          part[e & 3] += v[e];
-        }
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const uint32_t p0 = __float_as_uint(v[2 * e]), p1 = __float_as_uint(v[2 * e + 1]);
-          u[e] = __byte_perm(p0, p1, 0x7632);
-          u[16 + e] = pack2(fmaf(v[2 * e], kUp, -__uint_as_float(p0 & 0xFFFF0000u)),
-                            fmaf(v[2 * e + 1], kUp, -__uint_as_float(p1 & 0xFFFF0000u)));
-        }
-        tmem_st16(st + w * 32, u);
-        tmem_st16(st + w * 32 + 16, u + 16);
-      }
-      sum += (part[0] + part[1]) + (part[2] + part[3]);
-      tmem_st_wait();
       if (!waited && !product_done(b_last)) return false;
       tc_fence_before();
       mbar_arrive(s.p_full + 8 * b);
-    }
-    // ---- the part's result
-    if (done > 0 && !product_done(P::kWG == 2 ? g : (cnt - 1) & 1)) return false;
-    const bool merge = P::kWG == 2 && !two && cnt > 1;
-    if (merge && g == 1) ml[lane_row] = make_float2(ref, sum);
-    if (P::kWG == 2 && !two && g == 1) {
-      if (merge) {
-        tc_fence_before();
-        mbar_arrive(s.fin);
+      if (two) {
+        float t = ref;
+        ref = ref2, ref2 = t;
+        t = sum;
+        sum = sum2, sum2 = t;
+        b = 3 - b;
+      } else {
+        b_last = b;
+        b = b + 1 < P::kSB ? b + 1 : 0;
       }
-      mbar_arrive(s.unit_end);
-      if (!wait_warp(s.unit_end, unit & 1, s)) return false;  // it may have had no tile: not to run ahead
-      continue;
     }
-    float w0 = 1.0f, w1 = 0.0f;
-    if (merge) {
-      if (!wait_warp(s.fin, fin_seen & 1, s)) return false;
-      ++fin_seen;
-      tc_fence_after();
-      const float2 other = ml[lane_row];
-      const float both = fmaxf(ref, other.x), m = both == -INFINITY ? 0.0f : both;
-      w0 = ex2(ref - m);
-      w1 = ex2(other.x - m);
-      sum = w0 * sum + w1 * other.y;
-      ref = both;
-    }
+    // ---- the part's result, half of the columns each
+    if (!product_done(two ? 1 : b_last) || (two && !product_done(2))) return false;
     const bool whole = p.ta == 0 && p.tb == p.q.tiles;
     const int32_t bad = reinterpret_cast<volatile int32_t*>(s.sm + P::kBad)[ring];
     const uint32_t* nf = reinterpret_cast<const uint32_t*>(s.sm + P::kNf) + ring * 8;
@@ -709,58 +717,55 @@ __device__ bool softmax(const AttnArgs& a, const Shared& s, Walk<D> walk, uint32
     for (int w = 0; w < 8; ++w) any_nf |= nf[w];
     const int part_slot = 2 * c + (p.ta > 0 ? 0 : 1);
     float* po = a.part_o + (int64_t)part_slot * D * a.row_cap;
-    const int qrow = p.row0 + row, head = p.h * a.group + (live ? qrow - node * a.group : 0);
-    uint16_t* out = a.out + ((p.q.off + (live ? node : 0)) * a.n_q_heads + head) * (int64_t)D;
-    if (whole && bad && lane_row == 0) atomicOr(a.status, bad);
-    if (!whole && lane_row == 0 && row == 0) a.part_bad[part_slot] = bad;
-    if (!whole && live) *reinterpret_cast<float2*>(a.part_ml + 2 * ((int64_t)part_slot * a.row_cap + row)) = make_float2(ref, sum);
-    const float inv = 1.0f / sum;
+    if (threadIdx.x == 0) {
+      if (!whole) a.part_bad[part_slot] = bad;
+      else if (bad) atomicOr(a.status, bad);
+    }
+    for (int t = 0; t < (two ? 2 : 1); ++t) {
+      const int row = t * 128 + lane_row;
+      if ((row & ~31) >= p.rows) break;
+      float other;
+      if (!exchange(t ? sum2 : sum, other)) return false;
+      const float all = (t ? sum2 : sum) + other, inv = 1.0f / all;
+      const bool live = row < p.rows;
+      const int qrow = p.row0 + row, node = live ? qrow / a.group : 0;
+      uint16_t* out = a.out + ((p.q.off + node) * a.n_q_heads + p.h * a.group + (live ? qrow - node * a.group : 0)) * (int64_t)D;
+      if (!whole && live && g == 0)
+        *reinterpret_cast<float2*>(a.part_ml + 2 * ((int64_t)part_slot * a.row_cap + row)) = make_float2(t ? ref2 : ref, all);
 #pragma unroll 1
-    for (int d = 0; d < D; d += 16) {
-      float v[16];
-      tmem_ld16(lane_base + P::kO(two ? g : 0) + d, v);
-      if (merge) {
-        float x[16];
-        tmem_ld16(lane_base + P::kO(1) + d, x);
+      for (int d = g * (D / 2); d < (g + 1) * (D / 2); d += 16) {
+        float v[16];
+        tmem_ld16(lane_base + t * P::kO1 + d, v);
+        if (!live) continue;
+        if (any_nf) {
+          for (int x = node;;) {
+            if (nf[x >> 5] >> (x & 31) & 1u) {
+              const uint16_t* vr = a.v + (p.q.off + x) * a.v_stride + (int64_t)p.h * D + d;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) v[e] = w0 * v[e] + w1 * x[e];
-      }
-      if (any_nf && live) {
-        for (int x = node;;) {
-          if (nf[x >> 5] >> (x & 31) & 1u) {
-            const uint16_t* vr = a.v + (p.q.off + x) * a.v_stride + (int64_t)p.h * D + d;
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              if ((vr[e] & 0x7F80u) == 0x7F80u) v[e] += __uint_as_float((uint32_t)vr[e] << 16);
-          }
-          const int up = par[x];
-          if (up == 255) break;
-          x = up;
-        }
-      }
-      if (!live) continue;
-      if (whole) {
-        if (!bad) {
-#pragma unroll
-          for (int e = 0; e < 16; e += 8) {
-            uint4 x;
-            x.x = pack2(v[e] * inv, v[e + 1] * inv);
-            x.y = pack2(v[e + 2] * inv, v[e + 3] * inv);
-            x.z = pack2(v[e + 4] * inv, v[e + 5] * inv);
-            x.w = pack2(v[e + 6] * inv, v[e + 7] * inv);
-            *reinterpret_cast<uint4*>(out + d + e) = x;
+              for (int e = 0; e < 16; ++e)
+                if ((vr[e] & 0x7F80u) == 0x7F80u) v[e] += __uint_as_float((uint32_t)vr[e] << 16);
+            }
+            const int up = par[x];
+            if (up == 255) break;
+            x = up;
           }
         }
-      } else {
+        if (!whole) {
 #pragma unroll
-        for (int e = 0; e < 16; e += 4)
-          *reinterpret_cast<float4*>(po + ((int64_t)(d + e) / 4 * a.row_cap + row) * 4) =
-              make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+          for (int e = 0; e < 16; e += 4)
+            *reinterpret_cast<float4*>(po + ((int64_t)(d + e) / 4 * a.row_cap + row) * 4) =
+                make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+        } else if (!bad) {
+#pragma unroll
+          for (int e = 0; e < 16; e += 8)
+            *reinterpret_cast<uint4*>(out + d + e) =
+                make_uint4(pack2(v[e] * inv, v[e + 1] * inv), pack2(v[e + 2] * inv, v[e + 3] * inv),
+                           pack2(v[e + 4] * inv, v[e + 5] * inv), pack2(v[e + 6] * inv, v[e + 7] * inv));
+        }
       }
     }
     tc_fence_before();
     mbar_arrive(s.unit_end);
-    if (g == 1 && !wait_warp(s.unit_end, unit & 1, s)) return false;
   }
   return true;
 }
@@ -785,13 +790,13 @@ __global__ void __launch_bounds__(AttnPlan<D>::kThreads, 1) k_tree_attn(AttnArgs
   };
   s.full = bars(P::kSlots);
   s.empty = bars(P::kSlots);
-  s.s_full = bars(2);
-  s.p_full = bars(2);
-  s.o_done = bars(2);
+  s.s_full = bars(P::kSB);
+  s.p_full = bars(P::kSB);
+  s.o_done = bars(P::kSB);
   s.unit_end = bars(1);
   s.q_full = bars(1);
   s.q_free = bars(1);
-  s.fin = bars(1);
+  s.pair = bars(4);
   s.meta = bars(kMetaRing);
   s.reset = bars(1);
   s.drain = bars(1);
@@ -800,14 +805,14 @@ __global__ void __launch_bounds__(AttnPlan<D>::kThreads, 1) k_tree_attn(AttnArgs
       mbar_init(s.full + 8 * i, 128);
       mbar_init(s.empty + 8 * i, 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < P::kSB; ++i) {
       mbar_init(s.s_full + 8 * i, 1);
-      mbar_init(s.p_full + 8 * i, 128);
+      mbar_init(s.p_full + 8 * i, P::kSoftmaxThreads);
       mbar_init(s.o_done + 8 * i, 1);
     }
     mbar_init(s.q_full, 128);
     mbar_init(s.q_free, 1);
-    mbar_init(s.fin, 128);
+    for (int i = 0; i < 4; ++i) mbar_init(s.pair + 8 * i, 2);
     mbar_init(s.unit_end, P::kSoftmaxThreads);
     for (int i = 0; i < kMetaRing; ++i) mbar_init(s.meta + 8 * i, 128);
     mbar_init(s.reset, 128);
@@ -853,9 +858,8 @@ __global__ void __launch_bounds__(AttnPlan<D>::kThreads, 1) k_tree_attn(AttnArgs
   if (tid == 0 && misc[1]) atomicOr(a.status, kAttnTimeout);
 }
 
-// Adds the parts of the units that several CTAs worked on.  Block (c, y): the unit in which
-// CTA c + 1's share begins, if that is the first share to begin inside it; the y-th part
-// of its rows.
+// Adds the parts of the units that several CTAs worked on.  Block c takes the unit inside which
+// CTA c + 1's share begins, and of its outputs as many as there are such shares.
 constexpr int kJoinThreads = 256;
 
 template <int D>
@@ -870,31 +874,32 @@ __global__ void __launch_bounds__(kJoinThreads) k_tree_attn_join(AttnArgs a) {
   walk.next(a, p);
   if (p.ta == 0) return;
   const int64_t begin = share(s.total, s.ctas, c) - p.ta, end = begin + p.q.tiles;
-  if (share(s.total, s.ctas, c - 1) > begin) return;
-  int last = c;  // the parts are CTA c - 1's second slot and the first slots of c .. last
-  while (last + 1 < s.ctas && share(s.total, s.ctas, last + 1) < end) ++last;
+  // shares first .. last begin inside the unit: begin < total * i / ctas < end
+  const int first = (int)(((begin + 1) * s.ctas + s.total - 1) / s.total);
+  const int last = (int)((end * s.ctas + s.total - 1) / s.total) - 1;
+  // the parts are CTA first - 1's second slot and the first slots of first .. last
   int32_t bad = 0;
   for (int i = tid; i < p.q.n; i += kJoinThreads) {
     const int32_t x = a.parent[p.q.off + i];
     if (!(i == 0 ? x == -1 : x >= 0 && x < i)) bad |= kAttnBadRequest;
   }
-  for (int i = c - 1 + tid; i <= last; i += kJoinThreads) bad |= a.part_bad[2 * i + (i < c ? 1 : 0)];
+  for (int i = first - 1 + tid; i <= last; i += kJoinThreads) bad |= a.part_bad[2 * i + (i < first ? 1 : 0)];
   bad = (__syncthreads_or(bad & kAttnBadRequest) ? kAttnBadRequest : 0) | (__syncthreads_or(bad & kAttnBadBlock) ? kAttnBadBlock : 0);
   if (bad) {
     if (tid == 0) atomicOr(a.status, bad);
     return;
   }
-  for (int e = blockIdx.y * kJoinThreads + tid; e < p.rows * (D / 4); e += gridDim.y * kJoinThreads) {
+  for (int e = (c - first) * kJoinThreads + tid; e < p.rows * (D / 4); e += (last - first + 1) * kJoinThreads) {
     const int c4 = e / p.rows, row = e - c4 * p.rows;
-    auto slot = [&](int i) { return (int64_t)(2 * i + (i < c ? 1 : 0)); };
+    auto slot = [&](int i) { return (int64_t)(2 * i + (i < first ? 1 : 0)); };
     auto stat = [&](int i) { return *reinterpret_cast<const float2*>(a.part_ml + 2 * (slot(i) * a.row_cap + row)); };
     float top = -INFINITY;
-    for (int i = c - 1; i <= last; ++i) top = fmaxf(top, stat(i).x);
+    for (int i = first - 1; i <= last; ++i) top = fmaxf(top, stat(i).x);
     const float m = top == -INFINITY ? 0.0f : top;
     float sum = 0.0f;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
-    for (int i = c - 1; i <= last; ++i) {
+    for (int i = first - 1; i <= last; ++i) {
       const float2 t = stat(i);
       const float4 x = *reinterpret_cast<const float4*>(a.part_o + slot(i) * D * a.row_cap + ((int64_t)c4 * a.row_cap + row) * 4);
       const float w = ex2(t.x - m);
@@ -928,12 +933,11 @@ int launch_attn(const AttnArgs& a, cudaStream_t s) {
   }
   k_tree_attn<D><<<kAttnCtas, P::kThreads, P::kBytes, s>>>(a);
   W12_LAUNCH_CHECK("tree_attn kernel");
-  const int64_t items = (int64_t)a.row_cap * (D / 4);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kAttnCtas - 1, (unsigned)(items <= 2 * kJoinThreads ? 1 : items <= 8 * kJoinThreads ? 4 : 8));
+  cfg.gridDim = dim3(kAttnCtas - 1);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = s;
   cfg.attrs = attr;
