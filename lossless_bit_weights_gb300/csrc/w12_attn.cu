@@ -46,6 +46,20 @@ constexpr int kMetaRing = 2;     // units whose tree shared memory holds
 constexpr float kUp = 1.0f + 1.0f / 1048576.0f;
 constexpr float kRefSlack = 8.0f;  // log2 of the largest P before the reference moves
 
+// Division of numbers below 2^31 by a divisor up to 2^24: floor(n * mul / 2^shift), mul =
+// ceil(2^shift / d), shift = 31 + ceil(log2 d); the excess n (mul d - 2^shift) stays below 2^shift.
+struct FastDiv {
+  uint32_t mul, shift;
+  __device__ __forceinline__ int32_t operator()(int32_t n) const { return (int32_t)(((uint64_t)(uint32_t)n * mul) >> shift); }
+};
+
+FastDiv fast_div(int64_t d) {
+  FastDiv f{0, 31};
+  while ((int64_t)1 << (f.shift - 31) < d) ++f.shift;
+  f.mul = (uint32_t)((((uint64_t)1 << f.shift) + (uint64_t)d - 1) / (uint64_t)d);
+  return f;
+}
+
 struct AttnArgs {
   const uint16_t *q, *k, *v, *kc, *vc;
   int64_t q_stride, k_stride, v_stride, M;
@@ -53,6 +67,7 @@ struct AttnArgs {
   const int32_t *table, *cache_len, *parent, *req_offsets;
   int64_t table_stride, table_width;
   int32_t n_req, block_size, group, n_heads, n_q_heads, row_cap;
+  FastDiv by_block, by_group;
   float scale_log2;  // scale * log2(e)
   uint16_t* out;
   int32_t* status;
@@ -232,6 +247,9 @@ struct Walk {
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool in) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
 }
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 __device__ __forceinline__ void cp_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
@@ -358,91 +376,108 @@ __device__ bool produce(const AttnArgs& a, const Shared& s, Walk<D> walk) {
   constexpr int IT = P::kBK / (4 * RPW);  // rounds of a tile
   const int pt = (int)threadIdx.x - P::kSoftmaxThreads, pw = pt >> 5, lane = pt & 31;
   const int chunk = lane % CPR, sub = lane / CPR;
-  uint32_t* nf_all = reinterpret_cast<uint32_t*>(s.sm + P::kNf);
-  int32_t* bad_all = reinterpret_cast<int32_t*>(s.sm + P::kBad);
   uint32_t entry = 0;  // ring entries so far
   Part p;
   for (int unit = 0; walk.next(a, p); ++unit) {
-    const int ring = unit & 1;
-    // The last unit's scores are there and the one before it is at its end: the query rows of
-    // the one and the tree of the other may go.
-    if (unit > 0 && !wait_warp(s.q_free, (unit - 1) & 1, s)) return false;
-    uint32_t* nf = nf_all + ring * 8;
-    int32_t* bad = bad_all + ring;
-    // ---- the unit's tree, if the part reaches it
-    if (pt < 8) nf[pt] = 0;
-    if (pt == 8) *bad = 0;
-    mbar_arrive(s.reset);
-    if (!wait_warp(s.reset, unit & 1, s)) return false;
-    if ((int64_t)p.tb * P::kBK > p.q.len) {
-      uint8_t* par = s.sm + P::kPar + ring * kAttnMaxNodes;
-      for (int i = pt; i < p.q.n; i += 128) {
-        const int32_t x = a.parent[p.q.off + i];
-        const bool in = i == 0 ? x == -1 : x >= 0 && x < i;
-        par[i] = in && i ? (uint8_t)x : (uint8_t)255;  // 255: no parent
-        if (!in) atomicOr(bad, kAttnBadRequest);
-      }
-    }
-    mbar_arrive(s.meta + 8 * ring);
-    // ---- query rows, zero past the unit's
-    const int q_rows = p.rows > 128 ? 256 : 128;
-    for (int row0 = 0; row0 < q_rows; row0 += 4 * RPW) {
-      const int row = row0 + pw * RPW + sub, g = p.row0 + row, node = g / a.group;
-      const bool in = row < p.rows;
-      const uint16_t* src = in ? a.q + (p.q.off + node) * a.q_stride + (int64_t)(p.h * a.group + g - node * a.group) * D + chunk * 8
-                               : a.q;
-      cp16(s.base + P::kQ + (row >> 7) * P::kQTile + (chunk >> 3) * 16384 + (row & 127) * 128 +
-               (((chunk & 7) ^ (row & 7)) << 4),
-           src, in);
-    }
-    cp_arrive(s.q_full);
-    // ---- K and V tiles
-    const int cnt = p.tb - p.ta;
+    const int ring = unit & 1, cnt = p.tb - p.ta;
     const bool two = P::kRowTiles == 2 && p.rows > 128;
+    uint32_t* nf = reinterpret_cast<uint32_t*>(s.sm + P::kNf) + ring * 8;
+    int32_t* bad = reinterpret_cast<int32_t*>(s.sm + P::kBad) + ring;
+    bool bad_block = false;
     const int32_t* table = a.table + p.r * a.table_stride;
-    // Lane L finds the row that the warp copies in round L / RPW as its (L % RPW)-th: first the
-    // block (a load, on its way while the entry before is copied), then the address.
+    const int64_t head_off = (int64_t)p.h * a.head_stride;
+    // Lane L finds the row that the warp copies in round L / RPW as its (L % RPW)-th: its block (a
+    // load that is on its way while the entries before are copied), then its place in the cache,
+    // for K and V alike.
     const int my_row = (lane / RPW) * 4 * RPW + pw * RPW + lane % RPW;
-    auto find_block = [&](int item) -> int32_t {
-      bool is_v;
-      const int32_t j = (p.ta + ring_tile(item, cnt, two, is_v)) * P::kBK + my_row;
-      return lane < IT * RPW && j < p.q.len ? table[j / a.block_size] : 0;
+    auto find_block = [&](int tile) -> int32_t {
+      const int32_t j = tile * P::kBK + my_row;
+      return lane < IT * RPW && j < p.q.len ? table[a.by_block(j)] : 0;
     };
-    auto find_row = [&](int item, int32_t id) -> const uint16_t* {
-      bool is_v;
-      const int32_t j = (p.ta + ring_tile(item, cnt, two, is_v)) * P::kBK + my_row;
-      if (lane >= IT * RPW) return nullptr;
-      if (j < p.q.len) {
-        if ((uint32_t)id >= (uint64_t)a.n_blocks) {
-          atomicOr(bad, kAttnBadBlock);
-          return nullptr;
-        }
-        return (is_v ? a.vc : a.kc) + (int64_t)id * a.block_stride + (int64_t)(j % a.block_size) * a.token_stride +
-               (int64_t)p.h * a.head_stride;
+    auto find_place = [&](int tile, int32_t id) -> int64_t {  // -1: not in the cache
+      const int32_t j = tile * P::kBK + my_row;
+      if (lane >= IT * RPW) return 0;
+      if (j >= p.q.len) return -1;
+      if ((uint32_t)id >= (uint64_t)a.n_blocks) {
+        bad_block = true;
+        return -1;
       }
-      if (j - p.q.len < p.q.n)
-        return is_v ? a.v + (p.q.off + j - p.q.len) * a.v_stride + (int64_t)p.h * D
-                    : a.k + (p.q.off + j - p.q.len) * a.k_stride + (int64_t)p.h * D;
-      return nullptr;
+      return (int64_t)id * a.block_stride + (int64_t)(j - a.by_block(j) * a.block_size) * a.token_stride + head_off;
     };
-    const uint16_t* mine = find_row(0, find_block(0));
+    int64_t place[2] = {0, 0};  // of the tiles whose K is under way and whose V is not
+    int waiting = 0;
+    int32_t id = find_block(p.ta);
     for (int item = 0; item < 2 * cnt; ++item, ++entry) {
       bool is_v;
-      const int tile = p.ta + ring_tile(item, cnt, two, is_v);
-      const int next = min(item + 1, 2 * cnt - 1);
-      const int32_t next_id = find_block(next);
+      const int i = ring_tile(item, cnt, two, is_v), tile = p.ta + i;
+      int64_t at;
+      if (is_v) {
+        at = place[0];
+        place[0] = place[1];
+        --waiting;
+      } else {
+        at = find_place(tile, id);
+        id = find_block(p.ta + min(i + 1, cnt - 1));
+        place[waiting++ & 1] = at;
+      }
       const uint32_t slot = entry % P::kSlots, round = entry / P::kSlots;
       if (round > 0 && !wait_warp(s.empty + 8 * slot, (round - 1) & 1, s)) return false;
       const uint32_t dst = s.base + P::kRing + slot * P::kSlotBytes;
+      const uint16_t* cached = (is_v ? a.vc : a.kc) + chunk * 8;
+      const bool tail = (int64_t)(tile + 1) * P::kBK > p.q.len;
+      if (!tail && __all_sync(0xFFFFFFFFu, at >= 0)) {
 #pragma unroll
-      for (int it = 0; it < IT; ++it) {
-        const uint16_t* src =
-            reinterpret_cast<const uint16_t*>(__shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(mine), it * RPW + sub));
-        const int row = it * 4 * RPW + pw * RPW + sub;
-        cp16(dst + (chunk >> 3) * (P::kBK * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4),
-             src ? src + chunk * 8 : a.kc, src != nullptr);
+        for (int it = 0; it < IT; ++it) {
+          const int row = it * 4 * RPW + pw * RPW + sub;
+          cp16(dst + (chunk >> 3) * (P::kBK * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4),
+               cached + __shfl_sync(0xFFFFFFFFu, at, it * RPW + sub));
+        }
+      } else {
+#pragma unroll 1
+        for (int it = 0; it < IT; ++it) {
+          const int row = it * 4 * RPW + pw * RPW + sub;
+          const int64_t o = __shfl_sync(0xFFFFFFFFu, at, it * RPW + sub);
+          const int32_t node = tile * P::kBK + row - p.q.len;
+          const uint16_t* src = cached + o;
+          bool in = o >= 0;
+          if (node >= 0 && node < p.q.n) {
+            src = (is_v ? a.v + (p.q.off + node) * a.v_stride : a.k + (p.q.off + node) * a.k_stride) + (int64_t)p.h * D + chunk * 8;
+            in = true;
+          }
+          cp16(dst + (chunk >> 3) * (P::kBK * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4), in ? src : a.kc, in);
+        }
       }
-      if ((int64_t)(tile + 1) * P::kBK > p.q.len && is_v) {
+      if (item == 0) {
+        // ---- the unit's query rows (zero past its own) and its tree, behind the first keys.  The
+        // last unit's scores are there and the one before it is at its end: the rows of the one
+        // and the tree of the other may go.
+        if (unit > 0 && !wait_warp(s.q_free, (unit - 1) & 1, s)) return false;
+        const int q_rows = p.rows > 128 ? 256 : 128;
+        for (int row0 = 0; row0 < q_rows; row0 += 4 * RPW) {
+          const int row = row0 + pw * RPW + sub, r = p.row0 + row, node = a.by_group(r);
+          const bool in = row < p.rows;
+          cp16(s.base + P::kQ + (row >> 7) * P::kQTile + (chunk >> 3) * 16384 + (row & 127) * 128 +
+                   (((chunk & 7) ^ (row & 7)) << 4),
+               in ? a.q + (p.q.off + node) * a.q_stride + (int64_t)(p.h * a.group + r - node * a.group) * D + chunk * 8 : a.q, in);
+        }
+        if (pt < 8) nf[pt] = 0;
+        if (pt == 8) *bad = 0;
+        mbar_arrive(s.reset);
+        if (!wait_warp(s.reset, unit & 1, s)) return false;
+        if ((int64_t)p.tb * P::kBK > p.q.len) {
+          uint8_t* par = s.sm + P::kPar + ring * kAttnMaxNodes;
+          for (int n = pt; n < p.q.n; n += 128) {
+            const int32_t x = a.parent[p.q.off + n];
+            const bool in = n == 0 ? x == -1 : x >= 0 && x < n;
+            par[n] = in && n ? (uint8_t)x : (uint8_t)255;  // 255: no parent
+            if (!in) atomicOr(bad, kAttnBadRequest);
+          }
+        }
+        mbar_arrive(s.meta + 8 * ring);
+        cp_arrive(s.q_full);
+      }
+      if (item == 2 * cnt - 1 && bad_block) atomicOr(bad, kAttnBadBlock);
+      if (tail && is_v) {
         // A tile with drafted nodes: an infinity or a NaN in a node's V would reach every row
         // (0 * inf), also those that do not attend to it.  It is taken out here, the node
         // marked, and the rows that do attend to it get it back at the end.
@@ -470,7 +505,6 @@ __device__ bool produce(const AttnArgs& a, const Shared& s, Walk<D> walk) {
       } else {
         cp_arrive(s.full + 8 * slot);
       }
-      mine = find_row(next, next_id);
     }
   }
   cp_wait_all();
@@ -619,7 +653,7 @@ __device__ bool softmax(const AttnArgs& a, const Shared& s, Walk<D> walk, uint32
           const int l = lim - g * NC - 32 * w;
           may[w] = l >= 32 ? 0xFFFFFFFFu : l <= 0 ? 0u : (1u << l) - 1u;
         }
-        for (int x = row < p.rows ? (p.row0 + row) / a.group : -1; x >= 0;) {
+        for (int x = row < p.rows ? a.by_group(p.row0 + row) : -1; x >= 0;) {
           const int at = x + lim - g * NC;
           if (at < 0) break;
 #pragma unroll
@@ -728,7 +762,7 @@ __device__ bool softmax(const AttnArgs& a, const Shared& s, Walk<D> walk, uint32
       if (!exchange(t ? sum2 : sum, other)) return false;
       const float all = (t ? sum2 : sum) + other, inv = 1.0f / all;
       const bool live = row < p.rows;
-      const int qrow = p.row0 + row, node = live ? qrow / a.group : 0;
+      const int qrow = p.row0 + row, node = live ? a.by_group(qrow) : 0;
       uint16_t* out = a.out + ((p.q.off + node) * a.n_q_heads + p.h * a.group + (live ? qrow - node * a.group : 0)) * (int64_t)D;
       if (!whole && live && g == 0)
         *reinterpret_cast<float2*>(a.part_ml + 2 * ((int64_t)part_slot * a.row_cap + row)) = make_float2(t ? ref2 : ref, all);
@@ -893,21 +927,35 @@ __global__ void __launch_bounds__(kJoinThreads) k_tree_attn_join(AttnArgs a) {
     const int c4 = e / p.rows, row = e - c4 * p.rows;
     auto slot = [&](int i) { return (int64_t)(2 * i + (i < first ? 1 : 0)); };
     auto stat = [&](int i) { return *reinterpret_cast<const float2*>(a.part_ml + 2 * (slot(i) * a.row_cap + row)); };
-    float top = -INFINITY;
-    for (int i = first - 1; i <= last; ++i) top = fmaxf(top, stat(i).x);
-    const float m = top == -INFINITY ? 0.0f : top;
-    float sum = 0.0f;
+    // eight parts at a time, their statistics and values loaded together
+    float top = -INFINITY, sum = 0.0f;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-    for (int i = first - 1; i <= last; ++i) {
-      const float2 t = stat(i);
-      const float4 x = *reinterpret_cast<const float4*>(a.part_o + slot(i) * D * a.row_cap + ((int64_t)c4 * a.row_cap + row) * 4);
-      const float w = ex2(t.x - m);
-      sum += w * t.y;
-      o.x += w * x.x;
-      o.y += w * x.y;
-      o.z += w * x.z;
-      o.w += w * x.w;
+    for (int i0 = first - 1; i0 <= last; i0 += 8) {
+      float2 t[8];
+      float4 x[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const bool in = i0 + k <= last;
+        t[k] = in ? stat(i0 + k) : make_float2(-INFINITY, 0.0f);
+        x[k] = in ? *reinterpret_cast<const float4*>(a.part_o + slot(i0 + k) * D * a.row_cap + ((int64_t)c4 * a.row_cap + row) * 4)
+                  : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      }
+      float next = top;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) next = fmaxf(next, t[k].x);
+      const float m = next == -INFINITY ? 0.0f : next, fix = ex2(top - m);
+      sum *= fix;
+      o.x *= fix, o.y *= fix, o.z *= fix, o.w *= fix;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float w = ex2(t[k].x - m);
+        sum += w * t[k].y;
+        o.x += w * x[k].x;
+        o.y += w * x[k].y;
+        o.z += w * x[k].z;
+        o.w += w * x[k].w;
+      }
+      top = next;
     }
     const float inv = 1.0f / sum;
     const int g = p.row0 + row, node = g / a.group;
@@ -1029,6 +1077,8 @@ int tree_attn(const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_
   a.n_heads = (int32_t)H;
   a.n_q_heads = (int32_t)n_q_heads;
   a.row_cap = (int32_t)row_cap(M, a.group, D);
+  a.by_block = fast_div(a.block_size);
+  a.by_group = fast_div(a.group);
   a.scale_log2 = scale * 1.4426950408889634f;
   a.out = out;
   a.status = status;
