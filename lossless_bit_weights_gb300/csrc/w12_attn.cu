@@ -73,6 +73,7 @@ struct AttnArgs {
   int32_t* status;
   float *part_o, *part_ml;  // [2 * CTAs][D / 4][row_cap][4], [2 * CTAs][row_cap][2]
   int32_t* part_bad;        // [2 * CTAs]
+  struct JoinUnit* units;   // [CTAs]: the unit inside which a CTA's share begins
 };
 
 template <int D>
@@ -101,6 +102,14 @@ struct AttnPlan {
   // which the first gives way to the second O where a unit has two tiles of rows; D = 256:
   // four of 64 columns.
   static constexpr int kO1 = 128, kS0 = D <= 128 ? 128 : 256, kSCols = kBK;
+};
+
+// What the joining kernel has to know of a unit that several CTAs share.
+struct JoinUnit {
+  int64_t off;              // the request's first node
+  int32_t h, row0, rows;    // rows = 0: the CTA's share begins with a unit
+  int32_t first, last;      // the CTAs whose shares begin inside it
+  int32_t pad;
 };
 
 // ---------------------------------------------------------------- schedule
@@ -561,41 +570,38 @@ __device__ bool issue_mma(const AttnArgs& a, const Shared& s, Walk<D> walk, uint
     return true;
   };
   for (int unit = 0; walk.next(a, p); ++unit) {
-    const int cnt = p.tb - p.ta;
     const bool two = P::kRowTiles == 2 && p.rows > 128;
-    uint32_t k_addr, v_addr;
+    const int steps = (p.tb - p.ta) * (two ? 2 : 1);
+    uint32_t k_addr = 0, v_addr = 0;
     if (!wait(s.q_full, unit & 1, s)) return false;
     // The second O and score buffer 0 share their columns.
     bool ended = unit == 0;
     if (two ? !drained(0) : had_two && !(ended = wait(s.unit_end, (unit - 1) & 1, s))) return false;
     had_two = two;
-    for (int i = 0; i < (two ? 1 : min(cnt, 2)); ++i) {
-      if (!take(k_addr, slot_k)) return false;
-      if (!scores(0, k_addr, two ? 1 : i)) return false;
-      if (two && !scores(1, k_addr, 2)) return false;
-      umma_commit(s.empty + 8 * slot_k);
-    }
-    if (!ended && !wait(s.unit_end, (unit - 1) & 1, s)) return false;  // the last unit's outputs have been read
-    if (cnt <= (two ? 1 : 2)) umma_commit(s.q_free);  // (not before that: its tree goes with it)
-    tc_fence_after();
-    for (int i = 0, b = 0; i < cnt; ++i) {
-      if (!take(v_addr, slot_v)) return false;
-      const bool more = i + (two ? 1 : 2) < cnt, last = i + (two ? 2 : 3) == cnt;
-      if (two) {
-        if (!output(0, 1, v_addr, i > 0)) return false;
-        if (more && (!take(k_addr, slot_k) || !scores(0, k_addr, 1))) return false;
-        if (!output(1, 2, v_addr, i > 0)) return false;
-        umma_commit(s.empty + 8 * slot_v);
-        if (more && !scores(1, k_addr, 2)) return false;
-      } else {
-        if (!output(0, b, v_addr, i > 0)) return false;
-        umma_commit(s.empty + 8 * slot_v);
-        const int ahead = b + 2 < P::kSB ? b + 2 : b + 2 - P::kSB;
-        if (more && (!take(k_addr, slot_k) || !scores(0, k_addr, ahead))) return false;
-        b = b + 1 < P::kSB ? b + 1 : 0;
+    // A step is a tile of keys and a tile of rows; its scores run two steps ahead of its output.
+    // With two tiles of rows, every other step takes a tile of keys from the ring and the one
+    // after it gives it back.
+    int b_out = two ? 1 : 0, b_in = b_out;
+    for (int x = -2; x < steps; ++x) {
+      const bool opens = !two || !(x & 1), closes = !two || (x & 1);
+      if (x >= 0) {
+        if (!ended) {  // the last unit's outputs have been read
+          if (!wait(s.unit_end, (unit - 1) & 1, s)) return false;
+          ended = true;
+        }
+        if (x == 0 && steps <= 2) umma_commit(s.q_free);  // (not before that: its tree goes with it)
+        if (opens && !take(v_addr, slot_v)) return false;
+        if (!output(two ? x & 1 : 0, b_out, v_addr, x > (two ? 1 : 0))) return false;
+        if (closes) umma_commit(s.empty + 8 * slot_v);
+        b_out = two ? 3 - b_out : b_out + 1 < P::kSB ? b_out + 1 : 0;
       }
-      if (more) umma_commit(s.empty + 8 * slot_k);
-      if (more && last) umma_commit(s.q_free);
+      if (x + 2 < steps) {
+        if (opens && !take(k_addr, slot_k)) return false;
+        if (!scores(two ? x & 1 : 0, k_addr, b_in)) return false;
+        if (closes) umma_commit(s.empty + 8 * slot_k);
+        if (x + 3 == steps && x >= 0) umma_commit(s.q_free);
+        b_in = two ? 3 - b_in : b_in + 1 < P::kSB ? b_in + 1 : 0;
+      }
     }
   }
   return true;
@@ -859,7 +865,10 @@ __global__ void __launch_bounds__(AttnPlan<D>::kThreads, 1) k_tree_attn(AttnArgs
   const Start start = find_start<D>(a, c, P::kThreads, reinterpret_cast<int64_t*>(attn_sm + P::kRing), misc + 2);
   __syncthreads();  // the sums' scratch is the ring's from here on
   if (c == 0 && tid == 0 && misc[2]) atomicOr(a.status, kAttnBadRequest);
-  if (c >= start.ctas) return;
+  if (c >= start.ctas) {
+    if (tid == 0) a.units[c].rows = 0;
+    return;
+  }
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(s.base + P::kMisc) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -869,6 +878,16 @@ __global__ void __launch_bounds__(AttnPlan<D>::kThreads, 1) k_tree_attn(AttnArgs
   tc_fence_after();
   const uint32_t tmem = (uint32_t)misc[0];
   const Walk<D> walk(start, c);
+  if (tid == P::kThreads - 1) {  // (a thread of the MMA warp that has nothing else to do)
+    Part p;
+    Walk<D> w = walk;
+    w.next(a, p);
+    // shares first .. last begin inside the unit: begin < total * i / ctas < begin + tiles
+    const int64_t begin = share(start.total, start.ctas, c) - p.ta;
+    a.units[c] = JoinUnit{p.q.off, p.h, p.row0, p.ta > 0 ? p.rows : 0,
+                          (int32_t)(((begin + 1) * start.ctas + start.total - 1) / start.total),
+                          (int32_t)(((begin + p.q.tiles) * start.ctas + start.total - 1) / start.total) - 1, 0};
+  }
   bool ok = true;
   if (warp < P::kSoftmaxThreads / 32) {
     ok = softmax<D>(a, s, walk, tmem, c);
@@ -892,53 +911,39 @@ __global__ void __launch_bounds__(AttnPlan<D>::kThreads, 1) k_tree_attn(AttnArgs
   if (tid == 0 && misc[1]) atomicOr(a.status, kAttnTimeout);
 }
 
-// Adds the parts of the units that several CTAs worked on.  Block c takes the unit inside which
-// CTA c + 1's share begins, and of its outputs as many as there are such shares.
+// Adds the parts of the units that several CTAs worked on.  Block (c, y) takes, of the unit inside
+// which CTA c + 1's share begins, every (n * gridDim.y)-th run of outputs, n such shares there being.
 constexpr int kJoinThreads = 256;
 
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) k_tree_attn_join(AttnArgs a) {
-  __shared__ int64_t scratch[2 + kJoinThreads / 32];
-  const int tid = threadIdx.x, c = blockIdx.x + 1;
-  const Start s = find_start<D>(a, c, kJoinThreads, scratch, nullptr);
+  const int c = blockIdx.x + 1;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are the previous kernel's
-  if (c >= s.ctas) return;
-  Part p;
-  Walk<D> walk(s, c);
-  walk.next(a, p);
-  if (p.ta == 0) return;
-  const int64_t begin = share(s.total, s.ctas, c) - p.ta, end = begin + p.q.tiles;
-  // shares first .. last begin inside the unit: begin < total * i / ctas < end
-  const int first = (int)(((begin + 1) * s.ctas + s.total - 1) / s.total);
-  const int last = (int)((end * s.ctas + s.total - 1) / s.total) - 1;
-  // the parts are CTA first - 1's second slot and the first slots of first .. last
-  int32_t bad = 0;
-  for (int i = tid; i < p.q.n; i += kJoinThreads) {
-    const int32_t x = a.parent[p.q.off + i];
-    if (!(i == 0 ? x == -1 : x >= 0 && x < i)) bad |= kAttnBadRequest;
-  }
-  for (int i = first - 1 + tid; i <= last; i += kJoinThreads) bad |= a.part_bad[2 * i + (i < first ? 1 : 0)];
-  bad = (__syncthreads_or(bad & kAttnBadRequest) ? kAttnBadRequest : 0) | (__syncthreads_or(bad & kAttnBadBlock) ? kAttnBadBlock : 0);
-  if (bad) {
-    if (tid == 0) atomicOr(a.status, bad);
-    return;
-  }
-  for (int e = (c - first) * kJoinThreads + tid; e < p.rows * (D / 4); e += (last - first + 1) * kJoinThreads) {
-    const int c4 = e / p.rows, row = e - c4 * p.rows;
-    auto slot = [&](int i) { return (int64_t)(2 * i + (i < first ? 1 : 0)); };
-    auto stat = [&](int i) { return *reinterpret_cast<const float2*>(a.part_ml + 2 * (slot(i) * a.row_cap + row)); };
-    // eight parts at a time, their statistics and values loaded together
+  const JoinUnit u = a.units[c];
+  if (u.rows <= 0) return;  // nothing to join here; the other fields say nothing then
+  const int n = u.last - u.first + 1;
+  for (int e = ((c - u.first) * gridDim.y + blockIdx.y) * kJoinThreads + threadIdx.x; e < u.rows * (D / 4);
+       e += n * gridDim.y * kJoinThreads) {
+    const int c4 = e / u.rows, row = e - c4 * u.rows;
+    // the parts are CTA first - 1's second slot and the first slots of first .. last; eight at a
+    // time, their statistics and values loaded together
     float top = -INFINITY, sum = 0.0f;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int i0 = first - 1; i0 <= last; i0 += 8) {
+    int32_t bad = 0;
+    for (int i0 = u.first - 1; i0 <= u.last; i0 += 8) {
       float2 t[8];
       float4 x[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const bool in = i0 + k <= last;
-        t[k] = in ? stat(i0 + k) : make_float2(-INFINITY, 0.0f);
-        x[k] = in ? *reinterpret_cast<const float4*>(a.part_o + slot(i0 + k) * D * a.row_cap + ((int64_t)c4 * a.row_cap + row) * 4)
-                  : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        const int64_t slot = 2 * (int64_t)(i0 + k) + (i0 + k < u.first ? 1 : 0);
+        const bool in = i0 + k <= u.last;
+        t[k] = make_float2(-INFINITY, 0.0f);
+        x[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (in) {
+          t[k] = *reinterpret_cast<const float2*>(a.part_ml + 2 * (slot * a.row_cap + row));
+          x[k] = *reinterpret_cast<const float4*>(a.part_o + slot * D * a.row_cap + ((int64_t)c4 * a.row_cap + row) * 4);
+          bad |= a.part_bad[slot];
+        }
       }
       float next = top;
 #pragma unroll
@@ -957,9 +962,13 @@ __global__ void __launch_bounds__(kJoinThreads) k_tree_attn_join(AttnArgs a) {
       }
       top = next;
     }
+    if (bad) {  // the same for every output of the unit
+      if (e == 0) atomicOr(a.status, bad);
+      return;
+    }
     const float inv = 1.0f / sum;
-    const int g = p.row0 + row, node = g / a.group;
-    uint16_t* out = a.out + ((p.q.off + node) * a.n_q_heads + p.h * a.group + (g - node * a.group)) * (int64_t)D + c4 * 4;
+    const int g = u.row0 + row, node = a.by_group(g);
+    uint16_t* out = a.out + ((u.off + node) * a.n_q_heads + u.h * a.group + (g - node * a.group)) * (int64_t)D + c4 * 4;
     *reinterpret_cast<uint2*>(out) = make_uint2(pack2(o.x * inv, o.y * inv), pack2(o.z * inv, o.w * inv));
   }
 }
@@ -985,7 +994,7 @@ int launch_attn(const AttnArgs& a, cudaStream_t s) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kAttnCtas - 1);
+  cfg.gridDim = dim3(kAttnCtas - 1, a.row_cap * (D / 4) <= 4 * kJoinThreads ? 1 : 4);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = s;
   cfg.attrs = attr;
@@ -996,7 +1005,7 @@ int launch_attn(const AttnArgs& a, cudaStream_t s) {
 }
 
 struct AttnWs {
-  size_t o, ml, bad, total;
+  size_t o, ml, bad, units, total;
 };
 
 AttnWs attn_ws(int64_t M, int64_t group, int64_t D) {
@@ -1006,7 +1015,8 @@ AttnWs attn_ws(int64_t M, int64_t group, int64_t D) {
   w.o = 0;
   w.ml = up(slots * rows * (size_t)D * 4);
   w.bad = w.ml + up(slots * rows * 8);
-  w.total = w.bad + up(slots * 4);
+  w.units = w.bad + up(slots * 4);
+  w.total = w.units + up((size_t)kAttnCtas * sizeof(JoinUnit));
   return w;
 }
 
@@ -1086,6 +1096,7 @@ int tree_attn(const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_
   a.part_o = reinterpret_cast<float*>(base + w.o);
   a.part_ml = reinterpret_cast<float*>(base + w.ml);
   a.part_bad = reinterpret_cast<int32_t*>(base + w.bad);
+  a.units = reinterpret_cast<JoinUnit*>(base + w.units);
   cudaStream_t s = (cudaStream_t)stream;
   return D == 64 ? launch_attn<64>(a, s) : D == 128 ? launch_attn<128>(a, s) : launch_attn<256>(a, s);
 }
