@@ -298,12 +298,28 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t r[16]) 
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// A from tensor memory, B from shared memory.
-__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+// Products issued by one elected thread of a converged warp: the operands are then the warp's and
+// come from uniform registers.  64 back-to-back products of 128 x 64 x 16 took 32 cycles each this
+// way and 62 from inside a branch to one thread.
+__device__ __forceinline__ void umma_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(
-          d_tmem),
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n elect.sync _|q, 0xffffffff;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc)
+      : "memory");
+}
+// A from tensor memory.
+__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n elect.sync _|q, 0xffffffff;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void umma_commit_one(uint32_t bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(bar)
       : "memory");
 }
 
@@ -531,7 +547,7 @@ __device__ bool issue_mma(const AttnArgs& a, const Shared& s, Walk<D> walk, uint
   auto take = [&](uint32_t& addr, uint32_t& slot) {  // the next ring entry, filled
     slot = entry % P::kSlots;
     addr = s.base + P::kRing + slot * P::kSlotBytes;
-    if (!wait(s.full + 8 * slot, (entry / P::kSlots) & 1, s)) return false;
+    if (!wait_warp(s.full + 8 * slot, (entry / P::kSlots) & 1, s)) return false;
     fence_proxy_async_smem();  // the copies of other threads, before the tensor core reads them
     ++entry;
     return true;
@@ -539,7 +555,7 @@ __device__ bool issue_mma(const AttnArgs& a, const Shared& s, Walk<D> walk, uint
   // Scores overwrite the P of an earlier product.  Products with different results are not
   // ordered among themselves, so that product has to have ended.
   auto drained = [&](int b) {
-    return !(o_any >> b & 1u) || wait(s.o_done + 8 * b, (o_par >> b & 1u) ^ 1u, s);
+    return !(o_any >> b & 1u) || wait_warp(s.o_done + 8 * b, (o_par >> b & 1u) ^ 1u, s);
   };
   auto scores = [&](int row_tile, uint32_t k_addr, int b) {
     if (!drained(b)) return false;
@@ -547,13 +563,13 @@ __device__ bool issue_mma(const AttnArgs& a, const Shared& s, Walk<D> walk, uint
     const uint32_t q_addr = s.base + P::kQ + row_tile * P::kQTile, d = tmem + P::kS0 + b * P::kSCols;
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks)
-      umma_bf16(d, umma_desc(q_addr + (ks >> 2) * 16384 + (ks & 3) * 32),
-                umma_desc(k_addr + (ks >> 2) * (P::kBK * 128) + (ks & 3) * 32), kIdS, ks > 0);
-    umma_commit(s.s_full + 8 * b);
+      umma_ss(d, umma_desc(q_addr + (ks >> 2) * 16384 + (ks & 3) * 32),
+              umma_desc(k_addr + (ks >> 2) * (P::kBK * 128) + (ks & 3) * 32), kIdS, ks > 0);
+    umma_commit_one(s.s_full + 8 * b);
     return true;
   };
   auto output = [&](int row_tile, int b, uint32_t v_addr, bool acc) {  // o_done goes by the buffer of P
-    if (!wait(s.p_full + 8 * b, p_par >> b & 1u, s)) return false;
+    if (!wait_warp(s.p_full + 8 * b, p_par >> b & 1u, s)) return false;
     p_par ^= 1u << b;
     tc_fence_after();
     const uint32_t d = tmem + row_tile * P::kO1, a0 = tmem + P::kS0 + b * P::kSCols;
@@ -561,10 +577,10 @@ __device__ bool issue_mma(const AttnArgs& a, const Shared& s, Walk<D> walk, uint
     for (int ks = 0; ks < P::kBK / 16; ++ks) {  // 32 keys: 16 columns of upper pieces, 16 of lower ones
       const uint32_t p_addr = a0 + (ks >> 1) * 32 + (ks & 1) * 8;
       const uint64_t v_desc = umma_desc_v(v_addr + ks * 2048, P::kBK * 128);
-      umma_bf16_ts(d, p_addr, v_desc, kIdO, acc || ks > 0);
-      umma_bf16_ts(d, p_addr + 16, v_desc, kIdO, 1);
+      umma_ts(d, p_addr, v_desc, kIdO, acc || ks > 0);
+      umma_ts(d, p_addr + 16, v_desc, kIdO, 1);
     }
-    umma_commit(s.o_done + 8 * b);
+    umma_commit_one(s.o_done + 8 * b);
     o_par ^= 1u << b;
     o_any |= 1u << b;
     return true;
@@ -573,10 +589,10 @@ __device__ bool issue_mma(const AttnArgs& a, const Shared& s, Walk<D> walk, uint
     const bool two = P::kRowTiles == 2 && p.rows > 128;
     const int steps = (p.tb - p.ta) * (two ? 2 : 1);
     uint32_t k_addr = 0, v_addr = 0;
-    if (!wait(s.q_full, unit & 1, s)) return false;
+    if (!wait_warp(s.q_full, unit & 1, s)) return false;
     // The second O and score buffer 0 share their columns.
     bool ended = unit == 0;
-    if (two ? !drained(0) : had_two && !(ended = wait(s.unit_end, (unit - 1) & 1, s))) return false;
+    if (two ? !drained(0) : had_two && !(ended = wait_warp(s.unit_end, (unit - 1) & 1, s))) return false;
     had_two = two;
     // A step is a tile of keys and a tile of rows; its scores run two steps ahead of its output.
     // With two tiles of rows, every other step takes a tile of keys from the ring and the one
@@ -586,20 +602,20 @@ __device__ bool issue_mma(const AttnArgs& a, const Shared& s, Walk<D> walk, uint
       const bool opens = !two || !(x & 1), closes = !two || (x & 1);
       if (x >= 0) {
         if (!ended) {  // the last unit's outputs have been read
-          if (!wait(s.unit_end, (unit - 1) & 1, s)) return false;
+          if (!wait_warp(s.unit_end, (unit - 1) & 1, s)) return false;
           ended = true;
         }
-        if (x == 0 && steps <= 2) umma_commit(s.q_free);  // (not before that: its tree goes with it)
+        if (x == 0 && steps <= 2) umma_commit_one(s.q_free);  // (not before that: its tree goes with it)
         if (opens && !take(v_addr, slot_v)) return false;
         if (!output(two ? x & 1 : 0, b_out, v_addr, x > (two ? 1 : 0))) return false;
-        if (closes) umma_commit(s.empty + 8 * slot_v);
+        if (closes) umma_commit_one(s.empty + 8 * slot_v);
         b_out = two ? 3 - b_out : b_out + 1 < P::kSB ? b_out + 1 : 0;
       }
       if (x + 2 < steps) {
         if (opens && !take(k_addr, slot_k)) return false;
         if (!scores(two ? x & 1 : 0, k_addr, b_in)) return false;
-        if (closes) umma_commit(s.empty + 8 * slot_k);
-        if (x + 3 == steps && x >= 0) umma_commit(s.q_free);
+        if (closes) umma_commit_one(s.empty + 8 * slot_k);
+        if (x + 3 == steps && x >= 0) umma_commit_one(s.q_free);
         b_in = two ? 3 - b_in : b_in + 1 < P::kSB ? b_in + 1 : 0;
       }
     }
@@ -876,9 +892,9 @@ __global__ void __launch_bounds__(AttnPlan<D>::kThreads, 1) k_tree_attn(AttnArgs
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = (uint32_t)misc[0];
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, (uint32_t)misc[0], 0);
   const Walk<D> walk(start, c);
-  if (tid == P::kThreads - 1) {  // (a thread of the MMA warp that has nothing else to do)
+  if (tid == P::kThreads - 1) {
     Part p;
     Walk<D> w = walk;
     w.next(a, p);
@@ -894,10 +910,10 @@ __global__ void __launch_bounds__(AttnPlan<D>::kThreads, 1) k_tree_attn(AttnArgs
   } else if (warp < P::kSoftmaxThreads / 32 + 4) {
     ok = produce<D>(a, s, walk);
     if (!ok) cp_wait_all();
-  } else if ((tid & 31) == 0) {
+  } else {
     ok = issue_mma<D>(a, s, walk, tmem);
     if (!ok) {  // nothing may be in flight when tensor memory goes back
-      umma_commit(s.drain);
+      umma_commit_one(s.drain);
       mbar_wait_bounded(s.drain, 0);
     }
   }
