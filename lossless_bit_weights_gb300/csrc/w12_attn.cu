@@ -337,6 +337,24 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// Pairs of floats, one instruction for both.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ void unpair(uint64_t x, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   uint32_t d;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
@@ -429,21 +447,23 @@ __device__ bool produce(const AttnArgs& a, const Shared& s, Walk<D> walk) {
       }
       return (int64_t)id * a.block_stride + (int64_t)(j - a.by_block(j) * a.block_size) * a.token_stride + head_off;
     };
-    int64_t place[2] = {0, 0};  // of the tiles whose K is under way and whose V is not
-    int waiting = 0;
+    int64_t place0 = 0, place1 = 0;  // of the tiles whose K is under way and whose V is not, oldest first
+    bool waiting = false;
     int32_t id = find_block(p.ta);
     for (int item = 0; item < 2 * cnt; ++item, ++entry) {
       bool is_v;
       const int i = ring_tile(item, cnt, two, is_v), tile = p.ta + i;
       int64_t at;
       if (is_v) {
-        at = place[0];
-        place[0] = place[1];
-        --waiting;
+        at = place0;
+        place0 = place1;
+        waiting = !two && item < 2 * cnt - 1;  // K0 K1 V0 K2 V1 ...: one tile stays behind
       } else {
         at = find_place(tile, id);
         id = find_block(p.ta + min(i + 1, cnt - 1));
-        place[waiting++ & 1] = at;
+        if (waiting) place1 = at;
+        else place0 = at;
+        waiting = true;
       }
       const uint32_t slot = entry % P::kSlots, round = entry / P::kSlots;
       if (round > 0 && !wait_warp(s.empty + 8 * slot, (round - 1) & 1, s)) return false;
@@ -452,10 +472,15 @@ __device__ bool produce(const AttnArgs& a, const Shared& s, Walk<D> walk) {
       const bool tail = (int64_t)(tile + 1) * P::kBK > p.q.len;
       if (!tail && __all_sync(0xFFFFFFFFu, at >= 0)) {
 #pragma unroll
-        for (int it = 0; it < IT; ++it) {
-          const int row = it * 4 * RPW + pw * RPW + sub;
-          cp16(dst + (chunk >> 3) * (P::kBK * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4),
-               cached + __shfl_sync(0xFFFFFFFFu, at, it * RPW + sub));
+        for (int i0 = 0; i0 < IT; i0 += 8) {
+          int64_t o[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) o[k] = __shfl_sync(0xFFFFFFFFu, at, (i0 + k) * RPW + sub);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int row = (i0 + k) * 4 * RPW + pw * RPW + sub;
+            cp16(dst + (chunk >> 3) * (P::kBK * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4), cached + o[k]);
+          }
         }
       } else {
 #pragma unroll 1
@@ -729,24 +754,33 @@ __device__ bool softmax(const AttnArgs& a, const Shared& s, Walk<D> walk, uint32
           ref = next;
         }
         const float m = ref == -INFINITY ? 0.0f : ref;
-        float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        const uint64_t scale2 = pair(a.scale_log2, a.scale_log2), m2 = pair(-m, -m), up2 = pair(kUp, kUp);
+        uint64_t part[2] = {0, 0};
 #pragma unroll
         for (int w = 0; w < CH; ++w) {
           uint32_t u[32];  // upper pieces, lower pieces
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            const float x0 = ex2(fmaf(__uint_as_float(v[w * 32 + 2 * e]), a.scale_log2, -m));
-            const float x1 = ex2(fmaf(__uint_as_float(v[w * 32 + 2 * e + 1]), a.scale_log2, -m));
-            part[2 * (e & 1)] += x0;
-            part[2 * (e & 1) + 1] += x1;
+            float x0, x1;
+            unpair(fma2(pair(__uint_as_float(v[w * 32 + 2 * e]), __uint_as_float(v[w * 32 + 2 * e + 1])), scale2, m2), x0, x1);
+            x0 = ex2(x0);
+            x1 = ex2(x1);
+            const uint64_t x = pair(x0, x1);
+            part[e & 1] = add2(part[e & 1], x);
             const uint32_t p0 = __float_as_uint(x0), p1 = __float_as_uint(x1);
             u[e] = __byte_perm(p0, p1, 0x7632);
-            u[16 + e] = pack2(fmaf(x0, kUp, -__uint_as_float(p0 & 0xFFFF0000u)), fmaf(x1, kUp, -__uint_as_float(p1 & 0xFFFF0000u)));
+            unpair(fma2(x, up2, pair(-__uint_as_float(p0 & 0xFFFF0000u), -__uint_as_float(p1 & 0xFFFF0000u))), x0, x1);
+            u[16 + e] = pack2(x0, x1);
           }
           tmem_st16(st + w * 32, u);
           tmem_st16(st + w * 32 + 16, u + 16);
         }
-        sum += (part[0] + part[1]) + (part[2] + part[3]);
+        {
+          float x0, x1, x2, x3;
+          unpair(part[0], x0, x1);
+          unpair(part[1], x2, x3);
+          sum += (x0 + x1) + (x2 + x3);
+        }
         tmem_st_wait();
       }
       if (!waited && !product_done(b_last)) return false;
