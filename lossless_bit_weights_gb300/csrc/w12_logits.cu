@@ -3,12 +3,14 @@
 // behind them.
 //
 // One block takes one request and one chunk of the vocabulary.  It builds the request's
-// side of the rules for its chunk in shared memory (integer counts of the history, the
-// prompt flag, the place of the last bias entry, and a bitmap of the tokens that any rule
-// of the request can touch), then streams the chunk of each of the request's rows once.
-// A token outside the bitmap costs one bit test; one inside it takes its count from the
-// table plus the drafted tokens on the row's own path, so the table is never changed and
-// rows need no barriers between them.
+// side of the rules for its chunk in shared memory: integer counts of the history, the
+// prompt flag, the place of the last bias entry, and the list of the tokens that any rule of
+// the request can touch.  Then each row's chunk is streamed once, 64 bytes a thread in
+// flight: the untouched tokens (nearly all) go by with their mask bit alone.  The listed
+// tokens follow, one a lane, with the count from the table plus the drafted tokens on the
+// row's own path, so the table is never changed and rows need no barriers between them.
+// (A test at every token instead sent almost every warp through the formula: with 2500
+// distinct tokens in a history, 87 % of all runs of 128 tokens hold one.)
 #include <cstdint>
 
 #include "w12_internal.cuh"
@@ -45,40 +47,42 @@ __device__ __forceinline__ bool request_rows(const int32_t* offsets, int64_t M, 
   return true;
 }
 
-struct RowRules {
-  const uint32_t *cnt, *bits;
-  const int32_t *bias_at, *up, *parent, *draft;  // up: nearest node on the path whose token is in the chunk
-  int64_t v0;
-  bool has_rep, has_freq, has_pres;
-  float rep, freq, pres;
-  const float* bias_val;
-};
-
-// The formula for one token that some rule may touch; i = token - v0, node = the row's node.
-__device__ __noinline__ float apply_rules(const RowRules& w, float x, int i, int node) {
-  uint32_t c = w.cnt ? w.cnt[i] : 0u;
-  const int32_t tok = (int32_t)(w.v0 + i);
-  if (w.up)
-    for (int32_t p = w.up[node]; p >= 0;) {
-      if (w.draft[p] == tok) ++c;
-      p = w.parent[p] >= 0 ? w.up[w.parent[p]] : -1;
-    }
-  const uint32_t n = c & ~kPromptFlag;
-  if (c && w.has_rep) x = x > 0.0f ? __fdiv_rn(x, w.rep) : __fmul_rn(x, w.rep);
-  if (n) {
-    if (w.has_freq) x = __fsub_rn(x, __fmul_rn(w.freq, (float)n));
-    if (w.has_pres) x = __fsub_rn(x, w.pres);
-  }
-  if (w.bias_at && w.bias_at[i] > 0) x = __fadd_rn(x, w.bias_val[w.bias_at[i] - 1]);
-  return x;
-}
-
 __device__ __forceinline__ unsigned long long arg_key(float x, int64_t v) {
   return ((unsigned long long)((uint32_t)order_key(x) ^ 0x80000000u) << 32) | (0xFFFFFFFFu - (uint32_t)v);
 }
 
+// The largest value so far and its token, in a thread that sees its tokens in rising order.
+struct Best {
+  int32_t key = INT32_MIN;  // NaN counts as the one above: below every number, above nothing
+  int32_t at = -1;
+  float value = -INFINITY;
+
+  __device__ __forceinline__ void take(float f, int32_t i) {
+    const int32_t k = max(order_key(f), INT32_MIN + 1);
+    if (k > key || (k == key && i < at)) {
+      key = k;
+      at = i;
+      value = f;
+    }
+  }
+  // Whether one of four values, the largest of them `top`, may be larger.
+  __device__ __forceinline__ bool beaten(float top) const { return top > value || key <= INT32_MIN + 1; }
+};
+
+__device__ __forceinline__ float4 load4(const float* x, int i, int n, bool vec) {
+  if (vec && i + 4 <= n) return __ldcs(reinterpret_cast<const float4*>(x + i));
+  float4 f;
+  f.x = i < n ? x[i] : 0.0f;
+  f.y = i + 1 < n ? x[i + 1] : 0.0f;
+  f.z = i + 2 < n ? x[i + 2] : 0.0f;
+  f.w = i + 3 < n ? x[i + 3] : 0.0f;
+  return f;
+}
+
+template <bool WRITE>
 __global__ void __launch_bounds__(kRuleThreads) k_logit_rules(RuleArgs a) {
   extern __shared__ uint32_t sm[];
+  __shared__ int s_listed[kRuleWarps];
   const int r = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t v0 = (int64_t)blockIdx.x * a.chunk;
   const int width = (int)min((int64_t)a.chunk, a.V - v0);
@@ -88,24 +92,26 @@ __global__ void __launch_bounds__(kRuleThreads) k_logit_rules(RuleArgs a) {
     if (tid == 0) atomicOr(a.status, kRuleBadRequest);
     return;
   }
-  const bool count = a.r.rep || a.r.freq || a.r.pres;
+  if (n == 0) return;
+  const bool count = a.r.rep || a.r.freq || a.r.pres, bias = a.r.bias_off != nullptr;
   const bool tree = a.parent != nullptr;
-  // shared memory: bitmap, counts, bias places (chunk entries each), then the tree
-  uint32_t* bits = sm;
+  // shared memory: the rows' best keys, bitmap, counts and bias places (chunk entries each), the
+  // tree, the list of touched tokens
+  unsigned long long* best = reinterpret_cast<unsigned long long*>(sm);
+  uint32_t* bits = sm + (WRITE ? 0 : 2 * n);
   uint32_t* cnt = bits + a.chunk / 32;
   int32_t* bias_at = reinterpret_cast<int32_t*>(cnt + (count ? a.chunk : 0));
-  int32_t* parent = bias_at + (a.r.bias_off ? a.chunk : 0);
+  int32_t* parent = bias_at + (bias ? a.chunk : 0);
   int32_t* draft = parent + (tree ? n : 0);
-  int32_t* up = draft + (tree ? n : 0);
-  unsigned long long* best = reinterpret_cast<unsigned long long*>(
-      (reinterpret_cast<uintptr_t>(up + (tree ? n : 0)) + 7) & ~(uintptr_t)7);
+  int32_t* up = draft + (tree ? n : 0);  // the nearest node on the path whose token is in the chunk
+  uint16_t* list = reinterpret_cast<uint16_t*>(up + (tree ? n : 0));
 
   for (int i = tid; i < a.chunk / 32; i += kRuleThreads) bits[i] = 0;
   if (count)
     for (int i = tid; i < a.chunk; i += kRuleThreads) cnt[i] = 0;
-  if (a.r.bias_off)
+  if (bias)
     for (int i = tid; i < a.chunk; i += kRuleThreads) bias_at[i] = 0;
-  if (a.key)
+  if (!WRITE)
     for (int i = tid; i < n; i += kRuleThreads) best[i] = 0;
   bool ok = true;
   if (tree)
@@ -117,7 +123,7 @@ __global__ void __launch_bounds__(kRuleThreads) k_logit_rules(RuleArgs a) {
     }
   if (!__syncthreads_and(ok)) {
     if (tid == 0) atomicOr(a.status, kRuleBadRequest);
-    if (a.key)  // no token: acceptance reports the tree as invalid
+    if (!WRITE)  // no token: acceptance reports the tree as invalid
       for (int i = tid; i < n; i += kRuleThreads) a.key[(off + i) * a.chunks + blockIdx.x] = 0;
     return;
   }
@@ -127,15 +133,25 @@ __global__ void __launch_bounds__(kRuleThreads) k_logit_rules(RuleArgs a) {
     const int64_t prompt = a.r.prompt_len ? a.r.prompt_len[r] : 0;
     if (tid == 0 && (len != given || prompt < 0 || prompt > given)) atomicOr(a.status, kRuleClamped);
     const int32_t* h = a.r.hist + r * a.r.hist_stride;
-    for (int64_t j = tid; j < len; j += kRuleThreads) {
-      const int64_t i = (int64_t)h[j] - v0;
-      if (i >= 0 && i < width) {
-        if (j < prompt) atomicOr(&cnt[i], kPromptFlag); else atomicAdd(&cnt[i], 1u);
-        atomicOr(&bits[i >> 5], 1u << (i & 31));
+    for (int64_t j0 = 0; j0 < len; j0 += 8 * kRuleThreads) {  // eight loads on their way
+      int32_t t[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int64_t j = j0 + k * kRuleThreads + tid;
+        t[k] = j < len ? h[j] : -1;
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int64_t i = (int64_t)t[k] - v0;
+        if (t[k] >= 0 && i >= 0 && i < width) {
+          if (j0 + k * kRuleThreads + tid < prompt) atomicOr(&cnt[i], kPromptFlag);
+          else atomicAdd(&cnt[i], 1u);
+          atomicOr(&bits[i >> 5], 1u << (i & 31));
+        }
       }
     }
   }
-  if (a.r.bias_off) {
+  if (bias) {
     const int64_t g0 = a.r.bias_off[r], g1 = a.r.bias_off[r + 1];
     const int64_t b0 = min(max(g0, (int64_t)0), a.r.n_bias), b1 = min(max(g1, b0), a.r.n_bias);
     if (tid == 0 && (b0 != g0 || b1 != g1)) atomicOr(a.status, kRuleClamped);
@@ -158,51 +174,107 @@ __global__ void __launch_bounds__(kRuleThreads) k_logit_rules(RuleArgs a) {
       }
     }
   __syncthreads();
+  // ---- the touched tokens, listed in rising order (at most one word of the bitmap a thread:
+  // chunk <= 32 * threads)
+  const uint32_t mine = tid < a.chunk / 32 ? bits[tid] : 0u;
+  int before = __popc(mine);
+  for (int o = 1; o < 32; o <<= 1) {
+    const int t = __shfl_up_sync(0xFFFFFFFFu, before, o);
+    if (lane >= o) before += t;
+  }
+  if (lane == 31) s_listed[warp] = before;
+  __syncthreads();
+  int listed = 0;
+  before -= __popc(mine);
+  for (int w = 0; w < kRuleWarps; ++w) {
+    if (w < warp) before += s_listed[w];
+    listed += s_listed[w];
+  }
+  for (uint32_t m = mine; m; m &= m - 1) list[before++] = (uint16_t)(tid * 32 + __ffs((int)m) - 1);
+  __syncthreads();
 
-  RowRules w;
-  w.cnt = count ? cnt : nullptr;
-  w.bits = bits;
-  w.bias_at = a.r.bias_off ? bias_at : nullptr;
-  w.up = tree && count ? up : nullptr;
-  w.parent = parent;
-  w.draft = draft;
-  w.v0 = v0;
-  w.has_rep = a.r.rep != nullptr;
-  w.has_freq = a.r.freq != nullptr;
-  w.has_pres = a.r.pres != nullptr;
-  w.rep = w.has_rep ? a.r.rep[r] : 1.0f;
-  w.freq = w.has_freq ? a.r.freq[r] : 0.0f;
-  w.pres = w.has_pres ? a.r.pres[r] : 0.0f;
-  w.bias_val = a.r.bias_val;
+  const bool has_rep = a.r.rep != nullptr, has_freq = a.r.freq != nullptr, has_pres = a.r.pres != nullptr;
+  const float rep = has_rep ? a.r.rep[r] : 1.0f, freq = has_freq ? a.r.freq[r] : 0.0f, pres = has_pres ? a.r.pres[r] : 0.0f;
 
-  // a warp takes one part of one row's chunk
+  // ---- a warp takes one part of one row's chunk
   const int part_len = a.chunk / a.parts;
   for (int u = warp; u < n * a.parts; u += kRuleWarps) {
     const int node = u / a.parts, c0 = (u - node * a.parts) * part_len, c1 = min(width, c0 + part_len);
     const int64_t m = off + node;
     const float* x = a.logits + m * a.stride + v0;
-    float* y = a.out ? a.out + m * a.out_stride + v0 : nullptr;
+    float* y = WRITE ? a.out + m * a.out_stride + v0 : nullptr;
     const uint32_t* mask = a.r.mask ? a.r.mask + m * a.r.mask_stride + v0 / 32 : nullptr;
-    unsigned long long top = 0;
-    for (int i = c0 + lane; i < c1; i += 32) {
-      float f = x[i];
-      const bool allowed = !mask || (mask[i >> 5] >> (i & 31) & 1u);
-      if (bits[i >> 5] >> (i & 31) & 1u) f = apply_rules(w, f, i, node);
-      if (y) y[i] = allowed ? f : -INFINITY;
-      if (a.key && allowed) {
-        const unsigned long long k = arg_key(f, v0 + i);
-        top = k > top ? k : top;
+    Best top;
+    constexpr int U = 4;
+    for (int i0 = c0; i0 < c1; i0 += 128 * U) {
+      float4 f[U];
+      uint32_t allowed[U];
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const int i = i0 + k * 128 + 4 * lane;
+        f[k] = load4(x, i, c1, a.vec);
+        allowed[k] = i >= c1 ? 0u : mask ? mask[i >> 5] >> (i & 31) & 15u : 15u;
+      }
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const int i = i0 + k * 128 + 4 * lane;
+        if (i >= c1) break;
+        const uint32_t may = allowed[k] & (i + 4 <= c1 ? 15u : (1u << (c1 - i)) - 1u);
+        float v[4] = {f[k].x, f[k].y, f[k].z, f[k].w};
+        if (WRITE) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = may >> e & 1u ? v[e] : -INFINITY;
+          if (a.vec && i + 4 <= c1) {
+            __stcs(reinterpret_cast<float4*>(y + i), make_float4(v[0], v[1], v[2], v[3]));
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (i + e < c1) y[i + e] = v[e];
+          }
+        } else {
+          const uint32_t free = may & ~(bits[i >> 5] >> (i & 31));
+          float t[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) t[e] = free >> e & 1u ? v[e] : -INFINITY;
+          if (free && top.beaten(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])))) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (free >> e & 1u) top.take(v[e], i + e);
+          }
+        }
       }
     }
-    if (a.key) {
-      for (int o = 16; o; o >>= 1) {
-        const unsigned long long t = __shfl_xor_sync(0xFFFFFFFFu, top, o);
-        top = t > top ? t : top;
+    if (WRITE) __syncwarp();  // a listed token is written again, by another lane
+    for (int j = lane; j < listed; j += 32) {
+      const int i = list[j];
+      if (i < c0 || i >= c1 || (mask && !(mask[i >> 5] >> (i & 31) & 1u))) continue;
+      uint32_t c = count ? cnt[i] : 0u;
+      if (tree && count)
+        for (int32_t p = up[node]; p >= 0;) {
+          if (draft[p] == (int32_t)(v0 + i)) ++c;
+          p = parent[p] >= 0 ? up[parent[p]] : -1;
+        }
+      const uint32_t times = c & ~kPromptFlag;
+      float f = x[i];
+      if (c && has_rep) f = f > 0.0f ? __fdiv_rn(f, rep) : __fmul_rn(f, rep);
+      if (times) {
+        if (has_freq) f = __fsub_rn(f, __fmul_rn(freq, (float)times));
+        if (has_pres) f = __fsub_rn(f, pres);
       }
-      if (lane == 0 && top) atomicMax(&best[node], top);
+      if (bias && bias_at[i] > 0) f = __fadd_rn(f, a.r.bias_val[bias_at[i] - 1]);
+      if (WRITE) y[i] = f;
+      else top.take(f, i);
+    }
+    if (!WRITE) {
+      unsigned long long k = top.at < 0 ? 0ull : arg_key(top.value, v0 + top.at);
+      for (int o = 16; o; o >>= 1) {
+        const unsigned long long t = __shfl_xor_sync(0xFFFFFFFFu, k, o);
+        k = t > k ? t : k;
+      }
+      if (lane == 0 && k) atomicMax(&best[node], k);
     }
   }
-  if (a.key) {
+  if (!WRITE) {
     __syncthreads();
     for (int i = tid; i < n; i += kRuleThreads) a.key[(off + i) * a.chunks + blockIdx.x] = best[i];
   }
@@ -336,16 +408,20 @@ int launch_rules(const float* logits, int64_t stride, int64_t M, int64_t V, cons
   const bool count = rules->rep || rules->freq || rules->pres;
   const int64_t nodes = M < kRuleMaxNodes ? M : kRuleMaxNodes;
   const size_t smem = (size_t)p.chunk / 8 + (count ? (size_t)p.chunk * 4 : 0) + (rules->bias_off ? (size_t)p.chunk * 4 : 0) +
-                      (parent ? (size_t)nodes * 12 : 0) + 8 + (key ? (size_t)nodes * 8 : 0);
-  constexpr size_t most = 4096 / 8 + 4096 * 8 + kRuleMaxNodes * 20 + 8;
+                      (parent ? (size_t)nodes * 12 : 0) + (key ? (size_t)nodes * 8 : 0) + (size_t)p.chunk * 2;
+  constexpr size_t most = 4096 / 8 + 4096 * 10 + kRuleMaxNodes * 20;
   static int configured[64] = {0};
   int dev = 0;
   W12_CUDA_TRY(cudaGetDevice(&dev));
   if (dev >= 64 || !configured[dev]) {
-    W12_CUDA_TRY(cudaFuncSetAttribute(k_logit_rules, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most));
+    W12_CUDA_TRY(cudaFuncSetAttribute(k_logit_rules<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most));
+    W12_CUDA_TRY(cudaFuncSetAttribute(k_logit_rules<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most));
     if (dev < 64) configured[dev] = 1;
   }
-  k_logit_rules<<<dim3((unsigned)p.chunks, (unsigned)n_req), kRuleThreads, smem, s>>>(a);
+  a.vec = ((stride | (out ? out_stride : 0)) & 3) == 0 && (((uintptr_t)logits | (uintptr_t)out) & 15u) == 0;
+  const dim3 grid((unsigned)p.chunks, (unsigned)n_req);
+  if (key) k_logit_rules<false><<<grid, kRuleThreads, smem, s>>>(a);
+  else k_logit_rules<true><<<grid, kRuleThreads, smem, s>>>(a);
   W12_LAUNCH_CHECK(what);
   return W12_OK;
 }
