@@ -25,8 +25,12 @@
 // Above 128 rows (D <= 128) a tile of keys meets two tiles of rows in turn, with an O each,
 // so K and V are read once for 256 rows.  D = 256 has room for one O: 128 rows, tiles of
 // 64 keys.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include <cmath>
 #include <cstdint>
+#include <mutex>
 
 #include "w12_internal.cuh"
 
@@ -39,6 +43,10 @@ namespace {
 constexpr int kAttnMaxNodes = 256;
 constexpr int32_t kAttnBadRequest = 1, kAttnBadBlock = 2, kAttnTimeout = 4;
 constexpr int kAttnCtas = 152;  // one per SM of a GB300; fewer SMs only run them in turn
+// What a unit costs beside its tiles (its last product, its outputs, the next one's first scores), in
+// tiles; the shares count it in front of the unit.  24 requests of 33 to 12001 tokens took 161 us
+// at 0, 146 at 1, 133 at 2 and 128 at 4.
+constexpr int kUnitCost = 3;
 constexpr int kMetaRing = 2;     // units whose tree shared memory holds
 // P enters its product in two bf16 pieces, the upper one cut off, the lower one rounded: 2^-16
 // of P is lost instead of 2^-8.  The lower piece is taken of P (1 + 2^-20), so that it is above
@@ -68,6 +76,7 @@ struct AttnArgs {
   int64_t table_stride, table_width;
   int32_t n_req, block_size, group, n_heads, n_q_heads, row_cap;
   FastDiv by_block, by_group;
+  int32_t box_rows;  // tokens of a box of the tensor maps; 0: rows are copied by the threads
   float scale_log2;  // scale * log2(e)
   uint16_t* out;
   int32_t* status;
@@ -116,7 +125,7 @@ struct JoinUnit {
 
 struct Req {
   int64_t off;
-  int32_t n, len, tiles, row_units;
+  int32_t n, len, tiles, row_units;  // tiles: of a unit, its cost in front included
   bool ok;
 };
 
@@ -134,7 +143,7 @@ __device__ __forceinline__ Req load_request(const AttnArgs& a, int r) {
   q.n = (int32_t)n;
   q.len = (int32_t)len;
   if (n == 0) return q;
-  q.tiles = (q.len + q.n + P::kBK - 1) / P::kBK;
+  q.tiles = (q.len + q.n + P::kBK - 1) / P::kBK + kUnitCost;
   q.row_units = (q.n * a.group + P::kRows - 1) / P::kRows;
   return q;
 }
@@ -213,6 +222,7 @@ struct Part {
   Req q;
   int32_t r, h, row0, rows;  // rows row0 .. row0 + rows - 1 of the request's nodes * group
   int32_t ta, tb;            // tiles
+  int64_t begin;             // place of the unit's first tile among its request's
 };
 
 template <int D>
@@ -225,29 +235,33 @@ struct Walk {
   __device__ __forceinline__ Walk(const Start& s, int c)
       : at(s.at), left(c < s.ctas ? share(s.total, s.ctas, c + 1) - share(s.total, s.ctas, c) : 0), r(s.r), fresh(true) {}
 
+  // The next part with tiles; false at the share's end.
   __device__ __forceinline__ bool next(const AttnArgs& a, Part& p) {
-    if (left <= 0) return false;
-    if (fresh) {
-      while ((q = load_request<D>(a, r)).tiles == 0) ++r;  // left > 0: a request with tiles follows
-      fresh = false;
+    while (left > 0) {
+      if (fresh) {
+        while ((q = load_request<D>(a, r)).tiles == 0) ++r;  // left > 0: a request with tiles follows
+        fresh = false;
+      }
+      const int64_t u = at / q.tiles;
+      const int32_t ta = (int32_t)(at - u * q.tiles), take = (int32_t)min(left, (int64_t)(q.tiles - ta));
+      p.q = q;
+      p.r = r;
+      p.ta = max(ta - kUnitCost, 0);
+      p.tb = max(ta + take - kUnitCost, 0);
+      p.begin = at - ta + kUnitCost;
+      p.h = (int32_t)(u % a.n_heads);
+      p.row0 = (int32_t)(u / a.n_heads) * AttnPlan<D>::kRows;
+      p.rows = min(AttnPlan<D>::kRows, q.n * a.group - p.row0);
+      at += take;
+      left -= take;
+      if (at == (int64_t)q.tiles * q.row_units * a.n_heads) {
+        ++r;
+        at = 0;
+        fresh = true;
+      }
+      if (p.tb > p.ta) return true;
     }
-    const int64_t u = at / q.tiles;
-    p.q = q;
-    p.r = r;
-    p.ta = (int32_t)(at - u * q.tiles);
-    const int64_t take = left < q.tiles - p.ta ? left : q.tiles - p.ta;
-    p.tb = p.ta + (int32_t)take;
-    p.h = (int32_t)(u % a.n_heads);
-    p.row0 = (int32_t)(u / a.n_heads) * AttnPlan<D>::kRows;
-    p.rows = min(AttnPlan<D>::kRows, q.n * a.group - p.row0);
-    at += take;
-    left -= take;
-    if (at == (int64_t)q.tiles * q.row_units * a.n_heads) {
-      ++r;
-      at = 0;
-      fresh = true;
-    }
-    return true;
+    return false;
   }
 };
 
@@ -361,6 +375,16 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return d;
 }
 
+// A box of the cache: 64 columns x box_rows tokens of one head of one block, swizzled as it lands.
+__device__ __forceinline__ void box_load(uint32_t dst, const CUtensorMap* map, int col, int token, int head, int block,
+                                         uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+          dst),
+      "l"(map), "r"(col), "r"(token), "r"(head), "r"(block), "r"(bar)
+      : "memory");
+}
+
 // ---------------------------------------------------------------- the kernel
 
 struct Shared {
@@ -412,7 +436,8 @@ __device__ __forceinline__ int ring_tile(int item, int cnt, bool two, bool& is_v
 }
 
 template <int D>
-__device__ bool produce(const AttnArgs& a, const Shared& s, Walk<D> walk) {
+__device__ bool produce(const AttnArgs& a, const CUtensorMap* k_map, const CUtensorMap* v_map, const Shared& s,
+                        Walk<D> walk) {
   using P = AttnPlan<D>;
   constexpr int CPR = D / 8;              // 16-byte chunks of a row
   constexpr int RPW = 32 / CPR;           // rows a warp copies at once
@@ -432,14 +457,17 @@ __device__ bool produce(const AttnArgs& a, const Shared& s, Walk<D> walk) {
     // Lane L finds the row that the warp copies in round L / RPW as its (L % RPW)-th: its block (a
     // load that is on its way while the entries before are copied), then its place in the cache,
     // for K and V alike.
+    // Where a tile can go by boxes of the tensor maps, lane L sends for the 4 L + warp-th.
     const int my_row = (lane / RPW) * 4 * RPW + pw * RPW + lane % RPW;
-    auto find_block = [&](int tile) -> int32_t {
-      const int32_t j = tile * P::kBK + my_row;
-      return lane < IT * RPW && j < p.q.len ? table[a.by_block(j)] : 0;
+    const int boxes = a.box_rows ? P::kBK / a.box_rows : 1, my_box = (lane * 4 + pw) % boxes, my_slab = (lane * 4 + pw) / boxes;
+    auto find_block = [&](int tile, int row) -> int32_t {
+      const int32_t j = tile * P::kBK + row;
+      return row < P::kBK && j < p.q.len ? table[a.by_block(j)] : 0;
     };
+    const int ahead_row = a.box_rows ? my_box * a.box_rows : my_row;
     auto find_place = [&](int tile, int32_t id) -> int64_t {  // -1: not in the cache
       const int32_t j = tile * P::kBK + my_row;
-      if (lane >= IT * RPW) return 0;
+      if (my_row >= P::kBK) return 0;
       if (j >= p.q.len) return -1;
       if ((uint32_t)id >= (uint64_t)a.n_blocks) {
         bad_block = true;
@@ -449,18 +477,25 @@ __device__ bool produce(const AttnArgs& a, const Shared& s, Walk<D> walk) {
     };
     int64_t place0 = 0, place1 = 0;  // of the tiles whose K is under way and whose V is not, oldest first
     bool waiting = false;
-    int32_t id = find_block(p.ta);
+    int32_t id = find_block(p.ta, ahead_row);
     for (int item = 0; item < 2 * cnt; ++item, ++entry) {
       bool is_v;
       const int i = ring_tile(item, cnt, two, is_v), tile = p.ta + i;
+      const bool tail = (int64_t)(tile + 1) * P::kBK > p.q.len, by_box = a.box_rows && !tail;
       int64_t at;
       if (is_v) {
         at = place0;
         place0 = place1;
         waiting = !two && item < 2 * cnt - 1;  // K0 K1 V0 K2 V1 ...: one tile stays behind
       } else {
-        at = find_place(tile, id);
-        id = find_block(p.ta + min(i + 1, cnt - 1));
+        if (by_box) {
+          const bool in = (uint32_t)id < (uint64_t)a.n_blocks;
+          bad_block = bad_block || !in;
+          at = in ? id : 0;  // some block: the unit's outputs are dropped
+        } else {
+          at = find_place(tile, a.box_rows ? find_block(tile, my_row) : id);
+        }
+        id = find_block(p.ta + min(i + 1, cnt - 1), ahead_row);
         if (waiting) place1 = at;
         else place0 = at;
         waiting = true;
@@ -469,8 +504,17 @@ __device__ bool produce(const AttnArgs& a, const Shared& s, Walk<D> walk) {
       if (round > 0 && !wait_warp(s.empty + 8 * slot, (round - 1) & 1, s)) return false;
       const uint32_t dst = s.base + P::kRing + slot * P::kSlotBytes;
       const uint16_t* cached = (is_v ? a.vc : a.kc) + chunk * 8;
-      const bool tail = (int64_t)(tile + 1) * P::kBK > p.q.len;
-      if (!tail && __all_sync(0xFFFFFFFFu, at >= 0)) {
+      if (by_box) {
+        const uint32_t bar = s.full + 8 * slot;
+        if (my_slab < D / 64) {
+          const int32_t j = tile * P::kBK + my_box * a.box_rows;
+          mbar_arrive_expect_tx(bar, a.box_rows * 128);
+          box_load(dst + my_slab * (P::kBK * 128) + my_box * a.box_rows * 128, is_v ? v_map : k_map, my_slab * 64,
+                   j - a.by_block(j) * a.block_size, p.h, (int)at, bar);
+        } else {
+          mbar_arrive(bar);
+        }
+      } else if (!tail && __all_sync(0xFFFFFFFFu, at >= 0)) {
 #pragma unroll
         for (int i0 = 0; i0 < IT; i0 += 8) {
           int64_t o[8];
@@ -527,7 +571,8 @@ __device__ bool produce(const AttnArgs& a, const Shared& s, Walk<D> walk) {
         cp_arrive(s.q_full);
       }
       if (item == 2 * cnt - 1 && bad_block) atomicOr(bad, kAttnBadBlock);
-      if (tail && is_v) {
+      if (by_box) {
+      } else if (tail && is_v) {
         // A tile with drafted nodes: an infinity or a NaN in a node's V would reach every row
         // (0 * inf), also those that do not attend to it.  It is taken out here, the node
         // marked, and the rows that do attend to it get it back at the end.
@@ -799,7 +844,7 @@ __device__ bool softmax(const AttnArgs& a, const Shared& s, Walk<D> walk, uint32
     }
     // ---- the part's result, half of the columns each
     if (!product_done(two ? 1 : b_last) || (two && !product_done(2))) return false;
-    const bool whole = p.ta == 0 && p.tb == p.q.tiles;
+    const bool whole = p.ta == 0 && p.tb == p.q.tiles - kUnitCost;
     const int32_t bad = reinterpret_cast<volatile int32_t*>(s.sm + P::kBad)[ring];
     const uint32_t* nf = reinterpret_cast<const uint32_t*>(s.sm + P::kNf) + ring * 8;
     uint32_t any_nf = 0;
@@ -861,7 +906,8 @@ __device__ bool softmax(const AttnArgs& a, const Shared& s, Walk<D> walk, uint32
 }
 
 template <int D>
-__global__ void __launch_bounds__(AttnPlan<D>::kThreads, 1) k_tree_attn(AttnArgs a) {
+__global__ void __launch_bounds__(AttnPlan<D>::kThreads, 1) k_tree_attn(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap k_map,
+                const __grid_constant__ CUtensorMap v_map) {
   using P = AttnPlan<D>;
   extern __shared__ __align__(1024) uint8_t attn_sm[];
   const int tid = threadIdx.x, warp = tid >> 5, c = blockIdx.x;
@@ -931,19 +977,26 @@ __global__ void __launch_bounds__(AttnPlan<D>::kThreads, 1) k_tree_attn(AttnArgs
   if (tid == P::kThreads - 1) {
     Part p;
     Walk<D> w = walk;
-    w.next(a, p);
-    // shares first .. last begin inside the unit: begin < total * i / ctas < begin + tiles
-    const int64_t begin = share(start.total, start.ctas, c) - p.ta;
-    a.units[c] = JoinUnit{p.q.off, p.h, p.row0, p.ta > 0 ? p.rows : 0,
-                          (int32_t)(((begin + 1) * start.ctas + start.total - 1) / start.total),
-                          (int32_t)(((begin + p.q.tiles) * start.ctas + start.total - 1) / start.total) - 1, 0};
+    JoinUnit u{};
+    if (w.next(a, p) && p.ta > 0) {
+      // shares first .. last begin behind the unit's first tile: begin < total * i / ctas < end
+      const int64_t begin = share(start.total, start.ctas, c) - start.at + p.begin, end = begin + p.q.tiles - kUnitCost;
+      u = JoinUnit{p.q.off, p.h, p.row0, p.rows, (int32_t)(((begin + 1) * start.ctas + start.total - 1) / start.total),
+                   (int32_t)((end * start.ctas + start.total - 1) / start.total) - 1, 0};
+    }
+    a.units[c] = u;
   }
   bool ok = true;
   if (warp < P::kSoftmaxThreads / 32) {
     ok = softmax<D>(a, s, walk, tmem, c);
   } else if (warp < P::kSoftmaxThreads / 32 + 4) {
-    ok = produce<D>(a, s, walk);
-    if (!ok) cp_wait_all();
+    ok = produce<D>(a, &k_map, &v_map, s, walk);
+    if (!ok) {  // nothing may be on its way into shared memory when the block ends
+      cp_wait_all();
+      const long long began = clock64();
+      while (a.box_rows && clock64() - began < (1ll << 24)) {
+      }
+    }
   } else {
     ok = issue_mma<D>(a, s, walk, tmem);
     if (!ok) {  // nothing may be in flight when tensor memory goes back
@@ -1028,8 +1081,44 @@ int64_t row_cap(int64_t M, int64_t group, int64_t D) {
   return rows >= most ? most : (rows + 31) / 32 * 32;
 }
 
+PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
+  static std::once_flag once;
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  std::call_once(once, [] {
+    cudaDriverEntryPointQueryResult q;
+    void* p = nullptr;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  });
+  return fn;
+}
+
+// The cache as a 4-D tensor (column, token of a block, head, block) in boxes of 64 columns x `rows`
+// tokens, 128-byte swizzle.
+bool make_cache_map(CUtensorMap* map, const uint16_t* base, const kv_cache* c, int rows) {
+  auto enc = map_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[4] = {(cuuint64_t)c->head_dim, (cuuint64_t)c->block_size, (cuuint64_t)c->n_heads, (cuuint64_t)c->n_blocks};
+  cuuint64_t strides[3] = {(cuuint64_t)c->token_stride * 2, (cuuint64_t)c->head_stride * 2, (cuuint64_t)c->block_stride * 2};
+  cuuint32_t box[4] = {64, (cuuint32_t)rows, 1, 1}, one[4] = {1, 1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint16_t*>(base), dims, strides, box, one,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Tokens of a box: blocks of a power of two tokens, 8 or more, split a tile evenly or are split by
+// it; other block sizes (and strides of zero) go row by row through the threads.
+int box_rows(const kv_cache* c, int bk) {
+  const int64_t b = c->block_size, most = (int64_t)1 << 39;
+  if (b < 8 || (b & (b - 1)) || c->token_stride < 1 || c->head_stride < 1 || c->block_stride < 1 ||
+      c->token_stride >= most || c->head_stride >= most || c->block_stride >= most)
+    return 0;
+  return b < bk ? (int)b : bk;
+}
+
 template <int D>
-int launch_attn(const AttnArgs& a, cudaStream_t s) {
+int launch_attn(AttnArgs a, const kv_cache* c, cudaStream_t s) {
   using P = AttnPlan<D>;
   static int configured[64] = {0};
   int dev = 0;
@@ -1038,7 +1127,10 @@ int launch_attn(const AttnArgs& a, cudaStream_t s) {
     W12_CUDA_TRY(cudaFuncSetAttribute(k_tree_attn<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kBytes));
     if (dev < 64) configured[dev] = 1;
   }
-  k_tree_attn<D><<<kAttnCtas, P::kThreads, P::kBytes, s>>>(a);
+  CUtensorMap k_map{}, v_map{};
+  a.box_rows = box_rows(c, P::kBK);
+  if (a.box_rows && !(make_cache_map(&k_map, a.kc, c, a.box_rows) && make_cache_map(&v_map, a.vc, c, a.box_rows))) a.box_rows = 0;
+  k_tree_attn<D><<<kAttnCtas, P::kThreads, P::kBytes, s>>>(a, k_map, v_map);
   W12_LAUNCH_CHECK("tree_attn kernel");
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1148,7 +1240,7 @@ int tree_attn(const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_
   a.part_bad = reinterpret_cast<int32_t*>(base + w.bad);
   a.units = reinterpret_cast<JoinUnit*>(base + w.units);
   cudaStream_t s = (cudaStream_t)stream;
-  return D == 64 ? launch_attn<64>(a, s) : D == 128 ? launch_attn<128>(a, s) : launch_attn<256>(a, s);
+  return D == 64 ? launch_attn<64>(a, cache, s) : D == 128 ? launch_attn<128>(a, cache, s) : launch_attn<256>(a, cache, s);
 }
 
 }  // extern "C"

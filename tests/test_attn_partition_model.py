@@ -7,6 +7,7 @@ import random
 import pytest
 
 CTAS = 152
+COST = 3   # tiles that a unit counts for beside its own, in front of them
 
 
 def share(total, ctas, c):
@@ -14,16 +15,18 @@ def share(total, ctas, c):
 
 
 def walk(units, total, ctas, c):
-    """Parts (unit, ta, tb) of CTA c's share; units are (tiles, rows)."""
+    """Parts (unit, ta, tb) of CTA c's share; units are (tiles, rows).  Parts without tiles are left out."""
     at, left, u = share(total, ctas, c), share(total, ctas, c + 1) - share(total, ctas, c), 0
-    while at >= units[u][0]:
-        at -= units[u][0]
+    while at >= units[u][0] + COST:
+        at -= units[u][0] + COST
         u += 1
     parts = []
     while left > 0:
-        tb = min(units[u][0], at + left)
-        parts.append((u, at, tb))
-        left -= tb - at
+        end = min(units[u][0] + COST, at + left)
+        ta, tb = max(at - COST, 0), max(end - COST, 0)
+        if tb > ta:
+            parts.append((u, ta, tb))
+        left -= end - at
         at, u = 0, u + 1
     return parts
 
@@ -35,11 +38,11 @@ def test_parts_and_joins(seed):
     n = {"few long": rng.randint(1, 8), "many short": rng.randint(100, 900), "mixed": rng.randint(1, 300)}[kind]
     units = [({"few long": rng.randint(1, 3000), "many short": rng.randint(1, 3), "mixed": rng.choice([1, 2, 50, 300])}[kind],
               rng.randint(1, 256)) for _ in range(n)]
-    total = sum(t for t, _ in units)
+    total = sum(t + COST for t, _ in units)
     ctas = min(total, CTAS)
-    start = [0]
+    start = [COST]
     for t, _ in units:
-        start.append(start[-1] + t)
+        start.append(start[-1] + t + COST)
     taken = [[0] * t for t, _ in units]
     whole, slots, desc = set(), {}, {}
     for c in range(CTAS):
@@ -47,7 +50,6 @@ def test_parts_and_joins(seed):
             desc[c] = (0, None, None, None)                     # rows = 0, the rest left as it was
             continue
         parts = walk(units, total, ctas, c)
-        assert parts
         for k, (u, ta, tb) in enumerate(parts):
             for t in range(ta, tb):
                 taken[u][t] += 1
@@ -57,12 +59,13 @@ def test_parts_and_joins(seed):
             slot = 2 * c + (0 if ta > 0 else 1)
             assert 0 <= slot < 2 * CTAS and slot not in slots
             slots[slot] = u
-        u, ta, _ = parts[0]
-        begin = share(total, ctas, c) - ta
-        assert begin == start[u]
-        first = ((begin + 1) * ctas + total - 1) // total
-        last = ((begin + units[u][0]) * ctas + total - 1) // total - 1
-        desc[c] = (units[u][1] if ta > 0 else 0, u, first, last)
+        desc[c] = (0, None, None, None)
+        if parts and parts[0][1] > 0:
+            u = parts[0][0]
+            begin = start[u]
+            first = ((begin + 1) * ctas + total - 1) // total
+            last = ((begin + units[u][0]) * ctas + total - 1) // total - 1
+            desc[c] = (units[u][1], u, first, last)
     assert all(x == 1 for t in taken for x in t)
     joined, threads, gy = {}, 256, rng.choice([1, 4])
     for c in range(1, CTAS):
