@@ -13,6 +13,7 @@ together by :func:`encode`), :func:`w12_decode`, :func:`w12_decode_q8`,
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 import typing
@@ -165,6 +166,12 @@ def _empty(shape, dtype, device, stream) -> torch.Tensor:
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _raw_stream(stream, t: torch.Tensor) -> int:
+    """Handle of the stream, or of the current one of t's device (torch.cuda.current_stream builds an
+    object around it, which takes longer than a small call's other host work)."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else stream.cuda_stream
+
+
 def _zero_status(status, device, stream) -> torch.Tensor:
     """The caller's status word, or a new one zeroed on the call's stream."""
     if status is not None:
@@ -308,15 +315,16 @@ class Workspace:
             self.buf = torch.zeros(int(nbytes), dtype=torch.uint8, device=self.device)
         return self.buf
 
-    def scratch(self, nbytes: int, stream) -> torch.Tensor:
-        """A buffer for the calls on `stream` whose workspace needs no initial state, apart from
-        get()'s: what they leave in it must not stand where a GEMM expects its counters at zero."""
+    def scratch(self, nbytes: int, stream, raw: int) -> torch.Tensor:
+        """A buffer for the calls on `stream` (its handle `raw`; None: the current one) whose
+        workspace needs no initial state, apart from get()'s: what they leave in it must not
+        stand where a GEMM expects its counters at zero."""
         t = self._scratch
         if t is None or nbytes > t.numel():
             t = self._scratch = _empty(max(int(nbytes), 256), torch.uint8, self.device, stream)
-            self._scratch_stream = stream.cuda_stream
-        if stream.cuda_stream != self._scratch_stream:  # not to be reused while that stream still works on it
-            t.record_stream(stream)
+            self._scratch_stream = raw
+        if raw != self._scratch_stream:  # not to be reused while that stream still works on it
+            t.record_stream(torch.cuda.current_stream() if stream is None else stream)
         return t
 
     def status(self, stream=None) -> int:
@@ -621,7 +629,8 @@ def _rows16(t: torch.Tensor, name: str, dims: int) -> torch.Tensor:
         raise TypeError(f"expected bf16 bits (bfloat16/int16/uint16) in {name}, got {t.dtype}")
     if t.dim() != dims or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor of {dims} dimensions")
-    if t.stride(-1) != 1 and t.shape[-1] != 1 or t.stride(-2) != t.shape[-1] and t.shape[-2] != 1:
+    stride, shape = t.stride(), t.shape
+    if stride[-1] != 1 and shape[-1] != 1 or stride[-2] != shape[-1] and shape[-2] != 1:
         raise ValueError(f"the heads of a row of {name} must be adjacent")
     return t
 
@@ -680,14 +689,17 @@ def kv_slots(cache_len, add, table, pool, pool_pos, block_size: int, capacity: i
     # one allocation for the int64 results and one for the int32 ones
     wide = _empty(capacity + 3, torch.int64, dev, stream)
     slim = _empty(capacity + n_req, torch.int32, dev, stream)
-    out = Slots(wide[3:], slim[n_req:], slim[:n_req], wide[:2], wide[2:3], _zero_status(status, dev, stream))
+    status = _zero_status(status, dev, stream)
     w, i = wide.data_ptr(), slim.data_ptr()
-    _check(lib().kv_slots(_ptr(cache_len), _ptr(add), int(extra), n_req, _ptr(table), _row_stride(table),
-                          table.shape[1], _ptr(_i32(pool)), pool.numel(), _ptr(pool_pos), int(block_size),
-                          _ptr(None if path_nodes is None else _i32(path_nodes)),
-                          _ptr(None if req_offsets is None else _i32(req_offsets)), 0 if path_nodes is None else path_nodes.numel(), int(capacity), w + 24, i + 4 * n_req, i, w,
-                          w + 16, _ptr(out.status), _stream(stream)))
-    return out
+    _check((_lib or lib()).kv_slots(
+        cache_len.data_ptr(), add.data_ptr(), extra, n_req, table.data_ptr(), _row_stride(table), table.shape[1],
+        _i32(pool).data_ptr(), pool.numel(), pool_pos.data_ptr(), block_size,
+        None if path_nodes is None else _i32(path_nodes).data_ptr(),
+        None if req_offsets is None else _i32(req_offsets).data_ptr(), 0 if path_nodes is None else path_nodes.numel(),
+        capacity, w + 24, i + 4 * n_req, i, w, w + 16, status.data_ptr(), _raw_stream(stream, table)))
+    pool_pos, total, slot = wide.split_with_sizes((2, 1, capacity))
+    new_len, src = slim.split_with_sizes((n_req, capacity))
+    return Slots(slot, src, new_len, pool_pos, total, status)
 
 
 def _row_stride(t: torch.Tensor) -> int:
@@ -718,10 +730,22 @@ def kv_write(cache: KVCache, k, v, slot, src=None, layer: int = 0, status=None, 
     if src is not None and _i32(src).numel() != n:
         raise ValueError("src must have an entry for each slot")
     status = _zero_status(status, slot.device, stream)
-    _check(lib().kv_write(cache.desc(), layer, k.shape[0] if dims == 4 else 1, _ptr(k), k.stride(0) if dims == 4 else 0,
-                          k.stride(-3), _ptr(v), v.stride(0) if dims == 4 else 0, v.stride(-3), k.shape[-3], _ptr(slot),
-                          _ptr(src), n, _ptr(status), _stream(stream)))
+    ks, vs = k.stride(), v.stride()
+    _check((_lib or lib()).kv_write(
+        cache.desc(), layer, k.shape[0] if dims == 4 else 1, k.data_ptr(), ks[0] if dims == 4 else 0, ks[-3],
+        v.data_ptr(), vs[0] if dims == 4 else 0, vs[-3], k.shape[-3], slot.data_ptr(),
+        None if src is None else src.data_ptr(), n, status.data_ptr(), _raw_stream(stream, slot)))
     return status
+
+
+@functools.lru_cache(maxsize=256)
+def _attn_bytes(M: int, n_req: int, n_q_heads: int, n_heads: int, head_dim: int) -> int:
+    return int(lib().tree_attn_workspace_size(M, n_req, n_q_heads, n_heads, head_dim))
+
+
+@functools.lru_cache(maxsize=256)
+def _verify_bytes(M: int, V: int, n_req: int) -> int:
+    return int(lib().logits_verify_workspace_size(M, V, n_req))
 
 
 def tree_attn(q, k, v, cache: KVCache, table, cache_len, parent, req_offsets=None, layer: int = 0,
@@ -745,14 +769,13 @@ def tree_attn(q, k, v, cache: KVCache, table, cache_len, parent, req_offsets=Non
     elif _bits16(out).shape != q.shape:
         raise ValueError(f"out must be {tuple(q.shape)}")
     status = _zero_status(status, q.device, stream)
-    L = lib()
-    on = stream if stream is not None else torch.cuda.current_stream()
-    buf = (ws or Workspace(q.device)).scratch(L.tree_attn_workspace_size(M, n_req, hq, cache.n_heads, D), on)
-    _check(L.tree_attn(q.data_ptr(), q.stride(0), k.data_ptr(), k.stride(0), v.data_ptr(), v.stride(0), M, hq,
-                       cache.desc(), layer, table.data_ptr(), _row_stride(table), table.shape[1],
-                       cache_len.data_ptr(), parent.data_ptr(), _ptr(req_offsets), n_req,
-                       D ** -0.5 if scale is None else scale, out.data_ptr(), status.data_ptr(), buf.data_ptr(),
-                       buf.numel(), on.cuda_stream))
+    raw = _raw_stream(stream, q)
+    buf = (ws or Workspace(q.device)).scratch(_attn_bytes(M, n_req, hq, cache.n_heads, D), stream, raw)
+    _check((_lib or lib()).tree_attn(
+        q.data_ptr(), q.stride(0), k.data_ptr(), k.stride(0), v.data_ptr(), v.stride(0), M, hq, cache.desc(), layer,
+        table.data_ptr(), _row_stride(table), table.shape[1], cache_len.data_ptr(), parent.data_ptr(),
+        None if req_offsets is None else req_offsets.data_ptr(), n_req, D ** -0.5 if scale is None else scale,
+        out.data_ptr(), status.data_ptr(), buf.data_ptr(), buf.numel(), raw))
     return out, status
 
 
@@ -816,9 +839,9 @@ def logits_process(logits, rules: LogitRules, parent=None, draft=None, req_offse
     elif out.dtype != torch.float32 or out.shape != logits.shape or not out.is_cuda or (out.stride(1) != 1 and V != 1):
         raise ValueError(f"out must be a float32 CUDA tensor [{M}, {V}] with adjacent columns")
     status = _zero_status(status, logits.device, stream)
-    _check(lib().logits_process(logits.data_ptr(), stride, M, V, rules.desc(), _ptr(parent), _ptr(draft),
-                                _ptr(req_offsets), n_req, out.data_ptr(), _row_stride(out), status.data_ptr(),
-                                _stream(stream)))
+    _check((_lib or lib()).logits_process(
+        logits.data_ptr(), stride, M, V, rules.desc(), _ptr(parent), _ptr(draft), _ptr(req_offsets), n_req,
+        out.data_ptr(), _row_stride(out), status.data_ptr(), _raw_stream(stream, logits)))
     return out, status
 
 
@@ -827,14 +850,13 @@ def logits_verify(logits, rules: LogitRules, parent, draft, req_offsets=None, ws
     """Argmax under the rules and greedy acceptance, without writing the processed logits:
     returns (tok, path_len, path_nodes, bonus, status)."""
     M, V, n_req, stride = _rule_args(logits, rules, parent, draft, req_offsets)
-    L = lib()
     both = _empty(2 * M + 2 * n_req, torch.int32, logits.device, stream)
-    tok, path_nodes, path_len, bonus = both[:M], both[M:2 * M], both[2 * M:2 * M + n_req], both[2 * M + n_req:]
     status = _zero_status(status, logits.device, stream)
-    on = stream if stream is not None else torch.cuda.current_stream()
-    buf = (ws or Workspace(logits.device)).scratch(L.logits_verify_workspace_size(M, V, n_req), on)
+    raw = _raw_stream(stream, logits)
+    buf = (ws or Workspace(logits.device)).scratch(_verify_bytes(M, V, n_req), stream, raw)
     at = both.data_ptr()
-    _check(L.logits_verify(logits.data_ptr(), stride, M, V, rules.desc(), _ptr(parent), _ptr(draft), _ptr(req_offsets),
-                           n_req, at, at + 8 * M, at + 4 * M, at + 8 * M + 4 * n_req, status.data_ptr(), buf.data_ptr(),
-                           buf.numel(), on.cuda_stream))
+    _check((_lib or lib()).logits_verify(
+        logits.data_ptr(), stride, M, V, rules.desc(), _ptr(parent), _ptr(draft), _ptr(req_offsets), n_req, at, at + 8 * M,
+        at + 4 * M, at + 8 * M + 4 * n_req, status.data_ptr(), buf.data_ptr(), buf.numel(), raw))
+    tok, path_nodes, path_len, bonus = both.split_with_sizes((M, M, n_req, n_req))
     return tok, path_len, path_nodes, bonus, status

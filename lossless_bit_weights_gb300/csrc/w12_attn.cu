@@ -155,44 +155,51 @@ struct Start {
   int32_t r, ctas;
 };
 
-// Total number of tiles and, for CTA c of the grid, the request in which its share begins
-// (every thread of the block calls this; scratch: 2 + threads/32 int64 of shared memory).
+// Total number of tiles and, for CTA c of the grid, the request in which its share begins.  Every
+// thread of the block calls this.  Up to 32 requests each warp finds it for itself, without a
+// barrier; more take the whole block (scratch: 2 + threads / 32 int64 of shared memory).
 template <int D>
-__device__ __forceinline__ Start find_start(const AttnArgs& a, int c, int threads, int64_t* scratch, int32_t* bad) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = threads >> 5;
+__device__ __forceinline__ Start find_start(const AttnArgs& a, int c, int64_t* scratch) {
+  constexpr int threads = AttnPlan<D>::kThreads, warps = threads / 32;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const bool small = a.n_req <= 32;
   int64_t mine = 0, sum = 0;
-  for (int r = tid; r < a.n_req; r += threads) {
+  for (int r = small ? lane : tid; r < a.n_req; r += threads) {
     const Req q = load_request<D>(a, r);
-    if (!q.ok && bad) *bad = 1;
+    if (!q.ok && c == 0) atomicOr(a.status, kAttnBadRequest);
     mine = (int64_t)q.tiles * q.row_units * a.n_heads;
     sum += mine;
   }
-  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-  if (lane == 0) scratch[2 + warp] = sum;
-  __syncthreads();
   Start s{0, 0, 0, 0};
-  for (int w = 0; w < warps; ++w) s.total += scratch[2 + w];
-  s.ctas = (int32_t)(s.total < kAttnCtas ? s.total : kAttnCtas);
-  if (s.ctas == 0 || c >= s.ctas) return s;
-  const int64_t want = share(s.total, s.ctas, c);
-  if (a.n_req == 1) {
-    s.at = want;
+  int64_t v = small ? mine : sum;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t u = __shfl_up_sync(0xFFFFFFFFu, v, o);
+    if (lane >= o) v += u;
+  }
+  if (small) {
+    s.total = __shfl_sync(0xFFFFFFFFu, v, 31);
+    s.ctas = (int32_t)(s.total < kAttnCtas ? s.total : kAttnCtas);
+    if (c >= s.ctas) return s;
+    const int64_t want = share(s.total, s.ctas, c);
+    s.r = __ffs((int)__ballot_sync(0xFFFFFFFFu, want < v)) - 1;  // want < total: some lane says yes
+    s.at = want - __shfl_sync(0xFFFFFFFFu, v - mine, s.r);
     return s;
   }
+  if (lane == 31) scratch[2 + warp] = v;
+  __syncthreads();
+  for (int w = 0; w < warps; ++w) s.total += scratch[2 + w];
+  s.ctas = (int32_t)(s.total < kAttnCtas ? s.total : kAttnCtas);
+  if (c >= s.ctas) return s;
+  const int64_t want = share(s.total, s.ctas, c);
   int64_t carry = 0;
-  for (int r0 = 0; r0 < a.n_req; r0 += threads) {  // one pass unless there are more requests than threads
+  for (int r0 = 0; r0 < a.n_req; r0 += threads) {
     const int r = r0 + tid;
-    int64_t w = mine;
-    if (a.n_req > threads) {
-      w = 0;
-      if (r < a.n_req) {
-        const Req q = load_request<D>(a, r);
-        w = (int64_t)q.tiles * q.row_units * a.n_heads;
-      }
-    } else if (r >= a.n_req) {
-      w = 0;
+    int64_t w = 0;
+    if (r < a.n_req) {
+      const Req q = load_request<D>(a, r);
+      w = (int64_t)q.tiles * q.row_units * a.n_heads;
     }
-    int64_t v = w;
+    v = w;
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t u = __shfl_up_sync(0xFFFFFFFFu, v, o);
       if (lane >= o) v += u;
@@ -542,17 +549,21 @@ __device__ bool produce(const AttnArgs& a, const CUtensorMap* k_map, const CUten
         }
       }
       if (item == 0) {
-        // ---- the unit's query rows (zero past its own) and its tree, behind the first keys.  The
+        // ---- the unit's query rows (past them shared memory stays as it is) and its tree, behind the first keys.  The
         // last unit's scores are there and the one before it is at its end: the rows of the one
         // and the tree of the other may go.
         if (unit > 0 && !wait_warp(s.q_free, (unit - 1) & 1, s)) return false;
-        const int q_rows = p.rows > 128 ? 256 : 128;
-        for (int row0 = 0; row0 < q_rows; row0 += 4 * RPW) {
-          const int row = row0 + pw * RPW + sub, r = p.row0 + row, node = a.by_group(r);
-          const bool in = row < p.rows;
-          cp16(s.base + P::kQ + (row >> 7) * P::kQTile + (chunk >> 3) * 16384 + (row & 127) * 128 +
-                   (((chunk & 7) ^ (row & 7)) << 4),
-               in ? a.q + (p.q.off + node) * a.q_stride + (int64_t)(p.h * a.group + r - node * a.group) * D + chunk * 8 : a.q, in);
+        for (int row0 = 0; row0 < p.rows; row0 += P::kBK) {
+          const int r = p.row0 + row0 + my_row, node = a.by_group(r);
+          const int64_t o = (p.q.off + node) * a.q_stride + (int64_t)(p.h * a.group + r - node * a.group) * D;
+          for (int it = 0; it < IT && row0 + it * 4 * RPW < p.rows; ++it) {
+            const int row = row0 + it * 4 * RPW + pw * RPW + sub;
+            const int64_t from = __shfl_sync(0xFFFFFFFFu, o, it * RPW + sub);
+            if (row < p.rows)
+              cp16(s.base + P::kQ + (row >> 7) * P::kQTile + (chunk >> 3) * 16384 + (row & 127) * 128 +
+                       (((chunk & 7) ^ (row & 7)) << 4),
+                   a.q + from + chunk * 8);
+          }
         }
         if (pt < 8) nf[pt] = 0;
         if (pt == 8) *bad = 0;
@@ -777,7 +788,7 @@ __device__ bool softmax(const AttnArgs& a, const Shared& s, Walk<D> walk, uint32
         top[0] = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
         if (!exchange(top[0], top[1])) return false;
         const float want = fmaxf(top[0], top[1]) * a.scale_log2;
-        const bool move = want - ref > kRefSlack;
+        const bool move = row < p.rows && want - ref > kRefSlack;  // (rows past the unit's hold anything)
         if (__any_sync(0xFFFFFFFFu, move)) {
           const float next = move ? want : ref;
           if (i > 0) {
@@ -955,12 +966,8 @@ __global__ void __launch_bounds__(AttnPlan<D>::kThreads, 1) k_tree_attn(const __
     mbar_init(s.drain, 1);
     mbar_init_fence();
     misc[1] = 0;  // abort
-    misc[2] = 0;  // a request out of range
   }
-  __syncthreads();
-  const Start start = find_start<D>(a, c, P::kThreads, reinterpret_cast<int64_t*>(attn_sm + P::kRing), misc + 2);
-  __syncthreads();  // the sums' scratch is the ring's from here on
-  if (c == 0 && tid == 0 && misc[2]) atomicOr(a.status, kAttnBadRequest);
+  const Start start = find_start<D>(a, c, reinterpret_cast<int64_t*>(attn_sm + P::kRing));
   if (c >= start.ctas) {
     if (tid == 0) a.units[c].rows = 0;
     return;
