@@ -15,6 +15,15 @@
 
 #include "w12_internal.cuh"
 
+#ifndef MINB
+#define MINB 4
+#endif
+#ifndef CHMAX
+#define CHMAX 4096
+#endif
+#ifndef CHMIN
+#define CHMIN 1024
+#endif
 namespace w12 {
 namespace {
 
@@ -65,8 +74,6 @@ struct Best {
       value = f;
     }
   }
-  // Whether one of four values, the largest of them `top`, may be larger.
-  __device__ __forceinline__ bool beaten(float top) const { return top > value || key <= INT32_MIN + 1; }
 };
 
 __device__ __forceinline__ float4 load4(const float* x, int i, int n, bool vec) {
@@ -80,7 +87,7 @@ __device__ __forceinline__ float4 load4(const float* x, int i, int n, bool vec) 
 }
 
 template <bool WRITE>
-__global__ void __launch_bounds__(kRuleThreads) k_logit_rules(RuleArgs a) {
+__global__ void __launch_bounds__(kRuleThreads, MINB) k_logit_rules(const __grid_constant__ RuleArgs a) {
   extern __shared__ uint32_t sm[];
   __shared__ int s_listed[kRuleWarps];
   const int r = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -106,6 +113,10 @@ __global__ void __launch_bounds__(kRuleThreads) k_logit_rules(RuleArgs a) {
   int32_t* up = draft + (tree ? n : 0);  // the nearest node on the path whose token is in the chunk
   uint16_t* list = reinterpret_cast<uint16_t*>(up + (tree ? n : 0));
 
+  // the rows' chunk comes into L2 while the tables are made
+  if (a.vec)
+    for (int i = tid; i < n; i += kRuleThreads)
+      if (width >= 4) prefetch_l2(a.logits + (off + i) * a.stride + v0, (uint32_t)(width & ~3) * 4);
   for (int i = tid; i < a.chunk / 32; i += kRuleThreads) bits[i] = 0;
   if (count)
     for (int i = tid; i < a.chunk; i += kRuleThreads) cnt[i] = 0;
@@ -204,7 +215,10 @@ __global__ void __launch_bounds__(kRuleThreads) k_logit_rules(RuleArgs a) {
     const float* x = a.logits + m * a.stride + v0;
     float* y = WRITE ? a.out + m * a.out_stride + v0 : nullptr;
     const uint32_t* mask = a.r.mask ? a.r.mask + m * a.r.mask_stride + v0 / 32 : nullptr;
-    Best top;
+    // The untouched tokens: the largest value so far and the four tokens it was first seen among,
+    // three instructions for four tokens; which of the four is asked once, at the end.
+    float high = -INFINITY;
+    int high_at = -1;
     constexpr int U = 4;
     for (int i0 = c0; i0 < c1; i0 += 128 * U) {
       float4 f[U];
@@ -213,35 +227,52 @@ __global__ void __launch_bounds__(kRuleThreads) k_logit_rules(RuleArgs a) {
       for (int k = 0; k < U; ++k) {
         const int i = i0 + k * 128 + 4 * lane;
         f[k] = load4(x, i, c1, a.vec);
-        allowed[k] = i >= c1 ? 0u : mask ? mask[i >> 5] >> (i & 31) & 15u : 15u;
+        allowed[k] = i >= c1 ? 0u : mask ? mask[i >> 5] >> (i & 31) : 15u;
       }
 #pragma unroll
       for (int k = 0; k < U; ++k) {
         const int i = i0 + k * 128 + 4 * lane;
         if (i >= c1) break;
-        const uint32_t may = allowed[k] & (i + 4 <= c1 ? 15u : (1u << (c1 - i)) - 1u);
-        float v[4] = {f[k].x, f[k].y, f[k].z, f[k].w};
+        uint32_t may = allowed[k] & (i + 4 <= c1 ? 15u : (1u << (c1 - i)) - 1u);
+        if (!WRITE) may &= ~(bits[i >> 5] >> (i & 31));
+        if (may != 15u) {
+          f[k].x = may & 1u ? f[k].x : -INFINITY;
+          f[k].y = may & 2u ? f[k].y : -INFINITY;
+          f[k].z = may & 4u ? f[k].z : -INFINITY;
+          f[k].w = may & 8u ? f[k].w : -INFINITY;
+        }
         if (WRITE) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = may >> e & 1u ? v[e] : -INFINITY;
           if (a.vec && i + 4 <= c1) {
-            __stcs(reinterpret_cast<float4*>(y + i), make_float4(v[0], v[1], v[2], v[3]));
+            __stcs(reinterpret_cast<float4*>(y + i), f[k]);
           } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (i + e < c1) y[i + e] = v[e];
+            y[i] = f[k].x;
+            if (i + 1 < c1) y[i + 1] = f[k].y;
+            if (i + 2 < c1) y[i + 2] = f[k].z;
+            if (i + 3 < c1) y[i + 3] = f[k].w;
           }
         } else {
-          const uint32_t free = may & ~(bits[i >> 5] >> (i & 31));
-          float t[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) t[e] = free >> e & 1u ? v[e] : -INFINITY;
-          if (free && top.beaten(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])))) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (free >> e & 1u) top.take(v[e], i + e);
+          const float t = fmaxf(fmaxf(f[k].x, f[k].y), fmaxf(f[k].z, f[k].w));
+          if (t > high) {
+            high = t;
+            high_at = i;
           }
         }
+      }
+    }
+    Best top;
+    if (!WRITE) {
+      auto allows = [&](int i) {
+        return !(bits[i >> 5] >> (i & 31) & 1u) && (!mask || (mask[i >> 5] >> (i & 31) & 1u));
+      };
+      float most = high;
+      for (int o = 16; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
+      if (most > -INFINITY) {
+        if (high == most)  // the first of the four; the lanes' candidates meet in the keys below
+          for (int e = 3; e >= 0; --e)
+            if (high_at + e < c1 && allows(high_at + e) && x[high_at + e] == most) top.take(most, high_at + e);
+      } else {  // nothing above -inf: the first -inf, or else the first NaN
+        for (int i = c0 + lane; i < c1; i += 32)
+          if (allows(i)) top.take(x[i], i);
       }
     }
     if (WRITE) __syncwarp();  // a listed token is written again, by another lane
@@ -289,6 +320,7 @@ __global__ void __launch_bounds__(kRuleThreads) k_rule_accept(const unsigned lon
                                                               int32_t* __restrict__ path_nodes, int32_t* bonus) {
   __shared__ int32_t tok[kRuleMaxNodes], parent[kRuleMaxNodes], draft[kRuleMaxNodes];
   __shared__ unsigned long long s_best;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the keys are the previous kernel's
   const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int64_t off;
   int n;
@@ -356,7 +388,7 @@ struct RulePlan {
 // there are.  The largest of 4096, 2048, 1024 with at least two blocks per SM.
 RulePlan rule_plan(int64_t M, int64_t V, int32_t n_req) {
   RulePlan p{};
-  for (p.chunk = 4096; p.chunk > 1024; p.chunk /= 2)
+  for (p.chunk = CHMAX; p.chunk > CHMIN; p.chunk /= 2)
     if ((V + p.chunk - 1) / p.chunk * n_req >= 304) break;
   p.chunks = (int)((V + p.chunk - 1) / p.chunk);
   const int64_t rows = (M + n_req - 1) / n_req;
@@ -465,8 +497,17 @@ int logits_verify(const float* logits, int64_t stride, int64_t M, int64_t V, con
   st = launch_rules(logits, stride, M, V, rules, parent, draft, req_offsets, n_req, nullptr, 0, status, key,
                     (cudaStream_t)stream, "logits_verify: rules kernel");
   if (st) return st;
-  k_rule_accept<<<(unsigned)n_req, kRuleThreads, 0, (cudaStream_t)stream>>>(
-      key, rule_plan(M, V, n_req).chunks, parent, draft, req_offsets, M, tok, path_len, path_nodes, bonus);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)n_req);
+  cfg.blockDim = dim3(kRuleThreads);
+  cfg.stream = (cudaStream_t)stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  W12_CUDA_TRY(cudaLaunchKernelEx(&cfg, k_rule_accept, (const unsigned long long*)key, rule_plan(M, V, n_req).chunks, parent,
+                                  draft, req_offsets, M, tok, path_len, path_nodes, bonus));
   W12_LAUNCH_CHECK("logits_verify: acceptance kernel");
   return W12_OK;
 }
