@@ -68,7 +68,7 @@ __device__ __forceinline__ int owner(const int32_t* pre, int n, int32_t t) {
 // fills its part of the slots, of the new table entries and of the returned blocks, so
 // one launch does it all and nothing waits on another block: what a block reads (old table
 // entries, the pool's front) no block writes (new entries, the pool behind its back).
-__global__ void __launch_bounds__(kSlotThreads) k_kv_slots(SlotArgs a) {
+__global__ void __launch_bounds__(kSlotThreads) k_kv_slots(const __grid_constant__ SlotArgs a) {
   extern __shared__ int32_t sm[];
   int32_t* pre_tok = sm;                       // n_req + 1 each
   int32_t* pre_new = pre_tok + a.n_req + 1;
@@ -203,24 +203,43 @@ struct WriteArgs {
 };
 
 constexpr int kWriteThreads = 256;
+constexpr int kWriteTokens = 4;  // tokens of a block
 
-__global__ void __launch_bounds__(kWriteThreads) k_kv_write(WriteArgs a) {
+// A block copies four tokens of one layer, their slots and rows looked up together and four
+// 16-byte pieces a thread on their way.
+__global__ void __launch_bounds__(kWriteThreads) k_kv_write(const __grid_constant__ WriteArgs a) {
   const int64_t l = blockIdx.y;
   const int per_token = 2 * a.chunks;
-  for (int64_t t = blockIdx.x; t < a.n; t += gridDim.x) {
-    const int64_t slot = a.slot[t];
-    if (slot == -1) continue;
-    const int64_t row = a.src ? a.src[t] : t;
-    if (slot < 0 || slot >= a.n_slots || row < 0 || row >= a.n_rows) {
-      if (threadIdx.x == 0) atomicOr(a.status, 1);
-      continue;
+  for (int64_t t0 = (int64_t)blockIdx.x * kWriteTokens; t0 < a.n; t0 += (int64_t)gridDim.x * kWriteTokens) {
+    int64_t from[kWriteTokens], to[kWriteTokens];  // first the row and the slot, then the token's place in the cache
+#pragma unroll
+    for (int k = 0; k < kWriteTokens; ++k) {
+      const int64_t t = t0 + k;
+      to[k] = t < a.n ? a.slot[t] : -1;
+      from[k] = t >= a.n ? -1 : a.src ? a.src[t] : t;
     }
-    const int64_t block = slot / a.block_size;
-    const int64_t at = l * a.layer_stride + block * a.block_stride + (slot - block * a.block_size) * a.token_stride;
+#pragma unroll
+    for (int k = 0; k < kWriteTokens; ++k) {
+      if (to[k] == -1) continue;
+      if (to[k] < 0 || to[k] >= a.n_slots || from[k] < 0 || from[k] >= a.n_rows) {
+        if (threadIdx.x == 0) atomicOr(a.status, 1);
+        to[k] = -1;
+        continue;
+      }
+      const int64_t block = to[k] / a.block_size;
+      to[k] = l * a.layer_stride + block * a.block_stride + (to[k] - block * a.block_size) * a.token_stride;
+    }
     for (int e = threadIdx.x; e < per_token; e += kWriteThreads) {
       const int kv = e >= a.chunks, c = e - kv * a.chunks, h = c / a.head_chunks;
-      const uint4 x = *reinterpret_cast<const uint4*>(a.rows[kv] + l * a.rows_layer[kv] + row * a.rows_row[kv] + (int64_t)c * 8);
-      *reinterpret_cast<uint4*>(a.cache[kv] + at + h * a.head_stride + (int64_t)(c - h * a.head_chunks) * 8) = x;
+      const uint16_t* rows = a.rows[kv] + l * a.rows_layer[kv] + (int64_t)c * 8;
+      uint16_t* cache = a.cache[kv] + h * a.head_stride + (int64_t)(c - h * a.head_chunks) * 8;
+      uint4 x[kWriteTokens];
+#pragma unroll
+      for (int k = 0; k < kWriteTokens; ++k)
+        if (to[k] >= 0) x[k] = *reinterpret_cast<const uint4*>(rows + from[k] * a.rows_row[kv]);
+#pragma unroll
+      for (int k = 0; k < kWriteTokens; ++k)
+        if (to[k] >= 0) *reinterpret_cast<uint4*>(cache + to[k]) = x[k];
     }
   }
 }
@@ -346,7 +365,8 @@ int kv_write(const kv_cache* cache, int64_t layer, int64_t n_layers, const uint1
   a.block_size = cache->block_size;
   a.head_chunks = cache->head_dim / 8;
   a.chunks = cache->n_heads * a.head_chunks;
-  k_kv_write<<<dim3((unsigned)(n < 65536 ? n : 65536), (unsigned)n_layers), kWriteThreads, 0, (cudaStream_t)stream>>>(a);
+  const int64_t blocks = (n + kWriteTokens - 1) / kWriteTokens;
+  k_kv_write<<<dim3((unsigned)(blocks < 65536 ? blocks : 65536), (unsigned)n_layers), kWriteThreads, 0, (cudaStream_t)stream>>>(a);
   W12_LAUNCH_CHECK("kv_write kernel");
   return W12_OK;
 }

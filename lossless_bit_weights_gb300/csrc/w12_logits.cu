@@ -102,6 +102,18 @@ __global__ void __launch_bounds__(kRuleThreads, MINB) k_logit_rules(const __grid
   if (n == 0) return;
   const bool count = a.r.rep || a.r.freq || a.r.pres, bias = a.r.bias_off != nullptr;
   const bool tree = a.parent != nullptr;
+  const bool has_rep = a.r.rep != nullptr, has_freq = a.r.freq != nullptr, has_pres = a.r.pres != nullptr;
+  // everything of the request that does not wait for anything else
+  const float rep = has_rep ? a.r.rep[r] : 1.0f, freq = has_freq ? a.r.freq[r] : 0.0f, pres = has_pres ? a.r.pres[r] : 0.0f;
+  const int64_t h_given = count && a.r.hist ? a.r.hist_len[r] : 0;
+  const int64_t prompt = count && a.r.hist && a.r.prompt_len ? a.r.prompt_len[r] : 0;
+  const int64_t b_given = bias ? a.r.bias_off[r] : 0, b_end = bias ? a.r.bias_off[r + 1] : 0;
+  const int64_t len = min(max(h_given, (int64_t)0), a.r.hist_stride);
+  const int32_t* h = a.r.hist + r * a.r.hist_stride;
+  constexpr int H = 8;  // tokens of the history that a thread has on their way, the first ones from here on
+  int32_t told[H];
+#pragma unroll
+  for (int k = 0; k < H; ++k) told[k] = k * kRuleThreads + tid < len ? h[k * kRuleThreads + tid] : -1;
   // shared memory: the rows' best keys, bitmap, counts and bias places (chunk entries each), the
   // tree, the list of touched tokens
   unsigned long long* best = reinterpret_cast<unsigned long long*>(sm);
@@ -138,34 +150,26 @@ __global__ void __launch_bounds__(kRuleThreads, MINB) k_logit_rules(const __grid
       for (int i = tid; i < n; i += kRuleThreads) a.key[(off + i) * a.chunks + blockIdx.x] = 0;
     return;
   }
-  if (count && a.r.hist) {
-    const int64_t given = a.r.hist_len[r];
-    const int64_t len = min(max(given, (int64_t)0), a.r.hist_stride);
-    const int64_t prompt = a.r.prompt_len ? a.r.prompt_len[r] : 0;
-    if (tid == 0 && (len != given || prompt < 0 || prompt > given)) atomicOr(a.status, kRuleClamped);
-    const int32_t* h = a.r.hist + r * a.r.hist_stride;
-    for (int64_t j0 = 0; j0 < len; j0 += 8 * kRuleThreads) {  // eight loads on their way
-      int32_t t[8];
+  if (tid == 0 && (len != h_given || prompt < 0 || prompt > h_given)) atomicOr(a.status, kRuleClamped);
+  for (int64_t j0 = 0; j0 < len; j0 += H * kRuleThreads) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int64_t j = j0 + k * kRuleThreads + tid;
-        t[k] = j < len ? h[j] : -1;
+    for (int k = 0; k < H; ++k) {
+      const int64_t i = (int64_t)told[k] - v0;
+      if (told[k] >= 0 && i >= 0 && i < width) {
+        if (j0 + k * kRuleThreads + tid < prompt) atomicOr(&cnt[i], kPromptFlag);
+        else atomicAdd(&cnt[i], 1u);
+        atomicOr(&bits[i >> 5], 1u << (i & 31));
       }
+    }
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int64_t i = (int64_t)t[k] - v0;
-        if (t[k] >= 0 && i >= 0 && i < width) {
-          if (j0 + k * kRuleThreads + tid < prompt) atomicOr(&cnt[i], kPromptFlag);
-          else atomicAdd(&cnt[i], 1u);
-          atomicOr(&bits[i >> 5], 1u << (i & 31));
-        }
-      }
+    for (int k = 0; k < H; ++k) {
+      const int64_t j = j0 + (H + k) * kRuleThreads + tid;
+      told[k] = j < len ? h[j] : -1;
     }
   }
   if (bias) {
-    const int64_t g0 = a.r.bias_off[r], g1 = a.r.bias_off[r + 1];
-    const int64_t b0 = min(max(g0, (int64_t)0), a.r.n_bias), b1 = min(max(g1, b0), a.r.n_bias);
-    if (tid == 0 && (b0 != g0 || b1 != g1)) atomicOr(a.status, kRuleClamped);
+    const int64_t b0 = min(max(b_given, (int64_t)0), a.r.n_bias), b1 = min(max(b_end, b0), a.r.n_bias);
+    if (tid == 0 && (b0 != b_given || b1 != b_end)) atomicOr(a.status, kRuleClamped);
     for (int64_t j = b0 + tid; j < b1; j += kRuleThreads) {
       const int64_t i = (int64_t)a.r.bias_tok[j] - v0;
       if (i >= 0 && i < width) {
@@ -203,9 +207,6 @@ __global__ void __launch_bounds__(kRuleThreads, MINB) k_logit_rules(const __grid
   }
   for (uint32_t m = mine; m; m &= m - 1) list[before++] = (uint16_t)(tid * 32 + __ffs((int)m) - 1);
   __syncthreads();
-
-  const bool has_rep = a.r.rep != nullptr, has_freq = a.r.freq != nullptr, has_pres = a.r.pres != nullptr;
-  const float rep = has_rep ? a.r.rep[r] : 1.0f, freq = has_freq ? a.r.freq[r] : 0.0f, pres = has_pres ? a.r.pres[r] : 0.0f;
 
   // ---- a warp takes one part of one row's chunk
   const int part_len = a.chunk / a.parts;
@@ -276,25 +277,36 @@ __global__ void __launch_bounds__(kRuleThreads, MINB) k_logit_rules(const __grid
       }
     }
     if (WRITE) __syncwarp();  // a listed token is written again, by another lane
-    for (int j = lane; j < listed; j += 32) {
-      const int i = list[j];
-      if (i < c0 || i >= c1 || (mask && !(mask[i >> 5] >> (i & 31) & 1u))) continue;
-      uint32_t c = count ? cnt[i] : 0u;
-      if (tree && count)
-        for (int32_t p = up[node]; p >= 0;) {
-          if (draft[p] == (int32_t)(v0 + i)) ++c;
-          p = parent[p] >= 0 ? up[parent[p]] : -1;
-        }
-      const uint32_t times = c & ~kPromptFlag;
-      float f = x[i];
-      if (c && has_rep) f = f > 0.0f ? __fdiv_rn(f, rep) : __fmul_rn(f, rep);
-      if (times) {
-        if (has_freq) f = __fsub_rn(f, __fmul_rn(freq, (float)times));
-        if (has_pres) f = __fsub_rn(f, pres);
+    for (int j0 = lane; j0 < listed; j0 += 128) {  // four listed tokens a lane on their way
+      float f4[4];
+      int i4[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        i4[k] = j0 + 32 * k < listed ? list[j0 + 32 * k] : -1;
+        if (i4[k] < c0 || i4[k] >= c1 || (mask && !(mask[i4[k] >> 5] >> (i4[k] & 31) & 1u))) i4[k] = -1;
+        f4[k] = i4[k] >= 0 ? x[i4[k]] : 0.0f;
       }
-      if (bias && bias_at[i] > 0) f = __fadd_rn(f, a.r.bias_val[bias_at[i] - 1]);
-      if (WRITE) y[i] = f;
-      else top.take(f, i);
+#pragma unroll 1
+      for (int k = 0; k < 4; ++k) {
+        const int i = k == 0 ? i4[0] : k == 1 ? i4[1] : k == 2 ? i4[2] : i4[3];
+        if (i < 0) continue;
+        float f = k == 0 ? f4[0] : k == 1 ? f4[1] : k == 2 ? f4[2] : f4[3];
+        uint32_t c = count ? cnt[i] : 0u;
+        if (tree && count)
+          for (int32_t p = up[node]; p >= 0;) {
+            if (draft[p] == (int32_t)(v0 + i)) ++c;
+            p = parent[p] >= 0 ? up[parent[p]] : -1;
+          }
+        const uint32_t times = c & ~kPromptFlag;
+        if (c && has_rep) f = f > 0.0f ? __fdiv_rn(f, rep) : __fmul_rn(f, rep);
+        if (times) {
+          if (has_freq) f = __fsub_rn(f, __fmul_rn(freq, (float)times));
+          if (has_pres) f = __fsub_rn(f, pres);
+        }
+        if (bias && bias_at[i] > 0) f = __fadd_rn(f, a.r.bias_val[bias_at[i] - 1]);
+        if (WRITE) y[i] = f;
+        else top.take(f, i);
+      }
     }
     if (!WRITE) {
       unsigned long long k = top.at < 0 ? 0ull : arg_key(top.value, v0 + top.at);
