@@ -33,6 +33,7 @@
 #include <mutex>
 
 #include "w12_internal.cuh"
+#include "w12_pdl.cuh"
 
 namespace w12 {
 
@@ -148,7 +149,11 @@ __device__ __forceinline__ Req load_request(const AttnArgs& a, int r) {
   return q;
 }
 
-__device__ __forceinline__ int64_t share(int64_t total, int ctas, int c) { return total * c / ctas; }
+// Quotient of two non-negative numbers, in 32 bits where they allow it.
+__device__ __forceinline__ int64_t quotient(int64_t n, int64_t d) {
+  return ((n | d) >> 32) == 0 ? (int64_t)((uint32_t)n / (uint32_t)d) : n / d;
+}
+__device__ __forceinline__ int64_t share(int64_t total, int ctas, int c) { return quotient(total * c, ctas); }
 
 struct Start {
   int64_t total, at;  // all tiles; the place of the wanted tile within its request
@@ -249,15 +254,15 @@ struct Walk {
         while ((q = load_request<D>(a, r)).tiles == 0) ++r;  // left > 0: a request with tiles follows
         fresh = false;
       }
-      const int64_t u = at / q.tiles;
+      const int64_t u = quotient(at, q.tiles), row_unit = quotient(u, a.n_heads);
       const int32_t ta = (int32_t)(at - u * q.tiles), take = (int32_t)min(left, (int64_t)(q.tiles - ta));
       p.q = q;
       p.r = r;
       p.ta = max(ta - kUnitCost, 0);
       p.tb = max(ta + take - kUnitCost, 0);
       p.begin = at - ta + kUnitCost;
-      p.h = (int32_t)(u % a.n_heads);
-      p.row0 = (int32_t)(u / a.n_heads) * AttnPlan<D>::kRows;
+      p.h = (int32_t)(u - row_unit * a.n_heads);
+      p.row0 = (int32_t)row_unit * AttnPlan<D>::kRows;
       p.rows = min(AttnPlan<D>::kRows, q.n * a.group - p.row0);
       at += take;
       left -= take;
@@ -922,8 +927,6 @@ __global__ void __launch_bounds__(AttnPlan<D>::kThreads, 1) k_tree_attn(const __
   using P = AttnPlan<D>;
   extern __shared__ __align__(1024) uint8_t attn_sm[];
   const int tid = threadIdx.x, warp = tid >> 5, c = blockIdx.x;
-  // the kernel that adds the parts may be set up meanwhile; it waits for this one's end
-  if (tid == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   Shared s;
   s.sm = attn_sm;
   s.base = smem_u32(attn_sm);
@@ -967,6 +970,7 @@ __global__ void __launch_bounds__(AttnPlan<D>::kThreads, 1) k_tree_attn(const __
     mbar_init_fence();
     misc[1] = 0;  // abort
   }
+  pdl_enter();  // (the joining kernel may be set up from here on; it waits for this one's end)
   const Start start = find_start<D>(a, c, reinterpret_cast<int64_t*>(attn_sm + P::kRing));
   if (c >= start.ctas) {
     if (tid == 0) a.units[c].rows = 0;
@@ -988,8 +992,8 @@ __global__ void __launch_bounds__(AttnPlan<D>::kThreads, 1) k_tree_attn(const __
     if (w.next(a, p) && p.ta > 0) {
       // shares first .. last begin behind the unit's first tile: begin < total * i / ctas < end
       const int64_t begin = share(start.total, start.ctas, c) - start.at + p.begin, end = begin + p.q.tiles - kUnitCost;
-      u = JoinUnit{p.q.off, p.h, p.row0, p.rows, (int32_t)(((begin + 1) * start.ctas + start.total - 1) / start.total),
-                   (int32_t)((end * start.ctas + start.total - 1) / start.total) - 1, 0};
+      u = JoinUnit{p.q.off, p.h, p.row0, p.rows, (int32_t)quotient((begin + 1) * start.ctas + start.total - 1, start.total),
+                   (int32_t)quotient(end * start.ctas + start.total - 1, start.total) - 1, 0};
     }
     a.units[c] = u;
   }
@@ -1028,7 +1032,7 @@ constexpr int kJoinThreads = 256;
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) k_tree_attn_join(AttnArgs a) {
   const int c = blockIdx.x + 1;
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are the previous kernel's
+  pdl_enter();  // the parts are the previous kernel's
   const JoinUnit u = a.units[c];
   if (u.rows <= 0) return;  // nothing to join here; the other fields say nothing then
   const int n = u.last - u.first + 1;
@@ -1137,18 +1141,10 @@ int launch_attn(AttnArgs a, const kv_cache* c, cudaStream_t s) {
   CUtensorMap k_map{}, v_map{};
   a.box_rows = box_rows(c, P::kBK);
   if (a.box_rows && !(make_cache_map(&k_map, a.kc, c, a.box_rows) && make_cache_map(&v_map, a.vc, c, a.box_rows))) a.box_rows = 0;
-  k_tree_attn<D><<<kAttnCtas, P::kThreads, P::kBytes, s>>>(a, k_map, v_map);
+  W12_CUDA_TRY(launch_dependent(k_tree_attn<D>, dim3(kAttnCtas), P::kThreads, P::kBytes, s, a, k_map, v_map));
   W12_LAUNCH_CHECK("tree_attn kernel");
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kAttnCtas - 1, a.row_cap * (D / 4) <= 4 * kJoinThreads ? 1 : 4);
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = s;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  W12_CUDA_TRY(cudaLaunchKernelEx(&cfg, k_tree_attn_join<D>, a));
+  W12_CUDA_TRY(launch_dependent(k_tree_attn_join<D>, dim3(kAttnCtas - 1, a.row_cap * (D / 4) <= 4 * kJoinThreads ? 1 : 4),
+                                kJoinThreads, 0, s, a));
   W12_LAUNCH_CHECK("tree_attn: joining kernel");
   return W12_OK;
 }

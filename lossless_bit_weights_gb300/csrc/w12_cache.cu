@@ -3,6 +3,7 @@
 #include <cstdint>
 
 #include "w12_internal.cuh"
+#include "w12_pdl.cuh"
 
 namespace w12 {
 namespace {
@@ -69,6 +70,7 @@ __device__ __forceinline__ int owner(const int32_t* pre, int n, int32_t t) {
 // one launch does it all and nothing waits on another block: what a block reads (old table
 // entries, the pool's front) no block writes (new entries, the pool behind its back).
 __global__ void __launch_bounds__(kSlotThreads) k_kv_slots(const __grid_constant__ SlotArgs a) {
+  pdl_enter();
   extern __shared__ int32_t sm[];
   int32_t* pre_tok = sm;                       // n_req + 1 each
   int32_t* pre_new = pre_tok + a.n_req + 1;
@@ -208,6 +210,7 @@ constexpr int kWriteTokens = 4;  // tokens of a block
 // A block copies four tokens of one layer, their slots and rows looked up together and four
 // 16-byte pieces a thread on their way.
 __global__ void __launch_bounds__(kWriteThreads) k_kv_write(const __grid_constant__ WriteArgs a) {
+  pdl_enter();
   const int64_t l = blockIdx.y;
   const int per_token = 2 * a.chunks;
   for (int64_t t0 = (int64_t)blockIdx.x * kWriteTokens; t0 < a.n; t0 += (int64_t)gridDim.x * kWriteTokens) {
@@ -323,7 +326,7 @@ int kv_slots(const int32_t* cache_len, const int32_t* add, int32_t extra, int32_
     }
   }
   const int64_t blocks = (capacity + kSlotThreads - 1) / kSlotThreads;
-  k_kv_slots<<<(unsigned)(blocks < 608 ? blocks : 608), kSlotThreads, smem, (cudaStream_t)stream>>>(a);
+  W12_CUDA_TRY(launch_dependent(k_kv_slots, dim3((unsigned)(blocks < 608 ? blocks : 608)), kSlotThreads, smem, (cudaStream_t)stream, a));
   W12_LAUNCH_CHECK("kv_slots kernel");
   return W12_OK;
 }
@@ -366,7 +369,8 @@ int kv_write(const kv_cache* cache, int64_t layer, int64_t n_layers, const uint1
   a.head_chunks = cache->head_dim / 8;
   a.chunks = cache->n_heads * a.head_chunks;
   const int64_t blocks = (n + kWriteTokens - 1) / kWriteTokens;
-  k_kv_write<<<dim3((unsigned)(blocks < 65536 ? blocks : 65536), (unsigned)n_layers), kWriteThreads, 0, (cudaStream_t)stream>>>(a);
+  W12_CUDA_TRY(launch_dependent(k_kv_write, dim3((unsigned)(blocks < 65536 ? blocks : 65536), (unsigned)n_layers), kWriteThreads, 0,
+                                (cudaStream_t)stream, a));
   W12_LAUNCH_CHECK("kv_write kernel");
   return W12_OK;
 }

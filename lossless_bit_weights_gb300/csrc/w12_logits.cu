@@ -14,6 +14,7 @@
 #include <cstdint>
 
 #include "w12_internal.cuh"
+#include "w12_pdl.cuh"
 
 #ifndef MINB
 #define MINB 4
@@ -88,6 +89,7 @@ __device__ __forceinline__ float4 load4(const float* x, int i, int n, bool vec) 
 
 template <bool WRITE>
 __global__ void __launch_bounds__(kRuleThreads, MINB) k_logit_rules(const __grid_constant__ RuleArgs a) {
+  pdl_enter();
   extern __shared__ uint32_t sm[];
   __shared__ int s_listed[kRuleWarps];
   const int r = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -332,7 +334,7 @@ __global__ void __launch_bounds__(kRuleThreads) k_rule_accept(const unsigned lon
                                                               int32_t* __restrict__ path_nodes, int32_t* bonus) {
   __shared__ int32_t tok[kRuleMaxNodes], parent[kRuleMaxNodes], draft[kRuleMaxNodes];
   __shared__ unsigned long long s_best;
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the keys are the previous kernel's
+  pdl_enter();  // the keys are the previous kernel's
   const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int64_t off;
   int n;
@@ -464,8 +466,7 @@ int launch_rules(const float* logits, int64_t stride, int64_t M, int64_t V, cons
   }
   a.vec = ((stride | (out ? out_stride : 0)) & 3) == 0 && (((uintptr_t)logits | (uintptr_t)out) & 15u) == 0;
   const dim3 grid((unsigned)p.chunks, (unsigned)n_req);
-  if (key) k_logit_rules<false><<<grid, kRuleThreads, smem, s>>>(a);
-  else k_logit_rules<true><<<grid, kRuleThreads, smem, s>>>(a);
+  W12_CUDA_TRY(launch_dependent(key ? k_logit_rules<false> : k_logit_rules<true>, grid, kRuleThreads, smem, s, a));
   W12_LAUNCH_CHECK(what);
   return W12_OK;
 }
@@ -509,17 +510,8 @@ int logits_verify(const float* logits, int64_t stride, int64_t M, int64_t V, con
   st = launch_rules(logits, stride, M, V, rules, parent, draft, req_offsets, n_req, nullptr, 0, status, key,
                     (cudaStream_t)stream, "logits_verify: rules kernel");
   if (st) return st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)n_req);
-  cfg.blockDim = dim3(kRuleThreads);
-  cfg.stream = (cudaStream_t)stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  W12_CUDA_TRY(cudaLaunchKernelEx(&cfg, k_rule_accept, (const unsigned long long*)key, rule_plan(M, V, n_req).chunks, parent,
-                                  draft, req_offsets, M, tok, path_len, path_nodes, bonus));
+  W12_CUDA_TRY(launch_dependent(k_rule_accept, dim3((unsigned)n_req), kRuleThreads, 0, (cudaStream_t)stream, key,
+                                rule_plan(M, V, n_req).chunks, parent, draft, req_offsets, M, tok, path_len, path_nodes, bonus));
   W12_LAUNCH_CHECK("logits_verify: acceptance kernel");
   return W12_OK;
 }
