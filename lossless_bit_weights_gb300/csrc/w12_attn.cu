@@ -45,9 +45,9 @@ constexpr int kAttnMaxNodes = 256;
 constexpr int32_t kAttnBadRequest = 1, kAttnBadBlock = 2, kAttnTimeout = 4;
 constexpr int kAttnCtas = 152;  // one per SM of a GB300; fewer SMs only run them in turn
 // What a unit costs beside its tiles (its last product, its outputs, the next one's first scores), in
-// tiles; the shares count it in front of the unit.  24 requests of 33 to 12001 tokens took 161 us
-// at 0, 146 at 1, 133 at 2 and 128 at 4.
-constexpr int kUnitCost = 3;
+// tiles; the shares count it in front of the unit.  24 requests of 33 to 12001 tokens took 143 us
+// at 0, 130 at 1, 118 at 2 and 118 at 3.
+constexpr int kUnitCost = 2;
 constexpr int kMetaRing = 2;     // units whose tree shared memory holds
 // P enters its product in two bf16 pieces, the upper one cut off, the lower one rounded: 2^-16
 // of P is lost instead of 2^-8.  The lower piece is taken of P (1 + 2^-20), so that it is above
@@ -468,15 +468,15 @@ __device__ bool produce(const AttnArgs& a, const CUtensorMap* k_map, const CUten
     const int64_t head_off = (int64_t)p.h * a.head_stride;
     // Lane L finds the row that the warp copies in round L / RPW as its (L % RPW)-th: its block (a
     // load that is on its way while the entries before are copied), then its place in the cache,
-    // for K and V alike.
-    // Where a tile can go by boxes of the tensor maps, lane L sends for the 4 L + warp-th.
+    // for K and V alike.  Where a tile can go by boxes of the tensor maps, lane L sends for the 4 L + warp-th.
     const int my_row = (lane / RPW) * 4 * RPW + pw * RPW + lane % RPW;
     const int boxes = a.box_rows ? P::kBK / a.box_rows : 1, my_box = (lane * 4 + pw) % boxes, my_slab = (lane * 4 + pw) / boxes;
     auto find_block = [&](int tile, int row) -> int32_t {
       const int32_t j = tile * P::kBK + row;
       return row < P::kBK && j < p.q.len ? table[a.by_block(j)] : 0;
     };
-    const int ahead_row = a.box_rows ? my_box * a.box_rows : my_row;
+    auto is_tail = [&](int tile) { return (int64_t)(tile + 1) * P::kBK > p.q.len; };  // it holds drafted nodes
+    auto asked_row = [&](int tile) { return a.box_rows && !is_tail(tile) ? my_box * a.box_rows : my_row; };
     auto find_place = [&](int tile, int32_t id) -> int64_t {  // -1: not in the cache
       const int32_t j = tile * P::kBK + my_row;
       if (my_row >= P::kBK) return 0;
@@ -489,11 +489,11 @@ __device__ bool produce(const AttnArgs& a, const CUtensorMap* k_map, const CUten
     };
     int64_t place0 = 0, place1 = 0;  // of the tiles whose K is under way and whose V is not, oldest first
     bool waiting = false;
-    int32_t id = find_block(p.ta, ahead_row);
+    int32_t id = find_block(p.ta, asked_row(p.ta));
     for (int item = 0; item < 2 * cnt; ++item, ++entry) {
       bool is_v;
       const int i = ring_tile(item, cnt, two, is_v), tile = p.ta + i;
-      const bool tail = (int64_t)(tile + 1) * P::kBK > p.q.len, by_box = a.box_rows && !tail;
+      const bool tail = is_tail(tile), by_box = a.box_rows && !tail;
       int64_t at;
       if (is_v) {
         at = place0;
@@ -505,9 +505,10 @@ __device__ bool produce(const AttnArgs& a, const CUtensorMap* k_map, const CUten
           bad_block = bad_block || !in;
           at = in ? id : 0;  // some block: the unit's outputs are dropped
         } else {
-          at = find_place(tile, a.box_rows ? find_block(tile, my_row) : id);
+          at = find_place(tile, id);
         }
-        id = find_block(p.ta + min(i + 1, cnt - 1), ahead_row);
+        const int next = p.ta + min(i + 1, cnt - 1);
+        id = find_block(next, asked_row(next));
         if (waiting) place1 = at;
         else place0 = at;
         waiting = true;
@@ -515,7 +516,6 @@ __device__ bool produce(const AttnArgs& a, const CUtensorMap* k_map, const CUten
       const uint32_t slot = entry % P::kSlots, round = entry / P::kSlots;
       if (round > 0 && !wait_warp(s.empty + 8 * slot, (round - 1) & 1, s)) return false;
       const uint32_t dst = s.base + P::kRing + slot * P::kSlotBytes;
-      const uint16_t* cached = (is_v ? a.vc : a.kc) + chunk * 8;
       if (by_box) {
         const uint32_t bar = s.full + 8 * slot;
         if (my_slab < D / 64) {
@@ -526,37 +526,29 @@ __device__ bool produce(const AttnArgs& a, const CUtensorMap* k_map, const CUten
         } else {
           mbar_arrive(bar);
         }
-      } else if (!tail && __all_sync(0xFFFFFFFFu, at >= 0)) {
+      } else {
+        const uint16_t* mine = nullptr;  // the lane's row; none: zeros
+        const int32_t node = tile * P::kBK + my_row - p.q.len;
+        if (at >= 0) mine = (is_v ? a.vc : a.kc) + at;
+        else if (node >= 0 && node < p.q.n)
+          mine = (is_v ? a.v + (p.q.off + node) * a.v_stride : a.k + (p.q.off + node) * a.k_stride) + (int64_t)p.h * D;
 #pragma unroll
         for (int i0 = 0; i0 < IT; i0 += 8) {
-          int64_t o[8];
+          unsigned long long o[8];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) o[k] = __shfl_sync(0xFFFFFFFFu, at, (i0 + k) * RPW + sub);
+          for (int k = 0; k < 8; ++k) o[k] = __shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(mine), (i0 + k) * RPW + sub);
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             const int row = (i0 + k) * 4 * RPW + pw * RPW + sub;
-            cp16(dst + (chunk >> 3) * (P::kBK * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4), cached + o[k]);
+            cp16(dst + (chunk >> 3) * (P::kBK * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4),
+                 o[k] ? reinterpret_cast<const uint16_t*>(o[k]) + chunk * 8 : a.kc, o[k] != 0);
           }
-        }
-      } else {
-#pragma unroll 1
-        for (int it = 0; it < IT; ++it) {
-          const int row = it * 4 * RPW + pw * RPW + sub;
-          const int64_t o = __shfl_sync(0xFFFFFFFFu, at, it * RPW + sub);
-          const int32_t node = tile * P::kBK + row - p.q.len;
-          const uint16_t* src = cached + o;
-          bool in = o >= 0;
-          if (node >= 0 && node < p.q.n) {
-            src = (is_v ? a.v + (p.q.off + node) * a.v_stride : a.k + (p.q.off + node) * a.k_stride) + (int64_t)p.h * D + chunk * 8;
-            in = true;
-          }
-          cp16(dst + (chunk >> 3) * (P::kBK * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4), in ? src : a.kc, in);
         }
       }
       if (item == 0) {
-        // ---- the unit's query rows (past them shared memory stays as it is) and its tree, behind the first keys.  The
-        // last unit's scores are there and the one before it is at its end: the rows of the one
-        // and the tree of the other may go.
+        // ---- the unit's query rows (past them shared memory stays as it is) and its tree, behind
+        // the first keys.  The last unit's scores are there and the one before it is at its end:
+        // the rows of the one and the tree of the other may go.
         if (unit > 0 && !wait_warp(s.q_free, (unit - 1) & 1, s)) return false;
         for (int row0 = 0; row0 < p.rows; row0 += P::kBK) {
           const int r = p.row0 + row0 + my_row, node = a.by_group(r);
@@ -587,13 +579,14 @@ __device__ bool produce(const AttnArgs& a, const CUtensorMap* k_map, const CUten
         cp_arrive(s.q_full);
       }
       if (item == 2 * cnt - 1 && bad_block) atomicOr(bad, kAttnBadBlock);
-      if (by_box) {
+      if (by_box) {  // (its arrivals went with the boxes)
       } else if (tail && is_v) {
         // A tile with drafted nodes: an infinity or a NaN in a node's V would reach every row
         // (0 * inf), also those that do not attend to it.  It is taken out here, the node
         // marked, and the rows that do attend to it get it back at the end.
         cp_wait_all();
-        for (int it = 0; it < IT; ++it) {
+        const int32_t from = p.q.len - tile * P::kBK;  // the first node's row
+        for (int it = max(from, 0) / (4 * RPW); it < IT && it * 4 * RPW < from + p.q.n; ++it) {
           const int row = it * 4 * RPW + pw * RPW + sub;
           const int32_t node = tile * P::kBK + row - p.q.len;
           if (node < 0 || node >= p.q.n) continue;
@@ -1027,33 +1020,35 @@ __global__ void __launch_bounds__(AttnPlan<D>::kThreads, 1) k_tree_attn(const __
 
 // Adds the parts of the units that several CTAs worked on.  Block (c, y) takes, of the unit inside
 // which CTA c + 1's share begins, every (n * gridDim.y)-th run of outputs, n such shares there being.
+// Four threads share an output (four adjacent columns of a row): each adds every fourth part, eight
+// of them loaded together, and the four sums meet in a fixed order.
 constexpr int kJoinThreads = 256;
+constexpr int kJoinOutputs = kJoinThreads / 4;
 
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) k_tree_attn_join(AttnArgs a) {
-  const int c = blockIdx.x + 1;
+__global__ void __launch_bounds__(kJoinThreads) k_tree_attn_join(const __grid_constant__ AttnArgs a) {
+  const int c = blockIdx.x + 1, lane = threadIdx.x & 31, sub = lane >> 3;
   pdl_enter();  // the parts are the previous kernel's
   const JoinUnit u = a.units[c];
   if (u.rows <= 0) return;  // nothing to join here; the other fields say nothing then
-  const int n = u.last - u.first + 1;
-  for (int e = ((c - u.first) * gridDim.y + blockIdx.y) * kJoinThreads + threadIdx.x; e < u.rows * (D / 4);
-       e += n * gridDim.y * kJoinThreads) {
-    const int c4 = e / u.rows, row = e - c4 * u.rows;
-    // the parts are CTA first - 1's second slot and the first slots of first .. last; eight at a
-    // time, their statistics and values loaded together
+  const int n = u.last - u.first + 1, outputs = u.rows * (D / 4);
+  const int mine = (threadIdx.x >> 5) * 8 + (lane & 7);  // of the block's outputs
+  for (int e0 = ((c - u.first) * gridDim.y + blockIdx.y) * kJoinOutputs; e0 < outputs; e0 += n * gridDim.y * kJoinOutputs) {
+    const int e = min(e0 + mine, outputs - 1), c4 = e / u.rows, row = e - c4 * u.rows;
+    // the parts are CTA first - 1's second slot and the first slots of first .. last
     float top = -INFINITY, sum = 0.0f;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     int32_t bad = 0;
-    for (int i0 = u.first - 1; i0 <= u.last; i0 += 8) {
+    for (int i0 = u.first - 1 + sub; i0 <= u.last; i0 += 32) {
       float2 t[8];
       float4 x[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const int64_t slot = 2 * (int64_t)(i0 + k) + (i0 + k < u.first ? 1 : 0);
-        const bool in = i0 + k <= u.last;
+        const int i = i0 + 4 * k;
+        const int64_t slot = 2 * (int64_t)i + (i < u.first ? 1 : 0);
         t[k] = make_float2(-INFINITY, 0.0f);
         x[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (in) {
+        if (i <= u.last) {
           t[k] = *reinterpret_cast<const float2*>(a.part_ml + 2 * (slot * a.row_cap + row));
           x[k] = *reinterpret_cast<const float4*>(a.part_o + slot * D * a.row_cap + ((int64_t)c4 * a.row_cap + row) * 4);
           bad |= a.part_bad[slot];
@@ -1076,14 +1071,26 @@ __global__ void __launch_bounds__(kJoinThreads) k_tree_attn_join(AttnArgs a) {
       }
       top = next;
     }
+    float all = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
+    all = fmaxf(all, __shfl_xor_sync(0xFFFFFFFFu, all, 16));
+    const float fix = ex2(top - (all == -INFINITY ? 0.0f : all));
+    float v[5] = {sum * fix, o.x * fix, o.y * fix, o.z * fix, o.w * fix};
+#pragma unroll
+    for (int k = 0; k < 5; ++k) {
+      v[k] += __shfl_xor_sync(0xFFFFFFFFu, v[k], 8);
+      v[k] += __shfl_xor_sync(0xFFFFFFFFu, v[k], 16);
+    }
+    bad |= __shfl_xor_sync(0xFFFFFFFFu, bad, 8);
+    bad |= __shfl_xor_sync(0xFFFFFFFFu, bad, 16);
+    if (sub || e0 + mine >= outputs) continue;
     if (bad) {  // the same for every output of the unit
       if (e == 0) atomicOr(a.status, bad);
-      return;
+      continue;
     }
-    const float inv = 1.0f / sum;
+    const float inv = 1.0f / v[0];
     const int g = u.row0 + row, node = a.by_group(g);
     uint16_t* out = a.out + ((u.off + node) * a.n_q_heads + u.h * a.group + (g - node * a.group)) * (int64_t)D + c4 * 4;
-    *reinterpret_cast<uint2*>(out) = make_uint2(pack2(o.x * inv, o.y * inv), pack2(o.z * inv, o.w * inv));
+    *reinterpret_cast<uint2*>(out) = make_uint2(pack2(v[1] * inv, v[2] * inv), pack2(v[3] * inv, v[4] * inv));
   }
 }
 
@@ -1143,7 +1150,7 @@ int launch_attn(AttnArgs a, const kv_cache* c, cudaStream_t s) {
   if (a.box_rows && !(make_cache_map(&k_map, a.kc, c, a.box_rows) && make_cache_map(&v_map, a.vc, c, a.box_rows))) a.box_rows = 0;
   W12_CUDA_TRY(launch_dependent(k_tree_attn<D>, dim3(kAttnCtas), P::kThreads, P::kBytes, s, a, k_map, v_map));
   W12_LAUNCH_CHECK("tree_attn kernel");
-  W12_CUDA_TRY(launch_dependent(k_tree_attn_join<D>, dim3(kAttnCtas - 1, a.row_cap * (D / 4) <= 4 * kJoinThreads ? 1 : 4),
+  W12_CUDA_TRY(launch_dependent(k_tree_attn_join<D>, dim3(kAttnCtas - 1, a.row_cap * (D / 4) <= 16 * kJoinOutputs ? 2 : 8),
                                 kJoinThreads, 0, s, a));
   W12_LAUNCH_CHECK("tree_attn: joining kernel");
   return W12_OK;

@@ -16,15 +16,6 @@
 #include "w12_internal.cuh"
 #include "w12_pdl.cuh"
 
-#ifndef MINB
-#define MINB 4
-#endif
-#ifndef CHMAX
-#define CHMAX 4096
-#endif
-#ifndef CHMIN
-#define CHMIN 1024
-#endif
 namespace w12 {
 namespace {
 
@@ -88,7 +79,7 @@ __device__ __forceinline__ float4 load4(const float* x, int i, int n, bool vec) 
 }
 
 template <bool WRITE>
-__global__ void __launch_bounds__(kRuleThreads, MINB) k_logit_rules(const __grid_constant__ RuleArgs a) {
+__global__ void __launch_bounds__(kRuleThreads, 4) k_logit_rules(const __grid_constant__ RuleArgs a) {
   pdl_enter();
   extern __shared__ uint32_t sm[];
   __shared__ int s_listed[kRuleWarps];
@@ -402,7 +393,7 @@ struct RulePlan {
 // there are.  The largest of 4096, 2048, 1024 with at least two blocks per SM.
 RulePlan rule_plan(int64_t M, int64_t V, int32_t n_req) {
   RulePlan p{};
-  for (p.chunk = CHMAX; p.chunk > CHMIN; p.chunk /= 2)
+  for (p.chunk = 4096; p.chunk > 1024; p.chunk /= 2)
     if ((V + p.chunk - 1) / p.chunk * n_req >= 304) break;
   p.chunks = (int)((V + p.chunk - 1) / p.chunk);
   const int64_t rows = (M + n_req - 1) / n_req;

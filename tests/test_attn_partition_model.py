@@ -7,7 +7,7 @@ import random
 import pytest
 
 CTAS = 152
-COST = 3   # tiles that a unit counts for beside its own, in front of them
+COST = 2   # tiles that a unit counts for beside its own, in front of them
 
 
 def share(total, ctas, c):
@@ -67,7 +67,7 @@ def test_parts_and_joins(seed):
             last = ((begin + units[u][0]) * ctas + total - 1) // total - 1
             desc[c] = (units[u][1], u, first, last)
     assert all(x == 1 for t in taken for x in t)
-    joined, threads, gy = {}, 256, rng.choice([1, 4])
+    joined, threads, gy = {}, 64, rng.choice([2, 8])            # outputs of a block at a time
     for c in range(1, CTAS):
         rows, u, first, last = desc[c]
         if rows <= 0:
