@@ -686,20 +686,18 @@ def kv_slots(cache_len, add, table, pool, pool_pos, block_size: int, capacity: i
         raise ValueError(f"cache_len and add must have an entry for each of the table's {n_req} rows")
     if path_nodes is not None:
         _check_offsets(req_offsets, n_req)
-    # one allocation for the int64 results and one for the int32 ones
-    wide = _empty(capacity + 3, torch.int64, dev, stream)
-    slim = _empty(capacity + n_req, torch.int32, dev, stream)
+    slot, src = _empty(capacity, torch.int64, dev, stream), _empty(capacity, torch.int32, dev, stream)
+    new_len = _empty(n_req, torch.int32, dev, stream)
+    new_pos, total = _empty(2, torch.int64, dev, stream), _empty(1, torch.int64, dev, stream)
     status = _zero_status(status, dev, stream)
-    w, i = wide.data_ptr(), slim.data_ptr()
     _check((_lib or lib()).kv_slots(
         cache_len.data_ptr(), add.data_ptr(), extra, n_req, table.data_ptr(), _row_stride(table), table.shape[1],
         _i32(pool).data_ptr(), pool.numel(), pool_pos.data_ptr(), block_size,
         None if path_nodes is None else _i32(path_nodes).data_ptr(),
         None if req_offsets is None else _i32(req_offsets).data_ptr(), 0 if path_nodes is None else path_nodes.numel(),
-        capacity, w + 24, i + 4 * n_req, i, w, w + 16, status.data_ptr(), _raw_stream(stream, table)))
-    pool_pos, total, slot = wide.split_with_sizes((2, 1, capacity))
-    new_len, src = slim.split_with_sizes((n_req, capacity))
-    return Slots(slot, src, new_len, pool_pos, total, status)
+        capacity, slot.data_ptr(), src.data_ptr(), new_len.data_ptr(), new_pos.data_ptr(), total.data_ptr(),
+        status.data_ptr(), _raw_stream(stream, table)))
+    return Slots(slot, src, new_len, new_pos, total, status)
 
 
 def _row_stride(t: torch.Tensor) -> int:
@@ -850,13 +848,13 @@ def logits_verify(logits, rules: LogitRules, parent, draft, req_offsets=None, ws
     """Argmax under the rules and greedy acceptance, without writing the processed logits:
     returns (tok, path_len, path_nodes, bonus, status)."""
     M, V, n_req, stride = _rule_args(logits, rules, parent, draft, req_offsets)
-    both = _empty(2 * M + 2 * n_req, torch.int32, logits.device, stream)
-    status = _zero_status(status, logits.device, stream)
+    dev = logits.device
+    tok, path_nodes = _empty(M, torch.int32, dev, stream), _empty(M, torch.int32, dev, stream)
+    path_len, bonus = _empty(n_req, torch.int32, dev, stream), _empty(n_req, torch.int32, dev, stream)
+    status = _zero_status(status, dev, stream)
     raw = _raw_stream(stream, logits)
-    buf = (ws or Workspace(logits.device)).scratch(_verify_bytes(M, V, n_req), stream, raw)
-    at = both.data_ptr()
+    buf = (ws or Workspace(dev)).scratch(_verify_bytes(M, V, n_req), stream, raw)
     _check((_lib or lib()).logits_verify(
-        logits.data_ptr(), stride, M, V, rules.desc(), _ptr(parent), _ptr(draft), _ptr(req_offsets), n_req, at, at + 8 * M,
-        at + 4 * M, at + 8 * M + 4 * n_req, status.data_ptr(), buf.data_ptr(), buf.numel(), raw))
-    tok, path_nodes, path_len, bonus = both.split_with_sizes((M, M, n_req, n_req))
+        logits.data_ptr(), stride, M, V, rules.desc(), _ptr(parent), _ptr(draft), _ptr(req_offsets), n_req, tok.data_ptr(),
+        path_len.data_ptr(), path_nodes.data_ptr(), bonus.data_ptr(), status.data_ptr(), buf.data_ptr(), buf.numel(), raw))
     return tok, path_len, path_nodes, bonus, status
