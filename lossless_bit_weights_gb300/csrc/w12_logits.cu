@@ -37,6 +37,7 @@ struct RuleArgs {
   unsigned long long* key;  // [M][chunks] argmax keys, or null
   int32_t chunk, chunks, parts;
   bool vec;                 // rows allow 16-byte accesses
+  bool hist_vec;            // so do the histories
 };
 
 // Nodes of request r, or false: its offsets are out of range or it has too many.
@@ -103,10 +104,27 @@ __global__ void __launch_bounds__(kRuleThreads, 4) k_logit_rules(const __grid_co
   const int64_t b_given = bias ? a.r.bias_off[r] : 0, b_end = bias ? a.r.bias_off[r + 1] : 0;
   const int64_t len = min(max(h_given, (int64_t)0), a.r.hist_stride);
   const int32_t* h = a.r.hist + r * a.r.hist_stride;
-  constexpr int H = 8;  // tokens of the history that a thread has on their way, the first ones from here on
+  // tokens of the history that a thread has on their way (four adjacent ones at a time where the rows
+  // allow it), the first ones from here on
+  constexpr int H = 8;
   int32_t told[H];
+  auto place = [&](int64_t j0, int k) {  // of told[k]
+    return a.hist_vec ? j0 + ((k >> 2) * kRuleThreads + tid) * 4 + (k & 3) : j0 + k * kRuleThreads + tid;
+  };
+  auto ask = [&](int64_t j0) {
+    if (a.hist_vec) {
 #pragma unroll
-  for (int k = 0; k < H; ++k) told[k] = k * kRuleThreads + tid < len ? h[k * kRuleThreads + tid] : -1;
+      for (int k = 0; k < H; k += 4) {
+        const int64_t j = place(j0, k);  // (a row's length is at least hist_len, a multiple of four)
+        const int4 t = j < len ? *reinterpret_cast<const int4*>(h + j) : make_int4(-1, -1, -1, -1);
+        told[k] = t.x, told[k + 1] = t.y, told[k + 2] = t.z, told[k + 3] = t.w;
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < H; ++k) told[k] = place(j0, k) < len ? h[place(j0, k)] : -1;
+    }
+  };
+  ask(0);
   // shared memory: the rows' best keys, bitmap, counts and bias places (chunk entries each), the
   // tree, the list of touched tokens
   unsigned long long* best = reinterpret_cast<unsigned long long*>(sm);
@@ -147,25 +165,23 @@ __global__ void __launch_bounds__(kRuleThreads, 4) k_logit_rules(const __grid_co
   for (int64_t j0 = 0; j0 < len; j0 += H * kRuleThreads) {
 #pragma unroll
     for (int k = 0; k < H; ++k) {
-      const int64_t i = (int64_t)told[k] - v0;
-      if (told[k] >= 0 && i >= 0 && i < width) {
-        if (j0 + k * kRuleThreads + tid < prompt) atomicOr(&cnt[i], kPromptFlag);
+      // in 32 bits without a sign: a token below the chunk (or below zero) lands above its end
+      const uint32_t i = (uint32_t)told[k] - (uint32_t)v0;
+      const int64_t j = place(j0, k);
+      if (i < (uint32_t)width && j < len) {
+        if (j < prompt) atomicOr(&cnt[i], kPromptFlag);
         else atomicAdd(&cnt[i], 1u);
         atomicOr(&bits[i >> 5], 1u << (i & 31));
       }
     }
-#pragma unroll
-    for (int k = 0; k < H; ++k) {
-      const int64_t j = j0 + (H + k) * kRuleThreads + tid;
-      told[k] = j < len ? h[j] : -1;
-    }
+    ask(j0 + H * kRuleThreads);
   }
   if (bias) {
     const int64_t b0 = min(max(b_given, (int64_t)0), a.r.n_bias), b1 = min(max(b_end, b0), a.r.n_bias);
     if (tid == 0 && (b0 != b_given || b1 != b_end)) atomicOr(a.status, kRuleClamped);
     for (int64_t j = b0 + tid; j < b1; j += kRuleThreads) {
-      const int64_t i = (int64_t)a.r.bias_tok[j] - v0;
-      if (i >= 0 && i < width) {
+      const uint32_t i = (uint32_t)a.r.bias_tok[j] - (uint32_t)v0;
+      if (i < (uint32_t)width) {
         atomicMax(&bias_at[i], (int32_t)j + 1);
         atomicOr(&bits[i >> 5], 1u << (i & 31));
       }
@@ -273,12 +289,17 @@ __global__ void __launch_bounds__(kRuleThreads, 4) k_logit_rules(const __grid_co
     for (int j0 = lane; j0 < listed; j0 += 128) {  // four listed tokens a lane on their way
       float f4[4];
       int i4[4];
+      uint32_t m4[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        i4[k] = j0 + 32 * k < listed ? list[j0 + 32 * k] : -1;
-        if (i4[k] < c0 || i4[k] >= c1 || (mask && !(mask[i4[k] >> 5] >> (i4[k] & 31) & 1u))) i4[k] = -1;
-        f4[k] = i4[k] >= 0 ? x[i4[k]] : 0.0f;
+        const int i = j0 + 32 * k < listed ? list[j0 + 32 * k] : -1;
+        const bool in = i >= c0 && i < c1;
+        f4[k] = in ? x[i] : 0.0f;
+        m4[k] = in ? mask ? mask[i >> 5] >> (i & 31) & 1u : 1u : 0u;
+        i4[k] = i;
       }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) i4[k] = m4[k] ? i4[k] : -1;
 #pragma unroll 1
       for (int k = 0; k < 4; ++k) {
         const int i = k == 0 ? i4[0] : k == 1 ? i4[1] : k == 2 ? i4[2] : i4[3];
@@ -456,6 +477,7 @@ int launch_rules(const float* logits, int64_t stride, int64_t M, int64_t V, cons
     if (dev < 64) configured[dev] = 1;
   }
   a.vec = ((stride | (out ? out_stride : 0)) & 3) == 0 && (((uintptr_t)logits | (uintptr_t)out) & 15u) == 0;
+  a.hist_vec = rules->hist && (rules->hist_stride & 3) == 0 && ((uintptr_t)rules->hist & 15u) == 0;
   const dim3 grid((unsigned)p.chunks, (unsigned)n_req);
   W12_CUDA_TRY(launch_dependent(key ? k_logit_rules<false> : k_logit_rules<true>, grid, kRuleThreads, smem, s, a));
   W12_LAUNCH_CHECK(what);
