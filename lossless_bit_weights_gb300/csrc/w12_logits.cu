@@ -21,6 +21,7 @@ namespace {
 
 constexpr int kRuleThreads = 256;
 constexpr int kRuleWarps = kRuleThreads / 32;
+constexpr int kRuleParts = 8;        // parts of a row's chunk, at most
 constexpr int kRuleMaxNodes = 1024;  // nodes of one request
 constexpr uint32_t kPromptFlag = 0x80000000u;
 constexpr int32_t kRuleBadRequest = 1, kRuleClamped = 2;
@@ -83,7 +84,7 @@ template <bool WRITE>
 __global__ void __launch_bounds__(kRuleThreads, 4) k_logit_rules(const __grid_constant__ RuleArgs a) {
   pdl_enter();
   extern __shared__ uint32_t sm[];
-  __shared__ int s_listed[kRuleWarps];
+  __shared__ int s_listed[kRuleWarps], s_part[kRuleParts + 1];  // listed tokens: of a warp's words, before a part
   const int r = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t v0 = (int64_t)blockIdx.x * a.chunk;
   const int width = (int)min((int64_t)a.chunk, a.V - v0);
@@ -214,21 +215,39 @@ __global__ void __launch_bounds__(kRuleThreads, 4) k_logit_rules(const __grid_co
     if (w < warp) before += s_listed[w];
     listed += s_listed[w];
   }
+  const int part_len = a.chunk / a.parts;  // a multiple of 32
+  if (tid * 32 < a.chunk && tid * 32 % part_len == 0) s_part[tid * 32 / part_len] = before;
+  if (tid == 0) s_part[a.parts] = listed;
   for (uint32_t m = mine; m; m &= m - 1) list[before++] = (uint16_t)(tid * 32 + __ffs((int)m) - 1);
   __syncthreads();
 
-  // ---- a warp takes one part of one row's chunk
-  const int part_len = a.chunk / a.parts;
+  // ---- a warp takes one part of one row's chunk at a time
   for (int u = warp; u < n * a.parts; u += kRuleWarps) {
-    const int node = u / a.parts, c0 = (u - node * a.parts) * part_len, c1 = min(width, c0 + part_len);
+    const int node = u / a.parts, part = u - node * a.parts, c0 = part * part_len, c1 = min(width, c0 + part_len);
     const int64_t m = off + node;
     const float* x = a.logits + m * a.stride + v0;
     float* y = WRITE ? a.out + m * a.out_stride + v0 : nullptr;
     const uint32_t* mask = a.r.mask ? a.r.mask + m * a.r.mask_stride + v0 / 32 : nullptr;
-    // The untouched tokens: the largest value so far and the four tokens it was first seen among,
-    // three instructions for four tokens; which of the four is asked once, at the end.
+    // The untouched tokens: the largest value so far and the four tokens it was first seen among, kept
+    // with their values; which of the four it is is asked once, at the end.
     float high = -INFINITY;
     int high_at = -1;
+    float4 among = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    // listed tokens of the part: four a lane on their way, the first ones while the others stream
+    float f4[4];
+    uint32_t told4 = 0;
+    auto ask_listed = [&](int j0) {
+      told4 = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        f4[k] = 0.0f;
+        if (j0 + 32 * k >= s_part[part + 1]) continue;
+        const int i = list[j0 + 32 * k];
+        f4[k] = x[i];
+        told4 |= (mask ? mask[i >> 5] >> (i & 31) & 1u : 1u) << k;
+      }
+    };
+    ask_listed(s_part[part] + lane);
     constexpr int U = 4;
     for (int i0 = c0; i0 < c1; i0 += 128 * U) {
       float4 f[U];
@@ -265,45 +284,30 @@ __global__ void __launch_bounds__(kRuleThreads, 4) k_logit_rules(const __grid_co
           if (t > high) {
             high = t;
             high_at = i;
+            among = f[k];
           }
         }
       }
     }
     Best top;
     if (!WRITE) {
-      auto allows = [&](int i) {
-        return !(bits[i >> 5] >> (i & 31) & 1u) && (!mask || (mask[i >> 5] >> (i & 31) & 1u));
-      };
       float most = high;
       for (int o = 16; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
       if (most > -INFINITY) {
-        if (high == most)  // the first of the four; the lanes' candidates meet in the keys below
-          for (int e = 3; e >= 0; --e)
-            if (high_at + e < c1 && allows(high_at + e) && x[high_at + e] == most) top.take(most, high_at + e);
+        if (high == most)  // (tokens not allowed hold -inf; the lanes' candidates meet in the keys below)
+          top.take(most, high_at + (among.x == most ? 0 : among.y == most ? 1 : among.z == most ? 2 : 3));
       } else {  // nothing above -inf: the first -inf, or else the first NaN
         for (int i = c0 + lane; i < c1; i += 32)
-          if (allows(i)) top.take(x[i], i);
+          if (!(bits[i >> 5] >> (i & 31) & 1u) && (!mask || (mask[i >> 5] >> (i & 31) & 1u))) top.take(x[i], i);
       }
     }
     if (WRITE) __syncwarp();  // a listed token is written again, by another lane
-    for (int j0 = lane; j0 < listed; j0 += 128) {  // four listed tokens a lane on their way
-      float f4[4];
-      int i4[4];
-      uint32_t m4[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int i = j0 + 32 * k < listed ? list[j0 + 32 * k] : -1;
-        const bool in = i >= c0 && i < c1;
-        f4[k] = in ? x[i] : 0.0f;
-        m4[k] = in ? mask ? mask[i >> 5] >> (i & 31) & 1u : 1u : 0u;
-        i4[k] = i;
-      }
-#pragma unroll
-      for (int k = 0; k < 4; ++k) i4[k] = m4[k] ? i4[k] : -1;
+    for (int j0 = s_part[part] + lane; j0 < s_part[part + 1]; j0 += 128) {
+      if (j0 >= s_part[part] + 128) ask_listed(j0);
 #pragma unroll 1
       for (int k = 0; k < 4; ++k) {
-        const int i = k == 0 ? i4[0] : k == 1 ? i4[1] : k == 2 ? i4[2] : i4[3];
-        if (i < 0) continue;
+        if (!(told4 >> k & 1u)) continue;
+        const int i = list[j0 + 32 * k];
         float f = k == 0 ? f4[0] : k == 1 ? f4[1] : k == 2 ? f4[2] : f4[3];
         uint32_t c = count ? cnt[i] : 0u;
         if (tree && count)
@@ -418,7 +422,7 @@ RulePlan rule_plan(int64_t M, int64_t V, int32_t n_req) {
     if ((V + p.chunk - 1) / p.chunk * n_req >= 304) break;
   p.chunks = (int)((V + p.chunk - 1) / p.chunk);
   const int64_t rows = (M + n_req - 1) / n_req;
-  p.parts = rows >= 8 ? 1 : rows >= 4 ? 2 : rows >= 2 ? 4 : 8;
+  p.parts = rows >= 16 ? 1 : rows >= 8 ? 2 : rows >= 4 ? 4 : kRuleParts;
   return p;
 }
 
