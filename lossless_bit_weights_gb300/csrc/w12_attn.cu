@@ -95,7 +95,7 @@ struct AttnPlan {
   static constexpr int kSB = D <= 128 ? 3 : 4;       // score buffers in tensor memory
   static constexpr int kSlotBytes = kBK * D * 2;
   static constexpr int kSoftmaxThreads = 256;
-  static constexpr int kThreads = kSoftmaxThreads + 128 + 32;  // + producers + MMA warp
+  static constexpr int kThreads = kSoftmaxThreads + 128 + 64;  // + producers + the two product warps
   static constexpr int kQ = 0;
   static constexpr int kQTile = 128 * D * 2;
   static constexpr int kRing = kQ + kRowTiles * kQTile;
@@ -105,7 +105,7 @@ struct AttnPlan {
   static constexpr int kBad = kNf + kMetaRing * 32;            // kMetaRing words
   static constexpr int kMisc = kBad + kMetaRing * 4;           // tensor memory address, abort, schedule
   static constexpr int kBar = (kMisc + 16 + 7) & ~7;
-  static constexpr int kBytes = kBar + 8 * (2 * kSlots + 3 * kSB + 5 + kMetaRing + 4);
+  static constexpr int kBytes = kBar + 8 * (2 * kSlots + 3 * kSB + 6 + kMetaRing + 4);
   static_assert(kBytes <= 227 * 1024, "shared memory plan too large");
   static_assert(kThreads * 8 <= kSlots * kSlotBytes, "the ring holds the schedule's sums");
   // Tensor memory columns: O of the first tile of rows, then D <= 128: three score buffers, of
@@ -428,8 +428,8 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, const S
   return __all_sync(0xFFFFFFFFu, wait(bar, parity, s));
 }
 
-// Which tile the item-th ring entry of a part holds, in the order in which the MMA warp
-// takes them.  Rows in two halves: K0 V0 K1 V1 ...; tiles in turn: K0 K1 V0 K2 V1 ... V(n-1).
+// Which tile the item-th ring entry of a part holds, in the order in which they are
+// taken.  Rows in two halves: K0 V0 K1 V1 ...; tiles in turn: K0 K1 V0 K2 V1 ... V(n-1).
 __device__ __forceinline__ int ring_tile(int item, int cnt, bool two, bool& is_v) {
   if (two) {
     is_v = item & 1;
@@ -615,89 +615,111 @@ __device__ bool produce(const AttnArgs& a, const CUtensorMap* k_map, const CUten
   return true;
 }
 
+// A step of a unit is a tile of keys and a tile of rows: with one tile of rows, step x takes tile x
+// and score buffer x % kSB; with two, tile x / 2 and buffer 1 + x % 2.  Two warps issue the products,
+// the scores' and the outputs', each waiting only for what its own need (in one warp the two
+// chains of waits and issues added up to 2900 cycles a step, more than the memory's 2800).
+// A ring entry is waited for by the one warp that takes it.  The entry before it in the same slot may
+// be the other warp's, and has then been taken: the scores of a buffer come after the output
+// before them, and an output after its scores.
+struct Steps {
+  int b;
+  bool two;
+  __device__ __forceinline__ explicit Steps(bool two_) : b(two_ ? 1 : 0), two(two_) {}
+  __device__ __forceinline__ void next(int buffers) { b = two ? 3 - b : b + 1 < buffers ? b + 1 : 0; }
+};
+
+// Place of a tile's K or V among a part's ring entries (the inverse of ring_tile).
+__device__ __forceinline__ int ring_item(int tile, bool is_v, int cnt, bool two) {
+  if (two) return 2 * tile + is_v;
+  if (is_v) return tile == cnt - 1 ? 2 * cnt - 1 : 2 * tile + 2;
+  return tile < 2 ? tile : 2 * tile - 1;
+}
+
 template <int D>
-__device__ bool issue_mma(const AttnArgs& a, const Shared& s, Walk<D> walk, uint32_t tmem) {
+__device__ __forceinline__ bool take_entry(const Shared& s, uint32_t entry, uint32_t& addr, uint32_t& slot) {
   using P = AttnPlan<D>;
-  constexpr uint32_t kIdS = umma_idesc_n(P::kBK), kIdO = umma_idesc_n(D) | kTransposeB;
-  uint32_t entry = 0, slot_k = 0, slot_v = 0;
-  uint32_t p_par = 0, o_par = 0, o_any = 0;  // per score buffer: parities of what comes next; any product so far
+  slot = entry % P::kSlots;
+  addr = s.base + P::kRing + slot * P::kSlotBytes;
+  if (!wait_warp(s.full + 8 * slot, (entry / P::kSlots) & 1, s)) return false;
+  fence_proxy_async_smem();  // the copies of other threads, before the tensor core reads them
+  return true;
+}
+
+template <int D>
+__device__ bool issue_scores(const AttnArgs& a, const Shared& s, Walk<D> walk, uint32_t tmem) {
+  using P = AttnPlan<D>;
+  constexpr uint32_t kId = umma_idesc_n(P::kBK);
+  uint32_t entry = 0, slot = 0, k_addr = 0;
+  uint32_t used = 0, o_par = 0;  // per score buffer: scores before, parity of the output after them
   bool had_two = false;
   Part p;
-  auto take = [&](uint32_t& addr, uint32_t& slot) {  // the next ring entry, filled
-    slot = entry % P::kSlots;
-    addr = s.base + P::kRing + slot * P::kSlotBytes;
-    if (!wait_warp(s.full + 8 * slot, (entry / P::kSlots) & 1, s)) return false;
-    fence_proxy_async_smem();  // the copies of other threads, before the tensor core reads them
-    ++entry;
-    return true;
-  };
-  // Scores overwrite the P of an earlier product.  Products with different results are not
-  // ordered among themselves, so that product has to have ended.
-  auto drained = [&](int b) {
-    return !(o_any >> b & 1u) || wait_warp(s.o_done + 8 * b, (o_par >> b & 1u) ^ 1u, s);
-  };
-  auto scores = [&](int row_tile, uint32_t k_addr, int b) {
-    if (!drained(b)) return false;
-    tc_fence_after();
-    const uint32_t q_addr = s.base + P::kQ + row_tile * P::kQTile, d = tmem + P::kS0 + b * P::kSCols;
-#pragma unroll
-    for (int ks = 0; ks < D / 16; ++ks)
-      umma_ss(d, umma_desc(q_addr + (ks >> 2) * 16384 + (ks & 3) * 32),
-              umma_desc(k_addr + (ks >> 2) * (P::kBK * 128) + (ks & 3) * 32), kIdS, ks > 0);
-    umma_commit_one(s.s_full + 8 * b);
-    return true;
-  };
-  auto output = [&](int row_tile, int b, uint32_t v_addr, bool acc) {  // o_done goes by the buffer of P
-    if (!wait_warp(s.p_full + 8 * b, p_par >> b & 1u, s)) return false;
-    p_par ^= 1u << b;
-    tc_fence_after();
-    const uint32_t d = tmem + row_tile * P::kO1, a0 = tmem + P::kS0 + b * P::kSCols;
-#pragma unroll
-    for (int ks = 0; ks < P::kBK / 16; ++ks) {  // 32 keys: 16 columns of upper pieces, 16 of lower ones
-      const uint32_t p_addr = a0 + (ks >> 1) * 32 + (ks & 1) * 8;
-      const uint64_t v_desc = umma_desc_v(v_addr + ks * 2048, P::kBK * 128);
-      umma_ts(d, p_addr, v_desc, kIdO, acc || ks > 0);
-      umma_ts(d, p_addr + 16, v_desc, kIdO, 1);
-    }
-    umma_commit_one(s.o_done + 8 * b);
-    o_par ^= 1u << b;
-    o_any |= 1u << b;
-    return true;
-  };
   for (int unit = 0; walk.next(a, p); ++unit) {
+    const int cnt = p.tb - p.ta;
     const bool two = P::kRowTiles == 2 && p.rows > 128;
-    const int steps = (p.tb - p.ta) * (two ? 2 : 1);
-    uint32_t k_addr = 0, v_addr = 0;
+    const int steps = two ? 2 * cnt : cnt;
     if (!wait_warp(s.q_full, unit & 1, s)) return false;
-    // The second O and score buffer 0 share their columns.
+    // the second O and score buffer 0 share their columns
     bool ended = unit == 0;
-    if (two ? !drained(0) : had_two && !(ended = wait_warp(s.unit_end, (unit - 1) & 1, s))) return false;
+    if (had_two && !two && !(ended = wait_warp(s.unit_end, (unit - 1) & 1, s))) return false;
     had_two = two;
-    // A step is a tile of keys and a tile of rows; its scores run two steps ahead of its output.
-    // With two tiles of rows, every other step takes a tile of keys from the ring and the one
-    // after it gives it back.
-    int b_out = two ? 1 : 0, b_in = b_out;
-    for (int x = -2; x < steps; ++x) {
-      const bool opens = !two || !(x & 1), closes = !two || (x & 1);
-      if (x >= 0) {
-        if (!ended) {  // the last unit's outputs have been read
-          if (!wait_warp(s.unit_end, (unit - 1) & 1, s)) return false;
-          ended = true;
-        }
-        if (x == 0 && steps <= 2) umma_commit_one(s.q_free);  // (not before that: its tree goes with it)
-        if (opens && !take(v_addr, slot_v)) return false;
-        if (!output(two ? x & 1 : 0, b_out, v_addr, x > (two ? 1 : 0))) return false;
-        if (closes) umma_commit_one(s.empty + 8 * slot_v);
-        b_out = two ? 3 - b_out : b_out + 1 < P::kSB ? b_out + 1 : 0;
+    Steps at(two);
+    for (int x = 0; x < steps; ++x, at.next(P::kSB)) {
+      const int row_tile = two ? x & 1 : 0;
+      // The scores overwrite the P of an earlier product.  Products with different results are not
+      // ordered among themselves, so that product has to have ended.
+      if (used >> at.b & 1u) {
+        if (!wait_warp(s.o_done + 8 * at.b, o_par >> at.b & 1u, s)) return false;
+        o_par ^= 1u << at.b;
       }
-      if (x + 2 < steps) {
-        if (opens && !take(k_addr, slot_k)) return false;
-        if (!scores(two ? x & 1 : 0, k_addr, b_in)) return false;
-        if (closes) umma_commit_one(s.empty + 8 * slot_k);
-        if (x + 3 == steps && x >= 0) umma_commit_one(s.q_free);
-        b_in = two ? 3 - b_in : b_in + 1 < P::kSB ? b_in + 1 : 0;
-      }
+      used |= 1u << at.b;
+      if (!row_tile && !take_entry<D>(s, entry + ring_item(two ? x >> 1 : x, false, cnt, two), k_addr, slot)) return false;
+      tc_fence_after();
+      const uint32_t q_addr = s.base + P::kQ + row_tile * P::kQTile, d = tmem + P::kS0 + at.b * P::kSCols;
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks)
+        umma_ss(d, umma_desc(q_addr + (ks >> 2) * 16384 + (ks & 3) * 32),
+                umma_desc(k_addr + (ks >> 2) * (P::kBK * 128) + (ks & 3) * 32), kId, ks > 0);
+      umma_commit_one(s.s_full + 8 * at.b);
+      if (!two || row_tile) umma_commit_one(s.empty + 8 * slot);
     }
+    if (!ended && !wait_warp(s.unit_end, (unit - 1) & 1, s)) return false;
+    umma_commit_one(s.q_free);  // (not before the last unit's end: its tree goes with the query rows)
+    entry += 2 * cnt;
+  }
+  return true;
+}
+
+template <int D>
+__device__ bool issue_outputs(const AttnArgs& a, const Shared& s, Walk<D> walk, uint32_t tmem) {
+  using P = AttnPlan<D>;
+  constexpr uint32_t kId = umma_idesc_n(D) | kTransposeB;
+  uint32_t entry = 0, slot = 0, v_addr = 0, p_par = 0;
+  Part p;
+  for (int unit = 0; walk.next(a, p); ++unit) {
+    const int cnt = p.tb - p.ta;
+    const bool two = P::kRowTiles == 2 && p.rows > 128;
+    const int steps = two ? 2 * cnt : cnt;
+    if (unit > 0 && !wait_warp(s.unit_end, (unit - 1) & 1, s)) return false;  // the last unit's outputs have been read
+    Steps at(two);
+    for (int x = 0; x < steps; ++x, at.next(P::kSB)) {
+      const int row_tile = two ? x & 1 : 0, tile = two ? x >> 1 : x;
+      if (!wait_warp(s.p_full + 8 * at.b, p_par >> at.b & 1u, s)) return false;
+      p_par ^= 1u << at.b;
+      if (!row_tile && !take_entry<D>(s, entry + ring_item(tile, true, cnt, two), v_addr, slot)) return false;
+      tc_fence_after();
+      const uint32_t d = tmem + row_tile * P::kO1, a0 = tmem + P::kS0 + at.b * P::kSCols;
+#pragma unroll
+      for (int ks = 0; ks < P::kBK / 16; ++ks) {  // 32 keys: 16 columns of upper pieces, 16 of lower ones
+        const uint32_t p_addr = a0 + (ks >> 1) * 32 + (ks & 1) * 8;
+        const uint64_t v_desc = umma_desc_v(v_addr + ks * 2048, P::kBK * 128);
+        umma_ts(d, p_addr, v_desc, kId, tile > 0 || ks > 0);
+        umma_ts(d, p_addr + 16, v_desc, kId, 1);
+      }
+      umma_commit_one(s.o_done + 8 * at.b);
+      if (!two || row_tile) umma_commit_one(s.empty + 8 * slot);
+    }
+    entry += 2 * cnt;
   }
   return true;
 }
@@ -942,7 +964,7 @@ __global__ void __launch_bounds__(AttnPlan<D>::kThreads, 1) k_tree_attn(const __
   s.pair = bars(4);
   s.meta = bars(kMetaRing);
   s.reset = bars(1);
-  s.drain = bars(1);
+  s.drain = bars(2);
   if (tid == 0) {
     for (int i = 0; i < P::kSlots; ++i) {
       mbar_init(s.full + 8 * i, 128);
@@ -960,6 +982,7 @@ __global__ void __launch_bounds__(AttnPlan<D>::kThreads, 1) k_tree_attn(const __
     for (int i = 0; i < kMetaRing; ++i) mbar_init(s.meta + 8 * i, 128);
     mbar_init(s.reset, 128);
     mbar_init(s.drain, 1);
+    mbar_init(s.drain + 8, 1);
     mbar_init_fence();
     misc[1] = 0;  // abort
   }
@@ -1002,10 +1025,11 @@ __global__ void __launch_bounds__(AttnPlan<D>::kThreads, 1) k_tree_attn(const __
       }
     }
   } else {
-    ok = issue_mma<D>(a, s, walk, tmem);
+    const int second = warp - (P::kSoftmaxThreads / 32 + 4);
+    ok = second ? issue_outputs<D>(a, s, walk, tmem) : issue_scores<D>(a, s, walk, tmem);
     if (!ok) {  // nothing may be in flight when tensor memory goes back
-      umma_commit_one(s.drain);
-      mbar_wait_bounded(s.drain, 0);
+      umma_commit_one(s.drain + 8 * second);
+      mbar_wait_bounded(s.drain + 8 * second, 0);
     }
   }
   __syncwarp();
