@@ -44,6 +44,8 @@
  *    call that stores y may add a second kernel, launched plainly after the
  *    GEMM's grid, that adds the rows the GEMM split between CTAs; it signals
  *    early too and writes only y.
+ *  - The kernels of the calls on caches and logits at the end of this header are launched the same
+ *    way, but wait for the previous kernel before they touch anything, and signal only then.
  *  - bf16 tensors are passed as uint16_t bit patterns.
  *  - Shapes: 1 <= N, 1 <= K <= 65535 (the escape entry keeps the column in 16
  *    bits and reserves the all-ones column), 1 <= M.
@@ -516,7 +518,7 @@ typedef struct kv_cache {
  * 2; then the table and the pool stay as they were, *total = 0, every slot and src is -1,
  * new_len = cache_len and pool_pos_out = pool_pos.  A path node outside its request
  * gives its token src -1, which kv_write refuses, and sets bit 3.  *status (device
- * int32) is zeroed by the caller.  Errors: W12_ERR_INVALID_ARG (null pointer, pool_pos_out = pool_pos,
+ * int32) is zeroed by the caller.  Asynchronous; allocates nothing.  Errors: W12_ERR_INVALID_ARG (null pointer, pool_pos_out = pool_pos,
  * new_len = cache_len), W12_ERR_SHAPE (n_req outside 1..4096, block_size or table_width
  * outside 1..2^24, n_blocks outside 1..2^31-1, capacity outside 1..2^31-1). */
 W12_API int kv_slots(const int32_t* cache_len, const int32_t* add, int32_t extra, int32_t n_req, int32_t* table,
@@ -531,7 +533,7 @@ W12_API int kv_slots(const int32_t* cache_len, const int32_t* add, int32_t extra
  * n_heads * head_dim adjacent elements; v likewise; pointers and strides are multiples of
  * 8 elements.  A slot of -1 is skipped (kv_slots' padding).  Any other slot outside the
  * cache or row outside 0..n_rows-1 is skipped too and sets bit 0 of *status.  Two tokens
- * with one slot leave either's row.  head_dim: a multiple of 8 up to 1024.
+ * with one slot leave either's row.  head_dim: a multiple of 8 up to 1024.  Asynchronous.
  * Errors: W12_ERR_INVALID_ARG, W12_ERR_SHAPE. */
 W12_API int kv_write(const kv_cache* cache, int64_t layer, int64_t n_layers, const uint16_t* k, int64_t k_layer_stride,
                      int64_t k_row_stride, const uint16_t* v, int64_t v_layer_stride, int64_t v_row_stride,
@@ -546,15 +548,17 @@ W12_API int kv_write(const kv_cache* cache, int64_t layer, int64_t n_layers, con
  * One node per request is plain decoding; a chain (parent i - 1) is a prompt's chunk.
  * q[i] starts at q + i*q_stride, heads adjacent, likewise k and v (strides in elements);
  * out is [M, n_q_heads, head_dim] bf16, adjacent.  Scores, the softmax's statistics and the
- * sums are float; the probabilities are rounded to bf16 before they meet V, and the
- * output once.  Repeated calls give identical bits.
+ * sums are float; a probability meets V as the sum of two bf16 pieces (2^-16 of it is lost),
+ * and the output is rounded to bf16 once.  Repeated calls give identical bits.
  * head_dim 64, 128 or 256; at most 256 nodes a request.  A request whose numbers are out of range
  * (offsets, more than 256 nodes, a malformed tree, a length outside 0..table_width *
  * block_size) sets bit 0 of *status, one whose table names a block outside the cache
- * bit 1, and its out rows are left unwritten; other requests are not affected.
+ * bit 1, and its out rows are left unwritten; other requests are not affected.  Every device-side
+ * wait is bounded; one that runs out (about a second) sets bit 2, and outputs are incomplete.
  * K and V of a token that a node does not attend to do not reach its output, whatever
  * they hold.  ws: tree_attn_workspace_size bytes, no initial state needed (do not pass
  * a GEMM's workspace, whose counters must stay zero).
+ * *status (device int32) is zeroed by the caller.  Asynchronous; allocates nothing.
  * Errors: W12_ERR_INVALID_ARG (null or misaligned pointers or strides), W12_ERR_SHAPE,
  * W12_ERR_BUFFER_TOO_SMALL. */
 W12_API size_t tree_attn_workspace_size(int64_t M, int32_t n_req, int64_t n_q_heads, int64_t n_heads,

@@ -7,8 +7,10 @@ fallback: if libw12.so cannot be built or loaded, every call raises.
 The names mirror the C functions: ``w12_encode_plan``/``w12_encode`` (wrapped
 together by :func:`encode`), :func:`w12_decode`, :func:`w12_decode_q8`,
 :func:`w12_gemm`, :func:`w12_gemm_q8`, :func:`w12_lmhead_argmax`,
-:func:`w12_lmhead_verify`, :func:`tree_verify_tokens`, :func:`tree_verify` and
-:func:`w12_export_canonical`.
+:func:`w12_lmhead_verify`, :func:`tree_verify_tokens`, :func:`tree_verify`,
+:func:`w12_export_canonical`, and for attention layers over a paged cache
+:class:`KVCache`, :func:`kv_slots`, :func:`kv_write`, :func:`tree_attn`,
+:class:`LogitRules`, :func:`logits_process` and :func:`logits_verify`.
 """
 from __future__ import annotations
 

@@ -69,6 +69,8 @@ __device__ __forceinline__ int owner(const int32_t* pre, int n, int32_t t) {
 // fills its part of the slots, of the new table entries and of the returned blocks, so
 // one launch does it all and nothing waits on another block: what a block reads (old table
 // entries, the pool's front) no block writes (new entries, the pool behind its back).
+// Bound by the chain of its loads, not by bytes: 4.7 us for the commit of 24 requests, 10 us for
+// 448,507 new tokens of 500 requests (6 MB).
 __global__ void __launch_bounds__(kSlotThreads) k_kv_slots(const __grid_constant__ SlotArgs a) {
   pdl_enter();
   extern __shared__ int32_t sm[];
@@ -208,7 +210,9 @@ constexpr int kWriteThreads = 256;
 constexpr int kWriteTokens = 4;  // tokens of a block
 
 // A block copies four tokens of one layer, their slots and rows looked up together and four
-// 16-byte pieces a thread on their way.
+// 16-byte pieces a thread on their way.  Bound by bytes, read once and written once: 12289 tokens of
+// 8 heads of 128 (101 MB) in 21.6 us, 4.7 TB/s, 0.70 of the measured copy rate; one token a
+// block and one piece a thread took 28.
 __global__ void __launch_bounds__(kWriteThreads) k_kv_write(const __grid_constant__ WriteArgs a) {
   pdl_enter();
   const int64_t l = blockIdx.y;

@@ -11,7 +11,14 @@
 // row's own path, so the table is never changed and rows need no barriers between them.
 // (A test at every token instead sent almost every warp through the formula: with 2500
 // distinct tokens in a history, 87 % of all runs of 128 tokens hold one.)
+//
+// Bound by bytes, the logits read once (and written once where they are asked for): 192 rows of
+// 151936 tokens of 24 requests take 62 us with all rules (237 MB, 3.8 TB/s, 0.57 of the measured copy rate),
+// 45 us with the argmax and acceptance instead of the rows (118 MB, 2.6 TB/s).  What is left is
+// the making of the tables, during which a block streams nothing (about 13 us of the 45), the
+// history (4) and the listed tokens (5).
 #include <cstdint>
+#include <type_traits>
 
 #include "w12_internal.cuh"
 #include "w12_pdl.cuh"
@@ -83,7 +90,7 @@ __device__ __forceinline__ float4 load4(const float* x, int i, int n, bool vec) 
 template <bool WRITE>
 __global__ void __launch_bounds__(kRuleThreads, 4) k_logit_rules(const __grid_constant__ RuleArgs a) {
   pdl_enter();
-  extern __shared__ uint32_t sm[];
+  extern __shared__ __align__(16) uint32_t sm[];
   __shared__ int s_listed[kRuleWarps], s_part[kRuleParts + 1];  // listed tokens: of a warp's words, before a part
   const int r = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t v0 = (int64_t)blockIdx.x * a.chunk;
@@ -129,7 +136,7 @@ __global__ void __launch_bounds__(kRuleThreads, 4) k_logit_rules(const __grid_co
   // shared memory: the rows' best keys, bitmap, counts and bias places (chunk entries each), the
   // tree, the list of touched tokens
   unsigned long long* best = reinterpret_cast<unsigned long long*>(sm);
-  uint32_t* bits = sm + (WRITE ? 0 : 2 * n);
+  uint32_t* bits = sm + (WRITE ? 0 : 2 * ((n + 1) & ~1));  // 16-byte aligned, as are the tables behind it
   uint32_t* cnt = bits + a.chunk / 32;
   int32_t* bias_at = reinterpret_cast<int32_t*>(cnt + (count ? a.chunk : 0));
   int32_t* parent = bias_at + (bias ? a.chunk : 0);
@@ -141,11 +148,8 @@ __global__ void __launch_bounds__(kRuleThreads, 4) k_logit_rules(const __grid_co
   if (a.vec)
     for (int i = tid; i < n; i += kRuleThreads)
       if (width >= 4) prefetch_l2(a.logits + (off + i) * a.stride + v0, (uint32_t)(width & ~3) * 4);
-  for (int i = tid; i < a.chunk / 32; i += kRuleThreads) bits[i] = 0;
-  if (count)
-    for (int i = tid; i < a.chunk; i += kRuleThreads) cnt[i] = 0;
-  if (bias)
-    for (int i = tid; i < a.chunk; i += kRuleThreads) bias_at[i] = 0;
+  const int zeros = (a.chunk / 32 + (count ? a.chunk : 0) + (bias ? a.chunk : 0)) / 4;  // bitmap and tables, one run
+  for (int i = tid; i < zeros; i += kRuleThreads) reinterpret_cast<uint4*>(bits)[i] = make_uint4(0, 0, 0, 0);
   if (!WRITE)
     for (int i = tid; i < n; i += kRuleThreads) best[i] = 0;
   bool ok = true;
@@ -249,29 +253,29 @@ __global__ void __launch_bounds__(kRuleThreads, 4) k_logit_rules(const __grid_co
     };
     ask_listed(s_part[part] + lane);
     constexpr int U = 4;
-    for (int i0 = c0; i0 < c1; i0 += 128 * U) {
+    auto stream = [&](int i0, auto whole) {  // U runs of four tokens a lane; whole: none of them passes c1
       float4 f[U];
-      uint32_t allowed[U];
+      uint32_t hide[U];  // of the four tokens: not allowed, or listed (where nothing is written)
 #pragma unroll
       for (int k = 0; k < U; ++k) {
         const int i = i0 + k * 128 + 4 * lane;
-        f[k] = load4(x, i, c1, a.vec);
-        allowed[k] = i >= c1 ? 0u : mask ? mask[i >> 5] >> (i & 31) : 15u;
+        f[k] = whole.value ? __ldcs(reinterpret_cast<const float4*>(x + i)) : load4(x, i, c1, a.vec);
+        hide[k] = mask && (whole.value || i < c1) ? ~mask[i >> 5] >> (i & 31) : 0u;
       }
 #pragma unroll
       for (int k = 0; k < U; ++k) {
         const int i = i0 + k * 128 + 4 * lane;
-        if (i >= c1) break;
-        uint32_t may = allowed[k] & (i + 4 <= c1 ? 15u : (1u << (c1 - i)) - 1u);
-        if (!WRITE) may &= ~(bits[i >> 5] >> (i & 31));
-        if (may != 15u) {
-          f[k].x = may & 1u ? f[k].x : -INFINITY;
-          f[k].y = may & 2u ? f[k].y : -INFINITY;
-          f[k].z = may & 4u ? f[k].z : -INFINITY;
-          f[k].w = may & 8u ? f[k].w : -INFINITY;
+        if (!whole.value && i >= c1) break;
+        if (!WRITE) hide[k] |= bits[i >> 5] >> (i & 31);
+        if (!whole.value && i + 4 > c1) hide[k] |= 15u << (c1 - i);
+        if (hide[k] & 15u) {
+          f[k].x = hide[k] & 1u ? -INFINITY : f[k].x;
+          f[k].y = hide[k] & 2u ? -INFINITY : f[k].y;
+          f[k].z = hide[k] & 4u ? -INFINITY : f[k].z;
+          f[k].w = hide[k] & 8u ? -INFINITY : f[k].w;
         }
         if (WRITE) {
-          if (a.vec && i + 4 <= c1) {
+          if (whole.value || (a.vec && i + 4 <= c1)) {
             __stcs(reinterpret_cast<float4*>(y + i), f[k]);
           } else {
             y[i] = f[k].x;
@@ -288,7 +292,11 @@ __global__ void __launch_bounds__(kRuleThreads, 4) k_logit_rules(const __grid_co
           }
         }
       }
-    }
+    };
+    int at = c0;
+    if (a.vec)
+      for (; at + 128 * U <= c1; at += 128 * U) stream(at, std::true_type{});
+    for (; at < c1; at += 128 * U) stream(at, std::false_type{});
     Best top;
     if (!WRITE) {
       float most = high;
@@ -415,7 +423,11 @@ struct RulePlan {
 
 // Chunk of the vocabulary per block, a multiple of 256: the larger it is, the fewer blocks
 // scan a request's history and the more rows share the table; the smaller, the more blocks
-// there are.  The largest of 4096, 2048, 1024 with at least two blocks per SM.
+// there are.  The largest of 4096, 2048, 1024 with at least two blocks per SM: verify of 192 rows
+// took 45 us at 4096 and 49 at 2048, of a 16-node tree 18.0 at 1024, 17.3 at 512, 21.8 at 256.
+// Parts of a row's chunk, one a warp at a time: smaller ones even out trees of unequal size, larger ones
+// meet fewer loads' latencies (24 trees of 8 rows: 71 and 47 us at 1 part, 66 and 45 at 2, 67 and
+// 54 at 4, with and without the rows written; a 16-node tree 18 at 1, 21 at 2).
 RulePlan rule_plan(int64_t M, int64_t V, int32_t n_req) {
   RulePlan p{};
   for (p.chunk = 4096; p.chunk > 1024; p.chunk /= 2)
@@ -470,8 +482,8 @@ int launch_rules(const float* logits, int64_t stride, int64_t M, int64_t V, cons
   const bool count = rules->rep || rules->freq || rules->pres;
   const int64_t nodes = M < kRuleMaxNodes ? M : kRuleMaxNodes;
   const size_t smem = (size_t)p.chunk / 8 + (count ? (size_t)p.chunk * 4 : 0) + (rules->bias_off ? (size_t)p.chunk * 4 : 0) +
-                      (parent ? (size_t)nodes * 12 : 0) + (key ? (size_t)nodes * 8 : 0) + (size_t)p.chunk * 2;
-  constexpr size_t most = 4096 / 8 + 4096 * 10 + kRuleMaxNodes * 20;
+                      (parent ? (size_t)nodes * 12 : 0) + (key ? (size_t)(nodes + 1) * 8 : 0) + (size_t)p.chunk * 2;
+  constexpr size_t most = 4096 / 8 + 4096 * 10 + kRuleMaxNodes * 20 + 8;
   static int configured[64] = {0};
   int dev = 0;
   W12_CUDA_TRY(cudaGetDevice(&dev));
