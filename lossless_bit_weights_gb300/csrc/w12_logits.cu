@@ -13,10 +13,11 @@
 // distinct tokens in a history, 87 % of all runs of 128 tokens hold one.)
 //
 // Bound by bytes, the logits read once (and written once where they are asked for): 192 rows of
-// 151936 tokens of 24 requests take 62 us with all rules (237 MB, 3.8 TB/s, 0.57 of the measured copy rate),
-// 45 us with the argmax and acceptance instead of the rows (118 MB, 2.6 TB/s).  What is left is
-// the making of the tables, during which a block streams nothing (about 13 us of the 45), the
-// history (4) and the listed tokens (5).
+// 151936 tokens of 24 requests take 49 us with all rules (237 MB, 4.8 TB/s, 0.72 of the measured
+// copy rate), 37 us with the argmax and acceptance instead of the rows (117 MB, 3.2 TB/s).  What is
+// left is the making of the tables, during which a block streams nothing, the history and the
+// listed tokens (about 13, 4 and 5 us of the 37).  Instructions count as much as bytes: bounds
+// tests at every four tokens cost 12 and 8 us.
 #include <cstdint>
 #include <type_traits>
 
@@ -423,11 +424,11 @@ struct RulePlan {
 
 // Chunk of the vocabulary per block, a multiple of 256: the larger it is, the fewer blocks
 // scan a request's history and the more rows share the table; the smaller, the more blocks
-// there are.  The largest of 4096, 2048, 1024 with at least two blocks per SM: verify of 192 rows
-// took 45 us at 4096 and 49 at 2048, of a 16-node tree 18.0 at 1024, 17.3 at 512, 21.8 at 256.
+// there are.  The largest of 4096, 2048, 1024 with at least two blocks per SM: 192 rows took 50 us
+// written and 37 verified at 4096, 48 and 44 at 2048; a 16-node tree 15.5 at 1024, 15.8 at 512.
 // Parts of a row's chunk, one a warp at a time: smaller ones even out trees of unequal size, larger ones
-// meet fewer loads' latencies (24 trees of 8 rows: 71 and 47 us at 1 part, 66 and 45 at 2, 67 and
-// 54 at 4, with and without the rows written; a 16-node tree 18 at 1, 21 at 2).
+// meet fewer loads' latencies (24 trees of 8 rows: 52 and 36 us at 1 part, 50 and 37 at 2, 51 and
+// 44 at 4, written and verified; a 16-node tree 15.6 at 1, 20.6 at 2).
 RulePlan rule_plan(int64_t M, int64_t V, int32_t n_req) {
   RulePlan p{};
   for (p.chunk = 4096; p.chunk > 1024; p.chunk /= 2)
