@@ -569,6 +569,10 @@ W12_API int tree_attn(const uint16_t* q, int64_t q_stride, const uint16_t* k, in
                       const int32_t* parent, const int32_t* req_offsets, int32_t n_req, float scale, uint16_t* out,
                       int32_t* status, void* ws, size_t ws_bytes, void* stream);
 
+/* Diagnostic for tests of the path above: bounds the waits of tree_attn calls made after it, in SM
+ * clock cycles (cycles <= 0 restores the default, 2^31, about a second, which is also the most).  Returns W12_OK. */
+W12_API int tree_attn_set_wait_limit(int64_t cycles);
+
 /* ---------------------------------------------------------------------------
  * Rules on logits before the argmax (no counterpart in the pages): penalties for
  * repeated tokens, a bias per token, and a mask of the tokens a grammar allows.  Device

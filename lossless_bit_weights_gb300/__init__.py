@@ -117,6 +117,7 @@ SIGNATURES = [
     ("tree_attn_workspace_size", _SZ, [_I64, _I32, _I64, _I64, _I64]),
     ("tree_attn", ctypes.c_int, [_P, _I64, _P, _I64, _P, _I64, _I64, _I64, ctypes.POINTER(kv_cache), _I64, _P, _I64,
                                  _I64, _P, _P, _P, _I32, ctypes.c_float, _P, _P, _P, _SZ, _P]),
+    ("tree_attn_set_wait_limit", ctypes.c_int, [_I64]),
     ("logits_process", ctypes.c_int, [_P, _I64, _I64, _I64, ctypes.POINTER(logit_rules), _P, _P, _P, _I32, _P, _I64,
                                       _P, _P]),
     ("logits_verify_workspace_size", _SZ, [_I64, _I64, _I32]),
@@ -777,6 +778,11 @@ def tree_attn(q, k, v, cache: KVCache, table, cache_len, parent, req_offsets=Non
         None if req_offsets is None else req_offsets.data_ptr(), n_req, D ** -0.5 if scale is None else scale,
         out.data_ptr(), status.data_ptr(), buf.data_ptr(), buf.numel(), raw))
     return out, status
+
+
+def tree_attn_set_wait_limit(cycles: int) -> None:
+    """Diagnostic: bound of the waits of later tree_attn calls (0 = default)."""
+    _check(lib().tree_attn_set_wait_limit(int(cycles)))
 
 
 # ---------------------------------------------------------------- rules on logits

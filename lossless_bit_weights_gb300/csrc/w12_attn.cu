@@ -37,6 +37,7 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <mutex>
@@ -87,6 +88,7 @@ struct AttnArgs {
   int32_t n_req, block_size, group, n_heads, n_q_heads, row_cap;
   FastDiv by_block, by_group;
   int32_t box_rows;  // tokens of a box of the tensor maps; 0: rows are copied by the threads
+  uint32_t wait_cycles;  // bound of a wait
   float scale_log2;  // scale * log2(e)
   uint16_t* out;
   int32_t* status;
@@ -412,29 +414,38 @@ struct Shared {
   uint32_t base;         // shared-memory address of the block
   uint8_t* sm;
   volatile int32_t* abort;
+  uint32_t limit;        // cycles of a wait
   uint32_t full, empty, q_full, q_free, s_full, p_full, o_done, unit_end, meta, reset, drain, pair;
 };
 
-// A bounded wait; one that runs out stops every role of the CTA.
-__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int32_t* abort) {
+// A bounded wait; one that runs out stops every role of the CTA.  The hardware suspends the thread
+// in a try_wait for longer than a tile takes, so only waits that are stuck reach the slow path.
+__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int32_t* abort, uint32_t limit) {
   const long long start = clock64();
-  while (!mbar_try_wait(bar, parity)) {
+  bool done;
+  do {
+    done = mbar_try_wait(bar, parity);
     if (*abort) return false;
-    if (clock64() - start > kWaitCycles) {
+    if (clock64() - start > limit) {  // also where the phase came, late
       *abort = 1;
       return false;
     }
-  }
+  } while (!done);
   return true;
 }
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, const Shared& s) {
   if (mbar_try_wait(bar, parity)) return true;
-  return wait_slow(bar, parity, s.abort);
+  return wait_slow(bar, parity, s.abort, s.limit);
 }
 // The same answer for the whole warp, whose next steps (tensor memory accesses, shuffles) take
 // all of its threads.
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, const Shared& s) {
   return __all_sync(0xFFFFFFFFu, wait(bar, parity, s));
+}
+// The same with all of its time against the limit, the hardware's suspension too: for the wait that
+// always takes some time, the one for a tile's probabilities.
+__device__ __forceinline__ bool wait_warp_timed(uint32_t bar, uint32_t parity, const Shared& s) {
+  return __all_sync(0xFFFFFFFFu, mbar_test_wait(bar, parity) || wait_slow(bar, parity, s.abort, s.limit));
 }
 
 // Which tile the item-th ring entry of a part holds, in the order in which they are
@@ -620,7 +631,6 @@ __device__ bool produce(const AttnArgs& a, const CUtensorMap* k_map, const CUten
       }
     }
   }
-  cp_wait_all();
   return true;
 }
 
@@ -713,7 +723,7 @@ __device__ bool issue_outputs(const AttnArgs& a, const Shared& s, Walk<D> walk, 
     Steps at(two);
     for (int x = 0; x < steps; ++x, at.next(P::kSB)) {
       const int row_tile = two ? x & 1 : 0, tile = two ? x >> 1 : x;
-      if (!wait_warp(s.p_full + 8 * at.b, p_par >> at.b & 1u, s)) return false;
+      if (!wait_warp_timed(s.p_full + 8 * at.b, p_par >> at.b & 1u, s)) return false;
       p_par ^= 1u << at.b;
       if (!row_tile && !take_entry<D>(s, entry + ring_item(tile, true, cnt, two), v_addr, slot)) return false;
       tc_fence_after();
@@ -956,6 +966,7 @@ __global__ void __launch_bounds__(AttnPlan<D>::kThreads, 1) k_tree_attn(const __
   s.base = smem_u32(attn_sm);
   int32_t* misc = reinterpret_cast<int32_t*>(attn_sm + P::kMisc);
   s.abort = misc + 1;
+  s.limit = a.wait_cycles;
   uint32_t bar = s.base + P::kBar;
   auto bars = [&](int n) {
     const uint32_t b = bar;
@@ -1022,28 +1033,26 @@ __global__ void __launch_bounds__(AttnPlan<D>::kThreads, 1) k_tree_attn(const __
     }
     a.units[c] = u;
   }
-  bool ok = true;
   if (warp < P::kSoftmaxThreads / 32) {
-    ok = softmax<D>(a, s, walk, tmem, c);
+    softmax<D>(a, s, walk, tmem, c);
   } else if (warp < P::kSoftmaxThreads / 32 + 4) {
-    ok = produce<D>(a, &k_map, &v_map, s, walk);
-    if (!ok) {  // nothing may be on its way into shared memory when the block ends
-      cp_wait_all();
-      const long long began = clock64();
-      while (a.box_rows && clock64() - began < (1ll << 24)) {
-      }
-    }
+    produce<D>(a, &k_map, &v_map, s, walk);
+    cp_wait_all();
   } else {
     const int second = warp - (P::kSoftmaxThreads / 32 + 4);
-    ok = second ? issue_outputs<D>(a, s, walk, tmem) : issue_scores<D>(a, s, walk, tmem);
-    if (!ok) {  // nothing may be in flight when tensor memory goes back
-      umma_commit_one(s.drain + 8 * second);
-      mbar_wait_bounded(s.drain + 8 * second, 0);
-    }
+    if (second) issue_outputs<D>(a, s, walk, tmem);
+    else issue_scores<D>(a, s, walk, tmem);
+    umma_commit_one(s.drain + 8 * second);  // nothing may be in flight when tensor memory goes back
+    mbar_wait_bounded(s.drain + 8 * second, 0);
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
+  if (misc[1] && a.box_rows) {  // given up: boxes that nobody waited for land before the block ends (9 ms)
+    const long long began = clock64();
+    while (clock64() - began < (1ll << 24)) {
+    }
+  }
   if (warp == 0) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
@@ -1115,6 +1124,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_tree_attn_join(const __grid_co
     }
     bad |= __shfl_xor_sync(0xFFFFFFFFu, bad, 8);
     bad |= __shfl_xor_sync(0xFFFFFFFFu, bad, 16);
+    bad &= kAttnBadRequest | kAttnBadBlock;  // (a part that was given up holds anything)
     if (sub || e0 + mine >= outputs) continue;
     if (bad) {  // the same for every output of the unit
       if (e == 0) atomicOr(a.status, bad);
@@ -1126,6 +1136,8 @@ __global__ void __launch_bounds__(kJoinThreads) k_tree_attn_join(const __grid_co
     *reinterpret_cast<uint2*>(out) = make_uint2(pack2(v[1] * inv, v[2] * inv), pack2(v[3] * inv, v[4] * inv));
   }
 }
+
+std::atomic<uint32_t> g_wait_cycles{uint32_t(kWaitCycles)};
 
 int64_t row_cap(int64_t M, int64_t group, int64_t D) {
   const int64_t rows = M * group, most = D == 256 ? 128 : 256;
@@ -1215,6 +1227,11 @@ using namespace w12;
 
 extern "C" {
 
+int tree_attn_set_wait_limit(int64_t cycles) {
+  g_wait_cycles.store(uint32_t(cycles > 0 && cycles < kWaitCycles ? cycles : kWaitCycles), std::memory_order_relaxed);
+  return W12_OK;
+}
+
 size_t tree_attn_workspace_size(int64_t M, int32_t n_req, int64_t n_q_heads, int64_t n_heads, int64_t head_dim) {
   if (M < 1 || n_req < 1 || n_heads < 1 || n_q_heads < n_heads || n_q_heads % n_heads || M > 0x7FFFFFFF ||
       (head_dim != 64 && head_dim != 128 && head_dim != 256))
@@ -1278,6 +1295,7 @@ int tree_attn(const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_
   a.by_block = fast_div(a.block_size);
   a.by_group = fast_div(a.group);
   a.scale_log2 = scale * 1.4426950408889634f;
+  a.wait_cycles = g_wait_cycles.load(std::memory_order_relaxed);
   a.out = out;
   a.status = status;
   uint8_t* base = static_cast<uint8_t*>(ws);

@@ -381,6 +381,26 @@ def test_out_of_range_requests_are_reported_and_left_alone(w12, d):
         assert (out[p.off[r]:p.off[r + 1]] == 0x1234).all()
 
 
+@pytest.mark.parametrize("d,block", [(64, 16), (128, 16), (128, 24), (256, 64)])
+def test_a_wait_that_runs_out_is_reported(w12, d, block):
+    """Waits bounded far below a tile's latency: every role gives up, nothing stays in flight, the
+    call ends and reports it, and the next call on the same workspace gives the full result."""
+    p = Problem(23, [3000, 40, 700], [30, 5, 60], 2, 3, d, block)
+    args, ws = p.args(w12), w12.Workspace()
+    first, st = w12.tree_attn(*args, ws=ws)
+    assert int(st) == 0
+    w12.tree_attn_set_wait_limit(64)
+    try:
+        _, st = w12.tree_attn(*args, ws=ws)
+        torch.cuda.synchronize()
+    finally:
+        w12.tree_attn_set_wait_limit(0)
+    assert int(st) & 4
+    again, st = w12.tree_attn(*args, ws=ws)
+    assert int(st) == 0 and torch.equal(first, again)
+    p.check(again)
+
+
 def test_too_many_nodes_are_reported(w12):
     p = Problem(20, [100, 30], [257, 3], 1, 1, 64, 16)
     out, st = w12.tree_attn(*p.args(w12))
