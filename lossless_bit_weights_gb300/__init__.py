@@ -825,7 +825,7 @@ def _rule_args(logits, rules: LogitRules, parent, draft, req_offsets):
     M, V = logits.shape
     n_req = 1 if req_offsets is None else _i32(req_offsets).numel() - 1
     if rules.n_req - {n_req}:
-        raise ValueError(f"the rules are for {rules.n_req.pop()} requests, the rows of {n_req}")
+        raise ValueError(f"the rules are for {min(rules.n_req)} requests, the rows of {n_req}")
     if rules.rows is not None and (rules.rows != M or rules.words * 32 < V):
         raise ValueError(f"the mask must have {M} rows of {(V + 31) // 32} words or more")
     for t in (parent, draft):

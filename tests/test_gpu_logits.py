@@ -352,6 +352,15 @@ def test_another_stream(w12):
     p.check_verify(res)
 
 
+def test_a_refusal_leaves_the_rules_as_they_were(w12):
+    p = Problem(22, [2, 2], 700)
+    x, rules, (parent, draft, off) = f32(p.logits), p.rules(w12), p.tree()
+    for _ in range(2):  # the same mistake again is refused again
+        with pytest.raises(ValueError, match="2 requests"):
+            w12.logits_verify(x, rules, parent, draft, None)
+    p.check_verify(w12.logits_verify(x, rules, parent, draft, off))
+
+
 def test_refusals(w12):
     p = Problem(22, [2, 2], 700)
     x, rules, (parent, draft, off) = f32(p.logits), p.rules(w12), p.tree()
