@@ -559,8 +559,8 @@ W12_API int kv_write(const kv_cache* cache, int64_t layer, int64_t n_layers, con
  * they hold.  ws: tree_attn_workspace_size bytes, no initial state needed (do not pass
  * a GEMM's workspace, whose counters must stay zero).
  * *status (device int32) is zeroed by the caller.  Asynchronous; allocates nothing.
- * Errors: W12_ERR_INVALID_ARG (null or misaligned pointers or strides), W12_ERR_SHAPE,
- * W12_ERR_BUFFER_TOO_SMALL. */
+ * Errors: W12_ERR_INVALID_ARG (null or misaligned pointers or strides, out overlapping q, k or v),
+ * W12_ERR_SHAPE, W12_ERR_BUFFER_TOO_SMALL. */
 W12_API size_t tree_attn_workspace_size(int64_t M, int32_t n_req, int64_t n_q_heads, int64_t n_heads,
                                         int64_t head_dim);
 W12_API int tree_attn(const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_stride, const uint16_t* v,
@@ -611,10 +611,10 @@ typedef struct logit_rules {
 /* out[m*out_stride + v] = the formula above, for M rows of V logits (row m at
  * logits + m*stride) that are the nodes of n_req requests (parent, draft, req_offsets as
  * for tree_verify_tokens; parent and draft NULL: rows without drafted tokens).  out may be
- * logits.  A request that is out of range (offsets, a malformed tree, more than 1024
- * nodes) sets bit 0 of *status and its rows are left; a length or bias range out of range
- * is clamped and sets bit 1.  Asynchronous; allocates nothing.  Errors:
- * W12_ERR_INVALID_ARG, W12_ERR_SHAPE (M, V, n_req, strides). */
+ * logits (with its stride) and otherwise shares no element with it.  A request that is out of
+ * range (offsets, a malformed tree, more than 1024 nodes) sets bit 0 of *status and its rows
+ * are left; a length or bias range out of range is clamped and sets bit 1.  Asynchronous; allocates nothing.  Errors:
+ * W12_ERR_INVALID_ARG (also an out that overlaps logits otherwise), W12_ERR_SHAPE (M, V, n_req, strides). */
 W12_API int logits_process(const float* logits, int64_t stride, int64_t M, int64_t V, const logit_rules* rules,
                            const int32_t* parent, const int32_t* draft, const int32_t* req_offsets, int32_t n_req,
                            float* out, int64_t out_stride, int32_t* status, void* stream);

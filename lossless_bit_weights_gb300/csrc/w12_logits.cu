@@ -515,6 +515,13 @@ int logits_process(const float* logits, int64_t stride, int64_t M, int64_t V, co
   if (st) return st;
   if (!out) return fail(W12_ERR_INVALID_ARG, "logits_process: null pointer");
   if (out_stride < V) return fail(W12_ERR_SHAPE, "logits_process: out_stride=%lld is less than V", (long long)out_stride);
+  // In place, apart, or side by side in the rows of one array.
+  const uintptr_t l0 = (uintptr_t)logits, o0 = (uintptr_t)out, row = (uintptr_t)V * 4, pitch = (uintptr_t)stride * 4;
+  const uintptr_t by = (o0 > l0 ? o0 - l0 : l0 - o0) % pitch;
+  const bool alike = stride == out_stride || M == 1;
+  const bool apart = o0 >= l0 + (M - 1) * pitch + row || l0 >= o0 + (uintptr_t)(M - 1) * out_stride * 4 + row;
+  if (!apart && !(alike && (o0 == l0 || (M > 1 && by >= row && by + row <= pitch))))
+    return fail(W12_ERR_INVALID_ARG, "logits_process: out must be logits or not overlap it");
   return launch_rules(logits, stride, M, V, rules, parent, draft, req_offsets, n_req, out, out_stride, status, nullptr,
                       (cudaStream_t)stream, "logits_process kernel");
 }

@@ -417,6 +417,21 @@ def test_offsets_out_of_range_are_reported(w12):
     p.check(out, [0, 1])
 
 
+def test_out_must_not_overlap_its_inputs(w12):
+    p = Problem(22, [100], [5], 2, 2, 64, 16)
+    q, k, v, cache, table, lens, parent, off = p.args(w12)
+    both = torch.zeros((2 * q.shape[0],) + tuple(q.shape[1:]), dtype=q.dtype, device="cuda")
+    n = q.shape[0]
+    both[:n] = q
+    for out in (both[:n], both[1:n + 1]):
+        with pytest.raises(w12.W12Error, match="overlap") as e:
+            w12.tree_attn(both[:n], k, v, cache, table, lens, parent, off, out=out)
+        assert e.value.status == 1
+    out, st = w12.tree_attn(both[:n], k, v, cache, table, lens, parent, off, out=both[n:])
+    assert int(st) == 0
+    p.check(out)
+
+
 def test_refusals(w12):
     p = Problem(22, [100], [5], 2, 2, 64, 16)
     q, k, v, cache, table, lens, parent, off = p.args(w12)

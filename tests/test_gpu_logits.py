@@ -361,6 +361,23 @@ def test_a_refusal_leaves_the_rules_as_they_were(w12):
     p.check_verify(w12.logits_verify(x, rules, parent, draft, off))
 
 
+def test_out_in_place_apart_or_beside(w12):
+    p = Problem(22, [2, 2], 700)
+    rules, (parent, draft, off) = p.rules(w12), p.tree()
+    want, st = w12.logits_process(f32(p.logits), rules, parent, draft, off)
+    assert int(st) == 0
+    wide = torch.zeros((5, 1500), dtype=torch.float32, device="cuda")
+    x = wide[:4, :700]
+    for out in (wide[1:, :700], wide[:4, 1:701], wide[:4, 699:1399], wide.as_strided((4, 700), (1500, 1), 900), wide.view(-1)[:4 * 900].view(4, 900)[:, :700]):
+        with pytest.raises(w12.W12Error, match="overlap") as e:
+            w12.logits_process(x, rules, parent, draft, off, out=out)
+        assert e.value.status == 1
+    for out in (wide[:4, 700:1400], wide[:4, 800:], wide[1:, 800:], x):
+        x.copy_(f32(p.logits))
+        got, st = w12.logits_process(x, rules, parent, draft, off, out=out)
+        assert int(st) == 0 and torch.equal(got, want)
+
+
 def test_refusals(w12):
     p = Problem(22, [2, 2], 700)
     x, rules, (parent, draft, off) = f32(p.logits), p.rules(w12), p.tree()
