@@ -280,9 +280,6 @@ int kv_slots(const int32_t* cache_len, const int32_t* add, int32_t extra, int32_
              int64_t block_size, const int32_t* path_nodes, const int32_t* req_offsets, int64_t n_nodes,
              int64_t capacity, int64_t* slot, int32_t* src, int32_t* new_len, int64_t* pool_pos_out, int64_t* total,
              int32_t* status, void* stream) {
-  if (!cache_len || !add || !table || !pool || !pool_pos || !slot || !src || !new_len || !pool_pos_out || !total ||
-      !status)
-    return fail(W12_ERR_INVALID_ARG, "kv_slots: null pointer");
   if (pool_pos_out == pool_pos || new_len == cache_len)
     return fail(W12_ERR_INVALID_ARG, "kv_slots: pool_pos_out and new_len must not be the inputs");
   if (n_req < 1 || n_req > kSlotMaxReq || block_size < 1 || block_size > kMaxBlock || table_width < 1 ||
@@ -293,6 +290,10 @@ int kv_slots(const int32_t* cache_len, const int32_t* add, int32_t extra, int32_
                 "capacity=%lld out of range",
                 n_req, kSlotMaxReq, (long long)block_size, (long long)table_width, (long long)table_stride,
                 (long long)n_blocks, (long long)capacity);
+  // (after the sizes: a tensor of no elements has a null pointer)
+  if (!cache_len || !add || !table || !pool || !pool_pos || !slot || !src || !new_len || !pool_pos_out || !total ||
+      !status)
+    return fail(W12_ERR_INVALID_ARG, "kv_slots: null pointer");
   if (path_nodes && (n_nodes < 1 || n_nodes > 0x7FFFFFFF))
     return fail(W12_ERR_SHAPE, "kv_slots: n_nodes=%lld out of range", (long long)n_nodes);
   if (path_nodes && !req_offsets && n_req != 1)
