@@ -1264,6 +1264,8 @@ int tree_attn(const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_
       ((q_stride | k_stride | v_stride) & 7) || q_stride < 0 || k_stride < 0 || v_stride < 0)
     return fail(W12_ERR_INVALID_ARG,
                 "tree_attn: q, k, v, out and ws must be 16-byte aligned, strides non-negative multiples of 8");
+  const AttnWs w = attn_ws(M, n_q_heads / H, D);
+  if (ws_bytes < w.total) return fail(W12_ERR_BUFFER_TOO_SMALL, "tree_attn: workspace %zu < %zu", ws_bytes, w.total);
   // Some blocks write their rows while others still read.
   const uintptr_t o0 = (uintptr_t)out, o1 = o0 + (uintptr_t)(M * n_q_heads * D) * 2;
   auto meets = [&](const uint16_t* p, int64_t stride, int64_t heads) {
@@ -1271,8 +1273,6 @@ int tree_attn(const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_
   };
   if (meets(q, q_stride, n_q_heads) || meets(k, k_stride, H) || meets(v, v_stride, H))
     return fail(W12_ERR_INVALID_ARG, "tree_attn: out must not overlap q, k or v");
-  const AttnWs w = attn_ws(M, n_q_heads / H, D);
-  if (ws_bytes < w.total) return fail(W12_ERR_BUFFER_TOO_SMALL, "tree_attn: workspace %zu < %zu", ws_bytes, w.total);
   AttnArgs a{};
   a.q = q;
   a.k = k;
