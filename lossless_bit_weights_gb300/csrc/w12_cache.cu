@@ -206,35 +206,40 @@ struct WriteArgs {
   int32_t block_size, chunks, head_chunks;  // 16-byte chunks of a row and of a head
 };
 
-constexpr int kWriteThreads = 256;
+constexpr int kWriteThreads = 128;
 constexpr int kWriteTokens = 4;  // tokens of a block
 
-// A block copies four tokens of one layer, their slots and rows looked up together and four
-// 16-byte pieces a thread on their way.  Bound by bytes, read once and written once: 12289 tokens of
-// 8 heads of 128 (101 MB) in 21.6 us, 4.7 TB/s, 0.70 of the measured copy rate; one token a
-// block and one piece a thread took 28.
+// A block copies four tokens of one layer, a lane each for their slots and rows and four 16-byte
+// pieces a thread on their way.  Bound by bytes, read once and written once: 12289 tokens of
+// 8 heads of 128 (101 MB) in 17.6 us, 5.7 TB/s, 0.85 of the measured copy rate.  With every thread
+// dividing for all four tokens 21.4; with 256 threads 18.7, with 64 18.5, 512 27; two or
+// eight tokens a block 17.9 and 18.9.
 __global__ void __launch_bounds__(kWriteThreads) k_kv_write(const __grid_constant__ WriteArgs a) {
   pdl_enter();
   const int64_t l = blockIdx.y;
   const int per_token = 2 * a.chunks;
+  const int lane = threadIdx.x & 31;
   for (int64_t t0 = (int64_t)blockIdx.x * kWriteTokens; t0 < a.n; t0 += (int64_t)gridDim.x * kWriteTokens) {
-    int64_t from[kWriteTokens], to[kWriteTokens];  // first the row and the slot, then the token's place in the cache
-#pragma unroll
-    for (int k = 0; k < kWriteTokens; ++k) {
-      const int64_t t = t0 + k;
-      to[k] = t < a.n ? a.slot[t] : -1;
-      from[k] = t >= a.n ? -1 : a.src ? a.src[t] : t;
-    }
-#pragma unroll
-    for (int k = 0; k < kWriteTokens; ++k) {
-      if (to[k] == -1) continue;
-      if (to[k] < 0 || to[k] >= a.n_slots || from[k] < 0 || from[k] >= a.n_rows) {
-        if (threadIdx.x == 0) atomicOr(a.status, 1);
-        to[k] = -1;
-        continue;
+    // A lane finds one token's row and place in the cache (the division is long), and the warp shares them.
+    int64_t row = -1, place = -1;
+    if (lane < kWriteTokens && t0 + lane < a.n) {
+      place = a.slot[t0 + lane];
+      row = a.src ? a.src[t0 + lane] : t0 + lane;
+      if (place != -1) {
+        if (place < 0 || place >= a.n_slots || row < 0 || row >= a.n_rows) {
+          if (threadIdx.x < 32) atomicOr(a.status, 1);
+          place = -1;
+        } else {
+          const int64_t block = place / a.block_size;
+          place = l * a.layer_stride + block * a.block_stride + (place - block * a.block_size) * a.token_stride;
+        }
       }
-      const int64_t block = to[k] / a.block_size;
-      to[k] = l * a.layer_stride + block * a.block_stride + (to[k] - block * a.block_size) * a.token_stride;
+    }
+    int64_t from[kWriteTokens], to[kWriteTokens];
+#pragma unroll
+    for (int k = 0; k < kWriteTokens; ++k) {
+      from[k] = __shfl_sync(0xFFFFFFFFu, row, k);
+      to[k] = __shfl_sync(0xFFFFFFFFu, place, k);
     }
     for (int e = threadIdx.x; e < per_token; e += kWriteThreads) {
       const int kv = e >= a.chunks, c = e - kv * a.chunks, h = c / a.head_chunks;
