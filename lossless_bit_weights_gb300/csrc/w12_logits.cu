@@ -13,7 +13,7 @@
 // distinct tokens in a history, 87 % of all runs of 128 tokens hold one.)
 //
 // Bound by bytes, the logits read once (and written once where they are asked for): 192 rows of
-// 151936 tokens of 24 requests take 49 us with all rules (237 MB, 4.8 TB/s, 0.72 of the measured
+// 151936 tokens of 24 requests take 48 us with all rules (237 MB, 5.0 TB/s, 0.74 of the measured
 // copy rate), 37 us with the argmax and acceptance instead of the rows (117 MB, 3.2 TB/s).  What is
 // left is the making of the tables, during which a block streams nothing, the history and the
 // listed tokens (about 13, 4 and 5 us of the 37).  Instructions count as much as bytes: bounds
@@ -27,8 +27,8 @@
 namespace w12 {
 namespace {
 
-constexpr int kRuleThreads = 256;
-constexpr int kRuleWarps = kRuleThreads / 32;
+constexpr int kAcceptThreads = 512;
+constexpr int kAcceptWarps = kAcceptThreads / 32;
 constexpr int kRuleParts = 8;        // parts of a row's chunk, at most
 constexpr int kRuleMaxNodes = 1024;  // nodes of one request
 constexpr uint32_t kPromptFlag = 0x80000000u;
@@ -88,11 +88,12 @@ __device__ __forceinline__ float4 load4(const float* x, int i, int n, bool vec) 
   return f;
 }
 
-template <bool WRITE>
-__global__ void __launch_bounds__(kRuleThreads, 4) k_logit_rules(const __grid_constant__ RuleArgs a) {
+template <bool WRITE, int T>
+__global__ void __launch_bounds__(T, (1024 + T / 2) / T) k_logit_rules(const __grid_constant__ RuleArgs a) {
+  constexpr int kWarps = T / 32;
   pdl_enter();
   extern __shared__ __align__(16) uint32_t sm[];
-  __shared__ int s_listed[kRuleWarps], s_part[kRuleParts + 1];  // listed tokens: of a warp's words, before a part
+  __shared__ int s_listed[kWarps], s_part[kRuleParts + 1];  // listed tokens: of a warp's words, before a part
   const int r = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t v0 = (int64_t)blockIdx.x * a.chunk;
   const int width = (int)min((int64_t)a.chunk, a.V - v0);
@@ -118,7 +119,7 @@ __global__ void __launch_bounds__(kRuleThreads, 4) k_logit_rules(const __grid_co
   constexpr int H = 8;
   int32_t told[H];
   auto place = [&](int64_t j0, int k) {  // of told[k]
-    return a.hist_vec ? j0 + ((k >> 2) * kRuleThreads + tid) * 4 + (k & 3) : j0 + k * kRuleThreads + tid;
+    return a.hist_vec ? j0 + ((k >> 2) * T + tid) * 4 + (k & 3) : j0 + k * T + tid;
   };
   auto ask = [&](int64_t j0) {
     if (a.hist_vec) {
@@ -147,15 +148,15 @@ __global__ void __launch_bounds__(kRuleThreads, 4) k_logit_rules(const __grid_co
 
   // the rows' chunk comes into L2 while the tables are made
   if (a.vec)
-    for (int i = tid; i < n; i += kRuleThreads)
+    for (int i = tid; i < n; i += T)
       if (width >= 4) prefetch_l2(a.logits + (off + i) * a.stride + v0, (uint32_t)(width & ~3) * 4);
   const int zeros = (a.chunk / 32 + (count ? a.chunk : 0) + (bias ? a.chunk : 0)) / 4;  // bitmap and tables, one run
-  for (int i = tid; i < zeros; i += kRuleThreads) reinterpret_cast<uint4*>(bits)[i] = make_uint4(0, 0, 0, 0);
+  for (int i = tid; i < zeros; i += T) reinterpret_cast<uint4*>(bits)[i] = make_uint4(0, 0, 0, 0);
   if (!WRITE)
-    for (int i = tid; i < n; i += kRuleThreads) best[i] = 0;
+    for (int i = tid; i < n; i += T) best[i] = 0;
   bool ok = true;
   if (tree)
-    for (int i = tid; i < n; i += kRuleThreads) {
+    for (int i = tid; i < n; i += T) {
       const int32_t p = a.parent[off + i];
       ok = ok && (i == 0 ? p == -1 : p >= 0 && p < i);
       parent[i] = p;
@@ -164,11 +165,11 @@ __global__ void __launch_bounds__(kRuleThreads, 4) k_logit_rules(const __grid_co
   if (!__syncthreads_and(ok)) {
     if (tid == 0) atomicOr(a.status, kRuleBadRequest);
     if (!WRITE)  // no token: acceptance reports the tree as invalid
-      for (int i = tid; i < n; i += kRuleThreads) a.key[(off + i) * a.chunks + blockIdx.x] = 0;
+      for (int i = tid; i < n; i += T) a.key[(off + i) * a.chunks + blockIdx.x] = 0;
     return;
   }
   if (tid == 0 && (len != h_given || prompt < 0 || prompt > h_given)) atomicOr(a.status, kRuleClamped);
-  for (int64_t j0 = 0; j0 < len; j0 += H * kRuleThreads) {
+  for (int64_t j0 = 0; j0 < len; j0 += H * T) {
 #pragma unroll
     for (int k = 0; k < H; ++k) {
       // in 32 bits without a sign: a token below the chunk (or below zero) lands above its end
@@ -180,12 +181,12 @@ __global__ void __launch_bounds__(kRuleThreads, 4) k_logit_rules(const __grid_co
         atomicOr(&bits[i >> 5], 1u << (i & 31));
       }
     }
-    ask(j0 + H * kRuleThreads);
+    ask(j0 + H * T);
   }
   if (bias) {
     const int64_t b0 = min(max(b_given, (int64_t)0), a.r.n_bias), b1 = min(max(b_end, b0), a.r.n_bias);
     if (tid == 0 && (b0 != b_given || b1 != b_end)) atomicOr(a.status, kRuleClamped);
-    for (int64_t j = b0 + tid; j < b1; j += kRuleThreads) {
+    for (int64_t j = b0 + tid; j < b1; j += T) {
       const uint32_t i = (uint32_t)a.r.bias_tok[j] - (uint32_t)v0;
       if (i < (uint32_t)width) {
         atomicMax(&bias_at[i], (int32_t)j + 1);
@@ -194,7 +195,7 @@ __global__ void __launch_bounds__(kRuleThreads, 4) k_logit_rules(const __grid_co
     }
   }
   if (tree && count)
-    for (int i = tid; i < n; i += kRuleThreads) {
+    for (int i = tid; i < n; i += T) {
       int32_t p = i;
       while (p >= 0 && !(draft[p] >= v0 && draft[p] < v0 + width)) p = parent[p];
       up[i] = p;
@@ -216,7 +217,7 @@ __global__ void __launch_bounds__(kRuleThreads, 4) k_logit_rules(const __grid_co
   __syncthreads();
   int listed = 0;
   before -= __popc(mine);
-  for (int w = 0; w < kRuleWarps; ++w) {
+  for (int w = 0; w < kWarps; ++w) {
     if (w < warp) before += s_listed[w];
     listed += s_listed[w];
   }
@@ -227,7 +228,7 @@ __global__ void __launch_bounds__(kRuleThreads, 4) k_logit_rules(const __grid_co
   __syncthreads();
 
   // ---- a warp takes one part of one row's chunk at a time
-  for (int u = warp; u < n * a.parts; u += kRuleWarps) {
+  for (int u = warp; u < n * a.parts; u += kWarps) {
     const int node = u / a.parts, part = u - node * a.parts, c0 = part * part_len, c1 = min(width, c0 + part_len);
     const int64_t m = off + node;
     const float* x = a.logits + m * a.stride + v0;
@@ -346,12 +347,12 @@ __global__ void __launch_bounds__(kRuleThreads, 4) k_logit_rules(const __grid_co
   }
   if (!WRITE) {
     __syncthreads();
-    for (int i = tid; i < n; i += kRuleThreads) a.key[(off + i) * a.chunks + blockIdx.x] = best[i];
+    for (int i = tid; i < n; i += T) a.key[(off + i) * a.chunks + blockIdx.x] = best[i];
   }
 }
 
 // One block per request: the rows' tokens from their chunks' keys, then acceptance.
-__global__ void __launch_bounds__(kRuleThreads) k_rule_accept(const unsigned long long* __restrict__ key, int chunks,
+__global__ void __launch_bounds__(kAcceptThreads) k_rule_accept(const unsigned long long* __restrict__ key, int chunks,
                                                               const int32_t* __restrict__ parent_g,
                                                               const int32_t* __restrict__ draft_g,
                                                               const int32_t* __restrict__ offsets, int64_t M,
@@ -369,7 +370,7 @@ __global__ void __launch_bounds__(kRuleThreads) k_rule_accept(const unsigned lon
     return;
   }
   bool ok = true;
-  for (int i = tid; i < n; i += kRuleThreads) {
+  for (int i = tid; i < n; i += kAcceptThreads) {
     const int32_t p = parent_g[off + i];
     ok = ok && (i == 0 ? p == -1 : p >= 0 && p < i);
     parent[i] = p;
@@ -378,7 +379,7 @@ __global__ void __launch_bounds__(kRuleThreads) k_rule_accept(const unsigned lon
   }
   if (tid == 0) s_best = 0;
   ok = __syncthreads_and(ok) != 0;
-  for (int i = warp; i < n; i += kRuleWarps) {
+  for (int i = warp; i < n; i += kAcceptWarps) {
     unsigned long long top = 0;
     const unsigned long long* k = key + (off + i) * chunks;
     for (int c = lane; c < chunks; c += 32) top = k[c] > top ? k[c] : top;
@@ -394,7 +395,7 @@ __global__ void __launch_bounds__(kRuleThreads) k_rule_accept(const unsigned lon
   }
   __syncthreads();
   // every node walks its own path; the deepest accepted one wins, the lowest index among equals
-  for (int i = tid; i < n; i += kRuleThreads) {
+  for (int i = tid; i < n; i += kAcceptThreads) {
     int32_t depth = 0, p = i;
     bool taken = true;
     while (p > 0 && taken) {
@@ -419,16 +420,20 @@ __global__ void __launch_bounds__(kRuleThreads) k_rule_accept(const unsigned lon
 }
 
 struct RulePlan {
-  int chunk, chunks, parts;
+  int chunk, chunks, parts, threads;
 };
 
 // Chunk of the vocabulary per block, a multiple of 256: the larger it is, the fewer blocks
 // scan a request's history and the more rows share the table; the smaller, the more blocks
-// there are.  The largest of 4096, 2048, 1024 with at least two blocks per SM: 192 rows took 50 us
+// there are.  The largest of 4096, 2048, 1024 with at least two blocks per SM, at 256 threads: 192 rows took 50 us
 // written and 37 verified at 4096, 48 and 44 at 2048; a 16-node tree 15.5 at 1024, 15.8 at 512.
 // Parts of a row's chunk, one a warp at a time: smaller ones even out trees of unequal size, larger ones
 // meet fewer loads' latencies (24 trees of 8 rows: 52 and 36 us at 1 part, 50 and 37 at 2, 51 and
 // 44 at 4, written and verified; a 16-node tree 15.6 at 1, 20.6 at 2).
+// Threads: one row has eight parts, so eight warps (5.4 us, 5.8 at 384 threads, 5.9 at 512); where
+// every block has an SM's half to itself, 512 make its tables and sixteen rows at once (a 16-node tree
+// 12.0 us, 15.5 at 384, 15.7 at 256); else 384 (192 rows written 47.7 us, 49.4 at 256, 49.0 at 512;
+// verified 37.0, 37.0, 41.0).
 RulePlan rule_plan(int64_t M, int64_t V, int32_t n_req) {
   RulePlan p{};
   for (p.chunk = 4096; p.chunk > 1024; p.chunk /= 2)
@@ -436,6 +441,7 @@ RulePlan rule_plan(int64_t M, int64_t V, int32_t n_req) {
   p.chunks = (int)((V + p.chunk - 1) / p.chunk);
   const int64_t rows = (M + n_req - 1) / n_req;
   p.parts = rows >= 16 ? 1 : rows >= 8 ? 2 : rows >= 4 ? 4 : kRuleParts;
+  p.threads = M <= n_req ? 256 : (int64_t)p.chunks * n_req <= 304 ? 512 : 384;
   return p;
 }
 
@@ -458,6 +464,10 @@ int check_rules(const float* logits, int64_t stride, int64_t M, int64_t V, const
     return fail(W12_ERR_SHAPE, "%s: mask_stride=%lld is less than a row's words", fn, (long long)rules->mask_stride);
   return W12_OK;
 }
+
+void (*const kRuleKernels[6])(RuleArgs) = {  // 256, 384 and 512 threads; verified, written
+    k_logit_rules<false, 256>, k_logit_rules<false, 384>, k_logit_rules<false, 512>,
+    k_logit_rules<true, 256>,  k_logit_rules<true, 384>,  k_logit_rules<true, 512>};
 
 int launch_rules(const float* logits, int64_t stride, int64_t M, int64_t V, const logit_rules* rules,
                  const int32_t* parent, const int32_t* draft, const int32_t* req_offsets, int32_t n_req, float* out,
@@ -489,14 +499,14 @@ int launch_rules(const float* logits, int64_t stride, int64_t M, int64_t V, cons
   int dev = 0;
   W12_CUDA_TRY(cudaGetDevice(&dev));
   if (dev >= 64 || !configured[dev]) {
-    W12_CUDA_TRY(cudaFuncSetAttribute(k_logit_rules<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most));
-    W12_CUDA_TRY(cudaFuncSetAttribute(k_logit_rules<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most));
+    for (auto kernel : kRuleKernels)
+      W12_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most));
     if (dev < 64) configured[dev] = 1;
   }
   a.vec = ((stride | (out ? out_stride : 0)) & 3) == 0 && (((uintptr_t)logits | (uintptr_t)out) & 15u) == 0;
   a.hist_vec = rules->hist && (rules->hist_stride & 3) == 0 && ((uintptr_t)rules->hist & 15u) == 0;
   const dim3 grid((unsigned)p.chunks, (unsigned)n_req);
-  W12_CUDA_TRY(launch_dependent(key ? k_logit_rules<false> : k_logit_rules<true>, grid, kRuleThreads, smem, s, a));
+  W12_CUDA_TRY(launch_dependent(kRuleKernels[(key ? 0 : 3) + p.threads / 128 - 2], grid, p.threads, smem, s, a));
   W12_LAUNCH_CHECK(what);
   return W12_OK;
 }
@@ -547,7 +557,7 @@ int logits_verify(const float* logits, int64_t stride, int64_t M, int64_t V, con
   st = launch_rules(logits, stride, M, V, rules, parent, draft, req_offsets, n_req, nullptr, 0, status, key,
                     (cudaStream_t)stream, "logits_verify: rules kernel");
   if (st) return st;
-  W12_CUDA_TRY(launch_dependent(k_rule_accept, dim3((unsigned)n_req), kRuleThreads, 0, (cudaStream_t)stream, key,
+  W12_CUDA_TRY(launch_dependent(k_rule_accept, dim3((unsigned)n_req), kAcceptThreads, 0, (cudaStream_t)stream, key,
                                 rule_plan(M, V, n_req).chunks, parent, draft, req_offsets, M, tok, path_len, path_nodes, bonus));
   W12_LAUNCH_CHECK("logits_verify: acceptance kernel");
   return W12_OK;
