@@ -14,7 +14,7 @@ constexpr int kSlotThreads = 256;
 constexpr int kSlotMaxReq = 4096;
 constexpr int64_t kMaxBlock = 1 << 24;  // block_size and table_width
 
-constexpr int32_t kSlotBadRequest = 1, kSlotNoBlocks = 2, kSlotCapacity = 4, kSlotBadPath = 8;
+constexpr int32_t kSlotBadRequest = 1, kSlotNoBlocks = 2, kSlotCapacity = 4, kSlotBadEntry = 8;
 
 struct SlotArgs {
   const int32_t *cache_len, *add, *path_nodes, *req_offsets;
@@ -167,7 +167,8 @@ __global__ void __launch_bounds__(kSlotThreads) k_kv_slots(const __grid_constant
       const int32_t have = (len + bs - 1) / bs, b = p / bs;
       const int32_t id = b < have ? a.table[r * a.table_stride + b]
                                   : a.pool[(head + pre_new[r] + (b - have)) % a.n_blocks];
-      slot = (int64_t)id * bs + (p - b * bs);
+      slot = id < 0 ? -2 : (int64_t)id * bs + (p - b * bs);  // (-1 would be passed over)
+      if (id < 0) atomicOr(a.status, kSlotBadEntry);
       src = (int32_t)t;
       if (a.path_nodes) {
         const int32_t off = a.req_offsets ? a.req_offsets[r] : 0;
@@ -175,7 +176,7 @@ __global__ void __launch_bounds__(kSlotThreads) k_kv_slots(const __grid_constant
         const int32_t node = a.path_nodes[off + j];
         const bool in = node >= 0 && node < stop - off;
         src = in ? off + node : -1;
-        if (!in) atomicOr(a.status, kSlotBadPath);
+        if (!in) atomicOr(a.status, kSlotBadEntry);
       }
     }
     a.slot[t] = slot;

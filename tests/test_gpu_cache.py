@@ -171,6 +171,20 @@ def test_a_path_node_outside_its_request(w12):
     assert int(out.total) == 4
 
 
+@pytest.mark.parametrize("where", ["table", "pool"])
+def test_a_negative_entry_does_not_pass_for_padding(w12, where):
+    """-1 times the block size plus the last place of a block is -1, kv_slots' own padding."""
+    table, ring, pos = i32([[0, 1, 2]]), i32([3, 4, 5, 6]), i64([0, 3])
+    if where == "table":
+        table[0, 1] = -1  # positions 4 to 7
+    else:
+        ring[0] = -1      # positions 8 to 11 (two blocks are held)
+    out = w12.kv_slots(i32([5]), i32([7]), table, ring, pos, 4, 9)
+    want = [-2] * 3 + [12, 13, 14, 15] if where == "table" else [5, 6, 7] + [-2] * 4
+    assert out.slot.tolist() == want + [-1] * 2
+    assert int(out.status) == 8 and int(out.total) == 7
+
+
 def test_slot_refusals(w12):
     table, ring, pos = Pool(np.random.default_rng(6), [4, 4], 16, 4, 3).device()
     lens, add = i32([4, 4]), i32([1, 1])
