@@ -138,8 +138,8 @@ def generate(target: Target, prompts: list[list[int]], steps: int, block: int = 
         for r, t in enumerate(texts):  # the text before the root
             hist[r, :len(t) - 1] = i32(t[:-1])
         hist_len = i32([len(t) - 1 for t in texts])
-        rules = w12.LogitRules(hist=hist, hist_len=hist_len, prompt_len=torch.minimum(prompt_len, hist_len), repetition=rep,
-                               frequency=freq, presence=pres, bias=more, mask=allowed.expand(M, words).contiguous())
+        rules = w12.LogitRules(hist=hist, hist_len=hist_len, prompt_len=prompt_len, repetition=rep, frequency=freq,
+                               presence=pres, bias=more, mask=allowed.expand(M, words).contiguous())
         logits, k, v = target.forward(draft, cache, table, length, parent, off, status)
         _, path_len, path, bonus, _ = w12.logits_verify(logits, rules, parent, draft, off, ws=ws, status=status)
         commit(k, v, path_len, path, off, M)

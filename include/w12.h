@@ -580,14 +580,17 @@ W12_API int tree_attn_set_wait_limit(int64_t cycles);
  * pointers; NULL leaves a rule out.
  *   hist      request r's tokens are hist[r*hist_stride + i], i < hist_len[r], of which the
  *             first prompt_len[r] (NULL: 0) are its prompt.  They end before the
- *             root of its tree.
+ *             root of its tree.  Where the root itself is the prompt's last token (a
+ *             request's first step, nothing generated yet), prompt_len[r] is
+ *             hist_len[r] + 1.
  *   rep, freq, pres   n_req factors each.
  *   bias_off[n_req+1], bias_tok, bias_val[n_bias]   request r's entries
  *             bias_off[r] .. bias_off[r+1]-1; the last entry of a token counts.
  *   mask      row m allows token v if bit v%32 of mask[m*mask_stride + v/32] is set.
  * For row m of request r and token v, with count = occurrences of v behind the
- * prompt plus those among the drafted tokens from the root to the node, and seen = count >
- * 0 or v is in the prompt (float arithmetic, each step rounded):
+ * prompt plus those among the drafted tokens from the root to the node (a root that belongs to
+ * the prompt left out), and seen = count > 0 or v is in the prompt (float arithmetic, each step
+ * rounded):
  *   x = logits[m, v];  if seen: x = x > 0 ? x / rep : x * rep;
  *   x = x - freq * count;  if count > 0: x = x - pres;  x = x + bias[v];
  *   x = -inf if v is not allowed.

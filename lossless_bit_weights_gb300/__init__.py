@@ -789,7 +789,8 @@ def tree_attn_set_wait_limit(cycles: int) -> None:
 
 class LogitRules:
     """Rules on logits (include/w12.h, logit_rules); the tensors stay the caller's and may change
-    between calls.  hist [n_req, capacity] int32 with hist_len and prompt_len [n_req] int32;
+    between calls.  hist [n_req, capacity] int32 with hist_len and prompt_len [n_req] int32 (hist_len + 1
+    where the tree's root is the prompt's last token: a request's first step);
     repetition, frequency, presence [n_req] float32; bias: (offsets [n_req + 1], tokens, values);
     mask [M, words] int32, bit v%32 of word v/32 set where token v is allowed."""
 

@@ -113,6 +113,7 @@ __global__ void __launch_bounds__(T, (1024 + T / 2) / T) k_logit_rules(const __g
   const int64_t prompt = count && a.r.hist && a.r.prompt_len ? a.r.prompt_len[r] : 0;
   const int64_t b_given = bias ? a.r.bias_off[r] : 0, b_end = bias ? a.r.bias_off[r + 1] : 0;
   const int64_t len = min(max(h_given, (int64_t)0), a.r.hist_stride);
+  const bool root_read = tree && prompt > len;  // the root, behind the history, is the prompt's last token
   const int32_t* h = a.r.hist + r * a.r.hist_stride;
   // tokens of the history that a thread has on their way (four adjacent ones at a time where the rows
   // allow it), the first ones from here on
@@ -168,7 +169,7 @@ __global__ void __launch_bounds__(T, (1024 + T / 2) / T) k_logit_rules(const __g
       for (int i = tid; i < n; i += T) a.key[(off + i) * a.chunks + blockIdx.x] = 0;
     return;
   }
-  if (tid == 0 && (len != h_given || prompt < 0 || prompt > h_given)) atomicOr(a.status, kRuleClamped);
+  if (tid == 0 && (len != h_given || prompt < 0 || prompt > h_given + tree)) atomicOr(a.status, kRuleClamped);
   for (int64_t j0 = 0; j0 < len; j0 += H * T) {
 #pragma unroll
     for (int k = 0; k < H; ++k) {
@@ -322,7 +323,7 @@ __global__ void __launch_bounds__(T, (1024 + T / 2) / T) k_logit_rules(const __g
         uint32_t c = count ? cnt[i] : 0u;
         if (tree && count)
           for (int32_t p = up[node]; p >= 0;) {
-            if (draft[p] == (int32_t)(v0 + i)) ++c;
+            if (draft[p] == (int32_t)(v0 + i)) c = p == 0 && root_read ? c | kPromptFlag : c + 1;
             p = parent[p] >= 0 ? up[parent[p]] : -1;
           }
         const uint32_t times = c & ~kPromptFlag;

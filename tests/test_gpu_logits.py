@@ -404,3 +404,50 @@ def test_refusals(w12):
         w12.LogitRules(hist=i32([[1, 2]]))
     with pytest.raises(ValueError):
         w12.LogitRules(repetition=f32([1.0]), presence=f32([1.0, 2.0]))
+
+
+@pytest.mark.parametrize("n", [1, 2, 60])
+@pytest.mark.parametrize("V", [40, 9000])
+def test_a_root_that_ends_the_prompt_is_no_output(w12, n, V):
+    """A request's first step: the root is its prompt's last token (prompt_len = hist_len + 1), of which
+    nothing has been generated.  The root's row is then that of a call without a tree on the whole
+    prompt; below the root, only drafted tokens count."""
+    rng = np.random.default_rng(n * V)
+    prompt = rng.integers(0, min(V, 7), n).astype(np.int32)       # tokens repeat
+    draft = np.concatenate([prompt[-1:], [prompt[-1], prompt[0], 3, prompt[-1]]]).astype(np.int32)
+    parent = [-1, 0, 0, 1, 3]
+    x = (rng.standard_normal((5, V)) * 3).astype(np.float32)
+    x[:, :7] += 30.0                                              # the prompt's tokens are the best
+    rep, freq, pres = np.float32(1.3), np.float32(4.0), np.float32(8.0)
+    pen = dict(repetition=f32([rep]), frequency=f32([freq]), presence=f32([pres]))
+    hist = i32(np.concatenate([prompt, [0]])[None])
+    first = w12.LogitRules(hist=hist, hist_len=i32([n - 1]), prompt_len=i32([n]), **pen)
+    whole = w12.LogitRules(hist=hist, hist_len=i32([n]), prompt_len=i32([n]), **pen)
+    want = np.empty_like(x)
+    for m in range(5):
+        seen, count, p = np.isin(np.arange(V), prompt), np.zeros(V, np.float32), m
+        while p > 0:
+            count[draft[p]] += 1
+            p = parent[p]
+        seen |= count > 0
+        y = np.where(seen, np.where(x[m] > 0, x[m] / rep, x[m] * rep), x[m])
+        y = np.where(count > 0, y - freq * count, y)
+        want[m] = np.where(count > 0, y - pres, y)
+    out, st = w12.logits_process(f32(x), first, i32(parent), i32(draft))
+    assert int(st) == 0
+    alone, _ = w12.logits_process(f32(x[:1]), whole)
+    assert torch.equal(out[:1], alone)
+    assert np.array_equal(out.cpu().numpy(), want)
+    tok, path_len, _, bonus, st = w12.logits_verify(f32(x), first, i32(parent), i32(draft))
+    assert int(st) == 0 and tok.tolist() == want.argmax(1).tolist()
+    length, _, last = oracle.accept(want.argmax(1).astype(np.int32), np.asarray(parent, np.int32), draft)
+    assert int(path_len) == length and int(bonus) == last
+
+
+def test_a_prompt_ends_at_the_root(w12):
+    """One token more than the history and the root is out of range, as is one more than the history without a tree."""
+    hist, x = i32([[1, 2, 3, 4]]), torch.zeros((1, 50), device="cuda")
+    for prompt, tree, want in ((4, True, 0), (5, True, 2), (3, False, 0), (4, False, 2)):
+        rules = w12.LogitRules(hist=hist, hist_len=i32([3]), prompt_len=i32([prompt]), frequency=f32([1.0]))
+        _, st = w12.logits_process(x, rules, *([i32([-1]), i32([4])] if tree else []))
+        assert int(st) == want, (prompt, tree)

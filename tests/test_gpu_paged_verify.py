@@ -82,3 +82,11 @@ def test_drafts_are_accepted(ex):
     """Without penalties a text soon repeats itself; its own continuations are then right."""
     res = ex.generate(ex.Target(), [[7, 8, 9], [500] * 40], 30, penalties=(1.0, 0.0, 0.0))
     assert res.accepted > 0.3
+
+
+def test_the_prompt_is_not_penalised_as_output(ex):
+    """A token with a large bias is the first one generated although the prompt ends with it, and not the
+    second, which is penalised for the first."""
+    res = ex.generate(ex.Target(), [[50], [3, 50], [50, 7, 50]], 2, penalties=(1.0, 15.0, 15.0), banned=50, bias=20.0)
+    for r, text in enumerate(res.texts):
+        assert text[res.prompts[r]] == 50 and text[res.prompts[r] + 1] != 50
