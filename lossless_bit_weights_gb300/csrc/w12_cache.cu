@@ -327,14 +327,13 @@ int kv_slots(const int32_t* cache_len, const int32_t* add, int32_t extra, int32_
   a.n_req = n_req;
   a.block_size = (int32_t)block_size;
   const size_t smem = (size_t)(n_req + 1) * 3 * 4;
-  if (smem > 48 * 1024) {
-    static int configured[64] = {0};
-    int dev = 0;
-    W12_CUDA_TRY(cudaGetDevice(&dev));
-    if (dev >= 64 || !configured[dev]) {
-      W12_CUDA_TRY(cudaFuncSetAttribute(k_kv_slots, cudaFuncAttributeMaxDynamicSharedMemorySize, (kSlotMaxReq + 1) * 12));
-      if (dev < 64) configured[dev] = 1;
-    }
+  // (asked for whatever this call's size: the 48 KB that need no asking hold the kernel's static arrays too)
+  static int configured[64] = {0};
+  int dev = 0;
+  W12_CUDA_TRY(cudaGetDevice(&dev));
+  if (dev >= 64 || !configured[dev]) {
+    W12_CUDA_TRY(cudaFuncSetAttribute(k_kv_slots, cudaFuncAttributeMaxDynamicSharedMemorySize, (kSlotMaxReq + 1) * 12));
+    if (dev < 64) configured[dev] = 1;
   }
   const int64_t blocks = (capacity + kSlotThreads - 1) / kSlotThreads;
   W12_CUDA_TRY(launch_dependent(k_kv_slots, dim3((unsigned)(blocks < 608 ? blocks : 608)), kSlotThreads, smem, (cudaStream_t)stream, a));

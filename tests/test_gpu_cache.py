@@ -1,10 +1,15 @@
 """kv_slots and kv_write against plain host models: whole numbers and copies, so equal."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 
 torch = pytest.importorskip("torch")
 
 pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture(scope="module")
@@ -288,3 +293,24 @@ def test_write_refusals(w12):
     with pytest.raises(w12.W12Error) as e:               # rows at 8 bytes
         w12.kv_write(cache, flat[4:].view(3, 2, 64), k, i64([0]))
     assert e.value.status == 1
+
+
+# ---------------------------------------------------------------- slots again
+
+_MANY = """
+import sys, torch
+import lossless_bit_weights_gb300 as w12
+i32 = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")
+n = int(sys.argv[1])
+table, pool = torch.zeros((n, 1), dtype=torch.int32, device="cuda"), torch.arange(n, dtype=torch.int32, device="cuda")
+pos = torch.tensor([0, n], dtype=torch.int64, device="cuda")
+out = w12.kv_slots(i32([0] * n), i32([1] * n), table, pool, pos, 4, n)
+assert int(out.status) == 0 and out.slot.tolist() == [4 * i for i in range(n)] and out.new_len.tolist() == [1] * n
+"""
+
+
+@pytest.mark.parametrize("n_req", [4079, 4080, 4095, 4096])
+def test_any_number_of_requests_as_a_process_s_first_call(w12, n_req):
+    """Shared memory beside the prefix sums counts too; a call of more requests before must not matter."""
+    r = subprocess.run([sys.executable, "-c", _MANY, str(n_req)], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
