@@ -536,6 +536,11 @@ __device__ bool produce(const AttnArgs& a, const CUtensorMap* k_map, const CUten
       const uint32_t slot = entry % P::kSlots, round = entry / P::kSlots;
       if (round > 0 && !wait_warp(s.empty + 8 * slot, (round - 1) & 1, s)) return false;
       const uint32_t dst = s.base + P::kRing + slot * P::kSlotBytes;
+      // Before the arrivals of the part's last entry, behind which the softmax reads it.
+      if (item == 2 * cnt - 1 && bad_block) {
+        atomicOr(bad, kAttnBadBlock);
+        __threadfence_block();
+      }
       if (by_box) {
         const uint32_t bar = s.full + 8 * slot;
         if (my_slab < D / 64) {
@@ -598,7 +603,6 @@ __device__ bool produce(const AttnArgs& a, const CUtensorMap* k_map, const CUten
         mbar_arrive(s.meta + 8 * ring);
         cp_arrive(s.q_full);
       }
-      if (item == 2 * cnt - 1 && bad_block) atomicOr(bad, kAttnBadBlock);
       if (by_box) {  // (its arrivals went with the boxes)
       } else if (tail && is_v) {
         // A tile with drafted nodes: an infinity or a NaN in a node's V would reach every row

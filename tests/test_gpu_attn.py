@@ -465,3 +465,27 @@ def test_refusals(w12):
         call(torch.zeros((5, 4, 96), dtype=torch.int16, device="cuda"), *[torch.zeros((5, 2, 96), dtype=torch.int16, device="cuda")] * 2,
              w12.KVCache(odd, odd), table, lens, parent, off)
     assert e.value.status == 2
+
+
+@pytest.mark.parametrize("d,block", [(64, 16), (128, 32), (256, 64), (128, 24)])
+def test_a_bad_block_anywhere_in_a_long_request(w12, d, block):
+    """The request is split among many blocks of the grid, whose parts end in tiles of cached tokens: each of
+    them has to tell what it met before its results are used."""
+    lens, counts = [90, 20000, 40], [3, 4, 2]
+    p = Problem(24, lens, counts, 2, 2, d, block)
+    args, ws = list(p.args(w12)), w12.Workspace()
+    good, last = args[4], -(-lens[1] // block) - 1
+    rng = np.random.default_rng(d)
+    for at in [0, 1, last - 1, last] + rng.integers(0, last, 60).tolist():
+        for value in (-1, p.kc.shape[1], 2 ** 31 - 1):
+            args[4] = good.clone()
+            args[4][1, at] = value
+            out = torch.full(args[0].shape, 0x1234, dtype=torch.int16, device="cuda")
+            _, st = w12.tree_attn(*args, out=out, ws=ws)
+            assert int(st) == 2, (at, value)
+            assert (out[p.off[1]:p.off[2]] == 0x1234).all(), (at, value)
+    p.check(out, [0, 2])
+    args[4] = good
+    out, st = w12.tree_attn(*args, ws=ws)
+    assert int(st) == 0
+    p.check(out)
