@@ -703,10 +703,12 @@ __device__ bool issue_scores(const AttnArgs& a, const Shared& s, Walk<D> walk, u
       for (int ks = 0; ks < D / 16; ++ks)
         umma_ss(d, umma_desc(q_addr + (ks >> 2) * 16384 + (ks & 3) * 32),
                 umma_desc(k_addr + (ks >> 2) * (P::kBK * 128) + (ks & 3) * 32), kId, ks > 0);
+      // The last unit's end is waited for before this unit's last scores are handed over: without them this
+      // unit cannot end, so its end is never taken for the last one's.  (The products are on their way.)
+      if (x == steps - 1 && !ended && !wait_warp(s.unit_end, (unit - 1) & 1, s)) return false;
       umma_commit_one(s.s_full + 8 * at.b);
       if (!two || row_tile) umma_commit_one(s.empty + 8 * slot);
     }
-    if (!ended && !wait_warp(s.unit_end, (unit - 1) & 1, s)) return false;
     umma_commit_one(s.q_free);  // (not before the last unit's end: its tree goes with the query rows)
     entry += 2 * cnt;
   }
