@@ -1022,6 +1022,7 @@ __global__ void __launch_bounds__(AttnPlan<D>::kThreads, 1) k_tree_attn(const __
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(s.base + P::kMisc) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  if (a.n_req > 32) fence_proxy_async_smem();  // the schedule's sums stood where boxes will land
   tc_fence_before();
   __syncthreads();
   tc_fence_after();

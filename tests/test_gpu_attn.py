@@ -489,3 +489,18 @@ def test_a_bad_block_anywhere_in_a_long_request(w12, d, block):
     out, st = w12.tree_attn(*args, ws=ws)
     assert int(st) == 0
     p.check(out)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("n_req", [32, 33, 460])
+def test_long_requests_beyond_a_warp_s_schedule(w12, d, n_req):
+    """Above 32 requests the schedule's sums stand in the ring, whose first tiles land there by boxes."""
+    lens = [512 if r % 7 else 2000 for r in range(n_req)]
+    p = Problem(n_req, lens, [1 + r % 3 for r in range(n_req)], 1, 2, d, 64)
+    args, ws = p.args(w12), w12.Workspace()
+    out, st = w12.tree_attn(*args, ws=ws)
+    p.check(out)
+    assert int(st) == 0
+    for _ in range(20):
+        again, _ = w12.tree_attn(*args, ws=ws)
+        assert torch.equal(out, again)
