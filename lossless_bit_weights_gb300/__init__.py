@@ -311,7 +311,7 @@ class Workspace:
     def __init__(self, device=None):
         self.device = device or torch.device("cuda")
         self.buf = torch.zeros(256, dtype=torch.uint8, device=self.device)
-        self._scratch, self._scratch_stream = None, 0
+        self._scratch: dict[int, torch.Tensor] = {}  # by stream handle
 
     def get(self, nbytes: int) -> torch.Tensor:
         if nbytes > self.buf.numel():
@@ -319,15 +319,13 @@ class Workspace:
         return self.buf
 
     def scratch(self, nbytes: int, stream, raw: int) -> torch.Tensor:
-        """A buffer for the calls on `stream` (its handle `raw`; None: the current one) whose
+        """The buffer of the calls on `stream` (its handle `raw`; None: the current one) whose
         workspace needs no initial state, apart from get()'s: what they leave in it must not
-        stand where a GEMM expects its counters at zero."""
-        t = self._scratch
+        stand where a GEMM expects its counters at zero.  Every stream has its own, so calls on
+        streams that do not wait for one another do not meet in it."""
+        t = self._scratch.get(raw)
         if t is None or nbytes > t.numel():
-            t = self._scratch = _empty(max(int(nbytes), 256), torch.uint8, self.device, stream)
-            self._scratch_stream = raw
-        if raw != self._scratch_stream:  # not to be reused while that stream still works on it
-            t.record_stream(torch.cuda.current_stream() if stream is None else stream)
+            t = self._scratch[raw] = _empty(max(int(nbytes), 256), torch.uint8, self.device, stream)
         return t
 
     def status(self, stream=None) -> int:

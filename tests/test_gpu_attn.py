@@ -504,3 +504,22 @@ def test_long_requests_beyond_a_warp_s_schedule(w12, d, n_req):
     for _ in range(20):
         again, _ = w12.tree_attn(*args, ws=ws)
         assert torch.equal(out, again)
+
+
+def test_one_workspace_on_two_streams_at_once(w12):
+    """Calls on streams that do not wait for one another, over and over: each gives what it gives alone."""
+    ws = w12.Workspace()
+    ps = [Problem(25, [9000, 400], [30, 4], 2, 5, 128, 16), Problem(26, [7000], [16], 2, 5, 128, 16)]
+    args = [p.args(w12) for p in ps]
+    want = [w12.tree_attn(*a)[0] for a in args]
+    streams = [torch.cuda.Stream() for _ in ps]
+    outs = [[torch.empty_like(x) for _ in range(40)] for x in want]
+    status = [torch.zeros(1, dtype=torch.int32, device="cuda") for _ in ps]
+    torch.cuda.synchronize()
+    for i in range(40):
+        for s, a, o, st in zip(streams, args, outs, status):
+            w12.tree_attn(*a, out=o[i], ws=ws, status=st, stream=s)
+    torch.cuda.synchronize()
+    for p, x, o, st in zip(ps, want, outs, status):
+        p.check(x)
+        assert int(st) == 0 and all(torch.equal(x, y) for y in o)
