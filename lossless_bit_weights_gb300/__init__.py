@@ -312,6 +312,7 @@ class Workspace:
         self.device = device or torch.device("cuda")
         self.buf = torch.zeros(256, dtype=torch.uint8, device=self.device)
         self._scratch: dict[int, torch.Tensor] = {}  # by stream handle
+        self._outgrown: list[torch.Tensor] = []
 
     def get(self, nbytes: int) -> torch.Tensor:
         if nbytes > self.buf.numel():
@@ -322,10 +323,17 @@ class Workspace:
         """The buffer of the calls on `stream` (its handle `raw`; None: the current one) whose
         workspace needs no initial state, apart from get()'s: what they leave in it must not
         stand where a GEMM expects its counters at zero.  Every stream has its own, so calls on
-        streams that do not wait for one another do not meet in it."""
+        streams that do not wait for one another do not meet in it.  A CUDA graph keeps a buffer's
+        address: outgrown buffers live as long as the Workspace, which has to live as long as the
+        graph (buffers at least double, so all of them together are less than twice the last).
+        Graphs captured with one Workspace on one stream share its buffer: replay them in turn."""
         t = self._scratch.get(raw)
         if t is None or nbytes > t.numel():
-            t = self._scratch[raw] = _empty(max(int(nbytes), 256), torch.uint8, self.device, stream)
+            size = 256
+            if t is not None:
+                self._outgrown.append(t)
+                size = 2 * t.numel()
+            t = self._scratch[raw] = _empty(max(int(nbytes), size), torch.uint8, self.device, stream)
         return t
 
     def status(self, stream=None) -> int:

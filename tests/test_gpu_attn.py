@@ -523,3 +523,29 @@ def test_one_workspace_on_two_streams_at_once(w12):
     for p, x, o, st in zip(ps, want, outs, status):
         p.check(x)
         assert int(st) == 0 and all(torch.equal(x, y) for y in o)
+
+
+def test_a_graph_after_a_larger_call(w12):
+    """A capture on a stream that has called before, then a larger call on that stream: replays still find
+    their buffer, and nothing else is found changed by them."""
+    p, big = Problem(27, [9000, 5], [9, 3], 2, 5, 128, 16), Problem(28, [9000], [200], 2, 8, 128, 16)
+    args, ws, s = p.args(w12), w12.Workspace(), torch.cuda.Stream()
+    st, out = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.empty_like(args[0], memory_format=torch.contiguous_format)
+    torch.cuda.synchronize()
+    w12.tree_attn(*args, out=out, ws=ws, status=st, stream=s)
+    torch.cuda.synchronize()
+    want = out.clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        w12.tree_attn(*args, out=out, ws=ws, status=st)
+    x, _ = w12.tree_attn(*big.args(w12), ws=ws, stream=s)
+    torch.cuda.synchronize()
+    big.check(x)
+    with torch.cuda.stream(s):
+        fresh = [torch.full((1 << 20,), 7, dtype=torch.int32, device="cuda") for _ in range(64)]  # where a freed buffer stood
+    torch.cuda.synchronize()
+    out.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert int(st) == 0 and torch.equal(out, want)
+    assert all((t == 7).all() for t in fresh)
