@@ -519,9 +519,10 @@ typedef struct kv_cache {
  * new_len = cache_len and pool_pos_out = pool_pos.  A path node outside its request
  * gives its token src -1, a negative table or pool entry gives the tokens in it slot -2; kv_write
  * refuses both, and bit 3 is set.  *status (device int32) is zeroed by the caller.
- * Asynchronous; allocates nothing.  Errors: W12_ERR_INVALID_ARG (null pointer,
- * pool_pos_out = pool_pos, new_len = cache_len), W12_ERR_SHAPE (n_req outside 1..4096, block_size or table_width
- * outside 1..2^24, n_blocks outside 1..2^31-1, capacity outside 1..2^31-1). */
+ * Asynchronous; allocates nothing.  Errors: W12_ERR_INVALID_ARG (null pointer; results that
+ * overlap one another or what the call reads, as pool_pos_out = pool_pos or new_len = add), W12_ERR_SHAPE
+ * (n_req outside 1..4096, block_size or table_width outside 1..2^24, n_blocks outside 1..2^31-1,
+ * capacity outside 1..2^31-1). */
 W12_API int kv_slots(const int32_t* cache_len, const int32_t* add, int32_t extra, int32_t n_req, int32_t* table,
                      int64_t table_stride, int64_t table_width, int32_t* pool, int64_t n_blocks,
                      const int64_t* pool_pos, int64_t block_size, const int32_t* path_nodes,

@@ -304,6 +304,24 @@ int kv_slots(const int32_t* cache_len, const int32_t* add, int32_t extra, int32_
     return fail(W12_ERR_SHAPE, "kv_slots: n_nodes=%lld out of range", (long long)n_nodes);
   if (path_nodes && !req_offsets && n_req != 1)
     return fail(W12_ERR_INVALID_ARG, "kv_slots: req_offsets is null but n_req=%d", n_req);
+  // Some blocks write their results while others still read.
+  struct Range {
+    uintptr_t from, bytes;
+  };
+  auto range = [](const void* p, int64_t n, int size) { return Range{(uintptr_t)p, p ? (uintptr_t)n * size : 0}; };
+  const Range out[] = {range(slot, capacity, 8), range(src, capacity, 4), range(new_len, n_req, 4),
+                       range(pool_pos_out, 2, 8), range(total, 1, 8), range(status, 1, 4)};
+  const Range used[] = {range(cache_len, n_req, 4), range(add, n_req, 4),
+                        range(table, (n_req - 1) * table_stride + table_width, 4), range(pool, n_blocks, 4),
+                        range(pool_pos, 2, 8), range(path_nodes, n_nodes, 4),
+                        range(path_nodes ? req_offsets : nullptr, n_req + 1, 4)};
+  auto meet = [](const Range& x, const Range& y) { return x.from < y.from + y.bytes && y.from < x.from + x.bytes; };
+  for (const Range& o : out) {
+    bool bad = false;
+    for (const Range& u : used) bad = bad || meet(o, u);
+    for (const Range& x : out) bad = bad || (&x != &o && meet(o, x));
+    if (bad) return fail(W12_ERR_INVALID_ARG, "kv_slots: results must not overlap one another or what the call reads");
+  }
   SlotArgs a{};
   a.cache_len = cache_len;
   a.add = add;

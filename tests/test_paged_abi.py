@@ -111,3 +111,24 @@ def test_workspace_sizes(w12):
     lib = w12.lib()
     assert lib.tree_attn_workspace_size(0, 1, 8, 8, 128) == 0
     assert lib.tree_attn_workspace_size(16, 1, 40, 8, 128) > 0
+
+
+def test_slot_results_apart_from_what_is_read(w12):
+    """Blocks read requests' numbers while others already write results."""
+    names = ("len", "add", "table", "pool", "pos", "path", "off", "slot", "src", "new", "pos_out", "total", "status")
+    size = dict(len=8, add=8, table=28, pool=32, pos=16, path=16, off=12, slot=64, src=32, new=8, pos_out=16, total=8, status=4)
+    at = {n: 4096 * (i + 1) for i, n in enumerate(names)}
+
+    def call(**kw):
+        a = {n: ctypes.c_void_p(x) for n, x in dict(at, **kw).items()}
+        return w12.lib().kv_slots(a["len"], a["add"], 0, 2, a["table"], 4, 3, a["pool"], 8, a["pos"], 16, a["path"], a["off"], 4,
+                                  8, a["slot"], a["src"], a["new"], a["pos_out"], a["total"], a["status"], None)
+
+    results = names[7:]
+    for o in results:
+        for n in names:
+            if n != o:
+                assert call(**{o: at[n]}) == 1, (o, n)
+                assert call(**{o: at[n] + size[n] - 4}) == 1, (o, n)
+                assert call(**{o: at[n] + 4 - size[o]}) == 1, (o, n)
+                assert b"overlap" in w12.lib().w12_last_error() or (o, n) in (("new", "len"), ("pos_out", "pos"))
