@@ -518,7 +518,9 @@ typedef struct kv_cache {
  * 2; then the table and the pool stay as they were, *total = 0, every slot and src is -1,
  * new_len = cache_len and pool_pos_out = pool_pos.  A path node outside its request
  * gives its token src -1, a negative table or pool entry gives the tokens in it slot -2; kv_write
- * refuses both, and bit 3 is set.  *status (device int32) is zeroed by the caller.
+ * refuses both, and bit 3 is set, also where a request that ends returns a negative entry (it enters
+ * the pool as it is).  Entries are not held against the size of a cache: the ring may be smaller than the
+ * cache it serves, and kv_write and tree_attn check them.  *status (device int32) is zeroed by the caller.
  * Asynchronous; allocates nothing.  Errors: W12_ERR_INVALID_ARG (null pointer; results that
  * overlap one another or what the call reads, as pool_pos_out = pool_pos or new_len = add), W12_ERR_SHAPE
  * (n_req outside 1..4096, block_size or table_width outside 1..2^24, n_blocks outside 1..2^31-1,

@@ -189,7 +189,9 @@ __global__ void __launch_bounds__(kSlotThreads) k_kv_slots(const __grid_constant
   }
   for (int64_t b = t0; b < tot[2]; b += step) {
     const int r = owner(pre_old, a.n_req, (int32_t)b);
-    a.pool[(tail + b) % a.n_blocks] = a.table[r * a.table_stride + ((int32_t)b - pre_old[r])];
+    const int32_t id = a.table[r * a.table_stride + ((int32_t)b - pre_old[r])];
+    if (id < 0) atomicOr(a.status, kSlotBadEntry);
+    a.pool[(tail + b) % a.n_blocks] = id;
   }
 }
 

@@ -314,3 +314,15 @@ def test_any_number_of_requests_as_a_process_s_first_call(w12, n_req):
     """Shared memory beside the prefix sums counts too; a call of more requests before must not matter."""
     r = subprocess.run([sys.executable, "-c", _MANY, str(n_req)], cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("entry", [-1, -7, -2 ** 31])
+def test_a_released_negative_entry_is_reported(w12, entry):
+    table, ring, pos = i32([[0, 1], [2, entry]]), i32([3, 9, 9, 9]), i64([0, 1])
+    out = w12.kv_slots(i32([8, 8]), i32([0, -1]), table, ring, pos, 4, 2)
+    assert int(out.status) == 8
+    assert int(out.total) == 0 and out.new_len.tolist() == [8, 0] and out.pool_pos.tolist() == [0, 3]
+    assert ring.tolist() == [3, 2, entry, 9]
+    # the request that takes it is told too, and its tokens have no place
+    out = w12.kv_slots(out.new_len, i32([0, 9]), i32([[0, 1, 9], [9, 9, 9]]), ring, out.pool_pos, 4, 9)
+    assert int(out.status) == 8 and out.slot.tolist() == [12, 13, 14, 15, 8, 9, 10, 11, -2]
