@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(T, (1024 + T / 2) / T) k_logit_rules(const __g
   const int64_t prompt = count && a.r.hist && a.r.prompt_len ? a.r.prompt_len[r] : 0;
   const int64_t b_given = bias ? a.r.bias_off[r] : 0, b_end = bias ? a.r.bias_off[r + 1] : 0;
   const int64_t len = min(max(h_given, (int64_t)0), a.r.hist_stride);
-  const bool root_read = tree && prompt > len;  // the root, behind the history, is the prompt's last token
+  const bool root_read = tree && prompt > len;  // the root, behind the history, ends the prompt (all rows have it)
   const int32_t* h = a.r.hist + r * a.r.hist_stride;
   // tokens of the history that a thread has on their way (four adjacent ones at a time where the rows
   // allow it), the first ones from here on
@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(T, (1024 + T / 2) / T) k_logit_rules(const __g
       const int32_t p = a.parent[off + i];
       ok = ok && (i == 0 ? p == -1 : p >= 0 && p < i);
       parent[i] = p;
-      draft[i] = a.draft[off + i];
+      draft[i] = i == 0 && root_read ? -1 : a.draft[off + i];
     }
   if (!__syncthreads_and(ok)) {
     if (tid == 0) atomicOr(a.status, kRuleBadRequest);
@@ -183,6 +183,13 @@ __global__ void __launch_bounds__(T, (1024 + T / 2) / T) k_logit_rules(const __g
       }
     }
     ask(j0 + H * T);
+  }
+  if (root_read && tid == 0) {
+    const uint32_t i = (uint32_t)a.draft[off] - (uint32_t)v0;
+    if (i < (uint32_t)width) {
+      atomicOr(&cnt[i], kPromptFlag);
+      atomicOr(&bits[i >> 5], 1u << (i & 31));
+    }
   }
   if (bias) {
     const int64_t b0 = min(max(b_given, (int64_t)0), a.r.n_bias), b1 = min(max(b_end, b0), a.r.n_bias);
@@ -323,7 +330,7 @@ __global__ void __launch_bounds__(T, (1024 + T / 2) / T) k_logit_rules(const __g
         uint32_t c = count ? cnt[i] : 0u;
         if (tree && count)
           for (int32_t p = up[node]; p >= 0;) {
-            if (draft[p] == (int32_t)(v0 + i)) c = p == 0 && root_read ? c | kPromptFlag : c + 1;
+            if (draft[p] == (int32_t)(v0 + i)) ++c;
             p = parent[p] >= 0 ? up[parent[p]] : -1;
           }
         const uint32_t times = c & ~kPromptFlag;
