@@ -126,8 +126,15 @@ __global__ void __launch_bounds__(T, (1024 + T / 2) / T) k_logit_rules(const __g
     if (a.hist_vec) {
 #pragma unroll
       for (int k = 0; k < H; k += 4) {
-        const int64_t j = place(j0, k);  // (a row's length is at least hist_len, a multiple of four)
-        const int4 t = j < len ? *reinterpret_cast<const int4*>(h + j) : make_int4(-1, -1, -1, -1);
+        const int64_t j = place(j0, k);
+        int4 t = make_int4(-1, -1, -1, -1);
+        if (j + 4 <= len) {
+          t = *reinterpret_cast<const int4*>(h + j);
+        } else if (j < len) {  // the last row may end with its history
+          t.x = h[j];
+          if (j + 1 < len) t.y = h[j + 1];
+          if (j + 2 < len) t.z = h[j + 2];
+        }
         told[k] = t.x, told[k + 1] = t.y, told[k + 2] = t.z, told[k + 3] = t.w;
       }
     } else {

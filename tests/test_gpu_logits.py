@@ -4,6 +4,8 @@ The formula is a few float operations per token, each rounded, so the processed 
 compared bit for bit with the same operations in numpy's float32, and with the formula in 64
 bits within 8 roundings (2^-21) of the largest term.
 """
+import ctypes
+
 import numpy as np
 import pytest
 
@@ -451,3 +453,20 @@ def test_a_prompt_ends_at_the_root(w12):
         rules = w12.LogitRules(hist=hist, hist_len=i32([3]), prompt_len=i32([prompt]), frequency=f32([1.0]))
         _, st = w12.logits_process(x, rules, *([i32([-1]), i32([4])] if tree else []))
         assert int(st) == want, (prompt, tree)
+
+
+@pytest.mark.parametrize("n", range(1, 13))
+def test_a_history_that_ends_with_its_array(w12, n):
+    """The last row's history may be the array's last entries: nothing behind hist_len is needed."""
+    V, stride = 300, 12
+    rng = np.random.default_rng(n)
+    hist = i32(rng.integers(0, 9, stride + n))
+    hist_len, freq, off = i32([stride, n]), f32([0.5, 0.25]), i32([0, 1, 2])
+    x = torch.randn((2, V), device="cuda")
+    out, st = torch.empty_like(x), torch.zeros(1, dtype=torch.int32, device="cuda")
+    r = w12.logit_rules()
+    r.hist, r.hist_stride, r.hist_len, r.freq = hist.data_ptr(), stride, hist_len.data_ptr(), freq.data_ptr()
+    assert w12.lib().logits_process(x.data_ptr(), V, 2, V, ctypes.byref(r), None, None, off.data_ptr(), 2, out.data_ptr(), V,
+                                    st.data_ptr(), torch.cuda.current_stream().cuda_stream) == 0
+    count = torch.stack([torch.bincount(hist[:stride], minlength=V), torch.bincount(hist[stride:], minlength=V)])
+    assert torch.equal(out, x - freq[:, None] * count) and int(st) == 0
