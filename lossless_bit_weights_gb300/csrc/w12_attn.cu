@@ -1266,7 +1266,9 @@ int tree_attn(const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_
                 (long long)layer, (long long)cache->n_layers);
   if (!req_offsets && n_req != 1)
     return fail(W12_ERR_INVALID_ARG, "tree_attn: req_offsets is null but n_req=%d", n_req);
-  if (!(scale > 0.0f) || scale > 3e38f) return fail(W12_ERR_INVALID_ARG, "tree_attn: scale must be positive and finite");
+  const float scale_log2 = scale * 1.4426950408889634f;
+  if (!(scale > 0.0f) || !std::isfinite(scale_log2))
+    return fail(W12_ERR_INVALID_ARG, "tree_attn: scale and scale * log2(e) must be positive and finite");
   if ((((uintptr_t)q | (uintptr_t)k | (uintptr_t)v | (uintptr_t)out | (uintptr_t)ws) & 15u) ||
       ((q_stride | k_stride | v_stride) & 7) || q_stride < 0 || k_stride < 0 || v_stride < 0)
     return fail(W12_ERR_INVALID_ARG,
@@ -1308,7 +1310,7 @@ int tree_attn(const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_
   a.row_cap = (int32_t)row_cap(M, a.group, D);
   a.by_block = fast_div(a.block_size);
   a.by_group = fast_div(a.group);
-  a.scale_log2 = scale * 1.4426950408889634f;
+  a.scale_log2 = scale_log2;
   a.wait_cycles = g_wait_cycles.load(std::memory_order_relaxed);
   a.out = out;
   a.status = status;

@@ -132,3 +132,9 @@ def test_slot_results_apart_from_what_is_read(w12):
                 assert call(**{o: at[n] + size[n] - 4}) == 1, (o, n)
                 assert call(**{o: at[n] + 4 - size[o]}) == 1, (o, n)
                 assert b"overlap" in w12.lib().w12_last_error() or (o, n) in (("new", "len"), ("pos_out", "pos"))
+
+
+@pytest.mark.parametrize("scale", [2.4e38, 2.9e38, 3.4e38])
+def test_scales_that_pass_the_largest_float_in_base_two(w12, scale):
+    assert attn(w12, scale=scale) == 1
+    assert b"scale" in w12.lib().w12_last_error()
