@@ -561,7 +561,7 @@ W12_API int kv_write(const kv_cache* cache, int64_t layer, int64_t n_layers, con
  * wait is bounded; one that runs out (about a second) sets bit 2, and outputs are incomplete.
  * K and V of a token that a node does not attend to do not reach its output, whatever
  * they hold.  ws: tree_attn_workspace_size bytes, no initial state needed (do not pass
- * a GEMM's workspace, whose counters must stay zero).
+ * a GEMM's workspace, whose counters must stay zero); calls that may run at the same time need one each.
  * *status (device int32) is zeroed by the caller.  Asynchronous; allocates nothing.
  * Errors: W12_ERR_INVALID_ARG (null or misaligned pointers or strides, out overlapping q, k or v),
  * W12_ERR_SHAPE, W12_ERR_BUFFER_TOO_SMALL. */
@@ -631,7 +631,8 @@ W12_API int logits_process(const float* logits, int64_t stride, int64_t M, int64
  * processed logits: tok[M], path_len, path_nodes and bonus as tree_verify gives them for
  * logits_process's result, except that a row without an allowed token has tok -1, which
  * no draft matches, and path_nodes is -1 behind the path.  ws:
- * logits_verify_workspace_size bytes, no initial state needed (do not pass a GEMM's).
+ * logits_verify_workspace_size bytes, no initial state needed (do not pass a GEMM's); calls that may run
+ * at the same time need one each.
  * Errors as above and W12_ERR_BUFFER_TOO_SMALL. */
 W12_API size_t logits_verify_workspace_size(int64_t M, int64_t V, int32_t n_req);
 W12_API int logits_verify(const float* logits, int64_t stride, int64_t M, int64_t V, const logit_rules* rules,

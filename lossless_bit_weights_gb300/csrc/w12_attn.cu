@@ -29,9 +29,9 @@
 // so the shares of two 128-row halves run over the same keys at the same time).
 //
 // Measured on one GB300, kernel and join, back to back: 24 requests of 33 to 12001 tokens, 192
-// nodes, 40 heads on 8 of 128: 118 us for 617 MB (5.2 TB/s, 0.78 of the measured copy rate); 16
-// nodes over 65535 tokens 61 us (4.4 TB/s); 32 nodes over 131071 tokens, 24 heads on 4 of 256: 146
-// us (0.69 PFLOP/s); 16 nodes over 8191 tokens 21 us, one node over 711 tokens 12 us, of which a
+// nodes, 40 heads on 8 of 128: 119 us for 617 MB (5.2 TB/s, 0.77 of the measured copy rate); 16
+// nodes over 65535 tokens 61 us (4.4 TB/s); 32 nodes over 131071 tokens, 24 heads on 4 of 256: 148
+// us (0.70 PFLOP/s); 16 nodes over 8191 tokens 21 us, one node over 711 tokens 12 us, of which a
 // launch, the chain length -> table -> keys -> scores, a last product and the join are
 // about 10.
 #include <cuda.h>

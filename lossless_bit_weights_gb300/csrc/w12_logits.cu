@@ -14,7 +14,7 @@
 //
 // Bound by bytes, the logits read once (and written once where they are asked for): 192 rows of
 // 151936 tokens of 24 requests take 48 us with all rules (237 MB, 5.0 TB/s, 0.74 of the measured
-// copy rate), 37 us with the argmax and acceptance instead of the rows (117 MB, 3.2 TB/s).  What is
+// copy rate), 37.5 us with the argmax and acceptance instead of the rows (117 MB, 3.1 TB/s).  What is
 // left is the making of the tables, during which a block streams nothing, the history and the
 // listed tokens (about 13, 4 and 5 us of the 37).  Instructions count as much as bytes: bounds
 // tests at every four tokens cost 12 and 8 us.
@@ -440,15 +440,15 @@ struct RulePlan {
 
 // Chunk of the vocabulary per block, a multiple of 256: the larger it is, the fewer blocks
 // scan a request's history and the more rows share the table; the smaller, the more blocks
-// there are.  The largest of 4096, 2048, 1024 with at least two blocks per SM, at 256 threads: 192 rows took 50 us
-// written and 37 verified at 4096, 48 and 44 at 2048; a 16-node tree 15.5 at 1024, 15.8 at 512.
+// there are.  The largest of 4096, 2048, 1024 with at least two blocks per SM: 192 rows took 47.8 us
+// written and 37.5 verified at 4096, 51.3 and 49.8 at 2048; a 16-node tree 12.4 at 1024, 13.7 at 512.
 // Parts of a row's chunk, one a warp at a time: smaller ones even out trees of unequal size, larger ones
-// meet fewer loads' latencies (24 trees of 8 rows: 52 and 36 us at 1 part, 50 and 37 at 2, 51 and
-// 44 at 4, written and verified; a 16-node tree 15.6 at 1, 20.6 at 2).
-// Threads: one row has eight parts, so eight warps (5.4 us, 5.8 at 384 threads, 5.9 at 512); where
+// meet fewer loads' latencies (24 trees of 8 rows in the mean: 47.8 us at 1 part, 47.8 at 2, 49.7 at 4
+// written, 34.3, 37.5 and 43.3 verified; a 16-node tree 12.4 at 1, 14.0 at 2).
+// Threads: one row has eight parts, so eight warps (5.5 us, 5.9 at 384 threads, 5.9 at 512); where
 // every block has an SM's half to itself, 512 make its tables and sixteen rows at once (a 16-node tree
-// 12.0 us, 15.5 at 384, 15.7 at 256); else 384 (192 rows written 47.7 us, 49.4 at 256, 49.0 at 512;
-// verified 37.0, 37.0, 41.0).
+// 12.4 us, 15.0 at 384, 15.5 at 256); else 384 (192 rows written 47.8 us, 49.4 at 256, 49.2 at 512;
+// verified 37.5, 42.0, 46.3).
 RulePlan rule_plan(int64_t M, int64_t V, int32_t n_req) {
   RulePlan p{};
   for (p.chunk = 4096; p.chunk > 1024; p.chunk /= 2)
