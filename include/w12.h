@@ -578,6 +578,60 @@ W12_API int tree_attn(const uint16_t* q, int64_t q_stride, const uint16_t* k, in
 W12_API int tree_attn_set_wait_limit(int64_t cycles);
 
 /* ---------------------------------------------------------------------------
+ * From a layer's fused projection to attention (no counterpart in the pages).  Rows of w12_gemm hold,
+ * side by side, n_q_heads query heads, n_heads key heads and n_heads value heads of head_dim columns.
+ * A form says how they become q, k and v:
+ *   norms     a head x of q (of k) becomes x * rsqrt(mean(x^2) + eps) * w, w = q_norm (k_norm),
+ *             head_dim floats each; NULL: no norm.  The sum of squares is float.
+ *   rotation  pair j < rot_dim/2 of a head of q and of k, columns (j, j + rot_dim/2), or (2j, 2j+1)
+ *             where interleaved, is turned by the angle pos * inv_freq[j] and scaled by rot_scale:
+ *             (a, b) -> rot_scale * (a cos - b sin, b cos + a sin).  The angle is taken in 64 bits: far
+ *             positions lose nothing.  Columns from rot_dim on stay.  rot_dim = 0: no rotation.
+ * Everything is float until the one rounding to bf16 at the end (to nearest even).  Value heads are only rounded.
+ * head_dim: a multiple of 8 up to 256; rot_dim: a multiple of 8, head_dim or less.
+ */
+typedef struct qkv_form {
+  const float* q_norm;
+  const float* k_norm;
+  const float* inv_freq;
+  float eps, rot_scale;
+  int32_t n_q_heads, n_heads, head_dim, rot_dim, interleaved;
+} qkv_form;
+
+/* Positions of the rows of a pass.  Row i of request r (rows req_offsets[r] .. req_offsets[r+1]-1; NULL: one
+ * request of all rows) stands at pos[i] = cache_len[r] + its depth in the request's tree (parent as for
+ * tree_verify_tokens, with `rows` entries, at most 4096 nodes a request), or, with parent = NULL,
+ * + its place in the request (a prompt, or one token).  Rows of no request (a graph's padding) get -1.  A
+ * request that is out of range (offsets, a negative length, a position past 2^31 - 1, a malformed tree)
+ * sets bit 0 of *status, and its rows get -1.  pos serves all layers of the pass.  *status (device
+ * int32) is zeroed by the caller.  Asynchronous; allocates nothing.  Errors: W12_ERR_INVALID_ARG (null
+ * pointer, pos overlapping what the call reads), W12_ERR_SHAPE (n_req outside 1..65535, rows outside 1..2^31-1). */
+W12_API int tree_positions(const int32_t* cache_len, const int32_t* parent, const int32_t* req_offsets, int32_t n_req,
+                           int64_t rows, int32_t* pos, int32_t* status, void* stream);
+
+/* q [M, n_q_heads, head_dim], k and v [M, n_heads, head_dim] of M rows of float (x_bf16 = 0: w12_gemm's y) or
+ * bf16, row i at x + i*x_stride elements, with the position pos[i].  A row with a negative position is
+ * padding: its q, k and v are left as they were.  Rows of q start q_stride elements apart, heads adjacent;
+ * k and v likewise, so they may be parts of one array.  q, k and v of bf16 rows may stand in the
+ * place of the parts of x that they come from (same stride); otherwise they share no element with x or one
+ * another.  Pointers 16-byte aligned, strides multiples of 8 elements.  Asynchronous; allocates nothing.
+ * Errors: W12_ERR_INVALID_ARG, W12_ERR_SHAPE. */
+W12_API int qkv_rope(const void* x, int32_t x_bf16, int64_t x_stride, int64_t M, const qkv_form* form, const int32_t* pos,
+                     uint16_t* q, int64_t q_stride, uint16_t* k, int64_t k_stride, uint16_t* v, int64_t v_stride,
+                     void* stream);
+
+/* The same for tokens that need no acceptance (prompts, plain decoding), with K and V put straight into
+ * the cache: cache[layer] at slot[i] = k and v of row i.  q, k and v rows are written too where their pointers
+ * are not NULL (tree_attn takes the pass's own k and v from rows).  A slot of -1 is skipped (kv_slots' padding); any
+ * other slot outside the cache is skipped and sets bit 0 of *status; rows are written all the same.  A row with a
+ * negative position is padding: nothing is written for it, whatever its slot.  Two tokens with one slot leave
+ * either's values, column by column.  The cache shares no memory with the call's other arrays.
+ * Errors: as for qkv_rope. */
+W12_API int kv_append(const void* x, int32_t x_bf16, int64_t x_stride, int64_t M, const qkv_form* form, const int32_t* pos,
+                      const kv_cache* cache, int64_t layer, const int64_t* slot, uint16_t* q, int64_t q_stride, uint16_t* k,
+                      int64_t k_stride, uint16_t* v, int64_t v_stride, int32_t* status, void* stream);
+
+/* ---------------------------------------------------------------------------
  * Rules on logits before the argmax (no counterpart in the pages): penalties for
  * repeated tokens, a bias per token, and a mask of the tokens a grammar allows.  Device
  * pointers; NULL leaves a rule out.
@@ -639,6 +693,42 @@ W12_API int logits_verify(const float* logits, int64_t stride, int64_t M, int64_
                           const int32_t* parent, const int32_t* draft, const int32_t* req_offsets, int32_t n_req,
                           int32_t* tok, int32_t* path_len, int32_t* path_nodes, int32_t* bonus, int32_t* status,
                           void* ws, size_t ws_bytes, void* stream);
+
+/* Acceptance of draft trees against the target's probabilities (no counterpart in the pages, which accept
+ * greedily): with numbers u and u_bonus uniform in [0, 1), the accepted tokens and the bonus token are
+ * distributed as if the target had been sampled token by token, whatever the drafter proposes.
+ * Row m of logits (V at logits + m*stride) is node m's; a token's probability at the node is p = softmax(logits /
+ * temperature[r]) (NULL: 1).  A temperature below 1e-5 is the limit at zero: p is 1 at the largest logit, the
+ * lowest token among equals.  -inf and NaN leave a token out (logits_process writes -inf for what a
+ * grammar forbids; a top-k or top-p rule is written the same way); +inf tokens share p evenly.
+ * draft_probs (row m at draft_probs + m*probs_stride; NULL: below) holds the drafter's probabilities q at node m, from
+ * which m's children were drawn without replacement: each from what its earlier siblings left, renormalised
+ * (NaN and values outside 0..1 count as the nearest of them).  q is taken as given and should sum to 1.
+ * From the root on, the children of the last accepted node are tried in index order, x = draft[c]:
+ *   c is accepted if u[c] * q(x) / Q < p(x), and the walk goes on below it;
+ *   else p becomes max(p - q / Q, 0) divided by its sum, q(x) = 0, and Q (1 at first) becomes Q - q(x).
+ * With draft_probs = NULL the drafter gave the children for certain (its likeliest tokens, say): c is accepted
+ * if u[c] < p(x), else p(x) = 0 and p is divided by its sum.
+ * Where no child is accepted, bonus[r] is the first token at which the sum of p from token 0 on passes
+ * u_bonus[r].  A draft outside 0..V-1, a token that an earlier sibling had, and one that the drafter cannot have
+ * drawn any more (Q <= 0, or a refused one with q(x) = 0) are passed over and leave p and q.  Where a refusal leaves nothing
+ * (p <= q everywhere, or all that p held was refused), no further child is accepted and the bonus comes from p
+ * as it was at the node.  bonus[r] = -1 where the node allows no token.  Numbers u outside [0, 1) count as the nearest in it (NaN: 0).
+ * Decisions and sums are made to 2^-28 of a probability or better, so that borders between tokens of
+ * large vocabularies fall where the formula has them.  Repeated calls give identical results.
+ * parent, draft, req_offsets, path_len, path_nodes and bonus as for tree_verify_tokens, path_nodes -1 behind the path.
+ * A request that is out of range (offsets, a malformed tree, more than 1024 nodes, a temperature that is
+ * negative or NaN) sets bit 0 of *status and has path_len = bonus = -1, as has one without nodes.  *status (device int32) is
+ * zeroed by the caller.  ws: tree_verify_sampled_workspace_size bytes, 16-byte aligned, no initial
+ * state needed (do not pass a GEMM's); calls that may run at the same time need one each.  Asynchronous; allocates
+ * nothing.  Errors: W12_ERR_INVALID_ARG (null or misaligned pointers, results overlapping one another or what
+ * the call reads), W12_ERR_SHAPE (M, V, n_req, strides), W12_ERR_BUFFER_TOO_SMALL. */
+W12_API size_t tree_verify_sampled_workspace_size(int64_t M, int64_t V);
+W12_API int tree_verify_sampled(const float* logits, int64_t stride, int64_t M, int64_t V, const float* draft_probs,
+                                int64_t probs_stride, const int32_t* parent, const int32_t* draft,
+                                const int32_t* req_offsets, int32_t n_req, const float* u, const float* u_bonus,
+                                const float* temperature, int32_t* path_len, int32_t* path_nodes, int32_t* bonus,
+                                int32_t* status, void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -10,7 +10,9 @@ together by :func:`encode`), :func:`w12_decode`, :func:`w12_decode_q8`,
 :func:`w12_lmhead_verify`, :func:`tree_verify_tokens`, :func:`tree_verify`,
 :func:`w12_export_canonical`, and for attention layers over a paged cache
 :class:`KVCache`, :func:`kv_slots`, :func:`kv_write`, :func:`tree_attn`,
-:class:`LogitRules`, :func:`logits_process` and :func:`logits_verify`.
+:func:`tree_positions`, :class:`QKVForm`, :func:`qkv_rope`, :func:`kv_append`,
+:class:`LogitRules`, :func:`logits_process`, :func:`logits_verify` and, for sampled text,
+:func:`tree_verify_sampled`.
 """
 from __future__ import annotations
 
@@ -62,6 +64,13 @@ class logit_rules(ctypes.Structure):
                 ("pres", ctypes.c_void_p), ("bias_off", ctypes.c_void_p), ("bias_tok", ctypes.c_void_p),
                 ("bias_val", ctypes.c_void_p), ("n_bias", ctypes.c_int64), ("mask", ctypes.c_void_p),
                 ("mask_stride", ctypes.c_int64)]
+
+
+class qkv_form(ctypes.Structure):
+    _fields_ = [("q_norm", ctypes.c_void_p), ("k_norm", ctypes.c_void_p), ("inv_freq", ctypes.c_void_p),
+                ("eps", ctypes.c_float), ("rot_scale", ctypes.c_float), ("n_q_heads", ctypes.c_int32),
+                ("n_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32)]
 
 
 # (name, restype, argtypes) of every exported symbol, in include/w12.h order.
@@ -118,11 +127,18 @@ SIGNATURES = [
     ("tree_attn", ctypes.c_int, [_P, _I64, _P, _I64, _P, _I64, _I64, _I64, ctypes.POINTER(kv_cache), _I64, _P, _I64,
                                  _I64, _P, _P, _P, _I32, ctypes.c_float, _P, _P, _P, _SZ, _P]),
     ("tree_attn_set_wait_limit", ctypes.c_int, [_I64]),
+    ("tree_positions", ctypes.c_int, [_P, _P, _P, _I32, _I64, _P, _P, _P]),
+    ("qkv_rope", ctypes.c_int, [_P, _I32, _I64, _I64, ctypes.POINTER(qkv_form), _P, _P, _I64, _P, _I64, _P, _I64, _P]),
+    ("kv_append", ctypes.c_int, [_P, _I32, _I64, _I64, ctypes.POINTER(qkv_form), _P, ctypes.POINTER(kv_cache), _I64, _P,
+                                 _P, _I64, _P, _I64, _P, _I64, _P, _P]),
     ("logits_process", ctypes.c_int, [_P, _I64, _I64, _I64, ctypes.POINTER(logit_rules), _P, _P, _P, _I32, _P, _I64,
                                       _P, _P]),
     ("logits_verify_workspace_size", _SZ, [_I64, _I64, _I32]),
     ("logits_verify", ctypes.c_int, [_P, _I64, _I64, _I64, ctypes.POINTER(logit_rules), _P, _P, _P, _I32, _P, _P, _P,
                                      _P, _P, _P, _SZ, _P]),
+    ("tree_verify_sampled_workspace_size", _SZ, [_I64, _I64]),
+    ("tree_verify_sampled", ctypes.c_int, [_P, _I64, _I64, _I64, _P, _I64, _P, _P, _P, _I32, _P, _P, _P, _P, _P, _P, _P,
+                                           _P, _SZ, _P]),
 ]
 
 
@@ -791,6 +807,129 @@ def tree_attn_set_wait_limit(cycles: int) -> None:
     _check(lib().tree_attn_set_wait_limit(int(cycles)))
 
 
+# ---------------------------------------------------------------- from the projection to attention
+
+class QKVForm:
+    """How rows of a fused projection become q, k and v (include/w12.h, qkv_form): norms of each
+    head (q_norm, k_norm [head_dim], kept as float32), then the rotation by pos * inv_freq (float32
+    [rotated columns / 2]) of pairs (j, j + half), or of adjacent columns where interleaved,
+    scaled by rot_scale."""
+
+    def __init__(self, n_q_heads: int, n_heads: int, head_dim: int, q_norm=None, k_norm=None, eps: float = 1e-6,
+                 inv_freq=None, interleaved: bool = False, rot_scale: float = 1.0):
+        for name, w in (("q_norm", q_norm), ("k_norm", k_norm)):
+            if w is not None and (not w.is_cuda or w.numel() != head_dim or not w.is_floating_point()):
+                raise ValueError(f"{name} must be a floating-point CUDA tensor of {head_dim} values")
+        q_norm, k_norm = [None if w is None else w.float().contiguous() for w in (q_norm, k_norm)]
+        if inv_freq is not None and (_f32(inv_freq).dim() != 1 or 2 * inv_freq.numel() > head_dim):
+            raise ValueError(f"inv_freq must hold at most {head_dim // 2} values")
+        self.n_q_heads, self.n_heads, self.head_dim = int(n_q_heads), int(n_heads), int(head_dim)
+        self.width = (self.n_q_heads + 2 * self.n_heads) * self.head_dim
+        self._keep = [t for t in (q_norm, k_norm, inv_freq) if t is not None]
+        self._desc = qkv_form(_ptr(q_norm), _ptr(k_norm), _ptr(inv_freq), eps, rot_scale, self.n_q_heads, self.n_heads,
+                              self.head_dim, 0 if inv_freq is None else 2 * inv_freq.numel(), int(interleaved))
+        self._ref = ctypes.byref(self._desc)
+
+    def desc(self):
+        return self._ref
+
+
+def _one_device(first: torch.Tensor, *others) -> None:
+    dev = first.get_device()
+    for t in others:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("the call's tensors must be on one device")
+
+
+def tree_positions(cache_len, parent=None, req_offsets=None, rows: int | None = None, pos=None, status=None, stream=None):
+    """Positions [rows] int32 of a pass's rows: cache_len plus the depth in the request's tree, or
+    plus the place in the request where parent is None (prompts, single tokens); -1 for rows of no
+    request.  rows: parent's entries if not given.  Returns (pos, status)."""
+    n_req = _i32(cache_len).numel()
+    _check_offsets(req_offsets, n_req)
+    if rows is None:
+        if parent is None:
+            raise ValueError("rows is needed without parent")
+        rows = parent.numel()
+    if parent is not None and _i32(parent).numel() != rows:
+        raise ValueError(f"parent must have {rows} entries")
+    if pos is None:
+        pos = _empty(rows, torch.int32, cache_len.device, stream)
+    elif _i32(pos).numel() != rows:
+        raise ValueError(f"pos must have {rows} entries")
+    status = _zero_status(status, cache_len.device, stream)
+    _one_device(cache_len, parent, req_offsets, pos, status)
+    _check((_lib or lib()).tree_positions(
+        cache_len.data_ptr(), None if parent is None else parent.data_ptr(),
+        None if req_offsets is None else req_offsets.data_ptr(), n_req, rows, pos.data_ptr(), status.data_ptr(),
+        _raw_stream(stream, cache_len)))
+    return pos, status
+
+
+def _rope_rows(x, form: QKVForm, pos):
+    """M and whether the projection's rows are bf16."""
+    bf16 = x.dtype != torch.float32
+    if bf16 and x.dtype not in (torch.bfloat16, torch.int16, torch.uint16):
+        raise TypeError(f"expected float32 or bf16 bits (bfloat16/int16/uint16), got {x.dtype}")
+    if not x.is_cuda or x.dim() != 2 or x.shape[1] != form.width or x.stride(1) != 1:
+        raise ValueError(f"x must be a CUDA tensor [M, {form.width}] with adjacent columns")
+    if _i32(pos).numel() != x.shape[0]:
+        raise ValueError(f"pos must have {x.shape[0]} entries")
+    return x.shape[0], bf16
+
+
+def _rope_out(t, name: str, M: int, heads: int, dim: int):
+    if tuple(_rows16(t, name, 3).shape) != (M, heads, dim):
+        raise ValueError(f"{name} must be [{M}, {heads}, {dim}]")
+    return t
+
+
+def qkv_rope(x, form: QKVForm, pos, q=None, k=None, v=None, stream=None):
+    """q [M, query heads, D], k and v [M, heads, D] bf16 of the projection's rows x [M, form.width]
+    (float32 or bf16, any row stride) at the positions pos [M] int32 (see include/w12.h).  Rows with a
+    negative position are left as they were: give q, k and v for a batch with padding.  They may be
+    parts of one array, and of x itself in its own places where x is bf16.  Returns (q, k, v)."""
+    M, bf16 = _rope_rows(x, form, pos)
+    new = x.dtype if bf16 else torch.bfloat16
+    shapes = (form.n_q_heads, form.n_heads, form.n_heads)
+    out = [_empty((M, h, form.head_dim), new, x.device, stream) if t is None else _rope_out(t, n, M, h, form.head_dim)
+           for t, n, h in zip((q, k, v), "qkv", shapes)]
+    q, k, v = out
+    _one_device(x, pos, q, k, v, *form._keep)
+    _check((_lib or lib()).qkv_rope(
+        x.data_ptr(), bf16, _row_stride(x), M, form.desc(), pos.data_ptr(), q.data_ptr(), q.stride(0), k.data_ptr(),
+        k.stride(0), v.data_ptr(), v.stride(0), _raw_stream(stream, x)))
+    return q, k, v
+
+
+def kv_append(x, form: QKVForm, pos, cache: KVCache, slot, layer: int = 0, q=None, k=None, v=None, rows: bool = False,
+              status=None, stream=None):
+    """qkv_rope for tokens that need no acceptance: their K and V go into the cache's slots (slot [M]
+    int64, -1: none) in the same pass.  q is always written, k and v where they are given or with
+    rows=True (tree_attn takes them).  Returns (q, k, v, status), k and v None where not written."""
+    M, bf16 = _rope_rows(x, form, pos)
+    if slot.dtype != torch.int64 or not slot.is_cuda or not slot.is_contiguous() or slot.numel() != M:
+        raise ValueError(f"slot must be a contiguous int64 CUDA tensor of {M} entries")
+    if (cache.n_heads, cache.head_dim) != (form.n_heads, form.head_dim):
+        raise ValueError(f"the cache must hold {form.n_heads} heads of {form.head_dim}")
+    new = x.dtype if bf16 else torch.bfloat16
+    out = []
+    for t, n, h in zip((q, k, v), "qkv", (form.n_q_heads, form.n_heads, form.n_heads)):
+        if t is not None:
+            t = _rope_out(t, n, M, h, form.head_dim)
+        elif rows or n == "q":
+            t = _empty((M, h, form.head_dim), new, x.device, stream)
+        out.append(t)
+    q, k, v = out
+    status = _zero_status(status, x.device, stream)
+    _one_device(x, pos, slot, cache.k, cache.v, q, k, v, status, *form._keep)
+    stride = lambda t: 0 if t is None else t.stride(0)
+    _check((_lib or lib()).kv_append(
+        x.data_ptr(), bf16, _row_stride(x), M, form.desc(), pos.data_ptr(), cache.desc(), layer, slot.data_ptr(),
+        q.data_ptr(), q.stride(0), _ptr(k), stride(k), _ptr(v), stride(v), status.data_ptr(), _raw_stream(stream, x)))
+    return q, k, v, status
+
+
 # ---------------------------------------------------------------- rules on logits
 
 class LogitRules:
@@ -873,3 +1012,47 @@ def logits_verify(logits, rules: LogitRules, parent, draft, req_offsets=None, ws
         logits.data_ptr(), stride, M, V, rules.desc(), _ptr(parent), _ptr(draft), _ptr(req_offsets), n_req, tok.data_ptr(),
         path_len.data_ptr(), path_nodes.data_ptr(), bonus.data_ptr(), status.data_ptr(), buf.data_ptr(), buf.numel(), raw))
     return tok, path_len, path_nodes, bonus, status
+
+
+# ---------------------------------------------------------------- sampled acceptance
+
+@functools.lru_cache(maxsize=256)
+def _sampled_bytes(M: int, V: int) -> int:
+    return int(lib().tree_verify_sampled_workspace_size(M, V))
+
+
+def _float_rows(t, name: str, shape=None):
+    if t.dtype != torch.float32 or not t.is_cuda or t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] != 1):
+        raise ValueError(f"{name} must be a float32 CUDA tensor [M, V] with adjacent columns")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}")
+    return t
+
+
+def tree_verify_sampled(logits, parent, draft, u, u_bonus, draft_probs=None, temperature=None, req_offsets=None,
+                        ws: Workspace | None = None, status=None, stream=None):
+    """Acceptance of draft trees against the target's probabilities softmax(logits / temperature), from the
+    uniform numbers u [M] and u_bonus [n_req] (see include/w12.h): the tokens are distributed as the target's.
+    logits [M, V] float32; draft_probs [M, V] float32: the drafter's probabilities at each node, from which
+    its children were drawn without replacement (None: children given for certain); temperature [n_req]
+    float32 (None: 1; below 1e-5: greedy).  Returns (path_len, path_nodes, bonus, status)."""
+    M, V = _float_rows(logits, "logits").shape
+    n_req = 1 if req_offsets is None else _i32(req_offsets).numel() - 1
+    if draft_probs is not None:
+        _float_rows(draft_probs, "draft_probs", logits.shape)
+    if _i32(parent).numel() != M or _i32(draft).numel() != M or _f32(u).numel() != M:
+        raise ValueError(f"parent, draft and u must have {M} entries")
+    if _f32(u_bonus).numel() != n_req or temperature is not None and _f32(temperature).numel() != n_req:
+        raise ValueError(f"u_bonus and temperature must have {n_req} entries")
+    dev = logits.device
+    path_nodes = _empty(M, torch.int32, dev, stream)
+    path_len, bonus = _empty(n_req, torch.int32, dev, stream), _empty(n_req, torch.int32, dev, stream)
+    status = _zero_status(status, dev, stream)
+    _one_device(logits, parent, draft, u, u_bonus, draft_probs, temperature, req_offsets, status)
+    raw = _raw_stream(stream, logits)
+    buf = (ws or Workspace(dev)).scratch(_sampled_bytes(M, V), stream, raw)
+    _check((_lib or lib()).tree_verify_sampled(
+        logits.data_ptr(), _row_stride(logits), M, V, _ptr(draft_probs), 0 if draft_probs is None else _row_stride(draft_probs),
+        parent.data_ptr(), draft.data_ptr(), _ptr(req_offsets), n_req, u.data_ptr(), u_bonus.data_ptr(), _ptr(temperature),
+        path_len.data_ptr(), path_nodes.data_ptr(), bonus.data_ptr(), status.data_ptr(), buf.data_ptr(), buf.numel(), raw))
+    return path_len, path_nodes, bonus, status

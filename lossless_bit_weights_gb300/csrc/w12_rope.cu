@@ -1,0 +1,455 @@
+// w12_rope.cu - from a fused projection's rows to the q, k and v of attention: positions of tree
+// nodes, norms of each head and the position rotation in one pass, and the same with K and V going
+// straight into their slots of a paged cache.
+#include <cstdint>
+
+#include "w12_internal.cuh"
+#include "w12_pdl.cuh"
+
+namespace w12 {
+
+int check_cache(const kv_cache* c, const char* fn);
+
+namespace {
+
+// ---------------------------------------------------------------- positions
+
+constexpr int kPosThreads = 256;
+constexpr int kPosMaxNodes = 4096;  // nodes of one tree
+constexpr int32_t kPosBadRequest = 1;
+
+struct PosArgs {
+  const int32_t *cache_len, *parent, *req_offsets;
+  int32_t *pos, *status;
+  int64_t rows;
+  int32_t n_req;
+};
+
+// A request's rows [off, off + n), and whether its numbers are in range.
+__device__ __forceinline__ bool pos_request(const PosArgs& a, int r, int64_t& off, int64_t& n) {
+  const int64_t from = a.req_offsets ? a.req_offsets[r] : 0, to = a.req_offsets ? a.req_offsets[r + 1] : a.rows;
+  const int64_t len = a.cache_len[r];
+  off = min(max(from, (int64_t)0), a.rows);
+  n = max(min(to, a.rows) - off, (int64_t)0);
+  return from >= 0 && to >= from && to <= a.rows && len >= 0 && len + n <= 0x7FFFFFFF;
+}
+
+// Chains (prompts, single tokens): a thread finds its row's request by halving.
+__global__ void __launch_bounds__(kPosThreads) k_chain_positions(const __grid_constant__ PosArgs a) {
+  pdl_enter();
+  const int64_t t0 = (int64_t)blockIdx.x * kPosThreads + threadIdx.x, step = (int64_t)gridDim.x * kPosThreads;
+  for (int64_t r = t0; r < a.n_req; r += step) {
+    int64_t off, n;
+    if (!pos_request(a, (int)r, off, n)) atomicOr(a.status, kPosBadRequest);
+  }
+  for (int64_t i = t0; i < a.rows; i += step) {
+    int lo = 0, hi = a.n_req;  // the last request that starts at or before row i
+    while (a.req_offsets && hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (a.req_offsets[mid] <= i) lo = mid; else hi = mid;
+    }
+    int64_t off, n;
+    const bool ok = pos_request(a, lo, off, n) && i >= off && i < off + n;
+    a.pos[i] = ok ? (int32_t)(a.cache_len[lo] + (i - off)) : -1;
+  }
+}
+
+// Trees: a block takes a request and doubles the step of every node's way up until all ways end at
+// the root (3 rounds for 8 nodes, 12 for 4096), in shared memory.  Bound by its chain of loads
+// (offsets, parents) and barriers, not by bytes.  The blocks behind the requests' fill the rows of none.
+__global__ void __launch_bounds__(kPosThreads) k_tree_positions(const __grid_constant__ PosArgs a) {
+  pdl_enter();
+  __shared__ uint16_t up[2][kPosMaxNodes], depth[2][kPosMaxNodes];
+  const int tid = threadIdx.x;
+  if ((int)blockIdx.x >= a.n_req) {
+    const int64_t first = a.req_offsets ? a.req_offsets[0] : 0, last = a.req_offsets ? a.req_offsets[a.n_req] : a.rows;
+    const int64_t step = (int64_t)(gridDim.x - a.n_req) * kPosThreads;
+    for (int64_t i = (int64_t)(blockIdx.x - a.n_req) * kPosThreads + tid; i < a.rows; i += step)
+      if (i < first || i >= last) a.pos[i] = -1;
+    return;
+  }
+  int64_t off, n64;
+  bool ok = pos_request(a, blockIdx.x, off, n64) && n64 <= kPosMaxNodes;
+  const int n = ok ? (int)n64 : 0;
+  for (int i = tid; i < n; i += kPosThreads) {
+    const int32_t p = a.parent[off + i];
+    ok = ok && (i == 0 ? p == -1 : p >= 0 && p < i);
+    up[0][i] = (uint16_t)(i == 0 ? 0 : p & (kPosMaxNodes - 1));
+    depth[0][i] = i != 0;
+  }
+  if (!__syncthreads_and(ok)) {
+    for (int64_t i = tid; i < n64; i += kPosThreads) a.pos[off + i] = -1;
+    if (tid == 0) atomicOr(a.status, kPosBadRequest);
+    return;
+  }
+  int b = 0;
+  for (int reach = 1; reach < n; reach *= 2) {  // every way's first `reach` steps are counted
+    bool more = false;
+    for (int i = tid; i < n; i += kPosThreads) {
+      const int u = up[b][i];
+      depth[b ^ 1][i] = depth[b][i] + depth[b][u];
+      up[b ^ 1][i] = up[b][u];
+      more = more || up[b][u] != 0;
+    }
+    b ^= 1;
+    if (!__syncthreads_or(more)) break;
+  }
+  const int32_t len = n ? a.cache_len[blockIdx.x] : 0;
+  for (int i = tid; i < n; i += kPosThreads) a.pos[off + i] = len + depth[b][i];
+}
+
+// ---------------------------------------------------------------- norms and rotation
+
+struct RopeArgs {
+  const void* x;
+  int64_t x_stride, M;
+  const float *q_norm, *k_norm, *inv_freq;
+  const int32_t* pos;
+  uint16_t* out[3];        // q, k, v rows (null: not asked for)
+  int64_t out_stride[3];
+  uint16_t* cache[2];      // K, V at the layer, or null
+  int64_t block_stride, token_stride, head_stride, n_slots;
+  const int64_t* slot;
+  int32_t* status;
+  float eps, rot_scale;
+  int32_t n_q, n_kv, d, half, block_size;
+};
+
+constexpr int kRopeThreads = 128;
+constexpr int kRopeMaxDim = 256;
+
+__device__ __forceinline__ float bf16_low(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_high(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {  // a in the low half, to nearest even
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
+
+// A lane's eight columns of a head: [lo, lo+4) and [hi, hi+4), eight adjacent ones where NEXT.
+template <typename T, bool NEXT>
+__device__ __forceinline__ void load8(const T* x, int lo, int hi, float f[8]) {
+  if constexpr (sizeof(T) == 4) {
+    const float4 a = __ldcs(reinterpret_cast<const float4*>(x + lo)), b = __ldcs(reinterpret_cast<const float4*>(x + hi));
+    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+  } else {
+    uint2 a, b;
+    if constexpr (NEXT) {
+      const uint4 w = __ldcs(reinterpret_cast<const uint4*>(x + lo));
+      a = make_uint2(w.x, w.y), b = make_uint2(w.z, w.w);
+    } else {
+      a = __ldcs(reinterpret_cast<const uint2*>(x + lo)), b = __ldcs(reinterpret_cast<const uint2*>(x + hi));
+    }
+    f[0] = bf16_low(a.x), f[1] = bf16_high(a.x), f[2] = bf16_low(a.y), f[3] = bf16_high(a.y);
+    f[4] = bf16_low(b.x), f[5] = bf16_high(b.x), f[6] = bf16_low(b.y), f[7] = bf16_high(b.y);
+  }
+}
+
+template <bool NEXT>
+__device__ __forceinline__ void store8(uint16_t* y, int lo, int hi, const uint32_t w[4]) {
+  if constexpr (NEXT) {
+    *reinterpret_cast<uint4*>(y + lo) = make_uint4(w[0], w[1], w[2], w[3]);
+  } else {
+    *reinterpret_cast<uint2*>(y + lo) = make_uint2(w[0], w[1]);
+    *reinterpret_cast<uint2*>(y + hi) = make_uint2(w[2], w[3]);
+  }
+}
+
+// One row a block (and a share of its heads, gridDim.y), P lanes a head, eight columns a lane:
+//   y = x * rsqrt(mean(x^2) + eps) * w,   (a, b) -> s (a cos - b sin, b cos + a sin),
+// with both columns of a pair in one lane, so that the rotation needs no exchange and the norm one sum
+// over P lanes.  The angle pos * inv_freq is taken in turns and in 64 bits, where its whole turns are dropped
+// exactly; a float angle at position 10^6 would be off by 0.03.  The row's sines are found once, a
+// thread each, while the first heads are on their way.
+template <typename T, int P, bool NEXT>
+__global__ void __launch_bounds__(kRopeThreads) k_qkv_rope(const __grid_constant__ RopeArgs a) {
+  constexpr int kGroups = kRopeThreads / P;  // heads of a block at a time
+  constexpr int U = 4;                       // heads of a lane on their way
+  __shared__ __align__(16) float s_cos[kRopeMaxDim / 2], s_sin[kRopeMaxDim / 2];
+  __shared__ int64_t s_place;
+  pdl_enter();
+  const int tid = threadIdx.x, g = tid / P, u = tid % P;
+  const int64_t t = blockIdx.x;
+  const int heads = a.n_q + 2 * a.n_kv, first = blockIdx.y * kGroups + g, step = gridDim.y * kGroups;
+  const bool live = 8 * u < a.d, turned = 8 * u < 2 * a.half;
+  const int lo = !NEXT && turned ? 4 * u : 8 * u, hi = !NEXT && turned ? a.half + 4 * u : 8 * u + 4;
+  const int32_t pos = a.pos[t];
+  if (pos < 0) return;  // padding
+  const T* x = static_cast<const T*>(a.x) + t * a.x_stride;
+  float f[U][8];
+  auto ask = [&](int h0) {
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int h = h0 + k * step;
+      if (live && h < heads) {
+        load8<T, NEXT>(x + (int64_t)h * a.d, lo, hi, f[k]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[k][i] = 0.0f;
+      }
+    }
+  };
+  ask(first);
+  float wq[8], wk[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int c = i < 4 ? lo + i : hi + i - 4;
+    wq[i] = a.q_norm && live ? a.q_norm[c] : 1.0f;
+    wk[i] = a.k_norm && live ? a.k_norm[c] : 1.0f;
+  }
+  for (int j = tid; j < a.half; j += kRopeThreads) {
+    const double turns = (double)pos * ((double)a.inv_freq[j] * 0.15915494309189533576888);  // 1 / (2 pi)
+    float sn, cs;
+    sincospif(2.0f * (float)(turns - rint(turns)), &sn, &cs);
+    s_cos[j] = cs * a.rot_scale;
+    s_sin[j] = sn * a.rot_scale;
+  }
+  if (a.cache[0] && tid == kRopeThreads - 1) {
+    int64_t place = a.slot[t];
+    if (place != -1) {
+      if (place < 0 || place >= a.n_slots) {
+        atomicOr(a.status, 1);
+        place = -1;
+      } else {
+        const int64_t block = place / a.block_size;
+        place = block * a.block_stride + (place - block * a.block_size) * a.token_stride;
+      }
+    }
+    s_place = place;
+  }
+  __syncthreads();
+  const int64_t place = a.cache[0] ? s_place : -1;
+  float4 cs = make_float4(1.0f, 1.0f, 1.0f, 1.0f), sn = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (turned) {
+    cs = *reinterpret_cast<const float4*>(s_cos + 4 * u);
+    sn = *reinterpret_cast<const float4*>(s_sin + 4 * u);
+  }
+  const float inv_d = 1.0f / (float)a.d;
+  for (int h0 = first - g; h0 < heads; h0 += U * step) {  // the same for all lanes of a warp
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int h = h0 + g + k * step;
+      const int part = h < a.n_q ? 0 : h < a.n_q + a.n_kv ? 1 : 2;
+      float y[8];
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum = fmaf(f[k][i], f[k][i], sum);
+#pragma unroll
+      for (int o = P / 2; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+      const bool norm = part == 0 ? a.q_norm != nullptr : part == 1 && a.k_norm != nullptr;
+      const float r = norm ? rsqrtf(fmaf(sum, inv_d, a.eps)) : 1.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = norm ? f[k][i] * r * (part == 0 ? wq[i] : wk[i]) : f[k][i];
+      if (part < 2 && turned) {
+        if constexpr (NEXT) {
+          const float c4[4] = {cs.x, cs.y, cs.z, cs.w}, s4[4] = {sn.x, sn.y, sn.z, sn.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float p = y[2 * i], q = y[2 * i + 1];
+            y[2 * i] = fmaf(p, c4[i], -(q * s4[i]));
+            y[2 * i + 1] = fmaf(q, c4[i], p * s4[i]);
+          }
+        } else {
+          const float c4[4] = {cs.x, cs.y, cs.z, cs.w}, s4[4] = {sn.x, sn.y, sn.z, sn.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float p = y[i], q = y[i + 4];
+            y[i] = fmaf(p, c4[i], -(q * s4[i]));
+            y[i + 4] = fmaf(q, c4[i], p * s4[i]);
+          }
+        }
+      }
+      if (live && h < heads) {
+        const uint32_t w[4] = {pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7])};
+        const int in = h - (part == 0 ? 0 : part == 1 ? a.n_q : a.n_q + a.n_kv);
+        if (a.out[part]) store8<NEXT>(a.out[part] + t * a.out_stride[part] + (int64_t)in * a.d, lo, hi, w);
+        if (part && place >= 0) store8<NEXT>(a.cache[part - 1] + place + in * a.head_stride, lo, hi, w);
+      }
+    }
+    ask(h0 + g + U * step);
+  }
+}
+
+template <typename T, int P>
+constexpr auto rope_kernel(bool next) {
+  return next ? k_qkv_rope<T, P, true> : k_qkv_rope<T, P, false>;
+}
+
+// Rows of two strided arrays that share no element: apart, or side by side in the rows of one array.
+bool rows_apart(uintptr_t a, uintptr_t a_row, uintptr_t a_pitch, uintptr_t b, uintptr_t b_row, uintptr_t b_pitch, int64_t n) {
+  if (a + (n - 1) * a_pitch + a_row <= b || b + (n - 1) * b_pitch + b_row <= a) return true;
+  if (n < 2 || a_pitch != b_pitch) return false;
+  const uintptr_t by = (b > a ? b - a : a - b) % a_pitch;  // of the later one behind a row's start of the earlier
+  return by >= (b > a ? a_row : b_row) && by + (b > a ? b_row : a_row) <= a_pitch;
+}
+
+// The checks that both calls share, and the kernel's arguments but for the cache's.
+int rope_args(RopeArgs& a, const char* fn, const void* x, int32_t x_bf16, int64_t x_stride, int64_t M, const qkv_form* form,
+              const int32_t* pos, uint16_t* q, int64_t q_stride, uint16_t* k, int64_t k_stride, uint16_t* v,
+              int64_t v_stride) {
+  if (!form) return fail(W12_ERR_INVALID_ARG, "%s: null form", fn);
+  const int64_t nq = form->n_q_heads, nk = form->n_heads, d = form->head_dim;
+  if (nq < 1 || nk < 1 || nq > 65535 || nk > 65535 || d < 8 || d > kRopeMaxDim || (d & 7) || form->rot_dim < 0 ||
+      form->rot_dim > d || (form->rot_dim & 7))
+    return fail(W12_ERR_SHAPE, "%s: %lld + 2 x %lld heads of %lld (a multiple of 8 up to %d), %d of them rotated (a multiple of 8)",
+                fn, (long long)nq, (long long)nk, (long long)d, kRopeMaxDim, form->rot_dim);
+  const int64_t width = (nq + 2 * nk) * d;
+  if (M < 1 || M > 0x7FFFFFFF || (M > 1 && x_stride < width))
+    return fail(W12_ERR_SHAPE, "%s: M=%lld rows of %lld (stride %lld) out of range", fn, (long long)M, (long long)width,
+                (long long)x_stride);
+  if (!x || !pos) return fail(W12_ERR_INVALID_ARG, "%s: null pointer", fn);
+  if (form->rot_dim && !form->inv_freq) return fail(W12_ERR_INVALID_ARG, "%s: a rotation needs its frequencies", fn);
+  if (!(form->eps >= 0.0f) || !(form->eps <= 1e30f) || !(form->rot_scale >= -1e30f) || !(form->rot_scale <= 1e30f))
+    return fail(W12_ERR_INVALID_ARG, "%s: eps=%g, rot_scale=%g out of range", fn, form->eps, form->rot_scale);
+  uint16_t* out[3] = {q, k, v};
+  const int64_t stride[3] = {q_stride, k_stride, v_stride}, wide[3] = {nq * d, nk * d, nk * d}, at[3] = {0, nq * d, (nq + nk) * d};
+  uintptr_t bits = (uintptr_t)x;
+  int64_t strides = x_stride;
+  for (int i = 0; i < 3; ++i) {
+    if (!out[i]) continue;
+    bits |= (uintptr_t)out[i];
+    strides |= stride[i];
+    if (M > 1 && stride[i] < wide[i])
+      return fail(W12_ERR_SHAPE, "%s: rows of %lld at a stride of %lld", fn, (long long)wide[i], (long long)stride[i]);
+  }
+  if ((bits & 15u) || (strides & 7))
+    return fail(W12_ERR_INVALID_ARG, "%s: rows must be 16-byte aligned and their strides multiples of 8", fn);
+  const int size = x_bf16 ? 2 : 4;
+  for (int i = 0; i < 3; ++i) {
+    if (!out[i]) continue;
+    const uintptr_t o = (uintptr_t)out[i], row = (uintptr_t)wide[i] * 2, pitch = (uintptr_t)stride[i] * 2;
+    // in the place of the part of bf16 rows that it comes from, or nowhere in them
+    const bool same = x_bf16 && o == (uintptr_t)x + (uintptr_t)at[i] * 2 && (stride[i] == x_stride || M == 1);
+    bool ok = same || rows_apart(o, row, pitch, (uintptr_t)x, (uintptr_t)width * size, (uintptr_t)x_stride * size, M);
+    ok = ok && rows_apart(o, row, pitch, (uintptr_t)pos, (uintptr_t)M * 4, 0, M);
+    for (int j = 0; j < i; ++j)
+      ok = ok && (!out[j] || rows_apart(o, row, pitch, (uintptr_t)out[j], (uintptr_t)wide[j] * 2, (uintptr_t)stride[j] * 2, M));
+    if (!ok) return fail(W12_ERR_INVALID_ARG, "%s: q, k and v must not overlap one another or what the call reads", fn);
+    a.out[i] = out[i];
+    a.out_stride[i] = stride[i];
+  }
+  a.x = x;
+  a.x_stride = x_stride;
+  a.M = M;
+  a.q_norm = form->q_norm;
+  a.k_norm = form->k_norm;
+  a.inv_freq = form->inv_freq;
+  a.pos = pos;
+  a.eps = form->eps;
+  a.rot_scale = form->rot_scale;
+  a.n_q = (int32_t)nq;
+  a.n_kv = (int32_t)nk;
+  a.d = (int32_t)d;
+  a.half = form->rot_dim / 2;
+  return W12_OK;
+}
+
+int launch_rope(const RopeArgs& a, int32_t x_bf16, int32_t interleaved, cudaStream_t s, const char* what) {
+  const int lanes = a.d <= 64 ? 8 : a.d <= 128 ? 16 : 32;
+  const bool next = interleaved || a.half == 0;  // (without a rotation the columns may as well be adjacent)
+  using Kernel = void (*)(RopeArgs);
+  const Kernel kernels[2][3] = {
+      {rope_kernel<float, 8>(next), rope_kernel<float, 16>(next), rope_kernel<float, 32>(next)},
+      {rope_kernel<uint16_t, 8>(next), rope_kernel<uint16_t, 16>(next), rope_kernel<uint16_t, 32>(next)}};
+  const Kernel kernel = kernels[x_bf16 ? 1 : 0][lanes == 8 ? 0 : lanes == 16 ? 1 : 2];
+  const int groups = kRopeThreads / lanes, most = (a.n_q + 2 * a.n_kv + groups - 1) / groups;
+  // few rows: their heads over more blocks
+  int64_t split = 152 * 8 / a.M;
+  split = split < 1 ? 1 : split > most ? most : split;
+  W12_CUDA_TRY(launch_dependent(kernel, dim3((unsigned)a.M, (unsigned)split), kRopeThreads, 0, s, a));
+  W12_LAUNCH_CHECK(what);
+  return W12_OK;
+}
+
+}  // namespace
+}  // namespace w12
+
+using namespace w12;
+
+extern "C" {
+
+int tree_positions(const int32_t* cache_len, const int32_t* parent, const int32_t* req_offsets, int32_t n_req, int64_t rows,
+                   int32_t* pos, int32_t* status, void* stream) {
+  if (n_req < 1 || n_req > 65535 || rows < 1 || rows > 0x7FFFFFFF)
+    return fail(W12_ERR_SHAPE, "tree_positions: n_req=%d (1..65535), rows=%lld out of range", n_req, (long long)rows);
+  if (!cache_len || !pos || !status) return fail(W12_ERR_INVALID_ARG, "tree_positions: null pointer");
+  if (!req_offsets && n_req != 1)
+    return fail(W12_ERR_INVALID_ARG, "tree_positions: req_offsets is null but n_req=%d", n_req);
+  const uintptr_t o = (uintptr_t)pos, end = o + (uintptr_t)rows * 4;
+  auto meets = [&](const void* p, int64_t n) { return p && (uintptr_t)p < end && o < (uintptr_t)p + (uintptr_t)n * 4; };
+  if (meets(cache_len, n_req) || meets(parent, rows) || meets(req_offsets, n_req + 1) || meets(status, 1))
+    return fail(W12_ERR_INVALID_ARG, "tree_positions: pos must not overlap what the call reads");
+  PosArgs a{cache_len, parent, req_offsets, pos, status, rows, n_req};
+  const int64_t blocks = (rows + kPosThreads - 1) / kPosThreads;
+  if (parent) {
+    const int fill = (int)(blocks < 16 ? blocks : 16);
+    W12_CUDA_TRY(launch_dependent(k_tree_positions, dim3((unsigned)(n_req + fill)), kPosThreads, 0, (cudaStream_t)stream, a));
+  } else {
+    W12_CUDA_TRY(launch_dependent(k_chain_positions, dim3((unsigned)(blocks < 152 * 8 ? blocks : 152 * 8)), kPosThreads, 0,
+                                  (cudaStream_t)stream, a));
+  }
+  W12_LAUNCH_CHECK("tree_positions kernel");
+  return W12_OK;
+}
+
+int qkv_rope(const void* x, int32_t x_bf16, int64_t x_stride, int64_t M, const qkv_form* form, const int32_t* pos, uint16_t* q,
+             int64_t q_stride, uint16_t* k, int64_t k_stride, uint16_t* v, int64_t v_stride, void* stream) {
+  RopeArgs a{};
+  const int st = rope_args(a, "qkv_rope", x, x_bf16, x_stride, M, form, pos, q, q_stride, k, k_stride, v, v_stride);
+  if (st) return st;
+  if (!q || !k || !v) return fail(W12_ERR_INVALID_ARG, "qkv_rope: null pointer");
+  return launch_rope(a, x_bf16, form->interleaved, (cudaStream_t)stream, "qkv_rope kernel");
+}
+
+int kv_append(const void* x, int32_t x_bf16, int64_t x_stride, int64_t M, const qkv_form* form, const int32_t* pos,
+              const kv_cache* cache, int64_t layer, const int64_t* slot, uint16_t* q, int64_t q_stride, uint16_t* k,
+              int64_t k_stride, uint16_t* v, int64_t v_stride, int32_t* status, void* stream) {
+  RopeArgs a{};
+  int st = check_cache(cache, "kv_append");
+  if (st) return st;
+  st = rope_args(a, "kv_append", x, x_bf16, x_stride, M, form, pos, q, q_stride, k, k_stride, v, v_stride);
+  if (st) return st;
+  if (!slot || !status) return fail(W12_ERR_INVALID_ARG, "kv_append: null pointer");
+  if (cache->n_heads != form->n_heads || cache->head_dim != form->head_dim)
+    return fail(W12_ERR_SHAPE, "kv_append: a cache of %d heads of %d for rows with %d of %d", cache->n_heads, cache->head_dim,
+                form->n_heads, form->head_dim);
+  if (layer < 0 || layer >= cache->n_layers)
+    return fail(W12_ERR_SHAPE, "kv_append: layer %lld of %lld", (long long)layer, (long long)cache->n_layers);
+  // Rows and slots stand outside the cache.
+  const uintptr_t span = 2 * (uintptr_t)((cache->n_layers - 1) * cache->layer_stride + (cache->n_blocks - 1) * cache->block_stride +
+                                         (cache->block_size - 1) * cache->token_stride +
+                                         (cache->n_heads - 1) * cache->head_stride + cache->head_dim);
+  struct Range {
+    const void* p;
+    int64_t bytes;
+  };
+  const int64_t nk = form->n_heads * (int64_t)form->head_dim, nq = form->n_q_heads * (int64_t)form->head_dim;
+  const Range used[] = {{x, ((M - 1) * x_stride + nq + 2 * nk) * (x_bf16 ? 2 : 4)},
+                        {q, ((M - 1) * q_stride + nq) * 2},
+                        {k, ((M - 1) * k_stride + nk) * 2},
+                        {v, ((M - 1) * v_stride + nk) * 2},
+                        {pos, M * 4},
+                        {slot, M * 8},
+                        {status, 4}};
+  for (const Range& u : used)
+    for (const uint16_t* c : {cache->k, cache->v})
+      if (u.p && (uintptr_t)u.p < (uintptr_t)c + span && (uintptr_t)c < (uintptr_t)u.p + (uintptr_t)u.bytes)
+        return fail(W12_ERR_INVALID_ARG, "kv_append: the cache must not overlap the call's other arrays");
+  for (int i = 1; i < 4; ++i)
+    if (used[i].p && (uintptr_t)used[i].p < (uintptr_t)slot + (uintptr_t)M * 8 &&
+        (uintptr_t)slot < (uintptr_t)used[i].p + (uintptr_t)used[i].bytes)
+      return fail(W12_ERR_INVALID_ARG, "kv_append: q, k and v must not overlap the slots");
+  a.cache[0] = cache->k + layer * cache->layer_stride;
+  a.cache[1] = cache->v + layer * cache->layer_stride;
+  a.block_stride = cache->block_stride;
+  a.token_stride = cache->token_stride;
+  a.head_stride = cache->head_stride;
+  a.n_slots = cache->n_blocks * cache->block_size;
+  a.block_size = cache->block_size;
+  a.slot = slot;
+  a.status = status;
+  return launch_rope(a, x_bf16, form->interleaved, (cudaStream_t)stream, "kv_append kernel");
+}
+
+}  // extern "C"
