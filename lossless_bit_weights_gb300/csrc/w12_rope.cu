@@ -127,24 +127,40 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {  // a in the l
   return r;
 }
 
-// A lane's eight columns of a head: [lo, lo+4) and [hi, hi+4), eight adjacent ones where NEXT.
+// A lane's eight columns of a head, [lo, lo+4) and [hi, hi+4), eight adjacent ones where NEXT, as they were loaded.
 template <typename T, bool NEXT>
-__device__ __forceinline__ void load8(const T* x, int lo, int hi, float f[8]) {
-  if constexpr (sizeof(T) == 4) {
-    const float4 a = __ldcs(reinterpret_cast<const float4*>(x + lo)), b = __ldcs(reinterpret_cast<const float4*>(x + hi));
-    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-  } else {
-    uint2 a, b;
-    if constexpr (NEXT) {
-      const uint4 w = __ldcs(reinterpret_cast<const uint4*>(x + lo));
-      a = make_uint2(w.x, w.y), b = make_uint2(w.z, w.w);
-    } else {
-      a = __ldcs(reinterpret_cast<const uint2*>(x + lo)), b = __ldcs(reinterpret_cast<const uint2*>(x + hi));
-    }
-    f[0] = bf16_low(a.x), f[1] = bf16_high(a.x), f[2] = bf16_low(a.y), f[3] = bf16_high(a.y);
-    f[4] = bf16_low(b.x), f[5] = bf16_high(b.x), f[6] = bf16_low(b.y), f[7] = bf16_high(b.y);
+struct Eight;
+
+template <bool NEXT>
+struct Eight<float, NEXT> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* x, int lo, int hi) {
+    a = __ldcs(reinterpret_cast<const float4*>(x + lo));
+    b = __ldcs(reinterpret_cast<const float4*>(x + hi));
   }
-}
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
+  __device__ __forceinline__ void get(float f[8]) const {
+    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+  }
+};
+
+template <bool NEXT>
+struct Eight<uint16_t, NEXT> {
+  uint4 w;
+  __device__ __forceinline__ void load(const uint16_t* x, int lo, int hi) {
+    if constexpr (NEXT) {
+      w = __ldcs(reinterpret_cast<const uint4*>(x + lo));
+    } else {
+      const uint2 a = __ldcs(reinterpret_cast<const uint2*>(x + lo)), b = __ldcs(reinterpret_cast<const uint2*>(x + hi));
+      w = make_uint4(a.x, a.y, b.x, b.y);
+    }
+  }
+  __device__ __forceinline__ void zero() { w = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void get(float f[8]) const {
+    f[0] = bf16_low(w.x), f[1] = bf16_high(w.x), f[2] = bf16_low(w.y), f[3] = bf16_high(w.y);
+    f[4] = bf16_low(w.z), f[5] = bf16_high(w.z), f[6] = bf16_low(w.w), f[7] = bf16_high(w.w);
+  }
+};
 
 template <bool NEXT>
 __device__ __forceinline__ void store8(uint16_t* y, int lo, int hi, const uint32_t w[4]) {
@@ -156,14 +172,30 @@ __device__ __forceinline__ void store8(uint16_t* y, int lo, int hi, const uint32
   }
 }
 
+// Turns that a position moves a pair by, modulo 1, in units of 2^-64: inv_freq / (2 pi) = m R 2^(E - 278) with the
+// float's mantissa m and exponent E and R = 2^128 / (2 pi).  A position times it, modulo 2^64, drops whole
+// turns exactly and leaves an error below 2^-32 turns at 2^31 - 1.
+__device__ __forceinline__ uint64_t turns_of(float inv_freq) {
+  constexpr uint64_t kHigh = 0x28BE60DB9391054Aull, kLow = 0x7F09D5F47D4D3770ull;
+  const uint32_t bits = __float_as_uint(inv_freq), e = bits >> 23 & 255u;
+  const uint64_t m = (bits & 0x7FFFFFu) | (e ? 0x800000u : 0u);
+  const uint64_t w0 = m * kLow, t = __umul64hi(m, kLow), w1 = m * kHigh + t;
+  const uint64_t w2 = __umul64hi(m, kHigh) + (w1 < t);
+  const int s = 214 - (int)max(e, 1u);  // m R shifted right by s
+  uint64_t f = 0;
+  if (s >= 128) f = w2 >> (s - 128);
+  else if (s > 64) f = w1 >> (s - 64) | w2 << (128 - s);
+  else if (s == 64) f = w1;
+  else if (s > 0) f = w0 >> s | w1 << (64 - s);
+  return bits >> 31 ? 0 - f : f;
+}
+
 // One row a block (and a share of its heads, gridDim.y), P lanes a head, eight columns a lane:
 //   y = x * rsqrt(mean(x^2) + eps) * w,   (a, b) -> s (a cos - b sin, b cos + a sin),
 // with both columns of a pair in one lane, so that the rotation needs no exchange and the norm one sum
-// over P lanes.  The angle pos * inv_freq is taken in turns and in 64 bits, where its whole turns are dropped
-// exactly; a float angle at position 10^6 would be off by 0.03.  The row's sines are found once, a
-// thread each, while the first heads are on their way.
+// over P lanes.  The row's sines are found once, a thread each, while the first heads are on their way.
 template <typename T, int P, bool NEXT>
-__global__ void __launch_bounds__(kRopeThreads) k_qkv_rope(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(kRopeThreads, sizeof(T) == 4 ? 6 : 8) k_qkv_rope(const __grid_constant__ RopeArgs a) {
   constexpr int kGroups = kRopeThreads / P;  // heads of a block at a time
   constexpr int U = 4;                       // heads of a lane on their way
   __shared__ __align__(16) float s_cos[kRopeMaxDim / 2], s_sin[kRopeMaxDim / 2];
@@ -171,42 +203,39 @@ __global__ void __launch_bounds__(kRopeThreads) k_qkv_rope(const __grid_constant
   pdl_enter();
   const int tid = threadIdx.x, g = tid / P, u = tid % P;
   const int64_t t = blockIdx.x;
-  const int heads = a.n_q + 2 * a.n_kv, first = blockIdx.y * kGroups + g, step = gridDim.y * kGroups;
+  const int heads = a.n_q + 2 * a.n_kv, first = blockIdx.y * kGroups, step = gridDim.y * kGroups;
   const bool live = 8 * u < a.d, turned = 8 * u < 2 * a.half;
   const int lo = !NEXT && turned ? 4 * u : 8 * u, hi = !NEXT && turned ? a.half + 4 * u : 8 * u + 4;
-  const int32_t pos = a.pos[t];
-  if (pos < 0) return;  // padding
   const T* x = static_cast<const T*>(a.x) + t * a.x_stride;
-  float f[U][8];
+  Eight<T, NEXT> f[U];
   auto ask = [&](int h0) {
 #pragma unroll
     for (int k = 0; k < U; ++k) {
-      const int h = h0 + k * step;
-      if (live && h < heads) {
-        load8<T, NEXT>(x + (int64_t)h * a.d, lo, hi, f[k]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[k][i] = 0.0f;
-      }
+      const int h = h0 + g + k * step;
+      if (live && h < heads) f[k].load(x + h * a.d, lo, hi);
+      else f[k].zero();
     }
   };
+  const int32_t pos = a.pos[t];
   ask(first);
-  float wq[8], wk[8];
+  const float freq = tid < a.half ? a.inv_freq[tid] : 0.0f;
+  int64_t place = a.cache[0] ? a.slot[t] : -1;
+  float w[2][8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int c = i < 4 ? lo + i : hi + i - 4;
-    wq[i] = a.q_norm && live ? a.q_norm[c] : 1.0f;
-    wk[i] = a.k_norm && live ? a.k_norm[c] : 1.0f;
+    w[0][i] = a.q_norm && live ? a.q_norm[c] : 1.0f;
+    w[1][i] = a.k_norm && live ? a.k_norm[c] : 1.0f;
   }
-  for (int j = tid; j < a.half; j += kRopeThreads) {
-    const double turns = (double)pos * ((double)a.inv_freq[j] * 0.15915494309189533576888);  // 1 / (2 pi)
+  if (pos < 0) return;  // padding
+  if (tid < a.half) {  // (half <= 128 threads)
+    const int32_t turn = (int32_t)((uint64_t)(uint32_t)pos * turns_of(freq) >> 32);
     float sn, cs;
-    sincospif(2.0f * (float)(turns - rint(turns)), &sn, &cs);
-    s_cos[j] = cs * a.rot_scale;
-    s_sin[j] = sn * a.rot_scale;
+    sincospif((float)turn * 4.656612873077393e-10f, &sn, &cs);  // 2^-31: half turns
+    s_cos[tid] = cs * a.rot_scale;
+    s_sin[tid] = sn * a.rot_scale;
   }
   if (a.cache[0] && tid == kRopeThreads - 1) {
-    int64_t place = a.slot[t];
     if (place != -1) {
       if (place < 0 || place >= a.n_slots) {
         atomicOr(a.status, 1);
@@ -219,55 +248,51 @@ __global__ void __launch_bounds__(kRopeThreads) k_qkv_rope(const __grid_constant
     s_place = place;
   }
   __syncthreads();
-  const int64_t place = a.cache[0] ? s_place : -1;
-  float4 cs = make_float4(1.0f, 1.0f, 1.0f, 1.0f), sn = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  place = a.cache[0] ? s_place : -1;
+  float c4[4] = {1.0f, 1.0f, 1.0f, 1.0f}, s4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   if (turned) {
-    cs = *reinterpret_cast<const float4*>(s_cos + 4 * u);
-    sn = *reinterpret_cast<const float4*>(s_sin + 4 * u);
+    const float4 cs = *reinterpret_cast<const float4*>(s_cos + 4 * u), sn = *reinterpret_cast<const float4*>(s_sin + 4 * u);
+    c4[0] = cs.x, c4[1] = cs.y, c4[2] = cs.z, c4[3] = cs.w;
+    s4[0] = sn.x, s4[1] = sn.y, s4[2] = sn.z, s4[3] = sn.w;
   }
   const float inv_d = 1.0f / (float)a.d;
-  for (int h0 = first - g; h0 < heads; h0 += U * step) {  // the same for all lanes of a warp
+  for (int h0 = first; h0 < heads; h0 += U * step) {  // the same for all lanes
 #pragma unroll
     for (int k = 0; k < U; ++k) {
       const int h = h0 + g + k * step;
       const int part = h < a.n_q ? 0 : h < a.n_q + a.n_kv ? 1 : 2;
-      float y[8];
-      float sum = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sum = fmaf(f[k][i], f[k][i], sum);
-#pragma unroll
-      for (int o = P / 2; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
       const bool norm = part == 0 ? a.q_norm != nullptr : part == 1 && a.k_norm != nullptr;
-      const float r = norm ? rsqrtf(fmaf(sum, inv_d, a.eps)) : 1.0f;
+      float y[8];
+      f[k].get(y);
+      if (__any_sync(0xFFFFFFFFu, norm)) {
+        float sum = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = norm ? f[k][i] * r * (part == 0 ? wq[i] : wk[i]) : f[k][i];
+        for (int i = 0; i < 8; ++i) sum = fmaf(y[i], y[i], sum);
+#pragma unroll
+        for (int o = P / 2; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        const float r = rsqrtf(fmaf(sum, inv_d, a.eps));
+        if (norm) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y[i] = y[i] * r * (part == 0 ? w[0][i] : w[1][i]);
+        }
+      }
       if (part < 2 && turned) {
-        if constexpr (NEXT) {
-          const float c4[4] = {cs.x, cs.y, cs.z, cs.w}, s4[4] = {sn.x, sn.y, sn.z, sn.w};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float p = y[2 * i], q = y[2 * i + 1];
-            y[2 * i] = fmaf(p, c4[i], -(q * s4[i]));
-            y[2 * i + 1] = fmaf(q, c4[i], p * s4[i]);
-          }
-        } else {
-          const float c4[4] = {cs.x, cs.y, cs.z, cs.w}, s4[4] = {sn.x, sn.y, sn.z, sn.w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float p = y[i], q = y[i + 4];
-            y[i] = fmaf(p, c4[i], -(q * s4[i]));
-            y[i + 4] = fmaf(q, c4[i], p * s4[i]);
-          }
+        for (int i = 0; i < 4; ++i) {
+          float &p = NEXT ? y[2 * i] : y[i], &q = NEXT ? y[2 * i + 1] : y[i + 4];
+          const float p0 = p, q0 = q;
+          p = fmaf(p0, c4[i], -(q0 * s4[i]));
+          q = fmaf(q0, c4[i], p0 * s4[i]);
         }
       }
       if (live && h < heads) {
-        const uint32_t w[4] = {pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7])};
+        const uint32_t b[4] = {pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7])};
         const int in = h - (part == 0 ? 0 : part == 1 ? a.n_q : a.n_q + a.n_kv);
-        if (a.out[part]) store8<NEXT>(a.out[part] + t * a.out_stride[part] + (int64_t)in * a.d, lo, hi, w);
-        if (part && place >= 0) store8<NEXT>(a.cache[part - 1] + place + in * a.head_stride, lo, hi, w);
+        if (a.out[part]) store8<NEXT>(a.out[part] + t * a.out_stride[part] + in * a.d, lo, hi, b);
+        if (part && place >= 0) store8<NEXT>(a.cache[part - 1] + place + in * a.head_stride, lo, hi, b);
       }
     }
-    ask(h0 + g + U * step);
+    ask(h0 + U * step);
   }
 }
 

@@ -13,7 +13,7 @@
 // The bonus is the first token whose cumulative mass passes u M.  For large vocabularies the borders between
 // tokens stand 2^-20 of the mass apart and closer, so the masses have to be good to far more than a float:
 // each is a pair of floats (2^-28 of its value, from the exponent's 48-bit product on), summed without loss, and the
-// sums meet in 64 bits.  (With plain floats one token in some hundreds would differ from the formula's.)
+// sums stay pairs of floats.  (With plain floats one token in some hundreds would differ from the formula's.)
 #include <cstdint>
 
 #include "w12_internal.cuh"
@@ -44,9 +44,9 @@ struct SampleArgs {
 };
 
 struct UnitStat {
-  float most;   // largest logit (-inf: none, NaN left out)
-  int32_t at;   // its first token, of greedy requests
-  double sum;   // of the masses, in units of 2^Ref::log of the largest
+  float most;    // largest logit (-inf: none, NaN left out)
+  int32_t at;    // its first token, of greedy requests
+  float sum[2];  // of the masses, in the units of the largest
 };
 
 __device__ __forceinline__ bool sample_request(const SampleArgs& a, int r, int64_t& off, int& n) {
@@ -98,45 +98,112 @@ __device__ __forceinline__ void two_sum(uint64_t a, uint64_t b, uint64_t& s, uin
   t = add2(sub2(a, sub2(s, v)), sub2(b, v));
 }
 
-// ---------------------------------------------------------------- masses
-
-// What the masses of a row, or of a part of it, are measured in: 2^log, near the mass of the largest logit
-// `most`.  Its exponent most * c is rounded to a whole number, so that rows' parts differ by powers of two
-// alone; where it is past 2^21 (a tiny temperature), the float product would keep no fraction, and the logits
-// are taken relative to `most` instead, which is exact for those that still have a mass.
-struct Ref {
-  float most, shift, whole;
-  double log;
+// A sum as an unevaluated pair of floats, |l| at most half of h's last place.
+struct Pair {
+  float h, l;
 };
 
-__device__ __forceinline__ Ref make_ref(float most, double c) {
-  Ref r{most, 0.0f, 0.0f, 0.0};
-  if (most == INFINITY || most == -INFINITY) {
-    r.log = most;
-  } else if (fabs(most * c) >= 2097152.0) {
-    r.shift = most;
-    r.log = most * c;
-  } else {
-    r.whole = rintf((float)(most * c));
-    r.log = r.whole;
-  }
-  return r;
+__device__ __forceinline__ Pair operator+(Pair a, Pair b) {
+  const float s = a.h + b.h, v = s - a.h, e = ((a.h - (s - v)) + (b.h - v)) + (a.l + b.l);
+  const float h = s + e;
+  return {h, e - (h - s)};
+}
+__device__ __forceinline__ Pair operator-(Pair a, Pair b) { return a + Pair{-b.h, -b.l}; }
+__device__ __forceinline__ Pair operator*(Pair a, float x) {
+  const float p = __fmul_rn(a.h, x), e = fmaf(a.l, x, fmaf(a.h, x, -p));
+  const float h = p + e;
+  return {h, e - (h - p)};
+}
+__device__ __forceinline__ bool operator>(Pair a, Pair b) { return a.h > b.h || (a.h == b.h && a.l > b.l); }
+__device__ __forceinline__ double wide(Pair a) { return (double)a.h + (double)a.l; }
+
+__device__ __forceinline__ Pair shuffle_xor(Pair a, int o) {
+  return {__shfl_xor_sync(0xFFFFFFFFu, a.h, o), __shfl_xor_sync(0xFFFFFFFFu, a.l, o)};
+}
+__device__ __forceinline__ Pair shuffle(Pair a, int lane) {
+  return {__shfl_sync(0xFFFFFFFFu, a.h, lane), __shfl_sync(0xFFFFFFFFu, a.l, lane)};
 }
 
-__device__ __forceinline__ double rescale(double from, double to) { return from == to ? 1.0 : exp2(from - to); }
+__device__ __forceinline__ Pair warp_sum(Pair a) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) a = a + shuffle_xor(a, o);
+  return a;
+}
+
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, o));
+  return x;
+}
+
+// The first lane at which the sum of the lanes' masses from lane 0 on passes the target, and the sum before it;
+// where none does, the last lane with a mass (or -1) and passed = false.
+struct Found {
+  int lane;
+  bool passed;
+  Pair before, all;
+};
+
+__device__ __forceinline__ Found find_lane(Pair mine, Pair target) {
+  const int lane = threadIdx.x & 31;
+  Pair upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const Pair t{__shfl_up_sync(0xFFFFFFFFu, upto.h, o), __shfl_up_sync(0xFFFFFFFFu, upto.l, o)};
+    if (lane >= o) upto = t + upto;
+  }
+  const uint32_t some = __ballot_sync(0xFFFFFFFFu, mine.h > 0.0f);
+  const uint32_t over = __ballot_sync(0xFFFFFFFFu, mine.h > 0.0f && upto > target);
+  Found f;
+  f.passed = over != 0;
+  f.lane = over ? __ffs((int)over) - 1 : 31 - __clz((int)some);
+  f.all = shuffle(upto, 31);
+  f.before = f.lane > 0 ? shuffle(upto, f.lane - 1) : Pair{0.0f, 0.0f};
+  return f;
+}
+
+// ---------------------------------------------------------------- masses
 
 // log2(e) / T as a pair of floats.
 struct Slope {
-  double c;
   float hi, lo;
 };
 
 __device__ __forceinline__ Slope make_slope(float T) {
+  const double c = 1.4426950408889634074 / (double)T;
   Slope s;
-  s.c = 1.4426950408889634074 / (double)T;
-  s.hi = (float)s.c;
-  s.lo = (float)(s.c - (double)s.hi);
+  s.hi = (float)c;
+  s.lo = (float)(c - (double)s.hi);
   return s;
+}
+
+// What the masses of a row, or of a part of it, are measured in: about the mass of its largest logit
+// `most`.  The exponent most * c is rounded to a whole number, so that parts of rows differ by powers of two
+// alone; where it is past 2^21 (a tiny temperature), the float product would keep no fraction, and the logits
+// are taken relative to `most` instead, which is exact for those that still have a mass.
+struct Ref {
+  float most, shift, whole;
+};
+
+__device__ __forceinline__ Ref make_ref(float most, const Slope& c) {
+  const float x = most * c.hi;
+  const bool far = fabsf(x) >= 2097152.0f && fabsf(most) < INFINITY;
+  return Ref{most, far ? most : 0.0f, far ? 0.0f : fabsf(most) == INFINITY ? most : rintf(x)};
+}
+
+__device__ __noinline__ float far_scale(Ref from, Ref to, Slope c) {
+  const double k = (double)c.hi + (double)c.lo;
+  const double a = from.shift != 0.0f ? (double)from.shift * k : (double)from.whole;
+  const double b = to.shift != 0.0f ? (double)to.shift * k : (double)to.whole;
+  return (float)exp2(a - b);
+}
+
+// One unit of `from` in units of `to`.
+__device__ __forceinline__ float scale_of(const Ref& from, const Ref& to, const Slope& c) {
+  if (from.most == to.most) return 1.0f;
+  if (from.shift != 0.0f || to.shift != 0.0f) return far_scale(from, to, c);
+  const float k = from.whole - to.whole;
+  return k >= -126.0f ? __int_as_float((127 + (int)fminf(k, 127.0f)) << 23) : 0.0f;
 }
 
 // The masses of two logits, h + lo each: 2^(x - whole), x = (l - shift) c.  With n whole and |g| <= 1/2 (and
@@ -179,12 +246,6 @@ __device__ __forceinline__ void mass2(uint64_t l, const Ref& r, const Slope& c, 
   }
 }
 
-// One mass in 64 bits.
-__device__ __forceinline__ double mass1(float l, const Ref& r, const Slope& c) {
-  if (r.most == INFINITY) return l == INFINITY ? 1.0 : 0.0;
-  return l > -INFINITY ? exp2(((double)l - (double)r.shift) * c.c - (double)r.whole) : 0.0;
-}
-
 // What a refusal leaves of a mass, max(e - tau q, 0), for two tokens.
 __device__ __forceinline__ void left2(uint64_t& h, uint64_t& lo, uint64_t q, float tau_hi, float tau_lo) {
   const uint64_t p = mul2(q, both(-tau_hi)), rest = fma2(q, both(tau_hi), p);  // tau_hi q = rest - p
@@ -206,23 +267,11 @@ struct Sum {
     s = n;
     rest = add2(rest, add2(t, lo));
   }
-  __device__ __forceinline__ double value() const {
+  __device__ __forceinline__ Pair value() const {
     const float2 a = split2(s), b = split2(rest);
-    return ((double)a.x + (double)a.y) + ((double)b.x + (double)b.y);
+    return Pair{a.x, b.x} + Pair{a.y, b.y};
   }
 };
-
-__device__ __forceinline__ double warp_sum(double x) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
-  return x;
-}
-
-__device__ __forceinline__ float warp_max(float x) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, o));
-  return x;
-}
 
 // Four tokens from i on, `fill` behind the end.
 __device__ __forceinline__ float4 four(const float* x, int64_t i, int64_t end, bool vec, float fill) {
@@ -278,16 +327,15 @@ __global__ void __launch_bounds__(kStatThreads) k_sample_stats(const __grid_cons
 #pragma unroll
       for (int k = 0; k < kUnit / 128; ++k) most = fmaxf(most, fmaxf(fmaxf(f[k].x, f[k].y), fmaxf(f[k].z, f[k].w)));
       most = warp_max(most);
-      UnitStat st{most, -1, 0.0};
+      UnitStat st{most, -1, {0.0f, 0.0f}};
       if (most > -INFINITY) {
         if (greedy) {
           int32_t at = 0x7FFFFFFF;
 #pragma unroll
           for (int k = 0; k < kUnit / 128; ++k) first_at(f[k], v0 + k * 128 + 4 * lane, most, at);
           st.at = __reduce_min_sync(0xFFFFFFFFu, at);
-          st.sum = 1.0;
         } else {
-          const Ref ref = make_ref(most, c.c);
+          const Ref ref = make_ref(most, c);
           Sum sum;
 #pragma unroll
           for (int k = 0; k < kUnit / 128; ++k) {
@@ -297,7 +345,9 @@ __global__ void __launch_bounds__(kStatThreads) k_sample_stats(const __grid_cons
             mass2(pair2(f[k].z, f[k].w), ref, c, h, lo);
             sum.add(h, lo);
           }
-          st.sum = warp_sum(sum.value());
+          const Pair all = warp_sum(sum.value());
+          st.sum[0] = all.h;
+          st.sum[1] = all.l;
         }
       }
       if (lane == 0) a.stat[row * a.units + unit] = st;
@@ -317,13 +367,13 @@ struct Command {
   int32_t refused;       // the node's children are taken out (no q)
   int32_t owner;         // kOpFind: the block that holds the bonus token
   float most, tau_hi, tau_lo;
-  double log, target;    // kOpFind: the mass before the bonus token in the owner's ranges, in units of 2^log
+  Pair target;           // kOpFind: the mass before the bonus token in the owner's ranges, in the units of `most`
 };
 
 struct Total {
   float most;
   int32_t at;
-  double log, sum;
+  Pair sum;
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -353,16 +403,17 @@ __device__ __forceinline__ void send(const S& from, S* to, uint32_t rank) {
 
 struct WalkShared {
   int32_t parent[kSampleMaxNodes], draft[kSampleMaxNodes], refused[kSampleMaxNodes];
-  float u[kSampleMaxNodes], l[kSampleMaxNodes], q[kSampleMaxNodes];  // of a node: its number, its token's logit and q at the parent
-  float most[kSampleMaxNodes];                                       // of rows with children
+  float u[kSampleMaxNodes], q[kSampleMaxNodes];  // of a node: its number, and q of its token at the parent
+  Pair mass[kSampleMaxNodes];                    // its token's mass at the parent (the logit at first)
+  float most[kSampleMaxNodes];                   // of rows with children
   int32_t at[kSampleMaxNodes];
-  double sum[kSampleMaxNodes];
+  Pair sum[kSampleMaxNodes];
   uint32_t inner[kSampleMaxNodes / 32];
   Command cmd;
   Total total[kMaxCluster];
-  double warp_log[kWalkWarps], warp_sum[kWalkWarps], group[kWalkWarps];
-  float warp_most[kWalkWarps];
-  int32_t warp_at[kWalkWarps], n_refused, last;
+  Total range[kWalkWarps];
+  Pair group[kWalkWarps];
+  int32_t n_refused, last;
 };
 
 // The masses of four tokens from i on.
@@ -394,38 +445,34 @@ __device__ __forceinline__ float chance(float q) { return fminf(fmaxf(q, 0.0f), 
 
 __device__ __forceinline__ float4 chance4(float4 q) { return make_float4(chance(q.x), chance(q.y), chance(q.z), chance(q.w)); }
 
-// One warp's range of one row: its sum in units of 2^log, or its first largest token (greedy).
-__device__ __forceinline__ void sum_range(const SampleArgs& a, const Command& cmd, const Slope& c, bool greedy, int64_t row,
-                                          int64_t v0, int64_t v1, const int32_t* refused, int n_refused, float& most_out,
-                                          int32_t& at_out, double& log_out, double& sum_out) {
+// One warp's range of one row: its sum, or its first largest token (greedy).
+__device__ __forceinline__ Total sum_range(const SampleArgs& a, const Command& cmd, const Slope& c, bool greedy, int64_t row,
+                                           int64_t v0, int64_t v1, const int32_t* refused, int n_refused) {
   const int lane = threadIdx.x & 31;
   const float* x = a.logits + row * a.stride;
   const float* p = a.probs ? a.probs + row * a.probs_stride : nullptr;
   constexpr int U = 4;
-  float most = cmd.most;
+  Total t{cmd.most, 0x7FFFFFFF, {0.0f, 0.0f}};
   if (!cmd.known) {
-    most = -INFINITY;
+    t.most = -INFINITY;
     for (int64_t i0 = v0; i0 < v1; i0 += 128 * U) {
       float4 f[U];
 #pragma unroll
       for (int k = 0; k < U; ++k) f[k] = four(x, i0 + k * 128 + 4 * lane, v1, a.vec, -INFINITY);
 #pragma unroll
-      for (int k = 0; k < U; ++k) most = fmaxf(most, fmaxf(fmaxf(f[k].x, f[k].y), fmaxf(f[k].z, f[k].w)));
+      for (int k = 0; k < U; ++k) t.most = fmaxf(t.most, fmaxf(fmaxf(f[k].x, f[k].y), fmaxf(f[k].z, f[k].w)));
     }
-    most = warp_max(most);
+    t.most = warp_max(t.most);
   }
-  most_out = most;
-  at_out = 0x7FFFFFFF;
-  log_out = -INFINITY;
-  sum_out = 0.0;
-  if (most == -INFINITY) return;
+  if (t.most == -INFINITY) return t;
   if (greedy) {
     int32_t at = 0x7FFFFFFF;
-    for (int64_t i = v0 + 4 * lane; i < v1 && at == 0x7FFFFFFF; i += 128) first_at(four(x, i, v1, a.vec, -INFINITY), i, most, at);
-    at_out = __reduce_min_sync(0xFFFFFFFFu, at);
-    return;
+    for (int64_t i = v0 + 4 * lane; i < v1 && at == 0x7FFFFFFF; i += 128) first_at(four(x, i, v1, a.vec, -INFINITY), i, t.most, at);
+    __syncwarp();
+    t.at = __reduce_min_sync(0xFFFFFFFFu, at);
+    return t;
   }
-  const Ref ref = make_ref(most, c.c);
+  const Ref ref = make_ref(t.most, c);
   Sum sum;
   for (int64_t i0 = v0; i0 < v1; i0 += 128 * U) {
     float4 f[U], q[U];
@@ -441,8 +488,25 @@ __device__ __forceinline__ void sum_range(const SampleArgs& a, const Command& cm
       sum.add(m.h[1], m.lo[1]);
     }
   }
-  log_out = ref.log;
-  sum_out = warp_sum(sum.value());
+  t.sum = warp_sum(sum.value());
+  return t;
+}
+
+// The parts' largest logit, their first token at it, and their sum in its units (a part a lane, 0 <= lane < n).
+__device__ __forceinline__ Total join(const Total* part, int n, const Slope& c, Pair& mine) {
+  const int lane = threadIdx.x & 31;
+  Total t{-INFINITY, 0x7FFFFFFF, {0.0f, 0.0f}};
+  if (lane < n) t = part[lane];
+  const float most = warp_max(t.most);
+  t.at = __reduce_min_sync(0xFFFFFFFFu, t.most == most ? t.at : 0x7FFFFFFF);
+  mine = {0.0f, 0.0f};
+  if (t.sum.h > 0.0f) {
+    const float k = scale_of(make_ref(t.most, c), make_ref(most, c), c);
+    mine = {t.sum.h * k, t.sum.l * k};
+  }
+  t.most = most;
+  t.sum = warp_sum(mine);
+  return t;
 }
 
 // The bonus token, by the block that holds it: first the warp's range, then 128 tokens, then the token.  The
@@ -452,69 +516,56 @@ __device__ __forceinline__ void find_token(const SampleArgs& a, WalkShared& s, c
                                            int32_t* bonus) {
   const Command& cmd = s.cmd;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  double before = 0.0, seen = 0.0;
-  int range = 0;
-  for (int w = 0; w < kWalkWarps; ++w) {
-    const double m = s.warp_sum[w] > 0.0 ? s.warp_sum[w] * rescale(s.warp_log[w], cmd.log) : 0.0;
-    if (!(m > 0.0)) continue;
-    range = w;
-    before = seen;
-    seen += m;
-    if (seen > cmd.target) break;
+  const Ref whole = make_ref(cmd.most, c);
+  Pair mine{0.0f, 0.0f};
+  float k = 1.0f;
+  if (lane < kWalkWarps && s.range[lane].sum.h > 0.0f) {
+    const Ref part = make_ref(s.range[lane].most, c);
+    k = scale_of(part, whole, c);
+    mine = {s.range[lane].sum.h * k, s.range[lane].sum.l * k};
   }
-  const double target = (cmd.target - before) * rescale(cmd.log, s.warp_log[range]);
-  const Ref ref = make_ref(s.warp_most[range], c.c);
+  const Found in = find_lane(mine, cmd.target);
+  const int range = max(in.lane, 0);
+  const Ref ref = make_ref(s.range[range].most, c);
+  Pair target = cmd.target - in.before;
+  k = scale_of(whole, ref, c);
+  target = {target.h * k, target.l * k};
   const int64_t v0 = first + range * a.range, v1 = min(a.V, v0 + a.range);
   const float* x = a.logits + row * a.stride;
   const float* p = a.probs ? a.probs + row * a.probs_stride : nullptr;
   const int n_refused = cmd.refused ? s.n_refused : 0;
   if (tid == 0) s.last = -1;
-  double run = 0.0;
   for (int64_t base = v0; base < v1; base += 128 * kWalkWarps) {
     const int64_t i = base + warp * 128 + 4 * lane;
     const float4 q = cmd.residual ? four(p, i, v1, a.probs_vec, 0.0f) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     const Four f = masses4(four(x, i, v1, a.vec, -INFINITY), chance4(q), i, ref, c, cmd, s.refused, n_refused);
-    double m[4];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const float2 h = split2(f.h[k]), lo = split2(f.lo[k]);
-      m[2 * k] = (double)h.x + (double)lo.x;
-      m[2 * k + 1] = (double)h.y + (double)lo.y;
-    }
-    const double mine = (m[0] + m[1]) + (m[2] + m[3]);
-    double upto = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const double t = __shfl_up_sync(0xFFFFFFFFu, upto, o);
-      if (lane >= o) upto += t;
-    }
-    if (lane == 31) s.group[warp] = upto;
+    const float2 h0 = split2(f.h[0]), l0 = split2(f.lo[0]), h1 = split2(f.h[1]), l1 = split2(f.lo[1]);
+    const Pair m[4] = {{h0.x, l0.x}, {h0.y, l0.y}, {h1.x, l1.x}, {h1.y, l1.y}};
+    mine = (m[0] + m[1]) + (m[2] + m[3]);
+    const Pair all = warp_sum(mine);
+    if (lane == 0) s.group[warp] = all;
     __syncthreads();
-    int hit = -1;
-    for (int g = 0; g < kWalkWarps; ++g) {
-      const double m_g = s.group[g];
-      if (m_g > 0.0 && run + m_g > target) {
-        hit = g;
-        break;
+    const Found at = find_lane(lane < kWalkWarps ? s.group[lane] : Pair{0.0f, 0.0f}, target);
+    if (at.passed && at.lane == warp) {
+      const Pair rest = target - at.before;
+      const Found l = find_lane(mine, rest);
+      if (lane == l.lane) {
+        Pair sum = l.before;
+        int found = -1, last = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          sum = sum + m[e];
+          if (m[e].h > 0.0f) last = e;
+          if (found < 0 && m[e].h > 0.0f && sum > rest) found = e;
+        }
+        *bonus = (int32_t)i + (found >= 0 ? found : last);
       }
-      run += m_g;
     }
+    if (at.passed) return;
+    target = target - at.all;
     int last = -1;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) last = m[k] > 0.0 ? k : last;
-    if (hit == warp) {
-      double at = run + (upto - mine);
-      int found = 4;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        at += m[k];
-        if (found == 4 && m[k] > 0.0 && at > target) found = k;
-      }
-      const uint32_t passed = __ballot_sync(0xFFFFFFFFu, found < 4), some = __ballot_sync(0xFFFFFFFFu, last >= 0);
-      if (passed ? lane == __ffs((int)passed) - 1 : some && lane == 31 - __clz((int)some))
-        *bonus = (int32_t)i + (passed ? found : last);
-    }
-    if (hit >= 0) return;
+    for (int e = 0; e < 4; ++e) last = m[e].h > 0.0f ? e : last;
     if (last >= 0) atomicMax(&s.last, (int32_t)i + last);
     __syncthreads();
   }
@@ -555,7 +606,7 @@ __global__ void __launch_bounds__(kWalkThreads) k_sample_walk(const __grid_const
       a.path_nodes[off + i] = -1;
       if (i > 0 && fine) {
         atomicOr(&s.inner[p >> 5], 1u << (p & 31));
-        s.l[i] = s.draft[i] >= 0 ? a.logits[(off + p) * a.stride + x] : 0.0f;
+        s.mass[i].h = s.draft[i] >= 0 ? a.logits[(off + p) * a.stride + x] : 0.0f;
         s.q[i] = s.draft[i] >= 0 && a.probs ? chance(a.probs[(off + p) * a.probs_stride + x]) : 0.0f;
       }
     }
@@ -567,27 +618,21 @@ __global__ void __launch_bounds__(kWalkThreads) k_sample_walk(const __grid_const
       if (!(s.inner[i >> 5] >> (i & 31) & 1u)) continue;
       const UnitStat* st = a.stat + (off + i) * a.units;
       float most = -INFINITY;
+      for (int k = lane; k < a.units; k += 32) most = fmaxf(most, st[k].most);
+      most = warp_max(most);
+      const Ref ref = make_ref(most, c);
       int32_t at = 0x7FFFFFFF;
-      double log = -INFINITY, sum = 0.0;
+      Pair sum{0.0f, 0.0f};
       for (int k = lane; k < a.units; k += 32) {
         const UnitStat u = st[k];
-        if (u.most == -INFINITY) continue;
-        if (u.most > most || (u.most == most && u.at < at)) at = u.at;
-        most = fmaxf(most, u.most);
-        const double l = make_ref(u.most, c.c).log, top = fmax(l, log);
-        sum = sum * rescale(log, top) + u.sum * rescale(l, top);
-        log = top;
+        if (u.most == most) at = min(at, u.at);
+        if (u.sum[0] > 0.0f) {
+          const float scale = scale_of(make_ref(u.most, c), ref, c);
+          sum = sum + Pair{u.sum[0] * scale, u.sum[1] * scale};
+        }
       }
-#pragma unroll
-      for (int o = 16; o; o >>= 1) {
-        const float m = __shfl_xor_sync(0xFFFFFFFFu, most, o);
-        const int32_t t = __shfl_xor_sync(0xFFFFFFFFu, at, o);
-        if (m > most || (m == most && t < at)) at = t;
-        most = fmaxf(most, m);
-        const double l = __shfl_xor_sync(0xFFFFFFFFu, log, o), u = __shfl_xor_sync(0xFFFFFFFFu, sum, o), top = fmax(l, log);
-        sum = sum * rescale(log, top) + u * rescale(l, top);
-        log = top;
-      }
+      at = __reduce_min_sync(0xFFFFFFFFu, at);
+      sum = warp_sum(sum);
       if (lane == 0) {
         s.most[i] = most;
         s.at[i] = at;
@@ -595,23 +640,31 @@ __global__ void __launch_bounds__(kWalkThreads) k_sample_walk(const __grid_const
       }
     }
     __syncthreads();
+    if (!greedy)
+      for (int i = 1 + tid; ok && i < n; i += kWalkThreads) {
+        uint64_t h, lo;
+        mass2(both(s.mass[i].h), make_ref(s.most[s.parent[i]], c), c, h, lo);
+        s.mass[i] = {split2(h).x, split2(lo).x};
+      }
+    __syncthreads();
   }
 
   // ---- the walk's state (first block, warp 0)
   enum { kWalk, kRefused, kSummed } stage = kWalk;
   int cur = 0, last = 0, depth = 0;
   bool inner = false, summed = false, spent = false, refused = false;
-  double tau = 0.0, Q = 1.0, M = 0.0, log = 0.0;
+  double tau = 0.0, Q = 1.0, M = 0.0;
+  Pair mine{0.0f, 0.0f};  // of a block, in its lane
+  Total all{};
   Command cmd{};
-  const double u_bonus = fminf(fmaxf(a.u_bonus[r], 0.0f), 0.99999994f);
+  const float u_bonus = fminf(fmaxf(a.u_bonus[r], 0.0f), 0.99999994f);
   auto enter = [&](int node) {
     cur = last = node;
     inner = s.inner[node >> 5] >> (node & 31) & 1u;
     summed = spent = refused = false;
     tau = 0.0;
     Q = 1.0;
-    M = inner ? s.sum[node] : 0.0;
-    log = inner ? make_ref(s.most[node], c.c).log : 0.0;
+    M = inner ? wide(s.sum[node]) : 0.0;
   };
   auto ask = [&](bool residual) {
     cmd.op = kOpSum;
@@ -634,20 +687,12 @@ __global__ void __launch_bounds__(kWalkThreads) k_sample_walk(const __grid_const
     if (rank == 0 && warp == 0) {
       cmd.op = kOpDone;
       if (ok) {
-        if (stage != kWalk && !greedy) {  // the blocks' sums
-          log = -INFINITY;
-          for (int k = 0; k < cluster; ++k) log = fmax(log, s.total[k].log);
-          M = 0.0;
-          for (int k = 0; k < cluster; ++k)
-            if (s.total[k].sum > 0.0) M += s.total[k].sum * rescale(s.total[k].log, log);
-        }
+        if (stage != kWalk) all = join(s.total, cluster, c, mine);  // the blocks' sums
         bool ends = stage == kSummed, asked = false;
         if (stage == kRefused) {
-          summed = true;
-          if (!(M > 0.0)) {  // nothing is left: the bonus comes from p as it was
-            spent = true;
-            summed = false;
-          }
+          M = wide(all.sum);
+          summed = M > 0.0;
+          spent = !summed;  // nothing is left: the bonus comes from p as it was
         }
         while (!ends && !asked) {
           int j = -1;  // the next child
@@ -666,25 +711,24 @@ __global__ void __launch_bounds__(kWalkThreads) k_sample_walk(const __grid_const
           if (greedy) {
             take = s.most[cur] > -INFINITY && x == s.at[cur];
           } else {
-            if (spent || !(s.sum[cur] > 0.0)) continue;
+            if (spent || !(s.sum[cur].h > 0.0f)) continue;
             bool twice = false;  // a sibling with this token was refused before
             for (int i0 = cur + 1; i0 < j && !twice; i0 += 32)
               twice = __any_sync(0xFFFFFFFFu, i0 + lane < j && s.parent[i0 + lane] == cur && s.draft[i0 + lane] == x);
             if (twice) continue;
-            const double e = mass1(s.l[j], make_ref(s.most[cur], c.c), c), u = s.u[j], q = s.q[j];
-            take = a.probs ? Q > 0.0 && u * (q / Q) * M < e - tau * q : u * M < e;
+            const double e = wide(s.mass[j]), u = s.u[j], q = s.q[j];
+            take = a.probs ? Q > 0.0 && u * q * M < (e - tau * q) * Q : u * M < e;
             if (!take) {
               if (!a.probs) {
                 refused = true;
                 M = fmax(M - e, 0.0);
               } else if (q > 0.0 && Q > 0.0) {
-                tau += M / Q;
+                tau += Q == 1.0 ? M : M / Q;
                 Q -= q;
                 ask(true);
                 stage = kRefused;
                 asked = true;
               }
-              continue;
             }
           }
           if (take) {
@@ -694,48 +738,33 @@ __global__ void __launch_bounds__(kWalkThreads) k_sample_walk(const __grid_const
           }
         }
         if (ends) {
-          if (lane == 0 && stage != kSummed) a.path_len[r] = depth;
-          if (greedy) {
-            if (inner || stage == kSummed) {
-              float most = inner ? s.most[cur] : -INFINITY;
-              int32_t at = inner ? s.at[cur] : -1;
-              if (!inner)
-                for (int k = 0; k < cluster; ++k)
-                  if (s.total[k].most > most) {  // the blocks' tokens rise
-                    most = s.total[k].most;
-                    at = s.total[k].at;
-                  }
-              if (lane == 0) a.bonus[r] = most > -INFINITY ? at : -1;
-              cmd.op = kOpDone;
-            } else {
+          if (stage != kSummed) {
+            if (lane == 0) a.path_len[r] = depth;
+            if (greedy && inner) {
+              if (lane == 0) a.bonus[r] = s.most[cur] > -INFINITY ? s.at[cur] : -1;
+            } else if (!summed) {
               ask(false);
               stage = kSummed;
             }
-          } else if (stage != kSummed && !summed) {
-            ask(false);
-            stage = kSummed;
-          } else if (!(M > 0.0)) {
+          } else if (greedy) {
+            if (lane == 0) a.bonus[r] = all.most > -INFINITY ? all.at : -1;
+          } else if (!(all.sum.h > 0.0f)) {
             if (cmd.refused) {  // all that had a mass was refused: p as it was
               refused = false;
               ask(false);
-            } else {
-              if (lane == 0) a.bonus[r] = -1;
-              cmd.op = kOpDone;
+            } else if (lane == 0) {
+              a.bonus[r] = -1;
             }
           } else {
+            summed = true;
+          }
+          if (summed && !greedy) {
+            const Pair target = all.sum * u_bonus;
+            const Found f = find_lane(mine, target);
             cmd.op = kOpFind;
-            cmd.log = log;
-            const double target = u_bonus * M;
-            double before = 0.0, seen = 0.0;
-            for (int k = 0; k < cluster; ++k) {
-              const double m = s.total[k].sum > 0.0 ? s.total[k].sum * rescale(s.total[k].log, log) : 0.0;
-              if (!(m > 0.0)) continue;
-              cmd.owner = k;
-              before = seen;
-              seen += m;
-              if (seen > target) break;
-            }
-            cmd.target = target - before;
+            cmd.most = all.most;
+            cmd.owner = f.lane;
+            cmd.target = target - f.before;
           }
         }
       }
@@ -757,32 +786,14 @@ __global__ void __launch_bounds__(kWalkThreads) k_sample_walk(const __grid_const
       }
       __syncthreads();
     }
-    {
-      const int64_t v0 = first + warp * a.range, v1 = min(a.V, v0 + a.range);
-      float most;
-      int32_t at;
-      double wlog, wsum;
-      sum_range(a, s.cmd, c, greedy, row, v0, v1, s.refused, s.cmd.refused ? s.n_refused : 0, most, at, wlog, wsum);
-      if (lane == 0) {
-        s.warp_most[warp] = most;
-        s.warp_at[warp] = at;
-        s.warp_log[warp] = wlog;
-        s.warp_sum[warp] = wsum;
-      }
-    }
+    const int64_t v0 = first + warp * a.range, v1 = min(a.V, v0 + a.range);
+    const Total t = sum_range(a, s.cmd, c, greedy, row, v0, v1, s.refused, s.cmd.refused ? s.n_refused : 0);
+    if (lane == 0) s.range[warp] = t;
     __syncthreads();
-    if (tid == 0) {
-      Total t{-INFINITY, -1, -INFINITY, 0.0};
-      for (int w = 0; w < kWalkWarps; ++w) {
-        if (s.warp_most[w] > t.most) {
-          t.most = s.warp_most[w];
-          t.at = s.warp_at[w];
-        }
-        t.log = fmax(t.log, s.warp_log[w]);
-      }
-      for (int w = 0; w < kWalkWarps; ++w)
-        if (s.warp_sum[w] > 0.0) t.sum += s.warp_sum[w] * rescale(s.warp_log[w], t.log);
-      send(t, &s.total[rank], 0);
+    if (warp == 0) {
+      Pair part;
+      const Total sum = join(s.range, kWalkWarps, c, part);
+      if (lane == 0) send(sum, &s.total[rank], 0);
     }
     cluster_sync();
   }
