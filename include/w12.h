@@ -700,10 +700,11 @@ W12_API int logits_verify(const float* logits, int64_t stride, int64_t M, int64_
  * Row m of logits (V at logits + m*stride) is node m's; a token's probability at the node is p = softmax(logits /
  * temperature[r]) (NULL: 1).  A temperature below 1e-5 is the limit at zero: p is 1 at the largest logit, the
  * lowest token among equals.  -inf and NaN leave a token out (logits_process writes -inf for what a
- * grammar forbids; a top-k or top-p rule is written the same way); +inf tokens share p evenly.
+ * grammar forbids; a top-k or top-p rule is written the same way), as does a p below 2^-100 of the row's
+ * largest; +inf tokens share p evenly.
  * draft_probs (row m at draft_probs + m*probs_stride; NULL: below) holds the drafter's probabilities q at node m, from
  * which m's children were drawn without replacement: each from what its earlier siblings left, renormalised
- * (NaN and values outside 0..1 count as the nearest of them).  q is taken as given and should sum to 1.
+ * (NaN and negative values count as 0).  q is taken as given and should sum to 1.
  * From the root on, the children of the last accepted node are tried in index order, x = draft[c]:
  *   c is accepted if u[c] * q(x) / Q < p(x), and the walk goes on below it;
  *   else p becomes max(p - q / Q, 0) divided by its sum, q(x) = 0, and Q (1 at first) becomes Q - q(x).

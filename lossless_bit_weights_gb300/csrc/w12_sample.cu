@@ -15,6 +15,7 @@
 // each is a pair of floats (2^-28 of its value, from the exponent's 48-bit product on), summed without loss, and the
 // sums stay pairs of floats.  (With plain floats one token in some hundreds would differ from the formula's.)
 #include <cstdint>
+#include <type_traits>
 
 #include "w12_internal.cuh"
 #include "w12_pdl.cuh"
@@ -25,11 +26,16 @@ namespace {
 constexpr int kSampleMaxNodes = 1024;  // nodes of one request
 constexpr int kUnit = 1024;            // tokens of a row that a warp sums at once
 constexpr int kStatThreads = 256;
+constexpr int kStatTile = 1024;       // nodes whose rows a column of blocks takes
+constexpr int kStatRequests = 1024;   // offsets that fit in shared memory
 constexpr int kWalkThreads = 512;
 constexpr int kWalkWarps = kWalkThreads / 32;
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;
 constexpr int32_t kSampleBadRequest = 1;
 constexpr float kGreedy = 1e-5f;       // temperatures below are the limit at zero
+constexpr float kMost = 3.402823466e38f;  // the largest float
+constexpr float kLeast = 7.888609052210118e-31f;  // 2^-100: a smaller mass counts as none
+constexpr float kSlow = 1e-36f;        // with slopes below, no two floats' masses differ by 2^-100
 
 struct SampleArgs {
   const float *logits, *probs;
@@ -39,14 +45,14 @@ struct SampleArgs {
   int32_t *path_len, *path_nodes, *bonus, *status;
   struct UnitStat* stat;  // [M][units], of rows with children
   int64_t range;          // tokens of a warp in the walk, a multiple of 128
-  int32_t n_req, units, parts;
+  int32_t n_req, units;
   bool vec, probs_vec;    // rows allow 16-byte loads
 };
 
 struct UnitStat {
-  float most;    // largest logit (-inf: none, NaN left out)
-  int32_t at;    // its first token, of greedy requests
-  float sum[2];  // of the masses, in the units of the largest
+  float most;   // largest logit (-inf: none, NaN left out)
+  int32_t at;   // its first token, of greedy requests
+  float sum;    // of the masses in the units of the largest, to 2^-18
 };
 
 __device__ __forceinline__ bool sample_request(const SampleArgs& a, int r, int64_t& off, int& n) {
@@ -91,13 +97,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 }
 __device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) { return fma2(b, both(-1.0f), a); }
 
-// s + t = a + b exactly (no order of sizes needed)
-__device__ __forceinline__ void two_sum(uint64_t a, uint64_t b, uint64_t& s, uint64_t& t) {
-  s = add2(a, b);
-  const uint64_t v = sub2(s, a);
-  t = add2(sub2(a, sub2(s, v)), sub2(b, v));
-}
-
 // A sum as an unevaluated pair of floats, |l| at most half of h's last place.
 struct Pair {
   float h, l;
@@ -114,8 +113,18 @@ __device__ __forceinline__ Pair operator*(Pair a, float x) {
   const float h = p + e;
   return {h, e - (h - p)};
 }
+__device__ __forceinline__ Pair operator*(Pair a, Pair b) {
+  const float p = __fmul_rn(a.h, b.h), e = fmaf(a.h, b.l, fmaf(a.l, b.h, fmaf(a.h, b.h, -p)));
+  const float h = p + e;
+  return {h, e - (h - p)};
+}
+__device__ __forceinline__ Pair operator/(Pair a, Pair b) {
+  const float x = a.h / b.h;
+  const Pair rest = a - b * x;
+  const float y = rest.h / b.h, h = x + y;
+  return {h, y - (h - x)};
+}
 __device__ __forceinline__ bool operator>(Pair a, Pair b) { return a.h > b.h || (a.h == b.h && a.l > b.l); }
-__device__ __forceinline__ double wide(Pair a) { return (double)a.h + (double)a.l; }
 
 __device__ __forceinline__ Pair shuffle_xor(Pair a, int o) {
   return {__shfl_xor_sync(0xFFFFFFFFu, a.h, o), __shfl_xor_sync(0xFFFFFFFFu, a.l, o)};
@@ -125,7 +134,7 @@ __device__ __forceinline__ Pair shuffle(Pair a, int lane) {
 }
 
 __device__ __forceinline__ Pair warp_sum(Pair a) {
-#pragma unroll
+#pragma unroll 1
   for (int o = 16; o; o >>= 1) a = a + shuffle_xor(a, o);
   return a;
 }
@@ -147,7 +156,7 @@ struct Found {
 __device__ __forceinline__ Found find_lane(Pair mine, Pair target) {
   const int lane = threadIdx.x & 31;
   Pair upto = mine;
-#pragma unroll
+#pragma unroll 1
   for (int o = 1; o < 32; o <<= 1) {
     const Pair t{__shfl_up_sync(0xFFFFFFFFu, upto.h, o), __shfl_up_sync(0xFFFFFFFFu, upto.l, o)};
     if (lane >= o) upto = t + upto;
@@ -170,25 +179,29 @@ struct Slope {
 };
 
 __device__ __forceinline__ Slope make_slope(float T) {
-  const double c = 1.4426950408889634074 / (double)T;
-  Slope s;
-  s.hi = (float)c;
-  s.lo = (float)(c - (double)s.hi);
-  return s;
+  const float x = __fdiv_rn(1.44269502162933349609375f, T);
+  // (the first quotient's remainder is exact)
+  const float rest = fmaf(-x, T, 1.44269502162933349609375f) + 1.925963033500011e-8f;
+  return T < INFINITY ? Slope{x, __fdiv_rn(rest, T)} : Slope{0.0f, 0.0f};
 }
 
 // What the masses of a row, or of a part of it, are measured in: about the mass of its largest logit
 // `most`.  The exponent most * c is rounded to a whole number, so that parts of rows differ by powers of two
-// alone; where it is past 2^21 (a tiny temperature), the float product would keep no fraction, and the logits
-// are taken relative to `most` instead, which is exact for those that still have a mass.
+// alone; where it is past 2^16 (a tiny temperature), the float product would keep too little of a fraction, and the
+// logits are taken relative to `most` instead, which is exact for those that still have a mass.
 struct Ref {
   float most, shift, whole;
 };
 
 __device__ __forceinline__ Ref make_ref(float most, const Slope& c) {
   const float x = most * c.hi;
-  const bool far = fabsf(x) >= 2097152.0f && fabsf(most) < INFINITY;
+  const bool far = fabsf(x) >= 65536.0f && fabsf(most) < INFINITY;
   return Ref{most, far ? most : 0.0f, far ? 0.0f : fabsf(most) == INFINITY ? most : rintf(x)};
+}
+
+// The smallest logit, less the shift, that is looked at: 2^-125 of a unit.
+__device__ __forceinline__ float least_of(const Ref& r, const Slope& c) {
+  return fmaxf((r.whole - 125.0f) / c.hi, -kMost);
 }
 
 __device__ __noinline__ float far_scale(Ref from, Ref to, Slope c) {
@@ -206,70 +219,128 @@ __device__ __forceinline__ float scale_of(const Ref& from, const Ref& to, const 
   return k >= -126.0f ? __int_as_float((127 + (int)fminf(k, 127.0f)) << 23) : 0.0f;
 }
 
-// The masses of two logits, h + lo each: 2^(x - whole), x = (l - shift) c.  With n whole and |g| <= 1/2 (and
-// a little) 2^x = 2^n 2^g, 2^g = 1 + g ln 2 + g^2 (Taylor's terms to the eighth; 2^-32 is left out), whose first
-// two terms are pairs of floats.  Below 2^-125 (and for -inf and NaN) a mass is 0.
-__device__ __forceinline__ void mass2(uint64_t l, const Ref& r, const Slope& c, uint64_t& h, uint64_t& lo) {
-  constexpr float kLn2 = 0.6931471824645996f, kLn2Rest = -1.904654299957768e-9f;
+// 2^(j/32) as a float, and the rest of it as a part of that float.
+__device__ const float2 kRoots[32] = {
+    {1.0f, 0.0f}, {1.0218972f, -4.70845762e-08f}, {1.04427373f, 4.62854715e-08f}, {1.06714046f, -5.56042252e-08f},
+    {1.09050775f, -1.19921575e-08f}, {1.1143868f, -4.87760623e-08f}, {1.13878858f, 4.72978243e-08f}, {1.1637249f, -3.48144269e-08f},
+    {1.18920708f, 3.19341815e-08f}, {1.21524739f, -2.68866653e-08f}, {1.24185777f, 3.62105723e-08f}, {1.26905096f, 1.11842102e-09f},
+    {1.29683959f, -3.09907193e-08f}, {1.32523668f, -2.63830096e-08f}, {1.35425556f, -7.47521334e-09f}, {1.38390994f, -4.24563567e-08f},
+    {1.41421354f, 1.71142709e-08f}, {1.44518077f, 2.30019666e-08f}, {1.47682619f, -3.04768335e-08f}, {1.50916445f, -1.65385377e-08f},
+    {1.54221082f, 5.23333421e-09f}, {1.5759809f, -3.5920646e-08f}, {1.61049032f, 6.10759177e-09f}, {1.64575553f, -3.11405444e-08f},
+    {1.68179286f, -1.47196051e-08f}, {1.71861935f, -2.82181016e-08f}, {1.75625217f, -5.25879518e-09f}, {1.79470909f, -6.36038733e-09f},
+    {1.8340081f, -6.12825968e-09f}, {1.87416768f, -2.48804088e-08f}, {1.91520655f, 5.14060927e-09f}, {1.95714414f, -8.69726691e-09f}};
+
+// A row's constants of mass2; lane j keeps the j-th root, its exponent lowered by the unit's and by what the
+// bits of t bring with them.
+struct Scale {
+  float shift, least, hi, lo;
+  uint32_t root;
+  float rest;
+  bool endless;  // the largest logit is +inf: the infinite ones alone have a mass, alike
+};
+
+constexpr float kMagic = 393216.0f;  // 1.5 * 2^18: a float near it holds 32nds, its bits are kMagicBits + 32 x
+constexpr uint32_t kMagicBits = 0x48C00000u;
+constexpr float kExp1 = 0.6931471805599453f, kExp2 = 0.24022847f, kExp3 = 5.550410866482158e-2f;
+
+// (float bits of t) * 2^18 + this is the mass's float: j's root at the exponent of the whole part
+__device__ __forceinline__ uint32_t root_bits(float root, int j, float whole) {
+  return __float_as_uint(root) - ((uint32_t)j << 18) - ((uint32_t)(int32_t)whole << 23) - (kMagicBits << 18);
+}
+
+__device__ __forceinline__ Scale make_scale(const Ref& r, const Slope& c, float2 root) {
+  Scale s;
+  s.shift = r.shift;
+  s.hi = c.hi;
+  s.lo = c.lo;
+  s.endless = r.most == INFINITY;
+  s.least = s.endless ? 0.0f : least_of(r, c);
+  s.root = root_bits(root.x, threadIdx.x & 31, s.endless ? 0.0f : r.whole);
+  s.rest = root.y;
+  return s;
+}
+
+// The masses of two logits, h + lo each: 2^(x - whole), x = (l - shift) c.  With 32 x rounded to n,
+// 2^x = 2^(n / 32) 2^g, |g| <= 1/64; g comes from fused products without their rounding, and 2^g - 1 = g (ln 2 +
+// g (a + g b)) to 2^-33 (Taylor's terms, the second raised by 0.83 of the fourth's most), so that with the root's rest
+// a mass is good to 2^-30.  All lanes of a warp take part.  Without ANY the row has neither shift nor end,
+// and what has no mass comes out as 2^-125 or so.
+template <bool ANY>
+__device__ __forceinline__ void mass2(uint64_t l, const Scale& c, uint64_t& h, uint64_t& lo) {
+  const float2 given = split2(l);
+  if (ANY) l = add2(l, both(-c.shift));
   const float2 lf = split2(l);
-  l = add2(l, both(-r.shift));
-  const uint64_t p = mul2(l, both(c.hi));
-  const uint64_t npl = fma2(l, both(-c.lo), fma2(l, both(-c.hi), p));  // minus the product's rest
-  const float2 pf = split2(p);
-  const float least = r.whole - 125.0f;
-  const uint64_t q = pair2(fmaxf(pf.x, least), fmaxf(pf.y, least));
-  const uint64_t magic = both(12582912.0f);  // 1.5 * 2^23: the sum's low bits are the rounded exponent
-  const uint64_t t = add2(q, magic), f = sub2(q, sub2(t, magic));
-  const uint64_t g = sub2(f, npl), gl = sub2(sub2(f, g), npl);
-  uint64_t w = both(1.321548679014431e-6f);
-  w = fma2(w, g, both(1.5252733804059841e-5f));
-  w = fma2(w, g, both(1.540353039338161e-4f));
-  w = fma2(w, g, both(1.3333558146428443e-3f));
-  w = fma2(w, g, both(9.618129107628477e-3f));
-  w = fma2(w, g, both(5.550410866482158e-2f));
-  w = fma2(w, g, both(2.4022650695910072e-1f));
-  w = mul2(w, mul2(g, g));
-  const uint64_t tt = mul2(g, both(kLn2));
-  const uint64_t ntl = fma2(gl, both(-kLn2), fma2(g, both(-kLn2Rest), fma2(g, both(-kLn2), tt)));
-  const uint64_t s = add2(tt, w), sl = sub2(add2(sub2(tt, s), w), ntl);
-  const uint64_t e = add2(both(1.0f), s), el = add2(add2(sub2(both(1.0f), e), s), sl);
+  l = pair2(fmaxf(lf.x, c.least), fmaxf(lf.y, c.least));
+  const uint64_t t = fma2(l, both(c.hi), both(kMagic));
+  const uint64_t g = fma2(l, both(c.lo), fma2(l, both(c.hi), sub2(both(kMagic), t)));
   const float2 tf = split2(t);
-  const uint32_t base = (127u - (uint32_t)(int32_t)r.whole - 0x4B400000u) << 23;  // 2^(n - whole) as a float
-  const uint64_t two = pair2(__uint_as_float((__float_as_uint(tf.x) << 23) + base), __uint_as_float((__float_as_uint(tf.y) << 23) + base));
-  const float2 hf = split2(mul2(e, two)), gf = split2(mul2(el, two));
-  const bool x = pf.x > least, y = pf.y > least;
-  h = pair2(x ? hf.x : 0.0f, y ? hf.y : 0.0f);
-  lo = pair2(x ? gf.x : 0.0f, y ? gf.y : 0.0f);
-  if (r.most == INFINITY) {  // the infinite ones alone, alike
-    h = pair2(lf.x == INFINITY ? 1.0f : 0.0f, lf.y == INFINITY ? 1.0f : 0.0f);
+  const uint32_t tx = __float_as_uint(tf.x), ty = __float_as_uint(tf.y);
+  const uint64_t rest = pair2(__shfl_sync(0xFFFFFFFFu, c.rest, tx), __shfl_sync(0xFFFFFFFFu, c.rest, ty));
+  float x = __uint_as_float((tx << 18) + __shfl_sync(0xFFFFFFFFu, c.root, tx));
+  float y = __uint_as_float((ty << 18) + __shfl_sync(0xFFFFFFFFu, c.root, ty));
+  const uint64_t w = fma2(fma2(fma2(both(kExp3), g, both(kExp2)), g, both(kExp1)), g, rest);
+  if (ANY) {  // (at an endless temperature the clamp does not tell -inf)
+    x = given.x >= -kMost ? x : 0.0f;
+    y = given.y >= -kMost ? y : 0.0f;
+  }
+  h = pair2(x, y);
+  lo = mul2(h, w);
+  if (ANY && c.endless) {
+    h = pair2(given.x == INFINITY ? 1.0f : 0.0f, given.y == INFINITY ? 1.0f : 0.0f);
     lo = both(0.0f);
   }
 }
 
-// What a refusal leaves of a mass, max(e - tau q, 0), for two tokens.
+// Masses below 2^-100 are left out.
+__device__ __forceinline__ void least2(uint64_t& h, uint64_t& lo) {
+  const float2 hf = split2(h), gf = split2(lo);
+  const bool x = hf.x > kLeast, y = hf.y > kLeast;
+  h = pair2(x ? hf.x : 0.0f, y ? hf.y : 0.0f);
+  lo = pair2(x ? gf.x : 0.0f, y ? gf.y : 0.0f);
+}
+
+// A mass to 2^-20 or so: 2^((l - most) c + (most c - whole)).
+struct Rough {
+  float most, slope, start, least;
+};
+
+__device__ __forceinline__ Rough make_rough(const Ref& r, const Slope& c) {
+  Rough o{r.most, c.hi, 0.0f, fmaxf(-125.0f / c.hi, -kMost)};
+  if (r.shift == 0.0f && r.most < INFINITY) o.start = fmaf(r.most, c.lo, fmaf(r.most, c.hi, -r.whole));
+  return o;
+}
+
+__device__ __forceinline__ float rough(float l, const Rough& r) {
+  const float d = l - r.most;
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fmaf(d, r.slope, r.start)));
+  return d >= r.least ? e : 0.0f;
+}
+
+// What a refusal leaves of a mass, max(e - tau q, 0), for two tokens; less than 2^-100 is nothing.  (Where
+// something is left, h is the larger or the difference exact, so its rounding comes back from three operations.)
 __device__ __forceinline__ void left2(uint64_t& h, uint64_t& lo, uint64_t q, float tau_hi, float tau_lo) {
   const uint64_t p = mul2(q, both(-tau_hi)), rest = fma2(q, both(tau_hi), p);  // tau_hi q = rest - p
-  uint64_t s, t;
-  two_sum(h, p, s, t);
-  t = add2(t, fma2(q, both(-tau_lo), sub2(lo, rest)));
-  const float2 sf = split2(s), tf = split2(t);
-  const bool x = sf.x + tf.x > 0.0f, y = sf.y + tf.y > 0.0f;
+  const uint64_t s = add2(h, p);
+  const uint64_t t = add2(sub2(p, sub2(s, h)), fma2(q, both(-tau_lo), sub2(lo, rest)));
+  const float2 sf = split2(s), tf = split2(t), all = split2(add2(s, t));
+  const bool x = all.x > kLeast, y = all.y > kLeast;
   h = pair2(x ? sf.x : 0.0f, y ? sf.y : 0.0f);
   lo = pair2(x ? tf.x : 0.0f, y ? tf.y : 0.0f);
 }
 
-// A running sum of pairs without loss but in its last part, two at a time.
+// A running sum of pairs, two at a time.  It starts at 4, above every mass, so that an addition's rounding
+// comes back from three operations.
 struct Sum {
-  uint64_t s = 0, rest = 0;
+  uint64_t s = both(4.0f), rest = both(0.0f);
   __device__ __forceinline__ void add(uint64_t h, uint64_t lo) {
-    uint64_t n, t;
-    two_sum(s, h, n, t);
+    const uint64_t n = add2(s, h), t = sub2(h, sub2(n, s));
     s = n;
     rest = add2(rest, add2(t, lo));
   }
   __device__ __forceinline__ Pair value() const {
     const float2 a = split2(s), b = split2(rest);
-    return Pair{a.x, b.x} + Pair{a.y, b.y};
+    return (Pair{a.x, b.x} - Pair{4.0f, 0.0f}) + (Pair{a.y, b.y} - Pair{4.0f, 0.0f});
   }
 };
 
@@ -293,68 +364,114 @@ __device__ __forceinline__ void first_at(const float4& f, int64_t i, float most,
 // ---------------------------------------------------------------- rows with children
 
 // Largest logit and mass of every 1024 tokens of the rows whose nodes have children (what the walk asks of a
-// node it passes), a warp each, all 128 bytes a lane on their way at once.  Bound by the logits read once.
-__global__ void __launch_bounds__(kStatThreads) k_sample_stats(const __grid_constant__ SampleArgs a) {
+// node it passes).  Every block of a tile of nodes makes the list of its rows with children, and the tile's
+// warps share (row, 1024 tokens) evenly, 128 bytes a lane on their way at once and the next 4 KB coming into
+// L2.  Bound by the logits read once.  The masses are plain floats here: with a bound of 2^-18 on
+// their sums nearly all decisions are certain, and the walk sums again for the others.
+__global__ void __launch_bounds__(kStatThreads, 3) k_sample_stats(const __grid_constant__ SampleArgs a) {
   pdl_enter();
-  __shared__ uint32_t inner[kSampleMaxNodes / 32];
-  const int r = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
-  const int unit = blockIdx.x * (kStatThreads / 32) + (tid >> 5);
-  int64_t off;
-  int n;
-  if (!sample_request(a, r, off, n) || n < 2) return;
-  if (tid < kSampleMaxNodes / 32) inner[tid] = 0;
+  __shared__ int32_t offsets[kStatRequests + 1];
+  __shared__ uint32_t inner[kStatTile / 32];
+  __shared__ uint16_t request[kStatTile], list[kStatTile];
+  __shared__ int rows;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int64_t m0 = (int64_t)blockIdx.y * kStatTile, m1 = min(a.M, m0 + kStatTile + kSampleMaxNodes);
+  const bool here = a.req_offsets && a.n_req <= kStatRequests;
+  if (tid < kStatTile / 32) inner[tid] = 0;
+  if (here)
+#pragma unroll 1
+    for (int r = tid; r <= a.n_req; r += kStatThreads) offsets[r] = a.req_offsets[r];
   __syncthreads();
-  for (int i = 1 + tid; i < n; i += kStatThreads) {
-    const int32_t p = a.parent[off + i];
-    if (p >= 0 && p < i) atomicOr(&inner[p >> 5], 1u << (p & 31));
+  const int32_t* o = here ? offsets : a.req_offsets;
+#pragma unroll 1
+  for (int64_t m = m0 + tid; m < m1; m += kStatThreads) {
+    const int32_t p = a.parent[m];
+    int lo = 0, hi = a.n_req;  // the last request that starts at or before node m
+#pragma unroll 1
+    while (o && hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (o[mid] <= m) lo = mid; else hi = mid;
+    }
+    const int64_t off = o ? o[lo] : 0, end = o ? o[lo + 1] : a.M;
+    if (off < 0 || off > m || end <= m || end > a.M || end - off > kSampleMaxNodes || p < 0 || p >= m - off) continue;
+    const int64_t at = off + p - m0;
+    if (at >= 0 && at < kStatTile) {
+      request[at] = (uint16_t)lo;  // (all children write the same)
+      atomicOr(&inner[at >> 5], 1u << (at & 31));
+    }
   }
   __syncthreads();
-  if (unit >= a.units) return;
-  const float T = a.temperature ? a.temperature[r] : 1.0f;
-  const bool greedy = T < kGreedy;
-  const Slope c = make_slope(greedy ? 1.0f : T);
-  const int64_t v0 = (int64_t)unit * kUnit, v1 = min(a.V, v0 + kUnit);
-  int nth = 0;
-  for (int w = 0; w * 32 < n; ++w)
-    for (uint32_t m = inner[w]; m; m &= m - 1) {
-      if (nth++ % a.parts != (int)blockIdx.z) continue;
-      const int64_t row = off + w * 32 + __ffs((int)m) - 1;
-      const float* x = a.logits + row * a.stride;
-      float4 f[kUnit / 128];
-#pragma unroll
-      for (int k = 0; k < kUnit / 128; ++k) f[k] = four(x, v0 + k * 128 + 4 * lane, v1, a.vec, -INFINITY);
-      float most = -INFINITY;
-#pragma unroll
-      for (int k = 0; k < kUnit / 128; ++k) most = fmaxf(most, fmaxf(fmaxf(f[k].x, f[k].y), fmaxf(f[k].z, f[k].w)));
-      most = warp_max(most);
-      UnitStat st{most, -1, {0.0f, 0.0f}};
-      if (most > -INFINITY) {
-        if (greedy) {
-          int32_t at = 0x7FFFFFFF;
-#pragma unroll
-          for (int k = 0; k < kUnit / 128; ++k) first_at(f[k], v0 + k * 128 + 4 * lane, most, at);
-          st.at = __reduce_min_sync(0xFFFFFFFFu, at);
-        } else {
-          const Ref ref = make_ref(most, c);
-          Sum sum;
-#pragma unroll
-          for (int k = 0; k < kUnit / 128; ++k) {
-            uint64_t h, lo;
-            mass2(pair2(f[k].x, f[k].y), ref, c, h, lo);
-            sum.add(h, lo);
-            mass2(pair2(f[k].z, f[k].w), ref, c, h, lo);
-            sum.add(h, lo);
-          }
-          const Pair all = warp_sum(sum.value());
-          st.sum[0] = all.h;
-          st.sum[1] = all.l;
-        }
-      }
-      if (lane == 0) a.stat[row * a.units + unit] = st;
+  if (tid < 32) {
+    int before = 0;
+#pragma unroll 1
+    for (int w = 0; w < kStatTile / 32; ++w) {
+      const uint32_t word = inner[w];
+      if (word >> lane & 1u) list[before + __popc(word & ((1u << lane) - 1u))] = (uint16_t)(w * 32 + lane);
+      before += __popc(word);
     }
+    if (tid == 0) rows = before;
+  }
+  __syncthreads();
+  const int64_t items = (int64_t)rows * a.units, step = (int64_t)gridDim.x * (kStatThreads / 32);
+#pragma unroll 1
+  for (int64_t item = (int64_t)blockIdx.x * (kStatThreads / 32) + (tid >> 5); item < items; item += step) {
+    const int nth = (int)(item / a.units), unit = (int)(item - (int64_t)nth * a.units), at = list[nth];
+    const int64_t v0 = (int64_t)unit * kUnit, v1 = min(a.V, v0 + kUnit);
+    const float* x = a.logits + (m0 + at) * a.stride;
+    float4 f[kUnit / 128];
+#pragma unroll
+    for (int k = 0; k < kUnit / 128; ++k) f[k] = four(x, v0 + k * 128 + 4 * lane, v1, a.vec, -INFINITY);
+    if (a.vec && lane == 0 && item + step < items) {
+      const int next = (int)((item + step) / a.units);
+      const int64_t n0 = (item + step - (int64_t)next * a.units) * kUnit;
+      const uint32_t bytes = (uint32_t)(min(a.V - n0, (int64_t)kUnit) & ~(int64_t)3) * 4;
+      if (bytes) prefetch_l2(a.logits + (m0 + list[next]) * a.stride + n0, bytes);
+    }
+    const float T = a.temperature ? a.temperature[request[at]] : 1.0f;
+    float most = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < kUnit / 128; ++k) most = fmaxf(most, fmaxf(fmaxf(f[k].x, f[k].y), fmaxf(f[k].z, f[k].w)));
+    most = warp_max(most);
+    UnitStat st{most, -1, 0.0f};
+    if (most > -INFINITY) {
+      if (T < kGreedy) {
+        int32_t first = 0x7FFFFFFF;
+#pragma unroll
+        for (int k = 0; k < kUnit / 128; ++k) first_at(f[k], v0 + k * 128 + 4 * lane, most, first);
+        st.at = __reduce_min_sync(0xFFFFFFFFu, first);
+      } else {
+        const Slope c = make_slope(T);
+        const Rough ref = make_rough(make_ref(most, c), c);
+        if (most < INFINITY) {
+#pragma unroll
+          for (int k = 0; k < kUnit / 128; ++k)
+            st.sum += (rough(f[k].x, ref) + rough(f[k].y, ref)) + (rough(f[k].z, ref) + rough(f[k].w, ref));
+        } else {  // the infinite ones alone, alike
+#pragma unroll
+          for (int k = 0; k < kUnit / 128; ++k)
+            st.sum += (float)((f[k].x == most) + (f[k].y == most) + (f[k].z == most) + (f[k].w == most));
+        }
+#pragma unroll
+        for (int o2 = 16; o2; o2 >>= 1) st.sum += __shfl_xor_sync(0xFFFFFFFFu, st.sum, o2);
+      }
+    }
+    if (lane == 0) a.stat[(m0 + at) * a.units + unit] = st;
+  }
 }
 
 // ---------------------------------------------------------------- the walk
+
+// One lane's mass, by the arithmetic of mass2.
+__device__ __forceinline__ Pair mass1(float l, const Ref& r, const Slope& c) {
+  if (r.most == INFINITY) return {l == INFINITY ? 1.0f : 0.0f, 0.0f};
+  const float d = fmaxf(l - r.shift, least_of(r, c));  // (NaN: the least)
+  const float t = fmaf(d, c.hi, kMagic), g = fmaf(d, c.lo, fmaf(d, c.hi, kMagic - t));
+  const uint32_t n = __float_as_uint(t);
+  const float2 root = kRoots[n & 31u];
+  const float w = fmaf(fmaf(fmaf(kExp3, g, kExp2), g, kExp1), g, root.y);
+  const float h = __uint_as_float((n << 18) + root_bits(root.x, (int)(n & 31u), r.whole));
+  return l >= -kMost && h > kLeast ? Pair{h, h * w} : Pair{0.0f, 0.0f};
+}
 
 // What the first block of a cluster has all its blocks do next.
 enum : int32_t { kOpDone, kOpSum, kOpFind };
@@ -363,17 +480,19 @@ struct Command {
   int32_t op;
   int32_t node;          // of the request
   int32_t known;         // kOpSum: `most` is the row's; else every warp finds its range's
-  int32_t residual;      // tau q is taken off
+  int32_t residual;      // 1: tau q is taken off; 2: and p's own sum is wanted too, tau being about that
   int32_t refused;       // the node's children are taken out (no q)
   int32_t owner;         // kOpFind: the block that holds the bonus token
   float most, tau_hi, tau_lo;
+  float moved;           // kOpFind: what tau has changed by since the sums were made
   Pair target;           // kOpFind: the mass before the bonus token in the owner's ranges, in the units of `most`
 };
 
 struct Total {
   float most;
   int32_t at;
-  Pair sum;
+  Pair sum, whole;  // what is left; p's own sum (residual = 2)
+  float slope;      // minus the derivative of what is left by tau: q of the tokens that have some (residual = 2)
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -401,60 +520,87 @@ __device__ __forceinline__ void send(const S& from, S* to, uint32_t rank) {
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at + 4 * i), "r"(w[i]) : "memory");
 }
 
+// Where the walk stands at a node: what it waits for, the children tried, and what refusals have left.
+enum : int32_t { kStart, kRefused, kFirst, kPrecise, kSummed };
+
+struct Walk {
+  int32_t stage, cur, last, depth;
+  bool inner;    // the node has children
+  bool rough;    // M comes from the rows' kernel, to 2^-18
+  bool summed;   // the blocks hold the sums of what is left
+  bool refused;  // a child was refused (no q)
+  bool spent;    // nothing was left
+  Pair tau, Q, M, out;  // out: the refused children's masses (no q)
+};
+
 struct WalkShared {
   int32_t parent[kSampleMaxNodes], draft[kSampleMaxNodes], refused[kSampleMaxNodes];
   float u[kSampleMaxNodes], q[kSampleMaxNodes];  // of a node: its number, and q of its token at the parent
   Pair mass[kSampleMaxNodes];                    // its token's mass at the parent (the logit at first)
   float most[kSampleMaxNodes];                   // of rows with children
   int32_t at[kSampleMaxNodes];
-  Pair sum[kSampleMaxNodes];
+  float sum[kSampleMaxNodes];                    // to 2^-18
   uint32_t inner[kSampleMaxNodes / 32];
   Command cmd;
+  Walk walk;
   Total total[kMaxCluster];
   Total range[kWalkWarps];
   Pair group[kWalkWarps];
   int32_t n_refused, last;
 };
 
-// The masses of four tokens from i on.
+// The masses of four tokens from i on, without the refused ones.
 struct Four {
   uint64_t h[2], lo[2];
 };
 
-__device__ __forceinline__ Four masses4(const float4& f, const float4& q, int64_t i, const Ref& ref, const Slope& c,
-                                        const Command& cmd, const int32_t* refused, int n_refused) {
+__device__ __forceinline__ Four masses4(const float4& f, int64_t i, const Scale& c, const int32_t* refused, int n_refused) {
   Four m;
-  mass2(pair2(f.x, f.y), ref, c, m.h[0], m.lo[0]);
-  mass2(pair2(f.z, f.w), ref, c, m.h[1], m.lo[1]);
-  if (cmd.residual) {
-    left2(m.h[0], m.lo[0], pair2(q.x, q.y), cmd.tau_hi, cmd.tau_lo);
-    left2(m.h[1], m.lo[1], pair2(q.z, q.w), cmd.tau_hi, cmd.tau_lo);
-  }
+  mass2<true>(pair2(f.x, f.y), c, m.h[0], m.lo[0]);
+  mass2<true>(pair2(f.z, f.w), c, m.h[1], m.lo[1]);
+  least2(m.h[0], m.lo[0]);
+  least2(m.h[1], m.lo[1]);
+  uint32_t out = 0;  // of the four
+#pragma unroll 1
   for (int k = 0; k < n_refused; ++k) {
     const int64_t at = refused[k] - i;
-    if (at >= 0 && at < 4) {
-      const uint64_t keep = at & 1 ? 0x00000000FFFFFFFFull : 0xFFFFFFFF00000000ull;
-      m.h[at >> 1] &= keep;
-      m.lo[at >> 1] &= keep;
-    }
+    if (at >= 0 && at < 4) out |= 1u << at;
+  }
+  if (out) {
+    const uint64_t low = 0x00000000FFFFFFFFull, high = 0xFFFFFFFF00000000ull;
+    const uint64_t k0 = (out & 1u ? 0 : low) | (out & 2u ? 0 : high), k1 = (out & 4u ? 0 : low) | (out & 8u ? 0 : high);
+    m.h[0] &= k0, m.lo[0] &= k0, m.h[1] &= k1, m.lo[1] &= k1;
   }
   return m;
 }
 
-__device__ __forceinline__ float chance(float q) { return fminf(fmaxf(q, 0.0f), 1.0f); }  // (NaN: 0)
+__device__ __forceinline__ void left4(Four& m, const float4& q, float tau_hi, float tau_lo) {
+  left2(m.h[0], m.lo[0], pair2(q.x, q.y), tau_hi, tau_lo);
+  left2(m.h[1], m.lo[1], pair2(q.z, q.w), tau_hi, tau_lo);
+}
+
+// q of the tokens that have something left.
+__device__ __forceinline__ float slope4(const Four& m, const float4& q) {
+  const float2 a = split2(m.h[0]), b = split2(m.h[1]);
+  return ((a.x != 0.0f ? q.x : 0.0f) + (a.y != 0.0f ? q.y : 0.0f)) + ((b.x != 0.0f ? q.z : 0.0f) + (b.y != 0.0f ? q.w : 0.0f));
+}
+
+__device__ __forceinline__ float chance(float q) { return fmaxf(q, 0.0f); }  // (NaN: 0)
 
 __device__ __forceinline__ float4 chance4(float4 q) { return make_float4(chance(q.x), chance(q.y), chance(q.z), chance(q.w)); }
 
 // One warp's range of one row: its sum, or its first largest token (greedy).
-__device__ __forceinline__ Total sum_range(const SampleArgs& a, const Command& cmd, const Slope& c, bool greedy, int64_t row,
-                                           int64_t v0, int64_t v1, const int32_t* refused, int n_refused) {
+__device__ __forceinline__ Total sum_range(const SampleArgs& a, const Command& cmd, Slope c, bool greedy, int64_t row,
+                                           int64_t v0, int64_t v1, const int32_t* refused, int n_refused, float2 root) {
   const int lane = threadIdx.x & 31;
   const float* x = a.logits + row * a.stride;
   const float* p = a.probs ? a.probs + row * a.probs_stride : nullptr;
-  constexpr int U = 4;
-  Total t{cmd.most, 0x7FFFFFFF, {0.0f, 0.0f}};
+  constexpr int U = 2;
+  const int mode = cmd.residual;
+  Total t{cmd.most, 0x7FFFFFFF, {0.0f, 0.0f}, {0.0f, 0.0f}, 0.0f};
   if (!cmd.known) {
     t.most = -INFINITY;
+#pragma unroll 1
     for (int64_t i0 = v0; i0 < v1; i0 += 128 * U) {
       float4 f[U];
 #pragma unroll
@@ -467,37 +613,106 @@ __device__ __forceinline__ Total sum_range(const SampleArgs& a, const Command& c
   if (t.most == -INFINITY) return t;
   if (greedy) {
     int32_t at = 0x7FFFFFFF;
+#pragma unroll 1
     for (int64_t i = v0 + 4 * lane; i < v1 && at == 0x7FFFFFFF; i += 128) first_at(four(x, i, v1, a.vec, -INFINITY), i, t.most, at);
     __syncwarp();
     t.at = __reduce_min_sync(0xFFFFFFFFu, at);
     return t;
   }
-  const Ref ref = make_ref(t.most, c);
-  Sum sum;
-  for (int64_t i0 = v0; i0 < v1; i0 += 128 * U) {
-    float4 f[U], q[U];
-#pragma unroll
-    for (int k = 0; k < U; ++k) {
-      f[k] = four(x, i0 + k * 128 + 4 * lane, v1, a.vec, -INFINITY);
-      q[k] = cmd.residual ? four(p, i0 + k * 128 + 4 * lane, v1, a.probs_vec, 0.0f) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  const Scale scale = make_scale(make_ref(t.most, c), c, root);
+  Sum sum, whole;
+  auto add = [&](Four& m, const float4& q, bool left) {
+    if (left) {
+      if (mode == 2) {
+        whole.add(m.h[0], m.lo[0]);
+        whole.add(m.h[1], m.lo[1]);
+      }
+      left4(m, q, cmd.tau_hi, cmd.tau_lo);
+      if (mode == 2) t.slope += slope4(m, q);
     }
+    sum.add(m.h[0], m.lo[0]);
+    sum.add(m.h[1], m.lo[1]);
+  };
+  bool mine = false;  // does the range hold a refused token
+#pragma unroll 1
+  for (int k = 0; k < n_refused; ++k) mine = mine || (refused[k] >= v0 && refused[k] < v1);
+  const bool whole_steps = a.vec && (!mode || a.probs_vec) && !scale.endless && scale.shift == 0.0f && scale.hi >= kSlow;
+#pragma unroll 1
+  for (int64_t i0 = v0; i0 < v1;) {
+    bool plain = whole_steps && i0 + 128 * U <= v1;
+    if (plain && mine)
+#pragma unroll 1
+      for (int k = 0; k < n_refused; ++k) plain = plain && !(refused[k] >= i0 && refused[k] < i0 + 128 * U);
+    if (plain) {  // no branches inside, so that a warp's masses overlap one another
+      const int64_t i = i0 + 4 * lane;
+      float4 f[U], q[U];
+      Four m[U];
 #pragma unroll
-    for (int k = 0; k < U; ++k) {
-      const Four m = masses4(f[k], chance4(q[k]), i0 + k * 128 + 4 * lane, ref, c, cmd, refused, n_refused);
-      sum.add(m.h[0], m.lo[0]);
-      sum.add(m.h[1], m.lo[1]);
+      for (int k = 0; k < U; ++k) f[k] = *reinterpret_cast<const float4*>(x + i + k * 128);
+      if (mode) {
+#pragma unroll
+        for (int k = 0; k < U; ++k) q[k] = *reinterpret_cast<const float4*>(p + i + k * 128);
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+          mass2<false>(pair2(f[k].x, f[k].y), scale, m[k].h[0], m[k].lo[0]);
+          mass2<false>(pair2(f[k].z, f[k].w), scale, m[k].h[1], m[k].lo[1]);
+        }
+        if (mode == 2) {
+#pragma unroll
+          for (int k = 0; k < U; ++k) {
+            whole.add(m[k].h[0], m[k].lo[0]);
+            whole.add(m[k].h[1], m[k].lo[1]);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+          q[k] = chance4(q[k]);
+          left4(m[k], q[k], cmd.tau_hi, cmd.tau_lo);
+        }
+        if (mode == 2) {
+#pragma unroll
+          for (int k = 0; k < U; ++k) t.slope += slope4(m[k], q[k]);
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+          mass2<false>(pair2(f[k].x, f[k].y), scale, m[k].h[0], m[k].lo[0]);
+          mass2<false>(pair2(f[k].z, f[k].w), scale, m[k].h[1], m[k].lo[1]);
+          least2(m[k].h[0], m[k].lo[0]);
+          least2(m[k].h[1], m[k].lo[1]);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        sum.add(m[k].h[0], m[k].lo[0]);
+        sum.add(m[k].h[1], m[k].lo[1]);
+      }
+      i0 += 128 * U;
+    } else {
+      const int64_t i = i0 + 4 * lane;
+      Four m = masses4(four(x, i, v1, a.vec, -INFINITY), i, scale, refused, mine ? n_refused : 0);
+      add(m, mode ? chance4(four(p, i, v1, a.probs_vec, 0.0f)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f), mode != 0);
+      i0 += 128;
     }
   }
   t.sum = warp_sum(sum.value());
+  if (mode) {
+    t.whole = warp_sum(whole.value());
+#pragma unroll
+    for (int o = 16; o; o >>= 1) t.slope += __shfl_xor_sync(0xFFFFFFFFu, t.slope, o);
+  }
   return t;
 }
 
-// The parts' largest logit, their first token at it, and their sum in its units (a part a lane, 0 <= lane < n).
-__device__ __forceinline__ Total join(const Total* part, int n, const Slope& c, Pair& mine) {
+// The parts' largest logit, their first token at it, and their sums in its units (a part a lane, 0 <= lane < n <= 16).
+__device__ __forceinline__ Total join(const Total* part, int n, const Slope& c, bool whole, Pair& mine, float& slope) {
   const int lane = threadIdx.x & 31;
-  Total t{-INFINITY, 0x7FFFFFFF, {0.0f, 0.0f}};
+  Total t{-INFINITY, 0x7FFFFFFF, {0.0f, 0.0f}, {0.0f, 0.0f}, 0.0f};
   if (lane < n) t = part[lane];
-  const float most = warp_max(t.most);
+  float most = t.most;
+#pragma unroll
+  for (int o = 8; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
+  most = __shfl_sync(0xFFFFFFFFu, most, 0);
   t.at = __reduce_min_sync(0xFFFFFFFFu, t.most == most ? t.at : 0x7FFFFFFF);
   mine = {0.0f, 0.0f};
   if (t.sum.h > 0.0f) {
@@ -505,7 +720,20 @@ __device__ __forceinline__ Total join(const Total* part, int n, const Slope& c, 
     mine = {t.sum.h * k, t.sum.l * k};
   }
   t.most = most;
-  t.sum = warp_sum(mine);
+  t.sum = mine;
+#pragma unroll 1
+  for (int o = 8; o; o >>= 1) t.sum = t.sum + shuffle_xor(t.sum, o);
+  t.sum = shuffle(t.sum, 0);
+  slope = t.slope;
+  if (whole) {  // (of parts in the same units)
+#pragma unroll 1
+    for (int o = 8; o; o >>= 1) {
+      t.whole = t.whole + shuffle_xor(t.whole, o);
+      t.slope += __shfl_xor_sync(0xFFFFFFFFu, t.slope, o);
+    }
+    t.whole = shuffle(t.whole, 0);
+    t.slope = __shfl_sync(0xFFFFFFFFu, t.slope, 0);
+  }
   return t;
 }
 
@@ -513,7 +741,7 @@ __device__ __forceinline__ Total join(const Total* part, int n, const Slope& c, 
 // sums of ranges, groups and lanes are rounded differently; where the last tokens do not pass the
 // target by that, it is the last one with a mass.
 __device__ __forceinline__ void find_token(const SampleArgs& a, WalkShared& s, const Slope& c, int64_t row, int64_t first,
-                                           int32_t* bonus) {
+                                           float2 root, int32_t* bonus) {
   const Command& cmd = s.cmd;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const Ref whole = make_ref(cmd.most, c);
@@ -523,6 +751,7 @@ __device__ __forceinline__ void find_token(const SampleArgs& a, WalkShared& s, c
     const Ref part = make_ref(s.range[lane].most, c);
     k = scale_of(part, whole, c);
     mine = {s.range[lane].sum.h * k, s.range[lane].sum.l * k};
+    mine = mine - Pair{cmd.moved * s.range[lane].slope, 0.0f};
   }
   const Found in = find_lane(mine, cmd.target);
   const int range = max(in.lane, 0);
@@ -530,22 +759,25 @@ __device__ __forceinline__ void find_token(const SampleArgs& a, WalkShared& s, c
   Pair target = cmd.target - in.before;
   k = scale_of(whole, ref, c);
   target = {target.h * k, target.l * k};
+  const Scale scale = make_scale(ref, c, root);
   const int64_t v0 = first + range * a.range, v1 = min(a.V, v0 + a.range);
   const float* x = a.logits + row * a.stride;
   const float* p = a.probs ? a.probs + row * a.probs_stride : nullptr;
   const int n_refused = cmd.refused ? s.n_refused : 0;
   if (tid == 0) s.last = -1;
+#pragma unroll 1
   for (int64_t base = v0; base < v1; base += 128 * kWalkWarps) {
     const int64_t i = base + warp * 128 + 4 * lane;
-    const float4 q = cmd.residual ? four(p, i, v1, a.probs_vec, 0.0f) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    const Four f = masses4(four(x, i, v1, a.vec, -INFINITY), chance4(q), i, ref, c, cmd, s.refused, n_refused);
+    Four f = masses4(four(x, i, v1, a.vec, -INFINITY), i, scale, s.refused, n_refused);
+    if (cmd.residual) left4(f, chance4(four(p, i, v1, a.probs_vec, 0.0f)), cmd.tau_hi, cmd.tau_lo);
     const float2 h0 = split2(f.h[0]), l0 = split2(f.lo[0]), h1 = split2(f.h[1]), l1 = split2(f.lo[1]);
-    const Pair m[4] = {{h0.x, l0.x}, {h0.y, l0.y}, {h1.x, l1.x}, {h1.y, l1.y}};
+    const Pair none{0.0f, 0.0f};  // (adding it brings a pair in order)
+    const Pair m[4] = {none + Pair{h0.x, l0.x}, none + Pair{h0.y, l0.y}, none + Pair{h1.x, l1.x}, none + Pair{h1.y, l1.y}};
     mine = (m[0] + m[1]) + (m[2] + m[3]);
     const Pair all = warp_sum(mine);
     if (lane == 0) s.group[warp] = all;
     __syncthreads();
-    const Found at = find_lane(lane < kWalkWarps ? s.group[lane] : Pair{0.0f, 0.0f}, target);
+    const Found at = find_lane(lane < kWalkWarps ? s.group[lane] : none, target);
     if (at.passed && at.lane == warp) {
       const Pair rest = target - at.before;
       const Found l = find_lane(mine, rest);
@@ -572,13 +804,170 @@ __device__ __forceinline__ void find_token(const SampleArgs& a, WalkShared& s, c
   if (tid == 0) *bonus = s.last;
 }
 
+// What comes next, by the first block's first warp (all lanes alike): the walk goes on with the sums that it had
+// asked for, until it needs others or ends.
+__device__ __forceinline__ Command decide(const SampleArgs& a, WalkShared& s, Slope c, bool ok, bool greedy, int r, int64_t off,
+                                       int n, int cluster) {
+  const int lane = threadIdx.x & 31;
+  const Pair zero{0.0f, 0.0f}, one{1.0f, 0.0f};
+  Walk w = s.walk;
+  Command cmd = s.cmd;    // the last one
+  Pair mine{0.0f, 0.0f};  // of a block, in its lane
+  float slope = 0.0f;
+  Total all{};
+  auto enter = [&](int node) {
+    w.cur = w.last = node;
+    w.inner = s.inner[node >> 5] >> (node & 31) & 1u;
+    w.summed = w.spent = w.refused = false;
+    w.rough = true;
+    w.tau = w.out = zero;
+    w.Q = one;
+    w.M = {w.inner ? s.sum[node] : 0.0f, 0.0f};
+  };
+  auto ask = [&](int residual, bool off_refused) {
+    cmd.op = kOpSum;
+    cmd.node = w.cur;
+    cmd.known = w.inner;
+    cmd.most = w.inner ? s.most[w.cur] : 0.0f;
+    cmd.residual = residual;
+    cmd.refused = off_refused;
+    cmd.tau_hi = w.tau.h;
+    cmd.tau_lo = w.tau.l;
+    cmd.moved = 0.0f;
+  };
+  if (ok && w.stage == kStart) {
+    enter(0);
+    w.depth = 0;
+    if (lane == 0) a.path_nodes[off] = 0;
+  }
+  cmd.op = kOpDone;
+  if (ok) {
+    if (w.stage != kStart) all = join(s.total, cluster, c, w.stage == kFirst, mine, slope);  // the blocks' sums
+    bool ends = w.stage == kSummed, asked = false;
+    if (w.stage == kFirst) {
+      // p's sum was not known to the last bits, so tau was off: what is left has moved with it along its
+      // derivative.  (It bends only where a token's rest is within that of zero: 2^-36 or less.)
+      const Pair off_by = all.whole - w.tau;
+      cmd.moved = off_by.h;
+      w.tau = all.whole;
+      cmd.tau_hi = w.tau.h;
+      cmd.tau_lo = w.tau.l;
+      mine = mine - Pair{cmd.moved * slope, 0.0f};
+      all.sum = all.sum - Pair{cmd.moved * all.slope, 0.0f};
+      w.rough = false;
+    }
+    if (w.stage == kRefused || w.stage == kFirst) {
+      w.M = all.sum;
+      w.summed = w.M > zero;
+      w.spent = !w.summed;  // nothing is left: the bonus comes from p as it was
+    } else if (w.stage == kPrecise) {
+      w.M = all.sum - w.out;
+      if (!(w.M > zero)) w.M = zero;
+      w.rough = false;
+      w.summed = !w.refused;
+    }
+#pragma unroll 1
+    while (!ends && !asked) {
+      int j = -1;  // the next child
+#pragma unroll 1
+      for (int i0 = w.last + 1; i0 < n && j < 0; i0 += 32) {
+        const uint32_t b = __ballot_sync(0xFFFFFFFFu, i0 + lane < n && s.parent[i0 + lane] == w.cur);
+        if (b) j = i0 + __ffs((int)b) - 1;
+      }
+      if (j < 0) {
+        ends = true;
+        break;
+      }
+      w.last = j;
+      const int32_t x = s.draft[j];
+      if (x < 0) continue;
+      bool take;
+      if (greedy) {
+        take = s.most[w.cur] > -INFINITY && x == s.at[w.cur];
+      } else {
+        if (w.spent || !(s.sum[w.cur] > 0.0f)) continue;
+        bool twice = false;  // a sibling with this token was refused before
+#pragma unroll 1
+        for (int i0 = w.cur + 1; i0 < j && !twice; i0 += 32)
+          twice = __any_sync(0xFFFFFFFFu, i0 + lane < j && s.parent[i0 + lane] == w.cur && s.draft[i0 + lane] == x);
+        if (twice) continue;
+        const Pair e = zero + s.mass[j];
+        const float u = s.u[j], q = a.probs ? s.q[j] : 1.0f;
+        const Pair mine_u = w.M * u * q, limit = a.probs ? (e - w.tau * q) * w.Q : e;
+        const bool moves = !a.probs || (q > 0.0f && w.Q > zero);  // a refusal would change p
+        take = (!a.probs || w.Q > zero) && limit > mine_u;
+        if (w.rough && moves && fabsf((mine_u - limit).h) <= 6.2e-5f * u * q * (w.M + w.out).h) {  // it does not tell
+          w.last = j - 1;
+          ask(0, false);
+          w.stage = kPrecise;
+          asked = true;
+          continue;
+        }
+        if (!take && moves) {
+          w.summed = false;
+          if (!a.probs) {
+            w.refused = true;
+            w.out = w.out + e;
+            w.M = w.M - e;
+            if (!(w.M > zero)) w.M = zero;
+          } else {
+            w.tau = w.tau + (w.Q.h == 1.0f && w.Q.l == 0.0f ? w.M : w.M / w.Q);
+            w.Q = w.Q - Pair{q, 0.0f};
+            ask(w.rough ? 2 : 1, false);
+            w.stage = w.rough ? kFirst : kRefused;
+            asked = true;
+          }
+        }
+      }
+      if (take) {
+        ++w.depth;
+        if (lane == 0) a.path_nodes[off + w.depth] = j;
+        enter(j);
+      }
+    }
+    if (ends) {
+      if (w.stage != kSummed) {
+        if (lane == 0) a.path_len[r] = w.depth;
+        if (greedy && w.inner) {
+          if (lane == 0) a.bonus[r] = s.most[w.cur] > -INFINITY ? s.at[w.cur] : -1;
+        } else if (!w.summed) {
+          ask(0, w.refused);
+          w.stage = kSummed;
+        }
+      } else if (greedy) {
+        if (lane == 0) a.bonus[r] = all.most > -INFINITY ? all.at : -1;
+      } else if (!(all.sum.h > 0.0f)) {
+        if (cmd.refused) {  // all that had a mass was refused: p as it was
+          ask(0, false);
+        } else if (lane == 0) {
+          a.bonus[r] = -1;
+        }
+      } else {
+        w.summed = true;
+      }
+      if (w.summed && !greedy) {
+        const Pair target = all.sum * fminf(fmaxf(a.u_bonus[r], 0.0f), 0.99999994f);
+        const Found f = find_lane(mine, target);
+        cmd.op = kOpFind;
+        cmd.most = all.most;
+        cmd.owner = f.lane;
+        cmd.target = target - f.before;
+      }
+    }
+  }
+  __syncwarp();
+  if (lane == 0) s.walk = w;
+  return cmd;
+}
+
 // A cluster takes a request.  Its first block walks the tree (warp 0, all lanes alike) and has all blocks sum a
 // row's masses, a range of tokens a warp, where a refusal or the bonus token asks for it; only that
 // block decides what comes next, and the others do as they are told.
-__global__ void __launch_bounds__(kWalkThreads) k_sample_walk(const __grid_constant__ SampleArgs a, int cluster) {
+__global__ void __launch_bounds__(kWalkThreads, 2) k_sample_walk(const __grid_constant__ SampleArgs a, int cluster) {
   __shared__ WalkShared s;
   cluster_arrive();  // a block's shared memory is written to only when the block runs
-  pdl_enter();
+  // The rows' kernel has waited for all before it, so the tree and the numbers may be read while it runs.
+  if (a.M == 1) pdl_enter();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t rank = cluster_rank();
   const int r = blockIdx.x / cluster;
@@ -590,12 +979,40 @@ __global__ void __launch_bounds__(kWalkThreads) k_sample_walk(const __grid_const
   const float T = a.temperature ? a.temperature[r] : 1.0f;
   const bool greedy = T < kGreedy;
   const Slope c = make_slope(greedy ? 1.0f : T);
+  const float2 root = kRoots[lane];
 
   // ---- the nodes, and the sums of the rows with children
   if (rank == 0) {
     if (tid < kSampleMaxNodes / 32) s.inner[tid] = 0;
     __syncthreads();
     ok = ok && T >= 0.0f;
+    // A row's largest logit and its sum.  (The first rows' are read with the tree; of those without children
+    // nothing was written, and nothing is used.)
+    auto row_sum = [&](int i) {
+      const UnitStat* st = a.stat + (off + i) * a.units;
+      float most = -INFINITY;
+#pragma unroll 1
+      for (int k = lane; k < a.units; k += 32) most = fmaxf(most, st[k].most);
+      most = warp_max(most);
+      const Ref ref = make_ref(most, c);
+      int32_t at = 0x7FFFFFFF;
+      float sum = 0.0f;
+#pragma unroll 1
+      for (int k = lane; k < a.units; k += 32) {
+        const UnitStat u = st[k];
+        if (u.most == most) at = min(at, u.at);
+        if (u.sum > 0.0f) sum += u.sum * scale_of(make_ref(u.most, c), ref, c);
+      }
+      at = __reduce_min_sync(0xFFFFFFFFu, at);
+#pragma unroll
+      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+      if (lane == 0) {
+        s.most[i] = most;
+        s.at[i] = at;
+        s.sum[i] = sum;
+      }
+    };
+#pragma unroll 1
     for (int i = tid; i < n; i += kWalkThreads) {
       const int32_t p = a.parent[off + i], x = a.draft[off + i];
       const bool fine = i == 0 ? p == -1 : p >= 0 && p < i;
@@ -610,176 +1027,48 @@ __global__ void __launch_bounds__(kWalkThreads) k_sample_walk(const __grid_const
         s.q[i] = s.draft[i] >= 0 && a.probs ? chance(a.probs[(off + p) * a.probs_stride + x]) : 0.0f;
       }
     }
+    if (a.M > 1) pdl_enter();
+    if (warp < n && a.M > 1) row_sum(warp);
     ok = __syncthreads_and(ok);
     if (!ok && tid == 0) atomicOr(a.status, kSampleBadRequest);
     ok = ok && n > 0;
     if (!ok && tid == 0) a.path_len[r] = a.bonus[r] = -1;
-    for (int i = warp; ok && i < n; i += kWalkWarps) {
-      if (!(s.inner[i >> 5] >> (i & 31) & 1u)) continue;
-      const UnitStat* st = a.stat + (off + i) * a.units;
-      float most = -INFINITY;
-      for (int k = lane; k < a.units; k += 32) most = fmaxf(most, st[k].most);
-      most = warp_max(most);
-      const Ref ref = make_ref(most, c);
-      int32_t at = 0x7FFFFFFF;
-      Pair sum{0.0f, 0.0f};
-      for (int k = lane; k < a.units; k += 32) {
-        const UnitStat u = st[k];
-        if (u.most == most) at = min(at, u.at);
-        if (u.sum[0] > 0.0f) {
-          const float scale = scale_of(make_ref(u.most, c), ref, c);
-          sum = sum + Pair{u.sum[0] * scale, u.sum[1] * scale};
-        }
-      }
-      at = __reduce_min_sync(0xFFFFFFFFu, at);
-      sum = warp_sum(sum);
-      if (lane == 0) {
-        s.most[i] = most;
-        s.at[i] = at;
-        s.sum[i] = sum;
-      }
-    }
+#pragma unroll 1
+    for (int i = warp + kWalkWarps; ok && i < n; i += kWalkWarps)
+      if (s.inner[i >> 5] >> (i & 31) & 1u) row_sum(i);
     __syncthreads();
-    if (!greedy)
-      for (int i = 1 + tid; ok && i < n; i += kWalkThreads) {
-        uint64_t h, lo;
-        mass2(both(s.mass[i].h), make_ref(s.most[s.parent[i]], c), c, h, lo);
-        s.mass[i] = {split2(h).x, split2(lo).x};
+    if (ok && !greedy)
+#pragma unroll 1
+      for (int i0 = warp * 32; i0 < n; i0 += kWalkThreads) {
+        // (a lane has a row of its own, so it takes the roots from memory)
+        const int i = i0 + lane;
+        if (i > 0 && i < n) s.mass[i] = mass1(s.mass[i].h, make_ref(s.most[s.parent[i]], c), c);
       }
     __syncthreads();
   }
 
-  // ---- the walk's state (first block, warp 0)
-  enum { kWalk, kRefused, kSummed } stage = kWalk;
-  int cur = 0, last = 0, depth = 0;
-  bool inner = false, summed = false, spent = false, refused = false;
-  double tau = 0.0, Q = 1.0, M = 0.0;
-  Pair mine{0.0f, 0.0f};  // of a block, in its lane
-  Total all{};
-  Command cmd{};
-  const float u_bonus = fminf(fmaxf(a.u_bonus[r], 0.0f), 0.99999994f);
-  auto enter = [&](int node) {
-    cur = last = node;
-    inner = s.inner[node >> 5] >> (node & 31) & 1u;
-    summed = spent = refused = false;
-    tau = 0.0;
-    Q = 1.0;
-    M = inner ? wide(s.sum[node]) : 0.0;
-  };
-  auto ask = [&](bool residual) {
-    cmd.op = kOpSum;
-    cmd.node = cur;
-    cmd.known = inner;
-    cmd.most = inner ? s.most[cur] : 0.0f;
-    cmd.residual = residual;
-    cmd.refused = refused && !residual;
-    cmd.tau_hi = (float)tau;
-    cmd.tau_lo = (float)(tau - (double)cmd.tau_hi);
-  };
-  if (rank == 0 && warp == 0 && ok) {
-    enter(0);
-    if (lane == 0) a.path_nodes[off] = 0;
-  }
+  else if (a.M > 1) pdl_enter();
 
+  if (tid == 0) s.walk.stage = kStart;
   __syncwarp();
   cluster_wait();
   while (true) {
     if (rank == 0 && warp == 0) {
-      cmd.op = kOpDone;
-      if (ok) {
-        if (stage != kWalk) all = join(s.total, cluster, c, mine);  // the blocks' sums
-        bool ends = stage == kSummed, asked = false;
-        if (stage == kRefused) {
-          M = wide(all.sum);
-          summed = M > 0.0;
-          spent = !summed;  // nothing is left: the bonus comes from p as it was
-        }
-        while (!ends && !asked) {
-          int j = -1;  // the next child
-          for (int i0 = last + 1; i0 < n && j < 0; i0 += 32) {
-            const uint32_t b = __ballot_sync(0xFFFFFFFFu, i0 + lane < n && s.parent[i0 + lane] == cur);
-            if (b) j = i0 + __ffs((int)b) - 1;
-          }
-          if (j < 0) {
-            ends = true;
-            break;
-          }
-          last = j;
-          const int32_t x = s.draft[j];
-          if (x < 0) continue;
-          bool take;
-          if (greedy) {
-            take = s.most[cur] > -INFINITY && x == s.at[cur];
-          } else {
-            if (spent || !(s.sum[cur].h > 0.0f)) continue;
-            bool twice = false;  // a sibling with this token was refused before
-            for (int i0 = cur + 1; i0 < j && !twice; i0 += 32)
-              twice = __any_sync(0xFFFFFFFFu, i0 + lane < j && s.parent[i0 + lane] == cur && s.draft[i0 + lane] == x);
-            if (twice) continue;
-            const double e = wide(s.mass[j]), u = s.u[j], q = s.q[j];
-            take = a.probs ? Q > 0.0 && u * q * M < (e - tau * q) * Q : u * M < e;
-            if (!take) {
-              if (!a.probs) {
-                refused = true;
-                M = fmax(M - e, 0.0);
-              } else if (q > 0.0 && Q > 0.0) {
-                tau += Q == 1.0 ? M : M / Q;
-                Q -= q;
-                ask(true);
-                stage = kRefused;
-                asked = true;
-              }
-            }
-          }
-          if (take) {
-            ++depth;
-            if (lane == 0) a.path_nodes[off + depth] = j;
-            enter(j);
-          }
-        }
-        if (ends) {
-          if (stage != kSummed) {
-            if (lane == 0) a.path_len[r] = depth;
-            if (greedy && inner) {
-              if (lane == 0) a.bonus[r] = s.most[cur] > -INFINITY ? s.at[cur] : -1;
-            } else if (!summed) {
-              ask(false);
-              stage = kSummed;
-            }
-          } else if (greedy) {
-            if (lane == 0) a.bonus[r] = all.most > -INFINITY ? all.at : -1;
-          } else if (!(all.sum.h > 0.0f)) {
-            if (cmd.refused) {  // all that had a mass was refused: p as it was
-              refused = false;
-              ask(false);
-            } else if (lane == 0) {
-              a.bonus[r] = -1;
-            }
-          } else {
-            summed = true;
-          }
-          if (summed && !greedy) {
-            const Pair target = all.sum * u_bonus;
-            const Found f = find_lane(mine, target);
-            cmd.op = kOpFind;
-            cmd.most = all.most;
-            cmd.owner = f.lane;
-            cmd.target = target - f.before;
-          }
-        }
-      }
+      const Command cmd = decide(a, s, c, ok, greedy, r, off, n, cluster);
+      __syncwarp();
       if (lane < cluster) send(cmd, &s.cmd, (uint32_t)lane);
     }
     cluster_sync();
     if (s.cmd.op == kOpDone) break;
     const int64_t row = off + s.cmd.node;
     if (s.cmd.op == kOpFind) {
-      if (s.cmd.owner == (int32_t)rank) find_token(a, s, c, row, first, a.bonus + r);
+      if (s.cmd.owner == (int32_t)rank) find_token(a, s, c, row, first, root, a.bonus + r);
       break;
     }
     if (s.cmd.refused) {
       if (tid == 0) s.n_refused = 0;
       __syncthreads();
+#pragma unroll 1
       for (int i = s.cmd.node + 1 + tid; i < n; i += kWalkThreads) {
         const int32_t x = a.draft[off + i];
         if (a.parent[off + i] == s.cmd.node && x >= 0 && x < a.V) s.refused[atomicAdd(&s.n_refused, 1)] = x;
@@ -787,23 +1076,53 @@ __global__ void __launch_bounds__(kWalkThreads) k_sample_walk(const __grid_const
       __syncthreads();
     }
     const int64_t v0 = first + warp * a.range, v1 = min(a.V, v0 + a.range);
-    const Total t = sum_range(a, s.cmd, c, greedy, row, v0, v1, s.refused, s.cmd.refused ? s.n_refused : 0);
+    const int n_refused = s.cmd.refused ? s.n_refused : 0;
+    const Total t = sum_range(a, s.cmd, c, greedy, row, v0, v1, s.refused, n_refused, root);
     if (lane == 0) s.range[warp] = t;
     __syncthreads();
     if (warp == 0) {
       Pair part;
-      const Total sum = join(s.range, kWalkWarps, c, part);
+      float part_slope;
+      const Total sum = join(s.range, kWalkWarps, c, s.cmd.residual == 2, part, part_slope);
       if (lane == 0) send(sum, &s.total[rank], 0);
     }
     cluster_sync();
   }
 }
 
-// Blocks of a request's cluster: as many as fill the SMs, up to the eight that every device takes.
-int cluster_size(int32_t n_req, int64_t V) {
-  int c = 1;
-  while (c < kMaxCluster && 2 * c * (int64_t)n_req <= 152 && V > (int64_t)c * 8192) c *= 2;
-  return c;
+// Blocks of a request's cluster: as many as still leave all requests' clusters room at the same time.
+int cluster_size(int32_t n_req, int64_t V, int& size) {
+  constexpr int kSizes = 8;
+  static const int sizes[kSizes] = {16, 12, 8, 6, 4, 3, 2, 1};
+  static int room[64][kSizes] = {{0}};  // clusters that a device holds at once
+  int dev = 0;
+  W12_CUDA_TRY(cudaGetDevice(&dev));
+  size = 1;
+  if (dev >= 64) return W12_OK;
+  if (!room[dev][kSizes - 1]) {
+    W12_CUDA_TRY(cudaFuncSetAttribute(k_sample_walk, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
+    for (int i = 0; i < kSizes; ++i) {
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = (unsigned)sizes[i];
+      attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3((unsigned)sizes[i]);
+      cfg.blockDim = dim3(kWalkThreads);
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      int n = 0;
+      W12_CUDA_TRY(cudaOccupancyMaxActiveClusters(&n, k_sample_walk, &cfg));
+      room[dev][i] = n > 0 ? n : sizes[i] == 1;
+      if (getenv("ROOM")) printf("cluster %d: %d\n", sizes[i], n);
+    }
+  }
+  for (int i = 0; i < kSizes; ++i)
+    if (sizes[i] == 1 || (room[dev][i] >= n_req && V > sizes[i] * (int64_t)2048)) {
+      size = sizes[i];
+      break;
+    }
+  return W12_OK;
 }
 
 }  // namespace
@@ -854,7 +1173,9 @@ int tree_verify_sampled(const float* logits, int64_t stride, int64_t M, int64_t 
     for (const Range& x : out) bad = bad || (&x != &o && meet(o, x));
     if (bad) return fail(W12_ERR_INVALID_ARG, "%s: results must not overlap one another or what the call reads", fn);
   }
-  const int cluster = cluster_size(n_req, V);
+  int cluster = 1;
+  const int st = cluster_size(n_req, V, cluster);
+  if (st) return st;
   SampleArgs a{};
   a.logits = logits;
   a.probs = draft_probs;
@@ -880,12 +1201,11 @@ int tree_verify_sampled(const float* logits, int64_t stride, int64_t M, int64_t 
   a.vec = (stride & 3) == 0 && ((uintptr_t)logits & 15u) == 0;
   a.probs_vec = draft_probs && (probs_stride & 3) == 0 && ((uintptr_t)draft_probs & 15u) == 0;
   if (M > 1) {
-    const int per = kStatThreads / 32;
-    const int64_t blocks = (a.units + per - 1) / per * (int64_t)n_req, rows = (M + n_req - 1) / n_req;
-    // few requests: their rows over more blocks
-    a.parts = (int32_t)(blocks * 2 > 912 ? 1 : rows < 912 / blocks ? rows : 912 / blocks);
-    W12_CUDA_TRY(launch_dependent(k_sample_stats, dim3((unsigned)((a.units + per - 1) / per), (unsigned)n_req, (unsigned)a.parts),
-                                  kStatThreads, 0, (cudaStream_t)stream, a));
+    // three blocks an SM, if there is that much: half of the nodes have children, or nearly all
+    const int64_t tiles = (M + kStatTile - 1) / kStatTile, most = (M < kStatTile ? M : kStatTile) * (int64_t)a.units;
+    int64_t blocks = (most + kStatThreads / 32 - 1) / (kStatThreads / 32);
+    blocks = blocks < 456 ? blocks : 456;
+    W12_CUDA_TRY(launch_dependent(k_sample_stats, dim3((unsigned)blocks, (unsigned)tiles), kStatThreads, 0, (cudaStream_t)stream, a));
     W12_LAUNCH_CHECK("tree_verify_sampled: rows kernel");
   }
   cudaLaunchAttribute attr[2];
