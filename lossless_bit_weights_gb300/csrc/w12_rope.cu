@@ -34,23 +34,52 @@ __device__ __forceinline__ bool pos_request(const PosArgs& a, int r, int64_t& of
   return from >= 0 && to >= from && to <= a.rows && len >= 0 && len + n <= 0x7FFFFFFF;
 }
 
-// Chains (prompts, single tokens): a thread finds its row's request by halving.
+constexpr int kChainRows = 4;        // rows of a thread
+constexpr int kChainRequests = 2048;  // offsets that fit in shared memory
+
+// Chains (prompts, single tokens): a thread finds its first row's request by halving, in shared memory where the
+// offsets fit, and goes on from there.
 __global__ void __launch_bounds__(kPosThreads) k_chain_positions(const __grid_constant__ PosArgs a) {
   pdl_enter();
+  __shared__ int32_t offsets[kChainRequests + 1];
   const int64_t t0 = (int64_t)blockIdx.x * kPosThreads + threadIdx.x, step = (int64_t)gridDim.x * kPosThreads;
+  const bool here = a.req_offsets && a.n_req <= kChainRequests;
+  if (here)
+    for (int r = threadIdx.x; r <= a.n_req; r += kPosThreads) offsets[r] = a.req_offsets[r];
+  __syncthreads();
+  const int32_t* o = here ? offsets : a.req_offsets;
   for (int64_t r = t0; r < a.n_req; r += step) {
     int64_t off, n;
     if (!pos_request(a, (int)r, off, n)) atomicOr(a.status, kPosBadRequest);
   }
-  for (int64_t i = t0; i < a.rows; i += step) {
-    int lo = 0, hi = a.n_req;  // the last request that starts at or before row i
-    while (a.req_offsets && hi - lo > 1) {
+  for (int64_t i0 = t0 * kChainRows; i0 < a.rows; i0 += step * kChainRows) {
+    int lo = 0, hi = a.n_req;  // the last request that starts at or before row i0
+    while (o && hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (a.req_offsets[mid] <= i) lo = mid; else hi = mid;
+      if (o[mid] <= i0) lo = mid; else hi = mid;
     }
     int64_t off, n;
-    const bool ok = pos_request(a, lo, off, n) && i >= off && i < off + n;
-    a.pos[i] = ok ? (int32_t)(a.cache_len[lo] + (i - off)) : -1;
+    bool ok = pos_request(a, lo, off, n);
+    int32_t len = a.cache_len[lo], pos[kChainRows];
+#pragma unroll
+    for (int k = 0; k < kChainRows; ++k) {
+      const int64_t i = i0 + k;
+      bool next = false;
+      while (o && lo + 1 < a.n_req && o[lo + 1] <= i) {
+        ++lo;
+        next = true;
+      }
+      if (next) {
+        ok = pos_request(a, lo, off, n);
+        len = a.cache_len[lo];
+      }
+      pos[k] = ok && i >= off && i < off + n ? (int32_t)(len + (i - off)) : -1;
+    }
+    if (i0 + kChainRows <= a.rows && ((uintptr_t)a.pos & 15u) == 0) {
+      *reinterpret_cast<int4*>(a.pos + i0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+    } else {
+      for (int k = 0; k < kChainRows && i0 + k < a.rows; ++k) a.pos[i0 + k] = pos[k];
+    }
   }
 }
 
@@ -411,7 +440,8 @@ int tree_positions(const int32_t* cache_len, const int32_t* parent, const int32_
     const int fill = (int)(blocks < 16 ? blocks : 16);
     W12_CUDA_TRY(launch_dependent(k_tree_positions, dim3((unsigned)(n_req + fill)), kPosThreads, 0, (cudaStream_t)stream, a));
   } else {
-    W12_CUDA_TRY(launch_dependent(k_chain_positions, dim3((unsigned)(blocks < 152 * 8 ? blocks : 152 * 8)), kPosThreads, 0,
+    const int64_t fewer = (blocks + kChainRows - 1) / kChainRows;
+    W12_CUDA_TRY(launch_dependent(k_chain_positions, dim3((unsigned)(fewer < 152 * 8 ? fewer : 152 * 8)), kPosThreads, 0,
                                   (cudaStream_t)stream, a));
   }
   W12_LAUNCH_CHECK("tree_positions kernel");

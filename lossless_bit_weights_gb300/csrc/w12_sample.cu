@@ -24,7 +24,7 @@ namespace w12 {
 namespace {
 
 constexpr int kSampleMaxNodes = 1024;  // nodes of one request
-constexpr int kUnit = 1024;            // tokens of a row that a warp sums at once
+constexpr int kUnit = 2048;            // tokens of a row that a warp sums at once
 constexpr int kStatThreads = 256;
 constexpr int kStatTile = 1024;       // nodes whose rows a column of blocks takes
 constexpr int kStatRequests = 1024;   // offsets that fit in shared memory
@@ -49,7 +49,7 @@ struct SampleArgs {
   bool vec, probs_vec;    // rows allow 16-byte loads
 };
 
-struct UnitStat {
+struct alignas(16) UnitStat {
   float most;   // largest logit (-inf: none, NaN left out)
   int32_t at;   // its first token, of greedy requests
   float sum;    // of the masses in the units of the largest, to 2^-18
@@ -304,8 +304,8 @@ struct Rough {
   float most, slope, start, least;
 };
 
-__device__ __forceinline__ Rough make_rough(const Ref& r, const Slope& c) {
-  Rough o{r.most, c.hi, 0.0f, fmaxf(-125.0f / c.hi, -kMost)};
+__device__ __forceinline__ Rough make_rough(const Ref& r, const Slope& c, float least) {
+  Rough o{r.most, c.hi, 0.0f, least};
   if (r.shift == 0.0f && r.most < INFINITY) o.start = fmaf(r.most, c.lo, fmaf(r.most, c.hi, -r.whole));
   return o;
 }
@@ -363,20 +363,23 @@ __device__ __forceinline__ void first_at(const float4& f, int64_t i, float most,
 
 // ---------------------------------------------------------------- rows with children
 
-// Largest logit and mass of every 1024 tokens of the rows whose nodes have children (what the walk asks of a
+// Largest logit and mass of every 2048 tokens of the rows whose nodes have children (what the walk asks of a
 // node it passes).  Every block of a tile of nodes makes the list of its rows with children, and the tile's
-// warps share (row, 1024 tokens) evenly, 128 bytes a lane on their way at once and the next 4 KB coming into
+// warps share (row, 2048 tokens) evenly, 256 bytes a lane on their way at once and the next 8 KB coming into
 // L2.  Bound by the logits read once.  The masses are plain floats here: with a bound of 2^-18 on
 // their sums nearly all decisions are certain, and the walk sums again for the others.
-__global__ void __launch_bounds__(kStatThreads, 3) k_sample_stats(const __grid_constant__ SampleArgs a) {
+__global__ void __launch_bounds__(kStatThreads, 2) k_sample_stats(const __grid_constant__ SampleArgs a) {
   pdl_enter();
   __shared__ int32_t offsets[kStatRequests + 1];
-  __shared__ uint32_t inner[kStatTile / 32];
+  __shared__ uint32_t inner[kStatTile / 32];  // rows with children
   __shared__ uint16_t request[kStatTile], list[kStatTile];
+  __shared__ float4 slopes[kStatTile];  // of the listed rows: log2(e) / T, the least difference with a mass, greedy
   __shared__ int rows;
   const int tid = threadIdx.x, lane = tid & 31;
   const int64_t m0 = (int64_t)blockIdx.y * kStatTile, m1 = min(a.M, m0 + kStatTile + kSampleMaxNodes);
+  const uint32_t first = blockIdx.x * (kStatThreads / 32) + (tid >> 5), step = gridDim.x * (kStatThreads / 32);
   const bool here = a.req_offsets && a.n_req <= kStatRequests;
+  int32_t p = m0 + tid < m1 ? a.parent[m0 + tid] : -1;
   if (tid < kStatTile / 32) inner[tid] = 0;
   if (here)
 #pragma unroll 1
@@ -385,7 +388,7 @@ __global__ void __launch_bounds__(kStatThreads, 3) k_sample_stats(const __grid_c
   const int32_t* o = here ? offsets : a.req_offsets;
 #pragma unroll 1
   for (int64_t m = m0 + tid; m < m1; m += kStatThreads) {
-    const int32_t p = a.parent[m];
+    if (m != m0 + tid) p = a.parent[m];
     int lo = 0, hi = a.n_req;  // the last request that starts at or before node m
 #pragma unroll 1
     while (o && hi - lo > 1) {
@@ -404,7 +407,7 @@ __global__ void __launch_bounds__(kStatThreads, 3) k_sample_stats(const __grid_c
   if (tid < 32) {
     int before = 0;
 #pragma unroll 1
-    for (int w = 0; w < kStatTile / 32; ++w) {
+    for (int w = 0; w < kStatTile / 32 && m0 + w * 32 < a.M; ++w) {
       const uint32_t word = inner[w];
       if (word >> lane & 1u) list[before + __popc(word & ((1u << lane) - 1u))] = (uint16_t)(w * 32 + lane);
       before += __popc(word);
@@ -412,36 +415,53 @@ __global__ void __launch_bounds__(kStatThreads, 3) k_sample_stats(const __grid_c
     if (tid == 0) rows = before;
   }
   __syncthreads();
-  const int64_t items = (int64_t)rows * a.units, step = (int64_t)gridDim.x * (kStatThreads / 32);
+  if (tid < rows) {
 #pragma unroll 1
-  for (int64_t item = (int64_t)blockIdx.x * (kStatThreads / 32) + (tid >> 5); item < items; item += step) {
-    const int nth = (int)(item / a.units), unit = (int)(item - (int64_t)nth * a.units), at = list[nth];
+    for (int k = tid; k < rows; k += kStatThreads) {
+      const float T = a.temperature ? a.temperature[request[list[k]]] : 1.0f;
+      const Slope c = make_slope(T < kGreedy ? 1.0f : T);
+      slopes[k] = make_float4(c.hi, c.lo, fmaxf(-125.0f / c.hi, -kMost), T < kGreedy ? 1.0f : 0.0f);
+    }
+  }
+  __syncthreads();
+  // (at most 2^10 rows of 2^21 units)
+  const uint32_t units = a.units, items = rows * units, more = step / units, ahead = step - more * units;
+  uint32_t nth = first / units, unit = first - nth * units;
+#pragma unroll 1
+  for (uint32_t item = first; item < items; item += step) {
+    const int at = list[nth];
+    const float4 slope = slopes[nth];
     const int64_t v0 = (int64_t)unit * kUnit, v1 = min(a.V, v0 + kUnit);
     const float* x = a.logits + (m0 + at) * a.stride;
+    UnitStat* out = a.stat + (m0 + at) * a.units + unit;
     float4 f[kUnit / 128];
 #pragma unroll
     for (int k = 0; k < kUnit / 128; ++k) f[k] = four(x, v0 + k * 128 + 4 * lane, v1, a.vec, -INFINITY);
-    if (a.vec && lane == 0 && item + step < items) {
-      const int next = (int)((item + step) / a.units);
-      const int64_t n0 = (item + step - (int64_t)next * a.units) * kUnit;
-      const uint32_t bytes = (uint32_t)(min(a.V - n0, (int64_t)kUnit) & ~(int64_t)3) * 4;
-      if (bytes) prefetch_l2(a.logits + (m0 + list[next]) * a.stride + n0, bytes);
+    nth += more;
+    unit += ahead;
+    if (unit >= units) {
+      unit -= units;
+      ++nth;
     }
-    const float T = a.temperature ? a.temperature[request[at]] : 1.0f;
+    if (a.vec && lane == 0 && item + step < items) {
+      const int64_t n0 = (int64_t)unit * kUnit;
+      const uint32_t bytes = (uint32_t)(min(a.V - n0, (int64_t)kUnit) & ~(int64_t)3) * 4;
+      if (bytes) prefetch_l2(a.logits + (m0 + list[nth]) * a.stride + n0, bytes);
+    }
     float most = -INFINITY;
 #pragma unroll
     for (int k = 0; k < kUnit / 128; ++k) most = fmaxf(most, fmaxf(fmaxf(f[k].x, f[k].y), fmaxf(f[k].z, f[k].w)));
     most = warp_max(most);
     UnitStat st{most, -1, 0.0f};
     if (most > -INFINITY) {
-      if (T < kGreedy) {
-        int32_t first = 0x7FFFFFFF;
+      if (slope.w != 0.0f) {
+        int32_t token = 0x7FFFFFFF;
 #pragma unroll
-        for (int k = 0; k < kUnit / 128; ++k) first_at(f[k], v0 + k * 128 + 4 * lane, most, first);
-        st.at = __reduce_min_sync(0xFFFFFFFFu, first);
+        for (int k = 0; k < kUnit / 128; ++k) first_at(f[k], v0 + k * 128 + 4 * lane, most, token);
+        st.at = __reduce_min_sync(0xFFFFFFFFu, token);
       } else {
-        const Slope c = make_slope(T);
-        const Rough ref = make_rough(make_ref(most, c), c);
+        const Slope c{slope.x, slope.y};
+        const Rough ref = make_rough(make_ref(most, c), c, slope.z);
         if (most < INFINITY) {
 #pragma unroll
           for (int k = 0; k < kUnit / 128; ++k)
@@ -455,7 +475,7 @@ __global__ void __launch_bounds__(kStatThreads, 3) k_sample_stats(const __grid_c
         for (int o2 = 16; o2; o2 >>= 1) st.sum += __shfl_xor_sync(0xFFFFFFFFu, st.sum, o2);
       }
     }
-    if (lane == 0) a.stat[(m0 + at) * a.units + unit] = st;
+    if (lane == 0) *out = st;
   }
 }
 
@@ -1201,10 +1221,10 @@ int tree_verify_sampled(const float* logits, int64_t stride, int64_t M, int64_t 
   a.vec = (stride & 3) == 0 && ((uintptr_t)logits & 15u) == 0;
   a.probs_vec = draft_probs && (probs_stride & 3) == 0 && ((uintptr_t)draft_probs & 15u) == 0;
   if (M > 1) {
-    // three blocks an SM, if there is that much: half of the nodes have children, or nearly all
+    // two blocks an SM, if there is that much (half of the nodes have children, or nearly all)
     const int64_t tiles = (M + kStatTile - 1) / kStatTile, most = (M < kStatTile ? M : kStatTile) * (int64_t)a.units;
     int64_t blocks = (most + kStatThreads / 32 - 1) / (kStatThreads / 32);
-    blocks = blocks < 456 ? blocks : 456;
+    blocks = blocks < 304 ? blocks : 304;
     W12_CUDA_TRY(launch_dependent(k_sample_stats, dim3((unsigned)blocks, (unsigned)tiles), kStatThreads, 0, (cudaStream_t)stream, a));
     W12_LAUNCH_CHECK("tree_verify_sampled: rows kernel");
   }
