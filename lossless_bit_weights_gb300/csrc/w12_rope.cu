@@ -142,9 +142,14 @@ struct RopeArgs {
   int32_t* status;
   float eps, rot_scale;
   int32_t n_q, n_kv, d, half, block_size;
+  bool stream;
 };
 
 constexpr int kRopeThreads = 128;
+
+// Blocks on an SM, by the elements' size and the heads that a lane works on at once.
+constexpr int rope_blocks(int size, int at_once) { return size == 4 || at_once == 4 ? 7 : 8; }
+
 constexpr int kRopeMaxDim = 256;
 
 __device__ __forceinline__ float bf16_low(uint32_t w) { return __uint_as_float(w << 16); }
@@ -191,13 +196,24 @@ struct Eight<uint16_t, NEXT> {
   }
 };
 
+// (stream: more than L2 keeps, so that it should make room first)
 template <bool NEXT>
-__device__ __forceinline__ void store8(uint16_t* y, int lo, int hi, const uint32_t w[4]) {
+__device__ __forceinline__ void store8(uint16_t* y, int lo, int hi, const uint32_t w[4], bool stream) {
   if constexpr (NEXT) {
-    *reinterpret_cast<uint4*>(y + lo) = make_uint4(w[0], w[1], w[2], w[3]);
+    uint4* to = reinterpret_cast<uint4*>(y + lo);
+    const uint4 v = make_uint4(w[0], w[1], w[2], w[3]);
+    if (stream) __stcs(to, v);
+    else *to = v;
   } else {
-    *reinterpret_cast<uint2*>(y + lo) = make_uint2(w[0], w[1]);
-    *reinterpret_cast<uint2*>(y + hi) = make_uint2(w[2], w[3]);
+    uint2 *a = reinterpret_cast<uint2*>(y + lo), *b = reinterpret_cast<uint2*>(y + hi);
+    const uint2 v = make_uint2(w[0], w[1]), z = make_uint2(w[2], w[3]);
+    if (stream) {
+      __stcs(a, v);
+      __stcs(b, z);
+    } else {
+      *a = v;
+      *b = z;
+    }
   }
 }
 
@@ -219,15 +235,15 @@ __device__ __forceinline__ uint64_t turns_of(float inv_freq) {
   return bits >> 31 ? 0 - f : f;
 }
 
-// One row a block (and a share of its heads, gridDim.y), P lanes a head, eight columns a lane:
+// One row a block (and a share of its heads, gridDim.y), P lanes a head, eight columns a lane, U heads at a time:
 //   y = x * rsqrt(mean(x^2) + eps) * w,   (a, b) -> s (a cos - b sin, b cos + a sin),
 // with both columns of a pair in one lane, so that the rotation needs no exchange and the norm one sum
-// over P lanes.  The row's sines are found once, a thread each, while the first heads are on their way.
-template <typename T, int P, bool NEXT>
-__global__ void __launch_bounds__(kRopeThreads, sizeof(T) == 4 ? 6 : 8) k_qkv_rope(const __grid_constant__ RopeArgs a) {
+// over P lanes, the U heads' sums side by side.  The row's sines are found once, a thread each, while the first
+// heads are on their way; the next heads are on theirs while U are worked on.
+template <typename T, int P, bool NEXT, int U>
+__global__ void __launch_bounds__(kRopeThreads, rope_blocks(sizeof(T), U)) k_qkv_rope(const __grid_constant__ RopeArgs a) {
   constexpr int kGroups = kRopeThreads / P;  // heads of a block at a time
-  constexpr int U = 4;                       // heads of a lane on their way
-  __shared__ __align__(16) float s_cos[kRopeMaxDim / 2], s_sin[kRopeMaxDim / 2];
+  __shared__ __align__(16) float s_cos[kRopeMaxDim / 2], s_sin[kRopeMaxDim / 2], s_norm[2][kRopeMaxDim];
   __shared__ int64_t s_place;
   pdl_enter();
   const int tid = threadIdx.x, g = tid / P, u = tid % P;
@@ -236,26 +252,22 @@ __global__ void __launch_bounds__(kRopeThreads, sizeof(T) == 4 ? 6 : 8) k_qkv_ro
   const bool live = 8 * u < a.d, turned = 8 * u < 2 * a.half;
   const int lo = !NEXT && turned ? 4 * u : 8 * u, hi = !NEXT && turned ? a.half + 4 * u : 8 * u + 4;
   const T* x = static_cast<const T*>(a.x) + t * a.x_stride;
+  const bool norm = a.q_norm || a.k_norm;
   Eight<T, NEXT> f[U];
-  auto ask = [&](int h0) {
-#pragma unroll
-    for (int k = 0; k < U; ++k) {
-      const int h = h0 + g + k * step;
-      if (live && h < heads) f[k].load(x + h * a.d, lo, hi);
-      else f[k].zero();
-    }
+  auto ask = [&](Eight<T, NEXT>& to, int h) {
+    if (live && h < heads) to.load(x + h * a.d, lo, hi);
+    else to.zero();
   };
   const int32_t pos = a.pos[t];
-  ask(first);
+#pragma unroll
+  for (int k = 0; k < U; ++k) ask(f[k], first + g + k * step);
   const float freq = tid < a.half ? a.inv_freq[tid] : 0.0f;
   int64_t place = a.cache[0] ? a.slot[t] : -1;
-  float w[2][8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int c = i < 4 ? lo + i : hi + i - 4;
-    w[0][i] = a.q_norm && live ? a.q_norm[c] : 1.0f;
-    w[1][i] = a.k_norm && live ? a.k_norm[c] : 1.0f;
-  }
+  if (norm)
+    for (int c = tid; c < a.d; c += kRopeThreads) {
+      s_norm[0][c] = a.q_norm ? a.q_norm[c] : 1.0f;
+      s_norm[1][c] = a.k_norm ? a.k_norm[c] : 1.0f;
+    }
   if (pos < 0) return;  // padding
   if (tid < a.half) {  // (half <= 128 threads)
     const int32_t turn = (int32_t)((uint64_t)(uint32_t)pos * turns_of(freq) >> 32);
@@ -286,48 +298,61 @@ __global__ void __launch_bounds__(kRopeThreads, sizeof(T) == 4 ? 6 : 8) k_qkv_ro
   }
   const float inv_d = 1.0f / (float)a.d;
   for (int h0 = first; h0 < heads; h0 += U * step) {  // the same for all lanes
+    float y[U][8];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      f[k].get(y[k]);
+      ask(f[k], h0 + g + (U + k) * step);  // the next head takes this one's place
+    }
+    if (norm) {
+      float sum[U];
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        sum[k] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[k] = fmaf(y[k][i], y[k][i], sum[k]);
+      }
+#pragma unroll
+      for (int o = P / 2; o; o >>= 1)
+#pragma unroll
+        for (int k = 0; k < U; ++k) sum[k] += __shfl_xor_sync(0xFFFFFFFFu, sum[k], o);
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const int h = h0 + g + k * step, key = h >= a.n_q;
+        if (live && (key ? a.k_norm && h < a.n_q + a.n_kv : a.q_norm != nullptr)) {
+          const float r = rsqrtf(fmaf(sum[k], inv_d, a.eps));
+          const float4 w0 = *reinterpret_cast<const float4*>(s_norm[key] + lo), w1 = *reinterpret_cast<const float4*>(s_norm[key] + hi);
+          y[k][0] *= r * w0.x, y[k][1] *= r * w0.y, y[k][2] *= r * w0.z, y[k][3] *= r * w0.w;
+          y[k][4] *= r * w1.x, y[k][5] *= r * w1.y, y[k][6] *= r * w1.z, y[k][7] *= r * w1.w;
+        }
+      }
+    }
 #pragma unroll
     for (int k = 0; k < U; ++k) {
       const int h = h0 + g + k * step;
+      if (!live || h >= heads) continue;
       const int part = h < a.n_q ? 0 : h < a.n_q + a.n_kv ? 1 : 2;
-      const bool norm = part == 0 ? a.q_norm != nullptr : part == 1 && a.k_norm != nullptr;
-      float y[8];
-      f[k].get(y);
-      if (__any_sync(0xFFFFFFFFu, norm)) {
-        float sum = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sum = fmaf(y[i], y[i], sum);
-#pragma unroll
-        for (int o = P / 2; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-        const float r = rsqrtf(fmaf(sum, inv_d, a.eps));
-        if (norm) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) y[i] = y[i] * r * (part == 0 ? w[0][i] : w[1][i]);
-        }
-      }
-      if (part < 2 && turned) {
+      if (part < 2) {  // (columns that are not turned have cosine one)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          float &p = NEXT ? y[2 * i] : y[i], &q = NEXT ? y[2 * i + 1] : y[i + 4];
+          float &p = NEXT ? y[k][2 * i] : y[k][i], &q = NEXT ? y[k][2 * i + 1] : y[k][i + 4];
           const float p0 = p, q0 = q;
           p = fmaf(p0, c4[i], -(q0 * s4[i]));
           q = fmaf(q0, c4[i], p0 * s4[i]);
         }
       }
-      if (live && h < heads) {
-        const uint32_t b[4] = {pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7])};
-        const int in = h - (part == 0 ? 0 : part == 1 ? a.n_q : a.n_q + a.n_kv);
-        if (a.out[part]) store8<NEXT>(a.out[part] + t * a.out_stride[part] + in * a.d, lo, hi, b);
-        if (part && place >= 0) store8<NEXT>(a.cache[part - 1] + place + in * a.head_stride, lo, hi, b);
-      }
+      const uint32_t b[4] = {pack_bf16(y[k][0], y[k][1]), pack_bf16(y[k][2], y[k][3]), pack_bf16(y[k][4], y[k][5]),
+                             pack_bf16(y[k][6], y[k][7])};
+      const int in = h - (part == 0 ? 0 : part == 1 ? a.n_q : a.n_q + a.n_kv);
+      if (a.out[part]) store8<NEXT>(a.out[part] + t * a.out_stride[part] + in * a.d, lo, hi, b, a.stream);
+      if (part && place >= 0) store8<NEXT>(a.cache[part - 1] + place + in * a.head_stride, lo, hi, b, a.stream);
     }
-    ask(h0 + U * step);
   }
 }
 
-template <typename T, int P>
+template <typename T, int P, int U>
 constexpr auto rope_kernel(bool next) {
-  return next ? k_qkv_rope<T, P, true> : k_qkv_rope<T, P, false>;
+  return next ? k_qkv_rope<T, P, true, U> : k_qkv_rope<T, P, false, U>;
 }
 
 // Rows of two strided arrays that share no element: apart, or side by side in the rows of one array.
@@ -396,21 +421,23 @@ int rope_args(RopeArgs& a, const char* fn, const void* x, int32_t x_bf16, int64_
   a.n_kv = (int32_t)nk;
   a.d = (int32_t)d;
   a.half = form->rot_dim / 2;
+  a.stream = M * width * 2 > (int64_t)64 << 20;
   return W12_OK;
 }
 
 int launch_rope(const RopeArgs& a, int32_t x_bf16, int32_t interleaved, cudaStream_t s, const char* what) {
   const int lanes = a.d <= 64 ? 8 : a.d <= 128 ? 16 : 32;
   const bool next = interleaved || a.half == 0;  // (without a rotation the columns may as well be adjacent)
-  using Kernel = void (*)(RopeArgs);
-  const Kernel kernels[2][3] = {
-      {rope_kernel<float, 8>(next), rope_kernel<float, 16>(next), rope_kernel<float, 32>(next)},
-      {rope_kernel<uint16_t, 8>(next), rope_kernel<uint16_t, 16>(next), rope_kernel<uint16_t, 32>(next)}};
-  const Kernel kernel = kernels[x_bf16 ? 1 : 0][lanes == 8 ? 0 : lanes == 16 ? 1 : 2];
   const int groups = kRopeThreads / lanes, most = (a.n_q + 2 * a.n_kv + groups - 1) / groups;
   // few rows: their heads over more blocks
-  int64_t split = 152 * 8 / a.M;
+  int64_t split = 608 / a.M;
   split = split < 1 ? 1 : split > most ? most : split;
+  using Kernel = void (*)(RopeArgs);
+  const Kernel kernels[3][3] = {
+      {rope_kernel<float, 8, 2>(next), rope_kernel<float, 16, 2>(next), rope_kernel<float, 32, 2>(next)},
+      {rope_kernel<uint16_t, 8, 2>(next), rope_kernel<uint16_t, 16, 2>(next), rope_kernel<uint16_t, 32, 2>(next)},
+      {rope_kernel<uint16_t, 8, 4>(next), rope_kernel<uint16_t, 16, 4>(next), rope_kernel<uint16_t, 32, 4>(next)}};
+  const Kernel kernel = kernels[!x_bf16 ? 0 : split > 1 || a.q_norm || a.k_norm ? 1 : 2][lanes == 8 ? 0 : lanes == 16 ? 1 : 2];
   W12_CUDA_TRY(launch_dependent(kernel, dim3((unsigned)a.M, (unsigned)split), kRopeThreads, 0, s, a));
   W12_LAUNCH_CHECK(what);
   return W12_OK;
