@@ -809,6 +809,13 @@ def tree_attn_set_wait_limit(cycles: int) -> None:
 
 # ---------------------------------------------------------------- from the projection to attention
 
+def _one_device(first: torch.Tensor, *others) -> None:
+    dev = first.get_device()
+    for t in others:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("the call's tensors must be on one device")
+
+
 class QKVForm:
     """How rows of a fused projection become q, k and v (include/w12.h, qkv_form): norms of each
     head (q_norm, k_norm [head_dim], kept as float32), then the rotation by pos * inv_freq (float32
@@ -826,19 +833,14 @@ class QKVForm:
         self.n_q_heads, self.n_heads, self.head_dim = int(n_q_heads), int(n_heads), int(head_dim)
         self.width = (self.n_q_heads + 2 * self.n_heads) * self.head_dim
         self._keep = [t for t in (q_norm, k_norm, inv_freq) if t is not None]
+        _one_device(*self._keep) if self._keep else None
+        self.device = self._keep[0].get_device() if self._keep else None
         self._desc = qkv_form(_ptr(q_norm), _ptr(k_norm), _ptr(inv_freq), eps, rot_scale, self.n_q_heads, self.n_heads,
                               self.head_dim, 0 if inv_freq is None else 2 * inv_freq.numel(), int(interleaved))
         self._ref = ctypes.byref(self._desc)
 
     def desc(self):
         return self._ref
-
-
-def _one_device(first: torch.Tensor, *others) -> None:
-    dev = first.get_device()
-    for t in others:
-        if t is not None and t.get_device() != dev:
-            raise ValueError("the call's tensors must be on one device")
 
 
 def tree_positions(cache_len, parent=None, req_offsets=None, rows: int | None = None, pos=None, status=None, stream=None):
@@ -884,18 +886,32 @@ def _rope_out(t, name: str, M: int, heads: int, dim: int):
     return t
 
 
+def _rope_outs(x, form: QKVForm, pos, q, k, v, M: int, bf16: bool, want_kv: bool, stream):
+    """The rows that are written: those given, checked, or new ones."""
+    _one_device(x, pos, q, k, v)
+    if form.device is not None and form.device != x.get_device():
+        raise ValueError("the call's tensors must be on one device")
+    new = x.dtype if bf16 else torch.bfloat16
+    d, nq, nk = form.head_dim, form.n_q_heads, form.n_heads
+    q = _empty((M, nq, d), new, x.device, stream) if q is None else _rope_out(q, "q", M, nq, d)
+    if k is not None:
+        _rope_out(k, "k", M, nk, d)
+    elif want_kv:
+        k = _empty((M, nk, d), new, x.device, stream)
+    if v is not None:
+        _rope_out(v, "v", M, nk, d)
+    elif want_kv:
+        v = _empty((M, nk, d), new, x.device, stream)
+    return q, k, v
+
+
 def qkv_rope(x, form: QKVForm, pos, q=None, k=None, v=None, stream=None):
     """q [M, query heads, D], k and v [M, heads, D] bf16 of the projection's rows x [M, form.width]
     (float32 or bf16, any row stride) at the positions pos [M] int32 (see include/w12.h).  Rows with a
     negative position are left as they were: give q, k and v for a batch with padding.  They may be
     parts of one array, and of x itself in its own places where x is bf16.  Returns (q, k, v)."""
     M, bf16 = _rope_rows(x, form, pos)
-    new = x.dtype if bf16 else torch.bfloat16
-    shapes = (form.n_q_heads, form.n_heads, form.n_heads)
-    out = [_empty((M, h, form.head_dim), new, x.device, stream) if t is None else _rope_out(t, n, M, h, form.head_dim)
-           for t, n, h in zip((q, k, v), "qkv", shapes)]
-    q, k, v = out
-    _one_device(x, pos, q, k, v, *form._keep)
+    q, k, v = _rope_outs(x, form, pos, q, k, v, M, bf16, True, stream)
     _check((_lib or lib()).qkv_rope(
         x.data_ptr(), bf16, _row_stride(x), M, form.desc(), pos.data_ptr(), q.data_ptr(), q.stride(0), k.data_ptr(),
         k.stride(0), v.data_ptr(), v.stride(0), _raw_stream(stream, x)))
@@ -910,23 +926,15 @@ def kv_append(x, form: QKVForm, pos, cache: KVCache, slot, layer: int = 0, q=Non
     M, bf16 = _rope_rows(x, form, pos)
     if slot.dtype != torch.int64 or not slot.is_cuda or not slot.is_contiguous() or slot.numel() != M:
         raise ValueError(f"slot must be a contiguous int64 CUDA tensor of {M} entries")
-    if (cache.n_heads, cache.head_dim) != (form.n_heads, form.head_dim):
+    if cache.n_heads != form.n_heads or cache.head_dim != form.head_dim:
         raise ValueError(f"the cache must hold {form.n_heads} heads of {form.head_dim}")
-    new = x.dtype if bf16 else torch.bfloat16
-    out = []
-    for t, n, h in zip((q, k, v), "qkv", (form.n_q_heads, form.n_heads, form.n_heads)):
-        if t is not None:
-            t = _rope_out(t, n, M, h, form.head_dim)
-        elif rows or n == "q":
-            t = _empty((M, h, form.head_dim), new, x.device, stream)
-        out.append(t)
-    q, k, v = out
+    q, k, v = _rope_outs(x, form, pos, q, k, v, M, bf16, rows, stream)
     status = _zero_status(status, x.device, stream)
-    _one_device(x, pos, slot, cache.k, cache.v, q, k, v, status, *form._keep)
-    stride = lambda t: 0 if t is None else t.stride(0)
+    _one_device(x, slot, cache.k, cache.v, status)
     _check((_lib or lib()).kv_append(
         x.data_ptr(), bf16, _row_stride(x), M, form.desc(), pos.data_ptr(), cache.desc(), layer, slot.data_ptr(),
-        q.data_ptr(), q.stride(0), _ptr(k), stride(k), _ptr(v), stride(v), status.data_ptr(), _raw_stream(stream, x)))
+        q.data_ptr(), q.stride(0), _ptr(k), 0 if k is None else k.stride(0), _ptr(v), 0 if v is None else v.stride(0),
+        status.data_ptr(), _raw_stream(stream, x)))
     return q, k, v, status
 
 

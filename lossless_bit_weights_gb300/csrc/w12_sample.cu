@@ -10,10 +10,10 @@
 // a refusal costs one sum over the vocabulary, no row is ever stored, and the bonus token comes from the
 // masses max(e - tau q, 0) of the last sum.  Without q, q is 1 at the child's own token.
 //
-// The bonus is the first token whose cumulative mass passes u M.  For large vocabularies the borders between
-// tokens stand 2^-20 of the mass apart and closer, so the masses have to be good to far more than a float:
-// each is a pair of floats (2^-28 of its value, from the exponent's 48-bit product on), summed without loss, and the
-// sums stay pairs of floats.  (With plain floats one token in some hundreds would differ from the formula's.)
+// The bonus is the first token whose cumulative mass passes u M.  In a large vocabulary the borders between
+// tokens stand 2^-20 of the mass apart and closer, so a mass has to be good to far more than a float: it
+// is a pair of floats (2^-30 of its value), summed without loss, and the sums stay pairs.  (With plain floats one
+// token in some hundreds would differ from the formula's.)
 #include <cstdint>
 #include <type_traits>
 
@@ -24,13 +24,14 @@ namespace w12 {
 namespace {
 
 constexpr int kSampleMaxNodes = 1024;  // nodes of one request
-constexpr int kUnit = 2048;            // tokens of a row that a warp sums at once
+constexpr int kUnit = 1024;            // tokens of a row that a warp sums at once
 constexpr int kStatThreads = 256;
 constexpr int kStatTile = 1024;       // nodes whose rows a column of blocks takes
 constexpr int kStatRequests = 1024;   // offsets that fit in shared memory
 constexpr int kWalkThreads = 512;
 constexpr int kWalkWarps = kWalkThreads / 32;
 constexpr int kMaxCluster = 16;
+static_assert(kWalkWarps <= 16 && kMaxCluster <= 16, "join takes a part a lane of half a warp");
 constexpr int32_t kSampleBadRequest = 1;
 constexpr float kGreedy = 1e-5f;       // temperatures below are the limit at zero
 constexpr float kMost = 3.402823466e38f;  // the largest float
@@ -50,9 +51,9 @@ struct SampleArgs {
 };
 
 struct alignas(16) UnitStat {
-  float most;   // largest logit (-inf: none, NaN left out)
-  int32_t at;   // its first token, of greedy requests
-  float sum;    // of the masses in the units of the largest, to 2^-18
+  float most;    // largest logit (-inf: none, NaN left out)
+  int32_t at;    // its first token, of greedy requests
+  float sum[2];  // of the masses, in the units of the largest (without q to 2^-18)
 };
 
 __device__ __forceinline__ bool sample_request(const SampleArgs& a, int r, int64_t& off, int& n) {
@@ -173,16 +174,16 @@ __device__ __forceinline__ Found find_lane(Pair mine, Pair target) {
 
 // ---------------------------------------------------------------- masses
 
-// log2(e) / T as a pair of floats.
+// log2(e) / T as a pair of floats, and about one over it.
 struct Slope {
-  float hi, lo;
+  float hi, lo, over;
 };
 
 __device__ __forceinline__ Slope make_slope(float T) {
   const float x = __fdiv_rn(1.44269502162933349609375f, T);
   // (the first quotient's remainder is exact)
   const float rest = fmaf(-x, T, 1.44269502162933349609375f) + 1.925963033500011e-8f;
-  return T < INFINITY ? Slope{x, __fdiv_rn(rest, T)} : Slope{0.0f, 0.0f};
+  return T < INFINITY ? Slope{x, __fdiv_rn(rest, T), T * 0.6931471805599453f} : Slope{0.0f, 0.0f, INFINITY};
 }
 
 // What the masses of a row, or of a part of it, are measured in: about the mass of its largest logit
@@ -201,7 +202,7 @@ __device__ __forceinline__ Ref make_ref(float most, const Slope& c) {
 
 // The smallest logit, less the shift, that is looked at: 2^-125 of a unit.
 __device__ __forceinline__ float least_of(const Ref& r, const Slope& c) {
-  return fmaxf((r.whole - 125.0f) / c.hi, -kMost);
+  return fmaxf((r.whole - 125.0f) * c.over, -kMost);
 }
 
 __device__ __noinline__ float far_scale(Ref from, Ref to, Slope c) {
@@ -237,6 +238,7 @@ struct Scale {
   uint32_t root;
   float rest;
   bool endless;  // the largest logit is +inf: the infinite ones alone have a mass, alike
+  bool plain;    // neither that nor a shift, nor a slope at which the clamp does not tell -inf
 };
 
 constexpr float kMagic = 393216.0f;  // 1.5 * 2^18: a float near it holds 32nds, its bits are kMagicBits + 32 x
@@ -254,6 +256,7 @@ __device__ __forceinline__ Scale make_scale(const Ref& r, const Slope& c, float2
   s.hi = c.hi;
   s.lo = c.lo;
   s.endless = r.most == INFINITY;
+  s.plain = !s.endless && r.shift == 0.0f && c.hi >= kSlow;
   s.least = s.endless ? 0.0f : least_of(r, c);
   s.root = root_bits(root.x, threadIdx.x & 31, s.endless ? 0.0f : r.whole);
   s.rest = root.y;
@@ -263,8 +266,8 @@ __device__ __forceinline__ Scale make_scale(const Ref& r, const Slope& c, float2
 // The masses of two logits, h + lo each: 2^(x - whole), x = (l - shift) c.  With 32 x rounded to n,
 // 2^x = 2^(n / 32) 2^g, |g| <= 1/64; g comes from fused products without their rounding, and 2^g - 1 = g (ln 2 +
 // g (a + g b)) to 2^-33 (Taylor's terms, the second raised by 0.83 of the fourth's most), so that with the root's rest
-// a mass is good to 2^-30.  All lanes of a warp take part.  Without ANY the row has neither shift nor end,
-// and what has no mass comes out as 2^-125 or so.
+// a mass is good to 2^-30.  What has none comes out as 2^-125 or so, which least2 and left2 take for nothing.
+// All lanes of a warp take part.  Without ANY the scale is plain.
 template <bool ANY>
 __device__ __forceinline__ void mass2(uint64_t l, const Scale& c, uint64_t& h, uint64_t& lo) {
   const float2 given = split2(l);
@@ -299,24 +302,6 @@ __device__ __forceinline__ void least2(uint64_t& h, uint64_t& lo) {
   lo = pair2(x ? gf.x : 0.0f, y ? gf.y : 0.0f);
 }
 
-// A mass to 2^-20 or so: 2^((l - most) c + (most c - whole)).
-struct Rough {
-  float most, slope, start, least;
-};
-
-__device__ __forceinline__ Rough make_rough(const Ref& r, const Slope& c, float least) {
-  Rough o{r.most, c.hi, 0.0f, least};
-  if (r.shift == 0.0f && r.most < INFINITY) o.start = fmaf(r.most, c.lo, fmaf(r.most, c.hi, -r.whole));
-  return o;
-}
-
-__device__ __forceinline__ float rough(float l, const Rough& r) {
-  const float d = l - r.most;
-  float e;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fmaf(d, r.slope, r.start)));
-  return d >= r.least ? e : 0.0f;
-}
-
 // What a refusal leaves of a mass, max(e - tau q, 0), for two tokens; less than 2^-100 is nothing.  (Where
 // something is left, h is the larger or the difference exact, so its rounding comes back from three operations.)
 __device__ __forceinline__ void left2(uint64_t& h, uint64_t& lo, uint64_t q, float tau_hi, float tau_lo) {
@@ -329,6 +314,41 @@ __device__ __forceinline__ void left2(uint64_t& h, uint64_t& lo, uint64_t q, flo
   lo = pair2(x ? tf.x : 0.0f, y ? tf.y : 0.0f);
 }
 
+// The masses of four tokens, unless LEFT will look at them those below 2^-100 left out.
+struct Four {
+  uint64_t h[2], lo[2];
+};
+
+template <bool ANY, bool LEFT = false>
+__device__ __forceinline__ Four masses4(const float4& f, const Scale& c) {
+  Four m;
+  mass2<ANY>(pair2(f.x, f.y), c, m.h[0], m.lo[0]);
+  mass2<ANY>(pair2(f.z, f.w), c, m.h[1], m.lo[1]);
+  if (!LEFT) {
+    least2(m.h[0], m.lo[0]);
+    least2(m.h[1], m.lo[1]);
+  }
+  return m;
+}
+
+// A mass to 2^-20 or so, by plain floats: 2^((l - most) c + (most c - whole)).
+struct Rough {
+  float most, slope, start, least;
+};
+
+__device__ __forceinline__ Rough make_rough(const Ref& r, const Slope& c) {
+  Rough o{r.most, c.hi, 0.0f, fmaxf(-125.0f * c.over, -kMost)};
+  if (r.shift == 0.0f) o.start = fmaf(r.most, c.lo, fmaf(r.most, c.hi, -r.whole));
+  return o;
+}
+
+__device__ __forceinline__ float rough(float l, const Rough& r) {
+  const float d = l - r.most;
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fmaf(d, r.slope, r.start)));
+  return d >= r.least ? e : 0.0f;
+}
+
 // A running sum of pairs, two at a time.  It starts at 4, above every mass, so that an addition's rounding
 // comes back from three operations.
 struct Sum {
@@ -337,6 +357,10 @@ struct Sum {
     const uint64_t n = add2(s, h), t = sub2(h, sub2(n, s));
     s = n;
     rest = add2(rest, add2(t, lo));
+  }
+  __device__ __forceinline__ void add(const Four& m) {
+    add(m.h[0], m.lo[0]);
+    add(m.h[1], m.lo[1]);
   }
   __device__ __forceinline__ Pair value() const {
     const float2 a = split2(s), b = split2(rest);
@@ -363,22 +387,23 @@ __device__ __forceinline__ void first_at(const float4& f, int64_t i, float most,
 
 // ---------------------------------------------------------------- rows with children
 
-// Largest logit and mass of every 2048 tokens of the rows whose nodes have children (what the walk asks of a
+// Largest logit and mass of every 1024 tokens of the rows whose nodes have children (what the walk asks of a
 // node it passes).  Every block of a tile of nodes makes the list of its rows with children, and the tile's
-// warps share (row, 2048 tokens) evenly, 256 bytes a lane on their way at once and the next 8 KB coming into
-// L2.  Bound by the logits read once.  The masses are plain floats here: with a bound of 2^-18 on
-// their sums nearly all decisions are certain, and the walk sums again for the others.
+// warps share (row, 1024 tokens) evenly, 128 bytes a lane on their way at once and the next 4 KB coming into
+// L2.  Bound by the logits read once.  Without q the sums only serve decisions, which plain floats (good to
+// 2^-18 together) nearly always tell, and the walk sums again for the others: 64 chains of five in 59 us, 72 with pairs.
 __global__ void __launch_bounds__(kStatThreads, 2) k_sample_stats(const __grid_constant__ SampleArgs a) {
   pdl_enter();
   __shared__ int32_t offsets[kStatRequests + 1];
   __shared__ uint32_t inner[kStatTile / 32];  // rows with children
   __shared__ uint16_t request[kStatTile], list[kStatTile];
-  __shared__ float4 slopes[kStatTile];  // of the listed rows: log2(e) / T, the least difference with a mass, greedy
+  __shared__ float4 slopes[kStatTile];  // of the listed rows, and whether they are greedy
   __shared__ int rows;
   const int tid = threadIdx.x, lane = tid & 31;
   const int64_t m0 = (int64_t)blockIdx.y * kStatTile, m1 = min(a.M, m0 + kStatTile + kSampleMaxNodes);
   const uint32_t first = blockIdx.x * (kStatThreads / 32) + (tid >> 5), step = gridDim.x * (kStatThreads / 32);
   const bool here = a.req_offsets && a.n_req <= kStatRequests;
+  const float2 root = kRoots[lane];
   int32_t p = m0 + tid < m1 ? a.parent[m0 + tid] : -1;
   if (tid < kStatTile / 32) inner[tid] = 0;
   if (here)
@@ -420,7 +445,7 @@ __global__ void __launch_bounds__(kStatThreads, 2) k_sample_stats(const __grid_c
     for (int k = tid; k < rows; k += kStatThreads) {
       const float T = a.temperature ? a.temperature[request[list[k]]] : 1.0f;
       const Slope c = make_slope(T < kGreedy ? 1.0f : T);
-      slopes[k] = make_float4(c.hi, c.lo, fmaxf(-125.0f / c.hi, -kMost), T < kGreedy ? 1.0f : 0.0f);
+      slopes[k] = make_float4(c.hi, c.lo, c.over, T < kGreedy ? 1.0f : 0.0f);
     }
   }
   __syncthreads();
@@ -452,7 +477,7 @@ __global__ void __launch_bounds__(kStatThreads, 2) k_sample_stats(const __grid_c
 #pragma unroll
     for (int k = 0; k < kUnit / 128; ++k) most = fmaxf(most, fmaxf(fmaxf(f[k].x, f[k].y), fmaxf(f[k].z, f[k].w)));
     most = warp_max(most);
-    UnitStat st{most, -1, 0.0f};
+    UnitStat st{most, -1, {0.0f, 0.0f}};
     if (most > -INFINITY) {
       if (slope.w != 0.0f) {
         int32_t token = 0x7FFFFFFF;
@@ -460,19 +485,35 @@ __global__ void __launch_bounds__(kStatThreads, 2) k_sample_stats(const __grid_c
         for (int k = 0; k < kUnit / 128; ++k) first_at(f[k], v0 + k * 128 + 4 * lane, most, token);
         st.at = __reduce_min_sync(0xFFFFFFFFu, token);
       } else {
-        const Slope c{slope.x, slope.y};
-        const Rough ref = make_rough(make_ref(most, c), c, slope.z);
-        if (most < INFINITY) {
+        const Slope c{slope.x, slope.y, slope.z};
+        const Ref ref = make_ref(most, c);
+        if (!a.probs && most < INFINITY) {
+          const Rough r = make_rough(ref, c);
 #pragma unroll
           for (int k = 0; k < kUnit / 128; ++k)
-            st.sum += (rough(f[k].x, ref) + rough(f[k].y, ref)) + (rough(f[k].z, ref) + rough(f[k].w, ref));
-        } else {  // the infinite ones alone, alike
+            st.sum[0] += (rough(f[k].x, r) + rough(f[k].y, r)) + (rough(f[k].z, r) + rough(f[k].w, r));
 #pragma unroll
-          for (int k = 0; k < kUnit / 128; ++k)
-            st.sum += (float)((f[k].x == most) + (f[k].y == most) + (f[k].z == most) + (f[k].w == most));
+          for (int n = 16; n; n >>= 1) st.sum[0] += __shfl_xor_sync(0xFFFFFFFFu, st.sum[0], n);
+        } else {
+          const Scale scale = make_scale(ref, c, root);
+          Sum sum;
+          if (scale.plain) {
+#pragma unroll
+            for (int k = 0; k < kUnit / 128; ++k) {
+              Four m = masses4<false>(f[k], scale);
+              sum.add(m);
+            }
+          } else {
+#pragma unroll 1
+            for (int k = 0; k < kUnit / 128; ++k) {
+              const Four m = masses4<true>(four(x, v0 + k * 128 + 4 * lane, v1, a.vec, -INFINITY), scale);
+              sum.add(m);
+            }
+          }
+          const Pair all = warp_sum(sum.value());
+          st.sum[0] = all.h;
+          st.sum[1] = all.l;
         }
-#pragma unroll
-        for (int o2 = 16; o2; o2 >>= 1) st.sum += __shfl_xor_sync(0xFFFFFFFFu, st.sum, o2);
       }
     }
     if (lane == 0) *out = st;
@@ -500,19 +541,17 @@ struct Command {
   int32_t op;
   int32_t node;          // of the request
   int32_t known;         // kOpSum: `most` is the row's; else every warp finds its range's
-  int32_t residual;      // 1: tau q is taken off; 2: and p's own sum is wanted too, tau being about that
+  int32_t residual;      // tau q is taken off
   int32_t refused;       // the node's children are taken out (no q)
   int32_t owner;         // kOpFind: the block that holds the bonus token
   float most, tau_hi, tau_lo;
-  float moved;           // kOpFind: what tau has changed by since the sums were made
   Pair target;           // kOpFind: the mass before the bonus token in the owner's ranges, in the units of `most`
 };
 
 struct Total {
   float most;
   int32_t at;
-  Pair sum, whole;  // what is left; p's own sum (residual = 2)
-  float slope;      // minus the derivative of what is left by tau: q of the tokens that have some (residual = 2)
+  Pair sum;
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -541,16 +580,16 @@ __device__ __forceinline__ void send(const S& from, S* to, uint32_t rank) {
 }
 
 // Where the walk stands at a node: what it waits for, the children tried, and what refusals have left.
-enum : int32_t { kStart, kRefused, kFirst, kPrecise, kSummed };
+enum : int32_t { kStart, kRefused, kPrecise, kSummed };
 
 struct Walk {
   int32_t stage, cur, last, depth;
   bool inner;    // the node has children
-  bool rough;    // M comes from the rows' kernel, to 2^-18
+  bool rough;    // M is good to 2^-18 of p's sum only (no q)
   bool summed;   // the blocks hold the sums of what is left
   bool refused;  // a child was refused (no q)
   bool spent;    // nothing was left
-  Pair tau, Q, M, out;  // out: the refused children's masses (no q)
+  Pair tau, Q, M, out;  // out: the masses of the refused children (no q)
 };
 
 struct WalkShared {
@@ -559,7 +598,7 @@ struct WalkShared {
   Pair mass[kSampleMaxNodes];                    // its token's mass at the parent (the logit at first)
   float most[kSampleMaxNodes];                   // of rows with children
   int32_t at[kSampleMaxNodes];
-  float sum[kSampleMaxNodes];                    // to 2^-18
+  Pair sum[kSampleMaxNodes];
   uint32_t inner[kSampleMaxNodes / 32];
   Command cmd;
   Walk walk;
@@ -569,17 +608,8 @@ struct WalkShared {
   int32_t n_refused, last;
 };
 
-// The masses of four tokens from i on, without the refused ones.
-struct Four {
-  uint64_t h[2], lo[2];
-};
-
-__device__ __forceinline__ Four masses4(const float4& f, int64_t i, const Scale& c, const int32_t* refused, int n_refused) {
-  Four m;
-  mass2<true>(pair2(f.x, f.y), c, m.h[0], m.lo[0]);
-  mass2<true>(pair2(f.z, f.w), c, m.h[1], m.lo[1]);
-  least2(m.h[0], m.lo[0]);
-  least2(m.h[1], m.lo[1]);
+// The refused ones of four tokens from i on have no mass.
+__device__ __forceinline__ void without(Four& m, int64_t i, const int32_t* refused, int n_refused) {
   uint32_t out = 0;  // of the four
 #pragma unroll 1
   for (int k = 0; k < n_refused; ++k) {
@@ -591,18 +621,11 @@ __device__ __forceinline__ Four masses4(const float4& f, int64_t i, const Scale&
     const uint64_t k0 = (out & 1u ? 0 : low) | (out & 2u ? 0 : high), k1 = (out & 4u ? 0 : low) | (out & 8u ? 0 : high);
     m.h[0] &= k0, m.lo[0] &= k0, m.h[1] &= k1, m.lo[1] &= k1;
   }
-  return m;
 }
 
 __device__ __forceinline__ void left4(Four& m, const float4& q, float tau_hi, float tau_lo) {
   left2(m.h[0], m.lo[0], pair2(q.x, q.y), tau_hi, tau_lo);
   left2(m.h[1], m.lo[1], pair2(q.z, q.w), tau_hi, tau_lo);
-}
-
-// q of the tokens that have something left.
-__device__ __forceinline__ float slope4(const Four& m, const float4& q) {
-  const float2 a = split2(m.h[0]), b = split2(m.h[1]);
-  return ((a.x != 0.0f ? q.x : 0.0f) + (a.y != 0.0f ? q.y : 0.0f)) + ((b.x != 0.0f ? q.z : 0.0f) + (b.y != 0.0f ? q.w : 0.0f));
 }
 
 __device__ __forceinline__ float chance(float q) { return fmaxf(q, 0.0f); }  // (NaN: 0)
@@ -616,8 +639,7 @@ __device__ __forceinline__ Total sum_range(const SampleArgs& a, const Command& c
   const float* x = a.logits + row * a.stride;
   const float* p = a.probs ? a.probs + row * a.probs_stride : nullptr;
   constexpr int U = 2;
-  const int mode = cmd.residual;
-  Total t{cmd.most, 0x7FFFFFFF, {0.0f, 0.0f}, {0.0f, 0.0f}, 0.0f};
+  Total t{cmd.most, 0x7FFFFFFF, {0.0f, 0.0f}};
   if (!cmd.known) {
     t.most = -INFINITY;
 #pragma unroll 1
@@ -640,94 +662,53 @@ __device__ __forceinline__ Total sum_range(const SampleArgs& a, const Command& c
     return t;
   }
   const Scale scale = make_scale(make_ref(t.most, c), c, root);
-  Sum sum, whole;
-  auto add = [&](Four& m, const float4& q, bool left) {
-    if (left) {
-      if (mode == 2) {
-        whole.add(m.h[0], m.lo[0]);
-        whole.add(m.h[1], m.lo[1]);
-      }
-      left4(m, q, cmd.tau_hi, cmd.tau_lo);
-      if (mode == 2) t.slope += slope4(m, q);
-    }
-    sum.add(m.h[0], m.lo[0]);
-    sum.add(m.h[1], m.lo[1]);
-  };
+  Sum sum;
   bool mine = false;  // does the range hold a refused token
 #pragma unroll 1
   for (int k = 0; k < n_refused; ++k) mine = mine || (refused[k] >= v0 && refused[k] < v1);
-  const bool whole_steps = a.vec && (!mode || a.probs_vec) && !scale.endless && scale.shift == 0.0f && scale.hi >= kSlow;
+  const bool whole_steps = a.vec && (!cmd.residual || a.probs_vec) && scale.plain;
 #pragma unroll 1
   for (int64_t i0 = v0; i0 < v1;) {
     bool plain = whole_steps && i0 + 128 * U <= v1;
     if (plain && mine)
 #pragma unroll 1
       for (int k = 0; k < n_refused; ++k) plain = plain && !(refused[k] >= i0 && refused[k] < i0 + 128 * U);
+    const int64_t i = i0 + 4 * lane;
     if (plain) {  // no branches inside, so that a warp's masses overlap one another
-      const int64_t i = i0 + 4 * lane;
       float4 f[U], q[U];
       Four m[U];
 #pragma unroll
       for (int k = 0; k < U; ++k) f[k] = *reinterpret_cast<const float4*>(x + i + k * 128);
-      if (mode) {
+      if (cmd.residual) {
 #pragma unroll
         for (int k = 0; k < U; ++k) q[k] = *reinterpret_cast<const float4*>(p + i + k * 128);
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
-          mass2<false>(pair2(f[k].x, f[k].y), scale, m[k].h[0], m[k].lo[0]);
-          mass2<false>(pair2(f[k].z, f[k].w), scale, m[k].h[1], m[k].lo[1]);
-        }
-        if (mode == 2) {
+        for (int k = 0; k < U; ++k) m[k] = masses4<false, true>(f[k], scale);
 #pragma unroll
-          for (int k = 0; k < U; ++k) {
-            whole.add(m[k].h[0], m[k].lo[0]);
-            whole.add(m[k].h[1], m[k].lo[1]);
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-          q[k] = chance4(q[k]);
-          left4(m[k], q[k], cmd.tau_hi, cmd.tau_lo);
-        }
-        if (mode == 2) {
-#pragma unroll
-          for (int k = 0; k < U; ++k) t.slope += slope4(m[k], q[k]);
-        }
+        for (int k = 0; k < U; ++k) left4(m[k], chance4(q[k]), cmd.tau_hi, cmd.tau_lo);
       } else {
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
-          mass2<false>(pair2(f[k].x, f[k].y), scale, m[k].h[0], m[k].lo[0]);
-          mass2<false>(pair2(f[k].z, f[k].w), scale, m[k].h[1], m[k].lo[1]);
-          least2(m[k].h[0], m[k].lo[0]);
-          least2(m[k].h[1], m[k].lo[1]);
-        }
+        for (int k = 0; k < U; ++k) m[k] = masses4<false>(f[k], scale);
       }
 #pragma unroll
-      for (int k = 0; k < U; ++k) {
-        sum.add(m[k].h[0], m[k].lo[0]);
-        sum.add(m[k].h[1], m[k].lo[1]);
-      }
+      for (int k = 0; k < U; ++k) sum.add(m[k]);
       i0 += 128 * U;
     } else {
-      const int64_t i = i0 + 4 * lane;
-      Four m = masses4(four(x, i, v1, a.vec, -INFINITY), i, scale, refused, mine ? n_refused : 0);
-      add(m, mode ? chance4(four(p, i, v1, a.probs_vec, 0.0f)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f), mode != 0);
+      Four m = masses4<true>(four(x, i, v1, a.vec, -INFINITY), scale);
+      if (mine) without(m, i, refused, n_refused);
+      if (cmd.residual) left4(m, chance4(four(p, i, v1, a.probs_vec, 0.0f)), cmd.tau_hi, cmd.tau_lo);
+      sum.add(m);
       i0 += 128;
     }
   }
   t.sum = warp_sum(sum.value());
-  if (mode) {
-    t.whole = warp_sum(whole.value());
-#pragma unroll
-    for (int o = 16; o; o >>= 1) t.slope += __shfl_xor_sync(0xFFFFFFFFu, t.slope, o);
-  }
   return t;
 }
 
-// The parts' largest logit, their first token at it, and their sums in its units (a part a lane, 0 <= lane < n <= 16).
-__device__ __forceinline__ Total join(const Total* part, int n, const Slope& c, bool whole, Pair& mine, float& slope) {
+// The parts' largest logit, their first token at it, and their sum in its units (a part a lane, 0 <= lane < n <= 16).
+__device__ __forceinline__ Total join(const Total* part, int n, const Slope& c, Pair& mine) {
   const int lane = threadIdx.x & 31;
-  Total t{-INFINITY, 0x7FFFFFFF, {0.0f, 0.0f}, {0.0f, 0.0f}, 0.0f};
+  Total t{-INFINITY, 0x7FFFFFFF, {0.0f, 0.0f}};
   if (lane < n) t = part[lane];
   float most = t.most;
 #pragma unroll
@@ -744,16 +725,6 @@ __device__ __forceinline__ Total join(const Total* part, int n, const Slope& c, 
 #pragma unroll 1
   for (int o = 8; o; o >>= 1) t.sum = t.sum + shuffle_xor(t.sum, o);
   t.sum = shuffle(t.sum, 0);
-  slope = t.slope;
-  if (whole) {  // (of parts in the same units)
-#pragma unroll 1
-    for (int o = 8; o; o >>= 1) {
-      t.whole = t.whole + shuffle_xor(t.whole, o);
-      t.slope += __shfl_xor_sync(0xFFFFFFFFu, t.slope, o);
-    }
-    t.whole = shuffle(t.whole, 0);
-    t.slope = __shfl_sync(0xFFFFFFFFu, t.slope, 0);
-  }
   return t;
 }
 
@@ -771,7 +742,6 @@ __device__ __forceinline__ void find_token(const SampleArgs& a, WalkShared& s, c
     const Ref part = make_ref(s.range[lane].most, c);
     k = scale_of(part, whole, c);
     mine = {s.range[lane].sum.h * k, s.range[lane].sum.l * k};
-    mine = mine - Pair{cmd.moved * s.range[lane].slope, 0.0f};
   }
   const Found in = find_lane(mine, cmd.target);
   const int range = max(in.lane, 0);
@@ -788,7 +758,8 @@ __device__ __forceinline__ void find_token(const SampleArgs& a, WalkShared& s, c
 #pragma unroll 1
   for (int64_t base = v0; base < v1; base += 128 * kWalkWarps) {
     const int64_t i = base + warp * 128 + 4 * lane;
-    Four f = masses4(four(x, i, v1, a.vec, -INFINITY), i, scale, s.refused, n_refused);
+    Four f = masses4<true>(four(x, i, v1, a.vec, -INFINITY), scale);
+    without(f, i, s.refused, n_refused);
     if (cmd.residual) left4(f, chance4(four(p, i, v1, a.probs_vec, 0.0f)), cmd.tau_hi, cmd.tau_lo);
     const float2 h0 = split2(f.h[0]), l0 = split2(f.lo[0]), h1 = split2(f.h[1]), l1 = split2(f.lo[1]);
     const Pair none{0.0f, 0.0f};  // (adding it brings a pair in order)
@@ -833,18 +804,17 @@ __device__ __forceinline__ Command decide(const SampleArgs& a, WalkShared& s, Sl
   Walk w = s.walk;
   Command cmd = s.cmd;    // the last one
   Pair mine{0.0f, 0.0f};  // of a block, in its lane
-  float slope = 0.0f;
   Total all{};
   auto enter = [&](int node) {
     w.cur = w.last = node;
     w.inner = s.inner[node >> 5] >> (node & 31) & 1u;
     w.summed = w.spent = w.refused = false;
-    w.rough = true;
+    w.rough = !a.probs;
     w.tau = w.out = zero;
     w.Q = one;
-    w.M = {w.inner ? s.sum[node] : 0.0f, 0.0f};
+    w.M = w.inner ? s.sum[node] : zero;
   };
-  auto ask = [&](int residual, bool off_refused) {
+  auto ask = [&](bool residual, bool off_refused) {
     cmd.op = kOpSum;
     cmd.node = w.cur;
     cmd.known = w.inner;
@@ -853,7 +823,6 @@ __device__ __forceinline__ Command decide(const SampleArgs& a, WalkShared& s, Sl
     cmd.refused = off_refused;
     cmd.tau_hi = w.tau.h;
     cmd.tau_lo = w.tau.l;
-    cmd.moved = 0.0f;
   };
   if (ok && w.stage == kStart) {
     enter(0);
@@ -862,21 +831,9 @@ __device__ __forceinline__ Command decide(const SampleArgs& a, WalkShared& s, Sl
   }
   cmd.op = kOpDone;
   if (ok) {
-    if (w.stage != kStart) all = join(s.total, cluster, c, w.stage == kFirst, mine, slope);  // the blocks' sums
+    if (w.stage != kStart) all = join(s.total, cluster, c, mine);  // the blocks' sums
     bool ends = w.stage == kSummed, asked = false;
-    if (w.stage == kFirst) {
-      // p's sum was not known to the last bits, so tau was off: what is left has moved with it along its
-      // derivative.  (It bends only where a token's rest is within that of zero: 2^-36 or less.)
-      const Pair off_by = all.whole - w.tau;
-      cmd.moved = off_by.h;
-      w.tau = all.whole;
-      cmd.tau_hi = w.tau.h;
-      cmd.tau_lo = w.tau.l;
-      mine = mine - Pair{cmd.moved * slope, 0.0f};
-      all.sum = all.sum - Pair{cmd.moved * all.slope, 0.0f};
-      w.rough = false;
-    }
-    if (w.stage == kRefused || w.stage == kFirst) {
+    if (w.stage == kRefused) {
       w.M = all.sum;
       w.summed = w.M > zero;
       w.spent = !w.summed;  // nothing is left: the bonus comes from p as it was
@@ -905,7 +862,7 @@ __device__ __forceinline__ Command decide(const SampleArgs& a, WalkShared& s, Sl
       if (greedy) {
         take = s.most[w.cur] > -INFINITY && x == s.at[w.cur];
       } else {
-        if (w.spent || !(s.sum[w.cur] > 0.0f)) continue;
+        if (w.spent || !(s.sum[w.cur].h > 0.0f)) continue;
         bool twice = false;  // a sibling with this token was refused before
 #pragma unroll 1
         for (int i0 = w.cur + 1; i0 < j && !twice; i0 += 32)
@@ -916,9 +873,9 @@ __device__ __forceinline__ Command decide(const SampleArgs& a, WalkShared& s, Sl
         const Pair mine_u = w.M * u * q, limit = a.probs ? (e - w.tau * q) * w.Q : e;
         const bool moves = !a.probs || (q > 0.0f && w.Q > zero);  // a refusal would change p
         take = (!a.probs || w.Q > zero) && limit > mine_u;
-        if (w.rough && moves && fabsf((mine_u - limit).h) <= 6.2e-5f * u * q * (w.M + w.out).h) {  // it does not tell
+        if (w.rough && fabsf((mine_u - limit).h) <= 6.2e-5f * u * (w.M + w.out).h) {  // it does not tell
           w.last = j - 1;
-          ask(0, false);
+          ask(false, false);
           w.stage = kPrecise;
           asked = true;
           continue;
@@ -933,8 +890,8 @@ __device__ __forceinline__ Command decide(const SampleArgs& a, WalkShared& s, Sl
           } else {
             w.tau = w.tau + (w.Q.h == 1.0f && w.Q.l == 0.0f ? w.M : w.M / w.Q);
             w.Q = w.Q - Pair{q, 0.0f};
-            ask(w.rough ? 2 : 1, false);
-            w.stage = w.rough ? kFirst : kRefused;
+            ask(true, false);
+            w.stage = kRefused;
             asked = true;
           }
         }
@@ -951,14 +908,14 @@ __device__ __forceinline__ Command decide(const SampleArgs& a, WalkShared& s, Sl
         if (greedy && w.inner) {
           if (lane == 0) a.bonus[r] = s.most[w.cur] > -INFINITY ? s.at[w.cur] : -1;
         } else if (!w.summed) {
-          ask(0, w.refused);
+          ask(false, w.refused);
           w.stage = kSummed;
         }
       } else if (greedy) {
         if (lane == 0) a.bonus[r] = all.most > -INFINITY ? all.at : -1;
       } else if (!(all.sum.h > 0.0f)) {
         if (cmd.refused) {  // all that had a mass was refused: p as it was
-          ask(0, false);
+          ask(false, false);
         } else if (lane == 0) {
           a.bonus[r] = -1;
         }
@@ -1016,16 +973,18 @@ __global__ void __launch_bounds__(kWalkThreads, 2) k_sample_walk(const __grid_co
       most = warp_max(most);
       const Ref ref = make_ref(most, c);
       int32_t at = 0x7FFFFFFF;
-      float sum = 0.0f;
+      Pair sum{0.0f, 0.0f};
 #pragma unroll 1
       for (int k = lane; k < a.units; k += 32) {
         const UnitStat u = st[k];
         if (u.most == most) at = min(at, u.at);
-        if (u.sum > 0.0f) sum += u.sum * scale_of(make_ref(u.most, c), ref, c);
+        if (u.sum[0] > 0.0f) {
+          const float scale = scale_of(make_ref(u.most, c), ref, c);
+          sum = sum + Pair{u.sum[0] * scale, u.sum[1] * scale};
+        }
       }
       at = __reduce_min_sync(0xFFFFFFFFu, at);
-#pragma unroll
-      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+      sum = warp_sum(sum);
       if (lane == 0) {
         s.most[i] = most;
         s.at[i] = at;
@@ -1065,9 +1024,9 @@ __global__ void __launch_bounds__(kWalkThreads, 2) k_sample_walk(const __grid_co
         if (i > 0 && i < n) s.mass[i] = mass1(s.mass[i].h, make_ref(s.most[s.parent[i]], c), c);
       }
     __syncthreads();
+  } else if (a.M > 1) {
+    pdl_enter();
   }
-
-  else if (a.M > 1) pdl_enter();
 
   if (tid == 0) s.walk.stage = kStart;
   __syncwarp();
@@ -1102,8 +1061,7 @@ __global__ void __launch_bounds__(kWalkThreads, 2) k_sample_walk(const __grid_co
     __syncthreads();
     if (warp == 0) {
       Pair part;
-      float part_slope;
-      const Total sum = join(s.range, kWalkWarps, c, s.cmd.residual == 2, part, part_slope);
+      const Total sum = join(s.range, kWalkWarps, c, part);
       if (lane == 0) send(sum, &s.total[rank], 0);
     }
     cluster_sync();
@@ -1134,7 +1092,6 @@ int cluster_size(int32_t n_req, int64_t V, int& size) {
       int n = 0;
       W12_CUDA_TRY(cudaOccupancyMaxActiveClusters(&n, k_sample_walk, &cfg));
       room[dev][i] = n > 0 ? n : sizes[i] == 1;
-      if (getenv("ROOM")) printf("cluster %d: %d\n", sizes[i], n);
     }
   }
   for (int i = 0; i < kSizes; ++i)
