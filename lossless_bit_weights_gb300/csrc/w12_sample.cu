@@ -154,11 +154,12 @@ struct Found {
   Pair before, all;
 };
 
+template <int N>  // lanes from N on hold nothing
 __device__ __forceinline__ Found find_lane(Pair mine, Pair target) {
   const int lane = threadIdx.x & 31;
   Pair upto = mine;
 #pragma unroll 1
-  for (int o = 1; o < 32; o <<= 1) {
+  for (int o = 1; o < N; o <<= 1) {
     const Pair t{__shfl_up_sync(0xFFFFFFFFu, upto.h, o), __shfl_up_sync(0xFFFFFFFFu, upto.l, o)};
     if (lane >= o) upto = t + upto;
   }
@@ -167,7 +168,7 @@ __device__ __forceinline__ Found find_lane(Pair mine, Pair target) {
   Found f;
   f.passed = over != 0;
   f.lane = over ? __ffs((int)over) - 1 : 31 - __clz((int)some);
-  f.all = shuffle(upto, 31);
+  f.all = shuffle(upto, N - 1);
   f.before = f.lane > 0 ? shuffle(upto, f.lane - 1) : Pair{0.0f, 0.0f};
   return f;
 }
@@ -537,7 +538,7 @@ __device__ __forceinline__ Pair mass1(float l, const Ref& r, const Slope& c) {
 // What the first block of a cluster has all its blocks do next.
 enum : int32_t { kOpDone, kOpSum, kOpFind };
 
-struct Command {
+struct alignas(16) Command {
   int32_t op;
   int32_t node;          // of the request
   int32_t known;         // kOpSum: `most` is the row's; else every warp finds its range's
@@ -548,7 +549,7 @@ struct Command {
   Pair target;           // kOpFind: the mass before the bonus token in the owner's ranges, in the units of `most`
 };
 
-struct Total {
+struct alignas(16) Total {
   float most;
   int32_t at;
   Pair sum;
@@ -568,15 +569,18 @@ __device__ __forceinline__ void cluster_sync() {
   cluster_wait();
 }
 
-// 4-byte words of `from` (this block's shared memory) to the same place in block `rank` of the cluster.
+// 16-byte words of `from` to the same place as `to` (this block's shared memory) in block `rank` of the cluster.
 template <typename S>
 __device__ __forceinline__ void send(const S& from, S* to, uint32_t rank) {
+  static_assert(sizeof(S) % 16 == 0 && alignof(S) == 16, "sent in 16-byte words");
   uint32_t at;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(to)), "r"(rank));
-  const uint32_t* w = reinterpret_cast<const uint32_t*>(&from);
+  const uint4* w = reinterpret_cast<const uint4*>(&from);
 #pragma unroll
-  for (int i = 0; i < (int)(sizeof(S) / 4); ++i)
-    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at + 4 * i), "r"(w[i]) : "memory");
+  for (int i = 0; i < (int)(sizeof(S) / 16); ++i)
+    asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at + 16 * i), "r"(w[i].x), "r"(w[i].y), "r"(w[i].z),
+                 "r"(w[i].w)
+                 : "memory");
 }
 
 // Where the walk stands at a node: what it waits for, the children tried, and what refusals have left.
@@ -606,6 +610,7 @@ struct WalkShared {
   Total range[kWalkWarps];
   Pair group[kWalkWarps];
   int32_t n_refused, last;
+  float u_bonus;
 };
 
 // The refused ones of four tokens from i on have no mass.
@@ -705,26 +710,33 @@ __device__ __forceinline__ Total sum_range(const SampleArgs& a, const Command& c
   return t;
 }
 
-// The parts' largest logit, their first token at it, and their sum in its units (a part a lane, 0 <= lane < n <= 16).
-__device__ __forceinline__ Total join(const Total* part, int n, const Slope& c, Pair& mine) {
+// The parts' largest logit, their first token at it (greedy), and their sum in its units (a part a lane, 0 <= lane <
+// n <= 16).  All alike: the parts' largest logits are the row's.
+__device__ __forceinline__ Total join(const Total* part, int n, const Slope& c, bool greedy, bool alike, Pair& mine) {
   const int lane = threadIdx.x & 31;
   Total t{-INFINITY, 0x7FFFFFFF, {0.0f, 0.0f}};
   if (lane < n) t = part[lane];
-  float most = t.most;
-#pragma unroll
-  for (int o = 8; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
-  most = __shfl_sync(0xFFFFFFFFu, most, 0);
-  t.at = __reduce_min_sync(0xFFFFFFFFu, t.most == most ? t.at : 0x7FFFFFFF);
-  mine = {0.0f, 0.0f};
-  if (t.sum.h > 0.0f) {
-    const float k = scale_of(make_ref(t.most, c), make_ref(most, c), c);
-    mine = {t.sum.h * k, t.sum.l * k};
+  mine = t.sum;
+  float most = __shfl_sync(0xFFFFFFFFu, t.most, 0);
+  if (!alike) {
+    most = t.most;
+#pragma unroll 1
+    for (int o = 8; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
+    most = __shfl_sync(0xFFFFFFFFu, most, 0);
+    if (t.sum.h > 0.0f) {
+      const float k = scale_of(make_ref(t.most, c), make_ref(most, c), c);
+      mine = {t.sum.h * k, t.sum.l * k};
+    }
+  }
+  if (greedy) {
+    t.at = __reduce_min_sync(0xFFFFFFFFu, t.most == most ? t.at : 0x7FFFFFFF);
+  } else {
+    t.sum = mine;
+#pragma unroll 1
+    for (int o = 8; o; o >>= 1) t.sum = t.sum + shuffle_xor(t.sum, o);
+    t.sum = shuffle(t.sum, 0);
   }
   t.most = most;
-  t.sum = mine;
-#pragma unroll 1
-  for (int o = 8; o; o >>= 1) t.sum = t.sum + shuffle_xor(t.sum, o);
-  t.sum = shuffle(t.sum, 0);
   return t;
 }
 
@@ -743,7 +755,7 @@ __device__ __forceinline__ void find_token(const SampleArgs& a, WalkShared& s, c
     k = scale_of(part, whole, c);
     mine = {s.range[lane].sum.h * k, s.range[lane].sum.l * k};
   }
-  const Found in = find_lane(mine, cmd.target);
+  const Found in = find_lane<16>(mine, cmd.target);
   const int range = max(in.lane, 0);
   const Ref ref = make_ref(s.range[range].most, c);
   Pair target = cmd.target - in.before;
@@ -768,10 +780,10 @@ __device__ __forceinline__ void find_token(const SampleArgs& a, WalkShared& s, c
     const Pair all = warp_sum(mine);
     if (lane == 0) s.group[warp] = all;
     __syncthreads();
-    const Found at = find_lane(lane < kWalkWarps ? s.group[lane] : none, target);
+    const Found at = find_lane<16>(lane < kWalkWarps ? s.group[lane] : none, target);
     if (at.passed && at.lane == warp) {
       const Pair rest = target - at.before;
-      const Found l = find_lane(mine, rest);
+      const Found l = find_lane<32>(mine, rest);
       if (lane == l.lane) {
         Pair sum = l.before;
         int found = -1, last = 0;
@@ -831,7 +843,7 @@ __device__ __forceinline__ Command decide(const SampleArgs& a, WalkShared& s, Sl
   }
   cmd.op = kOpDone;
   if (ok) {
-    if (w.stage != kStart) all = join(s.total, cluster, c, mine);  // the blocks' sums
+    if (w.stage != kStart) all = join(s.total, cluster, c, greedy, cmd.known, mine);  // the blocks' sums
     bool ends = w.stage == kSummed, asked = false;
     if (w.stage == kRefused) {
       w.M = all.sum;
@@ -923,8 +935,8 @@ __device__ __forceinline__ Command decide(const SampleArgs& a, WalkShared& s, Sl
         w.summed = true;
       }
       if (w.summed && !greedy) {
-        const Pair target = all.sum * fminf(fmaxf(a.u_bonus[r], 0.0f), 0.99999994f);
-        const Found f = find_lane(mine, target);
+        const Pair target = all.sum * s.u_bonus;
+        const Found f = find_lane<16>(mine, target);
         cmd.op = kOpFind;
         cmd.most = all.most;
         cmd.owner = f.lane;
@@ -961,6 +973,7 @@ __global__ void __launch_bounds__(kWalkThreads, 2) k_sample_walk(const __grid_co
   // ---- the nodes, and the sums of the rows with children
   if (rank == 0) {
     if (tid < kSampleMaxNodes / 32) s.inner[tid] = 0;
+    if (tid == 0) s.u_bonus = fminf(fmaxf(a.u_bonus[r], 0.0f), 0.99999994f);
     __syncthreads();
     ok = ok && T >= 0.0f;
     // A row's largest logit and its sum.  (The first rows' are read with the tree; of those without children
@@ -1061,7 +1074,7 @@ __global__ void __launch_bounds__(kWalkThreads, 2) k_sample_walk(const __grid_co
     __syncthreads();
     if (warp == 0) {
       Pair part;
-      const Total sum = join(s.range, kWalkWarps, c, part);
+      const Total sum = join(s.range, kWalkWarps, c, greedy, s.cmd.known, part);
       if (lane == 0) send(sum, &s.total[rank], 0);
     }
     cluster_sync();
