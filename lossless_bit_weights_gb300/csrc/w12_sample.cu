@@ -647,13 +647,21 @@ __device__ __forceinline__ Total sum_range(const SampleArgs& a, const Command& c
   Total t{cmd.most, 0x7FFFFFFF, {0.0f, 0.0f}};
   if (!cmd.known) {
     t.most = -INFINITY;
+    constexpr int W = 8;  // loads of a lane on their way
+    int64_t i0 = v0;
+    if (a.vec)
 #pragma unroll 1
-    for (int64_t i0 = v0; i0 < v1; i0 += 128 * U) {
-      float4 f[U];
+      for (; i0 + 128 * W <= v1; i0 += 128 * W) {
+        float4 f[W];
 #pragma unroll
-      for (int k = 0; k < U; ++k) f[k] = four(x, i0 + k * 128 + 4 * lane, v1, a.vec, -INFINITY);
+        for (int k = 0; k < W; ++k) f[k] = *reinterpret_cast<const float4*>(x + i0 + k * 128 + 4 * lane);
 #pragma unroll
-      for (int k = 0; k < U; ++k) t.most = fmaxf(t.most, fmaxf(fmaxf(f[k].x, f[k].y), fmaxf(f[k].z, f[k].w)));
+        for (int k = 0; k < W; ++k) t.most = fmaxf(t.most, fmaxf(fmaxf(f[k].x, f[k].y), fmaxf(f[k].z, f[k].w)));
+      }
+#pragma unroll 4
+    for (; i0 < v1; i0 += 128) {
+      const float4 f = four(x, i0 + 4 * lane, v1, a.vec, -INFINITY);
+      t.most = fmaxf(t.most, fmaxf(fmaxf(f.x, f.y), fmaxf(f.z, f.w)));
     }
     t.most = warp_max(t.most);
   }
