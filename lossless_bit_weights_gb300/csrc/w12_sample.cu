@@ -45,9 +45,8 @@ struct SampleArgs {
   const float *u, *u_bonus, *temperature;
   int32_t *path_len, *path_nodes, *bonus, *status;
   struct UnitStat* stat;  // [M][units], of rows with children
-  int64_t range;          // tokens of a warp in the walk, a multiple of 128
+  int64_t range;          // places of a warp in the walk, a multiple of 128
   int32_t n_req, units;
-  bool vec, probs_vec;    // rows allow 16-byte loads
 };
 
 struct alignas(16) UnitStat {
@@ -369,18 +368,41 @@ struct Sum {
   }
 };
 
-// Four tokens from i on, `fill` behind the end.
-__device__ __forceinline__ float4 four(const float* x, int64_t i, int64_t end, bool vec, float fill) {
-  if (vec && i + 4 <= end) return *reinterpret_cast<const float4*>(x + i);
+// A row of logits and its row of q.  Places are counted from the 16-byte boundary at or before the row's first logit,
+// so that any row allows 16-byte loads: tokens stand at places lo .. hi - 1, token v at v + lo.
+struct Row {
+  const float *x, *p;
+  int lo;
+  int64_t hi;
+  bool p_vec;  // q's row is aligned like the logits'
+};
+
+__device__ __forceinline__ int off_boundary(const float* x) { return (int)((uintptr_t)x >> 2 & 3u); }
+
+__device__ __forceinline__ Row row_of(const SampleArgs& a, int64_t m) {
+  Row r;
+  r.x = a.logits + m * a.stride;
+  r.lo = off_boundary(r.x);
+  r.hi = a.V + r.lo;
+  r.x -= r.lo;
+  r.p = a.probs ? a.probs + m * a.probs_stride : nullptr;
+  r.p_vec = a.probs && off_boundary(r.p) == r.lo;
+  r.p = a.probs ? r.p - r.lo : nullptr;
+  return r;
+}
+
+// Four places from i on (a multiple of four), `fill` outside lo .. hi - 1.
+__device__ __forceinline__ float4 four(const float* x, int64_t i, int lo, int64_t hi, bool vec, float fill) {
+  if (vec && i >= lo && i + 4 <= hi) return *reinterpret_cast<const float4*>(x + i);
   float4 f = make_float4(fill, fill, fill, fill);
-  if (i < end) f.x = x[i];
-  if (i + 1 < end) f.y = x[i + 1];
-  if (i + 2 < end) f.z = x[i + 2];
-  if (i + 3 < end) f.w = x[i + 3];
+  if (i >= lo && i < hi) f.x = x[i];
+  if (i + 1 >= lo && i + 1 < hi) f.y = x[i + 1];
+  if (i + 2 >= lo && i + 2 < hi) f.z = x[i + 2];
+  if (i + 3 >= lo && i + 3 < hi) f.w = x[i + 3];
   return f;
 }
 
-// The first place of `most` among a float4 of tokens from i on (least: none).
+// The first place of `most` among four from i on.
 __device__ __forceinline__ void first_at(const float4& f, int64_t i, float most, int32_t& at) {
   const int k = f.x == most ? 0 : f.y == most ? 1 : f.z == most ? 2 : f.w == most ? 3 : 4;
   if (k < 4 && (int32_t)i + k < at) at = (int32_t)i + k;
@@ -457,22 +479,23 @@ __global__ void __launch_bounds__(kStatThreads, 2) k_sample_stats(const __grid_c
   for (uint32_t item = first; item < items; item += step) {
     const int at = list[nth];
     const float4 slope = slopes[nth];
-    const int64_t v0 = (int64_t)unit * kUnit, v1 = min(a.V, v0 + kUnit);
-    const float* x = a.logits + (m0 + at) * a.stride;
+    const Row row = row_of(a, m0 + at);
+    const int64_t v0 = (int64_t)unit * kUnit, v1 = min(row.hi, v0 + kUnit);
     UnitStat* out = a.stat + (m0 + at) * a.units + unit;
     float4 f[kUnit / 128];
 #pragma unroll
-    for (int k = 0; k < kUnit / 128; ++k) f[k] = four(x, v0 + k * 128 + 4 * lane, v1, a.vec, -INFINITY);
+    for (int k = 0; k < kUnit / 128; ++k) f[k] = four(row.x, v0 + k * 128 + 4 * lane, row.lo, v1, true, -INFINITY);
     nth += more;
     unit += ahead;
     if (unit >= units) {
       unit -= units;
       ++nth;
     }
-    if (a.vec && lane == 0 && item + step < items) {
+    if (lane == 0 && item + step < items) {
+      const Row next = row_of(a, m0 + list[nth]);
       const int64_t n0 = (int64_t)unit * kUnit;
-      const uint32_t bytes = (uint32_t)(min(a.V - n0, (int64_t)kUnit) & ~(int64_t)3) * 4;
-      if (bytes) prefetch_l2(a.logits + (m0 + list[nth]) * a.stride + n0, bytes);
+      const uint32_t bytes = (uint32_t)(max(min(next.hi - n0, (int64_t)kUnit), (int64_t)0) & ~(int64_t)3) * 4;
+      if (bytes) prefetch_l2(next.x + n0, bytes);
     }
     float most = -INFINITY;
 #pragma unroll
@@ -484,7 +507,7 @@ __global__ void __launch_bounds__(kStatThreads, 2) k_sample_stats(const __grid_c
         int32_t token = 0x7FFFFFFF;
 #pragma unroll
         for (int k = 0; k < kUnit / 128; ++k) first_at(f[k], v0 + k * 128 + 4 * lane, most, token);
-        st.at = __reduce_min_sync(0xFFFFFFFFu, token);
+        st.at = __reduce_min_sync(0xFFFFFFFFu, token) - row.lo;
       } else {
         const Slope c{slope.x, slope.y, slope.z};
         const Ref ref = make_ref(most, c);
@@ -507,7 +530,7 @@ __global__ void __launch_bounds__(kStatThreads, 2) k_sample_stats(const __grid_c
           } else {
 #pragma unroll 1
             for (int k = 0; k < kUnit / 128; ++k) {
-              const Four m = masses4<true>(four(x, v0 + k * 128 + 4 * lane, v1, a.vec, -INFINITY), scale);
+              const Four m = masses4<true>(four(row.x, v0 + k * 128 + 4 * lane, row.lo, v1, true, -INFINITY), scale);
               sum.add(m);
             }
           }
@@ -597,7 +620,8 @@ struct Walk {
 };
 
 struct WalkShared {
-  int32_t parent[kSampleMaxNodes], draft[kSampleMaxNodes], refused[kSampleMaxNodes];
+  int32_t parent[kSampleMaxNodes], draft[kSampleMaxNodes];
+  int32_t refused[kSampleMaxNodes];              // places
   float u[kSampleMaxNodes], q[kSampleMaxNodes];  // of a node: its number, and q of its token at the parent
   Pair mass[kSampleMaxNodes];                    // its token's mass at the parent (the logit at first)
   float most[kSampleMaxNodes];                   // of rows with children
@@ -638,29 +662,27 @@ __device__ __forceinline__ float chance(float q) { return fmaxf(q, 0.0f); }  // 
 __device__ __forceinline__ float4 chance4(float4 q) { return make_float4(chance(q.x), chance(q.y), chance(q.z), chance(q.w)); }
 
 // One warp's range of one row: its sum, or its first largest token (greedy).
-__device__ __forceinline__ Total sum_range(const SampleArgs& a, const Command& cmd, Slope c, bool greedy, int64_t row,
+__device__ __forceinline__ Total sum_range(const Row& row, const Command& cmd, Slope c, bool greedy,
                                            int64_t v0, int64_t v1, const int32_t* refused, int n_refused, float2 root) {
   const int lane = threadIdx.x & 31;
-  const float* x = a.logits + row * a.stride;
-  const float* p = a.probs ? a.probs + row * a.probs_stride : nullptr;
+  const float *x = row.x, *p = row.p;
   constexpr int U = 2;
   Total t{cmd.most, 0x7FFFFFFF, {0.0f, 0.0f}};
   if (!cmd.known) {
     t.most = -INFINITY;
     constexpr int W = 8;  // loads of a lane on their way
     int64_t i0 = v0;
-    if (a.vec)
 #pragma unroll 1
-      for (; i0 + 128 * W <= v1; i0 += 128 * W) {
-        float4 f[W];
+    for (; i0 + 128 * W <= v1; i0 += 128 * W) {
+      float4 f[W];
 #pragma unroll
-        for (int k = 0; k < W; ++k) f[k] = *reinterpret_cast<const float4*>(x + i0 + k * 128 + 4 * lane);
+      for (int k = 0; k < W; ++k) f[k] = four(x, i0 + k * 128 + 4 * lane, row.lo, v1, true, -INFINITY);
 #pragma unroll
-        for (int k = 0; k < W; ++k) t.most = fmaxf(t.most, fmaxf(fmaxf(f[k].x, f[k].y), fmaxf(f[k].z, f[k].w)));
-      }
+      for (int k = 0; k < W; ++k) t.most = fmaxf(t.most, fmaxf(fmaxf(f[k].x, f[k].y), fmaxf(f[k].z, f[k].w)));
+    }
 #pragma unroll 4
     for (; i0 < v1; i0 += 128) {
-      const float4 f = four(x, i0 + 4 * lane, v1, a.vec, -INFINITY);
+      const float4 f = four(x, i0 + 4 * lane, row.lo, v1, true, -INFINITY);
       t.most = fmaxf(t.most, fmaxf(fmaxf(f.x, f.y), fmaxf(f.z, f.w)));
     }
     t.most = warp_max(t.most);
@@ -669,9 +691,9 @@ __device__ __forceinline__ Total sum_range(const SampleArgs& a, const Command& c
   if (greedy) {
     int32_t at = 0x7FFFFFFF;
 #pragma unroll 1
-    for (int64_t i = v0 + 4 * lane; i < v1 && at == 0x7FFFFFFF; i += 128) first_at(four(x, i, v1, a.vec, -INFINITY), i, t.most, at);
+    for (int64_t i = v0 + 4 * lane; i < v1 && at == 0x7FFFFFFF; i += 128) first_at(four(x, i, row.lo, v1, true, -INFINITY), i, t.most, at);
     __syncwarp();
-    t.at = __reduce_min_sync(0xFFFFFFFFu, at);
+    t.at = __reduce_min_sync(0xFFFFFFFFu, at) - row.lo;
     return t;
   }
   const Scale scale = make_scale(make_ref(t.most, c), c, root);
@@ -679,10 +701,10 @@ __device__ __forceinline__ Total sum_range(const SampleArgs& a, const Command& c
   bool mine = false;  // does the range hold a refused token
 #pragma unroll 1
   for (int k = 0; k < n_refused; ++k) mine = mine || (refused[k] >= v0 && refused[k] < v1);
-  const bool whole_steps = a.vec && (!cmd.residual || a.probs_vec) && scale.plain;
+  const bool whole_steps = (!cmd.residual || row.p_vec) && scale.plain;
 #pragma unroll 1
   for (int64_t i0 = v0; i0 < v1;) {
-    bool plain = whole_steps && i0 + 128 * U <= v1;
+    bool plain = whole_steps && i0 >= row.lo && i0 + 128 * U <= v1;
     if (plain && mine)
 #pragma unroll 1
       for (int k = 0; k < n_refused; ++k) plain = plain && !(refused[k] >= i0 && refused[k] < i0 + 128 * U);
@@ -707,9 +729,9 @@ __device__ __forceinline__ Total sum_range(const SampleArgs& a, const Command& c
       for (int k = 0; k < U; ++k) sum.add(m[k]);
       i0 += 128 * U;
     } else {
-      Four m = masses4<true>(four(x, i, v1, a.vec, -INFINITY), scale);
+      Four m = masses4<true>(four(x, i, row.lo, v1, true, -INFINITY), scale);
       if (mine) without(m, i, refused, n_refused);
-      if (cmd.residual) left4(m, chance4(four(p, i, v1, a.probs_vec, 0.0f)), cmd.tau_hi, cmd.tau_lo);
+      if (cmd.residual) left4(m, chance4(four(p, i, row.lo, v1, row.p_vec, 0.0f)), cmd.tau_hi, cmd.tau_lo);
       sum.add(m);
       i0 += 128;
     }
@@ -751,7 +773,7 @@ __device__ __forceinline__ Total join(const Total* part, int n, const Slope& c, 
 // The bonus token, by the block that holds it: first the warp's range, then 128 tokens, then the token.  The
 // sums of ranges, groups and lanes are rounded differently; where the last tokens do not pass the
 // target by that, it is the last one with a mass.
-__device__ __forceinline__ void find_token(const SampleArgs& a, WalkShared& s, const Slope& c, int64_t row, int64_t first,
+__device__ __forceinline__ void find_token(const SampleArgs& a, WalkShared& s, const Slope& c, const Row& row, int64_t first,
                                            float2 root, int32_t* bonus) {
   const Command& cmd = s.cmd;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -770,17 +792,15 @@ __device__ __forceinline__ void find_token(const SampleArgs& a, WalkShared& s, c
   k = scale_of(whole, ref, c);
   target = {target.h * k, target.l * k};
   const Scale scale = make_scale(ref, c, root);
-  const int64_t v0 = first + range * a.range, v1 = min(a.V, v0 + a.range);
-  const float* x = a.logits + row * a.stride;
-  const float* p = a.probs ? a.probs + row * a.probs_stride : nullptr;
+  const int64_t v0 = first + range * a.range, v1 = min(row.hi, v0 + a.range);
   const int n_refused = cmd.refused ? s.n_refused : 0;
   if (tid == 0) s.last = -1;
 #pragma unroll 1
   for (int64_t base = v0; base < v1; base += 128 * kWalkWarps) {
     const int64_t i = base + warp * 128 + 4 * lane;
-    Four f = masses4<true>(four(x, i, v1, a.vec, -INFINITY), scale);
+    Four f = masses4<true>(four(row.x, i, row.lo, v1, true, -INFINITY), scale);
     without(f, i, s.refused, n_refused);
-    if (cmd.residual) left4(f, chance4(four(p, i, v1, a.probs_vec, 0.0f)), cmd.tau_hi, cmd.tau_lo);
+    if (cmd.residual) left4(f, chance4(four(row.p, i, row.lo, v1, row.p_vec, 0.0f)), cmd.tau_hi, cmd.tau_lo);
     const float2 h0 = split2(f.h[0]), l0 = split2(f.lo[0]), h1 = split2(f.h[1]), l1 = split2(f.lo[1]);
     const Pair none{0.0f, 0.0f};  // (adding it brings a pair in order)
     const Pair m[4] = {none + Pair{h0.x, l0.x}, none + Pair{h0.y, l0.y}, none + Pair{h1.x, l1.x}, none + Pair{h1.y, l1.y}};
@@ -801,7 +821,7 @@ __device__ __forceinline__ void find_token(const SampleArgs& a, WalkShared& s, c
           if (m[e].h > 0.0f) last = e;
           if (found < 0 && m[e].h > 0.0f && sum > rest) found = e;
         }
-        *bonus = (int32_t)i + (found >= 0 ? found : last);
+        *bonus = (int32_t)(i - row.lo) + (found >= 0 ? found : last);
       }
     }
     if (at.passed) return;
@@ -809,7 +829,7 @@ __device__ __forceinline__ void find_token(const SampleArgs& a, WalkShared& s, c
     int last = -1;
 #pragma unroll
     for (int e = 0; e < 4; ++e) last = m[e].h > 0.0f ? e : last;
-    if (last >= 0) atomicMax(&s.last, (int32_t)i + last);
+    if (last >= 0) atomicMax(&s.last, (int32_t)(i - row.lo) + last);
     __syncthreads();
   }
   if (tid == 0) *bonus = s.last;
@@ -968,7 +988,7 @@ __global__ void __launch_bounds__(kWalkThreads, 2) k_sample_walk(const __grid_co
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t rank = cluster_rank();
   const int r = blockIdx.x / cluster;
-  const int64_t first = (int64_t)rank * kWalkWarps * a.range;  // the block's tokens
+  const int64_t first = (int64_t)rank * kWalkWarps * a.range;  // the block's places
   int64_t off;
   int n;
   bool ok = sample_request(a, r, off, n);
@@ -1060,7 +1080,7 @@ __global__ void __launch_bounds__(kWalkThreads, 2) k_sample_walk(const __grid_co
     }
     cluster_sync();
     if (s.cmd.op == kOpDone) break;
-    const int64_t row = off + s.cmd.node;
+    const Row row = row_of(a, off + s.cmd.node);
     if (s.cmd.op == kOpFind) {
       if (s.cmd.owner == (int32_t)rank) find_token(a, s, c, row, first, root, a.bonus + r);
       break;
@@ -1071,13 +1091,13 @@ __global__ void __launch_bounds__(kWalkThreads, 2) k_sample_walk(const __grid_co
 #pragma unroll 1
       for (int i = s.cmd.node + 1 + tid; i < n; i += kWalkThreads) {
         const int32_t x = a.draft[off + i];
-        if (a.parent[off + i] == s.cmd.node && x >= 0 && x < a.V) s.refused[atomicAdd(&s.n_refused, 1)] = x;
+        if (a.parent[off + i] == s.cmd.node && x >= 0 && x < a.V) s.refused[atomicAdd(&s.n_refused, 1)] = x + row.lo;
       }
       __syncthreads();
     }
-    const int64_t v0 = first + warp * a.range, v1 = min(a.V, v0 + a.range);
+    const int64_t v0 = first + warp * a.range, v1 = min(row.hi, v0 + a.range);
     const int n_refused = s.cmd.refused ? s.n_refused : 0;
-    const Total t = sum_range(a, s.cmd, c, greedy, row, v0, v1, s.refused, n_refused, root);
+    const Total t = sum_range(row, s.cmd, c, greedy, v0, v1, s.refused, n_refused, root);
     if (lane == 0) s.range[warp] = t;
     __syncthreads();
     if (warp == 0) {
@@ -1088,6 +1108,8 @@ __global__ void __launch_bounds__(kWalkThreads, 2) k_sample_walk(const __grid_co
     cluster_sync();
   }
 }
+
+int64_t sample_units(int64_t V) { return (V + 3 + kUnit - 1) / kUnit; }  // (a row's places start up to three early)
 
 // Blocks of a request's cluster: as many as still leave all requests' clusters room at the same time.
 int cluster_size(int32_t n_req, int64_t V, int& size) {
@@ -1132,7 +1154,7 @@ extern "C" {
 
 size_t tree_verify_sampled_workspace_size(int64_t M, int64_t V) {
   if (M < 1 || V < 1) return 0;
-  return (size_t)M * (size_t)((V + kUnit - 1) / kUnit) * sizeof(UnitStat);
+  return (size_t)M * (size_t)sample_units(V) * sizeof(UnitStat);
 }
 
 int tree_verify_sampled(const float* logits, int64_t stride, int64_t M, int64_t V, const float* draft_probs,
@@ -1140,7 +1162,7 @@ int tree_verify_sampled(const float* logits, int64_t stride, int64_t M, int64_t 
                         int32_t n_req, const float* u, const float* u_bonus, const float* temperature, int32_t* path_len,
                         int32_t* path_nodes, int32_t* bonus, int32_t* status, void* ws, size_t ws_bytes, void* stream) {
   const char* fn = "tree_verify_sampled";
-  if (M < 1 || M > 0x7FFFFFFF || V < 1 || V > 0x7FFFFFFF || stride < V || (draft_probs && probs_stride < V) || n_req < 1 ||
+  if (M < 1 || M > 0x7FFFFFFF || V < 1 || V > 0x7FFFFFF0 || stride < V || (draft_probs && probs_stride < V) || n_req < 1 ||
       n_req > 65535)
     return fail(W12_ERR_SHAPE, "%s: M=%lld, V=%lld (strides %lld, %lld), n_req=%d (1..65535) out of range", fn, (long long)M,
                 (long long)V, (long long)stride, (long long)probs_stride, n_req);
@@ -1192,12 +1214,10 @@ int tree_verify_sampled(const float* logits, int64_t stride, int64_t M, int64_t 
   a.bonus = bonus;
   a.status = status;
   a.stat = static_cast<UnitStat*>(ws);
-  a.units = (int32_t)((V + kUnit - 1) / kUnit);
+  a.units = (int32_t)sample_units(V);
   const int64_t warps = (int64_t)cluster * kWalkWarps;
-  a.range = ((V + warps - 1) / warps + 127) / 128 * 128;
+  a.range = ((V + 3 + warps - 1) / warps + 127) / 128 * 128;
   a.n_req = n_req;
-  a.vec = (stride & 3) == 0 && ((uintptr_t)logits & 15u) == 0;
-  a.probs_vec = draft_probs && (probs_stride & 3) == 0 && ((uintptr_t)draft_probs & 15u) == 0;
   if (M > 1) {
     // two blocks an SM, if there is that much (half of the nodes have children, or nearly all)
     const int64_t tiles = (M + kStatTile - 1) / kStatTile, most = (M < kStatTile ? M : kStatTile) * (int64_t)a.units;

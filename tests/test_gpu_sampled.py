@@ -154,7 +154,8 @@ class Problem:
 
 
 SHAPES = [([1], 7), ([8], 33), ([16], 1000), ([5, 0, 1, 12], 1023), ([8] * 24, 1025), ([3, 2] * 40, 130), ([64], 4099),
-          ([6] * 3, 32000), ([2, 7], 50257), ([9], 151936), ([1] * 5, 151936), ([1, 2, 3], 1), ([4, 4], 2)]
+          ([6] * 3, 32000), ([2, 7], 50257), ([9], 151936), ([1] * 5, 151936), ([3, 1], 300007),
+          ([1, 2, 3], 1), ([4, 4], 2)]
 
 
 @pytest.mark.parametrize("counts,V", SHAPES)
@@ -183,9 +184,9 @@ def test_largest_tree(w12, n):
 @pytest.mark.parametrize("V", [1, 5, 1000, 33001])
 def test_strides_and_alignment(w12, V):
     p = Problem(2, [7, 5], V)
-    for pad, shift in ((1, 0), (8, 1), (4, 4), (4 - V % 4, 0), (0, 0)):
+    for pad, shift, other in ((1, 0, 0), (8, 1, 1), (4, 4, 2), (4 - V % 4, 0, 3), (0, 0, 0), (0, 3, 1)):
         big = [torch.full((12 * (V + pad) + 8,), 50.0, device="cuda") for _ in range(2)]
-        l, q = (b[shift:shift + 12 * (V + pad)].view(12, V + pad)[:, :V] for b in big)
+        l, q = (b[s:s + 12 * (V + pad)].view(12, V + pad)[:, :V] for b, s in zip(big, (shift, other)))
         l.copy_(f32(p.logits))
         q.copy_(f32(p.probs))
         p.check(w12, logits=l, probs=q)

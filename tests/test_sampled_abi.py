@@ -113,7 +113,7 @@ def test_sampled_workspace(w12):
     size = w12.lib().tree_verify_sampled_workspace_size
     assert sampled(w12, wsb=size(4, 100) - 1) == 3
     assert size(0, 10) == 0 and size(10, 0) == 0
-    assert size(1, 1) == 16 and size(1, 1024) == 16 and size(1, 1025) == 32 and size(192, 151936) == 192 * 149 * 16
+    assert size(1, 1) == 16 and size(1, 1021) == 16 and size(1, 1022) == 32 and size(192, 151936) == 192 * 149 * 16
 
 
 def test_binding_refusals(w12):
