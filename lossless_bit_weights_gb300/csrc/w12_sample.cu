@@ -521,12 +521,9 @@ __global__ void __launch_bounds__(kStatThreads, 2) k_sample_stats(const __grid_c
         } else {
           const Scale scale = make_scale(ref, c, root);
           Sum sum;
-          if (scale.plain) {
+          if (scale.plain) {  // (what has no mass adds 2^-115 of the largest at most)
 #pragma unroll
-            for (int k = 0; k < kUnit / 128; ++k) {
-              Four m = masses4<false>(f[k], scale);
-              sum.add(m);
-            }
+            for (int k = 0; k < kUnit / 128; ++k) sum.add(masses4<false, true>(f[k], scale));
           } else {
 #pragma unroll 1
             for (int k = 0; k < kUnit / 128; ++k) {
@@ -701,7 +698,7 @@ __device__ __forceinline__ Total sum_range(const Row& row, const Command& cmd, S
   bool mine = false;  // does the range hold a refused token
 #pragma unroll 1
   for (int k = 0; k < n_refused; ++k) mine = mine || (refused[k] >= v0 && refused[k] < v1);
-  const bool whole_steps = (!cmd.residual || row.p_vec) && scale.plain;
+  const bool whole_steps = (!cmd.residual || row.p_vec) && scale.plain && v1 - v0 <= 1 << 24;
 #pragma unroll 1
   for (int64_t i0 = v0; i0 < v1;) {
     bool plain = whole_steps && i0 >= row.lo && i0 + 128 * U <= v1;
@@ -723,7 +720,7 @@ __device__ __forceinline__ Total sum_range(const Row& row, const Command& cmd, S
         for (int k = 0; k < U; ++k) left4(m[k], chance4(q[k]), cmd.tau_hi, cmd.tau_lo);
       } else {
 #pragma unroll
-        for (int k = 0; k < U; ++k) m[k] = masses4<false>(f[k], scale);
+        for (int k = 0; k < U; ++k) m[k] = masses4<false, true>(f[k], scale);
       }
 #pragma unroll
       for (int k = 0; k < U; ++k) sum.add(m[k]);
@@ -737,6 +734,8 @@ __device__ __forceinline__ Total sum_range(const Row& row, const Command& cmd, S
     }
   }
   t.sum = warp_sum(sum.value());
+  // what has no mass stands in it with 2^-125 each, together less than 2^-101
+  if (!(t.sum.h > kLeast)) t.sum = {0.0f, 0.0f};
   return t;
 }
 
