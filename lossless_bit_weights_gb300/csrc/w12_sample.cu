@@ -658,41 +658,88 @@ __device__ __forceinline__ float chance(float q) { return fmaxf(q, 0.0f); }  // 
 
 __device__ __forceinline__ float4 chance4(float4 q) { return make_float4(chance(q.x), chance(q.y), chance(q.z), chance(q.w)); }
 
-// One warp's range of one row: its sum, or its first largest token (greedy).
-__device__ __forceinline__ Total sum_range(const Row& row, const Command& cmd, Slope c, bool greedy,
-                                           int64_t v0, int64_t v1, const int32_t* refused, int n_refused, float2 root) {
+// One warp's range of a row of a greedy request: its largest logit and the first token at it.
+__device__ __forceinline__ Total first_of_range(const Row& row, int64_t v0, int64_t v1) {
+  const int lane = threadIdx.x & 31;
+  Total t{-INFINITY, 0x7FFFFFFF, {0.0f, 0.0f}};
+  constexpr int W = 8;  // loads of a lane on their way
+#pragma unroll 1
+  for (int64_t i0 = v0; i0 < v1; i0 += 128 * W) {
+    float4 f[W];
+#pragma unroll
+    for (int k = 0; k < W; ++k) f[k] = four(row.x, i0 + k * 128 + 4 * lane, row.lo, v1, true, -INFINITY);
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+      const float most = fmaxf(fmaxf(f[k].x, f[k].y), fmaxf(f[k].z, f[k].w));
+      if (most > t.most) {
+        t.most = most;
+        t.at = 0x7FFFFFFF;
+        first_at(f[k], i0 + k * 128 + 4 * lane, most, t.at);
+      }
+    }
+  }
+  const float most = warp_max(t.most);
+  t.at = __reduce_min_sync(0xFFFFFFFFu, t.most == most ? t.at : 0x7FFFFFFF) - row.lo;
+  t.most = most;
+  return t;
+}
+
+// One warp's range of a row whose largest logit is not known (a node without children): the sum of its masses in one sweep, in units of the
+// largest logit of the first tokens, and of larger ones where they come (the sum so far changes by a power
+// of two then).  A mass may pass a unit by twice before that, which stays below the 4 that Sum starts at.
+__device__ __forceinline__ Total sum_unknown(const Row& row, const Slope& c, int64_t v0, int64_t v1, float2 root) {
+  const int lane = threadIdx.x & 31;
+  constexpr int U = 4;
+  Total t{-INFINITY, 0x7FFFFFFF, {0.0f, 0.0f}};
+  Scale scale{};
+  Sum sum;
+  float limit = -INFINITY;
+#pragma unroll 1
+  for (int64_t i0 = v0; i0 < v1; i0 += 128 * U) {
+    float4 f[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) f[k] = four(row.x, i0 + k * 128 + 4 * lane, row.lo, v1, true, -INFINITY);
+    float most = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < U; ++k) most = fmaxf(most, fmaxf(fmaxf(f[k].x, f[k].y), fmaxf(f[k].z, f[k].w)));
+    if (__any_sync(0xFFFFFFFFu, most > limit)) {
+      most = warp_max(most);
+      const Ref to = make_ref(most, c);
+      if (t.most > -INFINITY) {
+        const float k = scale_of(make_ref(t.most, c), to, c);
+        t.sum = t.sum + sum.value();
+        t.sum = {t.sum.h * k, t.sum.l * k};
+        sum = Sum();
+      }
+      t.most = most;
+      limit = most + c.over;
+      scale = make_scale(to, c, root);
+    }
+    if (t.most == -INFINITY) continue;
+    if (scale.plain && v1 - v0 <= 1 << 24) {
+#pragma unroll
+      for (int k = 0; k < U; ++k) sum.add(masses4<false, true>(f[k], scale));
+    } else {
+#pragma unroll 1
+      for (int k = 0; k < U; ++k) {
+        const int64_t i = i0 + k * 128 + 4 * lane;
+        sum.add(masses4<true>(four(row.x, i, row.lo, v1, true, -INFINITY), scale));
+      }
+    }
+  }
+  t.sum = warp_sum(t.sum + sum.value());
+  if (!(t.sum.h > kLeast)) t.sum = {0.0f, 0.0f};  // (see sum_range)
+  return t;
+}
+
+// One warp's range of a row whose largest logit is known: the sum of its masses, or of what refusals leave of them.
+__device__ __forceinline__ Total sum_range(const Row& row, const Command& cmd, const Slope& c, int64_t v0, int64_t v1,
+                                           const int32_t* refused, int n_refused, float2 root) {
   const int lane = threadIdx.x & 31;
   const float *x = row.x, *p = row.p;
   constexpr int U = 2;
   Total t{cmd.most, 0x7FFFFFFF, {0.0f, 0.0f}};
-  if (!cmd.known) {
-    t.most = -INFINITY;
-    constexpr int W = 8;  // loads of a lane on their way
-    int64_t i0 = v0;
-#pragma unroll 1
-    for (; i0 + 128 * W <= v1; i0 += 128 * W) {
-      float4 f[W];
-#pragma unroll
-      for (int k = 0; k < W; ++k) f[k] = four(x, i0 + k * 128 + 4 * lane, row.lo, v1, true, -INFINITY);
-#pragma unroll
-      for (int k = 0; k < W; ++k) t.most = fmaxf(t.most, fmaxf(fmaxf(f[k].x, f[k].y), fmaxf(f[k].z, f[k].w)));
-    }
-#pragma unroll 4
-    for (; i0 < v1; i0 += 128) {
-      const float4 f = four(x, i0 + 4 * lane, row.lo, v1, true, -INFINITY);
-      t.most = fmaxf(t.most, fmaxf(fmaxf(f.x, f.y), fmaxf(f.z, f.w)));
-    }
-    t.most = warp_max(t.most);
-  }
   if (t.most == -INFINITY) return t;
-  if (greedy) {
-    int32_t at = 0x7FFFFFFF;
-#pragma unroll 1
-    for (int64_t i = v0 + 4 * lane; i < v1 && at == 0x7FFFFFFF; i += 128) first_at(four(x, i, row.lo, v1, true, -INFINITY), i, t.most, at);
-    __syncwarp();
-    t.at = __reduce_min_sync(0xFFFFFFFFu, at) - row.lo;
-    return t;
-  }
   const Scale scale = make_scale(make_ref(t.most, c), c, root);
   Sum sum;
   bool mine = false;  // does the range hold a refused token
@@ -1096,7 +1143,9 @@ __global__ void __launch_bounds__(kWalkThreads, 2) k_sample_walk(const __grid_co
     }
     const int64_t v0 = first + warp * a.range, v1 = min(row.hi, v0 + a.range);
     const int n_refused = s.cmd.refused ? s.n_refused : 0;
-    const Total t = sum_range(row, s.cmd, c, greedy, v0, v1, s.refused, n_refused, root);
+    const Total t = s.cmd.known ? sum_range(row, s.cmd, c, v0, v1, s.refused, n_refused, root)
+                    : greedy    ? first_of_range(row, v0, v1)
+                                : sum_unknown(row, c, v0, v1, root);
     if (lane == 0) s.range[warp] = t;
     __syncthreads();
     if (warp == 0) {
