@@ -602,8 +602,8 @@ typedef struct qkv_form {
  * request of all rows) stands at pos[i] = cache_len[r] + its depth in the request's tree (parent as for
  * tree_verify_tokens, with `rows` entries, at most 4096 nodes a request), or, with parent = NULL,
  * + its place in the request (a prompt, or one token).  Rows of no request (a graph's padding) get -1.  A
- * request that is out of range (offsets, a negative length, a position past 2^31 - 1, a malformed tree)
- * sets bit 0 of *status, and its rows get -1.  pos serves all layers of the pass.  *status (device
+ * request that is out of range (offsets, a negative length, a length that with its rows passes 2^31 - 1, a
+ * malformed tree) sets bit 0 of *status, and its rows get -1.  pos serves all layers of the pass.  *status (device
  * int32) is zeroed by the caller.  Asynchronous; allocates nothing.  Errors: W12_ERR_INVALID_ARG (null
  * pointer, pos overlapping what the call reads), W12_ERR_SHAPE (n_req outside 1..65535, rows outside 1..2^31-1). */
 W12_API int tree_positions(const int32_t* cache_len, const int32_t* parent, const int32_t* req_offsets, int32_t n_req,
@@ -715,7 +715,7 @@ W12_API int logits_verify(const float* logits, int64_t stride, int64_t M, int64_
  * drawn any more (Q <= 0, or a refused one with q(x) = 0) are passed over and leave p and q.  Where a refusal leaves nothing
  * (p <= q everywhere, or all that p held was refused), no further child is accepted and the bonus comes from p
  * as it was at the node.  bonus[r] = -1 where the node allows no token.  Numbers u outside [0, 1) count as the nearest in it (NaN: 0).
- * Decisions and sums are made to 2^-28 of a probability or better, so that borders between tokens of
+ * Decisions and sums are made to 2^-28 of p's sum or better, so that borders between tokens of
  * large vocabularies fall where the formula has them.  Repeated calls give identical results.
  * parent, draft, req_offsets, path_len, path_nodes and bonus as for tree_verify_tokens, path_nodes -1 behind the path.
  * A request that is out of range (offsets, a malformed tree, more than 1024 nodes, a temperature that is

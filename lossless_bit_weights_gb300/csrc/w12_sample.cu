@@ -14,6 +14,13 @@
 // tokens stand 2^-20 of the mass apart and closer, so a mass has to be good to far more than a float: it
 // is a pair of floats (2^-30 of its value), summed without loss, and the sums stay pairs.  (With plain floats one
 // token in some hundreds would differ from the formula's.)
+//
+// Two kernels: the rows that the walk may pass are summed by all SMs first, then a cluster of blocks per request
+// walks its tree and sums a row again for every refusal.  192 nodes of 24 requests over 151936 tokens with q take
+// 57 us (the rows' 70.5 MB and 24 rows of q are 13 us at the measured copy rate, the rows that this walk really
+// needs 7), a 16-node tree 23, 64 chains of five without q 57 (160 MB), one row of 32000 tokens 10.  What is left is
+// the longest walk: a refusal is a round of the cluster, of which the sum over 19000 tokens a block is 4 to 6 us and two
+// cluster barriers, the joining and the decision about 3.
 #include <cstdint>
 #include <type_traits>
 
@@ -413,8 +420,10 @@ __device__ __forceinline__ void first_at(const float4& f, int64_t i, float most,
 // Largest logit and mass of every 1024 tokens of the rows whose nodes have children (what the walk asks of a
 // node it passes).  Every block of a tile of nodes makes the list of its rows with children, and the tile's
 // warps share (row, 1024 tokens) evenly, 128 bytes a lane on their way at once and the next 4 KB coming into
-// L2.  Bound by the logits read once.  Without q the sums only serve decisions, which plain floats (good to
-// 2^-18 together) nearly always tell, and the walk sums again for the others: 64 chains of five in 59 us, 72 with pairs.
+// L2.  Bound by the logits read once: 156 MB of 64 chains' 256 rows in 32 us (4.9 TB/s, under a profiler); with q by
+// the pairs' arithmetic too, 70.5 MB in 26.  Without q the sums only serve decisions, which plain floats (good
+// to 2^-18 together) nearly always tell, and the walk sums again for the others: 64 chains in 59 us, 72 with pairs.
+// Units of 512 tokens cost 5 us more, of 2048 are alike.
 __global__ void __launch_bounds__(kStatThreads, 2) k_sample_stats(const __grid_constant__ SampleArgs a) {
   pdl_enter();
   __shared__ int32_t offsets[kStatRequests + 1];
@@ -1025,7 +1034,10 @@ __device__ __forceinline__ Command decide(const SampleArgs& a, WalkShared& s, Sl
 
 // A cluster takes a request.  Its first block walks the tree (warp 0, all lanes alike) and has all blocks sum a
 // row's masses, a range of tokens a warp, where a refusal or the bonus token asks for it; only that
-// block decides what comes next, and the others do as they are told.
+// block decides what comes next, and the others do as they are told, so that no barrier depends on two blocks
+// reading the same.  Bound by those rounds' latencies, then by arithmetic (22 operations on pairs of floats a
+// token and refusal).  Blocks of 512 threads, two an SM at 64 registers: 192 nodes took 64 us with one an
+// SM at 128, 61 with 1024 threads; four of 256 threads 55, but a single tree 27 for 23.
 __global__ void __launch_bounds__(kWalkThreads, 2) k_sample_walk(const __grid_constant__ SampleArgs a, int cluster) {
   __shared__ WalkShared s;
   cluster_arrive();  // a block's shared memory is written to only when the block runs
@@ -1159,7 +1171,9 @@ __global__ void __launch_bounds__(kWalkThreads, 2) k_sample_walk(const __grid_co
 
 int64_t sample_units(int64_t V) { return (V + 3 + kUnit - 1) / kUnit; }  // (a row's places start up to three early)
 
-// Blocks of a request's cluster: as many as still leave all requests' clusters room at the same time.
+// Blocks of a request's cluster: as many as still leave all requests' clusters room at the same time, and 2048 tokens
+// or more a block.  (With rooms for a part of them the others start when those end: 24 requests at 16 blocks took 98 us
+// where 4 took 80, both in an earlier form.)
 int cluster_size(int32_t n_req, int64_t V, int& size) {
   constexpr int kSizes = 8;
   static const int sizes[kSizes] = {16, 12, 8, 6, 4, 3, 2, 1};

@@ -192,6 +192,20 @@ def test_strides_and_alignment(w12, V):
         p.check(w12, logits=l, probs=q)
 
 
+@pytest.mark.parametrize("V", [700, 9001])
+def test_rising_and_falling_rows(w12, V):
+    """Rows whose largest logit grows from one stretch of tokens to the next, and ends in a jump."""
+    for seed, order in enumerate((1, -1)):
+        p = Problem(seed, [1, 3, 1, 2], V, temperature=None)
+        rise = np.linspace(-40.0, 30.0, V)[::order].astype(np.float32)
+        p.logits = (rise + 0.1 * p.logits).astype(np.float32)
+        p.logits[0, -1] = 90.0
+        p.logits[4, V // 2:] = -np.inf
+        p.logits[4, :V // 3] = -np.inf
+        p.ub[[0, 2]] = 0.2, 0.999
+        p.check(w12)
+
+
 def test_masked_rows(w12):
     """-inf, NaN, the lowest float and +inf; rows with one token, rows with none."""
     for seed in range(4):
