@@ -603,7 +603,8 @@ typedef struct qkv_form {
  * tree_verify_tokens, with `rows` entries, at most 4096 nodes a request), or, with parent = NULL,
  * + its place in the request (a prompt, or one token).  Rows of no request (a graph's padding) get -1.  A
  * request that is out of range (offsets, a negative length, a length that with its rows passes 2^31 - 1, a
- * malformed tree) sets bit 0 of *status, and its rows get -1.  pos serves all layers of the pass.  *status (device
+ * malformed tree) sets bit 0 of *status, and its rows get -1.  Where offsets fall, so that requests share rows, these
+ * get either's position.  pos serves all layers of the pass.  *status (device
  * int32) is zeroed by the caller.  Asynchronous; allocates nothing.  Errors: W12_ERR_INVALID_ARG (null
  * pointer, pos overlapping what the call reads), W12_ERR_SHAPE (n_req outside 1..65535, rows outside 1..2^31-1). */
 W12_API int tree_positions(const int32_t* cache_len, const int32_t* parent, const int32_t* req_offsets, int32_t n_req,
@@ -719,11 +720,12 @@ W12_API int logits_verify(const float* logits, int64_t stride, int64_t M, int64_
  * large vocabularies fall where the formula has them.  Repeated calls give identical results.
  * parent, draft, req_offsets, path_len, path_nodes and bonus as for tree_verify_tokens, path_nodes -1 behind the path.
  * A request that is out of range (offsets, a malformed tree, more than 1024 nodes, a temperature that is
- * negative or NaN) sets bit 0 of *status and has path_len = bonus = -1, as has one without nodes.  *status (device int32) is
- * zeroed by the caller.  ws: tree_verify_sampled_workspace_size bytes, 16-byte aligned, no initial
+ * negative or NaN) sets bit 0 of *status and has path_len = bonus = -1, as has one without nodes; offsets that fall
+ * anywhere make all requests so.  *status (device int32) is zeroed by the caller.  ws: tree_verify_sampled_workspace_size bytes, 16-byte aligned, no initial
  * state needed (do not pass a GEMM's); calls that may run at the same time need one each.  Asynchronous; allocates
  * nothing.  Errors: W12_ERR_INVALID_ARG (null or misaligned pointers, results overlapping one another or what
- * the call reads), W12_ERR_SHAPE (M, V, n_req, strides), W12_ERR_BUFFER_TOO_SMALL. */
+ * the call reads), W12_ERR_SHAPE (M outside 1..65535 * 1024, V outside 1..2^31 - 16, n_req outside 1..65535,
+ * strides), W12_ERR_BUFFER_TOO_SMALL. */
 W12_API size_t tree_verify_sampled_workspace_size(int64_t M, int64_t V);
 W12_API int tree_verify_sampled(const float* logits, int64_t stride, int64_t M, int64_t V, const float* draft_probs,
                                 int64_t probs_stride, const int32_t* parent, const int32_t* draft,

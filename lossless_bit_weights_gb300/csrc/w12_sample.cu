@@ -52,6 +52,7 @@ struct SampleArgs {
   const float *u, *u_bonus, *temperature;
   int32_t *path_len, *path_nodes, *bonus, *status;
   struct UnitStat* stat;  // [M][units], of rows with children
+  int32_t* falls;         // whether the offsets fall somewhere
   int64_t range;          // places of a warp in the walk, a multiple of 128
   int32_t n_req, units;
 };
@@ -443,6 +444,13 @@ __global__ void __launch_bounds__(kStatThreads, 2) k_sample_stats(const __grid_c
     for (int r = tid; r <= a.n_req; r += kStatThreads) offsets[r] = a.req_offsets[r];
   __syncthreads();
   const int32_t* o = here ? offsets : a.req_offsets;
+  if (blockIdx.x == 0 && blockIdx.y == 0) {  // rows could then belong to two requests
+    bool fall = false;
+#pragma unroll 1
+    for (int r = tid; o && r < a.n_req; r += kStatThreads) fall = fall || o[r + 1] < o[r];
+    fall = __syncthreads_or(fall);
+    if (tid == 0) *a.falls = fall;
+  }
 #pragma unroll 1
   for (int64_t m = m0 + tid; m < m1; m += kStatThreads) {
     if (m != m0 + tid) p = a.parent[m];
@@ -1107,6 +1115,7 @@ __global__ void __launch_bounds__(kWalkThreads, 2) k_sample_walk(const __grid_co
     }
     if (a.M > 1) pdl_enter();
     if (warp < n && a.M > 1) row_sum(warp);
+    if (a.M > 1) ok = ok && !*a.falls;
     ok = __syncthreads_and(ok);
     if (!ok && tid == 0) atomicOr(a.status, kSampleBadRequest);
     ok = ok && n > 0;
@@ -1216,7 +1225,7 @@ extern "C" {
 
 size_t tree_verify_sampled_workspace_size(int64_t M, int64_t V) {
   if (M < 1 || V < 1) return 0;
-  return (size_t)M * (size_t)sample_units(V) * sizeof(UnitStat);
+  return 16 + (size_t)M * (size_t)sample_units(V) * sizeof(UnitStat);
 }
 
 int tree_verify_sampled(const float* logits, int64_t stride, int64_t M, int64_t V, const float* draft_probs,
@@ -1224,7 +1233,7 @@ int tree_verify_sampled(const float* logits, int64_t stride, int64_t M, int64_t 
                         int32_t n_req, const float* u, const float* u_bonus, const float* temperature, int32_t* path_len,
                         int32_t* path_nodes, int32_t* bonus, int32_t* status, void* ws, size_t ws_bytes, void* stream) {
   const char* fn = "tree_verify_sampled";
-  if (M < 1 || M > 0x7FFFFFFF || V < 1 || V > 0x7FFFFFF0 || stride < V || (draft_probs && probs_stride < V) || n_req < 1 ||
+  if (M < 1 || M > 65535 * (int64_t)kStatTile || V < 1 || V > 0x7FFFFFF0 || stride < V || (draft_probs && probs_stride < V) || n_req < 1 ||
       n_req > 65535)
     return fail(W12_ERR_SHAPE, "%s: M=%lld, V=%lld (strides %lld, %lld), n_req=%d (1..65535) out of range", fn, (long long)M,
                 (long long)V, (long long)stride, (long long)probs_stride, n_req);
@@ -1275,7 +1284,8 @@ int tree_verify_sampled(const float* logits, int64_t stride, int64_t M, int64_t 
   a.path_nodes = path_nodes;
   a.bonus = bonus;
   a.status = status;
-  a.stat = static_cast<UnitStat*>(ws);
+  a.falls = static_cast<int32_t*>(ws);
+  a.stat = reinterpret_cast<UnitStat*>(static_cast<char*>(ws) + 16);
   a.units = (int32_t)sample_units(V);
   const int64_t warps = (int64_t)cluster * kWalkWarps;
   a.range = ((V + 3 + warps - 1) / warps + 127) / 128 * 128;

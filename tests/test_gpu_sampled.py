@@ -301,11 +301,14 @@ def test_requests_out_of_range(w12):
             assert (int(length[r]), int(bonus[r])) == (-1, -1) and path[s].tolist() == [-1] * p.counts[r]
         else:
             assert (int(length[r]), int(bonus[r]), path[s].tolist()) == (want[0][r], want[2][r], want[1][s])
-    for off in ([0, 4, 3, 12, 14, 20], [0, 4, 7, 12, 14, 21], [-1, 4, 7, 12, 14, 20]):
+    want = p.want()
+    for off, bad in (([0, 4, 3, 12, 14, 20], range(5)), ([0, 4, 7, 12, 14, 21], [4]), ([-1, 4, 7, 12, 14, 20], [0])):
         a = p.args()
         a["req_offsets"] = i32(off)
-        *_, status = w12.tree_verify_sampled(f32(p.logits), draft_probs=f32(p.probs), **a)
+        length, _, bonus, status = w12.tree_verify_sampled(f32(p.logits), draft_probs=f32(p.probs), **a)
         assert int(status) == 1
+        for r in range(5):
+            assert (int(length[r]), int(bonus[r])) == ((-1, -1) if r in bad else (want[0][r], want[2][r])), (off, r)
     one = Problem(1, [1025], 10, temperature=None)
     length, _, bonus, status = w12.tree_verify_sampled(f32(one.logits), draft_probs=f32(one.probs), **one.args())
     assert (int(length), int(bonus), int(status)) == (-1, -1, 1)

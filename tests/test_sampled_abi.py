@@ -99,7 +99,8 @@ def sampled(w12, **kw):
 
 @pytest.mark.parametrize("kw,status", [
     *[({name: None}, 1) for name in ("logits", "parent", "draft", "u", "ub", "plen", "nodes", "bonus", "status", "ws")],
-    (dict(M=0), 2), (dict(M=1 << 31), 2), (dict(V=0), 2), (dict(V=1 << 31, stride=1 << 31), 2), (dict(stride=99), 2),
+    (dict(M=0), 2), (dict(M=65535 * 1024 + 1), 2), (dict(V=0), 2), (dict(V=(1 << 31) - 15, stride=1 << 31), 2),
+    (dict(stride=99), 2),
     (dict(probs=V(1 << 41), ps=99), 2), (dict(n_req=0), 2), (dict(n_req=70000), 2), (dict(n_req=2), 1),
     (dict(ws=V((1 << 36) + 8)), 1), (dict(wsb=0), 3),
     (dict(plen=Q), 1), (dict(nodes=POS), 1), (dict(bonus=U), 1), (dict(status=SLOT), 1), (dict(ws=V(1 << 40)), 1),
@@ -113,7 +114,7 @@ def test_sampled_workspace(w12):
     size = w12.lib().tree_verify_sampled_workspace_size
     assert sampled(w12, wsb=size(4, 100) - 1) == 3
     assert size(0, 10) == 0 and size(10, 0) == 0
-    assert size(1, 1) == 16 and size(1, 1021) == 16 and size(1, 1022) == 32 and size(192, 151936) == 192 * 149 * 16
+    assert size(1, 1) == 32 and size(1, 1021) == 32 and size(1, 1022) == 48 and size(192, 151936) == 16 + 192 * 149 * 16
 
 
 def test_binding_refusals(w12):
