@@ -868,41 +868,58 @@ def tree_positions(cache_len, parent=None, req_offsets=None, rows: int | None = 
     return pos, status
 
 
+_BITS16 = (torch.bfloat16, torch.int16, torch.uint16)
+
+
 def _rope_rows(x, form: QKVForm, pos):
     """M and whether the projection's rows are bf16."""
-    bf16 = x.dtype != torch.float32
-    if bf16 and x.dtype not in (torch.bfloat16, torch.int16, torch.uint16):
-        raise TypeError(f"expected float32 or bf16 bits (bfloat16/int16/uint16), got {x.dtype}")
-    if not x.is_cuda or x.dim() != 2 or x.shape[1] != form.width or x.stride(1) != 1:
+    dtype = x.dtype
+    bf16 = dtype is not torch.float32
+    if bf16 and dtype not in _BITS16:
+        raise TypeError(f"expected float32 or bf16 bits (bfloat16/int16/uint16), got {dtype}")
+    shape = x.shape
+    if not x.is_cuda or len(shape) != 2 or shape[1] != form.width or x.stride(1) != 1:
         raise ValueError(f"x must be a CUDA tensor [M, {form.width}] with adjacent columns")
-    if _i32(pos).numel() != x.shape[0]:
-        raise ValueError(f"pos must have {x.shape[0]} entries")
-    return x.shape[0], bf16
-
-
-def _rope_out(t, name: str, M: int, heads: int, dim: int):
-    if tuple(_rows16(t, name, 3).shape) != (M, heads, dim):
-        raise ValueError(f"{name} must be [{M}, {heads}, {dim}]")
-    return t
-
-
-def _rope_outs(x, form: QKVForm, pos, q, k, v, M: int, bf16: bool, want_kv: bool, stream):
-    """The rows that are written: those given, checked, or new ones."""
-    _one_device(x, pos, q, k, v)
-    if form.device is not None and form.device != x.get_device():
+    M, dev = shape[0], x.get_device()
+    if _i32(pos).numel() != M:
+        raise ValueError(f"pos must have {M} entries")
+    if pos.get_device() != dev or form.device not in (None, dev):
         raise ValueError("the call's tensors must be on one device")
-    new = x.dtype if bf16 else torch.bfloat16
+    return M, bf16
+
+
+def _rope_out(t, name: str, M: int, heads: int, dim: int, x) -> int:
+    """The row stride of given rows."""
+    if _rows16(t, name, 3).shape != (M, heads, dim):
+        raise ValueError(f"{name} must be [{M}, {heads}, {dim}]")
+    if t.get_device() != x.get_device():
+        raise ValueError("the call's tensors must be on one device")
+    return t.stride(0) if M > 1 else heads * dim
+
+
+def _rope_outs(x, form: QKVForm, q, k, v, M: int, bf16: bool, want_kv: bool, stream):
+    """The rows that are written, those given or new ones, and their strides (0: not written)."""
     d, nq, nk = form.head_dim, form.n_q_heads, form.n_heads
-    q = _empty((M, nq, d), new, x.device, stream) if q is None else _rope_out(q, "q", M, nq, d)
+    new, dev = x.dtype if bf16 else torch.bfloat16, x.device
+    qs, ks = nq * d, nk * d
+    vs = ks
+    if q is None:
+        q = _empty((M, nq, d), new, dev, stream)
+    else:
+        qs = _rope_out(q, "q", M, nq, d, x)
     if k is not None:
-        _rope_out(k, "k", M, nk, d)
+        ks = _rope_out(k, "k", M, nk, d, x)
     elif want_kv:
-        k = _empty((M, nk, d), new, x.device, stream)
+        k = _empty((M, nk, d), new, dev, stream)
+    else:
+        ks = 0
     if v is not None:
-        _rope_out(v, "v", M, nk, d)
+        vs = _rope_out(v, "v", M, nk, d, x)
     elif want_kv:
-        v = _empty((M, nk, d), new, x.device, stream)
-    return q, k, v
+        v = _empty((M, nk, d), new, dev, stream)
+    else:
+        vs = 0
+    return q, k, v, qs, ks, vs
 
 
 def qkv_rope(x, form: QKVForm, pos, q=None, k=None, v=None, stream=None):
@@ -911,10 +928,9 @@ def qkv_rope(x, form: QKVForm, pos, q=None, k=None, v=None, stream=None):
     negative position are left as they were: give q, k and v for a batch with padding.  They may be
     parts of one array, and of x itself in its own places where x is bf16.  Returns (q, k, v)."""
     M, bf16 = _rope_rows(x, form, pos)
-    q, k, v = _rope_outs(x, form, pos, q, k, v, M, bf16, True, stream)
-    _check((_lib or lib()).qkv_rope(
-        x.data_ptr(), bf16, _row_stride(x), M, form.desc(), pos.data_ptr(), q.data_ptr(), q.stride(0), k.data_ptr(),
-        k.stride(0), v.data_ptr(), v.stride(0), _raw_stream(stream, x)))
+    q, k, v, qs, ks, vs = _rope_outs(x, form, q, k, v, M, bf16, True, stream)
+    _check((_lib or lib()).qkv_rope(x.data_ptr(), bf16, x.stride(0) if M > 1 else form.width, M, form._ref, pos.data_ptr(),
+                                    q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, _raw_stream(stream, x)))
     return q, k, v
 
 
@@ -924,16 +940,16 @@ def kv_append(x, form: QKVForm, pos, cache: KVCache, slot, layer: int = 0, q=Non
     int64, -1: none) in the same pass.  q is always written, k and v where they are given or with
     rows=True (tree_attn takes them).  Returns (q, k, v, status), k and v None where not written."""
     M, bf16 = _rope_rows(x, form, pos)
-    if slot.dtype != torch.int64 or not slot.is_cuda or not slot.is_contiguous() or slot.numel() != M:
+    if slot.dtype is not torch.int64 or not slot.is_cuda or not slot.is_contiguous() or slot.numel() != M:
         raise ValueError(f"slot must be a contiguous int64 CUDA tensor of {M} entries")
     if cache.n_heads != form.n_heads or cache.head_dim != form.head_dim:
         raise ValueError(f"the cache must hold {form.n_heads} heads of {form.head_dim}")
-    q, k, v = _rope_outs(x, form, pos, q, k, v, M, bf16, rows, stream)
+    q, k, v, qs, ks, vs = _rope_outs(x, form, q, k, v, M, bf16, rows, stream)
     status = _zero_status(status, x.device, stream)
     _one_device(x, slot, cache.k, cache.v, status)
     _check((_lib or lib()).kv_append(
-        x.data_ptr(), bf16, _row_stride(x), M, form.desc(), pos.data_ptr(), cache.desc(), layer, slot.data_ptr(),
-        q.data_ptr(), q.stride(0), _ptr(k), 0 if k is None else k.stride(0), _ptr(v), 0 if v is None else v.stride(0),
+        x.data_ptr(), bf16, x.stride(0) if M > 1 else form.width, M, form._ref, pos.data_ptr(), cache._ref, layer,
+        slot.data_ptr(), q.data_ptr(), qs, None if k is None else k.data_ptr(), ks, None if v is None else v.data_ptr(), vs,
         status.data_ptr(), _raw_stream(stream, x)))
     return q, k, v, status
 
@@ -1029,12 +1045,10 @@ def _sampled_bytes(M: int, V: int) -> int:
     return int(lib().tree_verify_sampled_workspace_size(M, V))
 
 
-def _float_rows(t, name: str, shape=None):
-    if t.dtype != torch.float32 or not t.is_cuda or t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] != 1):
+def _float_rows(t, name: str):
+    if t.dtype is not torch.float32 or not t.is_cuda or t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] != 1):
         raise ValueError(f"{name} must be a float32 CUDA tensor [M, V] with adjacent columns")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must be {tuple(shape)}")
-    return t
+    return t.shape
 
 
 def tree_verify_sampled(logits, parent, draft, u, u_bonus, draft_probs=None, temperature=None, req_offsets=None,
@@ -1044,10 +1058,13 @@ def tree_verify_sampled(logits, parent, draft, u, u_bonus, draft_probs=None, tem
     logits [M, V] float32; draft_probs [M, V] float32: the drafter's probabilities at each node, from which
     its children were drawn without replacement (None: children given for certain); temperature [n_req]
     float32 (None: 1; below 1e-5: greedy).  Returns (path_len, path_nodes, bonus, status)."""
-    M, V = _float_rows(logits, "logits").shape
+    M, V = _float_rows(logits, "logits")
     n_req = 1 if req_offsets is None else _i32(req_offsets).numel() - 1
+    stride, probs, probs_stride = logits.stride(0) if M > 1 else V, None, 0
     if draft_probs is not None:
-        _float_rows(draft_probs, "draft_probs", logits.shape)
+        if _float_rows(draft_probs, "draft_probs") != (M, V):
+            raise ValueError(f"draft_probs must be [{M}, {V}]")
+        probs, probs_stride = draft_probs.data_ptr(), draft_probs.stride(0) if M > 1 else V
     if _i32(parent).numel() != M or _i32(draft).numel() != M or _f32(u).numel() != M:
         raise ValueError(f"parent, draft and u must have {M} entries")
     if _f32(u_bonus).numel() != n_req or temperature is not None and _f32(temperature).numel() != n_req:
@@ -1060,7 +1077,8 @@ def tree_verify_sampled(logits, parent, draft, u, u_bonus, draft_probs=None, tem
     raw = _raw_stream(stream, logits)
     buf = (ws or Workspace(dev)).scratch(_sampled_bytes(M, V), stream, raw)
     _check((_lib or lib()).tree_verify_sampled(
-        logits.data_ptr(), _row_stride(logits), M, V, _ptr(draft_probs), 0 if draft_probs is None else _row_stride(draft_probs),
-        parent.data_ptr(), draft.data_ptr(), _ptr(req_offsets), n_req, u.data_ptr(), u_bonus.data_ptr(), _ptr(temperature),
-        path_len.data_ptr(), path_nodes.data_ptr(), bonus.data_ptr(), status.data_ptr(), buf.data_ptr(), buf.numel(), raw))
+        logits.data_ptr(), stride, M, V, probs, probs_stride, parent.data_ptr(), draft.data_ptr(),
+        None if req_offsets is None else req_offsets.data_ptr(), n_req, u.data_ptr(), u_bonus.data_ptr(),
+        None if temperature is None else temperature.data_ptr(), path_len.data_ptr(), path_nodes.data_ptr(), bonus.data_ptr(),
+        status.data_ptr(), buf.data_ptr(), buf.numel(), raw))
     return path_len, path_nodes, bonus, status
