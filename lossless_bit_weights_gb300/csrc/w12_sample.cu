@@ -581,6 +581,7 @@ struct alignas(16) Command {
   int32_t known;         // kOpSum: `most` is the row's; else every warp finds its range's
   int32_t residual;      // tau q is taken off
   int32_t refused;       // the node's children are taken out (no q)
+  int32_t last;          // kOpSum: the bonus token comes from these masses, if there are any
   int32_t owner;         // kOpFind: the block that holds the bonus token
   float most, tau_hi, tau_lo;
   Pair target;           // kOpFind: the mass before the bonus token in the owner's ranges, in the units of `most`
@@ -644,11 +645,10 @@ struct WalkShared {
   uint32_t inner[kSampleMaxNodes / 32];
   Command cmd;
   Walk walk;
-  Total total[kMaxCluster];
+  Total total[kMaxCluster];  // the blocks', in the first one, or in all for a last command
   Total range[kWalkWarps];
   Pair group[kWalkWarps];
   int32_t n_refused, last;
-  float u_bonus;
 };
 
 // The refused ones of four tokens from i on have no mass.
@@ -833,14 +833,15 @@ __device__ __forceinline__ Total join(const Total* part, int n, const Slope& c, 
   return t;
 }
 
-// The bonus token, by the block that holds it: first the warp's range, then 128 tokens, then the token.  The
+// The bonus token, by the block that holds it (`target` before it in the block's ranges, in units of `most`): first
+// the warp's range, then 128 tokens, then the token.  The
 // sums of ranges, groups and lanes are rounded differently; where the last tokens do not pass the
 // target by that, it is the last one with a mass.
 __device__ __forceinline__ void find_token(const SampleArgs& a, WalkShared& s, const Slope& c, const Row& row, int64_t first,
-                                           float2 root, int32_t* bonus) {
+                                           float2 root, float most, Pair target, int32_t* bonus) {
   const Command& cmd = s.cmd;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const Ref whole = make_ref(cmd.most, c);
+  const Ref whole = make_ref(most, c);
   Pair mine{0.0f, 0.0f};
   float k = 1.0f;
   if (lane < kWalkWarps && s.range[lane].sum.h > 0.0f) {
@@ -848,10 +849,10 @@ __device__ __forceinline__ void find_token(const SampleArgs& a, WalkShared& s, c
     k = scale_of(part, whole, c);
     mine = {s.range[lane].sum.h * k, s.range[lane].sum.l * k};
   }
-  const Found in = find_lane<16>(mine, cmd.target);
+  const Found in = find_lane<16>(mine, target);
   const int range = max(in.lane, 0);
   const Ref ref = make_ref(s.range[range].most, c);
-  Pair target = cmd.target - in.before;
+  target = target - in.before;
   k = scale_of(whole, ref, c);
   target = {target.h * k, target.l * k};
   const Scale scale = make_scale(ref, c, root);
@@ -900,8 +901,8 @@ __device__ __forceinline__ void find_token(const SampleArgs& a, WalkShared& s, c
 
 // What comes next, by the first block's first warp (all lanes alike): the walk goes on with the sums that it had
 // asked for, until it needs others or ends.
-__device__ __forceinline__ Command decide(const SampleArgs& a, WalkShared& s, Slope c, bool ok, bool greedy, int r, int64_t off,
-                                       int n, int cluster) {
+__device__ __forceinline__ Command decide(const SampleArgs& a, WalkShared& s, Slope c, float u_bonus, bool ok, bool greedy, int r,
+                                          int64_t off, int n, int cluster) {
   const int lane = threadIdx.x & 31;
   const Pair zero{0.0f, 0.0f}, one{1.0f, 0.0f};
   Walk w = s.walk;
@@ -917,13 +918,14 @@ __device__ __forceinline__ Command decide(const SampleArgs& a, WalkShared& s, Sl
     w.Q = one;
     w.M = w.inner ? s.sum[node] : zero;
   };
-  auto ask = [&](bool residual, bool off_refused) {
+  auto ask = [&](bool residual, bool off_refused, bool last) {
     cmd.op = kOpSum;
     cmd.node = w.cur;
     cmd.known = w.inner;
     cmd.most = w.inner ? s.most[w.cur] : 0.0f;
     cmd.residual = residual;
     cmd.refused = off_refused;
+    cmd.last = last;
     cmd.tau_hi = w.tau.h;
     cmd.tau_lo = w.tau.l;
   };
@@ -978,7 +980,7 @@ __device__ __forceinline__ Command decide(const SampleArgs& a, WalkShared& s, Sl
         take = (!a.probs || w.Q > zero) && limit > mine_u;
         if (w.rough && fabsf((mine_u - limit).h) <= 6.2e-5f * u * (w.M + w.out).h) {  // it does not tell
           w.last = j - 1;
-          ask(false, false);
+          ask(false, false, false);
           w.stage = kPrecise;
           asked = true;
           continue;
@@ -993,7 +995,12 @@ __device__ __forceinline__ Command decide(const SampleArgs& a, WalkShared& s, Sl
           } else {
             w.tau = w.tau + (w.Q.h == 1.0f && w.Q.l == 0.0f ? w.M : w.M / w.Q);
             w.Q = w.Q - Pair{q, 0.0f};
-            ask(true, false);
+            bool more = false;  // children behind this one
+#pragma unroll 1
+            for (int i0 = j + 1; i0 < n && !more; i0 += 32)
+              more = __any_sync(0xFFFFFFFFu, i0 + lane < n && s.parent[i0 + lane] == w.cur);
+            if (!more && lane == 0) a.path_len[r] = w.depth;
+            ask(true, false, !more);
             w.stage = kRefused;
             asked = true;
           }
@@ -1011,14 +1018,14 @@ __device__ __forceinline__ Command decide(const SampleArgs& a, WalkShared& s, Sl
         if (greedy && w.inner) {
           if (lane == 0) a.bonus[r] = s.most[w.cur] > -INFINITY ? s.at[w.cur] : -1;
         } else if (!w.summed) {
-          ask(false, w.refused);
+          ask(false, w.refused, !greedy);
           w.stage = kSummed;
         }
       } else if (greedy) {
         if (lane == 0) a.bonus[r] = all.most > -INFINITY ? all.at : -1;
       } else if (!(all.sum.h > 0.0f)) {
         if (cmd.refused) {  // all that had a mass was refused: p as it was
-          ask(false, false);
+          ask(false, false, true);
         } else if (lane == 0) {
           a.bonus[r] = -1;
         }
@@ -1026,7 +1033,7 @@ __device__ __forceinline__ Command decide(const SampleArgs& a, WalkShared& s, Sl
         w.summed = true;
       }
       if (w.summed && !greedy) {
-        const Pair target = all.sum * s.u_bonus;
+        const Pair target = all.sum * u_bonus;
         const Found f = find_lane<16>(mine, target);
         cmd.op = kOpFind;
         cmd.most = all.most;
@@ -1059,7 +1066,7 @@ __global__ void __launch_bounds__(kWalkThreads, 2) k_sample_walk(const __grid_co
   int n;
   bool ok = sample_request(a, r, off, n);
   if (!ok) n = 0;
-  const float T = a.temperature ? a.temperature[r] : 1.0f;
+  const float T = a.temperature ? a.temperature[r] : 1.0f, u_bonus = fminf(fmaxf(a.u_bonus[r], 0.0f), 0.99999994f);
   const bool greedy = T < kGreedy;
   const Slope c = make_slope(greedy ? 1.0f : T);
   const float2 root = kRoots[lane];
@@ -1067,7 +1074,6 @@ __global__ void __launch_bounds__(kWalkThreads, 2) k_sample_walk(const __grid_co
   // ---- the nodes, and the sums of the rows with children
   if (rank == 0) {
     if (tid < kSampleMaxNodes / 32) s.inner[tid] = 0;
-    if (tid == 0) s.u_bonus = fminf(fmaxf(a.u_bonus[r], 0.0f), 0.99999994f);
     __syncthreads();
     ok = ok && T >= 0.0f;
     // A row's largest logit and its sum.  (The first rows' are read with the tree; of those without children
@@ -1139,9 +1145,12 @@ __global__ void __launch_bounds__(kWalkThreads, 2) k_sample_walk(const __grid_co
   if (tid == 0) s.walk.stage = kStart;
   __syncwarp();
   cluster_wait();
+  int holder = -1;  // of the bonus token, and what find_token is told
+  float most = 0.0f;
+  Pair target{0.0f, 0.0f};
   while (true) {
     if (rank == 0 && warp == 0) {
-      const Command cmd = decide(a, s, c, ok, greedy, r, off, n, cluster);
+      const Command cmd = decide(a, s, c, u_bonus, ok, greedy, r, off, n, cluster);
       __syncwarp();
       if (lane < cluster) send(cmd, &s.cmd, (uint32_t)lane);
     }
@@ -1149,7 +1158,9 @@ __global__ void __launch_bounds__(kWalkThreads, 2) k_sample_walk(const __grid_co
     if (s.cmd.op == kOpDone) break;
     const Row row = row_of(a, off + s.cmd.node);
     if (s.cmd.op == kOpFind) {
-      if (s.cmd.owner == (int32_t)rank) find_token(a, s, c, row, first, root, a.bonus + r);
+      holder = s.cmd.owner;
+      most = s.cmd.most;
+      target = s.cmd.target;
       break;
     }
     if (s.cmd.refused) {
@@ -1172,10 +1183,23 @@ __global__ void __launch_bounds__(kWalkThreads, 2) k_sample_walk(const __grid_co
     if (warp == 0) {
       Pair part;
       const Total sum = join(s.range, kWalkWarps, c, greedy, s.cmd.known, part);
-      if (lane == 0) send(sum, &s.total[rank], 0);
+      if (s.cmd.last ? lane < cluster : lane == 0) send(sum, &s.total[rank], (uint32_t)lane);
     }
     cluster_sync();
+    if (s.cmd.last) {  // every block sees for itself who holds the bonus token
+      Pair mine;
+      const Total all = join(s.total, cluster, c, false, s.cmd.known, mine);
+      if (all.sum.h > 0.0f) {
+        target = all.sum * u_bonus;
+        const Found f = find_lane<16>(mine, target);
+        holder = f.lane;
+        most = all.most;
+        target = target - f.before;
+        break;
+      }
+    }
   }
+  if (holder == (int)rank) find_token(a, s, c, row_of(a, off + s.cmd.node), first, root, most, target, a.bonus + r);
 }
 
 int64_t sample_units(int64_t V) { return (V + 3 + kUnit - 1) / kUnit; }  // (a row's places start up to three early)
