@@ -31,7 +31,7 @@ namespace w12 {
 namespace {
 
 constexpr int kSampleMaxNodes = 1024;  // nodes of one request
-constexpr int kUnit = 1024;            // tokens of a row that a warp sums at once
+constexpr int kUnit = 1024;            // places of a row that make a unit of the rows' kernel
 constexpr int kStatThreads = 256;
 constexpr int kStatTile = 1024;       // nodes whose rows a column of blocks takes
 constexpr int kStatRequests = 1024;   // offsets that fit in shared memory
@@ -339,22 +339,16 @@ __device__ __forceinline__ Four masses4(const float4& f, const Scale& c) {
   return m;
 }
 
-// A mass to 2^-20 or so, by plain floats: 2^((l - most) c + (most c - whole)).
-struct Rough {
-  float most, slope, start, least;
-};
-
-__device__ __forceinline__ Rough make_rough(const Ref& r, const Slope& c) {
-  Rough o{r.most, c.hi, 0.0f, fmaxf(-125.0f * c.over, -kMost)};
-  if (r.shift == 0.0f) o.start = fmaf(r.most, c.lo, fmaf(r.most, c.hi, -r.whole));
-  return o;
+// 2^x and 2^((l - most) c) by plain floats, to 2^-20 or so.
+__device__ __forceinline__ float rough_exp2(float x) {
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x));
+  return e;
 }
 
-__device__ __forceinline__ float rough(float l, const Rough& r) {
-  const float d = l - r.most;
-  float e;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fmaf(d, r.slope, r.start)));
-  return d >= r.least ? e : 0.0f;
+__device__ __forceinline__ float rough(float l, float most, float slope, float least) {
+  const float d = l == most ? 0.0f : l - most;  // (equal infinities)
+  return d >= least ? rough_exp2(d * slope) : 0.0f;
 }
 
 // A running sum of pairs, two at a time.  It starts at 4, above every mass, so that an addition's rounding
@@ -416,16 +410,135 @@ __device__ __forceinline__ void first_at(const float4& f, int64_t i, float most,
   if (k < 4 && (int32_t)i + k < at) at = (int32_t)i + k;
 }
 
+// ---------------------------------------------------------------- ranges of a row
+
+struct alignas(16) Total {
+  float most;
+  int32_t at;
+  Pair sum;
+};
+
+// One warp's range of a row of a greedy request: its largest logit and the first token at it.
+__device__ __forceinline__ Total first_of_range(const Row& row, int64_t v0, int64_t v1) {
+  const int lane = threadIdx.x & 31;
+  Total t{-INFINITY, 0x7FFFFFFF, {0.0f, 0.0f}};
+  constexpr int W = 8;  // loads of a lane on their way
+#pragma unroll 1
+  for (int64_t i0 = v0; i0 < v1; i0 += 128 * W) {
+    float4 f[W];
+#pragma unroll
+    for (int k = 0; k < W; ++k) f[k] = four(row.x, i0 + k * 128 + 4 * lane, row.lo, v1, true, -INFINITY);
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+      const float most = fmaxf(fmaxf(f[k].x, f[k].y), fmaxf(f[k].z, f[k].w));
+      if (most > t.most) {
+        t.most = most;
+        t.at = 0x7FFFFFFF;
+        first_at(f[k], i0 + k * 128 + 4 * lane, most, t.at);
+      }
+    }
+  }
+  const float most = warp_max(t.most);
+  t.at = __reduce_min_sync(0xFFFFFFFFu, t.most == most ? t.at : 0x7FFFFFFF) - row.lo;
+  t.most = most;
+  return t;
+}
+
+// One warp's range of a row whose largest logit is not known (a node without children): the sum of its masses in one sweep, in units of the
+// largest logit of the first tokens, and of larger ones where they come (the sum so far changes by a power
+// of two then).  A mass may pass a unit by twice before that, which stays below the 4 that Sum starts at.
+template <int U>  // loads of a lane on their way
+__device__ __forceinline__ Total sum_unknown(const Row& row, const Slope& c, int64_t v0, int64_t v1, float2 root) {
+  const int lane = threadIdx.x & 31;
+  Total t{-INFINITY, 0x7FFFFFFF, {0.0f, 0.0f}};
+  Scale scale{};
+  Sum sum;
+  float limit = -INFINITY;
+#pragma unroll 1
+  for (int64_t i0 = v0; i0 < v1; i0 += 128 * U) {
+    float4 f[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) f[k] = four(row.x, i0 + k * 128 + 4 * lane, row.lo, v1, true, -INFINITY);
+    float most = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < U; ++k) most = fmaxf(most, fmaxf(fmaxf(f[k].x, f[k].y), fmaxf(f[k].z, f[k].w)));
+    if (__any_sync(0xFFFFFFFFu, most > limit)) {
+      most = warp_max(most);
+      const Ref to = make_ref(most, c);
+      if (t.most > -INFINITY) {
+        const float k = scale_of(make_ref(t.most, c), to, c);
+        t.sum = t.sum + sum.value();
+        t.sum = {t.sum.h * k, t.sum.l * k};
+        sum = Sum();
+      }
+      t.most = most;
+      limit = most + c.over;
+      scale = make_scale(to, c, root);
+    }
+    if (t.most == -INFINITY) continue;
+    if (scale.plain && v1 - v0 <= 1 << 24) {
+#pragma unroll
+      for (int k = 0; k < U; ++k) sum.add(masses4<false, true>(f[k], scale));
+    } else {
+#pragma unroll 1
+      for (int k = 0; k < U; ++k) {
+        const int64_t i = i0 + k * 128 + 4 * lane;
+        sum.add(masses4<true>(four(row.x, i, row.lo, v1, true, -INFINITY), scale));
+      }
+    }
+  }
+  t.sum = warp_sum(t.sum + sum.value());
+  if (!(t.sum.h > kLeast)) t.sum = {0.0f, 0.0f};  // (see sum_range)
+  return t;
+}
+
+// The same by plain floats, to 2^-18: a lane's sum in the mass of its own largest logit, which grows with it.
+template <int U>
+__device__ __forceinline__ Total rough_unknown(const Row& row, const Slope& c, int64_t v0, int64_t v1) {
+  const int lane = threadIdx.x & 31;
+  Total t{-INFINITY, 0x7FFFFFFF, {0.0f, 0.0f}};
+  const float least = fmaxf(-125.0f * c.over, -kMost);
+  float sum = 0.0f;
+#pragma unroll 1
+  for (int64_t i0 = v0; i0 < v1; i0 += 128 * U) {
+    float4 f[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) f[k] = four(row.x, i0 + k * 128 + 4 * lane, row.lo, v1, true, -INFINITY);
+    float most = t.most;
+#pragma unroll
+    for (int k = 0; k < U; ++k) most = fmaxf(most, fmaxf(fmaxf(f[k].x, f[k].y), fmaxf(f[k].z, f[k].w)));
+    if (most > t.most) {
+      sum *= rough(t.most, most, c.hi, least);
+      t.most = most;
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k)
+      sum += (rough(f[k].x, most, c.hi, least) + rough(f[k].y, most, c.hi, least)) +
+             (rough(f[k].z, most, c.hi, least) + rough(f[k].w, most, c.hi, least));
+  }
+  const float most = warp_max(t.most);
+  sum *= rough(t.most, most, c.hi, least);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+  t.most = most;
+  if (most == -INFINITY) return t;  // (its -inf count as equal to the largest)
+  const Ref r = make_ref(most, c);
+  if (most < INFINITY && r.shift == 0.0f) sum *= rough_exp2(fmaf(most, c.lo, fmaf(most, c.hi, -r.whole)));
+  t.sum = {sum, 0.0f};
+  return t;
+}
+
 // ---------------------------------------------------------------- rows with children
 
-// Largest logit and mass of every 1024 tokens of the rows whose nodes have children (what the walk asks of a
-// node it passes).  Every block of a tile of nodes makes the list of its rows with children, and the tile's
-// warps share (row, 1024 tokens) evenly, 128 bytes a lane on their way at once and the next 4 KB coming into
-// L2.  Bound by the logits read once: 156 MB of 64 chains' 256 rows in 32 us (4.9 TB/s, under a profiler); with q by
-// the pairs' arithmetic too, 70.5 MB in 26.  Without q the sums only serve decisions, which plain floats (good
-// to 2^-18 together) nearly always tell, and the walk sums again for the others: 64 chains in 59 us, 72 with pairs.
-// Units of 512 tokens cost 5 us more, of 2048 are alike.
-__global__ void __launch_bounds__(kStatThreads, 2) k_sample_stats(const __grid_constant__ SampleArgs a) {
+// Largest logit and mass of the rows whose nodes have children (what the walk asks of a node it passes), in units of
+// 1024 places.  Every block of a tile of nodes makes the list of its rows with children, and the tile's warps take
+// equal shares of all units, 128 bytes a lane on their way.  Without q the sums only serve decisions, which plain floats
+// (good to 2^-18 together) nearly always tell, and the walk sums again for the others.
+// Bound by the logits read once, and with q by the pairs' arithmetic: 256 rows of 151936 (156 MB) in 30.3 us without q
+// (5.1 TB/s, 0.76 of the measured copy rate; 2.8 of it to make the list), 116 rows (70.5 MB) in 20.5 with q, 16.6 if they
+// were rough.  Pairs for the chains too made their call 72 us for 59.  Bringing each warp's share into L2 ahead in bulk
+// took 9 us more; two or four blocks an SM about 1; one row after another by a request's blocks twice the time.
+__global__ void __launch_bounds__(kStatThreads, 3) k_sample_stats(const __grid_constant__ SampleArgs a) {
   pdl_enter();
   __shared__ int32_t offsets[kStatRequests + 1];
   __shared__ uint32_t inner[kStatTile / 32];  // rows with children
@@ -434,7 +547,6 @@ __global__ void __launch_bounds__(kStatThreads, 2) k_sample_stats(const __grid_c
   __shared__ int rows;
   const int tid = threadIdx.x, lane = tid & 31;
   const int64_t m0 = (int64_t)blockIdx.y * kStatTile, m1 = min(a.M, m0 + kStatTile + kSampleMaxNodes);
-  const uint32_t first = blockIdx.x * (kStatThreads / 32) + (tid >> 5), step = gridDim.x * (kStatThreads / 32);
   const bool here = a.req_offsets && a.n_req <= kStatRequests;
   const float2 root = kRoots[lane];
   int32_t p = m0 + tid < m1 ? a.parent[m0 + tid] : -1;
@@ -489,72 +601,28 @@ __global__ void __launch_bounds__(kStatThreads, 2) k_sample_stats(const __grid_c
     }
   }
   __syncthreads();
-  // (at most 2^10 rows of 2^21 units)
-  const uint32_t units = a.units, items = rows * units, more = step / units, ahead = step - more * units;
-  uint32_t nth = first / units, unit = first - nth * units;
+  // An equal share of all units for every warp, one stretch after another; a stretch in one row has one sum, in the
+  // place of its first unit.  (At most 2^10 rows of 2^21 units.)
+  const uint32_t units = a.units;
+  const int64_t items = (int64_t)rows * units, warps = (int64_t)gridDim.x * (kStatThreads / 32);
+  const int64_t mine = (int64_t)blockIdx.x * (kStatThreads / 32) + (tid >> 5), stop = items * (mine + 1) / warps;
 #pragma unroll 1
-  for (uint32_t item = first; item < items; item += step) {
-    const int at = list[nth];
+  for (int64_t item = items * mine / warps; item < stop;) {
+    const uint32_t nth = (uint32_t)item / units, unit = (uint32_t)item - nth * units;
+    const uint32_t run = (uint32_t)min(stop - item, (int64_t)(units - unit));
     const float4 slope = slopes[nth];
-    const Row row = row_of(a, m0 + at);
-    const int64_t v0 = (int64_t)unit * kUnit, v1 = min(row.hi, v0 + kUnit);
-    UnitStat* out = a.stat + (m0 + at) * a.units + unit;
-    float4 f[kUnit / 128];
-#pragma unroll
-    for (int k = 0; k < kUnit / 128; ++k) f[k] = four(row.x, v0 + k * 128 + 4 * lane, row.lo, v1, true, -INFINITY);
-    nth += more;
-    unit += ahead;
-    if (unit >= units) {
-      unit -= units;
-      ++nth;
-    }
-    if (lane == 0 && item + step < items) {
-      const Row next = row_of(a, m0 + list[nth]);
-      const int64_t n0 = (int64_t)unit * kUnit;
-      const uint32_t bytes = (uint32_t)(max(min(next.hi - n0, (int64_t)kUnit), (int64_t)0) & ~(int64_t)3) * 4;
-      if (bytes) prefetch_l2(next.x + n0, bytes);
-    }
-    float most = -INFINITY;
-#pragma unroll
-    for (int k = 0; k < kUnit / 128; ++k) most = fmaxf(most, fmaxf(fmaxf(f[k].x, f[k].y), fmaxf(f[k].z, f[k].w)));
-    most = warp_max(most);
-    UnitStat st{most, -1, {0.0f, 0.0f}};
-    if (most > -INFINITY) {
-      if (slope.w != 0.0f) {
-        int32_t token = 0x7FFFFFFF;
-#pragma unroll
-        for (int k = 0; k < kUnit / 128; ++k) first_at(f[k], v0 + k * 128 + 4 * lane, most, token);
-        st.at = __reduce_min_sync(0xFFFFFFFFu, token) - row.lo;
-      } else {
-        const Slope c{slope.x, slope.y, slope.z};
-        const Ref ref = make_ref(most, c);
-        if (!a.probs && most < INFINITY) {
-          const Rough r = make_rough(ref, c);
-#pragma unroll
-          for (int k = 0; k < kUnit / 128; ++k)
-            st.sum[0] += (rough(f[k].x, r) + rough(f[k].y, r)) + (rough(f[k].z, r) + rough(f[k].w, r));
-#pragma unroll
-          for (int n = 16; n; n >>= 1) st.sum[0] += __shfl_xor_sync(0xFFFFFFFFu, st.sum[0], n);
-        } else {
-          const Scale scale = make_scale(ref, c, root);
-          Sum sum;
-          if (scale.plain) {  // (what has no mass adds 2^-115 of the largest at most)
-#pragma unroll
-            for (int k = 0; k < kUnit / 128; ++k) sum.add(masses4<false, true>(f[k], scale));
-          } else {
+    const int64_t m = m0 + list[nth];
+    const Row row = row_of(a, m);
+    const int64_t v0 = (int64_t)unit * kUnit, v1 = min(row.hi, v0 + (int64_t)run * kUnit);
+    const Slope c{slope.x, slope.y, slope.z};
+    const Total t = slope.w != 0.0f ? first_of_range(row, v0, v1)
+                    : a.probs       ? sum_unknown<8>(row, c, v0, v1, root)
+                                    : rough_unknown<8>(row, c, v0, v1);
+    UnitStat* out = a.stat + m * units + unit;
 #pragma unroll 1
-            for (int k = 0; k < kUnit / 128; ++k) {
-              const Four m = masses4<true>(four(row.x, v0 + k * 128 + 4 * lane, row.lo, v1, true, -INFINITY), scale);
-              sum.add(m);
-            }
-          }
-          const Pair all = warp_sum(sum.value());
-          st.sum[0] = all.h;
-          st.sum[1] = all.l;
-        }
-      }
-    }
-    if (lane == 0) *out = st;
+    for (uint32_t k = lane; k < run; k += 32)
+      out[k] = k ? UnitStat{-INFINITY, -1, {0.0f, 0.0f}} : UnitStat{t.most, t.at, {t.sum.h, t.sum.l}};
+    item += run;
   }
 }
 
@@ -585,12 +653,6 @@ struct alignas(16) Command {
   int32_t owner;         // kOpFind: the block that holds the bonus token
   float most, tau_hi, tau_lo;
   Pair target;           // kOpFind: the mass before the bonus token in the owner's ranges, in the units of `most`
-};
-
-struct alignas(16) Total {
-  float most;
-  int32_t at;
-  Pair sum;
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -674,80 +736,6 @@ __device__ __forceinline__ void left4(Four& m, const float4& q, float tau_hi, fl
 __device__ __forceinline__ float chance(float q) { return fmaxf(q, 0.0f); }  // (NaN: 0)
 
 __device__ __forceinline__ float4 chance4(float4 q) { return make_float4(chance(q.x), chance(q.y), chance(q.z), chance(q.w)); }
-
-// One warp's range of a row of a greedy request: its largest logit and the first token at it.
-__device__ __forceinline__ Total first_of_range(const Row& row, int64_t v0, int64_t v1) {
-  const int lane = threadIdx.x & 31;
-  Total t{-INFINITY, 0x7FFFFFFF, {0.0f, 0.0f}};
-  constexpr int W = 8;  // loads of a lane on their way
-#pragma unroll 1
-  for (int64_t i0 = v0; i0 < v1; i0 += 128 * W) {
-    float4 f[W];
-#pragma unroll
-    for (int k = 0; k < W; ++k) f[k] = four(row.x, i0 + k * 128 + 4 * lane, row.lo, v1, true, -INFINITY);
-#pragma unroll
-    for (int k = 0; k < W; ++k) {
-      const float most = fmaxf(fmaxf(f[k].x, f[k].y), fmaxf(f[k].z, f[k].w));
-      if (most > t.most) {
-        t.most = most;
-        t.at = 0x7FFFFFFF;
-        first_at(f[k], i0 + k * 128 + 4 * lane, most, t.at);
-      }
-    }
-  }
-  const float most = warp_max(t.most);
-  t.at = __reduce_min_sync(0xFFFFFFFFu, t.most == most ? t.at : 0x7FFFFFFF) - row.lo;
-  t.most = most;
-  return t;
-}
-
-// One warp's range of a row whose largest logit is not known (a node without children): the sum of its masses in one sweep, in units of the
-// largest logit of the first tokens, and of larger ones where they come (the sum so far changes by a power
-// of two then).  A mass may pass a unit by twice before that, which stays below the 4 that Sum starts at.
-__device__ __forceinline__ Total sum_unknown(const Row& row, const Slope& c, int64_t v0, int64_t v1, float2 root) {
-  const int lane = threadIdx.x & 31;
-  constexpr int U = 4;
-  Total t{-INFINITY, 0x7FFFFFFF, {0.0f, 0.0f}};
-  Scale scale{};
-  Sum sum;
-  float limit = -INFINITY;
-#pragma unroll 1
-  for (int64_t i0 = v0; i0 < v1; i0 += 128 * U) {
-    float4 f[U];
-#pragma unroll
-    for (int k = 0; k < U; ++k) f[k] = four(row.x, i0 + k * 128 + 4 * lane, row.lo, v1, true, -INFINITY);
-    float most = -INFINITY;
-#pragma unroll
-    for (int k = 0; k < U; ++k) most = fmaxf(most, fmaxf(fmaxf(f[k].x, f[k].y), fmaxf(f[k].z, f[k].w)));
-    if (__any_sync(0xFFFFFFFFu, most > limit)) {
-      most = warp_max(most);
-      const Ref to = make_ref(most, c);
-      if (t.most > -INFINITY) {
-        const float k = scale_of(make_ref(t.most, c), to, c);
-        t.sum = t.sum + sum.value();
-        t.sum = {t.sum.h * k, t.sum.l * k};
-        sum = Sum();
-      }
-      t.most = most;
-      limit = most + c.over;
-      scale = make_scale(to, c, root);
-    }
-    if (t.most == -INFINITY) continue;
-    if (scale.plain && v1 - v0 <= 1 << 24) {
-#pragma unroll
-      for (int k = 0; k < U; ++k) sum.add(masses4<false, true>(f[k], scale));
-    } else {
-#pragma unroll 1
-      for (int k = 0; k < U; ++k) {
-        const int64_t i = i0 + k * 128 + 4 * lane;
-        sum.add(masses4<true>(four(row.x, i, row.lo, v1, true, -INFINITY), scale));
-      }
-    }
-  }
-  t.sum = warp_sum(t.sum + sum.value());
-  if (!(t.sum.h > kLeast)) t.sum = {0.0f, 0.0f};  // (see sum_range)
-  return t;
-}
 
 // One warp's range of a row whose largest logit is known: the sum of its masses, or of what refusals leave of them.
 __device__ __forceinline__ Total sum_range(const Row& row, const Command& cmd, const Slope& c, int64_t v0, int64_t v1,
@@ -1080,20 +1068,37 @@ __global__ void __launch_bounds__(kWalkThreads, 2) k_sample_walk(const __grid_co
     // nothing was written, and nothing is used.)
     auto row_sum = [&](int i) {
       const UnitStat* st = a.stat + (off + i) * a.units;
+      constexpr int W = 6;  // loads of a lane on their way
       float most = -INFINITY;
-#pragma unroll 1
-      for (int k = lane; k < a.units; k += 32) most = fmaxf(most, st[k].most);
-      most = warp_max(most);
-      const Ref ref = make_ref(most, c);
       int32_t at = 0x7FFFFFFF;
       Pair sum{0.0f, 0.0f};
 #pragma unroll 1
-      for (int k = lane; k < a.units; k += 32) {
-        const UnitStat u = st[k];
-        if (u.most == most) at = min(at, u.at);
-        if (u.sum[0] > 0.0f) {
-          const float scale = scale_of(make_ref(u.most, c), ref, c);
-          sum = sum + Pair{u.sum[0] * scale, u.sum[1] * scale};
+      for (int k0 = lane; k0 - lane < a.units; k0 += 32 * W) {
+        UnitStat u[W];
+        float top = most;
+#pragma unroll
+        for (int k = 0; k < W; ++k) {
+          u[k] = k0 + 32 * k < a.units ? st[k0 + 32 * k] : UnitStat{-INFINITY, 0x7FFFFFFF, {0.0f, 0.0f}};
+          top = fmaxf(top, u[k].most);
+        }
+        top = warp_max(top);
+        const Ref ref = make_ref(top, c);
+        if (top > most) {
+          const float scale = sum.h > 0.0f ? scale_of(make_ref(most, c), ref, c) : 0.0f;
+          sum = {sum.h * scale, sum.l * scale};
+          most = top;
+          at = 0x7FFFFFFF;
+        }
+#pragma unroll 1
+        for (int k = 0; k < W; ++k) {
+          const UnitStat v = u[0];
+#pragma unroll
+          for (int e = 1; e < W; ++e) u[e - 1] = u[e];  // (a loop's body once, with its registers named)
+          if (v.most == most) at = min(at, v.at);
+          if (v.sum[0] > 0.0f) {
+            const float scale = scale_of(make_ref(v.most, c), ref, c);
+            sum = sum + Pair{v.sum[0] * scale, v.sum[1] * scale};
+          }
         }
       }
       at = __reduce_min_sync(0xFFFFFFFFu, at);
@@ -1177,7 +1182,7 @@ __global__ void __launch_bounds__(kWalkThreads, 2) k_sample_walk(const __grid_co
     const int n_refused = s.cmd.refused ? s.n_refused : 0;
     const Total t = s.cmd.known ? sum_range(row, s.cmd, c, v0, v1, s.refused, n_refused, root)
                     : greedy    ? first_of_range(row, v0, v1)
-                                : sum_unknown(row, c, v0, v1, root);
+                                : sum_unknown<4>(row, c, v0, v1, root);
     if (lane == 0) s.range[warp] = t;
     __syncthreads();
     if (warp == 0) {
@@ -1315,10 +1320,10 @@ int tree_verify_sampled(const float* logits, int64_t stride, int64_t M, int64_t 
   a.range = ((V + 3 + warps - 1) / warps + 127) / 128 * 128;
   a.n_req = n_req;
   if (M > 1) {
-    // two blocks an SM, if there is that much (half of the nodes have children, or nearly all)
+    // three blocks an SM, if there is that much (half of the nodes have children, or nearly all)
     const int64_t tiles = (M + kStatTile - 1) / kStatTile, most = (M < kStatTile ? M : kStatTile) * (int64_t)a.units;
     int64_t blocks = (most + kStatThreads / 32 - 1) / (kStatThreads / 32);
-    blocks = blocks < 304 ? blocks : 304;
+    blocks = blocks < 456 ? blocks : 456;
     W12_CUDA_TRY(launch_dependent(k_sample_stats, dim3((unsigned)blocks, (unsigned)tiles), kStatThreads, 0, (cudaStream_t)stream, a));
     W12_LAUNCH_CHECK("tree_verify_sampled: rows kernel");
   }
