@@ -17,8 +17,8 @@
 //
 // Two kernels: the rows that the walk may pass are summed by all SMs first, then a cluster of blocks per request
 // walks its tree and sums a row again for every refusal.  192 nodes of 24 requests over 151936 tokens with q take
-// 57 us (the rows' 70.5 MB and 24 rows of q are 13 us at the measured copy rate, the rows that this walk really
-// needs 7), a 16-node tree 23, 64 chains of five without q 57 (160 MB), one row of 32000 tokens 10.  What is left is
+// 55 us (the rows' 70.5 MB and 24 rows of q are 13 us at the measured copy rate, the rows that these walks really
+// need 7), a 16-node tree 23, 64 chains of five without q 58 (193 MB), one row of 32000 tokens 9.5.  What is left is
 // the longest walk: a refusal is a round of the cluster, of which the sum over 19000 tokens a block is 4 to 6 us and two
 // cluster barriers, the joining and the decision about 3.
 #include <cstdint>
@@ -444,9 +444,9 @@ __device__ __forceinline__ Total first_of_range(const Row& row, int64_t v0, int6
   return t;
 }
 
-// One warp's range of a row whose largest logit is not known (a node without children): the sum of its masses in one sweep, in units of the
-// largest logit of the first tokens, and of larger ones where they come (the sum so far changes by a power
-// of two then).  A mass may pass a unit by twice before that, which stays below the 4 that Sum starts at.
+// One warp's range of a row whose largest logit is not known (a node without children): the sum of its masses in
+// one sweep, in units of the largest logit of the first tokens, and of larger ones where they come (the sum so far
+// changes by a power of two then).  A mass may pass a unit by twice before that, which stays below the 4 that Sum starts at.
 template <int U>  // loads of a lane on their way
 __device__ __forceinline__ Total sum_unknown(const Row& row, const Slope& c, int64_t v0, int64_t v1, float2 root) {
   const int lane = threadIdx.x & 31;
@@ -1039,8 +1039,8 @@ __device__ __forceinline__ Command decide(const SampleArgs& a, WalkShared& s, Sl
 // row's masses, a range of tokens a warp, where a refusal or the bonus token asks for it; only that
 // block decides what comes next, and the others do as they are told, so that no barrier depends on two blocks
 // reading the same.  Bound by those rounds' latencies, then by arithmetic (22 operations on pairs of floats a
-// token and refusal).  Blocks of 512 threads, two an SM at 64 registers: 192 nodes took 64 us with one an
-// SM at 128, 61 with 1024 threads; four of 256 threads 55, but a single tree 27 for 23.
+// token and refusal).  Blocks of 512 threads, two an SM at 64 registers: an earlier form, 57 us for 192 nodes, took 64
+// with one an SM at 128, 61 with 1024 threads; four of 256 threads 55, but a single tree 27 for 23.
 __global__ void __launch_bounds__(kWalkThreads, 2) k_sample_walk(const __grid_constant__ SampleArgs a, int cluster) {
   __shared__ WalkShared s;
   cluster_arrive();  // a block's shared memory is written to only when the block runs
@@ -1185,15 +1185,17 @@ __global__ void __launch_bounds__(kWalkThreads, 2) k_sample_walk(const __grid_co
                                 : sum_unknown<4>(row, c, v0, v1, root);
     if (lane == 0) s.range[warp] = t;
     __syncthreads();
+    // (Behind the round's second barrier the first block may already have sent the next command.)
+    const bool last = s.cmd.last, known = s.cmd.known;
     if (warp == 0) {
       Pair part;
-      const Total sum = join(s.range, kWalkWarps, c, greedy, s.cmd.known, part);
-      if (s.cmd.last ? lane < cluster : lane == 0) send(sum, &s.total[rank], (uint32_t)lane);
+      const Total sum = join(s.range, kWalkWarps, c, greedy, known, part);
+      if (last ? lane < cluster : lane == 0) send(sum, &s.total[rank], (uint32_t)lane);
     }
     cluster_sync();
-    if (s.cmd.last) {  // every block sees for itself who holds the bonus token
+    if (last) {  // every block sees for itself who holds the bonus token
       Pair mine;
-      const Total all = join(s.total, cluster, c, false, s.cmd.known, mine);
+      const Total all = join(s.total, cluster, c, false, known, mine);
       if (all.sum.h > 0.0f) {
         target = all.sum * u_bonus;
         const Found f = find_lane<16>(mine, target);
@@ -1209,9 +1211,9 @@ __global__ void __launch_bounds__(kWalkThreads, 2) k_sample_walk(const __grid_co
 
 int64_t sample_units(int64_t V) { return (V + 3 + kUnit - 1) / kUnit; }  // (a row's places start up to three early)
 
-// Blocks of a request's cluster: as many as still leave all requests' clusters room at the same time, and 2048 tokens
-// or more a block.  (With rooms for a part of them the others start when those end: 24 requests at 16 blocks took 98 us
-// where 4 took 80, both in an earlier form.)
+// Blocks of a request's cluster: as many as still leave all requests' clusters room at the same time, and 2048
+// tokens or more a block.  (With room for a part of them the others start when those end: 24 requests at 16 blocks took
+// 98 us where 4 took 80, both in an earlier form.)
 int cluster_size(int32_t n_req, int64_t V, int& size) {
   constexpr int kSizes = 8;
   static const int sizes[kSizes] = {16, 12, 8, 6, 4, 3, 2, 1};

@@ -278,6 +278,21 @@ def test_nothing_left(w12):
     p.check(w12)
 
 
+@pytest.mark.parametrize("counts", [[2], [4], [2, 4, 7] * 8, [2] * 64])
+def test_rounds_that_end_and_go_on(w12, counts):
+    """A last sum that leaves nothing is followed by another round, beside requests that end with theirs; every
+    run gives the same."""
+    p = Problem(13, counts, 40000, temperature=None, shape="star")
+    for r in range(0, len(counts), 2):
+        s = slice(p.off[r], p.off[r + 1])
+        p.probs[s] = 1.0
+        p.u[s] = 0.999
+    got, ws = p.check(w12), w12.Workspace()
+    logits, probs, a = f32(p.logits), f32(p.probs), p.args()
+    runs = [w12.tree_verify_sampled(logits, draft_probs=probs, ws=ws, **a) for _ in range(50)]
+    assert all(tuple(t.tolist() for t in x[:3]) == got and int(x[3]) == 0 for x in runs)
+
+
 def test_numbers_at_the_ends(w12):
     for u, ub in ((0.0, 0.0), (1.0, 1.0), (np.nan, np.nan), (-3.0, 5.0), (0.99999994, 0.99999994)):
         p = Problem(4, [6, 3], 777, temperature=None)
