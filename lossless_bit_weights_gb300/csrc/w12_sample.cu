@@ -1213,37 +1213,31 @@ int64_t sample_units(int64_t V) { return (V + 3 + kUnit - 1) / kUnit; }  // (a r
 
 // Blocks of a request's cluster: as many as still leave all requests' clusters room at the same time, and 2048
 // tokens or more a block.  (With room for a part of them the others start when those end: 24 requests at 16 blocks took
-// 98 us where 4 took 80, both in an earlier form.)
+// 98 us where 4 took 80, both in an earlier form.  24 requests have room for clusters of 10: 52.5 us, 8 took 55.)
 int cluster_size(int32_t n_req, int64_t V, int& size) {
-  constexpr int kSizes = 8;
-  static const int sizes[kSizes] = {16, 12, 8, 6, 4, 3, 2, 1};
-  static int room[64][kSizes] = {{0}};  // clusters that a device holds at once
+  static int room[64][kMaxCluster + 1] = {{0}};  // clusters of a size that a device holds at once
   int dev = 0;
   W12_CUDA_TRY(cudaGetDevice(&dev));
   size = 1;
   if (dev >= 64) return W12_OK;
-  if (!room[dev][kSizes - 1]) {
+  if (!room[dev][1]) {
     W12_CUDA_TRY(cudaFuncSetAttribute(k_sample_walk, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
-    for (int i = 0; i < kSizes; ++i) {
+    for (int blocks = kMaxCluster; blocks; --blocks) {
       cudaLaunchAttribute attr[1];
       attr[0].id = cudaLaunchAttributeClusterDimension;
-      attr[0].val.clusterDim.x = (unsigned)sizes[i];
+      attr[0].val.clusterDim.x = (unsigned)blocks;
       attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
       cudaLaunchConfig_t cfg = {};
-      cfg.gridDim = dim3((unsigned)sizes[i]);
+      cfg.gridDim = dim3((unsigned)blocks);
       cfg.blockDim = dim3(kWalkThreads);
       cfg.attrs = attr;
       cfg.numAttrs = 1;
       int n = 0;
       W12_CUDA_TRY(cudaOccupancyMaxActiveClusters(&n, k_sample_walk, &cfg));
-      room[dev][i] = n > 0 ? n : sizes[i] == 1;
+      room[dev][blocks] = n > 0 ? n : blocks == 1;
     }
   }
-  for (int i = 0; i < kSizes; ++i)
-    if (sizes[i] == 1 || (room[dev][i] >= n_req && V > sizes[i] * (int64_t)2048)) {
-      size = sizes[i];
-      break;
-    }
+  for (size = kMaxCluster; size > 1 && (room[dev][size] < n_req || V <= size * (int64_t)2048);) --size;
   return W12_OK;
 }
 
