@@ -17,10 +17,10 @@
 //
 // Two kernels: the rows that the walk may pass are summed by all SMs first, then a cluster of blocks per request
 // walks its tree and sums a row again for every refusal.  192 nodes of 24 requests over 151936 tokens with q take
-// 55 us (the rows' 70.5 MB and 24 rows of q are 13 us at the measured copy rate, the rows that these walks really
-// need 7), a 16-node tree 23, 64 chains of five without q 58 (193 MB), one row of 32000 tokens 9.5.  What is left is
-// the longest walk: a refusal is a round of the cluster, of which the sum over 19000 tokens a block is 4 to 6 us and two
-// cluster barriers, the joining and the decision about 3.
+// 50.5 us (the rows' 70.5 MB and 24 rows of q are 13 us at the measured copy rate, the rows that these walks really
+// need 7), a 16-node tree 23, 64 chains of five without q 55.5 (193 MB), one row of 32000 tokens 9.2.  What is left is
+// the longest walk: a refusal is a round of the cluster, of which the sum over 15000 tokens a block is 4 to 6 us and a
+// cluster barrier, the joining and the decision 2 to 3.
 #include <cstdint>
 #include <type_traits>
 
@@ -640,7 +640,7 @@ __device__ __forceinline__ Pair mass1(float l, const Ref& r, const Slope& c) {
   return l >= -kMost && h > kLeast ? Pair{h, h * w} : Pair{0.0f, 0.0f};
 }
 
-// What the first block of a cluster has all its blocks do next.
+// What a cluster's blocks do next.
 enum : int32_t { kOpDone, kOpSum, kOpFind };
 
 struct alignas(16) Command {
@@ -696,18 +696,39 @@ struct Walk {
   Pair tau, Q, M, out;  // out: the masses of the refused children (no q)
 };
 
-struct WalkShared {
+// What all blocks have from the first one, beside its tree: each then comes to the same decisions.
+struct alignas(16) Given {
+  int64_t off;
+  int32_t n, ok;
+  Slope slope;
+  float u_bonus;
+  int32_t greedy;
+};
+
+struct alignas(16) Tree {
   int32_t parent[kSampleMaxNodes], draft[kSampleMaxNodes];
-  int32_t refused[kSampleMaxNodes];              // places
   float u[kSampleMaxNodes], q[kSampleMaxNodes];  // of a node: its number, and q of its token at the parent
-  Pair mass[kSampleMaxNodes];                    // its token's mass at the parent (the logit at first)
   float most[kSampleMaxNodes];                   // of rows with children
   int32_t at[kSampleMaxNodes];
-  Pair sum[kSampleMaxNodes];
+  Pair mass[kSampleMaxNodes];                    // its token's mass at the parent (the logit at first)
+  Pair sum[kSampleMaxNodes];                     // of rows with children
   uint32_t inner[kSampleMaxNodes / 32];
+
+  // Where the 16-byte words of four nodes stand: kWords of them, the last for 128 nodes.
+  static constexpr int kWords = 11;
+  static __device__ __forceinline__ int place(int four, int word) {
+    const int array = word < 6 ? word : word < 8 ? 6 : word < 10 ? 8 : 10;
+    return array * 4 * kSampleMaxNodes + (word < 6 || word == 10 ? 16 * four : 32 * four + 16 * (word & 1));
+  }
+};
+static_assert(sizeof(Tree) == (10 * 4 + 4 / 32.0) * kSampleMaxNodes, "arrays one behind another");
+
+struct WalkShared : Tree {
+  int32_t refused[kSampleMaxNodes];  // places
   Command cmd;
   Walk walk;
-  Total total[kMaxCluster];  // the blocks', in the first one, or in all for a last command
+  Total total[2][kMaxCluster];  // the blocks', of every other round
+  Given given;
   Total range[kWalkWarps];
   Pair group[kWalkWarps];
   int32_t n_refused, last;
@@ -887,11 +908,13 @@ __device__ __forceinline__ void find_token(const SampleArgs& a, WalkShared& s, c
   if (tid == 0) *bonus = s.last;
 }
 
-// What comes next, by the first block's first warp (all lanes alike): the walk goes on with the sums that it had
-// asked for, until it needs others or ends.
-__device__ __forceinline__ Command decide(const SampleArgs& a, WalkShared& s, Slope c, float u_bonus, bool ok, bool greedy, int r,
-                                          int64_t off, int n, int cluster) {
-  const int lane = threadIdx.x & 31;
+// What comes next, by a block's first warp (all lanes alike, and all blocks): the walk goes on with the sums that it
+// had asked for, until it needs others or ends.  The first block writes the results.
+__device__ __forceinline__ Command decide(const SampleArgs& a, WalkShared& s, const Total* total, Slope c, bool greedy, int r,
+                                          bool writes, int cluster) {
+  const int lane = threadIdx.x & 31, n = s.given.n;
+  const bool ok = s.given.ok;
+  writes = writes && lane == 0;
   const Pair zero{0.0f, 0.0f}, one{1.0f, 0.0f};
   Walk w = s.walk;
   Command cmd = s.cmd;    // the last one
@@ -920,11 +943,11 @@ __device__ __forceinline__ Command decide(const SampleArgs& a, WalkShared& s, Sl
   if (ok && w.stage == kStart) {
     enter(0);
     w.depth = 0;
-    if (lane == 0) a.path_nodes[off] = 0;
+    if (writes) a.path_nodes[s.given.off] = 0;
   }
   cmd.op = kOpDone;
   if (ok) {
-    if (w.stage != kStart) all = join(s.total, cluster, c, greedy, cmd.known, mine);  // the blocks' sums
+    if (w.stage != kStart) all = join(total, cluster, c, greedy, cmd.known, mine);  // the blocks' sums
     bool ends = w.stage == kSummed, asked = false;
     if (w.stage == kRefused) {
       w.M = all.sum;
@@ -987,7 +1010,7 @@ __device__ __forceinline__ Command decide(const SampleArgs& a, WalkShared& s, Sl
 #pragma unroll 1
             for (int i0 = j + 1; i0 < n && !more; i0 += 32)
               more = __any_sync(0xFFFFFFFFu, i0 + lane < n && s.parent[i0 + lane] == w.cur);
-            if (!more && lane == 0) a.path_len[r] = w.depth;
+            if (!more && writes) a.path_len[r] = w.depth;
             ask(true, false, !more);
             w.stage = kRefused;
             asked = true;
@@ -996,32 +1019,32 @@ __device__ __forceinline__ Command decide(const SampleArgs& a, WalkShared& s, Sl
       }
       if (take) {
         ++w.depth;
-        if (lane == 0) a.path_nodes[off + w.depth] = j;
+        if (writes) a.path_nodes[s.given.off + w.depth] = j;
         enter(j);
       }
     }
     if (ends) {
       if (w.stage != kSummed) {
-        if (lane == 0) a.path_len[r] = w.depth;
+        if (writes) a.path_len[r] = w.depth;
         if (greedy && w.inner) {
-          if (lane == 0) a.bonus[r] = s.most[w.cur] > -INFINITY ? s.at[w.cur] : -1;
+          if (writes) a.bonus[r] = s.most[w.cur] > -INFINITY ? s.at[w.cur] : -1;
         } else if (!w.summed) {
           ask(false, w.refused, !greedy);
           w.stage = kSummed;
         }
       } else if (greedy) {
-        if (lane == 0) a.bonus[r] = all.most > -INFINITY ? all.at : -1;
+        if (writes) a.bonus[r] = all.most > -INFINITY ? all.at : -1;
       } else if (!(all.sum.h > 0.0f)) {
         if (cmd.refused) {  // all that had a mass was refused: p as it was
           ask(false, false, true);
-        } else if (lane == 0) {
+        } else if (writes) {
           a.bonus[r] = -1;
         }
       } else {
         w.summed = true;
       }
       if (w.summed && !greedy) {
-        const Pair target = all.sum * u_bonus;
+        const Pair target = all.sum * s.given.u_bonus;
         const Found f = find_lane<16>(mine, target);
         cmd.op = kOpFind;
         cmd.most = all.most;
@@ -1035,12 +1058,15 @@ __device__ __forceinline__ Command decide(const SampleArgs& a, WalkShared& s, Sl
   return cmd;
 }
 
-// A cluster takes a request.  Its first block walks the tree (warp 0, all lanes alike) and has all blocks sum a
-// row's masses, a range of tokens a warp, where a refusal or the bonus token asks for it; only that
-// block decides what comes next, and the others do as they are told, so that no barrier depends on two blocks
-// reading the same.  Bound by those rounds' latencies, then by arithmetic (22 operations on pairs of floats a
-// token and refusal).  Blocks of 512 threads, two an SM at 64 registers: an earlier form, 57 us for 192 nodes, took 64
-// with one an SM at 128, 61 with 1024 threads; four of 256 threads 55, but a single tree 27 for 23.
+// A cluster takes a request.  Its first block reads the tree, the numbers and the sums of the rows with children and
+// sends all of them to the others; then every block walks the tree (warp 0, all lanes alike), and where a refusal or
+// the bonus token asks for a row's masses, each sums its part, a range of tokens a warp, and sends the sum to all.
+// No block reads what decides from memory itself, so that all come to the same and no barrier can miss one.  Bound by the
+// rounds' latencies (of a single tree's 6 us a round 3 are sums), then by arithmetic (22 operations on pairs of floats
+// a token and refusal).  With the first block alone deciding, and a second barrier a round for its command, 192 nodes
+// took 52.5 us for 50.5, 64 chains 57.6 for 55.5.  Blocks of 512 threads, two an SM at 64 registers: an earlier
+// form, 57 us for 192 nodes, took 64 with one an SM at 128, 61 with 1024 threads; four of 256 threads 55, but a single
+// tree 27 for 23.
 __global__ void __launch_bounds__(kWalkThreads, 2) k_sample_walk(const __grid_constant__ SampleArgs a, int cluster) {
   __shared__ WalkShared s;
   cluster_arrive();  // a block's shared memory is written to only when the block runs
@@ -1050,17 +1076,17 @@ __global__ void __launch_bounds__(kWalkThreads, 2) k_sample_walk(const __grid_co
   const uint32_t rank = cluster_rank();
   const int r = blockIdx.x / cluster;
   const int64_t first = (int64_t)rank * kWalkWarps * a.range;  // the block's places
-  int64_t off;
-  int n;
-  bool ok = sample_request(a, r, off, n);
-  if (!ok) n = 0;
-  const float T = a.temperature ? a.temperature[r] : 1.0f, u_bonus = fminf(fmaxf(a.u_bonus[r], 0.0f), 0.99999994f);
-  const bool greedy = T < kGreedy;
-  const Slope c = make_slope(greedy ? 1.0f : T);
   const float2 root = kRoots[lane];
 
   // ---- the nodes, and the sums of the rows with children
   if (rank == 0) {
+    int64_t off = 0;
+    int n = 0;
+    bool ok = sample_request(a, r, off, n);
+    if (!ok) n = 0;
+    const float T = a.temperature ? a.temperature[r] : 1.0f, u_bonus = fminf(fmaxf(a.u_bonus[r], 0.0f), 0.99999994f);
+    const bool greedy = T < kGreedy;
+    const Slope c = make_slope(greedy ? 1.0f : T);
     if (tid < kSampleMaxNodes / 32) s.inner[tid] = 0;
     __syncthreads();
     ok = ok && T >= 0.0f;
@@ -1143,25 +1169,38 @@ __global__ void __launch_bounds__(kWalkThreads, 2) k_sample_walk(const __grid_co
         if (i > 0 && i < n) s.mass[i] = mass1(s.mass[i].h, make_ref(s.most[s.parent[i]], c), c);
       }
     __syncthreads();
-  } else if (a.M > 1) {
-    pdl_enter();
+    cluster_wait();
+    if (tid < cluster) send(Given{off, n, ok, c, u_bonus, greedy}, &s.given, (uint32_t)tid);
+#pragma unroll 1
+    for (int k = tid; ok && k < (n + 3) / 4 * Tree::kWords * (cluster - 1); k += kWalkThreads) {
+      const int nth = k / (cluster - 1), four = nth / Tree::kWords, word = nth - four * Tree::kWords;
+      if (word == 10 && four > (n - 1) / 128) continue;
+      uint4* w = reinterpret_cast<uint4*>(reinterpret_cast<char*>(&s) + Tree::place(four, word));
+      send(*w, w, (uint32_t)(1 + k - nth * (cluster - 1)));
+    }
+  } else {
+    if (a.M > 1) pdl_enter();
+    cluster_wait();
   }
 
   if (tid == 0) s.walk.stage = kStart;
-  __syncwarp();
-  cluster_wait();
+  cluster_sync();
+  const bool greedy = s.given.greedy;
+  const Slope c = s.given.slope;
   int holder = -1;  // of the bonus token, and what find_token is told
   float most = 0.0f;
   Pair target{0.0f, 0.0f};
+  int turn = 0;  // a block may send its next sums while another still reads the last ones
   while (true) {
-    if (rank == 0 && warp == 0) {
-      const Command cmd = decide(a, s, c, u_bonus, ok, greedy, r, off, n, cluster);
+    if (warp == 0) {
+      const Command cmd = decide(a, s, s.total[turn], c, greedy, r, rank == 0, cluster);
       __syncwarp();
-      if (lane < cluster) send(cmd, &s.cmd, (uint32_t)lane);
+      if (lane == 0) s.cmd = cmd;
     }
-    cluster_sync();
+    turn ^= 1;
+    __syncthreads();
     if (s.cmd.op == kOpDone) break;
-    const Row row = row_of(a, off + s.cmd.node);
+    const Row row = row_of(a, s.given.off + s.cmd.node);
     if (s.cmd.op == kOpFind) {
       holder = s.cmd.owner;
       most = s.cmd.most;
@@ -1172,10 +1211,8 @@ __global__ void __launch_bounds__(kWalkThreads, 2) k_sample_walk(const __grid_co
       if (tid == 0) s.n_refused = 0;
       __syncthreads();
 #pragma unroll 1
-      for (int i = s.cmd.node + 1 + tid; i < n; i += kWalkThreads) {
-        const int32_t x = a.draft[off + i];
-        if (a.parent[off + i] == s.cmd.node && x >= 0 && x < a.V) s.refused[atomicAdd(&s.n_refused, 1)] = x + row.lo;
-      }
+      for (int i = s.cmd.node + 1 + tid; i < s.given.n; i += kWalkThreads)
+        if (s.parent[i] == s.cmd.node && s.draft[i] >= 0) s.refused[atomicAdd(&s.n_refused, 1)] = s.draft[i] + row.lo;
       __syncthreads();
     }
     const int64_t v0 = first + warp * a.range, v1 = min(row.hi, v0 + a.range);
@@ -1185,19 +1222,18 @@ __global__ void __launch_bounds__(kWalkThreads, 2) k_sample_walk(const __grid_co
                                 : sum_unknown<4>(row, c, v0, v1, root);
     if (lane == 0) s.range[warp] = t;
     __syncthreads();
-    // (Behind the round's second barrier the first block may already have sent the next command.)
-    const bool last = s.cmd.last, known = s.cmd.known;
+    const bool last = s.cmd.last, known = s.cmd.known;  // (behind the barrier the first warp goes on to the next command)
     if (warp == 0) {
       Pair part;
       const Total sum = join(s.range, kWalkWarps, c, greedy, known, part);
-      if (last ? lane < cluster : lane == 0) send(sum, &s.total[rank], (uint32_t)lane);
+      if (lane < cluster) send(sum, &s.total[turn][rank], (uint32_t)lane);
     }
     cluster_sync();
-    if (last) {  // every block sees for itself who holds the bonus token
+    if (last) {  // every warp sees for itself which block holds the bonus token
       Pair mine;
-      const Total all = join(s.total, cluster, c, false, known, mine);
+      const Total all = join(s.total[turn], cluster, c, false, known, mine);
       if (all.sum.h > 0.0f) {
-        target = all.sum * u_bonus;
+        target = all.sum * s.given.u_bonus;
         const Found f = find_lane<16>(mine, target);
         holder = f.lane;
         most = all.most;
@@ -1206,7 +1242,7 @@ __global__ void __launch_bounds__(kWalkThreads, 2) k_sample_walk(const __grid_co
       }
     }
   }
-  if (holder == (int)rank) find_token(a, s, c, row_of(a, off + s.cmd.node), first, root, most, target, a.bonus + r);
+  if (holder == (int)rank) find_token(a, s, c, row_of(a, s.given.off + s.cmd.node), first, root, most, target, a.bonus + r);
 }
 
 int64_t sample_units(int64_t V) { return (V + 3 + kUnit - 1) / kUnit; }  // (a row's places start up to three early)
