@@ -17,8 +17,8 @@
 //
 // Two kernels: the rows that the walk may pass are summed by all SMs first, then a cluster of blocks per request
 // walks its tree and sums a row again for every refusal.  192 nodes of 24 requests over 151936 tokens with q take
-// 50.5 us (the rows' 70.5 MB and 24 rows of q are 13 us at the measured copy rate, the rows that these walks really
-// need 7), a 16-node tree 23, 64 chains of five without q 55.5 (193 MB), one row of 32000 tokens 9.2.  What is left is
+// 50 us (the rows' 70.5 MB and 24 rows of q are 13 us at the measured copy rate, the rows that these walks really
+// need 7), a 16-node tree 23, 64 chains of five without q 55 (193 MB), one row of 32000 tokens 9.  What is left is
 // the longest walk: a refusal is a round of the cluster, of which the sum over 15000 tokens a block is 4 to 6 us and a
 // cluster barrier, the joining and the decision 2 to 3.
 #include <cstdint>
@@ -1060,13 +1060,14 @@ __device__ __forceinline__ Command decide(const SampleArgs& a, WalkShared& s, co
 
 // A cluster takes a request.  Its first block reads the tree, the numbers and the sums of the rows with children and
 // sends all of them to the others; then every block walks the tree (warp 0, all lanes alike), and where a refusal or
-// the bonus token asks for a row's masses, each sums its part, a range of tokens a warp, and sends the sum to all.
-// No block reads what decides from memory itself, so that all come to the same and no barrier can miss one.  Bound by the
-// rounds' latencies (of a single tree's 6 us a round 3 are sums), then by arithmetic (22 operations on pairs of floats
-// a token and refusal).  With the first block alone deciding, and a second barrier a round for its command, 192 nodes
-// took 52.5 us for 50.5, 64 chains 57.6 for 55.5.  Blocks of 512 threads, two an SM at 64 registers: an earlier
-// form, 57 us for 192 nodes, took 64 with one an SM at 128, 61 with 1024 threads; four of 256 threads 55, but a single
-// tree 27 for 23.
+// the bonus token asks for a row's masses, each sums its part, a range of tokens a warp, and sends the sum to all. No
+// block reads what decides from memory itself, so that all come to the same and no barrier can miss one.  Bound by
+// the rounds' latencies (a single tree's round has 3 us of sums, as much for joining and deciding, 1 for the
+// barrier), then by arithmetic (22 operations on pairs of floats a token and refusal).  With the first block alone
+// deciding, and a second barrier a round for its command, 192 nodes took 52.5 us for 50, 64 chains 57.6 for 55.2.
+// Asynchronous copies of a sum's next tokens to shared memory brought nothing.  Blocks of 512 threads, two an SM at
+// 64 registers: an earlier form, 57 us for 192 nodes, took 64 with one an SM at 128, 61 with 1024 threads; four of
+// 256 threads 55, but a single tree 27 for 23.
 __global__ void __launch_bounds__(kWalkThreads, 2) k_sample_walk(const __grid_constant__ SampleArgs a, int cluster) {
   __shared__ WalkShared s;
   cluster_arrive();  // a block's shared memory is written to only when the block runs
