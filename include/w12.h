@@ -716,8 +716,9 @@ W12_API int logits_verify(const float* logits, int64_t stride, int64_t M, int64_
  * drawn any more (Q <= 0, or a refused one with q(x) = 0) are passed over and leave p and q.  Where a refusal leaves nothing
  * (p <= q everywhere, or all that p held was refused), no further child is accepted and the bonus comes from p
  * as it was at the node.  bonus[r] = -1 where the node allows no token.  Numbers u outside [0, 1) count as the nearest in it (NaN: 0).
- * Decisions and sums are made to 2^-28 of p's sum or better, so that borders between tokens of
- * large vocabularies fall where the formula has them.  Repeated calls give identical results.
+ * Sums are made to 2^-28 of the node's sum (of the logits' masses) or better, after j refusals with draft_probs to
+ * j + 1 times 2^-27 of it, so that borders between tokens of large vocabularies fall where the formula has them
+ * (temperatures up to 1e30).  Repeated calls give identical results.
  * parent, draft, req_offsets, path_len, path_nodes and bonus as for tree_verify_tokens, path_nodes -1 behind the path.
  * A request that is out of range (offsets, a malformed tree, more than 1024 nodes, a temperature that is
  * negative or NaN) sets bit 0 of *status and has path_len = bonus = -1, as has one without nodes; offsets that fall

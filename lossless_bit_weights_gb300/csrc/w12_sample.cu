@@ -12,8 +12,10 @@
 //
 // The bonus is the first token whose cumulative mass passes u M.  In a large vocabulary the borders between
 // tokens stand 2^-20 of the mass apart and closer, so a mass has to be good to far more than a float: it
-// is a pair of floats (2^-30 of its value), summed without loss, and the sums stay pairs.  (With plain floats one
-// token in some hundreds would differ from the formula's.)
+// is a pair of floats (2.8e-9 of its value), the sums stay pairs, and what adding rounds off is kept: a sum is good to
+// 2^-28.  (With plain floats one token in some hundreds would differ from the formula's.)  tau takes its error from the
+// sums before it: after j refusals a sum is off by j + 1 times 2^-27 of S at most, since what tau adds to one sum's error
+// the next takes off again (sum of q over what is left: Q at most), and left2 rounds three times by 2^-30.5 of e.
 //
 // Two kernels: the rows that the walk may pass are summed by all SMs first, then a cluster of blocks per request
 // walks its tree and sums a row again for every refusal.  192 nodes of 24 requests over 151936 tokens with q take
@@ -273,8 +275,9 @@ __device__ __forceinline__ Scale make_scale(const Ref& r, const Slope& c, float2
 
 // The masses of two logits, h + lo each: 2^(x - whole), x = (l - shift) c.  With 32 x rounded to n,
 // 2^x = 2^(n / 32) 2^g, |g| <= 1/64; g comes from fused products without their rounding, and 2^g - 1 = g (ln 2 +
-// g (a + g b)) to 2^-33 (Taylor's terms, the second raised by 0.83 of the fourth's most), so that with the root's rest
-// a mass is good to 2^-30.  What has none comes out as 2^-125 or so, which least2 and left2 take for nothing.
+// g (a + g b)) to 2^-33 (Taylor's terms, the second raised by 0.83 of the fourth's most), with the root's rest.  The roundings
+// are g's two (2^-31 each), w's last two (2^-30.5, 2^-31) and lo's (2^-30.5): a mass is good to 2.8e-9 of itself at worst
+// (2^-28.6 was the most found).  What has none comes out as 2^-125 or so, which least2 and left2 take for nothing.
 // All lanes of a warp take part.  Without ANY the scale is plain.
 template <bool ANY>
 __device__ __forceinline__ void mass2(uint64_t l, const Scale& c, uint64_t& h, uint64_t& lo) {
@@ -351,24 +354,34 @@ __device__ __forceinline__ float rough(float l, float most, float slope, float l
   return d >= least ? rough_exp2(d * slope) : 0.0f;
 }
 
-// A running sum of pairs, two at a time.  It starts at 4, above every mass, so that an addition's rounding
-// comes back from three operations.
+// A running sum of masses, two side by side, and what its additions round off (Knuth's six operations, since a mass
+// may be larger than the sum so far).  Low parts are up to 1.1 % of their masses and often of one sign, so they are
+// added like the masses, two as one: that sum's rounding, 2^-30.5 of the masses, is the only loss.  `rest` takes
+// 2^-24 of the sum at a time, which a float adds up to 2^-30 of it at worst over kStretch places; longer ranges settle.
+// With the low parts in `rest`, and sums that start above every mass for the sake of three operations, 9496 equal masses
+// lost up to 2^-25.4 of their sum, 42752 2^-23.5; 192 nodes then took 50.4 us (53.4 now), 64 chains 55.3 (57.8).
+// (Masses brought into order, lo the rounding of h, would lose nothing: 56.4 us.)
 struct Sum {
-  uint64_t s = both(4.0f), rest = both(0.0f);
-  __device__ __forceinline__ void add(uint64_t h, uint64_t lo) {
-    const uint64_t n = add2(s, h), t = sub2(h, sub2(n, s));
+  uint64_t s = both(0.0f), rest = both(0.0f);
+  __device__ __forceinline__ uint64_t step(uint64_t x) {  // (what it leaves)
+    const uint64_t n = add2(s, x), v = sub2(n, s), t = add2(sub2(s, sub2(n, v)), sub2(x, v));
     s = n;
-    rest = add2(rest, add2(t, lo));
+    return t;
   }
   __device__ __forceinline__ void add(const Four& m) {
-    add(m.h[0], m.lo[0]);
-    add(m.h[1], m.lo[1]);
+    const uint64_t x = add2(step(m.h[0]), step(m.h[1]));
+    const uint64_t l = add2(m.lo[0], m.lo[1]), n = add2(s, l), y = sub2(l, sub2(n, s));  // (smaller than the sum)
+    s = n;
+    rest = add2(rest, add2(x, y));
   }
+  __device__ __forceinline__ void settle() { rest = step(rest); }
   __device__ __forceinline__ Pair value() const {
     const float2 a = split2(s), b = split2(rest);
-    return (Pair{a.x, b.x} - Pair{4.0f, 0.0f}) + (Pair{a.y, b.y} - Pair{4.0f, 0.0f});
+    return Pair{a.x, b.x} + Pair{a.y, b.y};
   }
 };
+
+constexpr int kStretch = 1 << 15;  // places of a warp
 
 // A row of logits and its row of q.  Places are counted from the 16-byte boundary at or before the row's first logit,
 // so that any row allows 16-byte loads: tokens stand at places lo .. hi - 1, token v at v + lo.
@@ -446,7 +459,7 @@ __device__ __forceinline__ Total first_of_range(const Row& row, int64_t v0, int6
 
 // One warp's range of a row whose largest logit is not known (a node without children): the sum of its masses in
 // one sweep, in units of the largest logit of the first tokens, and of larger ones where they come (the sum so far
-// changes by a power of two then).  A mass may pass a unit by twice before that, which stays below the 4 that Sum starts at.
+// changes by a power of two then).  A mass may pass a unit by twice before that.
 template <int U>  // loads of a lane on their way
 __device__ __forceinline__ Total sum_unknown(const Row& row, const Slope& c, int64_t v0, int64_t v1, float2 root) {
   const int lane = threadIdx.x & 31;
@@ -476,7 +489,7 @@ __device__ __forceinline__ Total sum_unknown(const Row& row, const Slope& c, int
       scale = make_scale(to, c, root);
     }
     if (t.most == -INFINITY) continue;
-    if (scale.plain && v1 - v0 <= 1 << 24) {
+    if (scale.plain && v1 - v0 <= kStretch) {
 #pragma unroll
       for (int k = 0; k < U; ++k) sum.add(masses4<false, true>(f[k], scale));
     } else {
@@ -484,6 +497,7 @@ __device__ __forceinline__ Total sum_unknown(const Row& row, const Slope& c, int
       for (int k = 0; k < U; ++k) {
         const int64_t i = i0 + k * 128 + 4 * lane;
         sum.add(masses4<true>(four(row.x, i, row.lo, v1, true, -INFINITY), scale));
+        sum.settle();
       }
     }
   }
@@ -601,15 +615,15 @@ __global__ void __launch_bounds__(kStatThreads, 3) k_sample_stats(const __grid_c
     }
   }
   __syncthreads();
-  // An equal share of all units for every warp, one stretch after another; a stretch in one row has one sum, in the
-  // place of its first unit.  (At most 2^10 rows of 2^21 units.)
+  // An equal share of all units for every warp, one stretch after another; a stretch in one row, of up to kStretch
+  // places where it is summed in pairs, has one sum, in the place of its first unit.  (At most 2^10 rows of 2^21 units.)
   const uint32_t units = a.units;
   const int64_t items = (int64_t)rows * units, warps = (int64_t)gridDim.x * (kStatThreads / 32);
   const int64_t mine = (int64_t)blockIdx.x * (kStatThreads / 32) + (tid >> 5), stop = items * (mine + 1) / warps;
 #pragma unroll 1
   for (int64_t item = items * mine / warps; item < stop;) {
     const uint32_t nth = (uint32_t)item / units, unit = (uint32_t)item - nth * units;
-    const uint32_t run = (uint32_t)min(stop - item, (int64_t)(units - unit));
+    const uint32_t run = (uint32_t)min(stop - item, (int64_t)(a.probs ? min(units - unit, kStretch / kUnit) : units - unit));
     const float4 slope = slopes[nth];
     const int64_t m = m0 + list[nth];
     const Row row = row_of(a, m);
@@ -771,7 +785,7 @@ __device__ __forceinline__ Total sum_range(const Row& row, const Command& cmd, c
   bool mine = false;  // does the range hold a refused token
 #pragma unroll 1
   for (int k = 0; k < n_refused; ++k) mine = mine || (refused[k] >= v0 && refused[k] < v1);
-  const bool whole_steps = (!cmd.residual || row.p_vec) && scale.plain && v1 - v0 <= 1 << 24;
+  const bool whole_steps = (!cmd.residual || row.p_vec) && scale.plain && v1 - v0 <= kStretch;
 #pragma unroll 1
   for (int64_t i0 = v0; i0 < v1;) {
     bool plain = whole_steps && i0 >= row.lo && i0 + 128 * U <= v1;
@@ -803,6 +817,7 @@ __device__ __forceinline__ Total sum_range(const Row& row, const Command& cmd, c
       if (mine) without(m, i, refused, n_refused);
       if (cmd.residual) left4(m, chance4(four(p, i, row.lo, v1, row.p_vec, 0.0f)), cmd.tau_hi, cmd.tau_lo);
       sum.add(m);
+      sum.settle();
       i0 += 128;
     }
   }
