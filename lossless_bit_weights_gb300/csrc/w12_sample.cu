@@ -62,7 +62,7 @@ struct SampleArgs {
 struct alignas(16) UnitStat {
   float most;    // largest logit (-inf: none, NaN left out)
   int32_t at;    // its first token, of greedy requests
-  float sum[2];  // of the masses, in the units of the largest (without q to 2^-18)
+  float sum[2];  // of the masses, in the units of the largest (without q to 2^-15)
 };
 
 __device__ __forceinline__ bool sample_request(const SampleArgs& a, int r, int64_t& off, int& n) {
@@ -506,7 +506,10 @@ __device__ __forceinline__ Total sum_unknown(const Row& row, const Slope& c, int
   return t;
 }
 
-// The same by plain floats, to 2^-18: a lane's sum in the mass of its own largest logit, which grows with it.
+// The same by plain floats, a lane's sum in the mass of its own largest logit, which grows with it.  Over kStretch
+// places that is good to 2^-15: 256 additions 2^-16 at worst, 32 changes of the largest logit 2^-16.7, the exponents'
+// roundings 2^-18 where 2^-31 of the sum is a mass, less where it is more.  (They do not cancel: 4600 additions that round
+// one way were seen to lose 6.8e-5 of the sum of 2^31 tokens.)
 template <int U>
 __device__ __forceinline__ Total rough_unknown(const Row& row, const Slope& c, int64_t v0, int64_t v1) {
   const int lane = threadIdx.x & 31;
@@ -547,7 +550,7 @@ __device__ __forceinline__ Total rough_unknown(const Row& row, const Slope& c, i
 // Largest logit and mass of the rows whose nodes have children (what the walk asks of a node it passes), in units of
 // 1024 places.  Every block of a tile of nodes makes the list of its rows with children, and the tile's warps take
 // equal shares of all units, 128 bytes a lane on their way.  Without q the sums only serve decisions, which plain floats
-// (good to 2^-18 together) nearly always tell, and the walk sums again for the others.
+// (good to 2^-15 together) nearly always tell, and the walk sums again for the others.
 // Bound by the logits read once, and with q by the pairs' arithmetic: 256 rows of 151936 (156 MB) in 30.3 us without q
 // (5.1 TB/s, 0.76 of the measured copy rate; 2.8 of it to make the list), 116 rows (70.5 MB) in 20.5 with q, 16.6 if they
 // were rough.  Pairs for the chains too made their call 72 us for 59.  Bringing each warp's share into L2 ahead in bulk
@@ -616,14 +619,14 @@ __global__ void __launch_bounds__(kStatThreads, 3) k_sample_stats(const __grid_c
   }
   __syncthreads();
   // An equal share of all units for every warp, one stretch after another; a stretch in one row, of up to kStretch
-  // places where it is summed in pairs, has one sum, in the place of its first unit.  (At most 2^10 rows of 2^21 units.)
+  // places, has one sum, in the place of its first unit.  (At most 2^10 rows of 2^21 units.)
   const uint32_t units = a.units;
   const int64_t items = (int64_t)rows * units, warps = (int64_t)gridDim.x * (kStatThreads / 32);
   const int64_t mine = (int64_t)blockIdx.x * (kStatThreads / 32) + (tid >> 5), stop = items * (mine + 1) / warps;
 #pragma unroll 1
   for (int64_t item = items * mine / warps; item < stop;) {
     const uint32_t nth = (uint32_t)item / units, unit = (uint32_t)item - nth * units;
-    const uint32_t run = (uint32_t)min(stop - item, (int64_t)(a.probs ? min(units - unit, kStretch / kUnit) : units - unit));
+    const uint32_t run = (uint32_t)min(stop - item, (int64_t)min(units - unit, kStretch / kUnit));
     const float4 slope = slopes[nth];
     const int64_t m = m0 + list[nth];
     const Row row = row_of(a, m);
@@ -703,7 +706,7 @@ enum : int32_t { kStart, kRefused, kPrecise, kSummed };
 struct Walk {
   int32_t stage, cur, last, depth;
   bool inner;    // the node has children
-  bool rough;    // M is good to 2^-18 of p's sum only (no q)
+  bool rough;    // M is good to 2^-15 of p's sum only (no q)
   bool summed;   // the blocks hold the sums of what is left
   bool refused;  // a child was refused (no q)
   bool spent;    // nothing was left
@@ -1004,7 +1007,8 @@ __device__ __forceinline__ Command decide(const SampleArgs& a, WalkShared& s, co
         const Pair mine_u = w.M * u * q, limit = a.probs ? (e - w.tau * q) * w.Q : e;
         const bool moves = !a.probs || (q > 0.0f && w.Q > zero);  // a refusal would change p
         take = (!a.probs || w.Q > zero) && limit > mine_u;
-        if (w.rough && fabsf((mine_u - limit).h) <= 6.2e-5f * u * (w.M + w.out).h) {  // it does not tell
+        // (2^-14: a rough sum does not tell)
+        if (w.rough && fabsf((mine_u - limit).h) <= 6.2e-5f * u * (w.M + w.out).h) {
           w.last = j - 1;
           ask(false, false, false);
           w.stage = kPrecise;

@@ -259,3 +259,21 @@ def test_second_child_on_random_rows(w12, R, probs):
             want.append((len(path) - 1, token))
         length, _, bonus = call(w12, rows, Ts, drafts, us, ubs, qs if probs else None)
         assert list(zip(length, bonus)) == want
+
+
+@pytest.mark.parametrize("a,side", [(-1.3634447, 1), (-0.06020798, -1)])
+def test_rough_sum_of_a_long_row(w12, a, side):
+    """A row of 2^31 tokens without q, whose decision a rough sum must not take: tokens of mass 1 and e^a, e^a, e^a in turn,
+    so that a lane's additions of 1 + 3 e^a all round one way (4600 of them lose 6.8e-5 of the sum; sums tell apart what is
+    6.2e-5 away).  The number stands 2e-6 of itself from p."""
+    n, x = (1 << 31) - (1 << 14), (1 << 31) - (1 << 15)
+    if torch.cuda.get_device_properties(0).total_memory < 40 << 30:
+        pytest.skip("needs 40 GB")
+    logits = torch.zeros((2, n), device="cuda")
+    logits[0].view(-1, 4)[:, 1:] = a
+    logits[0, x] = 16.0
+    e = np.exp(float(np.float32(a)))
+    p = np.exp(16.0) / (n / 4 * (1 + 3 * e) - 1 + np.exp(16.0))
+    u = np.float32(p * (1 - side * 2e-6))
+    length, path, _, status = w12.tree_verify_sampled(logits, i32([-1, 0]), i32([0, x]), f32([0.0, u]), f32([0.5]))
+    assert int(status) == 0 and length.tolist() == [side > 0] and path.tolist() == ([0, 1] if side > 0 else [0, -1])
