@@ -485,7 +485,7 @@ __device__ __forceinline__ Total sum_unknown(const Row& row, const Slope& c, int
         sum = Sum();
       }
       t.most = most;
-      limit = most + c.over;
+      limit = fminf(most + c.over, kMost);  // (+inf passes it at any temperature)
       scale = make_scale(to, c, root);
     }
     if (t.most == -INFINITY) continue;

@@ -1,0 +1,28 @@
+"""tree_verify_sampled at the ends of its documented ranges: against the definition in 64 bits of test_gpu_sampled.py."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from tests.test_gpu_sampled import Problem, f32, i32, w12  # noqa: F401 (the fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("T", [1.0, 1e30, np.inf])
+@pytest.mark.parametrize("probs", [True, False])
+@pytest.mark.parametrize("counts,V", [([1, 1], 5000), ([4, 6, 1], 3001), ([2] * 200, 60001)])
+def test_infinite_logits_at_any_temperature(w12, T, probs, counts, V):
+    """+inf tokens share p evenly, wherever they stand in the row and however flat the others are."""
+    p = Problem(3, counts, V, probs=probs, temperature=None)
+    rng = np.random.default_rng(4)
+    M = sum(counts)
+    for m in range(M):
+        p.logits[m, rng.integers(V // 2, V, m % 4)] = np.inf
+    p.logits[0, -1] = np.inf
+    for m in range(1, M, 3):  # drafts that may be taken
+        best = np.flatnonzero(np.isinf(p.logits[m - 1]))
+        if len(best):
+            p.draft[m] = best[0]
+    p.T = np.full(len(counts), T, np.float32)
+    p.check(w12)
