@@ -57,6 +57,7 @@ struct SampleArgs {
   int32_t* falls;         // whether the offsets fall somewhere
   int64_t range;          // places of a warp in the walk, a multiple of 128
   int32_t n_req, units;
+  bool rows_first;        // the rows' kernel stands before the walk (not for one node of one request)
 };
 
 struct alignas(16) UnitStat {
@@ -1091,7 +1092,7 @@ __global__ void __launch_bounds__(kWalkThreads, 2) k_sample_walk(const __grid_co
   __shared__ WalkShared s;
   cluster_arrive();  // a block's shared memory is written to only when the block runs
   // The rows' kernel has waited for all before it, so the tree and the numbers may be read while it runs.
-  if (a.M == 1) pdl_enter();
+  if (!a.rows_first) pdl_enter();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t rank = cluster_rank();
   const int r = blockIdx.x / cluster;
@@ -1170,9 +1171,9 @@ __global__ void __launch_bounds__(kWalkThreads, 2) k_sample_walk(const __grid_co
         s.q[i] = s.draft[i] >= 0 && a.probs ? chance(a.probs[(off + p) * a.probs_stride + x]) : 0.0f;
       }
     }
-    if (a.M > 1) pdl_enter();
-    if (warp < n && a.M > 1) row_sum(warp);
-    if (a.M > 1) ok = ok && !*a.falls;
+    if (a.rows_first) pdl_enter();
+    if (warp < n && a.rows_first) row_sum(warp);
+    if (a.rows_first) ok = ok && !*a.falls;
     ok = __syncthreads_and(ok);
     if (!ok && tid == 0) atomicOr(a.status, kSampleBadRequest);
     ok = ok && n > 0;
@@ -1199,7 +1200,7 @@ __global__ void __launch_bounds__(kWalkThreads, 2) k_sample_walk(const __grid_co
       send(*w, w, (uint32_t)(1 + k - nth * (cluster - 1)));
     }
   } else {
-    if (a.M > 1) pdl_enter();
+    if (a.rows_first) pdl_enter();
     cluster_wait();
   }
 
@@ -1371,7 +1372,8 @@ int tree_verify_sampled(const float* logits, int64_t stride, int64_t M, int64_t 
   const int64_t warps = (int64_t)cluster * kWalkWarps;
   a.range = ((V + 3 + warps - 1) / warps + 127) / 128 * 128;
   a.n_req = n_req;
-  if (M > 1) {
+  a.rows_first = M > 1 || n_req > 1;
+  if (a.rows_first) {
     // three blocks an SM, if there is that much (half of the nodes have children, or nearly all)
     const int64_t tiles = (M + kStatTile - 1) / kStatTile, most = (M < kStatTile ? M : kStatTile) * (int64_t)a.units;
     int64_t blocks = (most + kStatThreads / 32 - 1) / (kStatThreads / 32);

@@ -26,3 +26,19 @@ def test_infinite_logits_at_any_temperature(w12, T, probs, counts, V):
             p.draft[m] = best[0]
     p.T = np.full(len(counts), T, np.float32)
     p.check(w12)
+
+
+def test_offsets_of_a_single_node(w12):
+    """Offsets that fall make all requests out of range, with one node too; requests without nodes beside the one that
+    has it are in order."""
+    p = Problem(5, [1], 900, temperature=None)
+    want = p.want()
+    for off, whose in (([0, 1, 0, 1], None), ([0, 1, 1, 0], None), ([1, 0, 1, 1], None), ([0, 0, 1, 1], 1), ([0, 1, 1, 1], 0),
+                       ([0, 0, 0, 1], 2)):
+        length, path, bonus, status = w12.tree_verify_sampled(
+            f32(p.logits), i32([-1]), i32([0]), f32([0.0]), f32(np.repeat(p.ub, 3)), req_offsets=i32(off))
+        assert int(status) == (whose is None), off
+        assert length.tolist() == [0 if r == whose else -1 for r in range(3)], off
+        assert bonus.tolist() == [want[2][0] if r == whose else -1 for r in range(3)], off
+        if whose is not None:
+            assert path.tolist() == [0]
