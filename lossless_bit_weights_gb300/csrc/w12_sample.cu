@@ -24,6 +24,7 @@
 // the longest walk: a refusal is a round of the cluster, of which the sum over 15000 tokens a block is 4 to 6 us and a
 // cluster barrier, the joining and the decision 2 to 3.
 #include <cstdint>
+#include <mutex>
 #include <type_traits>
 
 #include "w12_internal.cuh"
@@ -1272,11 +1273,13 @@ int64_t sample_units(int64_t V) { return (V + 3 + kUnit - 1) / kUnit; }  // (a r
 // tokens or more a block.  (With room for a part of them the others start when those end: 24 requests at 16 blocks took
 // 98 us where 4 took 80, both in an earlier form.  24 requests have room for clusters of 10: 52.5 us, 8 took 55.)
 int cluster_size(int32_t n_req, int64_t V, int& size) {
+  static std::mutex mu;  // (a host thread that saw a part of the table would take smaller clusters)
   static int room[64][kMaxCluster + 1] = {{0}};  // clusters of a size that a device holds at once
   int dev = 0;
   W12_CUDA_TRY(cudaGetDevice(&dev));
   size = 1;
   if (dev >= 64) return W12_OK;
+  std::lock_guard<std::mutex> lk(mu);
   if (!room[dev][1]) {
     W12_CUDA_TRY(cudaFuncSetAttribute(k_sample_walk, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
     for (int blocks = kMaxCluster; blocks; --blocks) {
