@@ -557,6 +557,7 @@ __device__ __forceinline__ Total rough_unknown(const Row& row, const Slope& c, i
 // (5.1 TB/s, 0.76 of the measured copy rate; 2.8 of it to make the list), 116 rows (70.5 MB) in 20.5 with q, 16.6 if they
 // were rough.  Pairs for the chains too made their call 72 us for 59.  Bringing each warp's share into L2 ahead in bulk
 // took 9 us more; two or four blocks an SM about 1; one row after another by a request's blocks twice the time.
+template <bool PAIRS>
 __global__ void __launch_bounds__(kStatThreads, 3) k_sample_stats(const __grid_constant__ SampleArgs a) {
   pdl_enter();
   __shared__ int32_t offsets[kStatRequests + 1];
@@ -635,7 +636,7 @@ __global__ void __launch_bounds__(kStatThreads, 3) k_sample_stats(const __grid_c
     const int64_t v0 = (int64_t)unit * kUnit, v1 = min(row.hi, v0 + (int64_t)run * kUnit);
     const Slope c{slope.x, slope.y, slope.z};
     const Total t = slope.w != 0.0f ? first_of_range(row, v0, v1)
-                    : a.probs       ? sum_unknown<8>(row, c, v0, v1, root)
+                    : PAIRS         ? sum_unknown<8>(row, c, v0, v1, root)
                                     : rough_unknown<8>(row, c, v0, v1);
     UnitStat* out = a.stat + m * units + unit;
 #pragma unroll 1
@@ -1381,7 +1382,8 @@ int tree_verify_sampled(const float* logits, int64_t stride, int64_t M, int64_t 
     const int64_t tiles = (M + kStatTile - 1) / kStatTile, most = (M < kStatTile ? M : kStatTile) * (int64_t)a.units;
     int64_t blocks = (most + kStatThreads / 32 - 1) / (kStatThreads / 32);
     blocks = blocks < 456 ? blocks : 456;
-    W12_CUDA_TRY(launch_dependent(k_sample_stats, dim3((unsigned)blocks, (unsigned)tiles), kStatThreads, 0, (cudaStream_t)stream, a));
+    W12_CUDA_TRY(launch_dependent(draft_probs ? k_sample_stats<true> : k_sample_stats<false>,
+                                  dim3((unsigned)blocks, (unsigned)tiles), kStatThreads, 0, (cudaStream_t)stream, a));
     W12_LAUNCH_CHECK("tree_verify_sampled: rows kernel");
   }
   cudaLaunchAttribute attr[2];
