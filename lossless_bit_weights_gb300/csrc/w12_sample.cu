@@ -995,16 +995,25 @@ __device__ __forceinline__ Command decide(const SampleArgs& a, WalkShared& s, co
       w.last = j;
       const int32_t x = s.draft[j];
       if (x < 0) continue;
-      bool take;
-      if (greedy) {
-        take = s.most[w.cur] > -INFINITY && x == s.at[w.cur];
-      } else {
-        if (w.spent || !(s.sum[w.cur].h > 0.0f)) continue;
+      bool take = greedy && x == s.at[w.cur];
+      if (greedy ? !(s.most[w.cur] > -INFINITY) : w.spent || !(s.sum[w.cur].h > 0.0f)) continue;
+      if (!greedy || a.probs) {
         bool twice = false;  // a sibling with this token was refused before
 #pragma unroll 1
         for (int i0 = w.cur + 1; i0 < j && !twice; i0 += 32)
           twice = __any_sync(0xFFFFFFFFu, i0 + lane < j && s.parent[i0 + lane] == w.cur && s.draft[i0 + lane] == x);
         if (twice) continue;
+      }
+      if (greedy && a.probs) {
+        // p stays 1 at its token, unless q was all of what it had left there when a sibling was refused (tau: Q then)
+        const Pair q{s.q[j], 0.0f};
+        if (take) {
+          take = w.Q > q * s.u[j] && w.Q > zero && (!(w.tau > zero) || w.tau > q);
+        } else if (q > zero && w.Q > zero) {
+          w.tau = w.Q;
+          w.Q = w.Q - q;
+        }
+      } else if (!greedy) {
         const Pair e = zero + s.mass[j];
         const float u = s.u[j], q = a.probs ? s.q[j] : 1.0f;
         const Pair mine_u = w.M * u * q, limit = a.probs ? (e - w.tau * q) * w.Q : e;

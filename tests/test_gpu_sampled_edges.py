@@ -82,3 +82,35 @@ def test_first_calls_of_many_threads(w12):
     """The process's first calls come from 16 host threads at once, each on a stream and workspace of its own."""
     r = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr
+
+
+@pytest.mark.parametrize("V", [2, 3, 7])
+def test_greedy_requests_whose_drafter_was_sure(w12, V):
+    """At temperature 0 the rule is the same: a token that the drafter had none of any more is passed over, and where
+    it was certain of the target's token, a refused sibling leaves nothing."""
+    rng = np.random.default_rng(V)
+    for seed in range(6):
+        p = Problem(seed, [6] * 100, V, temperature=None, sd=8.0, shape="star" if seed % 2 else "tree")
+        p.T = np.zeros(100, np.float32)
+        p.draft = rng.integers(-1, V + 1, p.draft.shape).astype(np.int32)
+        if seed < 4:                     # q of one token at a time, with rounding's leavings on the others
+            sure = rng.integers(0, V, len(p.draft))
+            p.probs = (p.probs * np.float32(1e-8)).astype(np.float32)
+            p.probs[np.arange(len(sure)), sure] = 1.0
+        p.check(w12)
+
+
+@pytest.mark.parametrize("q,draft,length", [
+    ([1.0, 1e-8, 0.0], [0, 1], 0),            # after the first there is nothing the drafter could have drawn
+    ([1e-9, 1.0, 0.0], [0, 1], 0),            # nothing is left of p
+    ([0.0, 1.0, 0.0], [0, 1], 1),             # a token with q = 0 changes nothing
+    ([0.5, 0.25, 0.25], [0, 2, 1], 1), ([0.5, 0.25, 0.25], [0, 0, 1], 1), ([0.5, 0.25, 0.25], [0, 3, -1, 1], 1),
+    ([0.7, 0.7, 0.0], [0, 1], 0),             # u q is above what is left
+    ([0.6, 0.6, 0.0], [1, 0], 1)])
+def test_greedy_child(w12, q, draft, length):
+    n = len(draft) + 1
+    logits = f32(np.tile([0.0, 5.0, 1.0], (n, 1)))
+    got, path, bonus, status = w12.tree_verify_sampled(
+        logits, i32([-1] + [0] * (n - 1)), i32([0] + draft), f32(np.full(n, 0.875)), f32([0.5]),
+        draft_probs=f32(np.tile(q, (n, 1))), temperature=f32([0.0]))
+    assert (int(status), int(got), int(bonus)) == (0, length, 1)
