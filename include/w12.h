@@ -614,8 +614,8 @@ W12_API int tree_positions(const int32_t* cache_len, const int32_t* parent, cons
  * bf16, row i at x + i*x_stride elements, with the position pos[i].  A row with a negative position is
  * padding: its q, k and v are left as they were.  Rows of q start q_stride elements apart, heads adjacent;
  * k and v likewise, so they may be parts of one array.  q, k and v of bf16 rows may stand in the
- * place of the parts of x that they come from (same stride); otherwise they share no element with x or one
- * another.  Pointers 16-byte aligned, strides multiples of 8 elements.  Asynchronous; allocates nothing.
+ * place of the parts of x that they come from (same stride); otherwise they share no element with x, with one
+ * another or with pos and the form's arrays.  Pointers 16-byte aligned, strides multiples of 8 elements.  Asynchronous; allocates nothing.
  * Errors: W12_ERR_INVALID_ARG, W12_ERR_SHAPE. */
 W12_API int qkv_rope(const void* x, int32_t x_bf16, int64_t x_stride, int64_t M, const qkv_form* form, const int32_t* pos,
                      uint16_t* q, int64_t q_stride, uint16_t* k, int64_t k_stride, uint16_t* v, int64_t v_stride,
@@ -626,7 +626,7 @@ W12_API int qkv_rope(const void* x, int32_t x_bf16, int64_t x_stride, int64_t M,
  * are not NULL (tree_attn takes the pass's own k and v from rows).  A slot of -1 is skipped (kv_slots' padding); any
  * other slot outside the cache is skipped and sets bit 0 of *status; rows are written all the same.  A row with a
  * negative position is padding: nothing is written for it, whatever its slot.  Two tokens with one slot leave
- * either's values, column by column.  The cache shares no memory with the call's other arrays.
+ * either's values, column by column.  The cache and *status share no memory with the call's other arrays.
  * Errors: as for qkv_rope. */
 W12_API int kv_append(const void* x, int32_t x_bf16, int64_t x_stride, int64_t M, const qkv_form* form, const int32_t* pos,
                       const kv_cache* cache, int64_t layer, const int64_t* slot, uint16_t* q, int64_t q_stride, uint16_t* k,

@@ -2,6 +2,7 @@
 // nodes, norms of each head and the position rotation in one pass, and the same with K and V going
 // straight into their slots of a paged cache.
 #include <cstdint>
+#include <iterator>
 
 #include "w12_internal.cuh"
 #include "w12_pdl.cuh"
@@ -403,6 +404,9 @@ int rope_args(RopeArgs& a, const char* fn, const void* x, int32_t x_bf16, int64_
   if ((bits & 15u) || (strides & 7))
     return fail(W12_ERR_INVALID_ARG, "%s: rows must be 16-byte aligned and their strides multiples of 8", fn);
   const int size = x_bf16 ? 2 : 4;
+  // what all rows read: the norms' weights and the frequencies
+  const float* const form_array[3] = {form->q_norm, form->k_norm, form->rot_dim ? form->inv_freq : nullptr};
+  const uintptr_t form_bytes[3] = {(uintptr_t)d * 4, (uintptr_t)d * 4, (uintptr_t)form->rot_dim * 2};
   for (int i = 0; i < 3; ++i) {
     if (!out[i]) continue;
     const uintptr_t o = (uintptr_t)out[i], row = (uintptr_t)wide[i] * 2, pitch = (uintptr_t)stride[i] * 2;
@@ -410,6 +414,8 @@ int rope_args(RopeArgs& a, const char* fn, const void* x, int32_t x_bf16, int64_
     const bool same = x_bf16 && o == (uintptr_t)x + (uintptr_t)at[i] * 2 && (stride[i] == x_stride || M == 1);
     bool ok = same || rows_apart(o, row, pitch, (uintptr_t)x, (uintptr_t)width * size, (uintptr_t)x_stride * size, M);
     ok = ok && rows_apart(o, row, pitch, (uintptr_t)pos, (uintptr_t)M * 4, 0, M);
+    for (int j = 0; j < 3; ++j)
+      ok = ok && (!form_array[j] || rows_apart(o, row, pitch, (uintptr_t)form_array[j], form_bytes[j], 0, M));
     for (int j = 0; j < i; ++j)
       ok = ok && (!out[j] || rows_apart(o, row, pitch, (uintptr_t)out[j], (uintptr_t)wide[j] * 2, (uintptr_t)stride[j] * 2, M));
     if (!ok) return fail(W12_ERR_INVALID_ARG, "%s: q, k and v must not overlap one another or what the call reads", fn);
@@ -506,7 +512,7 @@ int kv_append(const void* x, int32_t x_bf16, int64_t x_stride, int64_t M, const 
                 form->n_heads, form->head_dim);
   if (layer < 0 || layer >= cache->n_layers)
     return fail(W12_ERR_SHAPE, "kv_append: layer %lld of %lld", (long long)layer, (long long)cache->n_layers);
-  // Rows and slots stand outside the cache.
+  // Rows, slots and the form's arrays stand outside the cache, and the status outside them all.
   const uintptr_t span = 2 * (uintptr_t)((cache->n_layers - 1) * cache->layer_stride + (cache->n_blocks - 1) * cache->block_stride +
                                          (cache->block_size - 1) * cache->token_stride +
                                          (cache->n_heads - 1) * cache->head_stride + cache->head_dim);
@@ -521,11 +527,18 @@ int kv_append(const void* x, int32_t x_bf16, int64_t x_stride, int64_t M, const 
                         {v, ((M - 1) * v_stride + nk) * 2},
                         {pos, M * 4},
                         {slot, M * 8},
+                        {form->q_norm, form->head_dim * 4},
+                        {form->k_norm, form->head_dim * 4},
+                        {form->rot_dim ? form->inv_freq : nullptr, form->rot_dim * 2},
                         {status, 4}};
   for (const Range& u : used)
     for (const uint16_t* c : {cache->k, cache->v})
       if (u.p && (uintptr_t)u.p < (uintptr_t)c + span && (uintptr_t)c < (uintptr_t)u.p + (uintptr_t)u.bytes)
         return fail(W12_ERR_INVALID_ARG, "kv_append: the cache must not overlap the call's other arrays");
+  for (const Range& u : used)
+    if (u.p && &u != std::end(used) - 1 && (uintptr_t)u.p < (uintptr_t)status + 4 &&
+        (uintptr_t)status < (uintptr_t)u.p + (uintptr_t)u.bytes)
+      return fail(W12_ERR_INVALID_ARG, "kv_append: status must not overlap the call's other arrays");
   for (int i = 1; i < 4; ++i)
     if (used[i].p && (uintptr_t)used[i].p < (uintptr_t)slot + (uintptr_t)M * 8 &&
         (uintptr_t)slot < (uintptr_t)used[i].p + (uintptr_t)used[i].bytes)

@@ -20,7 +20,7 @@ def golden_dir():
 
 # Their calls pass made-up addresses and rely on being refused; should a check let one through, it must end at the
 # missing device and not in a kernel.
-MADE_UP_ADDRESSES = ("test_abi.py", "test_paged_abi.py", "test_sampled_abi.py")
+MADE_UP_ADDRESSES = ("test_abi.py", "test_paged_abi.py", "test_sampled_abi.py", "test_rope_abi.py")
 
 
 @pytest.fixture(autouse=True)

@@ -14,7 +14,7 @@ sys.exit(pytest.main(["-q", "-rA", *sys.argv[1:]]))
 """
 
 
-@pytest.mark.parametrize("name", ["test_abi.py", "test_paged_abi.py", "test_sampled_abi.py"])
+@pytest.mark.parametrize("name", ["test_abi.py", "test_paged_abi.py", "test_sampled_abi.py", "test_rope_abi.py"])
 def test_argument_checks_are_skipped(name):
     torch = pytest.importorskip("torch")
     if torch.cuda.is_available():
