@@ -217,19 +217,25 @@ __device__ __forceinline__ float least_of(const Ref& r, const Slope& c) {
   return fmaxf((r.whole - 125.0f) * c.over, -kMost);
 }
 
-__device__ __noinline__ float far_scale(Ref from, Ref to, Slope c) {
+// (no power of two, so that the factor is a pair as well)
+__device__ __noinline__ Pair far_scaled(Pair x, Ref from, Ref to, Slope c) {
   const double k = (double)c.hi + (double)c.lo;
-  const double a = from.shift != 0.0f ? (double)from.shift * k : (double)from.whole;
-  const double b = to.shift != 0.0f ? (double)to.shift * k : (double)to.whole;
-  return (float)exp2(a - b);
+  // (of two shifts the difference is exact)
+  const double d = from.shift != 0.0f && to.shift != 0.0f ? ((double)from.shift - (double)to.shift) * k
+                   : from.shift != 0.0f                   ? (double)from.shift * k - (double)to.whole
+                                                          : (double)from.whole - (double)to.shift * k;
+  const double e = exp2(d);
+  const float h = (float)e;
+  return x * Pair{h, h < INFINITY ? (float)(e - (double)h) : 0.0f};
 }
 
-// One unit of `from` in units of `to`.
-__device__ __forceinline__ float scale_of(const Ref& from, const Ref& to, const Slope& c) {
-  if (from.most == to.most) return 1.0f;
-  if (from.shift != 0.0f || to.shift != 0.0f) return far_scale(from, to, c);
-  const float k = from.whole - to.whole;
-  return k >= -126.0f ? __int_as_float((127 + (int)fminf(k, 127.0f)) << 23) : 0.0f;
+// A mass, or a sum of them, in units of `to` instead of `from`.
+__device__ __forceinline__ Pair scaled(Pair x, const Ref& from, const Ref& to, const Slope& c) {
+  if (from.most == to.most) return x;
+  if (from.shift != 0.0f || to.shift != 0.0f) return far_scaled(x, from, to, c);
+  const float w = from.whole - to.whole;
+  const float k = w >= -126.0f ? __int_as_float((127 + (int)fminf(w, 127.0f)) << 23) : 0.0f;
+  return {x.h * k, x.l * k};
 }
 
 // 2^(j/32) as a float, and the rest of it as a part of that float.
@@ -481,9 +487,7 @@ __device__ __forceinline__ Total sum_unknown(const Row& row, const Slope& c, int
       most = warp_max(most);
       const Ref to = make_ref(most, c);
       if (t.most > -INFINITY) {
-        const float k = scale_of(make_ref(t.most, c), to, c);
-        t.sum = t.sum + sum.value();
-        t.sum = {t.sum.h * k, t.sum.l * k};
+        t.sum = scaled(t.sum + sum.value(), make_ref(t.most, c), to, c);
         sum = Sum();
       }
       t.most = most;
@@ -846,10 +850,7 @@ __device__ __forceinline__ Total join(const Total* part, int n, const Slope& c, 
 #pragma unroll 1
     for (int o = 8; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
     most = __shfl_sync(0xFFFFFFFFu, most, 0);
-    if (t.sum.h > 0.0f) {
-      const float k = scale_of(make_ref(t.most, c), make_ref(most, c), c);
-      mine = {t.sum.h * k, t.sum.l * k};
-    }
+    if (t.sum.h > 0.0f) mine = scaled(t.sum, make_ref(t.most, c), make_ref(most, c), c);
   }
   if (greedy) {
     t.at = __reduce_min_sync(0xFFFFFFFFu, t.most == most ? t.at : 0x7FFFFFFF);
@@ -873,18 +874,12 @@ __device__ __forceinline__ void find_token(const SampleArgs& a, WalkShared& s, c
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const Ref whole = make_ref(most, c);
   Pair mine{0.0f, 0.0f};
-  float k = 1.0f;
-  if (lane < kWalkWarps && s.range[lane].sum.h > 0.0f) {
-    const Ref part = make_ref(s.range[lane].most, c);
-    k = scale_of(part, whole, c);
-    mine = {s.range[lane].sum.h * k, s.range[lane].sum.l * k};
-  }
+  if (lane < kWalkWarps && s.range[lane].sum.h > 0.0f)
+    mine = scaled(s.range[lane].sum, make_ref(s.range[lane].most, c), whole, c);
   const Found in = find_lane<16>(mine, target);
   const int range = max(in.lane, 0);
   const Ref ref = make_ref(s.range[range].most, c);
-  target = target - in.before;
-  k = scale_of(whole, ref, c);
-  target = {target.h * k, target.l * k};
+  target = scaled(target - in.before, whole, ref, c);
   const Scale scale = make_scale(ref, c, root);
   const int64_t v0 = first + range * a.range, v1 = min(row.hi, v0 + a.range);
   const int n_refused = cmd.refused ? s.n_refused : 0;
@@ -1142,8 +1137,7 @@ __global__ void __launch_bounds__(kWalkThreads, 2) k_sample_walk(const __grid_co
         top = warp_max(top);
         const Ref ref = make_ref(top, c);
         if (top > most) {
-          const float scale = sum.h > 0.0f ? scale_of(make_ref(most, c), ref, c) : 0.0f;
-          sum = {sum.h * scale, sum.l * scale};
+          if (sum.h > 0.0f) sum = scaled(sum, make_ref(most, c), ref, c);
           most = top;
           at = 0x7FFFFFFF;
         }
@@ -1153,10 +1147,7 @@ __global__ void __launch_bounds__(kWalkThreads, 2) k_sample_walk(const __grid_co
 #pragma unroll
           for (int e = 1; e < W; ++e) u[e - 1] = u[e];  // (a loop's body once, with its registers named)
           if (v.most == most) at = min(at, v.at);
-          if (v.sum[0] > 0.0f) {
-            const float scale = scale_of(make_ref(v.most, c), ref, c);
-            sum = sum + Pair{v.sum[0] * scale, v.sum[1] * scale};
-          }
+          if (v.sum[0] > 0.0f) sum = sum + scaled(Pair{v.sum[0], v.sum[1]}, make_ref(v.most, c), ref, c);
         }
       }
       at = __reduce_min_sync(0xFFFFFFFFu, at);

@@ -277,3 +277,42 @@ def test_rough_sum_of_a_long_row(w12, a, side):
     u = np.float32(p * (1 - side * 2e-6))
     length, path, _, status = w12.tree_verify_sampled(logits, i32([-1, 0]), i32([0, x]), f32([0.0, u]), f32([0.5]))
     assert int(status) == 0 and length.tolist() == [side > 0] and path.tolist() == ([0, 1] if side > 0 else [0, -1])
+
+
+@pytest.mark.parametrize("rising", [True, False])
+@pytest.mark.parametrize("probs", [None, True, False])
+def test_borders_between_far_logits(w12, rising, probs):
+    """Logits whose exponents pass 2^16, two tokens a row in ranges of their own: parts of a row then differ by no power of two.
+    Without drafts (probs None) the bonus' border, else the child's.  All but that factor is exact here, and that is a
+    pair of floats, so 2^-28 is far from what may come out."""
+    R, V = 256, 4100
+    a, b = (3000, 200) if rising else (200, 3000)         # the larger logit's token, and the other
+    rng = np.random.default_rng(7)
+    q, rows, T, u, want = 0.875 if probs else 1.0, np.full((R, V), -np.inf, np.float32), [], [], []
+    while len(u) < R:
+        t = float(np.float32(rng.uniform(0.8, 1.2)))
+        d = 0.03125 * int(rng.integers(1, 50))
+        p = 1 / (1 + np.exp(-d / t))                       # of a
+        first = p if a < b or probs is not None else 1 - p  # the border: of the lower token, or of the child's
+        n = np.float32(first / q)
+        for x in (n, np.nextafter(n, np.float32(0)), np.nextafter(n, np.float32(1))):
+            gap = float(x) * q - first
+            if 2.0 ** -28 < abs(gap) < 2.0 ** -26 and x < 1 and len(u) < R:
+                rows[len(u), a], rows[len(u), b] = 2.0 ** 18, 2.0 ** 18 - d
+                T.append(t)
+                u.append(x)
+                want.append(gap < 0)
+    want = np.array(want)
+    assert 50 < want.sum() < R - 50
+    zero, off = np.zeros(R), np.arange(R + 1)
+    if probs is None:
+        length, _, bonus, status = w12.tree_verify_sampled(f32(rows), i32(zero - 1), i32(zero), f32(zero), f32(u),
+                                                           temperature=f32(T), req_offsets=i32(off))
+        assert int(status) == 0 and (bonus.cpu().numpy() == np.where(want, min(a, b), max(a, b))).all()
+        return
+    pr = np.zeros(V, np.float32)
+    pr[a], pr[7] = q, 1 - q
+    length, _, _, status = w12.tree_verify_sampled(
+        f32(np.repeat(rows, 2, 0)), i32(np.tile([-1, 0], R)), i32(np.tile([0, a], R)), f32(np.stack([zero, u], 1).ravel()),
+        f32(zero), draft_probs=f32(np.tile(pr, (2 * R, 1))) if probs else None, temperature=f32(T), req_offsets=i32(2 * off))
+    assert int(status) == 0 and (length.cpu().numpy() == want).all()
