@@ -585,8 +585,9 @@ W12_API int tree_attn_set_wait_limit(int64_t cycles);
  *             head_dim floats each; NULL: no norm.  The sum of squares is float.
  *   rotation  pair j < rot_dim/2 of a head of q and of k, columns (j, j + rot_dim/2), or (2j, 2j+1)
  *             where interleaved, is turned by the angle pos * inv_freq[j] and scaled by rot_scale:
- *             (a, b) -> rot_scale * (a cos - b sin, b cos + a sin).  The angle is taken in 64 bits: far
- *             positions lose nothing.  Columns from rot_dim on stay.  rot_dim = 0: no rotation.
+ *             (a, b) -> rot_scale * (a cos - b sin, b cos + a sin).  The angle is taken in 64 bits, so that far
+ *             positions lose nothing, and rounded to a float without its whole turns (2^-26 turns at most).
+ *             Columns from rot_dim on stay.  rot_dim = 0: no rotation.
  * Everything is float until the one rounding to bf16 at the end (to nearest even).  Value heads are only rounded.
  * head_dim: a multiple of 8 up to 256; rot_dim: a multiple of 8, head_dim or less.
  */
@@ -717,7 +718,7 @@ W12_API int logits_verify(const float* logits, int64_t stride, int64_t M, int64_
  * (p <= q everywhere, or all that p held was refused), no further child is accepted and the bonus comes from p
  * as it was at the node.  bonus[r] = -1 where the node allows no token.  Numbers u outside [0, 1) count as the nearest in it (NaN: 0).
  * Sums are made to 2^-28 of the node's sum (of the logits' masses) or better, after j refusals with draft_probs to
- * j + 1 times 2^-27 of it, so that borders between tokens of large vocabularies fall where the formula has them
+ * j + 1 times 2^-27 of it (what a refusal leaves below that may count as nothing), so that borders between tokens of large vocabularies fall where the formula has them
  * (temperatures up to 1e30).  Repeated calls give identical results.
  * parent, draft, req_offsets, path_len, path_nodes and bonus as for tree_verify_tokens, path_nodes -1 behind the path.
  * A request that is out of range (offsets, a malformed tree, more than 1024 nodes, a temperature that is

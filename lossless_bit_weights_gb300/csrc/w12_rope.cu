@@ -221,7 +221,8 @@ __device__ __forceinline__ void store8(uint16_t* y, int lo, int hi, const uint32
 
 // Turns that a position moves a pair by, modulo 1, in units of 2^-64: inv_freq / (2 pi) = m R 2^(E - 278) with the
 // float's mantissa m and exponent E and R = 2^128 / (2 pi).  A position times it, modulo 2^64, drops whole
-// turns exactly and leaves an error below 2^-32 turns at 2^31 - 1.
+// turns exactly and leaves an error below 1.5 * 2^-32 turns at 2^31 - 1 (the product's cut to 32 bits among it).  The float
+// that sine and cosine are taken of rounds by 2^-26 turns at most.
 __device__ __forceinline__ uint64_t turns_of(float inv_freq) {
   constexpr uint64_t kHigh = 0x28BE60DB9391054Aull, kLow = 0x7F09D5F47D4D3770ull;
   const uint32_t bits = __float_as_uint(inv_freq), e = bits >> 23 & 255u;
@@ -243,8 +244,9 @@ __device__ __forceinline__ uint64_t turns_of(float inv_freq) {
 // over P lanes, the U heads' sums side by side.  The row's sines are found once, a thread each, while the first
 // heads are on their way; the next heads are on theirs while U are worked on.
 // Bound by bytes, the row read once and written once: 12289 float rows of 56 heads of 128, with norms, into a cache in
-// 80.6 us (529 MB, 6.56 TB/s, 0.97 of the measured copy rate), 12289 bf16 rows of 32 heads of 256 without norms in 61.1
-// (6.59 TB/s).  bf16 rows with norms are bound by instructions, 71 us.  Few rows are launch and latency: one 2.0 us, 192 3.8.
+// 80.7 us (529 MB, 6.55 TB/s, 0.97 of the measured copy rate), 12289 bf16 rows of 32 heads of 256 without norms in 61.3
+// (6.57 TB/s).  bf16 rows with norms are bound by instructions, 71 us for those heads, 67 for the 56 of 128.  Few rows are
+// launch and latency: one 2.0 us, 192 3.8.
 // What it took on the way (float, bf16): all heads' loads behind the position's 92, 99; the sums one by
 // one 88, 79 with norms; rows that L2 cannot keep not streamed out 82, 62.
 // U = 2 for float (4: 121 us) and for bf16 rows with norms (4: 82 for 67) or few rows (4: 4.9 us for 3.8 at 192 rows);

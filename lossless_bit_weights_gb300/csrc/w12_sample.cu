@@ -19,8 +19,8 @@
 //
 // Two kernels: the rows that the walk may pass are summed by all SMs first, then a cluster of blocks per request
 // walks its tree and sums a row again for every refusal.  192 nodes of 24 requests over 151936 tokens with q take
-// 50 us (the rows' 70.5 MB and 24 rows of q are 13 us at the measured copy rate, the rows that these walks really
-// need 7), a 16-node tree 23, 64 chains of five without q 55 (193 MB), one row of 32000 tokens 9.  What is left is
+// 54 us (the rows' 70.5 MB and 24 rows of q are 13 us at the measured copy rate, the rows that these walks really
+// need 7), a 16-node tree 23, 64 chains of five without q 57 (193 MB), one row of 32000 tokens 9.  What is left is
 // the longest walk: a refusal is a round of the cluster, of which the sum over 15000 tokens a block is 4 to 6 us and a
 // cluster barrier, the joining and the decision 2 to 3.
 #include <cstdint>
@@ -368,7 +368,8 @@ __device__ __forceinline__ float rough(float l, float most, float slope, float l
 // 2^-24 of the sum at a time, which a float adds up to 2^-30 of it at worst over kStretch places; longer ranges settle.
 // With the low parts in `rest`, and sums that start above every mass for the sake of three operations, 9496 equal masses
 // lost up to 2^-25.4 of their sum, 42752 2^-23.5; 192 nodes then took 50.4 us (53.4 now), 64 chains 55.3 (57.8).
-// (Masses brought into order, lo the rounding of h, would lose nothing: 56.4 us.)
+// (Masses brought into order, lo the rounding of h, would lose nothing: 56.4 us.  The larger of sum and mass by comparison
+// in place of three of the six operations 57.0.)
 struct Sum {
   uint64_t s = both(0.0f), rest = both(0.0f);
   __device__ __forceinline__ uint64_t step(uint64_t x) {  // (what it leaves)
@@ -557,9 +558,10 @@ __device__ __forceinline__ Total rough_unknown(const Row& row, const Slope& c, i
 // 1024 places.  Every block of a tile of nodes makes the list of its rows with children, and the tile's warps take
 // equal shares of all units, 128 bytes a lane on their way.  Without q the sums only serve decisions, which plain floats
 // (good to 2^-15 together) nearly always tell, and the walk sums again for the others.
-// Bound by the logits read once, and with q by the pairs' arithmetic: 256 rows of 151936 (156 MB) in 30.3 us without q
-// (5.1 TB/s, 0.76 of the measured copy rate; 2.8 of it to make the list), 116 rows (70.5 MB) in 20.5 with q, 16.6 if they
-// were rough.  Pairs for the chains too made their call 72 us for 59.  Bringing each warp's share into L2 ahead in bulk
+// Bound by the logits read once, and with q by the pairs' arithmetic: 256 rows of 151936 (156 MB) in 30.7 us without q
+// (5.1 TB/s, 0.75 of the measured copy rate; 2.8 of it to make the list), 116 rows (70.5 MB) in 23.4 with q, 16.6 if they
+// were rough.  A form for each, since the pairs spill 28 bytes at 80 registers (loads of four steps in place of eight spill
+// nothing and take 23.8).  Pairs for the chains too made their call 72 us for 59.  Bringing each warp's share into L2 ahead in bulk
 // took 9 us more; two or four blocks an SM about 1; one row after another by a request's blocks twice the time.
 template <bool PAIRS>
 __global__ void __launch_bounds__(kStatThreads, 3) k_sample_stats(const __grid_constant__ SampleArgs a) {
@@ -1089,11 +1091,11 @@ __device__ __forceinline__ Command decide(const SampleArgs& a, WalkShared& s, co
 // the bonus token asks for a row's masses, each sums its part, a range of tokens a warp, and sends the sum to all. No
 // block reads what decides from memory itself, so that all come to the same and no barrier can miss one.  Bound by
 // the rounds' latencies (a single tree's round has 3 us of sums, as much for joining and deciding, 1 for the
-// barrier), then by arithmetic (22 operations on pairs of floats a token and refusal).  With the first block alone
-// deciding, and a second barrier a round for its command, 192 nodes took 52.5 us for 50, 64 chains 57.6 for 55.2.
+// barrier), then by arithmetic (27 operations on pairs of floats a token and refusal).  With the first block alone
+// deciding, and a second barrier a round for its command, 192 nodes took 52.5 us for 50 then, 64 chains 57.6 for 55.2.
 // Asynchronous copies of a sum's next tokens to shared memory brought nothing.  Blocks of 512 threads, two an SM at
 // 64 registers: an earlier form, 57 us for 192 nodes, took 64 with one an SM at 128, 61 with 1024 threads; four of
-// 256 threads 55, but a single tree 27 for 23.
+// 256 threads 55, but a single tree 27 for 23.  (72 bytes are spilled at 64 registers.)
 __global__ void __launch_bounds__(kWalkThreads, 2) k_sample_walk(const __grid_constant__ SampleArgs a, int cluster) {
   __shared__ WalkShared s;
   cluster_arrive();  // a block's shared memory is written to only when the block runs
